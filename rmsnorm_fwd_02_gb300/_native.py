@@ -1,5 +1,5 @@
-"""ctypes binding of ``librmsnorm_train.so`` with the C ABI's names (include/rmsnorm_train.h
-and include/layernorm_train.h).
+"""ctypes binding of ``librmsnorm_train.so`` with the C ABI's names (include/rmsnorm_train.h,
+include/layernorm_train.h and include/dropout_train.h).
 
 Argument marshalling only: tensors become device pointers, the current torch stream
 becomes the ``cudaStream_t``, sizes and strides are passed through, and a nonzero status
@@ -23,6 +23,7 @@ RMSN_W_FP32 = 1
 # every C entry point declared in include/rmsnorm_train.h, with its ctypes signature
 _i64, _i32, _vp, _int, _f32, _size = (C.c_int64, C.c_int32, C.c_void_p, C.c_int, C.c_float,
                                       C.c_size_t)
+_u64, _f64 = C.c_uint64, C.c_double
 SIGNATURES = {
     "rmsnorm_train_fwd": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _i64, _i32, _i32, _i64,
                                  _i64, _f32, _vp]),
@@ -43,7 +44,17 @@ SIGNATURES = {
                                    _i64, _i32, _int, _vp]),
     "layernorm_train_launch_plan": (_int, [_i32, _int, C.POINTER(C.c_int64), _int]),
     "layernorm_train_device_error": (_int, [C.POINTER(C.c_uint), _int]),
+    # include/dropout_train.h
+    "dropout_train_fwd": (_int, [_vp, _vp, _vp, _int, _i64, _f64, _u64, _u64, _vp, _vp]),
+    "dropout_train_bwd": (_int, [_vp, _vp, _int, _i64, _f64, _u64, _u64, _vp, _vp]),
+    "rmsnorm_dropout_train_fwd": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _i64, _i32, _i32,
+                                         _i64, _i64, _f32, _f64, _u64, _u64, _vp, _vp]),
+    "rmsnorm_dropout_train_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp,
+                                         _size, _i64, _i32, _i32, _f64, _u64, _u64, _vp, _int,
+                                         _vp]),
 }
+
+DROPOUT_BF16, DROPOUT_FP32, DROPOUT_FP16 = 0, 1, 2
 
 PLAN_FWD, PLAN_FWD_RESIDUAL, PLAN_BWD, PLAN_BWD_DH, PLAN_BWD_ND, PLAN_BWD_ND_DH = 0, 1, 2, 3, 4, 5
 LN_PLAN_FWD, LN_PLAN_BWD = 0, 1
@@ -199,3 +210,40 @@ def layernorm_train_device_error(reset=True):
     if st != RMSN_OK:
         raise RmsnError("layernorm_train_device_error", st)
     return int(flags.value)
+
+
+# ---- dropout (include/dropout_train.h) --------------------------------------------------
+
+def dropout_train_fwd(x, residual, y, dtype, n, p, seed, offset, step, stream=None):
+    st = lib().dropout_train_fwd(_ptr(x), _ptr(residual), _ptr(y), dtype, n, p, seed, offset,
+                                 _ptr(step), _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("dropout_train_fwd", st)
+
+
+def dropout_train_bwd(dy, dx, dtype, n, p, seed, offset, step, stream=None):
+    st = lib().dropout_train_bwd(_ptr(dy), _ptr(dx), dtype, n, p, seed, offset, _ptr(step),
+                                 _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("dropout_train_bwd", st)
+
+
+def rmsnorm_dropout_train_fwd(x, residual, w, w_dtype, y, h_out, rstd, T, nh, H, s_tok, s_head,
+                              eps, p, seed, offset, step, stream=None):
+    st = lib().rmsnorm_dropout_train_fwd(_ptr(x), _ptr(residual), _ptr(w), w_dtype, _ptr(y),
+                                         _ptr(h_out), _ptr(rstd), T, nh, H, s_tok, s_head, eps,
+                                         p, seed, offset, _ptr(step), _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_dropout_train_fwd", st)
+
+
+def rmsnorm_dropout_train_bwd(h, dy, dh, rstd, w, w_dtype, dx, dresidual, dw, workspace,
+                              workspace_bytes, T, nh, H, p, seed, offset, step, deterministic,
+                              stream=None):
+    st = lib().rmsnorm_dropout_train_bwd(_ptr(h), _ptr(dy), _ptr(dh), _ptr(rstd), _ptr(w),
+                                         w_dtype, _ptr(dx), _ptr(dresidual), _ptr(dw),
+                                         _ptr(workspace), workspace_bytes, T, nh, H, p, seed,
+                                         offset, _ptr(step), int(deterministic),
+                                         _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_dropout_train_bwd", st)

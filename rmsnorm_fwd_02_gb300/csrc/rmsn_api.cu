@@ -8,7 +8,8 @@
 #include <mutex>
 #include <unordered_map>
 
-#include "rmsnorm_train.h"  // include/ (on the include path)
+#include "dropout_train.h"  // include/ (on the include path)
+#include "rmsnorm_train.h"
 #include "rmsn_launch.h"
 
 namespace rmsn {
@@ -198,6 +199,14 @@ int det_partials(int32_t R, const Shape& s) {
 
 // ---- helpers used by the kernel translation units ------------------------------------
 
+int check_device(int* sms) {
+  int dev = 0, st;
+  if ((st = current_device(&dev)) != RMSN_OK) return st;
+  if ((st = device_setup(dev)) != RMSN_OK) return st;
+  if (sms != nullptr) *sms = g_sms[dev];
+  return RMSN_OK;
+}
+
 // Launch shapes: a thread owns VPT 16-byte column vectors of every row its group takes;
 // each kernel's vector count and row-group layout follow from H (and from the residual
 // form or dh), chosen for rows in flight within the kernel build's register budget.
@@ -358,16 +367,25 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaS
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-// Both backward entry points: rstd given (rstd_out unused), or rstd == nullptr and the
+// The dropout form's own arguments of the backward.
+struct BwdDrop {
+  DropParams params;
+  void* dx_drop;
+};
+
+// The backward entry points: rstd given (rstd_out unused), or rstd == nullptr and the
 // row pass recomputes it with eps, writing it to rstd_out (the small path computes it into
-// rstd_out first and reads it back).
+// rstd_out first and reads it back).  With `drop`, dx is the residual's gradient and
+// drop->dx_drop the added branch's (rstd given).
 int bwd_common(const void* x, const void* dy, const void* dh, const float* rstd, float eps,
                float* rstd_out, const void* w, int w_dtype, void* dx, float* dw, void* workspace,
                size_t workspace_bytes, int64_t T, int32_t nh, int32_t H, int64_t s_tok,
-               int64_t s_head, int deterministic, void* stream) {
+               int64_t s_head, int deterministic, void* stream, const BwdDrop* drop = nullptr) {
   int st = check_view(T, nh, H, s_tok, s_head, w_dtype);
   if (st != RMSN_OK) return st;
-  if (!x || !dy || !w || !dx || !dw) return RMSN_ERR_INVALID_ARG;
+  // (the dropout form takes NULL row tensors when there are no rows)
+  if (!w || !dw || ((drop == nullptr || T > 0) && (!x || !dy || !dx)))
+    return RMSN_ERR_INVALID_ARG;
   if (deterministic != 0 && deterministic != 1) return RMSN_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(dy) || !aligned16(dh) || !aligned16(w) || !aligned16(dx) ||
       !aligned16(dw) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(rstd) & 3u))
@@ -381,7 +399,7 @@ int bwd_common(const void* x, const void* dy, const void* dh, const float* rstd,
 
   const bool fp32w = (w_dtype == RMSN_W_FP32);
   if (bwd_is_small(R)) {  // one launch, no workspace
-    BwdArgs a{};
+    BwdDropArgs a{};
     a.x = static_cast<const __nv_bfloat16*>(x);
     a.dy = static_cast<const __nv_bfloat16*>(dy);
     a.dh = static_cast<const __nv_bfloat16*>(dh);
@@ -392,6 +410,12 @@ int bwd_common(const void* x, const void* dy, const void* dh, const float* rstd,
     a.map = RowMapArgs{nh, H, s_tok, nh > 1 ? s_head : 0};
     a.R = static_cast<int32_t>(R);
     a.err = g_err_ptr[dev];
+    if (drop != nullptr) {
+      a.drop = drop->params;
+      a.dx_drop = static_cast<__nv_bfloat16*>(drop->dx_drop);
+      return launch_bwd_small_drop(a, dw, fp32w, stream_) == cudaSuccess ? RMSN_OK
+                                                                         : RMSN_ERR_CUDA;
+    }
     if (rstd == nullptr && R > 0) {  // rstd first, then the one-launch backward reads it
       if (launch_rstd_rows(a, rstd_out, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
       a.rstd = rstd_out;
@@ -418,7 +442,7 @@ int bwd_common(const void* x, const void* dy, const void* dh, const float* rstd,
     const size_t need = ctl_bytes + static_cast<size_t>(P) * 2 * H * sizeof(float);
     if (workspace == nullptr || workspace_bytes < need) return RMSN_ERR_WORKSPACE;
 
-    BwdArgs a{};
+    BwdDropArgs a{};
     a.x = static_cast<const __nv_bfloat16*>(x);
     a.dy = static_cast<const __nv_bfloat16*>(dy);
     a.dh = static_cast<const __nv_bfloat16*>(dh);
@@ -438,7 +462,15 @@ int bwd_common(const void* x, const void* dy, const void* dh, const float* rstd,
     a.stages = s.stages;
     a.P = P;
     a.err = g_err_ptr[dev];
-    if (launch_bwd_rows(a, s, fp32w, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
+    cudaError_t e;
+    if (drop != nullptr) {
+      a.drop = drop->params;
+      a.dx_drop = static_cast<__nv_bfloat16*>(drop->dx_drop);
+      e = launch_bwd_rows_drop(a, s, fp32w, stream_);
+    } else {
+      e = launch_bwd_rows(a, s, fp32w, stream_);
+    }
+    if (e != cudaSuccess) return RMSN_ERR_CUDA;
   }
   unsigned* ctl = (deterministic || R == 0) ? nullptr : static_cast<unsigned*>(workspace);
   if (launch_dw_finish(part, dw, P, H, ctl, g_sms[dev], stream_) != cudaSuccess)
@@ -544,6 +576,71 @@ int rmsnorm_train_bwd_recompute(const void* x, const void* dy, const void* dh, c
   if (!std::isfinite(eps) || eps < 0.f) return RMSN_ERR_INVALID_ARG;
   return bwd_common(x, dy, dh, nullptr, eps, rstd_out, w, w_dtype, dx, dw, workspace,
                     workspace_bytes, T, nh, H, s_tok, s_head, deterministic, stream);
+}
+
+int rmsnorm_dropout_train_fwd(const void* x, const void* residual, const void* w, int w_dtype,
+                              void* y, void* h_out, float* rstd, int64_t T, int32_t nh,
+                              int32_t H, int64_t s_tok, int64_t s_head, float eps, double p,
+                              uint64_t seed, uint64_t offset, const uint64_t* step,
+                              void* stream) {
+  int st = check_view(T, nh, H, s_tok, s_head, w_dtype);
+  if (st != RMSN_OK) return st;
+  if (!w || (T > 0 && (!x || !residual || !y || !h_out || !rstd))) return RMSN_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(residual) ||
+      !aligned16(h_out) || (reinterpret_cast<uintptr_t>(rstd) & 3u))
+    return RMSN_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return RMSN_ERR_INVALID_ARG;
+  FwdDropArgs a{};
+  if (!drop_params(p, seed, offset, step, &a.drop)) return RMSN_ERR_INVALID_ARG;
+  const int64_t R = T * static_cast<int64_t>(nh);
+  if (R == 0) return RMSN_OK;
+  if (!a.drop.active)  // nothing is dropped: the residual form
+    return rmsnorm_train_fwd(x, residual, w, w_dtype, y, h_out, rstd, T, nh, H, s_tok, s_head,
+                             eps, stream);
+
+  int dev = 0;
+  if ((st = current_device(&dev)) != RMSN_OK) return st;
+  if ((st = device_setup(dev)) != RMSN_OK) return st;
+
+  const bool fp32w = (w_dtype == RMSN_W_FP32);
+  const Shape s = fwd_shape(H, true);
+  const int occ = fwd_drop_blocks_per_sm(s, fp32w);
+  int64_t P = (R + s.groups - 1) / s.groups;
+  const int64_t cap = static_cast<int64_t>(g_sms[dev]) * occ;
+  if (P > cap) P = cap;
+
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.res = static_cast<const __nv_bfloat16*>(residual);
+  a.w = w;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  a.h = static_cast<__nv_bfloat16*>(h_out);
+  a.rstd = rstd;
+  a.map = RowMapArgs{nh, H, s_tok, nh > 1 ? s_head : 0};
+  a.R = static_cast<int32_t>(R);
+  a.contig = is_contig(nh, H, s_tok, s_head) ? 1 : 0;
+  a.eps = eps;
+  a.groups = s.groups;
+  a.ntg = s.ntg;
+  a.stages = s.stages;
+  a.P = static_cast<int32_t>(P);
+  a.err = g_err_ptr[dev];
+  return launch_fwd_drop(a, s, fp32w, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RMSN_OK
+             : RMSN_ERR_CUDA;
+}
+
+int rmsnorm_dropout_train_bwd(const void* h, const void* dy, const void* dh, const float* rstd,
+                              const void* w, int w_dtype, void* dx, void* dresidual, float* dw,
+                              void* workspace, size_t workspace_bytes, int64_t T, int32_t nh,
+                              int32_t H, double p, uint64_t seed, uint64_t offset,
+                              const uint64_t* step, int deterministic, void* stream) {
+  if ((T > 0 && (!rstd || !dx)) || !aligned16(dx)) return RMSN_ERR_INVALID_ARG;
+  BwdDrop drop{};
+  if (!drop_params(p, seed, offset, step, &drop.params)) return RMSN_ERR_INVALID_ARG;
+  drop.dx_drop = dx;
+  const int64_t row = nh > 0 && H > 0 ? static_cast<int64_t>(nh) * H : 0;
+  return bwd_common(h, dy, dh, rstd, 0.f, nullptr, w, w_dtype, dresidual, dw, workspace,
+                    workspace_bytes, T, nh, H, row, H, deterministic, stream, &drop);
 }
 
 int rmsnorm_train_launch_plan(int32_t H, int op, int64_t* out, int n_out) {

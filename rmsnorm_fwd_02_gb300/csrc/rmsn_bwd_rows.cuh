@@ -1,9 +1,10 @@
 // rmsn_bwd_rows.cuh -- the RMSNorm training backward's row pass for sm_103a: dx fused with
 // the compensated dw partial sums, one program for both modes (the partition is chosen at
 // run time: a fixed chunk of rows per CTA, or a fixed prefix plus rows handed out from a
-// counter).  Included by rmsn_bwd.cu (builds that read rstd) and rmsn_bwd_rc.cu (builds
-// that recompute it); each CTA writes one dw partial to the workspace, and the fixed-order
-// finish kernel (rmsn_bwd.cu) adds them.
+// counter).  Included by rmsn_bwd.cu (builds that read rstd), rmsn_bwd_rc.cu (builds
+// that recompute it) and rmsn_drop_bwd.cu (builds that also write the gradient through the
+// dropout on the added branch); each CTA writes one dw partial to the workspace, and the
+// fixed-order finish kernel (rmsn_bwd.cu) adds them.
 //
 // Per normalized row, with r the forward's rstd (flashinfer PR #8827, description: the
 // backward's BF16 dx and FP32 dw; the residual form's combined gradient):
@@ -30,6 +31,9 @@
 // Arithmetic runs on packed FP32 pairs (f32x2): two columns per instruction.
 #pragma once
 
+#include <type_traits>
+
+#include "drop_philox.cuh"
 #include "rmsn_common.cuh"
 #include "rmsn_launch.h"
 #include "rmsn_tmem.cuh"
@@ -92,9 +96,13 @@ struct RowSums {
 //    H=1536, 26 stages a CTA, S=4: 1.7 us behind the deterministic chunks).
 // Either way CTA k writes its dw partial to a.part[k], and dx does not depend on the
 // partition.
-template <int VPT, int kCls, bool kFp32W, bool kDh, bool kRc>
+//
+// kDrop: the row's gradient (total, dh included) is the residual's, written to a.dx; the
+// gradient of the added branch before its dropout, keep * scale * total rounded once from
+// FP32, goes to a.dx_drop, with the keep bits drawn here again.
+template <int VPT, int kCls, bool kFp32W, bool kDh, bool kRc, bool kDrop>
 __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_per_sm(kCls))
-    rmsn_bwd_rows_kernel(const BwdArgs a) {
+    rmsn_bwd_rows_kernel(const std::conditional_t<kDrop, BwdDropArgs, BwdArgs> a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int NT = kDh ? 3 : 2;  // staged tensors: x, dy [, dh]
   const int H = a.map.H;
@@ -304,6 +312,8 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
       for (int q = 0; q < 4; ++q) p[q] = wv[v][q];
     }
   };
+  uint2 ctr = make_uint2(0u, 0u);
+  if constexpr (kDrop) ctr = drop_counter(a.drop);
   const float inv_h = 1.0f / static_cast<float>(H);
   const float hf = static_cast<float>(H);
   // Phase A of group g's row in slot s (valid: the row exists): its share of
@@ -417,7 +427,11 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
           if constexpr (kDh) hv = lds128_at(st + 2u * dy_off + 16u * c);
           f2 wl[4];
           wvec(v, c, wl);
-          uint32_t o[4];
+          uint32_t o[4], od[4];
+          uint32_t k8 = 0u;
+          if constexpr (kDrop)
+            k8 = drop_keep8(a.drop,
+                            drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 x2 = bf2_to_f2(u4_get(xv, q));
@@ -426,6 +440,8 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
             f2 d = f2_mul(f2_fma(x2, ncr2, gw), rs2);  // (g - xhat*c) * rstd
             if constexpr (kDh) d = f2_add(d, bf2_to_f2(u4_get(hv, q)));
             o[q] = f2_to_bf2(d);
+            if constexpr (kDrop)
+              od[q] = f2_to_bf2(f2_mul(d, f2_splat(a.drop.scale))) & drop_word_mask(k8, q);
             dyx[q] = f2_mul(d2, x2);
             if constexpr (!kTm) {
               // dw: running sum of the exact products dy*x*rs_hi with a Fast2Sum
@@ -438,6 +454,8 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
             }
           }
           stg128(a.dx + out_row + c * 8, make_uint4(o[0], o[1], o[2], o[3]));
+          if constexpr (kDrop)
+            stg128(a.dx_drop + out_row + c * 8, make_uint4(od[0], od[1], od[2], od[3]));
         }
         if constexpr (kTm) {
           __syncwarp();
@@ -615,18 +633,18 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
   }
 }
 
-// The kernel build for a launch shape (both modes), per kRc; each value's translation unit
+// The kernel build for a launch shape (both modes), per kRc and kDrop; each translation unit
 // instantiates only its own builds.  (bwd_shape gives 1-vector lanes the narrow class, 2-
 // and 4-vector threads the multi, tensor-memory or wide class, 3-vector threads the multi
 // or tensor-memory class.)
-template <bool kRc>
+template <bool kRc, bool kDrop = false>
 const void* pick_rows_kernel(const Shape& s, bool fp32w, bool dh) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
 #define RMSN_PICK(V, C)                                                               \
-  (fp32w ? (dh ? fn(&rmsn_bwd_rows_kernel<V, C, true, true, kRc>)                     \
-               : fn(&rmsn_bwd_rows_kernel<V, C, true, false, kRc>))                   \
-         : (dh ? fn(&rmsn_bwd_rows_kernel<V, C, false, true, kRc>)                    \
-               : fn(&rmsn_bwd_rows_kernel<V, C, false, false, kRc>)))
+  (fp32w ? (dh ? fn(&rmsn_bwd_rows_kernel<V, C, true, true, kRc, kDrop>)              \
+               : fn(&rmsn_bwd_rows_kernel<V, C, true, false, kRc, kDrop>))            \
+         : (dh ? fn(&rmsn_bwd_rows_kernel<V, C, false, true, kRc, kDrop>)             \
+               : fn(&rmsn_bwd_rows_kernel<V, C, false, false, kRc, kDrop>)))
   if (s.cls == kBwdTm)
     return s.vpt == 2 ? RMSN_PICK(2, kBwdTm)
                       : (s.vpt == 3 ? RMSN_PICK(3, kBwdTm) : RMSN_PICK(4, kBwdTm));

@@ -440,6 +440,9 @@ __device__ __forceinline__ void copy_rows_contig(__nv_bfloat16* dst, const __nv_
 }
 
 // ---- host helpers of every kernel translation unit (defined in rmsn_api.cu) ----
+// RMSN_OK if the current device can run the library (its SM count in *sms if wanted), else the
+// status to return.
+int check_device(int* sms = nullptr);
 // Opts fn into the shared-memory size the row kernels use (once per device).
 cudaError_t prepare_kernel(const void* fn, size_t smem);
 // Resident CTAs an SM of fn at this block size and shared memory (cached per device).

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "drop_launch.h"
+
 namespace rmsn {
 
 constexpr int kMaxH = 8192;
@@ -104,6 +106,11 @@ struct FwdArgs {
   unsigned* err;              // device error word
 };
 
+// The residual form with dropout on x: h = BF16(dropout(x) + residual).
+struct FwdDropArgs : FwdArgs {
+  DropParams drop;
+};
+
 struct BwdArgs {
   const __nv_bfloat16* x;     // forward's normalized input, strided
   const __nv_bfloat16* dy;    // contiguous
@@ -128,6 +135,13 @@ struct BwdArgs {
   unsigned* err;
 };
 
+// The backward of the dropout form: dx holds the residual's gradient (the total), dx_drop the
+// gradient of x before its dropout.
+struct BwdDropArgs : BwdArgs {
+  DropParams drop;
+  __nv_bfloat16* dx_drop;     // contiguous
+};
+
 // Shape of the forward / backward row kernels for width H.
 Shape fwd_shape(int H, bool residual);
 Shape bwd_shape(int H, bool with_dh);  // both modes
@@ -135,6 +149,8 @@ Shape bwd_shape(int H, bool with_dh);  // both modes
 // Launchers: return the CUDA launch status.  `pdl` opts the launch into programmatic
 // dependent launch (overlap with the previous kernel on the stream).
 cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, bool fp32w, cudaStream_t st);
+int fwd_drop_blocks_per_sm(const Shape& s, bool fp32w);
+cudaError_t launch_fwd_drop(const FwdDropArgs& a, const Shape& s, bool fp32w, cudaStream_t st);
 // The row-pass kernel build for a shape (one program for both modes), with rstd given or
 // recomputed (rc): rmsn_bwd.cu and rmsn_bwd_rc.cu.
 const void* bwd_rows_fn(const Shape& s, bool fp32w, bool dh, bool rc);
@@ -145,6 +161,8 @@ int bwd_blocks_per_sm(const Shape& s, bool fp32w, bool rc);
 // The row pass, either mode: a.ctl null (deterministic: fixed chunks) or the
 // non-deterministic pool's words.
 cudaError_t launch_bwd_rows(const BwdArgs& a, const Shape& s, bool fp32w, cudaStream_t st);
+cudaError_t launch_bwd_rows_drop(const BwdDropArgs& a, const Shape& s, bool fp32w,
+                                 cudaStream_t st);
 // ctl: the non-deterministic pool words to clear once the partials are summed, or null;
 // sms: the GPU's SM count (the finish build that takes a whole SM a CTA runs only where
 // its grid fits one wave).
@@ -165,6 +183,7 @@ constexpr int kSmallSlices = kSmallThreads / kSmallColVecs;   // row slices a co
 constexpr int64_t kSmallMaxRows = 256;
 bool bwd_is_small(int64_t R);
 cudaError_t launch_bwd_small(const BwdArgs& a, float* dw, bool fp32w, cudaStream_t st);
+cudaError_t launch_bwd_small_drop(const BwdDropArgs& a, float* dw, bool fp32w, cudaStream_t st);
 // rstd of rows [0, R) into `rstd` (one warp a row, the forward's formula), for the small
 // path of the backward that recomputes rstd.
 cudaError_t launch_rstd_rows(const BwdArgs& a, float* rstd, cudaStream_t st);

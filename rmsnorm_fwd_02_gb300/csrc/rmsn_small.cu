@@ -19,6 +19,9 @@
 // Every order is fixed by (R, H), so dw is bit-reproducible in both modes.  (The pages'
 // column-task kernel for small T has the same split of dw over columns; this one also
 // carries the row tasks, so that one launch returns dx and dw.)
+#include <type_traits>
+
+#include "drop_philox.cuh"
 #include "rmsn_common.cuh"
 #include "rmsn_launch.h"
 
@@ -39,9 +42,12 @@ constexpr int kSmallCols = kSmallColVecs * 8;
 
 }  // namespace
 
-template <int VPT, bool kFp32W, bool kDh>
+// kDrop: as in the row pass, the row tasks also write the gradient through the dropout on the
+// added branch.
+template <int VPT, bool kFp32W, bool kDh, bool kDrop>
 __global__ void __launch_bounds__(kSmallThreads)
-    rmsn_bwd_small_kernel(const BwdArgs a, float* __restrict__ dw, int Pr) {
+    rmsn_bwd_small_kernel(const std::conditional_t<kDrop, BwdDropArgs, BwdArgs> a,
+                          float* __restrict__ dw, int Pr) {
   __shared__ __align__(16) float sm[2 * kSmallSlices * kSmallCols];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -101,6 +107,8 @@ __global__ void __launch_bounds__(kSmallThreads)
     const float inv_h = 1.0f / static_cast<float>(H);
     const f2 rs2 = f2_splat(rs);
     const f2 ncr2 = f2_splat(-(dot * (rs * inv_h)) * rs);
+    uint2 ctr = make_uint2(0u, 0u);
+    if constexpr (kDrop) ctr = drop_counter(a.drop);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = lt + v * gt;
@@ -108,15 +116,23 @@ __global__ void __launch_bounds__(kSmallThreads)
         uint4 hv = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (kDh)
           hv = *reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(row) * H + c * 8);
-        uint32_t o[4];
+        uint32_t o[4], od[4];
+        uint32_t k8 = 0u;
+        if constexpr (kDrop)
+          k8 = drop_keep8(a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f2 gw = f2_mul(bf2_to_f2(u4_get(dv[v], q)), wv[v][q]);
           f2 d = f2_mul(f2_fma(bf2_to_f2(u4_get(xv[v], q)), ncr2, gw), rs2);
           if constexpr (kDh) d = f2_add(d, bf2_to_f2(u4_get(hv, q)));
           o[q] = f2_to_bf2(d);
+          if constexpr (kDrop)
+            od[q] = f2_to_bf2(f2_mul(d, f2_splat(a.drop.scale))) & drop_word_mask(k8, q);
         }
         stg128(a.dx + static_cast<size_t>(row) * H + c * 8, make_uint4(o[0], o[1], o[2], o[3]));
+        if constexpr (kDrop)
+          stg128(a.dx_drop + static_cast<size_t>(row) * H + c * 8,
+                 make_uint4(od[0], od[1], od[2], od[3]));
       }
     }
     return;
@@ -212,13 +228,34 @@ __global__ void __launch_bounds__(kSmallThreads)
 
 namespace {
 
-template <int VPT>
+template <int VPT, bool kDrop>
 const void* small_ptr_v(bool fp32w, bool dh) {
+  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
   if (fp32w)
-    return dh ? reinterpret_cast<const void*>(&rmsn_bwd_small_kernel<VPT, true, true>)
-              : reinterpret_cast<const void*>(&rmsn_bwd_small_kernel<VPT, true, false>);
-  return dh ? reinterpret_cast<const void*>(&rmsn_bwd_small_kernel<VPT, false, true>)
-            : reinterpret_cast<const void*>(&rmsn_bwd_small_kernel<VPT, false, false>);
+    return dh ? fn(&rmsn_bwd_small_kernel<VPT, true, true, kDrop>)
+              : fn(&rmsn_bwd_small_kernel<VPT, true, false, kDrop>);
+  return dh ? fn(&rmsn_bwd_small_kernel<VPT, false, true, kDrop>)
+            : fn(&rmsn_bwd_small_kernel<VPT, false, false, kDrop>);
+}
+
+template <bool kDrop, typename Args>
+cudaError_t launch_small(const Args& a, float* dw, bool fp32w, cudaStream_t st) {
+  const int NV = a.map.H / 8;
+  const int vpt = (NV + kSmallThreads - 1) / kSmallThreads;  // 1..4 for H <= 8192
+  const bool dh = a.dh != nullptr;
+  const void* fn = vpt == 1   ? small_ptr_v<1, kDrop>(fp32w, dh)
+                   : vpt == 2 ? small_ptr_v<2, kDrop>(fp32w, dh)
+                   : vpt == 3 ? small_ptr_v<3, kDrop>(fp32w, dh)
+                              : small_ptr_v<4, kDrop>(fp32w, dh);
+  const int per = (NV + vpt - 1) / vpt;
+  const int gt = per <= 32 ? 32 : (per + 31) / 32 * 32;
+  const int groups = kSmallThreads / gt;
+  int Pr = (a.R + groups - 1) / groups;
+  const int Pc = (NV + kSmallColVecs - 1) / kSmallColVecs;
+  Args copy = a;
+  void* args[] = {&copy, &dw, &Pr};
+  return launch_pdl(fn, dim3(static_cast<unsigned>(Pr + Pc)), dim3(kSmallThreads), 0, st,
+                    args);
 }
 
 }  // namespace
@@ -272,21 +309,11 @@ cudaError_t launch_rstd_rows(const BwdArgs& a, float* rstd, cudaStream_t st) {
 }
 
 cudaError_t launch_bwd_small(const BwdArgs& a, float* dw, bool fp32w, cudaStream_t st) {
-  const int NV = a.map.H / 8;
-  const int vpt = (NV + kSmallThreads - 1) / kSmallThreads;  // 1..4 for H <= 8192
-  const void* fn = vpt == 1 ? small_ptr_v<1>(fp32w, a.dh != nullptr)
-                 : vpt == 2 ? small_ptr_v<2>(fp32w, a.dh != nullptr)
-                 : vpt == 3 ? small_ptr_v<3>(fp32w, a.dh != nullptr)
-                            : small_ptr_v<4>(fp32w, a.dh != nullptr);
-  const int per = (NV + vpt - 1) / vpt;
-  const int gt = per <= 32 ? 32 : (per + 31) / 32 * 32;
-  const int groups = kSmallThreads / gt;
-  int Pr = (a.R + groups - 1) / groups;
-  const int Pc = (NV + kSmallColVecs - 1) / kSmallColVecs;
-  BwdArgs copy = a;
-  void* args[] = {&copy, &dw, &Pr};
-  return launch_pdl(fn, dim3(static_cast<unsigned>(Pr + Pc)), dim3(kSmallThreads), 0, st,
-                    args);
+  return launch_small<false>(a, dw, fp32w, st);
+}
+
+cudaError_t launch_bwd_small_drop(const BwdDropArgs& a, float* dw, bool fp32w, cudaStream_t st) {
+  return launch_small<true>(a, dw, fp32w, st);
 }
 
 }  // namespace rmsn
