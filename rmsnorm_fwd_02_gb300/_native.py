@@ -1,5 +1,5 @@
 """ctypes binding of ``librmsnorm_train.so`` with the C ABI's names (include/rmsnorm_train.h,
-include/layernorm_train.h and include/dropout_train.h).
+include/layernorm_train.h, include/dropout_train.h and include/groupnorm_train.h).
 
 Argument marshalling only: tensors become device pointers, the current torch stream
 becomes the ``cudaStream_t``, sizes and strides are passed through, and a nonzero status
@@ -52,9 +52,22 @@ SIGNATURES = {
     "rmsnorm_dropout_train_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp,
                                          _size, _i64, _i32, _i32, _f64, _u64, _u64, _vp, _int,
                                          _vp]),
+    # include/groupnorm_train.h
+    "groupnorm_train_fwd_workspace_bytes": (_size, [_int, _i64, _i64, _i32, _i32]),
+    "groupnorm_train_bwd_workspace_bytes": (_size, [_int, _i64, _i64, _i32, _i32]),
+    "groupnorm_train_fwd": (_int, [_vp, _int, _vp, _vp, _int, _vp, _vp, _vp, _vp, _size, _i64,
+                                   _i64, _i32, _i32, _i64, _i64, _f32, _int, _vp]),
+    "groupnorm_train_bwd": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp,
+                                   _size, _i64, _i64, _i32, _i32, _i64, _i64, _int, _vp]),
+    "groupnorm_train_launch_plan": (_int, [_int, _i64, _i64, _i32, _i32, _int,
+                                           C.POINTER(C.c_int64), _int]),
 }
 
 DROPOUT_BF16, DROPOUT_FP32, DROPOUT_FP16 = 0, 1, 2
+GROUPNORM_BF16, GROUPNORM_FP32, GROUPNORM_FP16 = 0, 1, 2
+GROUPNORM_ACT_NONE, GROUPNORM_ACT_SILU, GROUPNORM_ACT_GELU = 0, 1, 2
+GROUPNORM_PLAN_FIELDS = ("on_chip", "channels", "threads", "cluster_ctas", "ctas", "smem",
+                         "samples", "out_ctas")
 
 PLAN_FWD, PLAN_FWD_RESIDUAL, PLAN_BWD, PLAN_BWD_DH, PLAN_BWD_ND, PLAN_BWD_ND_DH = 0, 1, 2, 3, 4, 5
 LN_PLAN_FWD, LN_PLAN_BWD = 0, 1
@@ -247,3 +260,42 @@ def rmsnorm_dropout_train_bwd(h, dy, dh, rstd, w, w_dtype, dx, dresidual, dw, wo
                                          _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("rmsnorm_dropout_train_bwd", st)
+
+
+# ---- group norm (include/groupnorm_train.h) ---------------------------------------------
+
+def groupnorm_train_fwd_workspace_bytes(dtype, N, S, C_, G):
+    return int(lib().groupnorm_train_fwd_workspace_bytes(dtype, N, S, C_, G))
+
+
+def groupnorm_train_bwd_workspace_bytes(dtype, N, S, C_, G):
+    return int(lib().groupnorm_train_bwd_workspace_bytes(dtype, N, S, C_, G))
+
+
+def groupnorm_train_fwd(x, dtype, w, b, wb_dtype, y, mean, rstd, workspace, workspace_bytes, N, S,
+                        C_, G, s_n, s_s, eps, act, stream=None):
+    st = lib().groupnorm_train_fwd(_ptr(x), dtype, _ptr(w), _ptr(b), wb_dtype, _ptr(y),
+                                   _ptr(mean), _ptr(rstd), _ptr(workspace), workspace_bytes, N,
+                                   S, C_, G, s_n, s_s, eps, act, _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("groupnorm_train_fwd", st)
+
+
+def groupnorm_train_bwd(x, dy, dtype, mean, rstd, w, b, wb_dtype, dx, dw, db, workspace,
+                        workspace_bytes, N, S, C_, G, s_n, s_s, act, stream=None):
+    st = lib().groupnorm_train_bwd(_ptr(x), _ptr(dy), dtype, _ptr(mean), _ptr(rstd), _ptr(w),
+                                   _ptr(b), wb_dtype, _ptr(dx), _ptr(dw), _ptr(db),
+                                   _ptr(workspace), workspace_bytes, N, S, C_, G, s_n, s_s, act,
+                                   _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("groupnorm_train_bwd", st)
+
+
+def groupnorm_train_launch_plan(dtype, N, S, C_, G, backward):
+    """The library's group norm launch plan for a shape, as a dict."""
+    out = (C.c_int64 * len(GROUPNORM_PLAN_FIELDS))()
+    st = lib().groupnorm_train_launch_plan(dtype, N, S, C_, G, int(backward), out,
+                                           len(GROUPNORM_PLAN_FIELDS))
+    if st != RMSN_OK:
+        raise RmsnError("groupnorm_train_launch_plan", st)
+    return dict(zip(GROUPNORM_PLAN_FIELDS, (int(v) for v in out)))

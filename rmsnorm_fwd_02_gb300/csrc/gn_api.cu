@@ -1,0 +1,332 @@
+// gn_api.cu -- the group norm C ABI (include/groupnorm_train.h): argument checks, launch
+// planning and kernel launches.  Never allocates, frees or synchronizes; every launch goes on
+// the caller's stream.
+#include <cmath>
+#include <cstdint>
+#include <numeric>
+
+#include "gn_launch.h"
+#include "groupnorm_train.h"  // include/ (on the include path)
+#include "rmsn_common.cuh"
+
+namespace gnorm {
+
+namespace {
+
+constexpr int kMaxC = 4096;
+constexpr int64_t kMaxElements = int64_t{1} << 40;
+constexpr size_t kMaxSmem = 227 * 1024;
+// two CTAs an SM, so that one's loads overlap the other's exchange and stores
+constexpr size_t kHalfSmem = 112 * 1024;
+// The partition is a function of the shape, not of the GPU; its constants suit 152 SMs.
+constexpr int kSMs = 152;
+constexpr int kThreads = 256;  // threads a CTA aims at
+// Bytes a place's slab aims at: at least a DRAM burst of two 64-byte halves.
+constexpr int kSlabBytes = 128, kWideSlabBytes = 256, kMinSlabBytes = 32;
+constexpr int kSmallCta = 16 * 1024;  // staged bytes below which a CTA is not split further
+// two launches: bytes of x (and dy) a pair of launches may take, to be found in L2 again
+constexpr int64_t kL2Bytes = int64_t{48} << 20;
+
+int elem_bytes(int dtype) { return dtype == GROUPNORM_FP32 ? 4 : 2; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The slab of gs groups, and the threads for `rows` places a CTA at most.
+GnShape slab_shape(int dtype, int C, int G, int gs, int64_t rows) {
+  GnShape s{};
+  s.ev = 16 / elem_bytes(dtype);
+  s.cg = C / G;
+  s.gs = gs;
+  s.cs = gs * s.cg;
+  s.vecs = s.cs / s.ev;
+  s.slabs = G / gs;
+  int64_t lanes = s.vecs >= kThreads ? 1 : kThreads / s.vecs;
+  if (lanes > rows) lanes = rows;
+  s.iters = static_cast<int>(ceil_div(rows, lanes));
+  s.lanes = static_cast<int>(ceil_div(rows, s.iters));  // evened out
+  s.threads = (s.lanes * s.vecs + 31) / 32 * 32;
+  s.ctas = 1;
+  return s;
+}
+
+int least_groups(int dtype, int C, int G) {
+  const int ev = 16 / elem_bytes(dtype);
+  return ev / std::gcd(C / G, ev);
+}
+
+// The slab of at least `bytes` a place (fewest groups), or the widest there is.
+int slab_groups(int dtype, int C, int G, int bytes) {
+  const int gs0 = least_groups(dtype, C, G), units = G / gs0;
+  const int one = gs0 * (C / G) * elem_bytes(dtype);
+  int best = gs0;
+  for (int m = 1; m <= units; ++m) {
+    if (units % m != 0) continue;
+    if (one * m / 16 > kMaxThreads) break;
+    best = gs0 * m;
+    if (one * m >= bytes) break;
+  }
+  return best;
+}
+
+// One launch with the slab on chip: the fewest CTAs a cluster that let two CTAs share an SM
+// (else one), more while the GPU has idle SMs and the CTAs are not small; threads == 0 if a
+// cluster of kMaxCluster cannot hold the slab.
+GnShape on_chip_shape(int dtype, int64_t N, int64_t S, int C, int G, int gs, bool bwd) {
+  GnShape best{};
+  for (int k = 1; k <= kMaxCluster; k *= 2) {
+    if (k > 1 && k > S) break;
+    const int64_t rows = ceil_div(S, k);
+    if (rows > (1 << 20)) continue;  // beyond any shared memory
+    GnShape s = slab_shape(dtype, C, G, gs, rows);
+    s.ctas = k;
+    s.on_chip = 1;
+    const size_t stage = gn_stage_bytes(s, bwd);
+    s.smem = stage + gn_extra_floats(s, bwd) * sizeof(float);
+    if (s.smem > kMaxSmem) continue;
+    best = s;
+    if (s.smem > kHalfSmem) continue;
+    if (N * s.slabs * k >= kSMs || stage <= kSmallCta) break;
+  }
+  return best;
+}
+
+GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
+  const int64_t sample = S * C * elem_bytes(dtype) * (bwd ? 2 : 1);
+  // on chip: from slabs of kSlabBytes, narrower while clusters do not hold them or leave SMs
+  // idle
+  GnShape chip{};
+  const int gs0 = least_groups(dtype, C, G);
+  const int one = gs0 * (C / G) * elem_bytes(dtype);
+  for (int bytes = kSlabBytes; bytes >= kMinSlabBytes; bytes /= 2) {
+    const int gs = slab_groups(dtype, C, G, bytes);
+    const GnShape s = on_chip_shape(dtype, N, S, C, G, gs, bwd);
+    if (s.threads != 0) {
+      chip = s;
+      if (N * s.slabs * s.ctas >= kSMs || gn_stage_bytes(s, bwd) <= kSmallCta) break;
+    }
+    if (gs == gs0 || one >= bytes) break;  // no narrower slab
+  }
+  if (chip.threads != 0) {
+    const int64_t most = 16 * kSMs / (static_cast<int64_t>(chip.slabs) * chip.ctas);
+    chip.lanes_n = static_cast<int>(N < most ? N : (most > 0 ? most : 1));
+    chip.samples = N < INT32_MAX ? static_cast<int>(N) : INT32_MAX;
+    return chip;
+  }
+  // two launches
+  const int gs = slab_groups(dtype, C, G, kWideSlabBytes);
+  GnShape s = slab_shape(dtype, C, G, gs, S);
+  int64_t per = kL2Bytes / (sample > 0 ? sample : 1);
+  if (per < 1) per = 1;
+  s.samples = static_cast<int>(N < per ? N : per);
+  s.ctas = 1;
+  while (s.ctas < kMaxCluster && S >= static_cast<int64_t>(s.ctas) * 2 * s.lanes * 4) s.ctas *= 2;
+  const int64_t units = static_cast<int64_t>(s.samples) * s.slabs;
+  const int64_t lane_rows = static_cast<int64_t>(s.ctas) * s.lanes;  // places a cluster step
+  int64_t chunks = ceil_div(2 * kSMs, units * s.ctas);
+  if (chunks > S / (lane_rows * 8)) chunks = S / (lane_rows * 8);
+  if (chunks < ceil_div(S, lane_rows * 256)) chunks = ceil_div(S, lane_rows * 256);
+  if (chunks < 1) chunks = 1;
+  s.chunks = static_cast<int>(chunks);
+  s.iters = static_cast<int>(ceil_div(ceil_div(ceil_div(S, chunks), s.ctas), s.lanes));
+  int64_t parts = ceil_div(8 * kSMs, units);
+  if (parts > ceil_div(S, static_cast<int64_t>(s.lanes) * 4))
+    parts = ceil_div(S, static_cast<int64_t>(s.lanes) * 4);
+  // a CTA's places fit 31 bits
+  s.parts = static_cast<int>(parts);
+  s.part_iters = static_cast<int>(ceil_div(ceil_div(S, parts), s.lanes));
+  s.smem = gn_extra_floats(s, bwd) * sizeof(float);
+  return s;
+}
+
+int check_sizes(int dtype, int64_t N, int64_t S, int32_t C, int32_t G) {
+  if (dtype != GROUPNORM_BF16 && dtype != GROUPNORM_FP32 && dtype != GROUPNORM_FP16)
+    return RMSN_ERR_INVALID_ARG;
+  if (N < 0 || S < 0 || (N > 0 && S == 0) || C <= 0 || G <= 0 || C % 8 != 0 || C % G != 0)
+    return RMSN_ERR_INVALID_ARG;
+  if (C > kMaxC || N > INT32_MAX || S > INT32_MAX) return RMSN_ERR_UNSUPPORTED;
+  if (least_groups(dtype, C, G) * (C / G) * elem_bytes(dtype) / 16 > kMaxThreads)
+    return RMSN_ERR_UNSUPPORTED;
+  if (N > 0 && N > (kMaxElements - 1) / (S * C)) return RMSN_ERR_UNSUPPORTED;
+  return RMSN_OK;
+}
+
+size_t part_bytes(const GnShape& s, int64_t N, int G) {
+  if (s.on_chip) return 0;
+  const size_t n = static_cast<size_t>(N) * s.chunks * G * sizeof(float2);
+  return (n + 15) & ~static_cast<size_t>(15);
+}
+int64_t col_rows(const GnShape& s, int64_t N) {
+  return s.on_chip ? static_cast<int64_t>(s.lanes_n) * s.ctas : N * s.chunks * s.ctas;
+}
+size_t workspace_bytes(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
+  const GnShape s = plan(dtype, N, S, C, G, bwd);
+  return part_bytes(s, N, G) +
+         (bwd ? static_cast<size_t>(col_rows(s, N)) * 2 * C * sizeof(float) : 0);
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int check_common(int dtype, const void* x, const void* out, const void* w, const void* b,
+                 int wb_dtype, const float* mean, const float* rstd, const void* workspace,
+                 int64_t N, int64_t S, int32_t C, int32_t G, int64_t s_n, int64_t s_s, int act) {
+  const int st = check_sizes(dtype, N, S, C, G);
+  if (st != RMSN_OK) return st;
+  if (wb_dtype != GROUPNORM_BF16 && wb_dtype != GROUPNORM_FP32 && wb_dtype != GROUPNORM_FP16)
+    return RMSN_ERR_INVALID_ARG;
+  if (act != GROUPNORM_ACT_NONE && act != GROUPNORM_ACT_SILU && act != GROUPNORM_ACT_GELU)
+    return RMSN_ERR_INVALID_ARG;
+  if (!w || !b || (N > 0 && (!x || !out || !mean || !rstd))) return RMSN_ERR_INVALID_ARG;
+  const unsigned wa = static_cast<unsigned>(elem_bytes(wb_dtype));
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w, wa) || !aligned(b, wa) ||
+      !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16))
+    return RMSN_ERR_INVALID_ARG;
+  const int ev = 16 / elem_bytes(dtype);
+  if (s_n < 0 || s_s < 0 || s_n % ev != 0 || s_s % ev != 0) return RMSN_ERR_INVALID_ARG;
+  return RMSN_OK;
+}
+
+GnArgs make_args(const void* x, const void* w, const void* b, int wb_dtype, void* out,
+                 float* mean, float* rstd, void* workspace, int64_t N, int64_t S, int32_t C,
+                 int32_t G, int64_t s_n, int64_t s_s, const GnShape& s) {
+  GnArgs a{};
+  a.x = x;
+  a.w = w;
+  a.b = b;
+  a.out = out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.part = static_cast<float2*>(workspace);
+  a.cols = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + part_bytes(s, N, G));
+  a.s_n = s_n;
+  a.s_s = s_s;
+  a.n0 = 0;
+  a.n1 = N;
+  a.S = S;
+  a.C = C;
+  a.G = G;
+  a.wb_dtype = wb_dtype;
+  a.s = s;
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_cluster(const void* fn, int64_t ctas, const GnShape& s, const GnArgs& a,
+                           cudaStream_t st) {
+  cudaError_t e = rmsn::prepare_kernel(fn, s.smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(s.threads));
+  cfg.dynamicSmemBytes = s.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(s.ctas);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = s.ctas > 1 ? 2 : 1;
+  GnArgs copy = a;
+  void* args[] = {&copy};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace gnorm
+
+using namespace gnorm;
+
+extern "C" {
+
+size_t groupnorm_train_fwd_workspace_bytes(int dtype, int64_t N, int64_t S, int32_t C,
+                                           int32_t G) {
+  if (check_sizes(dtype, N, S, C, G) != RMSN_OK || N == 0) return 0;
+  return workspace_bytes(dtype, N, S, C, G, false);
+}
+
+size_t groupnorm_train_bwd_workspace_bytes(int dtype, int64_t N, int64_t S, int32_t C,
+                                           int32_t G) {
+  if (check_sizes(dtype, N, S, C, G) != RMSN_OK || N == 0) return 0;
+  return workspace_bytes(dtype, N, S, C, G, true);
+}
+
+int groupnorm_train_fwd(const void* x, int dtype, const void* w, const void* b, int wb_dtype,
+                        void* y, float* mean, float* rstd, void* workspace,
+                        size_t workspace_bytes, int64_t N, int64_t S, int32_t C, int32_t G,
+                        int64_t s_n, int64_t s_s, float eps, int act, void* stream) {
+  int st = check_common(dtype, x, y, w, b, wb_dtype, mean, rstd, workspace, N, S, C, G, s_n, s_s,
+                        act);
+  if (st != RMSN_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.f) return RMSN_ERR_INVALID_ARG;
+  if (N == 0) return RMSN_OK;
+  const GnShape s = plan(dtype, N, S, C, G, false);
+  const size_t need = part_bytes(s, N, G);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return RMSN_ERR_WORKSPACE;
+  if ((st = rmsn::check_device()) != RMSN_OK) return st;
+  const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  GnArgs a = make_args(x, w, b, wb_dtype, y, mean, rstd, workspace, N, S, C, G, s_n, s_s, s);
+  a.eps = eps;
+  if (s.on_chip)
+    return launch_gn_fwd(a, dtype, act, stream_) == cudaSuccess ? RMSN_OK : RMSN_ERR_CUDA;
+  for (a.n0 = 0; a.n0 < N; a.n0 += s.samples) {
+    a.n1 = a.n0 + s.samples < N ? a.n0 + s.samples : N;
+    if (launch_gn_fwd(a, dtype, act, stream_) != cudaSuccess ||
+        launch_gn_fwd_out(a, dtype, act, stream_) != cudaSuccess)
+      return RMSN_ERR_CUDA;
+  }
+  return RMSN_OK;
+}
+
+int groupnorm_train_bwd(const void* x, const void* dy, int dtype, const float* mean,
+                        const float* rstd, const void* w, const void* b, int wb_dtype, void* dx,
+                        float* dw, float* db, void* workspace, size_t workspace_bytes, int64_t N,
+                        int64_t S, int32_t C, int32_t G, int64_t s_n, int64_t s_s, int act,
+                        void* stream) {
+  int st = check_common(dtype, x, dx, w, b, wb_dtype, mean, rstd, workspace, N, S, C, G, s_n, s_s,
+                        act);
+  if (st != RMSN_OK) return st;
+  if (!dw || !db || (N > 0 && !dy)) return RMSN_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(dw, 4) || !aligned(db, 4)) return RMSN_ERR_INVALID_ARG;
+  GnShape s{};
+  int64_t rows = 0;
+  if (N > 0) {
+    s = plan(dtype, N, S, C, G, true);
+    rows = col_rows(s, N);
+    const size_t need = part_bytes(s, N, G) + static_cast<size_t>(rows) * 2 * C * sizeof(float);
+    if (workspace == nullptr || workspace_bytes < need) return RMSN_ERR_WORKSPACE;
+  }
+  if ((st = rmsn::check_device()) != RMSN_OK) return st;
+  const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  GnArgs a = make_args(x, w, b, wb_dtype, dx, const_cast<float*>(mean), const_cast<float*>(rstd),
+                       workspace, N, S, C, G, s_n, s_s, s);
+  a.dy = dy;
+  if (N > 0 && s.on_chip) {
+    if (launch_gn_bwd(a, dtype, act, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
+  } else {
+    for (a.n0 = 0; a.n0 < N; a.n0 += s.samples) {
+      a.n1 = a.n0 + s.samples < N ? a.n0 + s.samples : N;
+      if (launch_gn_bwd(a, dtype, act, stream_) != cudaSuccess ||
+          launch_gn_bwd_out(a, dtype, act, stream_) != cudaSuccess)
+        return RMSN_ERR_CUDA;
+    }
+  }
+  return launch_gn_finish(a.cols, dw, db, rows, C, stream_) == cudaSuccess ? RMSN_OK
+                                                                         : RMSN_ERR_CUDA;
+}
+
+int groupnorm_train_launch_plan(int dtype, int64_t N, int64_t S, int32_t C, int32_t G,
+                                int backward, int64_t* out, int n_out) {
+  if (!out || n_out < 0 || (backward != 0 && backward != 1)) return RMSN_ERR_INVALID_ARG;
+  const int st = check_sizes(dtype, N, S, C, G);
+  if (st != RMSN_OK) return st;
+  if (N == 0) return RMSN_ERR_INVALID_ARG;
+  const GnShape s = plan(dtype, N, S, C, G, backward != 0);
+  const int64_t v[GROUPNORM_PLAN_FIELDS] = {
+      s.on_chip, s.cs, s.threads, s.ctas, gn_stats_ctas(s, s.samples),
+      static_cast<int64_t>(s.smem), s.samples, s.on_chip ? 0 : gn_out_ctas(s, s.samples)};
+  for (int i = 0; i < n_out && i < GROUPNORM_PLAN_FIELDS; ++i) out[i] = v[i];
+  return RMSN_OK;
+}
+
+}  // extern "C"
