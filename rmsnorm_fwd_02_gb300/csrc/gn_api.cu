@@ -15,15 +15,16 @@ namespace {
 
 constexpr int kMaxC = 4096;
 constexpr int64_t kMaxElements = int64_t{1} << 40;
-constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kMaxSmem = 227 * 1024;  // a CTA's
+constexpr size_t kSmSmem = 220 * 1024;   // an SM's, over the CTAs it holds
 // two CTAs an SM, so that one's loads overlap the other's exchange and stores
-constexpr size_t kHalfSmem = 112 * 1024;
+constexpr size_t kHalfSmem = kSmSmem / 2;
 // The partition is a function of the shape, not of the GPU; its constants suit 152 SMs.
 constexpr int kSMs = 152;
-constexpr int kThreads = 256;  // threads a CTA aims at
 // Bytes a place's slab aims at: at least a DRAM burst of two 64-byte halves.
 constexpr int kSlabBytes = 128, kWideSlabBytes = 256, kMinSlabBytes = 32;
 constexpr int kSmallCta = 16 * 1024;  // staged bytes below which a CTA is not split further
+constexpr int kMaxStages = 4;
 // two launches: bytes of x (and dy) a pair of launches may take, to be found in L2 again
 constexpr int64_t kL2Bytes = int64_t{48} << 20;
 
@@ -60,7 +61,7 @@ int slab_groups(int dtype, int C, int G, int bytes) {
   int best = gs0;
   for (int m = 1; m <= units; ++m) {
     if (units % m != 0) continue;
-    if (one * m / 16 > kMaxThreads) break;
+    if (one * m / 16 > kWideThreads) break;
     best = gs0 * m;
     if (one * m >= bytes) break;
   }
@@ -78,7 +79,9 @@ GnShape on_chip_shape(int dtype, int64_t N, int64_t S, int C, int G, int gs, boo
     if (rows > (1 << 20)) continue;  // beyond any shared memory
     GnShape s = slab_shape(dtype, C, G, gs, rows);
     s.ctas = k;
+    s.ctas_log2 = k == 1 ? 0 : (k == 2 ? 1 : (k == 4 ? 2 : 3));
     s.on_chip = 1;
+    s.stages = 1;
     const size_t stage = gn_stage_bytes(s, bwd);
     s.smem = stage + gn_extra_floats(s, bwd) * sizeof(float);
     if (s.smem > kMaxSmem) continue;
@@ -87,6 +90,31 @@ GnShape on_chip_shape(int dtype, int64_t N, int64_t S, int C, int G, int gs, boo
     if (N * s.slabs * k >= kSMs || stage <= kSmallCta) break;
   }
   return best;
+}
+
+// How many clusters take a slab's samples, and how many samples each has staged: all at once
+// while the SMs hold a CTA for every piece, else a loop over samples with the next ones on
+// their way -- as many CTAs an SM as leave two stages each (two at least, while two fit).
+void on_chip_loop(GnShape* s, int64_t N, bool bwd) {
+  const size_t stage = gn_stage_bytes(*s, bwd), extra = s->smem - stage;
+  const bool wide = s->vecs > kThreads;
+  int most = min_ctas(wide) * max_threads(wide) / s->threads;  // by registers
+  if (most > 16) most = 16;
+  int ctas = static_cast<int>(kSmSmem / (2 * stage + extra));
+  if (ctas < 2 && 2 * s->smem <= kSmSmem) ctas = 2;
+  ctas = ctas < 1 ? 1 : (ctas > most ? most : ctas);
+  const int64_t clusters = static_cast<int64_t>(s->slabs) * s->ctas;  // CTAs of one sample
+  int64_t lanes = static_cast<int64_t>(kSMs) * ctas / clusters;
+  if (lanes < 1) lanes = 1;
+  if (N <= lanes) {
+    s->lanes_n = static_cast<int>(N);
+    return;
+  }
+  s->lanes_n = static_cast<int>(lanes);
+  const size_t room = kSmSmem / ctas;
+  int stages = room > extra ? static_cast<int>((room - extra) / stage) : 1;
+  s->stages = stages < 1 ? 1 : (stages > kMaxStages ? kMaxStages : stages);
+  s->smem = stage * s->stages + extra;
 }
 
 GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
@@ -106,9 +134,8 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
     if (gs == gs0 || one >= bytes) break;  // no narrower slab
   }
   if (chip.threads != 0) {
-    const int64_t most = 16 * kSMs / (static_cast<int64_t>(chip.slabs) * chip.ctas);
-    chip.lanes_n = static_cast<int>(N < most ? N : (most > 0 ? most : 1));
-    chip.samples = N < INT32_MAX ? static_cast<int>(N) : INT32_MAX;
+    on_chip_loop(&chip, N, bwd);
+    chip.samples = static_cast<int>(N);
     return chip;
   }
   // two launches
@@ -117,23 +144,29 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
   int64_t per = kL2Bytes / (sample > 0 ? sample : 1);
   if (per < 1) per = 1;
   s.samples = static_cast<int>(N < per ? N : per);
-  s.ctas = 1;
-  while (s.ctas < kMaxCluster && S >= static_cast<int64_t>(s.ctas) * 2 * s.lanes * 4) s.ctas *= 2;
+  while (s.ctas < kMaxCluster && S >= static_cast<int64_t>(s.ctas) * 2 * s.lanes * 4) {
+    s.ctas *= 2;
+    ++s.ctas_log2;
+  }
   const int64_t units = static_cast<int64_t>(s.samples) * s.slabs;
   const int64_t lane_rows = static_cast<int64_t>(s.ctas) * s.lanes;  // places a cluster step
-  int64_t chunks = ceil_div(2 * kSMs, units * s.ctas);
+  // at most one wave of the statistics kernel, each thread 8 to 256 places
+  int64_t chunks = kSMs * kCtas / (units * s.ctas);
   if (chunks > S / (lane_rows * 8)) chunks = S / (lane_rows * 8);
   if (chunks < ceil_div(S, lane_rows * 256)) chunks = ceil_div(S, lane_rows * 256);
-  if (chunks < 1) chunks = 1;
   s.chunks = static_cast<int>(chunks);
-  s.iters = static_cast<int>(ceil_div(ceil_div(ceil_div(S, chunks), s.ctas), s.lanes));
-  int64_t parts = ceil_div(8 * kSMs, units);
+  s.chunk_base = static_cast<int>(S / chunks);
+  s.chunk_more = static_cast<int>(S % chunks);
+  s.iters = 0;  // nothing stays staged
+  // two waves of the second kernel, a thread four places at least
+  int64_t parts = 2 * kSMs * kCtas / units;
   if (parts > ceil_div(S, static_cast<int64_t>(s.lanes) * 4))
     parts = ceil_div(S, static_cast<int64_t>(s.lanes) * 4);
-  // a CTA's places fit 31 bits
+  if (parts < 1) parts = 1;
   s.parts = static_cast<int>(parts);
-  s.part_iters = static_cast<int>(ceil_div(ceil_div(S, parts), s.lanes));
-  s.smem = gn_extra_floats(s, bwd) * sizeof(float);
+  s.part_base = static_cast<int>(S / parts);
+  s.part_more = static_cast<int>(S % parts);
+  s.smem = gn_stage_bytes(s, bwd) + gn_extra_floats(s, bwd) * sizeof(float);
   return s;
 }
 
@@ -143,7 +176,7 @@ int check_sizes(int dtype, int64_t N, int64_t S, int32_t C, int32_t G) {
   if (N < 0 || S < 0 || (N > 0 && S == 0) || C <= 0 || G <= 0 || C % 8 != 0 || C % G != 0)
     return RMSN_ERR_INVALID_ARG;
   if (C > kMaxC || N > INT32_MAX || S > INT32_MAX) return RMSN_ERR_UNSUPPORTED;
-  if (least_groups(dtype, C, G) * (C / G) * elem_bytes(dtype) / 16 > kMaxThreads)
+  if (least_groups(dtype, C, G) * (C / G) * elem_bytes(dtype) / 16 > kWideThreads)
     return RMSN_ERR_UNSUPPORTED;
   if (N > 0 && N > (kMaxElements - 1) / (S * C)) return RMSN_ERR_UNSUPPORTED;
   return RMSN_OK;
@@ -209,6 +242,16 @@ GnArgs make_args(const void* x, const void* w, const void* b, int wb_dtype, void
 }
 
 }  // namespace
+
+cudaError_t launch_out(const void* fn, const GnArgs& a, bool bwd, cudaStream_t st) {
+  const size_t smem = gn_out_smem(a.s, bwd);
+  const cudaError_t e = rmsn::prepare_kernel(fn, smem);
+  if (e != cudaSuccess) return e;
+  GnArgs copy = a;
+  void* args[] = {&copy};
+  return rmsn::launch_pdl(fn, dim3(static_cast<unsigned>(gn_out_ctas(a.s, a.n1 - a.n0))),
+                          dim3(static_cast<unsigned>(a.s.threads)), smem, st, args);
+}
 
 cudaError_t launch_cluster(const void* fn, int64_t ctas, const GnShape& s, const GnArgs& a,
                            cudaStream_t st) {

@@ -13,63 +13,53 @@
 
 namespace gnorm {
 
-// A thread's constants for its channels: xhat = (x - mean) * rstd, z = xhat * w + b.
+// A thread's constants for its channels: d = x - mean, z = d * scale + bias, scale = rstd * w.
 template <typename T>
 struct Consts {
   static constexpr int kPairs = VecOf<T>::kPairs;
-  f2 mean[kPairs], rstd[kPairs], w[kPairs], b[kPairs];
-  __device__ __forceinline__ void load_params(const GnArgs& a, int ch) {
+  f2 nm[kPairs], scale[kPairs], bias[kPairs];
+  // w, b: the slab's parameters in shared memory; mean, rstd: the sample's group values from the
+  // slab's first group on; c: the thread's first channel, place r of group g
+  __device__ __forceinline__ void load(const float* w, const float* b, const float* mean,
+                                       const float* rstd, int cg, int c, int g, int r) {
+    lds_pairs<kPairs>(w + c, scale);
+    lds_pairs<kPairs>(b + c, bias);
+    float m = mean[g], q = rstd[g];
+    float v[2 * kPairs], u[2 * kPairs];
+#pragma unroll
+    for (int j = 0; j < 2 * kPairs; ++j) {
+      v[j] = -m;
+      u[j] = q;
+      if (j + 1 < 2 * kPairs && ++r == cg) {
+        r = 0;
+        ++g;
+        m = mean[g];
+        q = rstd[g];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      w[i] = f2_make(load_param(a.w, a.wb_dtype, ch + 2 * i),
-                     load_param(a.w, a.wb_dtype, ch + 2 * i + 1));
-      b[i] = f2_make(load_param(a.b, a.wb_dtype, ch + 2 * i),
-                     load_param(a.b, a.wb_dtype, ch + 2 * i + 1));
+      nm[i] = f2_make(v[2 * i], v[2 * i + 1]);
+      scale[i] = f2_mul(scale[i], f2_make(u[2 * i], u[2 * i + 1]));
     }
   }
-  // group values of sample n, the slab's first group g0 and this thread's first channel c
-  __device__ __forceinline__ void load_stats(const GnArgs& a, int64_t n, int g0, int c) {
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int64_t p = n * a.G + g0 + group_of(a.s, c + 2 * i);
-      const int64_t q = n * a.G + g0 + group_of(a.s, c + 2 * i + 1);
-      mean[i] = f2_make(a.mean[p], a.mean[q]);
-      rstd[i] = f2_make(a.rstd[p], a.rstd[q]);
-    }
+  // pair i of x and dy: d, and dz = dy * act'(z)
+  template <int kAct>
+  __device__ __forceinline__ f2 dz(const uint4& xu, f2 dy, int i, f2& d) const {
+    d = VecOf<T>::plus(xu, i, nm[i]);
+    return act_grad2<kAct>(f2_fma(d, scale[i], bias[i]), dy);
   }
 };
 
-template <typename T, int kAct>
-__device__ __forceinline__ void xhat_dz(const Consts<T>& k, const uint4& xu, const uint4& du,
-                                        f2* xhat, f2* dz) {
-  constexpr int NP = VecOf<T>::kPairs;
-  f2 x[NP], dy[NP];
-  VecOf<T>::unpack(xu, x);
-  VecOf<T>::unpack(du, dy);
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    xhat[i] = f2_mul(f2_sub(x[i], k.mean[i]), k.rstd[i]);
-    dz[i] = act_grad2<T, kAct>(f2_fma(xhat[i], k.w[i], k.b[i]), dy[i]);
-  }
-}
-
-// The group terms of dx: dx = rw * dz - (rc1 + xhat * rc2), with rw = rstd * w and
-// rc1 = rstd * mean(g), rc2 = rstd * mean(g * xhat).
+// The group terms of dx = scale * dz + nc1 + d * nc2, with nc1 = -rstd * mean(g) and
+// nc2 = -rstd^2 * mean(g * xhat).
 template <typename T>
 struct GroupTerms {
   static constexpr int kPairs = VecOf<T>::kPairs;
-  f2 rw[kPairs], nc1[kPairs], nc2[kPairs];  // negated
-  // gf[2 g] = mean(g * xhat), gf[2 g + 1] = mean(g)
-  __device__ __forceinline__ void load(const GnShape& s, const Consts<T>& k, const float* gf,
-                                       int c) {
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int g = group_of(s, c + 2 * i), h = group_of(s, c + 2 * i + 1);
-      const f2 nr = f2_mul(k.rstd[i], f2_splat(-1.f));
-      rw[i] = f2_mul(k.rstd[i], k.w[i]);
-      nc2[i] = f2_mul(nr, f2_make(gf[2 * g], gf[2 * h]));
-      nc1[i] = f2_mul(nr, f2_make(gf[2 * g + 1], gf[2 * h + 1]));
-    }
+  f2 nc1[kPairs], nc2[kPairs];
+  __device__ __forceinline__ void load(const float* c0, const float* c1, int c) {
+    lds_pairs<kPairs>(c0 + c, nc1);
+    lds_pairs<kPairs>(c1 + c, nc2);
   }
 };
 
@@ -77,317 +67,404 @@ template <typename T, int kAct>
 __device__ __forceinline__ uint4 dx_vec(const Consts<T>& k, const GroupTerms<T>& t,
                                         const uint4& xu, const uint4& du) {
   constexpr int NP = VecOf<T>::kPairs;
-  f2 xhat[NP], dz[NP];
-  xhat_dz<T, kAct>(k, xu, du, xhat, dz);
+  f2 v[NP];
+  VecOf<T>::unpack(du, v);
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
-    dz[i] = f2_fma(dz[i], t.rw[i], f2_fma(xhat[i], t.nc2[i], t.nc1[i]));
-  return VecOf<T>::pack(dz);
+  for (int i = 0; i < NP; ++i) {
+    f2 d;
+    const f2 dz = k.template dz<kAct>(xu, v[i], i, d);
+    v[i] = f2_fma(dz, k.scale[i], f2_fma(d, t.nc2[i], t.nc1[i]));
+  }
+  return VecOf<T>::pack(v);
 }
 
-template <typename T, int kAct, bool kOnChip>
-__global__ void __launch_bounds__(kMaxThreads, 1) gn_bwd_kernel(const GnArgs a) {
+// A thread's column sums over its places: A = sum of dz * d, B = sum of dz.
+template <typename T, int kAct>
+struct ColumnSums {
+  static constexpr int kPairs = VecOf<T>::kPairs;
+  f2 A[kPairs], B[kPairs];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) A[i] = B[i] = f2_splat(0.f);
+  }
+  __device__ __forceinline__ void add(const Consts<T>& k, const uint4& xu, const uint4& du) {
+    f2 dy[kPairs];
+    VecOf<T>::unpack(du, dy);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      f2 d;
+      const f2 dz = k.template dz<kAct>(xu, dy[i], i, d);
+      A[i] = f2_fma(dz, d, A[i]);
+      B[i] = f2_add(B[i], dz);
+    }
+  }
+};
+
+template <typename T, int kAct, bool kOnChip, bool kWide>
+__global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
+    gn_bwd_kernel(const GnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int NP = VecOf<T>::kPairs;
   const GnShape& s = a.s;
   const Smem m = carve(smem, s, true);
-  uint4* stage_x = reinterpret_cast<uint4*>(smem);
-  uint4* stage_d = stage_x + static_cast<size_t>(s.iters) * s.threads;
-
+  const Owner o = owner<kOnChip>(a);
   const int tid = threadIdx.x;
-  const int lane = tid / s.vecs, vec = tid - lane * s.vecs;
-  const bool active = lane < s.lanes;
-  const int rank = s.ctas > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
-  const int unit = blockIdx.x / s.ctas;
-  const int slab = unit % s.slabs, rest = unit / s.slabs;
-  const int c = vec * s.ev, ch = slab * s.cs + c;
-  const int chunk = kOnChip ? 0 : rest % s.chunks;
-  const int64_t lo = kOnChip ? 0 : piece_start(a.S, chunk, s.chunks);
-  const int64_t hi = kOnChip ? a.S : piece_start(a.S, chunk + 1, s.chunks);
-  const int64_t r0 = lo + piece_start(hi - lo, rank, s.ctas);
-  const int64_t r1 = lo + piece_start(hi - lo, rank + 1, s.ctas);
-  const int rows = static_cast<int>(r1 - r0);
-  const int cnt = active && lane < rows ? (rows - lane + s.lanes - 1) / s.lanes : 0;
+  const int ch = o.slab * s.cs + o.c, group0 = o.slab * s.gs;
+  const int og = o.c / s.cg, orr = o.c - og * s.cg;
+  const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
+  const T* const px = static_cast<const T*>(a.x) + (o.r0 + o.lane) * a.s_s + ch;
+  const int64_t at0 = (o.r0 + o.lane) * a.C + ch;  // in sample 0 of dy and dx
+  const T* const pd = static_cast<const T*>(a.dy) + at0;
+  const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
 
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
 
-  Consts<T> k;
-  if (active) k.load_params(a, ch);
-  if constexpr (kOnChip)  // running column totals (sum, compensation)
+  // on chip: this thread's slots of stage k are stage[(2 * k * iters + i) * threads] for x, and
+  // iters * threads behind them for dy
+  uint4* const stage = reinterpret_cast<uint4*>(smem) + tid;
+  const int dy_off = s.iters * s.threads;
+  auto stage_places = [&](int64_t n, int k, int from, int to) {
+    if (n < a.n1) {
+      const T* p = px + n * a.s_n + from * step;
+      const T* q = pd + n * a.S * a.C + from * dstep;
+      uint4* d = stage + (2 * k * s.iters + from) * s.threads;
+      for (int i = from; i < min(to, o.cnt); ++i, p += step, q += dstep, d += s.threads) {
+        cp_async_16(d, p);
+        cp_async_16(d + dy_off, q);
+      }
+    }
+    cp_async_commit();
+  };
+  constexpr int kBatches = 4;  // of a single-stage sample
+  const int per = (s.iters + kBatches - 1) / kBatches;
+  int64_t n = a.n0 + (kOnChip ? o.rest : o.rest / s.chunks);
+  if constexpr (kOnChip) {
+    if (s.stages == 1)
+      for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
+    for (int k = 0; k + 1 < s.stages; ++k) stage_places(n + k * s.lanes_n, k, 0, s.iters);
+    // running column totals (sum, compensation)
     for (int i = tid; i < 4 * s.cs; i += s.threads) m.run[i] = 0.f;
+  }
+  Ring<2> ring;
+  if constexpr (!kOnChip) {
+    ring = Ring<2>{stage,
+                   {reinterpret_cast<const unsigned char*>(px + n * a.s_n),
+                    reinterpret_cast<const unsigned char*>(pd + n * a.S * a.C)},
+                   {step * static_cast<int64_t>(sizeof(T)), dstep * static_cast<int64_t>(sizeof(T))},
+                   o.cnt, s.threads, 0};
+    ring.start();
+  }
+  load_params(a, m.w, m.b, o.slab);
+  __syncthreads();
 
-  for (int64_t n = a.n0 + (kOnChip ? rest : rest / s.chunks); n < a.n1;
-       n += kOnChip ? s.lanes_n : a.n1) {
-    const T* px = static_cast<const T*>(a.x) + n * a.s_n + (r0 + lane) * a.s_s + ch;
-    const T* pd = static_cast<const T*>(a.dy) + (n * a.S + r0 + lane) * a.C + ch;
-    const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
-    f2 A[NP], B[NP];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) A[i] = B[i] = f2_splat(0.f);
-    auto add = [&](const uint4& xu, const uint4& du) {
-      f2 xhat[NP], dz[NP];
-      xhat_dz<T, kAct>(k, xu, du, xhat, dz);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        A[i] = f2_fma(dz[i], xhat[i], A[i]);
-        B[i] = f2_add(B[i], dz[i]);
-      }
-    };
+  const int l8 = tid & 7, oct = (tid & 31) >> 3, w = tid >> 5, nw = s.threads >> 5;
+  for (int k = 0; n < a.n1; n += kOnChip ? s.lanes_n : a.n1) {
+    const float* const mean = a.mean + n * a.G + group0;
+    const float* const rstd = a.rstd + n * a.G + group0;
+    Consts<T> q;
+    ColumnSums<T, kAct> sum;
+    sum.clear();
+    const uint4* const mine = stage + 2 * k * s.iters * s.threads;
     if constexpr (kOnChip) {
-      constexpr int kBatches = 4;
-      const int per = (s.iters + kBatches - 1) / kBatches;
-#pragma unroll 1
-      for (int b = 0; b < kBatches; ++b) {
-        const int end = min(cnt, (b + 1) * per);
-        for (int i = b * per; i < end; ++i) {
-          cp_async_16(stage_x + i * s.threads + tid, px + i * step);
-          cp_async_16(stage_d + i * s.threads + tid, pd + i * dstep);
+      if (s.stages == 1) {  // the sums follow the copies, batch by batch
+        if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
+        for (int b = 0; b < kBatches; ++b) {
+          cp_async_wait(kBatches - 1 - b);
+          const int end = min(o.cnt, (b + 1) * per);
+#pragma unroll 2
+          for (int i = b * per; i < end; ++i)
+            sum.add(q, mine[i * s.threads], mine[dy_off + i * s.threads]);
         }
-        cp_async_commit();
-      }
-      if (active) k.load_stats(a, n, slab * s.gs, c);
-#pragma unroll 1
-      for (int b = 0; b < kBatches; ++b) {
-        cp_async_wait(kBatches - 1 - b);
-        const int end = min(cnt, (b + 1) * per);
-        for (int i = b * per; i < end; ++i)
-          add(stage_x[i * s.threads + tid], stage_d[i * s.threads + tid]);
+      } else {
+        const int ahead = s.stages - 1;
+        stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
+                     0, s.iters);
+        if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
+        cp_async_wait(ahead);
+#pragma unroll 2
+        for (int i = 0; i < o.cnt; ++i)
+          sum.add(q, mine[i * s.threads], mine[dy_off + i * s.threads]);
       }
     } else {
-      if (active) k.load_stats(a, n, slab * s.gs, c);
-      constexpr int kU = 4;
-      for (int i = 0; i < cnt; i += kU) {
-        uint4 xu[kU], du[kU];
-#pragma unroll
-        for (int j = 0; j < kU; ++j)
-          if (i + j < cnt) {
-            xu[j] = *reinterpret_cast<const uint4*>(px + (i + j) * step);
-            du[j] = *reinterpret_cast<const uint4*>(pd + (i + j) * dstep);
-          }
-#pragma unroll
-        for (int j = 0; j < kU; ++j)
-          if (i + j < cnt) add(xu[j], du[j]);
-      }
+      if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
+      ring.run([&](int, const uint4* slot) {
+        sum.add(q, *slot, slot[kRingSlots * s.threads]);
+      });
     }
 
-    // column sums over the CTA's places: A in [0, cs), B in [cs, 2 cs)
-    const int plane = s.lanes * s.cs;
-    if (active) {
-      f2* ra = reinterpret_cast<f2*>(m.red) + tid * NP;
-      f2* rb = reinterpret_cast<f2*>(m.red + plane) + tid * NP;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        ra[i] = A[i];
-        rb[i] = B[i];
+    // column sums over the CTA's places: A * rstd (= sum of dz * xhat) in col[0, cs), B in
+    // [cs, 2 cs); a warp takes eight quads of columns, four lanes of each at a time
+    const int rs = red_stride(s), plane = s.lanes * rs;
+    if (o.lane < s.lanes) {
+      sts_pairs<NP>(m.red + o.lane * rs + o.c, sum.A);
+      sts_pairs<NP>(m.red + plane + o.lane * rs + o.c, sum.B);
+    }
+    __syncthreads();
+    const int tasks = (s.cs + 31) >> 5;
+    for (int t = w; t < 2 * tasks; t += nw) {
+      const int half = t >= tasks ? 1 : 0;
+      const int c = 4 * (8 * (t - half * tasks) + l8);
+      const float* p = m.red + half * plane + (c < s.cs ? c : 0);
+      f2 v[2] = {f2_splat(0.f), f2_splat(0.f)};
+#pragma unroll 4
+      for (int l = oct; l < s.lanes; l += 4) {
+        f2 u[2];
+        lds_quad(p + l * rs, u);
+        v[0] = f2_add(v[0], u[0]);
+        v[1] = f2_add(v[1], u[1]);
+      }
+      v[0] = across_octets(v[0]);
+      v[1] = across_octets(v[1]);
+      // lane `oct` of the four keeps column c + oct
+      const float mine_v = oct == 0 ? f2_lo(v[0])
+                           : oct == 1 ? f2_hi(v[0]) : (oct == 2 ? f2_lo(v[1]) : f2_hi(v[1]));
+      if (c < s.cs) {
+        const int cc = c + oct, at = half * s.cs + cc;
+        const float val = half == 0 ? mine_v * rstd[cc / s.cg] : mine_v;
+        m.col[at] = val;
+        if constexpr (kOnChip) {  // Kahan's running sum over the samples
+          const float y = __fsub_rn(val, m.run[2 * at + 1]);
+          const float r = __fadd_rn(m.run[2 * at], y);
+          m.run[2 * at + 1] = __fsub_rn(__fsub_rn(r, m.run[2 * at]), y);
+          m.run[2 * at] = r;
+        } else {
+          a.cols[((n * s.chunks + o.chunk) * s.ctas + o.rank) * 2 * a.C + half * a.C +
+                 o.slab * s.cs + cc] = val;
+        }
       }
     }
     __syncthreads();
-    for (int t = tid; t < 2 * s.cs; t += s.threads) {
-      const float* src = t < s.cs ? m.red + t : m.red + plane + (t - s.cs);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      int l = 0;
-      for (; l + 4 <= s.lanes; l += 4)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += src[(l + j) * s.cs];
-      for (; l < s.lanes; ++l) acc[0] += src[l * s.cs];
-      const float v = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-      m.col[t] = v;
-      if constexpr (kOnChip) {  // Kahan's running sum over the samples
-        const float y = __fsub_rn(v, m.run[2 * t + 1]);
-        const float sum = __fadd_rn(m.run[2 * t], y);
-        m.run[2 * t + 1] = __fsub_rn(__fsub_rn(sum, m.run[2 * t]), y);
-        m.run[2 * t] = sum;
-      }
-    }
-    __syncthreads();
-    // the CTA's group sums of w * A and w * B: a warp a group
-    for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
+    // the CTA's group sums of w * A and w * B: an octet of threads a group
+    for (int b = 4 * w; b < s.gs; b += 4 * nw) {  // whole warps: the shuffles need them
+      const int g = b + oct;
       float sa = 0.f, sb = 0.f;
-      for (int i = tid & 31; i < s.cg; i += 32) {
-        const float w = load_param(a.w, a.wb_dtype, slab * s.cs + g * s.cg + i);
-        sa = __fmaf_rn(w, m.col[g * s.cg + i], sa);
-        sb = __fmaf_rn(w, m.col[s.cs + g * s.cg + i], sb);
-      }
-      sa = warp_allsum(sa);
-      sb = warp_allsum(sb);
-      if ((tid & 31) == 0) {
+      if (g < s.gs)
+        for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
+          sa = __fmaf_rn(m.w[i], m.col[i], sa);
+          sb = __fmaf_rn(m.w[i], m.col[s.cs + i], sb);
+        }
+      sa = octet_sum(sa);
+      sb = octet_sum(sb);
+      if (l8 == 0 && g < s.gs) {
         m.gm[2 * g] = sa;
         m.gm[2 * g + 1] = sb;
       }
     }
-    if constexpr (!kOnChip) {  // this CTA's column sums, for dw and db
-      float* out = a.cols + ((n * s.chunks + chunk) * s.ctas + rank) * 2 * a.C + slab * s.cs;
-      for (int t = tid; t < 2 * s.cs; t += s.threads)
-        out[t < s.cs ? t : a.C + t - s.cs] = m.col[t];
+    // the cluster's: an octet of threads a group, a CTA a thread
+    if (s.ctas > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
     }
-    __syncthreads();
-    gather_cluster(m, s);
-    for (int g = tid; g < s.gs; g += s.threads) {
-      float sa = 0.f, sb = 0.f;
-      for (int q = 0; q < s.ctas; ++q) {
-        sa += m.all[g * s.ctas + q].x;
-        sb += m.all[g * s.ctas + q].y;
-      }
+    for (int b = 4 * w; b < s.gs; b += 4 * nw) {
+      const int g = b + oct;
+      float2 v = make_float2(0.f, 0.f);
+      if (g < s.gs && l8 < s.ctas)
+        v = s.ctas > 1 ? ld_peer_f2(peer_addr(m.gm + 2 * g, static_cast<uint32_t>(l8)))
+                       : make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
+      const float sa = octet_sum(v.x), sb = octet_sum(v.y);
       if constexpr (kOnChip) {
-        const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
-        m.gf[2 * g] = sa / total;
-        m.gf[2 * g + 1] = sb / total;
-      } else if (rank == 0) {
-        a.part[(n * s.chunks + chunk) * a.G + slab * s.gs + g] = make_float2(sa, sb);
+        if (g < s.gs) {
+          const float r = rstd[g];
+          const float nc1 = -r * (sb / total), nc2 = -r * r * (sa / total);
+          for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
+            m.c0[i] = nc1;
+            m.c1[i] = nc2;
+          }
+        }
+      } else if (l8 == 0 && g < s.gs && o.rank == 0) {
+        a.part[(n * s.chunks + o.chunk) * a.G + group0 + g] = make_float2(sa, sb);
       }
     }
+    if (s.ctas > 1) cluster_arrive();  // this CTA's reads of the others are done
     if constexpr (kOnChip) {
       __syncthreads();
-      if (cnt > 0) {
+      if (o.cnt > 0) {
         GroupTerms<T> t;
-        t.load(s, k, m.gf, c);
-        T* po = static_cast<T*>(a.out) + (n * a.S + r0 + lane) * a.C + ch;
+        t.load(m.c0, m.c1, o.c);
+        T* po = static_cast<T*>(a.out) + n * a.S * a.C + at0;
 #pragma unroll 2
-        for (int i = 0; i < cnt; ++i)
-          stg128(po + i * dstep, dx_vec<T, kAct>(k, t, stage_x[i * s.threads + tid],
-                                                 stage_d[i * s.threads + tid]));
+        for (int i = 0; i < o.cnt; ++i, po += dstep)
+          stg128(po, dx_vec<T, kAct>(q, t, mine[i * s.threads], mine[dy_off + i * s.threads]));
+      }
+      if (s.stages == 1) {
+        for (int b = 0; b < kBatches; ++b)
+          stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
+      } else if (++k == s.stages) {
+        k = 0;
       }
     }
-    release_cluster(s);
+    if (s.ctas > 1) cluster_wait();
   }
   if constexpr (kOnChip) {  // this CTA's totals over its samples
-    // (each thread reads the running sums it wrote itself)
-    float* out = a.cols + (static_cast<int64_t>(rest) * s.ctas + rank) * 2 * a.C + slab * s.cs;
+    __syncthreads();
+    float* out = a.cols + (static_cast<int64_t>(o.rest) * s.ctas + o.rank) * 2 * a.C +
+                 o.slab * s.cs;
     for (int t = tid; t < 2 * s.cs; t += s.threads)
       out[t < s.cs ? t : a.C + t - s.cs] = m.run[2 * t];
   }
 }
 
-// The second launch: the chunks' group sums add up (in a fixed order), and dx is formed from x
-// and dy, read again backwards.
-template <typename T, int kAct>
-__global__ void __launch_bounds__(kMaxThreads, 1) gn_bwd_out_kernel(const GnArgs a) {
-  extern __shared__ __align__(128) float gf[];  // [gs][2]
+// The second launch: the chunks' group sums add up (an octet of threads a group, a fixed order),
+// and dx is formed from x and dy, read again backwards.  As in the forward, the first copies do
+// not wait for the sums.
+template <typename T, int kAct, bool kWide>
+__global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
+    gn_bwd_out_kernel(const GnArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const int tid = threadIdx.x;
-  const int lane = tid / s.vecs, vec = tid - lane * s.vecs;
-  const int unit = gridDim.x - 1 - blockIdx.x;
-  const int slab = unit % s.slabs, rest = unit / s.slabs;
-  const int part = rest % s.parts;
-  const int64_t n = a.n0 + rest / s.parts;
-  const int64_t r0 = piece_start(a.S, part, s.parts);
-  const int rows = static_cast<int>(piece_start(a.S, part + 1, s.parts) - r0);
-  const int c = vec * s.ev, ch = slab * s.cs + c;
+  int64_t n;
+  const Owner o = out_owner(a, &n);
+  const int ch = o.slab * s.cs + o.c, group0 = o.slab * s.gs;
+  const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
+  const int64_t at = (n * a.S + o.r0 + o.lane) * a.C + ch;
+  const T* px = static_cast<const T*>(a.x) + n * a.s_n + (o.r0 + o.lane) * a.s_s + ch;
+  Ring<2> ring{reinterpret_cast<uint4*>(smem) + tid,
+               {reinterpret_cast<const unsigned char*>(px),
+                reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.dy) + at)},
+               {step * static_cast<int64_t>(sizeof(T)), dstep * static_cast<int64_t>(sizeof(T))},
+               o.cnt, s.threads, 0};
+  ring.start();
+  float* w = reinterpret_cast<float*>(smem + gn_stage_bytes(s, true));
+  float* b = w + s.cs;
+  float* c0 = b + s.cs;
+  float* c1 = c0 + s.cs;
+  load_params(a, w, b, o.slab);
+  const float* const mean = a.mean + n * a.G + group0;
+  const float* const rstd = a.rstd + n * a.G + group0;
 
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
 
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
-  for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
-    const float2* p = a.part + n * s.chunks * a.G + slab * s.gs + g;
+  const int l8 = tid & 7;
+  for (int g0 = 4 * (tid >> 5); g0 < s.gs; g0 += s.threads >> 3) {
+    const int g = g0 + ((tid & 31) >> 3);
+    const float2* p = a.part + n * s.chunks * a.G + group0 + g;
+    const int chunks = g < s.gs ? s.chunks : 0;
     float sa = 0.f, sb = 0.f;
-    for (int q = tid & 31; q < s.chunks; q += 32) {
+#pragma unroll 4
+    for (int q = l8; q < chunks; q += 8) {
       const float2 v = p[static_cast<int64_t>(q) * a.G];
       sa += v.x;
       sb += v.y;
     }
-    sa = warp_allsum(sa);
-    sb = warp_allsum(sb);
-    if ((tid & 31) == 0) {
-      gf[2 * g] = sa / total;
-      gf[2 * g + 1] = sb / total;
+    sa = octet_sum(sa);
+    sb = octet_sum(sb);
+    if (g < s.gs) {
+      const float r = rstd[g];
+      const float nc1 = -r * (sb / total), nc2 = -r * r * (sa / total);
+      for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
+        c0[i] = nc1;
+        c1[i] = nc2;
+      }
     }
   }
   __syncthreads();
-  if (lane >= s.lanes || lane >= rows) return;
+  if (o.cnt == 0) return;
 
   Consts<T> k;
-  k.load_params(a, ch);
-  k.load_stats(a, n, slab * s.gs, c);
+  const int og = o.c / s.cg;
+  k.load(w, b, mean, rstd, s.cg, o.c, og, o.c - og * s.cg);
   GroupTerms<T> t;
-  t.load(s, k, gf, c);
-  const T* px = static_cast<const T*>(a.x) + n * a.s_n + (r0 + lane) * a.s_s + ch;
-  const int64_t at = (n * a.S + r0 + lane) * a.C + ch;
-  const T* pd = static_cast<const T*>(a.dy) + at;
+  t.load(c0, c1, o.c);
   T* po = static_cast<T*>(a.out) + at;
-  const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
-  const int cnt = (rows - lane + s.lanes - 1) / s.lanes;
-  constexpr int kU = 4;
-  for (int i = 0; i < cnt; i += kU) {
-    uint4 xu[kU], du[kU];
-#pragma unroll
-    for (int j = 0; j < kU; ++j)
-      if (i + j < cnt) {
-        xu[j] = *reinterpret_cast<const uint4*>(px + (i + j) * step);
-        du[j] = *reinterpret_cast<const uint4*>(pd + (i + j) * dstep);
-      }
-#pragma unroll
-    for (int j = 0; j < kU; ++j)
-      if (i + j < cnt)  // dx is not read here again: it leaves L2 first
-        __stcs(reinterpret_cast<uint4*>(po + (i + j) * dstep), dx_vec<T, kAct>(k, t, xu[j], du[j]));
-  }
+  ring.run([&](int, const uint4* slot) {  // dx is not read here again: it leaves L2 first
+    __stcs(reinterpret_cast<uint4*>(po),
+           dx_vec<T, kAct>(k, t, *slot, slot[kRingSlots * s.threads]));
+    po += dstep;
+  });
 }
 
 constexpr int kFinishCols = 32, kFinishSlices = 32;
 
 // dw_c and db_c: column t of the [rows][2 C] sums, 32 slices of rows a column, each added in
-// row order in FP64 and then in slice order.
+// row order (loads a few rows ahead) and then in slice order, with TwoSum's error terms beside.
 __global__ void __launch_bounds__(kFinishCols* kFinishSlices)
     gn_finish_kernel(const float* __restrict__ cols, float* __restrict__ dw,
                      float* __restrict__ db, int64_t rows, int C) {
-  __shared__ double sh[kFinishSlices][kFinishCols + 1];
+  __shared__ float sh[kFinishSlices][kFinishCols + 1], se[kFinishSlices][kFinishCols + 1];
   const int x = threadIdx.x % kFinishCols, y = threadIdx.x / kFinishCols;
   const int t = blockIdx.x * kFinishCols + x;
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
-  double acc = 0.0;
+  float sum = 0.f, err = 0.f;
+  auto add = [&](float v) {
+    const float r = __fadd_rn(sum, v), b = __fsub_rn(r, sum);
+    err += __fadd_rn(__fsub_rn(sum, __fsub_rn(r, b)), __fsub_rn(v, b));
+    sum = r;
+  };
   if (t < 2 * C) {
     const int64_t end = rows * (y + 1) / kFinishSlices;
-    for (int64_t r = rows * y / kFinishSlices; r < end; ++r) acc += cols[r * 2 * C + t];
+    int64_t r = rows * y / kFinishSlices;
+    const float* p = cols + r * 2 * C + t;
+    constexpr int kU = 8;
+    for (; r + kU <= end; r += kU, p += static_cast<int64_t>(kU) * 2 * C) {
+      float v[kU];
+#pragma unroll
+      for (int j = 0; j < kU; ++j) v[j] = p[static_cast<int64_t>(j) * 2 * C];
+#pragma unroll
+      for (int j = 0; j < kU; ++j) add(v[j]);
+    }
+    for (; r < end; ++r, p += 2 * static_cast<int64_t>(C)) add(*p);
   }
-  sh[y][x] = acc;
+  sh[y][x] = sum;
+  se[y][x] = err;
   __syncthreads();
   if (y == 0 && t < 2 * C) {
-    for (int i = 1; i < kFinishSlices; ++i) acc += sh[i][x];
-    (t < C ? dw : db)[t < C ? t : t - C] = static_cast<float>(acc);
+    for (int i = 1; i < kFinishSlices; ++i) {
+      err += se[i][x];
+      add(sh[i][x]);
+    }
+    (t < C ? dw : db)[t < C ? t : t - C] = sum + err;
   }
 }
 
 namespace {
 
-template <typename T, bool kOnChip>
+// The kernel builds for a dtype T, activation and width.
+template <typename T, bool kOnChip, bool kWide>
 const void* pick_sums(int act) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_NONE, kOnChip>)
-         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_SILU, kOnChip>)
-                                     : fn(&gn_bwd_kernel<T, GROUPNORM_ACT_GELU, kOnChip>);
+  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_NONE, kOnChip, kWide>)
+         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_SILU, kOnChip, kWide>)
+                                     : fn(&gn_bwd_kernel<T, GROUPNORM_ACT_GELU, kOnChip, kWide>);
 }
 template <typename T>
-const void* pick_out(int act) {
+const void* pick_bwd(const GnShape& s, int act) {
+  if (s.vecs > kThreads)
+    return s.on_chip ? pick_sums<T, true, true>(act) : pick_sums<T, false, true>(act);
+  return s.on_chip ? pick_sums<T, true, false>(act) : pick_sums<T, false, false>(act);
+}
+template <typename T, bool kWide>
+const void* pick_act(int act) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_NONE>)
-         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_SILU>)
-                                     : fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_GELU>);
+  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_NONE, kWide>)
+         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_SILU, kWide>)
+                                     : fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_GELU, kWide>);
+}
+template <typename T>
+const void* pick_out(const GnShape& s, int act) {
+  return s.vecs > kThreads ? pick_act<T, true>(act) : pick_act<T, false>(act);
 }
 
 }  // namespace
 
 cudaError_t launch_gn_bwd(const GnArgs& a, int dtype, int act, cudaStream_t st) {
-  const bool chip = a.s.on_chip != 0;
-  const void* fn =
-      dtype == GROUPNORM_BF16
-          ? (chip ? pick_sums<__nv_bfloat16, true>(act) : pick_sums<__nv_bfloat16, false>(act))
-      : dtype == GROUPNORM_FP32
-          ? (chip ? pick_sums<float, true>(act) : pick_sums<float, false>(act))
-          : (chip ? pick_sums<__half, true>(act) : pick_sums<__half, false>(act));
+  const void* fn = dtype == GROUPNORM_BF16   ? pick_bwd<__nv_bfloat16>(a.s, act)
+                   : dtype == GROUPNORM_FP32 ? pick_bwd<float>(a.s, act)
+                                             : pick_bwd<__half>(a.s, act);
   return launch_cluster(fn, gn_stats_ctas(a.s, a.n1 - a.n0), a.s, a, st);
 }
 
 cudaError_t launch_gn_bwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st) {
-  const void* fn = dtype == GROUPNORM_BF16   ? pick_out<__nv_bfloat16>(act)
-                   : dtype == GROUPNORM_FP32 ? pick_out<float>(act)
-                                             : pick_out<__half>(act);
-  GnArgs copy = a;
-  void* args[] = {&copy};
-  return launch_pdl(fn, dim3(static_cast<unsigned>(gn_out_ctas(a.s, a.n1 - a.n0))),
-                    dim3(static_cast<unsigned>(a.s.threads)), 8 * static_cast<size_t>(a.s.gs), st,
-                    args);
+  const void* fn = dtype == GROUPNORM_BF16   ? pick_out<__nv_bfloat16>(a.s, act)
+                   : dtype == GROUPNORM_FP32 ? pick_out<float>(a.s, act)
+                                             : pick_out<__half>(a.s, act);
+  return launch_out(fn, a, true, st);
 }
 
 cudaError_t launch_gn_finish(const float* cols, float* dw, float* db, int64_t rows, int C,

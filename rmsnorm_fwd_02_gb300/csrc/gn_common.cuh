@@ -1,5 +1,5 @@
-// gn_common.cuh -- device helpers of the group norm kernels: activations, parameters, and the
-// sums over a CTA and a cluster.
+// gn_common.cuh -- device helpers of the group norm kernels: activations, parameters, staging,
+// and the sums over a CTA and a cluster.
 #pragma once
 
 #include <type_traits>
@@ -26,21 +26,11 @@ __device__ __forceinline__ float rcp_approx(float a) {
   return r;
 }
 
-// 1 / (1 + exp(-z)) of a pair, to a few FP32 roundings.  16-bit activations share one
-// reciprocal between the two (1/a = b * 1/(ab)); exp(-z) is held to 2^62 so that ab stays
-// finite, which leaves sigmoid below 2^-62 at 2^-62 -- and the smaller (the clamp) of a NaN
-// and 62 is 62, so neither element's NaN reaches the other through the product (it stays in z).
-template <typename T>
+// 1 / (1 + exp(-z)) of a pair, to a few FP32 roundings (z below -87: 0).
 __device__ __forceinline__ f2 sigmoid2(f2 z) {
   const f2 t = f2_mul(z, f2_splat(-1.44269504088896340736f));
-  if constexpr (sizeof(T) == 2) {
-    const float a = 1.f + ex2_approx(fminf(f2_lo(t), 62.f));
-    const float b = 1.f + ex2_approx(fminf(f2_hi(t), 62.f));
-    const float r = rcp_approx(a * b);
-    return f2_make(r * b, r * a);
-  } else {
-    return f2_make(rcp_approx(1.f + ex2_approx(f2_lo(t))), rcp_approx(1.f + ex2_approx(f2_hi(t))));
-  }
+  const f2 d = f2_add(f2_make(ex2_approx(f2_lo(t)), ex2_approx(f2_hi(t))), f2_splat(1.f));
+  return f2_make(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
 }
 
 __device__ __forceinline__ float normal_cdf(float z) {
@@ -52,19 +42,19 @@ __device__ __forceinline__ float gelu_slope(float z) {
                    normal_cdf(z));
 }
 
-template <typename T, int kAct>
+template <int kAct>
 __device__ __forceinline__ f2 act2(f2 z) {
-  if constexpr (kAct == GROUPNORM_ACT_SILU) return f2_mul(z, sigmoid2<T>(z));
+  if constexpr (kAct == GROUPNORM_ACT_SILU) return f2_mul(z, sigmoid2(z));
   if constexpr (kAct == GROUPNORM_ACT_GELU)
     return f2_make(f2_lo(z) * normal_cdf(f2_lo(z)), f2_hi(z) * normal_cdf(f2_hi(z)));
   return z;
 }
 
 // dy * act'(z)
-template <typename T, int kAct>
+template <int kAct>
 __device__ __forceinline__ f2 act_grad2(f2 z, f2 dy) {
   if constexpr (kAct == GROUPNORM_ACT_SILU) {  // s + z s (1 - s)
-    const f2 s = sigmoid2<T>(z);
+    const f2 s = sigmoid2(z);
     return f2_mul(dy, f2_fma(f2_mul(z, s), f2_sub(f2_splat(1.f), s), s));
   }
   if constexpr (kAct == GROUPNORM_ACT_GELU)
@@ -77,6 +67,17 @@ __device__ __forceinline__ float load_param(const void* p, int dtype, int i) {
   if (dtype == GROUPNORM_FP32) return static_cast<const float*>(p)[i];
   if (dtype == GROUPNORM_BF16) return widen1(static_cast<const __nv_bfloat16*>(p)[i]);
   return widen1(static_cast<const __half*>(p)[i]);
+}
+
+// 2 kPairs consecutive floats of shared memory (16-byte aligned) as pairs.
+template <int kPairs>
+__device__ __forceinline__ void lds_pairs(const float* p, f2* out) {
+#pragma unroll
+  for (int i = 0; i < kPairs; i += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 2 * i);
+    out[i] = f2_make(v.x, v.y);
+    out[i + 1] = f2_make(v.z, v.w);
+  }
 }
 
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
@@ -111,91 +112,183 @@ __device__ __forceinline__ float2 ld_peer_f2(uint32_t addr) {
   return v;
 }
 
-// First place of piece k of `pieces` of `places` places.
-__device__ __forceinline__ int64_t piece_start(int64_t places, int64_t k, int64_t pieces) {
-  return places * k / pieces;
+// Four neighbouring floats of shared memory (16-byte aligned) as two pairs, and back.
+__device__ __forceinline__ void lds_quad(const float* p, f2 (&v)[2]) { lds_pairs<2>(p, v); }
+__device__ __forceinline__ void sts_quad(float* p, const f2 (&v)[2]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f2_lo(v[0]), f2_hi(v[0]), f2_lo(v[1]), f2_hi(v[1]));
+}
+
+// A thread's 2 kPairs column values to its place in a plane of red.
+template <int kPairs>
+__device__ __forceinline__ void sts_pairs(float* p, const f2* v) {
+#pragma unroll
+  for (int i = 0; i < kPairs; i += 2) {
+    const f2 q[2] = {v[i], v[i + 1]};
+    sts_quad(p + 2 * i, q);
+  }
+}
+
+// Sum over the eight lanes of an aligned octet; every lane gets the same bits.
+__device__ __forceinline__ float octet_sum(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sum over the four octets of a warp, lane by lane.
+__device__ __forceinline__ float across_octets(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+
+__device__ __forceinline__ f2 across_octets(f2 v) {
+  return f2_make(across_octets(f2_lo(v)), across_octets(f2_hi(v)));
+}
+
+// f(i, vector) for i in [from, to), vectors `stride` 16-byte units apart, four loads ahead.
+template <typename F>
+__device__ __forceinline__ void for_staged(const uint4* p, int from, int to, int stride, F f) {
+  int i = from;
+  p += from * stride;
+  for (; i + 4 <= to; i += 4, p += 4 * stride) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = p[j * stride];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f(i + j, u[j]);
+  }
+  for (; i < to; ++i, p += stride) f(i, *p);
+}
+
+// First of `places` places that rank k of a cluster takes.
+__device__ __forceinline__ int rank_start(int places, int k, const GnShape& s) {
+  return static_cast<int>((static_cast<int64_t>(places) * k) >> s.ctas_log2);
 }
 
 struct Smem {
-  float* red;
-  float* parts;
-  float* gm;      // [gs][2]
-  float2* all;    // [gs][ctas]
-  float* gf;      // [gs][2]
-  float* col;     // [2][cs]
-  float* run;     // [2][cs][2]
+  float* red;   // [2][lanes][red_stride]
+  float* gm;    // [gs][2]
+  float* w;     // [cs]
+  float* b;     // [cs]
+  float* c0;    // [cs]
+  float* c1;    // [cs]
+  float* col;   // [2][cs]
+  float* run;   // [2][cs][2]
 };
 __device__ __forceinline__ Smem carve(unsigned char* base, const GnShape& s, bool bwd) {
   Smem m;
-  float* p = reinterpret_cast<float*>(base + gn_stage_bytes(s, bwd));
-  m.red = p;
-  p += (bwd ? 2 : 1) * s.threads * s.ev;
-  // pairs of floats from here on, but for `parts`, which goes last
-  m.gm = p;
-  p += 2 * s.gs;
-  m.all = reinterpret_cast<float2*>(p);
-  p += 2 * s.gs * s.ctas;
-  m.gf = p;
-  p += 2 * s.gs;
-  m.col = p;
-  p += bwd ? 2 * s.cs : 0;
-  m.run = p;
-  p += bwd && s.on_chip ? 4 * s.cs : 0;
-  m.parts = p;
+  float* p = reinterpret_cast<float*>(base + gn_stage_bytes(s, bwd) * (s.on_chip ? s.stages : 1));
+  m.w = p;  // 16-byte aligned: cs is a multiple of 4
+  m.b = m.w + s.cs;
+  m.c0 = m.b + s.cs;
+  m.c1 = m.c0 + s.cs;
+  m.red = m.c1 + s.cs;
+  m.col = m.red + 2 * s.lanes * red_stride(s);
+  m.run = m.col + 2 * s.cs;
+  m.gm = m.run + (bwd && s.on_chip ? 4 * s.cs : 0);
   return m;
 }
+// The slab's parameters to shared memory (no synchronization).
+__device__ __forceinline__ void load_params(const GnArgs& a, float* w, float* b, int slab) {
+  for (int i = threadIdx.x; i < a.s.cs; i += a.s.threads) {
+    w[i] = load_param(a.w, a.wb_dtype, slab * a.s.cs + i);
+    b[i] = load_param(a.b, a.wb_dtype, slab * a.s.cs + i);
+  }
+}
 
-// Sums of red [lanes][cs] over the lanes and channels of each group, in a fixed order, to
-// out[2 g] (stride 2).  Warps share a group's values evenly, then one thread a group adds the
-// warps' parts.  Starts and ends with the CTA synchronized.
-__device__ __forceinline__ void group_sums(const Smem& m, const GnShape& s, float* out) {
-  __syncthreads();
-  const int nw = s.threads >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = s.gs < nw ? nw / s.gs : 1;  // warps a group
-  const int n = s.lanes * s.cg;
-  for (int t = w; t < s.gs * per; t += nw) {
-    const int g = t / per, k = t - g * per;
-    const float* src = m.red + g * s.cg;
-    float acc = 0.f;
-    for (int i = k * 32 + lane; i < n; i += per * 32) {
-      const int l = i / s.cg;
-      acc += src[l * s.cs + (i - l * s.cg)];
+// What a thread of the statistics kernels owns.
+struct Owner {
+  int lane, rank, slab, rest, chunk;
+  int c;            // its first channel in the slab
+  int len;          // places of the chunk
+  int64_t r0;       // first place of the CTA
+  int rows;         // places of the CTA
+  int cnt;          // places of the thread
+};
+template <bool kOnChip>
+__device__ __forceinline__ Owner owner(const GnArgs& a) {
+  const GnShape& s = a.s;
+  Owner o;
+  o.lane = threadIdx.x / s.vecs;
+  o.c = (threadIdx.x - o.lane * s.vecs) * s.ev;
+  o.rank = s.ctas > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
+  const int unit = blockIdx.x >> s.ctas_log2;
+  o.rest = unit / s.slabs;
+  o.slab = unit - o.rest * s.slabs;
+  o.chunk = 0;
+  o.len = static_cast<int>(a.S);
+  o.r0 = 0;
+  if constexpr (!kOnChip) {
+    o.chunk = o.rest % s.chunks;
+    o.len = s.chunk_base + (o.chunk < s.chunk_more ? 1 : 0);
+    o.r0 = static_cast<int64_t>(o.chunk) * s.chunk_base + min(o.chunk, s.chunk_more);
+  }
+  const int start = rank_start(o.len, o.rank, s);
+  o.r0 += start;
+  o.rows = rank_start(o.len, o.rank + 1, s) - start;
+  o.cnt = o.lane < s.lanes && o.lane < o.rows ? (o.rows - o.lane + s.lanes - 1) / s.lanes : 0;
+  return o;
+}
+
+// What a thread of the second launch's kernels owns (no cluster).
+__device__ __forceinline__ Owner out_owner(const GnArgs& a, int64_t* n) {
+  const GnShape& s = a.s;
+  Owner o;
+  o.lane = threadIdx.x / s.vecs;
+  o.c = (threadIdx.x - o.lane * s.vecs) * s.ev;
+  o.rank = 0;
+  const int unit = gridDim.x - 1 - blockIdx.x;  // backwards
+  o.rest = unit / s.slabs;
+  o.slab = unit - o.rest * s.slabs;
+  const int sample = o.rest / s.parts;
+  o.chunk = o.rest - sample * s.parts;
+  *n = a.n0 + sample;
+  o.len = o.rows = s.part_base + (o.chunk < s.part_more ? 1 : 0);
+  o.r0 = static_cast<int64_t>(o.chunk) * s.part_base + min(o.chunk, s.part_more);
+  o.cnt = o.lane < s.lanes && o.lane < o.rows ? (o.rows - o.lane + s.lanes - 1) / s.lanes : 0;
+  return o;
+}
+
+// A thread's own copies through its ring: kTensors 16-byte vectors a place (tensor t's slots
+// kRingGroups * kRingPlaces * threads behind tensor t - 1's), kRingPlaces places a copy group,
+// kRingGroups - 1 groups on their way while one is used.
+template <int kTensors>
+struct Ring {
+  uint4* slot;
+  const unsigned char* p[kTensors];
+  int64_t step[kTensors];  // bytes
+  int cnt, threads, next;
+  __device__ __forceinline__ void issue() {
+#pragma unroll
+    for (int j = 0; j < kRingPlaces; ++j, ++next) {
+      if (next < cnt) {
+        uint4* d = slot + (next & (kRingGroups * kRingPlaces - 1)) * threads;
+#pragma unroll
+        for (int t = 0; t < kTensors; ++t) {
+          cp_async_16(d + t * kRingGroups * kRingPlaces * threads, p[t]);
+          p[t] += step[t];
+        }
+      }
     }
-    acc = warp_allsum(acc);
-    if (lane == 0) m.parts[t] = acc;
+    cp_async_commit();
   }
-  __syncthreads();
-  for (int g = threadIdx.x; g < s.gs; g += s.threads) {
-    float acc = 0.f;
-    for (int k = 0; k < per; ++k) acc += m.parts[g * per + k];
-    out[2 * g] = acc;
+  __device__ __forceinline__ void start() {
+    next = 0;
+#pragma unroll
+    for (int g = 0; g + 1 < kRingGroups; ++g) issue();
   }
-  __syncthreads();
-}
-
-// Gathers every cluster CTA's group values m.gm into m.all[g][k].  Starts and ends with the
-// CTA synchronized; the caller pairs the arrival made here, after its reads, with a
-// cluster_wait() before gm changes or the CTA exits.
-__device__ __forceinline__ void gather_cluster(const Smem& m, const GnShape& s) {
-  if (s.ctas > 1) {
-    cluster_arrive();
-    cluster_wait();
-    for (int i = threadIdx.x; i < s.gs * s.ctas; i += s.threads) {
-      const int g = i / s.ctas, k = i - g * s.ctas;
-      m.all[i] = ld_peer_f2(peer_addr(m.gm + 2 * g, static_cast<uint32_t>(k)));
+  // f(place, its slots' base) for every place of the thread, in order
+  template <typename F>
+  __device__ __forceinline__ void run(F f) {
+    for (int i = 0; i < cnt; i += kRingPlaces) {
+      issue();
+      cp_async_wait(kRingGroups - 1);
+#pragma unroll
+      for (int j = 0; j < kRingPlaces; ++j)
+        if (i + j < cnt)
+          f(i + j, slot + ((i + j) & (kRingGroups * kRingPlaces - 1)) * threads);
     }
-    cluster_arrive();
-  } else {
-    for (int g = threadIdx.x; g < s.gs; g += s.threads)
-      m.all[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
   }
-  __syncthreads();
-}
-__device__ __forceinline__ void release_cluster(const GnShape& s) {
-  if (s.ctas > 1) cluster_wait();
-}
-
-// The group of channel c of a slab.
-__device__ __forceinline__ int group_of(const GnShape& s, int c) { return c / s.cg; }
+};
+constexpr int kRingSlots = kRingGroups * kRingPlaces;
 
 }  // namespace gnorm

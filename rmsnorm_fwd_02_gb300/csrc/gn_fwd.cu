@@ -3,16 +3,16 @@
 //
 // HBM-bound: one read and one write of the activation.  Where a cluster's shared memory holds
 // a sample's slab (gn_launch.h), one launch reads it once: asynchronous 16-byte copies stage
-// each thread's own vectors, the statistics follow them batch by batch as they land, the
-// cluster's CTAs exchange a few floats a group, and the staged vectors are normalized and
-// written.  Larger samples take two launches, the second reading x again -- from L2 where the
-// samples of one pair of launches fit it, which is how many a pair takes.
+// each thread's own vectors (the next samples' on their way meanwhile), the cluster's CTAs
+// exchange a few floats a group, and the staged vectors are normalized and written.  Larger
+// samples take two launches, the second reading x again -- from L2 where the samples of one
+// pair of launches fit it, which is how many a pair takes.
 //
 // Statistics: each thread sums its channels' values less the first of them, K (sum d and
 // sum d^2 of d = x - K), so neither sum cancels when the mean is far from zero; a column's
 // mean is K + sum d / n and its M2 = sum d^2 - (sum d)^2 / n.  Means combine weighted by their
-// counts, and M2 about the combined mean: M2 = sum of M2_i + n_i (mean_i - mean)^2, from
-// threads to the CTA, the cluster and (two launches) the sample.
+// counts, and M2 about the combined mean: M2 = sum of M2_i + n_i (mean_i - mean)^2 -- from
+// threads to columns, groups, the cluster and (two launches) the sample.
 #include "gn_common.cuh"
 
 namespace gnorm {
@@ -20,20 +20,20 @@ namespace gnorm {
 template <typename T>
 struct ColumnStats {
   static constexpr int kPairs = VecOf<T>::kPairs;
-  f2 k[kPairs], s[kPairs], q[kPairs];
-  __device__ __forceinline__ void add(const uint4& u, bool first) {
+  f2 nk[kPairs], s[kPairs], q[kPairs];  // -K, sum d, sum d^2
+  __device__ __forceinline__ void start(const uint4& u) {
     f2 x[kPairs];
     VecOf<T>::unpack(u, x);
-    if (first) {
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        k[i] = x[i];
-        s[i] = q[i] = f2_splat(0.f);
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const f2 d = f2_sub(x[i], k[i]);
+      nk[i] = f2_mul(x[i], f2_splat(-1.f));
+      s[i] = q[i] = f2_splat(0.f);
+    }
+  }
+  __device__ __forceinline__ void add(const uint4& u) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const f2 d = VecOf<T>::plus(u, i, nk[i]);
       s[i] = f2_add(s[i], d);
       q[i] = f2_fma(d, d, q[i]);
     }
@@ -42,278 +42,361 @@ struct ColumnStats {
 
 __device__ __forceinline__ float clamp_below(float v) { return v < 0.f ? 0.f : v; }  // NaN stays
 
-// y of one vector: act((x - mean) * a + b), a = rstd * w.
-template <typename T, int kAct>
-__device__ __forceinline__ uint4 norm_vec(const uint4& u, const f2* mean, const f2* a,
-                                          const f2* b) {
-  constexpr int NP = VecOf<T>::kPairs;
-  f2 x[NP];
-  VecOf<T>::unpack(u, x);
-#pragma unroll
-  for (int i = 0; i < NP; ++i) x[i] = act2<T, kAct>(f2_fma(f2_sub(x[i], mean[i]), a[i], b[i]));
-  return VecOf<T>::pack(x);
-}
-
-// A thread's constants for its channels [c, c + ev) of the slab at channel c0 of x.
+// A thread's constants for its channels: z = (x - mean) * scale + bias, scale = rstd * w.
 template <typename T>
-__device__ __forceinline__ void load_consts(const GnArgs& a, const float* gf, int c, int ch,
-                                            f2* mean, f2* scale, f2* bias) {
+struct Consts {
+  static constexpr int kPairs = VecOf<T>::kPairs;
+  f2 nm[kPairs], scale[kPairs], bias[kPairs];
+  __device__ __forceinline__ void load(const float* c0, const float* c1, const float* b, int c) {
+    lds_pairs<kPairs>(c0 + c, nm);
+    lds_pairs<kPairs>(c1 + c, scale);
+    lds_pairs<kPairs>(b + c, bias);
+  }
+  template <int kAct>
+  __device__ __forceinline__ uint4 norm(const uint4& u) const {
+    f2 z[kPairs];
 #pragma unroll
-  for (int i = 0; i < VecOf<T>::kPairs; ++i) {
-    const int g0 = group_of(a.s, c + 2 * i), g1 = group_of(a.s, c + 2 * i + 1);
-    mean[i] = f2_make(gf[2 * g0], gf[2 * g1]);
-    scale[i] = f2_make(gf[2 * g0 + 1] * load_param(a.w, a.wb_dtype, ch + 2 * i),
-                       gf[2 * g1 + 1] * load_param(a.w, a.wb_dtype, ch + 2 * i + 1));
-    bias[i] = f2_make(load_param(a.b, a.wb_dtype, ch + 2 * i),
-                      load_param(a.b, a.wb_dtype, ch + 2 * i + 1));
+    for (int i = 0; i < kPairs; ++i)
+      z[i] = act2<kAct>(f2_fma(VecOf<T>::plus(u, i, nm[i]), scale[i], bias[i]));
+    return VecOf<T>::pack(z);
+  }
+};
+
+// The CTA's group values (mean, M2) to m.gm from its threads' statistics: columns over the
+// lanes, then groups over their columns (an octet of threads a group).  A warp takes eight
+// quads of columns, four lanes of each at a time: wide loads, and the other warps' issue slots
+// stay free.  A column's lanes combine about lane 0's mean, r: with d = mean_l - r,
+// mean = r + sum n_l d / n and M2 = sum (M2_l + n_l d^2) - (sum n_l d)^2 / n; what that can
+// cancel is at most the number of lanes times the rest.
+template <typename T>
+__device__ __forceinline__ void cta_stats(const Smem& m, const GnShape& s, const Owner& o,
+                                          const ColumnStats<T>& st) {
+  constexpr int NP = VecOf<T>::kPairs;
+  const int rs = red_stride(s), plane = s.lanes * rs;
+  if (o.lane < s.lanes) {
+    const f2 ic = f2_splat(o.cnt > 0 ? 1.f / static_cast<float>(o.cnt) : 0.f);
+    f2 mean[NP], m2[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const f2 sm = f2_mul(st.s[i], ic);  // mean of d
+      mean[i] = o.cnt > 0 ? f2_sub(sm, st.nk[i]) : f2_splat(0.f);
+      m2[i] = o.cnt > 0 ? f2_sub(st.q[i], f2_mul(sm, st.s[i])) : f2_splat(0.f);
+    }
+    sts_pairs<NP>(m.red + o.lane * rs + o.c, mean);
+    sts_pairs<NP>(m.red + plane + o.lane * rs + o.c, m2);
+  }
+  __syncthreads();
+  const int nw = s.threads >> 5, w = threadIdx.x >> 5, l8 = threadIdx.x & 7;
+  const int oct = (threadIdx.x & 31) >> 3;
+  const float rows = static_cast<float>(o.rows);
+  // lane l of the threads has base places, one more below `more`
+  const int base = o.rows / s.lanes, more = o.rows - base * s.lanes;
+  for (int t = w; 32 * t < s.cs; t += nw) {
+    const int c = 4 * (8 * t + l8);
+    const float* p = m.red + (c < s.cs ? c : 0);
+    f2 ref[2], sum[2], q[2];
+    lds_quad(p, ref);
+    sum[0] = sum[1] = q[0] = q[1] = f2_splat(0.f);
+#pragma unroll 2
+    for (int l = oct; l < s.lanes; l += 4) {
+      f2 mean[2], m2[2];
+      lds_quad(p + l * rs, mean);
+      lds_quad(p + plane + l * rs, m2);
+      const f2 n = f2_splat(static_cast<float>(base + (l < more)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const f2 d = f2_sub(mean[i], ref[i]), nd = f2_mul(n, d);
+        sum[i] = f2_add(sum[i], nd);
+        q[i] = f2_add(q[i], f2_fma(nd, d, m2[i]));
+      }
+    }
+    const f2 inv = f2_splat(o.rows > 0 ? 1.f / rows : 0.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sum[i] = across_octets(sum[i]);
+      q[i] = across_octets(q[i]);
+      const f2 d = f2_mul(sum[i], inv);
+      ref[i] = f2_add(ref[i], d);
+      q[i] = f2_sub(q[i], f2_mul(d, sum[i]));
+    }
+    if (oct == 0 && c < s.cs) {
+      sts_quad(m.col + c, ref);
+      sts_quad(m.col + s.cs + c, q);
+    }
+  }
+  __syncthreads();
+  const float icg = 1.f / static_cast<float>(s.cg);
+  for (int g0 = 4 * w; g0 < s.gs; g0 += 4 * nw) {  // whole warps: the shuffles need them
+    const int g = g0 + oct;
+    const float* p = m.col + g * s.cg;
+    float sum = 0.f;
+    if (g < s.gs)
+      for (int i = l8; i < s.cg; i += 8) sum += p[i];
+    const float mean = octet_sum(sum) * icg;
+    float m2 = 0.f;
+    if (g < s.gs)
+      for (int i = l8; i < s.cg; i += 8) {
+        const float d = p[i] - mean;
+        m2 += __fmaf_rn(d * d, rows, p[s.cs + i]);
+      }
+    m2 = octet_sum(m2);
+    if (l8 == 0 && g < s.gs) {
+      m.gm[2 * g] = mean;
+      m.gm[2 * g + 1] = m2;
+    }
   }
 }
 
-template <typename T, int kAct, bool kOnChip>
-__global__ void __launch_bounds__(kMaxThreads, 1) gn_fwd_kernel(const GnArgs a) {
+template <typename T, int kAct, bool kOnChip, bool kWide>
+__global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
+    gn_fwd_kernel(const GnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int NP = VecOf<T>::kPairs;
   const GnShape& s = a.s;
   const Smem m = carve(smem, s, false);
-  uint4* stage = reinterpret_cast<uint4*>(smem);
-
+  const Owner o = owner<kOnChip>(a);
   const int tid = threadIdx.x;
-  const int lane = tid / s.vecs, vec = tid - lane * s.vecs;
-  const bool active = lane < s.lanes;
-  const int rank = s.ctas > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
-  const int unit = blockIdx.x / s.ctas;
-  const int slab = unit % s.slabs, rest = unit / s.slabs;
-  const int c = vec * s.ev, ch = slab * s.cs + c;
-  const int chunk = kOnChip ? 0 : rest % s.chunks;
-  const int64_t lo = kOnChip ? 0 : piece_start(a.S, chunk, s.chunks);
-  const int64_t hi = kOnChip ? a.S : piece_start(a.S, chunk + 1, s.chunks);
-  const int64_t r0 = lo + piece_start(hi - lo, rank, s.ctas);
-  const int64_t r1 = lo + piece_start(hi - lo, rank + 1, s.ctas);
-  const int rows = static_cast<int>(r1 - r0);
-  const int cnt = active && lane < rows ? (rows - lane + s.lanes - 1) / s.lanes : 0;
+  const int ch = o.slab * s.cs + o.c;
+  const int64_t step = s.lanes * a.s_s;
+  const T* const px = static_cast<const T*>(a.x) + (o.r0 + o.lane) * a.s_s + ch;
+  const float total = static_cast<float>(o.len) * static_cast<float>(s.cg);
+  const int l8 = tid & 7;
+  // places and values a group of cluster rank l8
+  const float nk = l8 < s.ctas ? static_cast<float>(rank_start(o.len, l8 + 1, s) -
+                                                    rank_start(o.len, l8, s)) *
+                                     static_cast<float>(s.cg)
+                               : 0.f;
 
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
 
-  for (int64_t n = a.n0 + (kOnChip ? rest : rest / s.chunks); n < a.n1;
-       n += kOnChip ? s.lanes_n : a.n1) {
-    const T* px = static_cast<const T*>(a.x) + n * a.s_n + (r0 + lane) * a.s_s + ch;
-    const int64_t step = s.lanes * a.s_s;
+  // on chip: this thread's slots of stage k are stage[(k * iters + i) * threads]
+  uint4* const stage = reinterpret_cast<uint4*>(smem) + tid;
+  auto stage_places = [&](int64_t n, int k, int from, int to) {
+    if (n < a.n1) {
+      const T* p = px + n * a.s_n + from * step;
+      uint4* d = stage + (k * s.iters + from) * s.threads;
+      for (int i = from; i < min(to, o.cnt); ++i, p += step, d += s.threads) cp_async_16(d, p);
+    }
+    cp_async_commit();
+  };
+  constexpr int kBatches = 4;  // of a single-stage sample
+  const int per = (s.iters + kBatches - 1) / kBatches;
+  int64_t n = a.n0 + (kOnChip ? o.rest : o.rest / s.chunks);
+  if constexpr (kOnChip) {
+    if (s.stages == 1)
+      for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
+    for (int k = 0; k + 1 < s.stages; ++k) stage_places(n + k * s.lanes_n, k, 0, s.iters);
+    load_params(a, m.w, m.b, o.slab);
+  }
+
+  for (int k = 0; n < a.n1; n += kOnChip ? s.lanes_n : a.n1) {
     ColumnStats<T> st;
+    const uint4* const mine = stage + k * s.iters * s.threads;
     if constexpr (kOnChip) {
-      constexpr int kBatches = 4;
-      const int per = (s.iters + kBatches - 1) / kBatches;
-#pragma unroll 1
-      for (int b = 0; b < kBatches; ++b) {
-        const int end = min(cnt, (b + 1) * per);
-        for (int i = b * per; i < end; ++i)
-          cp_async_16(stage + i * s.threads + tid, px + i * step);
-        cp_async_commit();
-      }
-#pragma unroll 1
-      for (int b = 0; b < kBatches; ++b) {
-        cp_async_wait(kBatches - 1 - b);
-        const int end = min(cnt, (b + 1) * per);
-        for (int i = b * per; i < end; ++i) st.add(stage[i * s.threads + tid], i == 0);
+      if (s.stages == 1) {  // the sums follow the copies, batch by batch
+        for (int b = 0; b < kBatches; ++b) {
+          cp_async_wait(kBatches - 1 - b);
+          if (b == 0 && o.cnt > 0) st.start(mine[0]);
+          for_staged(mine, b * per, min(o.cnt, (b + 1) * per), s.threads,
+                     [&](int, const uint4& u) { st.add(u); });
+        }
+      } else {
+        const int ahead = s.stages - 1;
+        stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
+                     0, s.iters);
+        cp_async_wait(ahead);
+        if (o.cnt > 0) st.start(mine[0]);
+        for_staged(mine, 0, o.cnt, s.threads, [&](int, const uint4& u) { st.add(u); });
       }
     } else {
-      constexpr int kU = 8;
-      for (int i = 0; i < cnt; i += kU) {
-        uint4 u[kU];
-#pragma unroll
-        for (int j = 0; j < kU; ++j)
-          if (i + j < cnt) u[j] = *reinterpret_cast<const uint4*>(px + (i + j) * step);
-#pragma unroll
-        for (int j = 0; j < kU; ++j)
-          if (i + j < cnt) st.add(u[j], i + j == 0);
-      }
+      Ring<1> ring{stage, {reinterpret_cast<const unsigned char*>(px + n * a.s_n)},
+                   {step * static_cast<int64_t>(sizeof(T))}, o.cnt, s.threads, 0};
+      ring.start();
+      ring.run([&](int i, const uint4* slot) {
+        if (i == 0) st.start(*slot);
+        st.add(*slot);
+      });
     }
+    cta_stats(m, s, o, st);
 
-    // the CTA's sums and, about their means, its M2
-    const float fc = static_cast<float>(cnt), ic = cnt > 0 ? 1.f / fc : 0.f;
-    f2* red = reinterpret_cast<f2*>(m.red) + tid * NP;
-    if (active) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-        red[i] = cnt > 0 ? f2_fma(f2_splat(fc), st.k[i], st.s[i]) : f2_splat(0.f);
+    // the cluster's group values: an octet of threads a group, a CTA a thread
+    if (s.ctas > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
     }
-    group_sums(m, s, m.gm);
-    const float cta_n = static_cast<float>(rows) * static_cast<float>(s.cg);
-    if (active) {
-      const float inv = rows > 0 ? 1.f / cta_n : 0.f;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const f2 gm = f2_make(m.gm[2 * group_of(s, c + 2 * i)] * inv,
-                              m.gm[2 * group_of(s, c + 2 * i + 1)] * inv);
-        const f2 sm = f2_mul(st.s[i], f2_splat(ic));           // mean of d
-        const f2 m2 = f2_sub(st.q[i], f2_mul(sm, st.s[i]));
-        const f2 d = f2_add(f2_sub(st.k[i], gm), sm);
-        red[i] = cnt > 0 ? f2_fma(f2_mul(d, d), f2_splat(fc), m2) : f2_splat(0.f);
-      }
-    }
-    group_sums(m, s, m.gm + 1);
-
-    // the cluster's
-    gather_cluster(m, s);
-    for (int g = tid; g < s.gs; g += s.threads) {
-      const float total = static_cast<float>(hi - lo) * static_cast<float>(s.cg);
-      float sum = 0.f;
-      for (int k = 0; k < s.ctas; ++k) sum += m.all[g * s.ctas + k].x;
-      const float mean = sum / total;
-      float m2 = 0.f;
-      for (int k = 0; k < s.ctas; ++k) {
-        const float2 v = m.all[g * s.ctas + k];
-        const float nk = static_cast<float>(piece_start(hi - lo, k + 1, s.ctas) -
-                                            piece_start(hi - lo, k, s.ctas)) *
-                         static_cast<float>(s.cg);
-        const float d = nk > 0.f ? v.x / nk - mean : 0.f;
-        m2 += __fmaf_rn(d * d, nk, v.y);
-      }
-      const int64_t at = n * a.G + slab * s.gs + g;
+    for (int g0 = 4 * (tid >> 5); g0 < s.gs; g0 += s.threads >> 3) {
+      const int g = g0 + ((tid & 31) >> 3);
+      float2 v = make_float2(0.f, 0.f);
+      if (g < s.gs && l8 < s.ctas)
+        v = s.ctas > 1 ? ld_peer_f2(peer_addr(m.gm + 2 * g, static_cast<uint32_t>(l8)))
+                       : make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
+      const float mean = octet_sum(nk * v.x) / total;
+      const float d = nk > 0.f ? v.x - mean : 0.f;
+      const float m2 = octet_sum(__fmaf_rn(d * d, nk, v.y));
       if constexpr (kOnChip) {
         const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
-        m.gf[2 * g] = mean;
-        m.gf[2 * g + 1] = rstd;
-        if (rank == 0) {
-          a.mean[at] = mean;
-          a.rstd[at] = rstd;
+        if (g < s.gs) {
+          for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
+            m.c0[i] = -mean;
+            m.c1[i] = rstd * m.w[i];
+          }
+          if (l8 == 0 && o.rank == 0) {
+            a.mean[n * a.G + o.slab * s.gs + g] = mean;
+            a.rstd[n * a.G + o.slab * s.gs + g] = rstd;
+          }
         }
-      } else if (rank == 0) {
-        a.part[(n * s.chunks + chunk) * a.G + slab * s.gs + g] = make_float2(mean, m2);
+      } else if (l8 == 0 && g < s.gs && o.rank == 0) {
+        a.part[(n * s.chunks + o.chunk) * a.G + o.slab * s.gs + g] = make_float2(mean, m2);
       }
     }
+    if (s.ctas > 1) cluster_arrive();  // this CTA's reads of the others are done
     if constexpr (kOnChip) {
       __syncthreads();
-      if (cnt > 0) {
-        f2 mean[NP], scale[NP], bias[NP];
-        load_consts<T>(a, m.gf, c, ch, mean, scale, bias);
-        T* py = static_cast<T*>(a.out) + (n * a.S + r0 + lane) * a.C + ch;
+      if (o.cnt > 0) {
+        Consts<T> q;
+        q.load(m.c0, m.c1, m.b, o.c);
+        T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
         const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
-#pragma unroll 2
-        for (int i = 0; i < cnt; ++i)
-          stg128(py + i * ystep, norm_vec<T, kAct>(stage[i * s.threads + tid], mean, scale, bias));
+        for_staged(mine, 0, o.cnt, s.threads, [&](int, const uint4& u) {
+          stg128(py, q.template norm<kAct>(u));
+          py += ystep;
+        });
+      }
+      if (s.stages == 1) {
+        for (int b = 0; b < kBatches; ++b)
+          stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
+      } else if (++k == s.stages) {
+        k = 0;
       }
     }
-    release_cluster(s);
+    if (s.ctas > 1) cluster_wait();
   }
 }
 
-// The second launch: the chunks' statistics combine into the sample's (lanes of a warp take
-// the chunks of a group), and the CTA's places are read again, normalized and written.  CTAs
+// The second launch: the chunks' statistics combine into the sample's (an octet of threads
+// takes a group's chunks), and the CTA's places are read again, normalized and written.  CTAs
 // run through the places backwards, so that the last ones the statistics read come first, while
-// L2 still holds them.
-template <typename T, int kAct>
-__global__ void __launch_bounds__(kMaxThreads, 1) gn_fwd_out_kernel(const GnArgs a) {
-  extern __shared__ __align__(128) float gf[];  // [gs][2]
-  constexpr int NP = VecOf<T>::kPairs;
+// L2 still holds them; their first copies are on their way before the statistics are waited
+// for (x is no output of that launch, which itself waited for whatever wrote x).
+template <typename T, int kAct, bool kWide>
+__global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
+    gn_fwd_out_kernel(const GnArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const int tid = threadIdx.x;
-  const int lane = tid / s.vecs, vec = tid - lane * s.vecs;
-  const int unit = gridDim.x - 1 - blockIdx.x;
-  const int slab = unit % s.slabs, rest = unit / s.slabs;
-  const int part = rest % s.parts;
-  const int64_t n = a.n0 + rest / s.parts;
-  const int64_t r0 = piece_start(a.S, part, s.parts);
-  const int rows = static_cast<int>(piece_start(a.S, part + 1, s.parts) - r0);
-  const int c = vec * s.ev, ch = slab * s.cs + c;
+  int64_t n;
+  const Owner o = out_owner(a, &n);
+  const int ch = o.slab * s.cs + o.c;
+  const int64_t step = s.lanes * a.s_s;
+  const T* px = static_cast<const T*>(a.x) + n * a.s_n + (o.r0 + o.lane) * a.s_s + ch;
+  Ring<1> ring{reinterpret_cast<uint4*>(smem) + tid, {reinterpret_cast<const unsigned char*>(px)},
+               {step * static_cast<int64_t>(sizeof(T))}, o.cnt, s.threads, 0};
+  ring.start();
+  float* w = reinterpret_cast<float*>(smem + gn_stage_bytes(s, false));
+  float* b = w + s.cs;
+  float* c0 = b + s.cs;
+  float* c1 = c0 + s.cs;
+  load_params(a, w, b, o.slab);
+  __syncthreads();
 
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
 
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
-  for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
-    const float2* p = a.part + n * s.chunks * a.G + slab * s.gs + g;
+  const float cg = static_cast<float>(s.cg);
+  const int l8 = tid & 7;
+  for (int g0 = 4 * (tid >> 5); g0 < s.gs; g0 += s.threads >> 3) {
+    const int g = g0 + ((tid & 31) >> 3);
+    const float2* p = a.part + n * s.chunks * a.G + o.slab * s.gs + g;
+    const int chunks = g < s.gs ? s.chunks : 0;
     auto count = [&](int k) {
-      return static_cast<float>(piece_start(a.S, k + 1, s.chunks) - piece_start(a.S, k, s.chunks)) *
-             static_cast<float>(s.cg);
+      return static_cast<float>(s.chunk_base + (k < s.chunk_more ? 1 : 0)) * cg;
     };
     float sum = 0.f, m2 = 0.f;
-    for (int k = tid & 31; k < s.chunks; k += 32)
+#pragma unroll 4
+    for (int k = l8; k < chunks; k += 8)
       sum = __fmaf_rn(p[static_cast<int64_t>(k) * a.G].x, count(k), sum);
-    const float mean = warp_allsum(sum) / total;
-    for (int k = tid & 31; k < s.chunks; k += 32) {
+    const float mean = octet_sum(sum) / total;
+#pragma unroll 4
+    for (int k = l8; k < chunks; k += 8) {
       const float2 v = p[static_cast<int64_t>(k) * a.G];
       const float d = v.x - mean;
       m2 += __fmaf_rn(d * d, count(k), v.y);
     }
-    m2 = warp_allsum(m2);
-    if ((tid & 31) == 0) {
+    m2 = octet_sum(m2);
+    if (g < s.gs) {
       const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
-      gf[2 * g] = mean;
-      gf[2 * g + 1] = rstd;
-      if (part == 0) {
-        a.mean[n * a.G + slab * s.gs + g] = mean;
-        a.rstd[n * a.G + slab * s.gs + g] = rstd;
+      for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
+        c0[i] = -mean;
+        c1[i] = rstd * w[i];
+      }
+      if (l8 == 0 && o.chunk == 0) {
+        a.mean[n * a.G + o.slab * s.gs + g] = mean;
+        a.rstd[n * a.G + o.slab * s.gs + g] = rstd;
       }
     }
   }
   __syncthreads();
-  if (lane >= s.lanes || lane >= rows) return;
+  if (o.cnt == 0) return;
 
-  f2 mean[NP], scale[NP], bias[NP];
-  load_consts<T>(a, gf, c, ch, mean, scale, bias);
-  const T* px = static_cast<const T*>(a.x) + n * a.s_n + (r0 + lane) * a.s_s + ch;
-  T* py = static_cast<T*>(a.out) + (n * a.S + r0 + lane) * a.C + ch;
-  const int64_t step = s.lanes * a.s_s, ystep = static_cast<int64_t>(s.lanes) * a.C;
-  const int cnt = (rows - lane + s.lanes - 1) / s.lanes;
-  constexpr int kU = 4;
-  for (int i = 0; i < cnt; i += kU) {
-    uint4 u[kU];
-#pragma unroll
-    for (int j = 0; j < kU; ++j)
-      if (i + j < cnt) u[j] = *reinterpret_cast<const uint4*>(px + (i + j) * step);
-#pragma unroll
-    for (int j = 0; j < kU; ++j)
-      if (i + j < cnt)  // y is not read here again: it leaves L2 first
-        __stcs(reinterpret_cast<uint4*>(py + (i + j) * ystep),
-               norm_vec<T, kAct>(u[j], mean, scale, bias));
-  }
+  Consts<T> q;
+  q.load(c0, c1, b, o.c);
+  T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
+  const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
+  ring.run([&](int, const uint4* slot) {  // y is not read here again: it leaves L2 first
+    __stcs(reinterpret_cast<uint4*>(py), q.template norm<kAct>(*slot));
+    py += ystep;
+  });
 }
 
 namespace {
 
-// The build of kernel F<T, act> for a dtype and activation.
-template <typename T, bool kOnChip>
+// The kernel builds for a dtype T, activation and width.
+template <typename T, bool kOnChip, bool kWide>
 const void* pick_stats(int act) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
   if constexpr (!kOnChip) {
-    return fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, false>);  // statistics only
+    return fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, false, kWide>);  // statistics only
   } else {
-    return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, true>)
-           : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_SILU, true>)
-                                       : fn(&gn_fwd_kernel<T, GROUPNORM_ACT_GELU, true>);
+    return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, true, kWide>)
+           : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_SILU, true, kWide>)
+                                       : fn(&gn_fwd_kernel<T, GROUPNORM_ACT_GELU, true, kWide>);
   }
 }
 template <typename T>
-const void* pick_out(int act) {
+const void* pick_fwd(const GnShape& s, int act) {
+  if (s.vecs > kThreads)
+    return s.on_chip ? pick_stats<T, true, true>(act) : pick_stats<T, false, true>(act);
+  return s.on_chip ? pick_stats<T, true, false>(act) : pick_stats<T, false, false>(act);
+}
+template <typename T, bool kWide>
+const void* pick_act(int act) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_NONE>)
-         : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_SILU>)
-                                     : fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_GELU>);
+  return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_NONE, kWide>)
+         : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_SILU, kWide>)
+                                     : fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_GELU, kWide>);
+}
+template <typename T>
+const void* pick_out(const GnShape& s, int act) {
+  return s.vecs > kThreads ? pick_act<T, true>(act) : pick_act<T, false>(act);
 }
 
 }  // namespace
 
 cudaError_t launch_gn_fwd(const GnArgs& a, int dtype, int act, cudaStream_t st) {
-  const bool chip = a.s.on_chip != 0;
-  const void* fn =
-      dtype == GROUPNORM_BF16
-          ? (chip ? pick_stats<__nv_bfloat16, true>(act) : pick_stats<__nv_bfloat16, false>(act))
-      : dtype == GROUPNORM_FP32
-          ? (chip ? pick_stats<float, true>(act) : pick_stats<float, false>(act))
-          : (chip ? pick_stats<__half, true>(act) : pick_stats<__half, false>(act));
+  const void* fn = dtype == GROUPNORM_BF16   ? pick_fwd<__nv_bfloat16>(a.s, act)
+                   : dtype == GROUPNORM_FP32 ? pick_fwd<float>(a.s, act)
+                                             : pick_fwd<__half>(a.s, act);
   return launch_cluster(fn, gn_stats_ctas(a.s, a.n1 - a.n0), a.s, a, st);
 }
 
 cudaError_t launch_gn_fwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st) {
-  const void* fn = dtype == GROUPNORM_BF16   ? pick_out<__nv_bfloat16>(act)
-                   : dtype == GROUPNORM_FP32 ? pick_out<float>(act)
-                                             : pick_out<__half>(act);
-  GnArgs copy = a;
-  void* args[] = {&copy};
-  return launch_pdl(fn, dim3(static_cast<unsigned>(gn_out_ctas(a.s, a.n1 - a.n0))),
-                    dim3(static_cast<unsigned>(a.s.threads)), 8 * static_cast<size_t>(a.s.gs), st,
-                    args);
+  const void* fn = dtype == GROUPNORM_BF16   ? pick_out<__nv_bfloat16>(a.s, act)
+                   : dtype == GROUPNORM_FP32 ? pick_out<float>(a.s, act)
+                                             : pick_out<__half>(a.s, act);
+  return launch_out(fn, a, false, st);
 }
 
 }  // namespace gnorm

@@ -19,14 +19,18 @@ struct GnShape {
   int slabs;     // slabs a sample
   int lanes;     // rows of threads
   int threads;   // lanes * vecs, up to whole warps
-  int ctas;      // CTAs a cluster
+  int ctas;      // CTAs a cluster, 1 << ctas_log2
+  int ctas_log2;
   int iters;     // most places a thread takes
   int on_chip;   // the slab stays in shared memory between statistics and output
   int lanes_n;   // on chip: clusters a slab (each takes samples lane, lane + lanes_n, ...)
-  int chunks;    // two launches: chunks of places a sample's statistics are split into
+  int stages;    // on chip: samples a cluster has staged or on their way
+  int chunks;    // two launches: chunks of places a sample's statistics are split into: the
+                 // first chunk_more of chunk_base + 1 places, the others of chunk_base
+  int chunk_base, chunk_more;
   int samples;   // two launches: samples a pair of launches takes
-  int parts;     // two launches: chunks of places of the second launch
-  int part_iters;  // most places a thread of the second launch takes
+  int parts;     // two launches: chunks of places of the second launch, alike
+  int part_base, part_more;
   size_t smem;   // dynamic shared memory of the (first) launch
 };
 
@@ -50,27 +54,42 @@ struct GnArgs {
   GnShape s;
 };
 
-constexpr int kMaxThreads = 512;
+// Two builds of every kernel: CTAs of up to kThreads threads, kCtas of them an SM (80 registers
+// a thread, no spills; the forward's second launch fits four, with 64), and, for slabs of more
+// than kThreads vectors, up to kWideThreads threads, one CTA an SM (128 registers).
+constexpr int kThreads = 256, kWideThreads = 512;
+constexpr int kCtas = 3;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int max_threads(bool wide) { return wide ? kWideThreads : kThreads; }
+constexpr int min_ctas(bool wide) { return wide ? 1 : kCtas; }
 
-// Shared memory behind the staged vectors (floats unless said otherwise), in this order:
-//   red    tensors * threads * ev: per-thread column values on their way to sums
-//   parts  kMaxWarps + gs: per-warp partial sums of groups
-//   gm     2 * gs: the CTA's group values, then
-//   all    2 * gs * ctas: every CTA's (float2), gathered
-//   gf     2 * gs: the sample's final group values
-//   col    backward: 2 * cs column sums; on chip: + 4 * cs running totals (sum, compensation)
+// Shared memory behind the staged vectors (floats), in this order:
+//   red   2 planes [lanes][red_stride]: per-thread column values on their way to column sums
+//         (forward: mean and M2; backward: A and B)
+//   gm    2 * gs: the CTA's group values
+//   w, b  cs parameters each
+//   c0, c1  cs channel constants each (forward: -mean and rstd * w; backward: nc1 and nc2)
+//   col   2 * cs column values; on chip backward: + 4 * cs running totals (sum, compensation)
+// A row of red is padded so that four rows of eight columns fall on 32 different banks wherever
+// the slab is a multiple of 32 channels.
+inline __host__ __device__ int red_stride(const GnShape& s) { return s.cs + (s.cs % 32 ? 0 : 8); }
 inline __host__ __device__ size_t gn_extra_floats(const GnShape& s, bool bwd) {
-  size_t n = static_cast<size_t>(bwd ? 2 : 1) * s.threads * s.ev;
-  n += kMaxWarps + s.gs;
-  n += 2 * static_cast<size_t>(s.gs) + 2 * static_cast<size_t>(s.gs) * s.ctas +
-       2 * static_cast<size_t>(s.gs);
-  if (bwd) n += static_cast<size_t>(s.on_chip ? 6 : 2) * s.cs;
+  size_t n = 2 * static_cast<size_t>(s.lanes) * red_stride(s);
+  n += 2 * static_cast<size_t>(s.gs) + 6 * static_cast<size_t>(s.cs);
+  if (bwd && s.on_chip) n += 4 * static_cast<size_t>(s.cs);
   return (n + 3) & ~static_cast<size_t>(3);
 }
+// Two launches: each thread's copies run through a ring of kRingGroups groups of kRingPlaces
+// places; on chip, `iters` places are staged.
+constexpr int kRingGroups = 4, kRingPlaces = 2;
+// Bytes of one staged sample, or of the ring.
 inline __host__ __device__ size_t gn_stage_bytes(const GnShape& s, bool bwd) {
-  return s.on_chip ? static_cast<size_t>(bwd ? 2 : 1) * s.iters * s.threads * 16 : 0;
+  return static_cast<size_t>(bwd ? 2 : 1) * (s.on_chip ? s.iters : kRingGroups * kRingPlaces) *
+         s.threads * 16;
+}
+// Shared memory of the second launch: the ring, then w, b, c0, c1 as above.
+inline __host__ __device__ size_t gn_out_smem(const GnShape& s, bool bwd) {
+  return gn_stage_bytes(s, bwd) + (4 * static_cast<size_t>(s.cs)) * sizeof(float);
 }
 
 // CTAs of the launches over `samples` samples.
@@ -84,6 +103,9 @@ inline int64_t gn_out_ctas(const GnShape& s, int64_t samples) {
 // Launches fn over `ctas` CTAs in clusters of s.ctas, with programmatic dependent launch.
 cudaError_t launch_cluster(const void* fn, int64_t ctas, const GnShape& s, const GnArgs& a,
                            cudaStream_t st);
+
+// Launches fn, a second launch, over the samples [a.n0, a.n1).
+cudaError_t launch_out(const void* fn, const GnArgs& a, bool bwd, cudaStream_t st);
 
 // Launch the statistics (and, on chip, the output) of samples [a.n0, a.n1); then, for two
 // launches, the output.  dtype and act: GROUPNORM_*.

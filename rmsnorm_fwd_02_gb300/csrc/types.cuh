@@ -19,6 +19,19 @@ struct VecOf<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = bf2_to_f2(u4_get(u, i));
   }
+  // pair i of u plus nk, each rounded once: a mixed-precision fma x * 1 + nk per element reads
+  // the 16-bit halves without a conversion
+  __device__ static __forceinline__ f2 plus(const uint4& u, int i, f2 nk) {
+    f2 r;
+    asm("{\n\t.reg .b16 a0, a1, one;\n\t.reg .f32 c0, c1, p0, p1;\n\t"
+        "mov.b32 {a0, a1}, %1;\n\tmov.b16 one, 0x3F80;\n\tmov.b64 {c0, c1}, %2;\n\t"
+        "fma.rn.f32.bf16 p0, a0, one, c0;\n\t"
+        "fma.rn.f32.bf16 p1, a1, one, c1;\n\t"
+        "mov.b64 %0, {p0, p1};\n\t}"
+        : "=l"(r.v)
+        : "r"(u4_get(u, i)), "l"(nk.v));
+    return r;
+  }
   __device__ static __forceinline__ uint4 pack(const f2 (&f)[4]) {
     return make_uint4(f2_to_bf2(f[0]), f2_to_bf2(f[1]), f2_to_bf2(f[2]), f2_to_bf2(f[3]));
   }
@@ -39,6 +52,17 @@ struct VecOf<__half> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = widen(u4_get(u, i));
   }
+  __device__ static __forceinline__ f2 plus(const uint4& u, int i, f2 nk) {
+    f2 r;
+    asm("{\n\t.reg .b16 a0, a1, one;\n\t.reg .f32 c0, c1, p0, p1;\n\t"
+        "mov.b32 {a0, a1}, %1;\n\tmov.b16 one, 0x3C00;\n\tmov.b64 {c0, c1}, %2;\n\t"
+        "fma.rn.f32.f16 p0, a0, one, c0;\n\t"
+        "fma.rn.f32.f16 p1, a1, one, c1;\n\t"
+        "mov.b64 %0, {p0, p1};\n\t}"
+        : "=l"(r.v)
+        : "r"(u4_get(u, i)), "l"(nk.v));
+    return r;
+  }
   __device__ static __forceinline__ uint4 pack(const f2 (&f)[4]) {
     return make_uint4(narrow(f[0]), narrow(f[1]), narrow(f[2]), narrow(f[3]));
   }
@@ -50,6 +74,11 @@ struct VecOf<float> {
   __device__ static __forceinline__ void unpack(const uint4& u, f2 (&f)[2]) {
     f[0] = f2_make(__uint_as_float(u.x), __uint_as_float(u.y));
     f[1] = f2_make(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  __device__ static __forceinline__ f2 plus(const uint4& u, int i, f2 nk) {
+    return f2_add(i == 0 ? f2_make(__uint_as_float(u.x), __uint_as_float(u.y))
+                         : f2_make(__uint_as_float(u.z), __uint_as_float(u.w)),
+                  nk);
   }
   __device__ static __forceinline__ uint4 pack(const f2 (&f)[2]) {
     return make_uint4(__float_as_uint(f2_lo(f[0])), __float_as_uint(f2_hi(f[0])),

@@ -57,8 +57,10 @@ def depth(x, groups, bwd):
     else:
         chunks = p["ctas"] // (p["samples"] * slabs * p["cluster_ctas"])
         rows = -(-s // (chunks * p["cluster_ctas"])) + 1
+    # a thread's places (at least half the lanes the plan has threads for), four lanes of a
+    # column at a time, eight columns of a group, eight chunks; the trees between
     places = rows // max(1, (lanes + 1) // 2) + 2
-    return places + lanes * max(1, c // groups) / 32 + 1 + 5 + 16 + 8 + chunks / 32 + 6
+    return places + lanes / 4 + 3 + c // groups / 8 + 4 + 4 + chunks / 8 + 4
 
 
 def case(seed, n, s, c, dtype, wb=FP, offset=0.0):
