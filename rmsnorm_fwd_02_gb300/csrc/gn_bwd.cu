@@ -5,7 +5,7 @@
 // mean(g * xhat) and mean(g) are w-weighted sums of them, and dw_c, db_c their sums over the
 // samples -- one set of sums serves all.  As the forward (gn_fwd.cu): one launch that keeps x
 // and dy on chip between the sums and dx where a cluster's shared memory holds them, else two
-// launches over as many samples as L2 holds.  dz is formed twice from x and dy rather than kept
+// launches over as many slabs as L2 holds.  dz is formed twice from x and dy rather than kept
 // (keeping it in FP32 would double the staged bytes).  The column sums of each CTA (on chip:
 // over all the samples it takes, compensated) go to the workspace, and a finishing kernel adds
 // them in a fixed order.
@@ -43,11 +43,18 @@ struct Consts {
       scale[i] = f2_mul(scale[i], f2_make(u[2 * i], u[2 * i + 1]));
     }
   }
-  // pair i of x and dy: d, and dz = dy * act'(z)
+  // d, and dz = dy * act'(z), of pairs h and h + 1 of a vector
   template <int kAct>
-  __device__ __forceinline__ f2 dz(const uint4& xu, f2 dy, int i, f2& d) const {
-    d = VecOf<T>::plus(xu, i, nm[i]);
-    return act_grad2<kAct>(f2_fma(d, scale[i], bias[i]), dy);
+  __device__ __forceinline__ void dz(const uint4& xu, const uint4& du, int h, f2 (&d)[2],
+                                     f2 (&out)[2]) const {
+    f2 z[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      d[i] = VecOf<T>::plus(xu, h + i, nm[h + i]);
+      z[i] = f2_fma(d[i], scale[h + i], bias[h + i]);
+      out[i] = VecOf<T>::pair(du, h + i);
+    }
+    act_grad_vec<kAct>(z, out);
   }
 };
 
@@ -68,12 +75,13 @@ __device__ __forceinline__ uint4 dx_vec(const Consts<T>& k, const GroupTerms<T>&
                                         const uint4& xu, const uint4& du) {
   constexpr int NP = VecOf<T>::kPairs;
   f2 v[NP];
-  VecOf<T>::unpack(du, v);
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    f2 d;
-    const f2 dz = k.template dz<kAct>(xu, v[i], i, d);
-    v[i] = f2_fma(dz, k.scale[i], f2_fma(d, t.nc2[i], t.nc1[i]));
+  for (int h = 0; h < NP; h += 2) {
+    f2 d[2], dz[2];
+    k.template dz<kAct>(xu, du, h, d, dz);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v[h + i] = f2_fma(dz[i], k.scale[h + i], f2_fma(d[i], t.nc2[h + i], t.nc1[h + i]));
   }
   return VecOf<T>::pack(v);
 }
@@ -88,14 +96,15 @@ struct ColumnSums {
     for (int i = 0; i < kPairs; ++i) A[i] = B[i] = f2_splat(0.f);
   }
   __device__ __forceinline__ void add(const Consts<T>& k, const uint4& xu, const uint4& du) {
-    f2 dy[kPairs];
-    VecOf<T>::unpack(du, dy);
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      f2 d;
-      const f2 dz = k.template dz<kAct>(xu, dy[i], i, d);
-      A[i] = f2_fma(dz, d, A[i]);
-      B[i] = f2_add(B[i], dz);
+    for (int h = 0; h < kPairs; h += 2) {
+      f2 d[2], dz[2];
+      k.template dz<kAct>(xu, du, h, d, dz);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        A[h + i] = f2_fma(dz[i], d[i], A[h + i]);
+        B[h + i] = f2_add(B[h + i], dz[i]);
+      }
     }
   }
 };
@@ -117,19 +126,18 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   const T* const pd = static_cast<const T*>(a.dy) + at0;
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
 
-  pdl_wait_prior_grid();
-  pdl_allow_next_grid();
+  if (kOnChip || !a.early) pdl_wait_prior_grid();
 
-  // on chip: this thread's slots of stage k are stage[(2 * k * iters + i) * threads] for x, and
-  // iters * threads behind them for dy
-  uint4* const stage = reinterpret_cast<uint4*>(smem) + tid;
-  const int dy_off = s.iters * s.threads;
+  // on chip: this thread's slot of place i of stage k is stage + (2 * k * iters + i) * stride for
+  // x, and dy_off behind it for dy
+  const uint32_t stride = 16u * s.threads, stage = smem_u32(smem) + 16u * tid;
+  const uint32_t dy_off = (kOnChip ? s.iters : kRingSlots) * stride;
   auto stage_places = [&](int64_t n, int k, int from, int to) {
-    if (n < a.n1) {
+    if (n < a.N) {
       const T* p = px + n * a.s_n + from * step;
       const T* q = pd + n * a.S * a.C + from * dstep;
-      uint4* d = stage + (2 * k * s.iters + from) * s.threads;
-      for (int i = from; i < min(to, o.cnt); ++i, p += step, q += dstep, d += s.threads) {
+      uint32_t d = stage + (2 * k * s.iters + from) * stride;
+      for (int i = from; i < min(to, o.cnt); ++i, p += step, q += dstep, d += stride) {
         cp_async_16(d, p);
         cp_async_16(d + dy_off, q);
       }
@@ -138,7 +146,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   };
   constexpr int kBatches = 4;  // of a single-stage sample
   const int per = (s.iters + kBatches - 1) / kBatches;
-  int64_t n = a.n0 + (kOnChip ? o.rest : o.rest / s.chunks);
+  int64_t n = o.n;
   if constexpr (kOnChip) {
     if (s.stages == 1)
       for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
@@ -148,33 +156,33 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   }
   Ring<2> ring;
   if constexpr (!kOnChip) {
-    ring = Ring<2>{stage,
+    ring = Ring<2>{stage, stride,
                    {reinterpret_cast<const unsigned char*>(px + n * a.s_n),
                     reinterpret_cast<const unsigned char*>(pd + n * a.S * a.C)},
                    {step * static_cast<int64_t>(sizeof(T)), dstep * static_cast<int64_t>(sizeof(T))},
-                   o.cnt, s.threads, 0};
+                   o.cnt};
     ring.start();
+    if (a.early) pdl_wait_prior_grid();
   }
+  pdl_allow_next_grid();
   load_params(a, m.w, m.b, o.slab);
   __syncthreads();
 
   const int l8 = tid & 7, oct = (tid & 31) >> 3, w = tid >> 5, nw = s.threads >> 5;
-  for (int k = 0; n < a.n1; n += kOnChip ? s.lanes_n : a.n1) {
+  for (int k = 0; n < a.N; n += kOnChip ? s.lanes_n : a.N) {
     const float* const mean = a.mean + n * a.G + group0;
     const float* const rstd = a.rstd + n * a.G + group0;
     Consts<T> q;
     ColumnSums<T, kAct> sum;
     sum.clear();
-    const uint4* const mine = stage + 2 * k * s.iters * s.threads;
+    const uint32_t mine = stage + 2 * k * s.iters * stride;
     if constexpr (kOnChip) {
       if (s.stages == 1) {  // the sums follow the copies, batch by batch
         if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
         for (int b = 0; b < kBatches; ++b) {
           cp_async_wait(kBatches - 1 - b);
-          const int end = min(o.cnt, (b + 1) * per);
-#pragma unroll 2
-          for (int i = b * per; i < end; ++i)
-            sum.add(q, mine[i * s.threads], mine[dy_off + i * s.threads]);
+          for_staged2(mine, dy_off, b * per, min(o.cnt, (b + 1) * per), stride,
+                      [&](const uint4& xu, const uint4& du) { sum.add(q, xu, du); });
         }
       } else {
         const int ahead = s.stages - 1;
@@ -182,15 +190,15 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
                      0, s.iters);
         if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
         cp_async_wait(ahead);
-#pragma unroll 2
-        for (int i = 0; i < o.cnt; ++i)
-          sum.add(q, mine[i * s.threads], mine[dy_off + i * s.threads]);
+        for_staged2(mine, dy_off, 0, o.cnt, stride,
+                    [&](const uint4& xu, const uint4& du) { sum.add(q, xu, du); });
       }
     } else {
       if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
-      ring.run([&](int, const uint4* slot) {
-        sum.add(q, *slot, slot[kRingSlots * s.threads]);
+      ring.run(o.cnt, [&](uint32_t slot) {
+        sum.add(q, lds128_at(slot), lds128_at(slot + dy_off));
       });
+      __syncthreads();  // red takes the rings' place
     }
 
     // column sums over the CTA's places: A * rstd (= sum of dz * xhat) in col[0, cs), B in
@@ -285,9 +293,10 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         GroupTerms<T> t;
         t.load(m.c0, m.c1, o.c);
         T* po = static_cast<T*>(a.out) + n * a.S * a.C + at0;
-#pragma unroll 2
-        for (int i = 0; i < o.cnt; ++i, po += dstep)
-          stg128(po, dx_vec<T, kAct>(q, t, mine[i * s.threads], mine[dy_off + i * s.threads]));
+        for_staged2(mine, dy_off, 0, o.cnt, stride, [&](const uint4& xu, const uint4& du) {
+          stg128(po, dx_vec<T, kAct>(q, t, xu, du));
+          po += dstep;
+        });
       }
       if (s.stages == 1) {
         for (int b = 0; b < kBatches; ++b)
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   }
   if constexpr (kOnChip) {  // this CTA's totals over its samples
     __syncthreads();
-    float* out = a.cols + (static_cast<int64_t>(o.rest) * s.ctas + o.rank) * 2 * a.C +
+    float* out = a.cols + (o.n * s.ctas + o.rank) * 2 * a.C +
                  o.slab * s.cs;
     for (int t = tid; t < 2 * s.cs; t += s.threads)
       out[t < s.cs ? t : a.C + t - s.cs] = m.run[2 * t];
@@ -316,17 +325,18 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const int tid = threadIdx.x;
-  int64_t n;
-  const Owner o = out_owner(a, &n);
+  const Owner o = out_owner(a);
+  const int64_t n = o.n;
   const int ch = o.slab * s.cs + o.c, group0 = o.slab * s.gs;
   const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
   const int64_t at = (n * a.S + o.r0 + o.lane) * a.C + ch;
   const T* px = static_cast<const T*>(a.x) + n * a.s_n + (o.r0 + o.lane) * a.s_s + ch;
-  Ring<2> ring{reinterpret_cast<uint4*>(smem) + tid,
+  const uint32_t stride = 16u * s.threads;
+  Ring<2> ring{smem_u32(smem) + 16u * tid, stride,
                {reinterpret_cast<const unsigned char*>(px),
                 reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.dy) + at)},
                {step * static_cast<int64_t>(sizeof(T)), dstep * static_cast<int64_t>(sizeof(T))},
-               o.cnt, s.threads, 0};
+               o.cnt};
   ring.start();
   float* w = reinterpret_cast<float*>(smem + gn_stage_bytes(s, true));
   float* b = w + s.cs;
@@ -372,9 +382,9 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   GroupTerms<T> t;
   t.load(c0, c1, o.c);
   T* po = static_cast<T*>(a.out) + at;
-  ring.run([&](int, const uint4* slot) {  // dx is not read here again: it leaves L2 first
+  ring.run(o.cnt, [&](uint32_t slot) {  // dx is not read here again: it leaves L2 first
     __stcs(reinterpret_cast<uint4*>(po),
-           dx_vec<T, kAct>(k, t, *slot, slot[kRingSlots * s.threads]));
+           dx_vec<T, kAct>(k, t, lds128_at(slot), lds128_at(slot + kRingSlots * stride)));
     po += dstep;
   });
 }
@@ -457,7 +467,7 @@ cudaError_t launch_gn_bwd(const GnArgs& a, int dtype, int act, cudaStream_t st) 
   const void* fn = dtype == GROUPNORM_BF16   ? pick_bwd<__nv_bfloat16>(a.s, act)
                    : dtype == GROUPNORM_FP32 ? pick_bwd<float>(a.s, act)
                                              : pick_bwd<__half>(a.s, act);
-  return launch_cluster(fn, gn_stats_ctas(a.s, a.n1 - a.n0), a.s, a, st);
+  return launch_cluster(fn, gn_stats_ctas(a.s, a.nu), a.s, a, st);
 }
 
 cudaError_t launch_gn_bwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st) {

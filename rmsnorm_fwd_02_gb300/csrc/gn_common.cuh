@@ -26,11 +26,22 @@ __device__ __forceinline__ float rcp_approx(float a) {
   return r;
 }
 
-// 1 / (1 + exp(-z)) of a pair, to a few FP32 roundings (z below -87: 0).
-__device__ __forceinline__ f2 sigmoid2(f2 z) {
-  const f2 t = f2_mul(z, f2_splat(-1.44269504088896340736f));
-  const f2 d = f2_add(f2_make(ex2_approx(f2_lo(t)), ex2_approx(f2_hi(t))), f2_splat(1.f));
-  return f2_make(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
+// s = 1 / (1 + exp(-z)) of pairs, to a few FP32 roundings.  A reciprocal takes the
+// special-function unit twice as long as an exponential, so the two values of a pair share one
+// (1/a = b * 1/(ab)).  exp(-z) is held to 2^62, which keeps ab finite and leaves a sigmoid below
+// 2^-62 there; the smaller of a NaN and 62 is 62, so a NaN (it stays in z) does not reach the
+// pair's other value.
+template <int kPairs>
+__device__ __forceinline__ void sigmoid_vec(const f2 (&z)[kPairs], f2 (&s)[kPairs]) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const f2 t = f2_mul(z[i], f2_splat(-1.44269504088896340736f));
+    const f2 d = f2_add(f2_make(ex2_approx(fminf(f2_lo(t), 62.f)),
+                                ex2_approx(fminf(f2_hi(t), 62.f))),
+                        f2_splat(1.f));
+    const float r = rcp_approx(f2_lo(d) * f2_hi(d));
+    s[i] = f2_make(r * f2_hi(d), r * f2_lo(d));
+  }
 }
 
 __device__ __forceinline__ float normal_cdf(float z) {
@@ -42,24 +53,35 @@ __device__ __forceinline__ float gelu_slope(float z) {
                    normal_cdf(z));
 }
 
-template <int kAct>
-__device__ __forceinline__ f2 act2(f2 z) {
-  if constexpr (kAct == GROUPNORM_ACT_SILU) return f2_mul(z, sigmoid2(z));
-  if constexpr (kAct == GROUPNORM_ACT_GELU)
-    return f2_make(f2_lo(z) * normal_cdf(f2_lo(z)), f2_hi(z) * normal_cdf(f2_hi(z)));
-  return z;
+// z becomes act(z).
+template <int kAct, int kPairs>
+__device__ __forceinline__ void act_vec(f2 (&z)[kPairs]) {
+  if constexpr (kAct == GROUPNORM_ACT_SILU) {
+    f2 s[kPairs];
+    sigmoid_vec(z, s);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) z[i] = f2_mul(z[i], s[i]);
+  } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      z[i] = f2_make(f2_lo(z[i]) * normal_cdf(f2_lo(z[i])), f2_hi(z[i]) * normal_cdf(f2_hi(z[i])));
+  }
 }
 
-// dy * act'(z)
-template <int kAct>
-__device__ __forceinline__ f2 act_grad2(f2 z, f2 dy) {
+// dy becomes dy * act'(z).
+template <int kAct, int kPairs>
+__device__ __forceinline__ void act_grad_vec(const f2 (&z)[kPairs], f2 (&dy)[kPairs]) {
   if constexpr (kAct == GROUPNORM_ACT_SILU) {  // s + z s (1 - s)
-    const f2 s = sigmoid2(z);
-    return f2_mul(dy, f2_fma(f2_mul(z, s), f2_sub(f2_splat(1.f), s), s));
+    f2 s[kPairs];
+    sigmoid_vec(z, s);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      dy[i] = f2_mul(dy[i], f2_fma(f2_mul(z[i], s[i]), f2_sub(f2_splat(1.f), s[i]), s[i]));
+  } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      dy[i] = f2_mul(dy[i], f2_make(gelu_slope(f2_lo(z[i])), gelu_slope(f2_hi(z[i]))));
   }
-  if constexpr (kAct == GROUPNORM_ACT_GELU)
-    return f2_mul(dy, f2_make(gelu_slope(f2_lo(z)), gelu_slope(f2_hi(z))));
-  return dy;
 }
 
 // Element i of a parameter array of dtype GROUPNORM_*.
@@ -80,9 +102,9 @@ __device__ __forceinline__ void lds_pairs(const float* p, f2* out) {
   }
 }
 
-__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
+// (staged vectors are addressed in the 32-bit shared window)
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -144,19 +166,37 @@ __device__ __forceinline__ f2 across_octets(f2 v) {
   return f2_make(across_octets(f2_lo(v)), across_octets(f2_hi(v)));
 }
 
-// f(i, vector) for i in [from, to), vectors `stride` 16-byte units apart, four loads ahead.
+// f(vector) for i in [from, to), vectors `stride` bytes apart from p on, four loads ahead.
 template <typename F>
-__device__ __forceinline__ void for_staged(const uint4* p, int from, int to, int stride, F f) {
+__device__ __forceinline__ void for_staged(uint32_t p, int from, int to, uint32_t stride, F f) {
   int i = from;
   p += from * stride;
   for (; i + 4 <= to; i += 4, p += 4 * stride) {
     uint4 u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = p[j * stride];
+    for (int j = 0; j < 4; ++j) u[j] = lds128_at(p + j * stride);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f(i + j, u[j]);
+    for (int j = 0; j < 4; ++j) f(u[j]);
   }
-  for (; i < to; ++i, p += stride) f(i, *p);
+  for (; i < to; ++i, p += stride) f(lds128_at(p));
+}
+// The same over pairs of vectors, the second `off` bytes behind the first, two pairs ahead.
+template <typename F>
+__device__ __forceinline__ void for_staged2(uint32_t p, uint32_t off, int from, int to,
+                                            uint32_t stride, F f) {
+  int i = from;
+  p += from * stride;
+  for (; i + 2 <= to; i += 2, p += 2 * stride) {
+    uint4 u[2], v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u[j] = lds128_at(p + j * stride);
+      v[j] = lds128_at(p + j * stride + off);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f(u[j], v[j]);
+  }
+  if (i < to) f(lds128_at(p), lds128_at(p + off));
 }
 
 // First of `places` places that rank k of a cluster takes.
@@ -176,15 +216,15 @@ struct Smem {
 };
 __device__ __forceinline__ Smem carve(unsigned char* base, const GnShape& s, bool bwd) {
   Smem m;
-  float* p = reinterpret_cast<float*>(base + gn_stage_bytes(s, bwd) * (s.on_chip ? s.stages : 1));
+  float* p = reinterpret_cast<float*>(base + gn_front_bytes(s, bwd));
   m.w = p;  // 16-byte aligned: cs is a multiple of 4
   m.b = m.w + s.cs;
   m.c0 = m.b + s.cs;
   m.c1 = m.c0 + s.cs;
-  m.red = m.c1 + s.cs;
-  m.col = m.red + 2 * s.lanes * red_stride(s);
+  m.col = m.c1 + s.cs;
   m.run = m.col + 2 * s.cs;
   m.gm = m.run + (bwd && s.on_chip ? 4 * s.cs : 0);
+  m.red = s.on_chip ? m.gm + (2 * s.gs + 3) / 4 * 4 : reinterpret_cast<float*>(base);
   return m;
 }
 // The slab's parameters to shared memory (no synchronization).
@@ -195,100 +235,118 @@ __device__ __forceinline__ void load_params(const GnArgs& a, float* w, float* b,
   }
 }
 
-// What a thread of the statistics kernels owns.
+// What a thread owns of its kernel's work.
 struct Owner {
-  int lane, rank, slab, rest, chunk;
+  int lane, rank, slab, chunk;
+  int64_t n;        // (first) sample
   int c;            // its first channel in the slab
   int len;          // places of the chunk
   int64_t r0;       // first place of the CTA
   int rows;         // places of the CTA
   int cnt;          // places of the thread
 };
+__device__ __forceinline__ void set_lane(Owner& o, const GnShape& s) {
+  o.lane = threadIdx.x / s.vecs;
+  o.c = (threadIdx.x - o.lane * s.vecs) * s.ev;
+}
+__device__ __forceinline__ void set_count(Owner& o, const GnShape& s) {
+  o.cnt = o.lane < s.lanes && o.lane < o.rows ? (o.rows - o.lane + s.lanes - 1) / s.lanes : 0;
+}
+// Unit `local` of a launch: neighbouring CTAs take neighbouring slabs of the same places.
+__device__ __forceinline__ void set_unit(Owner& o, const GnArgs& a, int local) {
+  const int64_t u = a.u0 + local;
+  o.n = u / a.s.slabs;
+  o.slab = static_cast<int>(u - o.n * a.s.slabs);
+}
 template <bool kOnChip>
 __device__ __forceinline__ Owner owner(const GnArgs& a) {
   const GnShape& s = a.s;
   Owner o;
-  o.lane = threadIdx.x / s.vecs;
-  o.c = (threadIdx.x - o.lane * s.vecs) * s.ev;
+  set_lane(o, s);
   o.rank = s.ctas > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
-  const int unit = blockIdx.x >> s.ctas_log2;
-  o.rest = unit / s.slabs;
-  o.slab = unit - o.rest * s.slabs;
-  o.chunk = 0;
-  o.len = static_cast<int>(a.S);
-  o.r0 = 0;
-  if constexpr (!kOnChip) {
-    o.chunk = o.rest % s.chunks;
+  const int cluster = blockIdx.x >> s.ctas_log2;
+  if constexpr (kOnChip) {
+    const int first = cluster / s.slabs;
+    o.n = first;
+    o.slab = cluster - first * s.slabs;
+    o.chunk = 0;
+    o.len = static_cast<int>(a.S);
+    o.r0 = 0;
+  } else {
+    o.chunk = cluster / a.nu;
+    set_unit(o, a, cluster - o.chunk * a.nu);
     o.len = s.chunk_base + (o.chunk < s.chunk_more ? 1 : 0);
     o.r0 = static_cast<int64_t>(o.chunk) * s.chunk_base + min(o.chunk, s.chunk_more);
   }
   const int start = rank_start(o.len, o.rank, s);
   o.r0 += start;
   o.rows = rank_start(o.len, o.rank + 1, s) - start;
-  o.cnt = o.lane < s.lanes && o.lane < o.rows ? (o.rows - o.lane + s.lanes - 1) / s.lanes : 0;
+  set_count(o, s);
   return o;
 }
 
-// What a thread of the second launch's kernels owns (no cluster).
-__device__ __forceinline__ Owner out_owner(const GnArgs& a, int64_t* n) {
+// The second launch's kernels (no cluster), backwards through the places.
+__device__ __forceinline__ Owner out_owner(const GnArgs& a) {
   const GnShape& s = a.s;
   Owner o;
-  o.lane = threadIdx.x / s.vecs;
-  o.c = (threadIdx.x - o.lane * s.vecs) * s.ev;
+  set_lane(o, s);
   o.rank = 0;
-  const int unit = gridDim.x - 1 - blockIdx.x;  // backwards
-  o.rest = unit / s.slabs;
-  o.slab = unit - o.rest * s.slabs;
-  const int sample = o.rest / s.parts;
-  o.chunk = o.rest - sample * s.parts;
-  *n = a.n0 + sample;
+  const int i = gridDim.x - 1 - blockIdx.x;
+  o.chunk = i / a.nu;
+  set_unit(o, a, i - o.chunk * a.nu);
   o.len = o.rows = s.part_base + (o.chunk < s.part_more ? 1 : 0);
   o.r0 = static_cast<int64_t>(o.chunk) * s.part_base + min(o.chunk, s.part_more);
-  o.cnt = o.lane < s.lanes && o.lane < o.rows ? (o.rows - o.lane + s.lanes - 1) / s.lanes : 0;
+  set_count(o, s);
   return o;
 }
 
 // A thread's own copies through its ring: kTensors 16-byte vectors a place (tensor t's slots
-// kRingGroups * kRingPlaces * threads behind tensor t - 1's), kRingPlaces places a copy group,
-// kRingGroups - 1 groups on their way while one is used.
+// kRingSlots strides behind tensor t - 1's), kRingPlaces places a copy group, kRingGroups - 1
+// groups on their way while one is used.  One turn of the ring is unrolled, so that slots are
+// fixed offsets.
+constexpr int kRingSlots = kRingGroups * kRingPlaces;
 template <int kTensors>
 struct Ring {
-  uint4* slot;
+  uint32_t slot;           // this thread's first slot (shared window)
+  uint32_t stride;         // bytes from slot to slot
   const unsigned char* p[kTensors];
-  int64_t step[kTensors];  // bytes
-  int cnt, threads, next;
-  __device__ __forceinline__ void issue() {
+  int64_t step[kTensors];  // bytes from place to place
+  int left;                // places not issued yet
+
+  __device__ __forceinline__ void issue(int group) {
 #pragma unroll
-    for (int j = 0; j < kRingPlaces; ++j, ++next) {
-      if (next < cnt) {
-        uint4* d = slot + (next & (kRingGroups * kRingPlaces - 1)) * threads;
+    for (int j = 0; j < kRingPlaces; ++j) {
+      if (left > 0) {
 #pragma unroll
         for (int t = 0; t < kTensors; ++t) {
-          cp_async_16(d + t * kRingGroups * kRingPlaces * threads, p[t]);
+          cp_async_16(slot + (group * kRingPlaces + j + t * kRingSlots) * stride, p[t]);
           p[t] += step[t];
         }
+        --left;
       }
     }
     cp_async_commit();
   }
   __device__ __forceinline__ void start() {
-    next = 0;
 #pragma unroll
-    for (int g = 0; g + 1 < kRingGroups; ++g) issue();
+    for (int g = 0; g + 1 < kRingGroups; ++g) issue(g);
   }
-  // f(place, its slots' base) for every place of the thread, in order
+  // f(its slot) for each of the thread's cnt places in order
   template <typename F>
-  __device__ __forceinline__ void run(F f) {
-    for (int i = 0; i < cnt; i += kRingPlaces) {
-      issue();
-      cp_async_wait(kRingGroups - 1);
+  __device__ __forceinline__ void run(int cnt, F f) {
+    for (int i = 0; i < cnt; i += kRingSlots) {
 #pragma unroll
-      for (int j = 0; j < kRingPlaces; ++j)
-        if (i + j < cnt)
-          f(i + j, slot + ((i + j) & (kRingGroups * kRingPlaces - 1)) * threads);
+      for (int g = 0; g < kRingGroups; ++g) {
+        if (i + g * kRingPlaces < cnt) {
+          issue((g + kRingGroups - 1) % kRingGroups);
+          cp_async_wait(kRingGroups - 1);
+#pragma unroll
+          for (int j = 0; j < kRingPlaces; ++j)
+            if (i + g * kRingPlaces + j < cnt) f(slot + (g * kRingPlaces + j) * stride);
+        }
+      }
     }
   }
 };
-constexpr int kRingSlots = kRingGroups * kRingPlaces;
 
 }  // namespace gnorm

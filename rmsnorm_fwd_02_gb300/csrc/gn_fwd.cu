@@ -5,8 +5,8 @@
 // a sample's slab (gn_launch.h), one launch reads it once: asynchronous 16-byte copies stage
 // each thread's own vectors (the next samples' on their way meanwhile), the cluster's CTAs
 // exchange a few floats a group, and the staged vectors are normalized and written.  Larger
-// samples take two launches, the second reading x again -- from L2 where the samples of one
-// pair of launches fit it, which is how many a pair takes.
+// samples take two launches, the second reading x again -- from L2, which holds the slabs of one
+// pair of launches.
 //
 // Statistics: each thread sums its channels' values less the first of them, K (sum d and
 // sum d^2 of d = x - K), so neither sum cancels when the mean is far from zero; a column's
@@ -56,8 +56,15 @@ struct Consts {
   __device__ __forceinline__ uint4 norm(const uint4& u) const {
     f2 z[kPairs];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      z[i] = act2<kAct>(f2_fma(VecOf<T>::plus(u, i, nm[i]), scale[i], bias[i]));
+    for (int h = 0; h < kPairs; h += 2) {  // four values at a time
+      f2 v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = f2_fma(VecOf<T>::plus(u, h + i, nm[h + i]), scale[h + i], bias[h + i]);
+      act_vec<kAct>(v);
+      z[h] = v[0];
+      z[h + 1] = v[1];
+    }
     return VecOf<T>::pack(z);
   }
 };
@@ -166,22 +173,28 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
                                      static_cast<float>(s.cg)
                                : 0.f;
 
-  pdl_wait_prior_grid();
-  pdl_allow_next_grid();
+  if (kOnChip || !a.early) pdl_wait_prior_grid();
 
-  // on chip: this thread's slots of stage k are stage[(k * iters + i) * threads]
-  uint4* const stage = reinterpret_cast<uint4*>(smem) + tid;
+  // on chip: this thread's slot of place i of stage k is stage + (k * iters + i) * stride
+  const uint32_t stride = 16u * s.threads, stage = smem_u32(smem) + 16u * tid;
   auto stage_places = [&](int64_t n, int k, int from, int to) {
-    if (n < a.n1) {
+    if (n < a.N) {
       const T* p = px + n * a.s_n + from * step;
-      uint4* d = stage + (k * s.iters + from) * s.threads;
-      for (int i = from; i < min(to, o.cnt); ++i, p += step, d += s.threads) cp_async_16(d, p);
+      uint32_t d = stage + (k * s.iters + from) * stride;
+      for (int i = from; i < min(to, o.cnt); ++i, p += step, d += stride) cp_async_16(d, p);
     }
     cp_async_commit();
   };
   constexpr int kBatches = 4;  // of a single-stage sample
   const int per = (s.iters + kBatches - 1) / kBatches;
-  int64_t n = a.n0 + (kOnChip ? o.rest : o.rest / s.chunks);
+  int64_t n = o.n;
+  Ring<1> ring{stage, stride, {reinterpret_cast<const unsigned char*>(px + n * a.s_n)},
+               {step * static_cast<int64_t>(sizeof(T))}, o.cnt};
+  if constexpr (!kOnChip) {
+    ring.start();
+    if (a.early) pdl_wait_prior_grid();
+  }
+  pdl_allow_next_grid();
   if constexpr (kOnChip) {
     if (s.stages == 1)
       for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
@@ -189,33 +202,32 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     load_params(a, m.w, m.b, o.slab);
   }
 
-  for (int k = 0; n < a.n1; n += kOnChip ? s.lanes_n : a.n1) {
+  for (int k = 0; n < a.N; n += kOnChip ? s.lanes_n : a.N) {
     ColumnStats<T> st;
-    const uint4* const mine = stage + k * s.iters * s.threads;
+    const uint32_t mine = stage + k * s.iters * stride;
     if constexpr (kOnChip) {
       if (s.stages == 1) {  // the sums follow the copies, batch by batch
         for (int b = 0; b < kBatches; ++b) {
           cp_async_wait(kBatches - 1 - b);
-          if (b == 0 && o.cnt > 0) st.start(mine[0]);
-          for_staged(mine, b * per, min(o.cnt, (b + 1) * per), s.threads,
-                     [&](int, const uint4& u) { st.add(u); });
+          if (b == 0 && o.cnt > 0) st.start(lds128_at(mine));
+          for_staged(mine, b * per, min(o.cnt, (b + 1) * per), stride,
+                     [&](const uint4& u) { st.add(u); });
         }
       } else {
         const int ahead = s.stages - 1;
         stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
                      0, s.iters);
         cp_async_wait(ahead);
-        if (o.cnt > 0) st.start(mine[0]);
-        for_staged(mine, 0, o.cnt, s.threads, [&](int, const uint4& u) { st.add(u); });
+        if (o.cnt > 0) st.start(lds128_at(mine));
+        for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) { st.add(u); });
       }
     } else {
-      Ring<1> ring{stage, {reinterpret_cast<const unsigned char*>(px + n * a.s_n)},
-                   {step * static_cast<int64_t>(sizeof(T))}, o.cnt, s.threads, 0};
-      ring.start();
-      ring.run([&](int i, const uint4* slot) {
-        if (i == 0) st.start(*slot);
-        st.add(*slot);
-      });
+      if (o.cnt > 0) {
+        cp_async_wait(kRingGroups - 2);
+        st.start(lds128_at(stage));
+      }
+      ring.run(o.cnt, [&](uint32_t slot) { st.add(lds128_at(slot)); });
+      __syncthreads();  // red takes the rings' place
     }
     cta_stats(m, s, o, st);
 
@@ -259,7 +271,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         q.load(m.c0, m.c1, m.b, o.c);
         T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
         const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
-        for_staged(mine, 0, o.cnt, s.threads, [&](int, const uint4& u) {
+        for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) {
           stg128(py, q.template norm<kAct>(u));
           py += ystep;
         });
@@ -286,13 +298,14 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const int tid = threadIdx.x;
-  int64_t n;
-  const Owner o = out_owner(a, &n);
+  const Owner o = out_owner(a);
+  const int64_t n = o.n;
   const int ch = o.slab * s.cs + o.c;
   const int64_t step = s.lanes * a.s_s;
   const T* px = static_cast<const T*>(a.x) + n * a.s_n + (o.r0 + o.lane) * a.s_s + ch;
-  Ring<1> ring{reinterpret_cast<uint4*>(smem) + tid, {reinterpret_cast<const unsigned char*>(px)},
-               {step * static_cast<int64_t>(sizeof(T))}, o.cnt, s.threads, 0};
+  Ring<1> ring{smem_u32(smem) + 16u * tid, 16u * s.threads,
+               {reinterpret_cast<const unsigned char*>(px)},
+               {step * static_cast<int64_t>(sizeof(T))}, o.cnt};
   ring.start();
   float* w = reinterpret_cast<float*>(smem + gn_stage_bytes(s, false));
   float* b = w + s.cs;
@@ -310,22 +323,22 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   for (int g0 = 4 * (tid >> 5); g0 < s.gs; g0 += s.threads >> 3) {
     const int g = g0 + ((tid & 31) >> 3);
     const float2* p = a.part + n * s.chunks * a.G + o.slab * s.gs + g;
+    // about the first chunk's mean, as in cta_stats
     const int chunks = g < s.gs ? s.chunks : 0;
-    auto count = [&](int k) {
-      return static_cast<float>(s.chunk_base + (k < s.chunk_more ? 1 : 0)) * cg;
-    };
+    const float ref = g < s.gs ? p[0].x : 0.f;
     float sum = 0.f, m2 = 0.f;
-#pragma unroll 4
-    for (int k = l8; k < chunks; k += 8)
-      sum = __fmaf_rn(p[static_cast<int64_t>(k) * a.G].x, count(k), sum);
-    const float mean = octet_sum(sum) / total;
 #pragma unroll 4
     for (int k = l8; k < chunks; k += 8) {
       const float2 v = p[static_cast<int64_t>(k) * a.G];
-      const float d = v.x - mean;
-      m2 += __fmaf_rn(d * d, count(k), v.y);
+      const float d = v.x - ref;
+      const float nd = static_cast<float>(s.chunk_base + (k < s.chunk_more ? 1 : 0)) * cg * d;
+      sum += nd;
+      m2 += __fmaf_rn(nd, d, v.y);
     }
+    sum = octet_sum(sum);
     m2 = octet_sum(m2);
+    const float off = sum / total, mean = ref + off;
+    m2 = __fmaf_rn(-off, sum, m2);
     if (g < s.gs) {
       const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
       for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
@@ -345,8 +358,8 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   q.load(c0, c1, b, o.c);
   T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
   const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
-  ring.run([&](int, const uint4* slot) {  // y is not read here again: it leaves L2 first
-    __stcs(reinterpret_cast<uint4*>(py), q.template norm<kAct>(*slot));
+  ring.run(o.cnt, [&](uint32_t slot) {  // y is not read here again: it leaves L2 first
+    __stcs(reinterpret_cast<uint4*>(py), q.template norm<kAct>(lds128_at(slot)));
     py += ystep;
   });
 }
@@ -389,7 +402,7 @@ cudaError_t launch_gn_fwd(const GnArgs& a, int dtype, int act, cudaStream_t st) 
   const void* fn = dtype == GROUPNORM_BF16   ? pick_fwd<__nv_bfloat16>(a.s, act)
                    : dtype == GROUPNORM_FP32 ? pick_fwd<float>(a.s, act)
                                              : pick_fwd<__half>(a.s, act);
-  return launch_cluster(fn, gn_stats_ctas(a.s, a.n1 - a.n0), a.s, a, st);
+  return launch_cluster(fn, gn_stats_ctas(a.s, a.nu), a.s, a, st);
 }
 
 cudaError_t launch_gn_fwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st) {

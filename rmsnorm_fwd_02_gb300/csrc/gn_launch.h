@@ -28,7 +28,7 @@ struct GnShape {
   int chunks;    // two launches: chunks of places a sample's statistics are split into: the
                  // first chunk_more of chunk_base + 1 places, the others of chunk_base
   int chunk_base, chunk_more;
-  int samples;   // two launches: samples a pair of launches takes
+  int units;     // two launches: units (slabs of samples) a pair of launches takes
   int parts;     // two launches: chunks of places of the second launch, alike
   int part_base, part_more;
   size_t smem;   // dynamic shared memory of the (first) launch
@@ -45,8 +45,12 @@ struct GnArgs {
   float2* part;          // two launches: [N][chunks][G]: (mean, M2), or (sum g*xhat, sum g)
   float* cols;           // backward: [.][2][C] column sums (dw, then db)
   int64_t s_n, s_s;      // x's strides
-  int64_t n0;            // first sample of this launch
-  int64_t n1;            // end of its samples
+  int64_t N;
+  // two launches: units [u0, u0 + nu) of the N * slabs, unit u the slab u % slabs of sample
+  // u / slabs; `early`: x was complete before the launch before this one began
+  int64_t u0;
+  int32_t nu;
+  int32_t early;
   int64_t S;
   int32_t C, G;
   int32_t wb_dtype;
@@ -54,60 +58,67 @@ struct GnArgs {
   GnShape s;
 };
 
-// Two builds of every kernel: CTAs of up to kThreads threads, kCtas of them an SM (80 registers
-// a thread, no spills; the forward's second launch fits four, with 64), and, for slabs of more
-// than kThreads vectors, up to kWideThreads threads, one CTA an SM (128 registers).
+// Two builds of every kernel, both with 128 registers a thread (enough for several vectors'
+// independent work, which hides more latency here than a third CTA of 80 registers did: 5-15 %
+// at every size measured): CTAs of up to kThreads threads, kCtas of them an SM, and, for slabs
+// of more than kThreads vectors, up to kWideThreads threads, one CTA an SM.
 constexpr int kThreads = 256, kWideThreads = 512;
-constexpr int kCtas = 3;
+constexpr int kCtas = 2;
 constexpr int kMaxCluster = 8;
 constexpr int max_threads(bool wide) { return wide ? kWideThreads : kThreads; }
 constexpr int min_ctas(bool wide) { return wide ? 1 : kCtas; }
 
-// Shared memory behind the staged vectors (floats), in this order:
-//   red   2 planes [lanes][red_stride]: per-thread column values on their way to column sums
-//         (forward: mean and M2; backward: A and B)
-//   gm    2 * gs: the CTA's group values
-//   w, b  cs parameters each
-//   c0, c1  cs channel constants each (forward: -mean and rstd * w; backward: nc1 and nc2)
-//   col   2 * cs column values; on chip backward: + 4 * cs running totals (sum, compensation)
-// A row of red is padded so that four rows of eight columns fall on 32 different banks wherever
-// the slab is a multiple of 32 channels.
-inline __host__ __device__ int red_stride(const GnShape& s) { return s.cs + (s.cs % 32 ? 0 : 8); }
-inline __host__ __device__ size_t gn_extra_floats(const GnShape& s, bool bwd) {
-  size_t n = 2 * static_cast<size_t>(s.lanes) * red_stride(s);
-  n += 2 * static_cast<size_t>(s.gs) + 6 * static_cast<size_t>(s.cs);
-  if (bwd && s.on_chip) n += 4 * static_cast<size_t>(s.cs);
-  return (n + 3) & ~static_cast<size_t>(3);
-}
 // Two launches: each thread's copies run through a ring of kRingGroups groups of kRingPlaces
-// places; on chip, `iters` places are staged.
+// places; on chip, `iters` places of each of `stages` samples are staged.
 constexpr int kRingGroups = 4, kRingPlaces = 2;
 // Bytes of one staged sample, or of the ring.
 inline __host__ __device__ size_t gn_stage_bytes(const GnShape& s, bool bwd) {
   return static_cast<size_t>(bwd ? 2 : 1) * (s.on_chip ? s.iters : kRingGroups * kRingPlaces) *
          s.threads * 16;
 }
+// Shared memory of the statistics kernels behind the staged vectors, in floats:
+//   w, b  cs parameters each
+//   c0, c1  cs channel constants each (forward: -mean and rstd * w; backward: nc1 and nc2)
+//   col   2 * cs column values; on chip backward: + 4 * cs running totals (sum, compensation)
+//   gm    2 * gs: the CTA's group values
+//   red   2 planes [lanes][red_stride]: per-thread column values on their way to column sums
+//         (forward: mean and M2; backward: A and B); two launches: over the ring, which is
+//         done by then
+// A row of red is padded so that four rows of eight columns fall on 32 different banks wherever
+// the slab is a multiple of 32 channels.
+inline __host__ __device__ int red_stride(const GnShape& s) { return s.cs + (s.cs % 32 ? 0 : 8); }
+inline __host__ __device__ size_t gn_red_bytes(const GnShape& s) {
+  return 2 * static_cast<size_t>(s.lanes) * red_stride(s) * sizeof(float);
+}
+inline __host__ __device__ size_t gn_front_bytes(const GnShape& s, bool bwd) {  // staged vectors
+  const size_t stage = gn_stage_bytes(s, bwd), red = gn_red_bytes(s);
+  if (s.on_chip) return stage * s.stages;
+  return ((stage > red ? stage : red) + 15) & ~static_cast<size_t>(15);
+}
+inline __host__ __device__ size_t gn_stats_smem(const GnShape& s, bool bwd) {
+  const size_t n = 6 * static_cast<size_t>(s.cs) + (bwd && s.on_chip ? 4 * s.cs : 0) +
+                   (2 * static_cast<size_t>(s.gs) + 3) / 4 * 4;
+  return gn_front_bytes(s, bwd) + n * sizeof(float) + (s.on_chip ? gn_red_bytes(s) : 0);
+}
 // Shared memory of the second launch: the ring, then w, b, c0, c1 as above.
 inline __host__ __device__ size_t gn_out_smem(const GnShape& s, bool bwd) {
   return gn_stage_bytes(s, bwd) + (4 * static_cast<size_t>(s.cs)) * sizeof(float);
 }
 
-// CTAs of the launches over `samples` samples.
-inline int64_t gn_stats_ctas(const GnShape& s, int64_t samples) {
-  return static_cast<int64_t>(s.slabs) * s.ctas * (s.on_chip ? s.lanes_n : samples * s.chunks);
+// CTAs of the launches (two launches: over nu units).
+inline int64_t gn_stats_ctas(const GnShape& s, int64_t nu) {
+  return s.on_chip ? static_cast<int64_t>(s.slabs) * s.ctas * s.lanes_n : nu * s.ctas * s.chunks;
 }
-inline int64_t gn_out_ctas(const GnShape& s, int64_t samples) {
-  return static_cast<int64_t>(s.slabs) * samples * s.parts;
-}
+inline int64_t gn_out_ctas(const GnShape& s, int64_t nu) { return nu * s.parts; }
 
 // Launches fn over `ctas` CTAs in clusters of s.ctas, with programmatic dependent launch.
 cudaError_t launch_cluster(const void* fn, int64_t ctas, const GnShape& s, const GnArgs& a,
                            cudaStream_t st);
 
-// Launches fn, a second launch, over the samples [a.n0, a.n1).
+// Launches fn, a second launch, over the units of a.
 cudaError_t launch_out(const void* fn, const GnArgs& a, bool bwd, cudaStream_t st);
 
-// Launch the statistics (and, on chip, the output) of samples [a.n0, a.n1); then, for two
+// Launch the statistics (and, on chip, the output) of a's samples or units; then, for two
 // launches, the output.  dtype and act: GROUPNORM_*.
 cudaError_t launch_gn_fwd(const GnArgs& a, int dtype, int act, cudaStream_t st);
 cudaError_t launch_gn_fwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st);

@@ -19,6 +19,9 @@ struct VecOf<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = bf2_to_f2(u4_get(u, i));
   }
+  __device__ static __forceinline__ f2 pair(const uint4& u, int i) {
+    return bf2_to_f2(u4_get(u, i));
+  }
   // pair i of u plus nk, each rounded once: a mixed-precision fma x * 1 + nk per element reads
   // the 16-bit halves without a conversion
   __device__ static __forceinline__ f2 plus(const uint4& u, int i, f2 nk) {
@@ -52,6 +55,7 @@ struct VecOf<__half> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = widen(u4_get(u, i));
   }
+  __device__ static __forceinline__ f2 pair(const uint4& u, int i) { return widen(u4_get(u, i)); }
   __device__ static __forceinline__ f2 plus(const uint4& u, int i, f2 nk) {
     f2 r;
     asm("{\n\t.reg .b16 a0, a1, one;\n\t.reg .f32 c0, c1, p0, p1;\n\t"
@@ -75,10 +79,12 @@ struct VecOf<float> {
     f[0] = f2_make(__uint_as_float(u.x), __uint_as_float(u.y));
     f[1] = f2_make(__uint_as_float(u.z), __uint_as_float(u.w));
   }
+  __device__ static __forceinline__ f2 pair(const uint4& u, int i) {
+    return i == 0 ? f2_make(__uint_as_float(u.x), __uint_as_float(u.y))
+                  : f2_make(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
   __device__ static __forceinline__ f2 plus(const uint4& u, int i, f2 nk) {
-    return f2_add(i == 0 ? f2_make(__uint_as_float(u.x), __uint_as_float(u.y))
-                         : f2_make(__uint_as_float(u.z), __uint_as_float(u.w)),
-                  nk);
+    return f2_add(pair(u, i), nk);
   }
   __device__ static __forceinline__ uint4 pack(const f2 (&f)[2]) {
     return make_uint4(__float_as_uint(f2_lo(f[0])), __float_as_uint(f2_hi(f[0])),

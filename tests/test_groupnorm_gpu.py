@@ -51,11 +51,10 @@ def depth(x, groups, bwd):
     n, s, c = x.shape
     p = N.groupnorm_train_launch_plan(GN._DTYPES[x.dtype], n, s, c, groups, bwd)
     lanes = max(1, p["threads"] * (16 // x.element_size()) // p["channels"])
-    slabs = c // p["channels"]
     if p["on_chip"]:
         rows, chunks = -(-s // p["cluster_ctas"]), 1
     else:
-        chunks = p["ctas"] // (p["samples"] * slabs * p["cluster_ctas"])
+        chunks = p["ctas"] // (p["units"] * p["cluster_ctas"])
         rows = -(-s // (chunks * p["cluster_ctas"])) + 1
     # a thread's places (at least half the lanes the plan has threads for), four lanes of a
     # column at a time, eight columns of a group, eight chunks; the trees between
@@ -196,7 +195,7 @@ def test_two_launches(n, s, c, groups, dtype):
     plans = [N.groupnorm_train_launch_plan(GN._DTYPES[dtype], n, s, c, groups, d) for d in (0, 1)]
     assert not plans[1]["on_chip"]
     if n > 1:
-        assert not plans[0]["on_chip"] and plans[0]["samples"] < n
+        assert not plans[0]["on_chip"] and plans[0]["units"] < n * c // plans[0]["channels"]
     got = check_fwd(x, w, b, groups, "silu")
     grads = check_bwd(dy, x, w, b, groups, "silu")
     assert all(torch.equal(p, q) for p, q in zip(got, R.groupnorm_fwd(x, w, b, groups, EPS, "silu")))
