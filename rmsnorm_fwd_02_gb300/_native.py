@@ -67,7 +67,7 @@ DROPOUT_BF16, DROPOUT_FP32, DROPOUT_FP16 = 0, 1, 2
 GROUPNORM_BF16, GROUPNORM_FP32, GROUPNORM_FP16 = 0, 1, 2
 GROUPNORM_ACT_NONE, GROUPNORM_ACT_SILU, GROUPNORM_ACT_GELU = 0, 1, 2
 GROUPNORM_PLAN_FIELDS = ("on_chip", "channels", "threads", "cluster_ctas", "ctas", "smem",
-                         "units", "out_ctas")
+                         "units", "chunks")
 
 PLAN_FWD, PLAN_FWD_RESIDUAL, PLAN_BWD, PLAN_BWD_DH, PLAN_BWD_ND, PLAN_BWD_ND_DH = 0, 1, 2, 3, 4, 5
 LN_PLAN_FWD, LN_PLAN_BWD = 0, 1

@@ -30,12 +30,11 @@ int64_t resident(int per_sm, int ctas) {
   return per_sm <= 4 ? t[per_sm - 1] : t[3] / 4 * per_sm;
 }
 // Bytes a place's slab aims at: at least a DRAM burst of two 64-byte halves.
-constexpr int kSlabBytes = 128, kWideSlabBytes = 256, kMinSlabBytes = 32;
+constexpr int kSlabBytes = 128, kMinSlabBytes = 32;
 constexpr int kSmallCta = 16 * 1024;  // staged bytes below which a CTA is not split further
 constexpr int kMaxStages = 4;
-constexpr int kChunkCluster = 4;
-// two launches: bytes of x (and dy) a pair of launches may take, to be found in L2 again
-constexpr int64_t kL2Bytes = int64_t{72} << 20;
+// streamed: bytes of x (and dy) a turn may take, to be found in L2 again
+constexpr int64_t kL2Bytes = int64_t{64} << 20;
 
 int elem_bytes(int dtype) { return dtype == GROUPNORM_FP32 ? 4 : 2; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -148,39 +147,28 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
     on_chip_loop(&chip, N, bwd);
     return chip;
   }
-  // two launches
-  int gs = slab_groups(dtype, C, G, kWideSlabBytes);
+  // streamed
+  int gs = slab_groups(dtype, C, G, kSlabBytes);
   auto slab_bytes = [&] { return S * gs * (C / G) * elem_bytes(dtype) * (bwd ? 2 : 1); };
-  for (int bytes = kWideSlabBytes / 2; bytes >= kMinSlabBytes && slab_bytes() > kL2Bytes; bytes /= 2)
-    gs = slab_groups(dtype, C, G, bytes);
+  if (slab_bytes() > kL2Bytes) gs = slab_groups(dtype, C, G, kSlabBytes / 2);
   GnShape s = slab_shape(dtype, C, G, gs, S, 4);
   const int64_t all = N * s.slabs;
   int64_t units = kL2Bytes / slab_bytes();
   units = units < 1 ? 1 : (units > all ? all : units);
   units = ceil_div(all, ceil_div(all, units));  // evened out
+  if (units > INT32_MAX / 2) units = INT32_MAX / 2;
   s.units = static_cast<int>(units);
-  // clusters only thin the partial statistics that the second launch adds up
-  while (s.ctas < kChunkCluster && S >= static_cast<int64_t>(s.ctas) * 2 * s.lanes * 4) {
-    s.ctas *= 2;
-    ++s.ctas_log2;
-  }
-  const int64_t lane_rows = static_cast<int64_t>(s.ctas) * s.lanes;  // places a cluster step
-  // at most one wave of the statistics kernel, each thread 8 to 256 places
-  int64_t chunks = resident(kCtas, s.ctas) / (units * s.ctas);
-  if (chunks > S / (lane_rows * 8)) chunks = S / (lane_rows * 8);
-  if (chunks < ceil_div(S, lane_rows * 256)) chunks = ceil_div(S, lane_rows * 256);
+  s.grid = kSMs * min_ctas(s.vecs > kThreads);
+  // a piece a CTA, each thread 4 to 256 places
+  int64_t chunks = s.grid / units;
+  if (chunks > S / (4 * s.lanes)) chunks = S / (4 * s.lanes);
+  if (chunks < ceil_div(S, 256 * static_cast<int64_t>(s.lanes)))
+    chunks = ceil_div(S, 256 * static_cast<int64_t>(s.lanes));
   s.chunks = static_cast<int>(chunks);
   s.chunk_base = static_cast<int>(S / chunks);
   s.chunk_more = static_cast<int>(S % chunks);
+  if (units * chunks < s.grid) s.grid = static_cast<int>(units * chunks);
   s.iters = 0;  // nothing stays staged
-  // two waves of the second kernel, a thread four places at least
-  int64_t parts = 2 * kSMs * kCtas / units;
-  if (parts > ceil_div(S, static_cast<int64_t>(s.lanes) * 4))
-    parts = ceil_div(S, static_cast<int64_t>(s.lanes) * 4);
-  if (parts < 1) parts = 1;
-  s.parts = static_cast<int>(parts);
-  s.part_base = static_cast<int>(S / parts);
-  s.part_more = static_cast<int>(S % parts);
   s.smem = gn_stats_smem(s, bwd);
   return s;
 }
@@ -203,7 +191,7 @@ size_t part_bytes(const GnShape& s, int64_t N, int G) {
   return (n + 15) & ~static_cast<size_t>(15);
 }
 int64_t col_rows(const GnShape& s, int64_t N) {
-  return s.on_chip ? static_cast<int64_t>(s.lanes_n) * s.ctas : N * s.chunks * s.ctas;
+  return s.on_chip ? static_cast<int64_t>(s.lanes_n) * s.ctas : N * s.chunks;
 }
 size_t workspace_bytes(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
   const GnShape s = plan(dtype, N, S, C, G, bwd);
@@ -257,34 +245,37 @@ GnArgs make_args(const void* x, const void* w, const void* b, int wb_dtype, void
 
 }  // namespace
 
-cudaError_t launch_out(const void* fn, const GnArgs& a, bool bwd, cudaStream_t st) {
-  const size_t smem = gn_out_smem(a.s, bwd);
-  const cudaError_t e = rmsn::prepare_kernel(fn, smem);
-  if (e != cudaSuccess) return e;
-  GnArgs copy = a;
-  void* args[] = {&copy};
-  return rmsn::launch_pdl(fn, dim3(static_cast<unsigned>(gn_out_ctas(a.s, a.nu))),
-                          dim3(static_cast<unsigned>(a.s.threads)), smem, st, args);
-}
-
-cudaError_t launch_cluster(const void* fn, int64_t ctas, const GnShape& s, const GnArgs& a,
-                           cudaStream_t st) {
+cudaError_t launch_gn(const void* fn, const GnArgs& a, cudaStream_t st) {
+  const GnShape& s = a.s;
   cudaError_t e = rmsn::prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
+  int64_t ctas = gn_ctas(s);
+  if (!s.on_chip) {  // no more than are resident together (the pieces do not depend on it)
+    int sms = 0;
+    if (rmsn::check_device(&sms) != RMSN_OK) return cudaErrorInvalidDevice;
+    const int64_t most = static_cast<int64_t>(sms) * rmsn::blocks_per_sm(fn, s.threads, s.smem);
+    if (ctas > most) ctas = most;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(static_cast<unsigned>(s.threads));
   cfg.dynamicSmemBytes = s.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(s.ctas);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = s.ctas > 1 ? 2 : 1;
+  if (s.on_chip) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(s.ctas);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = s.ctas > 1 ? 2 : 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.numAttrs = 1;
+  }
   GnArgs copy = a;
   void* args[] = {&copy};
   return cudaLaunchKernelExC(&cfg, fn, args);
@@ -324,16 +315,7 @@ int groupnorm_train_fwd(const void* x, int dtype, const void* w, const void* b, 
   const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
   GnArgs a = make_args(x, w, b, wb_dtype, y, mean, rstd, workspace, N, S, C, G, s_n, s_s, s);
   a.eps = eps;
-  if (s.on_chip)
-    return launch_gn_fwd(a, dtype, act, stream_) == cudaSuccess ? RMSN_OK : RMSN_ERR_CUDA;
-  const int64_t all = N * s.slabs;
-  for (a.u0 = 0; a.u0 < all; a.u0 += s.units, a.early = 1) {
-    a.nu = static_cast<int32_t>(all - a.u0 < s.units ? all - a.u0 : s.units);
-    if (launch_gn_fwd(a, dtype, act, stream_) != cudaSuccess ||
-        launch_gn_fwd_out(a, dtype, act, stream_) != cudaSuccess)
-      return RMSN_ERR_CUDA;
-  }
-  return RMSN_OK;
+  return launch_gn_fwd(a, dtype, act, stream_) == cudaSuccess ? RMSN_OK : RMSN_ERR_CUDA;
 }
 
 int groupnorm_train_bwd(const void* x, const void* dy, int dtype, const float* mean,
@@ -359,17 +341,7 @@ int groupnorm_train_bwd(const void* x, const void* dy, int dtype, const float* m
   GnArgs a = make_args(x, w, b, wb_dtype, dx, const_cast<float*>(mean), const_cast<float*>(rstd),
                        workspace, N, S, C, G, s_n, s_s, s);
   a.dy = dy;
-  if (N > 0 && s.on_chip) {
-    if (launch_gn_bwd(a, dtype, act, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
-  } else {
-    const int64_t all = N * s.slabs;
-    for (a.u0 = 0; a.u0 < all; a.u0 += s.units, a.early = 1) {
-      a.nu = static_cast<int32_t>(all - a.u0 < s.units ? all - a.u0 : s.units);
-      if (launch_gn_bwd(a, dtype, act, stream_) != cudaSuccess ||
-          launch_gn_bwd_out(a, dtype, act, stream_) != cudaSuccess)
-        return RMSN_ERR_CUDA;
-    }
-  }
+  if (N > 0 && launch_gn_bwd(a, dtype, act, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
   return launch_gn_finish(a.cols, dw, db, rows, C, stream_) == cudaSuccess ? RMSN_OK
                                                                          : RMSN_ERR_CUDA;
 }
@@ -382,9 +354,8 @@ int groupnorm_train_launch_plan(int dtype, int64_t N, int64_t S, int32_t C, int3
   if (N == 0) return RMSN_ERR_INVALID_ARG;
   const GnShape s = plan(dtype, N, S, C, G, backward != 0);
   const int64_t v[GROUPNORM_PLAN_FIELDS] = {
-      s.on_chip, s.cs, s.threads, s.ctas, gn_stats_ctas(s, s.units),
-      static_cast<int64_t>(s.smem), s.on_chip ? N * s.slabs : s.units,
-      s.on_chip ? 0 : gn_out_ctas(s, s.units)};
+      s.on_chip, s.cs, s.threads, s.on_chip ? s.ctas : 1, gn_ctas(s),
+      static_cast<int64_t>(s.smem), s.on_chip ? N * s.slabs : s.units, s.on_chip ? 1 : s.chunks};
   for (int i = 0; i < n_out && i < GROUPNORM_PLAN_FIELDS; ++i) out[i] = v[i];
   return RMSN_OK;
 }

@@ -3,12 +3,12 @@
 //
 // Per channel of a sample, A_c = sum over places of dz * xhat and B_c = sum of dz; a group's
 // mean(g * xhat) and mean(g) are w-weighted sums of them, and dw_c, db_c their sums over the
-// samples -- one set of sums serves all.  As the forward (gn_fwd.cu): one launch that keeps x
-// and dy on chip between the sums and dx where a cluster's shared memory holds them, else two
-// launches over as many slabs as L2 holds.  dz is formed twice from x and dy rather than kept
-// (keeping it in FP32 would double the staged bytes).  The column sums of each CTA (on chip:
-// over all the samples it takes, compensated) go to the workspace, and a finishing kernel adds
-// them in a fixed order.
+// samples -- one set of sums serves all.  As the forward (gn_fwd.cu): x and dy stay on chip
+// between the sums and dx where a cluster's shared memory holds them, and are streamed by a
+// cooperative grid, twice through L2, where not.  dz is formed twice from x and dy rather than
+// kept (keeping it in FP32 would double the staged bytes).  The column sums of each CTA (on
+// chip: over all the samples it takes, compensated) go to the workspace, and a finishing kernel
+// adds them in a fixed order.
 #include "gn_common.cuh"
 
 namespace gnorm {
@@ -109,14 +109,84 @@ struct ColumnSums {
   }
 };
 
-template <typename T, int kAct, bool kOnChip, bool kWide>
+// Column sums over the CTA's places from its threads': A * rstd (= sum of dz * xhat) to
+// m.col[0, cs), B to [cs, 2 cs).  A warp takes eight quads of columns, four lanes of each at a
+// time; each value also goes to sink(half, column of the slab, value).  Then the CTA's group sums
+// of w * A and w * B to m.gm, an octet of threads a group.
+template <typename T, int kAct, typename F>
+__device__ __forceinline__ void cta_sums(const Smem& m, const GnShape& s, const Owner& o,
+                                         const ColumnSums<T, kAct>& sum, const float* rstd,
+                                         F sink) {
+  constexpr int NP = VecOf<T>::kPairs;
+  const int w = threadIdx.x >> 5, nw = s.threads >> 5, l8 = threadIdx.x & 7;
+  const int oct = (threadIdx.x & 31) >> 3;
+  const int rs = red_stride(s), plane = s.lanes * rs;
+  if (o.lane < s.lanes) {
+    sts_pairs<NP>(m.red + o.lane * rs + o.c, sum.A);
+    sts_pairs<NP>(m.red + plane + o.lane * rs + o.c, sum.B);
+  }
+  __syncthreads();
+  const int tasks = (s.cs + 31) >> 5;
+  for (int t = w; t < 2 * tasks; t += nw) {
+    const int half = t >= tasks ? 1 : 0;
+    const int c = 4 * (8 * (t - half * tasks) + l8);
+    const float* p = m.red + half * plane + (c < s.cs ? c : 0);
+    f2 v[2] = {f2_splat(0.f), f2_splat(0.f)};
+#pragma unroll 4
+    for (int l = oct; l < s.lanes; l += 4) {
+      f2 u[2];
+      lds_quad(p + l * rs, u);
+      v[0] = f2_add(v[0], u[0]);
+      v[1] = f2_add(v[1], u[1]);
+    }
+    v[0] = across_octets(v[0]);
+    v[1] = across_octets(v[1]);
+    // lane `oct` of the four keeps column c + oct
+    const float mine = oct == 0 ? f2_lo(v[0])
+                       : oct == 1 ? f2_hi(v[0]) : (oct == 2 ? f2_lo(v[1]) : f2_hi(v[1]));
+    if (c < s.cs) {
+      const int cc = c + oct;
+      const float val = half == 0 ? mine * rstd[cc / s.cg] : mine;
+      m.col[half * s.cs + cc] = val;
+      sink(half, cc, val);
+    }
+  }
+  __syncthreads();
+  for (int b = 4 * w; b < s.gs; b += 4 * nw) {  // whole warps: the shuffles need them
+    const int g = b + oct;
+    float sa = 0.f, sb = 0.f;
+    if (g < s.gs)
+      for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
+        sa = __fmaf_rn(m.w[i], m.col[i], sa);
+        sb = __fmaf_rn(m.w[i], m.col[s.cs + i], sb);
+      }
+    sa = octet_sum(sa);
+    sb = octet_sum(sb);
+    if (l8 == 0 && g < s.gs) {
+      m.gm[2 * g] = sa;
+      m.gm[2 * g + 1] = sb;
+    }
+  }
+}
+
+// Channel constants of group g of the slab from its sums sa = sum g * xhat and sb = sum g, lane k
+// of `lanes` threads.
+__device__ __forceinline__ void set_group(const Smem& m, const GnShape& s, int g, int k, int lanes,
+                                          float rstd, float sa, float sb, float total) {
+  const float nc1 = -rstd * (sb / total), nc2 = -rstd * rstd * (sa / total);
+  for (int i = g * s.cg + k; i < (g + 1) * s.cg; i += lanes) {
+    m.c0[i] = nc1;
+    m.c1[i] = nc2;
+  }
+}
+
+template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     gn_bwd_kernel(const GnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int NP = VecOf<T>::kPairs;
   const GnShape& s = a.s;
   const Smem m = carve(smem, s, true);
-  const Owner o = owner<kOnChip>(a);
+  const Owner o = on_chip_owner(a);
   const int tid = threadIdx.x;
   const int ch = o.slab * s.cs + o.c, group0 = o.slab * s.gs;
   const int og = o.c / s.cg, orr = o.c - og * s.cg;
@@ -126,12 +196,13 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   const T* const pd = static_cast<const T*>(a.dy) + at0;
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
 
-  if (kOnChip || !a.early) pdl_wait_prior_grid();
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
 
-  // on chip: this thread's slot of place i of stage k is stage + (2 * k * iters + i) * stride for
-  // x, and dy_off behind it for dy
+  // this thread's slot of place i of stage k is stage + (2 * k * iters + i) * stride for x, and
+  // dy_off behind it for dy
   const uint32_t stride = 16u * s.threads, stage = smem_u32(smem) + 16u * tid;
-  const uint32_t dy_off = (kOnChip ? s.iters : kRingSlots) * stride;
+  const uint32_t dy_off = s.iters * stride;
   auto stage_places = [&](int64_t n, int k, int from, int to) {
     if (n < a.N) {
       const T* p = px + n * a.s_n + from * step;
@@ -147,118 +218,44 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   constexpr int kBatches = 4;  // of a single-stage sample
   const int per = (s.iters + kBatches - 1) / kBatches;
   int64_t n = o.n;
-  if constexpr (kOnChip) {
-    if (s.stages == 1)
-      for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
-    for (int k = 0; k + 1 < s.stages; ++k) stage_places(n + k * s.lanes_n, k, 0, s.iters);
-    // running column totals (sum, compensation)
-    for (int i = tid; i < 4 * s.cs; i += s.threads) m.run[i] = 0.f;
-  }
-  Ring<2> ring;
-  if constexpr (!kOnChip) {
-    ring = Ring<2>{stage, stride,
-                   {reinterpret_cast<const unsigned char*>(px + n * a.s_n),
-                    reinterpret_cast<const unsigned char*>(pd + n * a.S * a.C)},
-                   {step * static_cast<int64_t>(sizeof(T)), dstep * static_cast<int64_t>(sizeof(T))},
-                   o.cnt};
-    ring.start();
-    if (a.early) pdl_wait_prior_grid();
-  }
-  pdl_allow_next_grid();
+  if (s.stages == 1)
+    for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
+  for (int k = 0; k + 1 < s.stages; ++k) stage_places(n + k * s.lanes_n, k, 0, s.iters);
+  // running column totals (sum, compensation)
+  for (int i = tid; i < 4 * s.cs; i += s.threads) m.run[i] = 0.f;
   load_params(a, m.w, m.b, o.slab);
   __syncthreads();
 
-  const int l8 = tid & 7, oct = (tid & 31) >> 3, w = tid >> 5, nw = s.threads >> 5;
-  for (int k = 0; n < a.N; n += kOnChip ? s.lanes_n : a.N) {
+  const int l8 = tid & 7, oct = (tid & 31) >> 3;
+  for (int k = 0; n < a.N; n += s.lanes_n) {
     const float* const mean = a.mean + n * a.G + group0;
     const float* const rstd = a.rstd + n * a.G + group0;
     Consts<T> q;
     ColumnSums<T, kAct> sum;
     sum.clear();
     const uint32_t mine = stage + 2 * k * s.iters * stride;
-    if constexpr (kOnChip) {
-      if (s.stages == 1) {  // the sums follow the copies, batch by batch
-        if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
-        for (int b = 0; b < kBatches; ++b) {
-          cp_async_wait(kBatches - 1 - b);
-          for_staged2(mine, dy_off, b * per, min(o.cnt, (b + 1) * per), stride,
-                      [&](const uint4& xu, const uint4& du) { sum.add(q, xu, du); });
-        }
-      } else {
-        const int ahead = s.stages - 1;
-        stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
-                     0, s.iters);
-        if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
-        cp_async_wait(ahead);
-        for_staged2(mine, dy_off, 0, o.cnt, stride,
-                    [&](const uint4& xu, const uint4& du) { sum.add(q, xu, du); });
+    auto add = [&](const uint4& xu, const uint4& du) { sum.add(q, xu, du); };
+    if (s.stages == 1) {  // the sums follow the copies, batch by batch
+      if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
+      for (int b = 0; b < kBatches; ++b) {
+        cp_async_wait(kBatches - 1 - b);
+        for_staged2(mine, dy_off, b * per, min(o.cnt, (b + 1) * per), stride, add);
       }
     } else {
+      const int ahead = s.stages - 1;
+      stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
+                   0, s.iters);
       if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
-      ring.run(o.cnt, [&](uint32_t slot) {
-        sum.add(q, lds128_at(slot), lds128_at(slot + dy_off));
-      });
-      __syncthreads();  // red takes the rings' place
+      cp_async_wait(ahead);
+      for_staged2(mine, dy_off, 0, o.cnt, stride, add);
     }
-
-    // column sums over the CTA's places: A * rstd (= sum of dz * xhat) in col[0, cs), B in
-    // [cs, 2 cs); a warp takes eight quads of columns, four lanes of each at a time
-    const int rs = red_stride(s), plane = s.lanes * rs;
-    if (o.lane < s.lanes) {
-      sts_pairs<NP>(m.red + o.lane * rs + o.c, sum.A);
-      sts_pairs<NP>(m.red + plane + o.lane * rs + o.c, sum.B);
-    }
-    __syncthreads();
-    const int tasks = (s.cs + 31) >> 5;
-    for (int t = w; t < 2 * tasks; t += nw) {
-      const int half = t >= tasks ? 1 : 0;
-      const int c = 4 * (8 * (t - half * tasks) + l8);
-      const float* p = m.red + half * plane + (c < s.cs ? c : 0);
-      f2 v[2] = {f2_splat(0.f), f2_splat(0.f)};
-#pragma unroll 4
-      for (int l = oct; l < s.lanes; l += 4) {
-        f2 u[2];
-        lds_quad(p + l * rs, u);
-        v[0] = f2_add(v[0], u[0]);
-        v[1] = f2_add(v[1], u[1]);
-      }
-      v[0] = across_octets(v[0]);
-      v[1] = across_octets(v[1]);
-      // lane `oct` of the four keeps column c + oct
-      const float mine_v = oct == 0 ? f2_lo(v[0])
-                           : oct == 1 ? f2_hi(v[0]) : (oct == 2 ? f2_lo(v[1]) : f2_hi(v[1]));
-      if (c < s.cs) {
-        const int cc = c + oct, at = half * s.cs + cc;
-        const float val = half == 0 ? mine_v * rstd[cc / s.cg] : mine_v;
-        m.col[at] = val;
-        if constexpr (kOnChip) {  // Kahan's running sum over the samples
-          const float y = __fsub_rn(val, m.run[2 * at + 1]);
-          const float r = __fadd_rn(m.run[2 * at], y);
-          m.run[2 * at + 1] = __fsub_rn(__fsub_rn(r, m.run[2 * at]), y);
-          m.run[2 * at] = r;
-        } else {
-          a.cols[((n * s.chunks + o.chunk) * s.ctas + o.rank) * 2 * a.C + half * a.C +
-                 o.slab * s.cs + cc] = val;
-        }
-      }
-    }
-    __syncthreads();
-    // the CTA's group sums of w * A and w * B: an octet of threads a group
-    for (int b = 4 * w; b < s.gs; b += 4 * nw) {  // whole warps: the shuffles need them
-      const int g = b + oct;
-      float sa = 0.f, sb = 0.f;
-      if (g < s.gs)
-        for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
-          sa = __fmaf_rn(m.w[i], m.col[i], sa);
-          sb = __fmaf_rn(m.w[i], m.col[s.cs + i], sb);
-        }
-      sa = octet_sum(sa);
-      sb = octet_sum(sb);
-      if (l8 == 0 && g < s.gs) {
-        m.gm[2 * g] = sa;
-        m.gm[2 * g + 1] = sb;
-      }
-    }
+    cta_sums(m, s, o, sum, rstd, [&](int half, int c, float v) {
+      float* run = m.run + 2 * (half * s.cs + c);  // Kahan's running sum over the samples
+      const float y = __fsub_rn(v, run[1]);
+      const float r = __fadd_rn(run[0], y);
+      run[1] = __fsub_rn(__fsub_rn(r, run[0]), y);
+      run[0] = r;
+    });
     // the cluster's: an octet of threads a group, a CTA a thread
     if (s.ctas > 1) {
       cluster_arrive();
@@ -266,127 +263,142 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     } else {
       __syncthreads();
     }
-    for (int b = 4 * w; b < s.gs; b += 4 * nw) {
+    for (int b = 4 * (tid >> 5); b < s.gs; b += s.threads >> 3) {
       const int g = b + oct;
       float2 v = make_float2(0.f, 0.f);
       if (g < s.gs && l8 < s.ctas)
         v = s.ctas > 1 ? ld_peer_f2(peer_addr(m.gm + 2 * g, static_cast<uint32_t>(l8)))
                        : make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
       const float sa = octet_sum(v.x), sb = octet_sum(v.y);
-      if constexpr (kOnChip) {
-        if (g < s.gs) {
-          const float r = rstd[g];
-          const float nc1 = -r * (sb / total), nc2 = -r * r * (sa / total);
-          for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
-            m.c0[i] = nc1;
-            m.c1[i] = nc2;
-          }
-        }
-      } else if (l8 == 0 && g < s.gs && o.rank == 0) {
-        a.part[(n * s.chunks + o.chunk) * a.G + group0 + g] = make_float2(sa, sb);
-      }
+      if (g < s.gs) set_group(m, s, g, l8, 8, rstd[g], sa, sb, total);
     }
     if (s.ctas > 1) cluster_arrive();  // this CTA's reads of the others are done
-    if constexpr (kOnChip) {
+    __syncthreads();
+    if (o.cnt > 0) {
+      GroupTerms<T> t;
+      t.load(m.c0, m.c1, o.c);
+      T* po = static_cast<T*>(a.out) + n * a.S * a.C + at0;
+      for_staged2(mine, dy_off, 0, o.cnt, stride, [&](const uint4& xu, const uint4& du) {
+        stg128(po, dx_vec<T, kAct>(q, t, xu, du));
+        po += dstep;
+      });
+    }
+    if (s.stages == 1) {
+      for (int b = 0; b < kBatches; ++b) stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
+    } else if (++k == s.stages) {
+      k = 0;
+    }
+    if (s.ctas > 1) cluster_wait();
+  }
+  __syncthreads();
+  // this CTA's totals over its samples
+  float* out = a.cols + (o.n * s.ctas + o.rank) * 2 * a.C + o.slab * s.cs;
+  for (int t = tid; t < 2 * s.cs; t += s.threads)
+    out[t < s.cs ? t : a.C + t - s.cs] = m.run[2 * t];
+}
+
+// Streamed, as the forward's (gn_fwd.cu): a turn's sums, the barrier, its dx.
+template <typename T, int kAct, bool kWide>
+__global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
+    gn_bwd_stream_kernel(const GnArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const GnShape& s = a.s;
+  const Smem m = carve(smem, s, true);
+  const int tid = threadIdx.x, l = tid & 31;
+  const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
+  const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
+  const uint32_t stride = 16u * s.threads;
+  Owner o;
+  set_lane(o, s);
+  const int og = o.c / s.cg, orr = o.c - og * s.cg;
+  const int64_t all = a.N * s.slabs;
+  for (int64_t u0 = 0; u0 < all; u0 += s.units) {
+    const int nu = static_cast<int>(min(static_cast<int64_t>(s.units), all - u0));
+    const int pieces = nu * s.chunks;
+    auto place = [&] { return (o.n * a.S + o.r0 + o.lane) * a.C + o.slab * s.cs + o.c; };
+    auto ring_of = [&] {  // piece o's
+      const T* p = static_cast<const T*>(a.x) + o.n * a.s_n + (o.r0 + o.lane) * a.s_s +
+                   o.slab * s.cs + o.c;
+      return Ring<2>{smem_u32(smem) + 16u * tid, stride,
+                     {reinterpret_cast<const unsigned char*>(p),
+                      reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.dy) + place())},
+                     {step * static_cast<int64_t>(sizeof(T)),
+                      dstep * static_cast<int64_t>(sizeof(T))}, o.cnt};
+    };
+    Ring<2> ring{};
+    Consts<T> q;
+    for (int v = blockIdx.x; v < pieces; v += gridDim.x) {
+      set_piece(o, a, u0, nu, v);
+      ring = ring_of();
+      ring.start();
+      load_params(a, m.w, m.b, o.slab);
+      __syncthreads();
+      const float* const rstd = a.rstd + o.n * a.G + o.slab * s.gs;
+      if (o.cnt > 0)
+        q.load(m.w, m.b, a.mean + o.n * a.G + o.slab * s.gs, rstd, s.cg, o.c, og, orr);
+      ColumnSums<T, kAct> sum;
+      sum.clear();
+      ring.run(o.cnt, [&](uint32_t slot) {
+        sum.add(q, lds128_at(slot), lds128_at(slot + kRingSlots * stride));
+      });
+      __syncthreads();  // red takes the rings' place
+      float* cols = a.cols + (o.n * s.chunks + o.chunk) * 2 * a.C + o.slab * s.cs;
+      cta_sums(m, s, o, sum, rstd,
+               [&](int half, int c, float val) { cols[half * a.C + c] = val; });
+      __syncthreads();
+      float2* part = a.part + (o.n * s.chunks + o.chunk) * a.G + o.slab * s.gs;
+      for (int g = tid; g < s.gs; g += s.threads)
+        part[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
+    }
+    // the last piece summed is the first written: o is still its owner, q its constants
+    int v = blockIdx.x < pieces
+                ? blockIdx.x + (pieces - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) *
+                                   static_cast<int>(gridDim.x)
+                : -1;
+    if (v >= 0) {
+      ring = ring_of();
+      ring.start();
+    }
+    cooperative_groups::this_grid().sync();
+    for (; v >= 0; v -= gridDim.x) {
+      if (v + static_cast<int>(gridDim.x) < pieces) {  // not the one whose copies have started
+        set_piece(o, a, u0, nu, v);
+        ring = ring_of();
+        ring.start();
+        __syncthreads();  // the piece before is done with w, b, c0, c1
+        load_params(a, m.w, m.b, o.slab);
+        __syncthreads();
+        if (o.cnt > 0)
+          q.load(m.w, m.b, a.mean + o.n * a.G + o.slab * s.gs, a.rstd + o.n * a.G + o.slab * s.gs,
+                 s.cg, o.c, og, orr);
+      }
+      for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
+        const float2* p = a.part + o.n * s.chunks * a.G + o.slab * s.gs + g;
+        float sa = 0.f, sb = 0.f;
+#pragma unroll 4
+        for (int k = l; k < s.chunks; k += 32) {  // not through L1 (gn_fwd.cu)
+          const float2 x = __ldcg(p + static_cast<int64_t>(k) * a.G);
+          sa += x.x;
+          sb += x.y;
+        }
+        sa = warp_allsum(sa);
+        sb = warp_allsum(sb);
+        set_group(m, s, g, l, 32, a.rstd[o.n * a.G + o.slab * s.gs + g], sa, sb, total);
+      }
       __syncthreads();
       if (o.cnt > 0) {
         GroupTerms<T> t;
         t.load(m.c0, m.c1, o.c);
-        T* po = static_cast<T*>(a.out) + n * a.S * a.C + at0;
-        for_staged2(mine, dy_off, 0, o.cnt, stride, [&](const uint4& xu, const uint4& du) {
-          stg128(po, dx_vec<T, kAct>(q, t, xu, du));
+        T* po = static_cast<T*>(a.out) + place();
+        ring.run(o.cnt, [&](uint32_t slot) {  // dx is not read here again: it leaves L2 first
+          __stcs(reinterpret_cast<uint4*>(po),
+                 dx_vec<T, kAct>(q, t, lds128_at(slot), lds128_at(slot + kRingSlots * stride)));
           po += dstep;
         });
       }
-      if (s.stages == 1) {
-        for (int b = 0; b < kBatches; ++b)
-          stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
-      } else if (++k == s.stages) {
-        k = 0;
-      }
     }
-    if (s.ctas > 1) cluster_wait();
+    __syncthreads();  // the next turn's sums reuse the shared memory
   }
-  if constexpr (kOnChip) {  // this CTA's totals over its samples
-    __syncthreads();
-    float* out = a.cols + (o.n * s.ctas + o.rank) * 2 * a.C +
-                 o.slab * s.cs;
-    for (int t = tid; t < 2 * s.cs; t += s.threads)
-      out[t < s.cs ? t : a.C + t - s.cs] = m.run[2 * t];
-  }
-}
-
-// The second launch: the chunks' group sums add up (an octet of threads a group, a fixed order),
-// and dx is formed from x and dy, read again backwards.  As in the forward, the first copies do
-// not wait for the sums.
-template <typename T, int kAct, bool kWide>
-__global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
-    gn_bwd_out_kernel(const GnArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  const GnShape& s = a.s;
-  const int tid = threadIdx.x;
-  const Owner o = out_owner(a);
-  const int64_t n = o.n;
-  const int ch = o.slab * s.cs + o.c, group0 = o.slab * s.gs;
-  const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
-  const int64_t at = (n * a.S + o.r0 + o.lane) * a.C + ch;
-  const T* px = static_cast<const T*>(a.x) + n * a.s_n + (o.r0 + o.lane) * a.s_s + ch;
-  const uint32_t stride = 16u * s.threads;
-  Ring<2> ring{smem_u32(smem) + 16u * tid, stride,
-               {reinterpret_cast<const unsigned char*>(px),
-                reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.dy) + at)},
-               {step * static_cast<int64_t>(sizeof(T)), dstep * static_cast<int64_t>(sizeof(T))},
-               o.cnt};
-  ring.start();
-  float* w = reinterpret_cast<float*>(smem + gn_stage_bytes(s, true));
-  float* b = w + s.cs;
-  float* c0 = b + s.cs;
-  float* c1 = c0 + s.cs;
-  load_params(a, w, b, o.slab);
-  const float* const mean = a.mean + n * a.G + group0;
-  const float* const rstd = a.rstd + n * a.G + group0;
-
-  pdl_wait_prior_grid();
-  pdl_allow_next_grid();
-
-  const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
-  const int l8 = tid & 7;
-  for (int g0 = 4 * (tid >> 5); g0 < s.gs; g0 += s.threads >> 3) {
-    const int g = g0 + ((tid & 31) >> 3);
-    const float2* p = a.part + n * s.chunks * a.G + group0 + g;
-    const int chunks = g < s.gs ? s.chunks : 0;
-    float sa = 0.f, sb = 0.f;
-#pragma unroll 4
-    for (int q = l8; q < chunks; q += 8) {
-      const float2 v = p[static_cast<int64_t>(q) * a.G];
-      sa += v.x;
-      sb += v.y;
-    }
-    sa = octet_sum(sa);
-    sb = octet_sum(sb);
-    if (g < s.gs) {
-      const float r = rstd[g];
-      const float nc1 = -r * (sb / total), nc2 = -r * r * (sa / total);
-      for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
-        c0[i] = nc1;
-        c1[i] = nc2;
-      }
-    }
-  }
-  __syncthreads();
-  if (o.cnt == 0) return;
-
-  Consts<T> k;
-  const int og = o.c / s.cg;
-  k.load(w, b, mean, rstd, s.cg, o.c, og, o.c - og * s.cg);
-  GroupTerms<T> t;
-  t.load(c0, c1, o.c);
-  T* po = static_cast<T*>(a.out) + at;
-  ring.run(o.cnt, [&](uint32_t slot) {  // dx is not read here again: it leaves L2 first
-    __stcs(reinterpret_cast<uint4*>(po),
-           dx_vec<T, kAct>(k, t, lds128_at(slot), lds128_at(slot + kRingSlots * stride)));
-    po += dstep;
-  });
 }
 
 constexpr int kFinishCols = 32, kFinishSlices = 32;
@@ -436,29 +448,20 @@ __global__ void __launch_bounds__(kFinishCols* kFinishSlices)
 namespace {
 
 // The kernel builds for a dtype T, activation and width.
-template <typename T, bool kOnChip, bool kWide>
-const void* pick_sums(int act) {
+template <typename T, bool kWide>
+const void* pick_act(const GnShape& s, int act) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_NONE, kOnChip, kWide>)
-         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_SILU, kOnChip, kWide>)
-                                     : fn(&gn_bwd_kernel<T, GROUPNORM_ACT_GELU, kOnChip, kWide>);
+  if (s.on_chip)
+    return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_NONE, kWide>)
+           : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_kernel<T, GROUPNORM_ACT_SILU, kWide>)
+                                       : fn(&gn_bwd_kernel<T, GROUPNORM_ACT_GELU, kWide>);
+  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_stream_kernel<T, GROUPNORM_ACT_NONE, kWide>)
+         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_stream_kernel<T, GROUPNORM_ACT_SILU, kWide>)
+                                     : fn(&gn_bwd_stream_kernel<T, GROUPNORM_ACT_GELU, kWide>);
 }
 template <typename T>
 const void* pick_bwd(const GnShape& s, int act) {
-  if (s.vecs > kThreads)
-    return s.on_chip ? pick_sums<T, true, true>(act) : pick_sums<T, false, true>(act);
-  return s.on_chip ? pick_sums<T, true, false>(act) : pick_sums<T, false, false>(act);
-}
-template <typename T, bool kWide>
-const void* pick_act(int act) {
-  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  return act == GROUPNORM_ACT_NONE   ? fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_NONE, kWide>)
-         : act == GROUPNORM_ACT_SILU ? fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_SILU, kWide>)
-                                     : fn(&gn_bwd_out_kernel<T, GROUPNORM_ACT_GELU, kWide>);
-}
-template <typename T>
-const void* pick_out(const GnShape& s, int act) {
-  return s.vecs > kThreads ? pick_act<T, true>(act) : pick_act<T, false>(act);
+  return s.vecs > kThreads ? pick_act<T, true>(s, act) : pick_act<T, false>(s, act);
 }
 
 }  // namespace
@@ -467,14 +470,7 @@ cudaError_t launch_gn_bwd(const GnArgs& a, int dtype, int act, cudaStream_t st) 
   const void* fn = dtype == GROUPNORM_BF16   ? pick_bwd<__nv_bfloat16>(a.s, act)
                    : dtype == GROUPNORM_FP32 ? pick_bwd<float>(a.s, act)
                                              : pick_bwd<__half>(a.s, act);
-  return launch_cluster(fn, gn_stats_ctas(a.s, a.nu), a.s, a, st);
-}
-
-cudaError_t launch_gn_bwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st) {
-  const void* fn = dtype == GROUPNORM_BF16   ? pick_out<__nv_bfloat16>(a.s, act)
-                   : dtype == GROUPNORM_FP32 ? pick_out<float>(a.s, act)
-                                             : pick_out<__half>(a.s, act);
-  return launch_out(fn, a, true, st);
+  return launch_gn(fn, a, st);
 }
 
 cudaError_t launch_gn_finish(const float* cols, float* dw, float* db, int64_t rows, int C,

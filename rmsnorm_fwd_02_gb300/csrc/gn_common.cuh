@@ -2,7 +2,7 @@
 // and the sums over a CTA and a cluster.
 #pragma once
 
-#include <type_traits>
+#include <cooperative_groups.h>
 
 #include "gn_launch.h"
 #include "groupnorm_train.h"
@@ -252,52 +252,34 @@ __device__ __forceinline__ void set_lane(Owner& o, const GnShape& s) {
 __device__ __forceinline__ void set_count(Owner& o, const GnShape& s) {
   o.cnt = o.lane < s.lanes && o.lane < o.rows ? (o.rows - o.lane + s.lanes - 1) / s.lanes : 0;
 }
-// Unit `local` of a launch: neighbouring CTAs take neighbouring slabs of the same places.
-__device__ __forceinline__ void set_unit(Owner& o, const GnArgs& a, int local) {
-  const int64_t u = a.u0 + local;
-  o.n = u / a.s.slabs;
-  o.slab = static_cast<int>(u - o.n * a.s.slabs);
-}
-template <bool kOnChip>
-__device__ __forceinline__ Owner owner(const GnArgs& a) {
+__device__ __forceinline__ Owner on_chip_owner(const GnArgs& a) {
   const GnShape& s = a.s;
   Owner o;
   set_lane(o, s);
   o.rank = s.ctas > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
-  const int cluster = blockIdx.x >> s.ctas_log2;
-  if constexpr (kOnChip) {
-    const int first = cluster / s.slabs;
-    o.n = first;
-    o.slab = cluster - first * s.slabs;
-    o.chunk = 0;
-    o.len = static_cast<int>(a.S);
-    o.r0 = 0;
-  } else {
-    o.chunk = cluster / a.nu;
-    set_unit(o, a, cluster - o.chunk * a.nu);
-    o.len = s.chunk_base + (o.chunk < s.chunk_more ? 1 : 0);
-    o.r0 = static_cast<int64_t>(o.chunk) * s.chunk_base + min(o.chunk, s.chunk_more);
-  }
+  const int cluster = blockIdx.x >> s.ctas_log2, first = cluster / s.slabs;
+  o.n = first;
+  o.slab = cluster - first * s.slabs;
+  o.chunk = 0;
+  o.len = static_cast<int>(a.S);
   const int start = rank_start(o.len, o.rank, s);
-  o.r0 += start;
+  o.r0 = start;
   o.rows = rank_start(o.len, o.rank + 1, s) - start;
   set_count(o, s);
   return o;
 }
-
-// The second launch's kernels (no cluster), backwards through the places.
-__device__ __forceinline__ Owner out_owner(const GnArgs& a) {
+// Piece v of a turn that starts at unit u0 and takes nu: neighbouring pieces are neighbouring
+// slabs of the same places.
+__device__ __forceinline__ void set_piece(Owner& o, const GnArgs& a, int64_t u0, int nu, int v) {
   const GnShape& s = a.s;
-  Owner o;
-  set_lane(o, s);
   o.rank = 0;
-  const int i = gridDim.x - 1 - blockIdx.x;
-  o.chunk = i / a.nu;
-  set_unit(o, a, i - o.chunk * a.nu);
-  o.len = o.rows = s.part_base + (o.chunk < s.part_more ? 1 : 0);
-  o.r0 = static_cast<int64_t>(o.chunk) * s.part_base + min(o.chunk, s.part_more);
+  o.chunk = v / nu;
+  const int64_t u = u0 + (v - o.chunk * nu);
+  o.n = u / s.slabs;
+  o.slab = static_cast<int>(u - o.n * s.slabs);
+  o.len = o.rows = s.chunk_base + (o.chunk < s.chunk_more ? 1 : 0);
+  o.r0 = static_cast<int64_t>(o.chunk) * s.chunk_base + min(o.chunk, s.chunk_more);
   set_count(o, s);
-  return o;
 }
 
 // A thread's own copies through its ring: kTensors 16-byte vectors a place (tensor t's slots

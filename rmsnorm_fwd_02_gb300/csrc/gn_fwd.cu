@@ -2,17 +2,18 @@
 // (include/groupnorm_train.h gives the formulas).
 //
 // HBM-bound: one read and one write of the activation.  Where a cluster's shared memory holds
-// a sample's slab (gn_launch.h), one launch reads it once: asynchronous 16-byte copies stage
-// each thread's own vectors (the next samples' on their way meanwhile), the cluster's CTAs
-// exchange a few floats a group, and the staged vectors are normalized and written.  Larger
-// samples take two launches, the second reading x again -- from L2, which holds the slabs of one
-// pair of launches.
+// a sample's slab (gn_launch.h), x is read once: asynchronous 16-byte copies stage each
+// thread's own vectors (the next samples' on their way meanwhile), the cluster's CTAs exchange
+// a few floats a group, and the staged vectors are normalized and written.  Larger samples are
+// streamed: a cooperative grid takes as many of their slabs at a time as L2 holds, sums them,
+// meets at a barrier, and reads x again from L2 for the output.  (Two launches instead, with
+// their ramps, cost 5 us each more.)
 //
 // Statistics: each thread sums its channels' values less the first of them, K (sum d and
 // sum d^2 of d = x - K), so neither sum cancels when the mean is far from zero; a column's
 // mean is K + sum d / n and its M2 = sum d^2 - (sum d)^2 / n.  Means combine weighted by their
 // counts, and M2 about the combined mean: M2 = sum of M2_i + n_i (mean_i - mean)^2 -- from
-// threads to columns, groups, the cluster and (two launches) the sample.
+// threads to columns, groups, the cluster or the chunks.
 #include "gn_common.cuh"
 
 namespace gnorm {
@@ -68,6 +69,15 @@ struct Consts {
     return VecOf<T>::pack(z);
   }
 };
+
+// Channel constants of group g of the slab, lane k of `lanes` threads.
+__device__ __forceinline__ void set_group(const Smem& m, const GnShape& s, int g, int k, int lanes,
+                                          float mean, float rstd) {
+  for (int i = g * s.cg + k; i < (g + 1) * s.cg; i += lanes) {
+    m.c0[i] = -mean;
+    m.c1[i] = rstd * m.w[i];
+  }
+}
 
 // The CTA's group values (mean, M2) to m.gm from its threads' statistics: columns over the
 // lanes, then groups over their columns (an octet of threads a group).  A warp takes eight
@@ -154,28 +164,29 @@ __device__ __forceinline__ void cta_stats(const Smem& m, const GnShape& s, const
   }
 }
 
-template <typename T, int kAct, bool kOnChip, bool kWide>
+template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     gn_fwd_kernel(const GnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const Smem m = carve(smem, s, false);
-  const Owner o = owner<kOnChip>(a);
+  const Owner o = on_chip_owner(a);
   const int tid = threadIdx.x;
   const int ch = o.slab * s.cs + o.c;
   const int64_t step = s.lanes * a.s_s;
   const T* const px = static_cast<const T*>(a.x) + (o.r0 + o.lane) * a.s_s + ch;
   const float total = static_cast<float>(o.len) * static_cast<float>(s.cg);
   const int l8 = tid & 7;
-  // places and values a group of cluster rank l8
+  // values a group of cluster rank l8
   const float nk = l8 < s.ctas ? static_cast<float>(rank_start(o.len, l8 + 1, s) -
                                                     rank_start(o.len, l8, s)) *
                                      static_cast<float>(s.cg)
                                : 0.f;
 
-  if (kOnChip || !a.early) pdl_wait_prior_grid();
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
 
-  // on chip: this thread's slot of place i of stage k is stage + (k * iters + i) * stride
+  // this thread's slot of place i of stage k is stage + (k * iters + i) * stride
   const uint32_t stride = 16u * s.threads, stage = smem_u32(smem) + 16u * tid;
   auto stage_places = [&](int64_t n, int k, int from, int to) {
     if (n < a.N) {
@@ -188,46 +199,28 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   constexpr int kBatches = 4;  // of a single-stage sample
   const int per = (s.iters + kBatches - 1) / kBatches;
   int64_t n = o.n;
-  Ring<1> ring{stage, stride, {reinterpret_cast<const unsigned char*>(px + n * a.s_n)},
-               {step * static_cast<int64_t>(sizeof(T))}, o.cnt};
-  if constexpr (!kOnChip) {
-    ring.start();
-    if (a.early) pdl_wait_prior_grid();
-  }
-  pdl_allow_next_grid();
-  if constexpr (kOnChip) {
-    if (s.stages == 1)
-      for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
-    for (int k = 0; k + 1 < s.stages; ++k) stage_places(n + k * s.lanes_n, k, 0, s.iters);
-    load_params(a, m.w, m.b, o.slab);
-  }
+  if (s.stages == 1)
+    for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
+  for (int k = 0; k + 1 < s.stages; ++k) stage_places(n + k * s.lanes_n, k, 0, s.iters);
+  load_params(a, m.w, m.b, o.slab);
 
-  for (int k = 0; n < a.N; n += kOnChip ? s.lanes_n : a.N) {
+  for (int k = 0; n < a.N; n += s.lanes_n) {
     ColumnStats<T> st;
     const uint32_t mine = stage + k * s.iters * stride;
-    if constexpr (kOnChip) {
-      if (s.stages == 1) {  // the sums follow the copies, batch by batch
-        for (int b = 0; b < kBatches; ++b) {
-          cp_async_wait(kBatches - 1 - b);
-          if (b == 0 && o.cnt > 0) st.start(lds128_at(mine));
-          for_staged(mine, b * per, min(o.cnt, (b + 1) * per), stride,
-                     [&](const uint4& u) { st.add(u); });
-        }
-      } else {
-        const int ahead = s.stages - 1;
-        stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
-                     0, s.iters);
-        cp_async_wait(ahead);
-        if (o.cnt > 0) st.start(lds128_at(mine));
-        for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) { st.add(u); });
+    if (s.stages == 1) {  // the sums follow the copies, batch by batch
+      for (int b = 0; b < kBatches; ++b) {
+        cp_async_wait(kBatches - 1 - b);
+        if (b == 0 && o.cnt > 0) st.start(lds128_at(mine));
+        for_staged(mine, b * per, min(o.cnt, (b + 1) * per), stride,
+                   [&](const uint4& u) { st.add(u); });
       }
     } else {
-      if (o.cnt > 0) {
-        cp_async_wait(kRingGroups - 2);
-        st.start(lds128_at(stage));
-      }
-      ring.run(o.cnt, [&](uint32_t slot) { st.add(lds128_at(slot)); });
-      __syncthreads();  // red takes the rings' place
+      const int ahead = s.stages - 1;
+      stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
+                   0, s.iters);
+      cp_async_wait(ahead);
+      if (o.cnt > 0) st.start(lds128_at(mine));
+      for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) { st.add(u); });
     }
     cta_stats(m, s, o, st);
 
@@ -247,153 +240,157 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       const float mean = octet_sum(nk * v.x) / total;
       const float d = nk > 0.f ? v.x - mean : 0.f;
       const float m2 = octet_sum(__fmaf_rn(d * d, nk, v.y));
-      if constexpr (kOnChip) {
-        const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
-        if (g < s.gs) {
-          for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
-            m.c0[i] = -mean;
-            m.c1[i] = rstd * m.w[i];
-          }
-          if (l8 == 0 && o.rank == 0) {
-            a.mean[n * a.G + o.slab * s.gs + g] = mean;
-            a.rstd[n * a.G + o.slab * s.gs + g] = rstd;
-          }
+      const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
+      if (g < s.gs) {
+        set_group(m, s, g, l8, 8, mean, rstd);
+        if (l8 == 0 && o.rank == 0) {
+          a.mean[n * a.G + o.slab * s.gs + g] = mean;
+          a.rstd[n * a.G + o.slab * s.gs + g] = rstd;
         }
-      } else if (l8 == 0 && g < s.gs && o.rank == 0) {
-        a.part[(n * s.chunks + o.chunk) * a.G + o.slab * s.gs + g] = make_float2(mean, m2);
       }
     }
     if (s.ctas > 1) cluster_arrive();  // this CTA's reads of the others are done
-    if constexpr (kOnChip) {
-      __syncthreads();
-      if (o.cnt > 0) {
-        Consts<T> q;
-        q.load(m.c0, m.c1, m.b, o.c);
-        T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
-        const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
-        for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) {
-          stg128(py, q.template norm<kAct>(u));
-          py += ystep;
-        });
-      }
-      if (s.stages == 1) {
-        for (int b = 0; b < kBatches; ++b)
-          stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
-      } else if (++k == s.stages) {
-        k = 0;
-      }
+    __syncthreads();
+    if (o.cnt > 0) {
+      Consts<T> q;
+      q.load(m.c0, m.c1, m.b, o.c);
+      T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
+      const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
+      for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) {
+        stg128(py, q.template norm<kAct>(u));
+        py += ystep;
+      });
+    }
+    if (s.stages == 1) {
+      for (int b = 0; b < kBatches; ++b) stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
+    } else if (++k == s.stages) {
+      k = 0;
     }
     if (s.ctas > 1) cluster_wait();
   }
 }
 
-// The second launch: the chunks' statistics combine into the sample's (an octet of threads
-// takes a group's chunks), and the CTA's places are read again, normalized and written.  CTAs
-// run through the places backwards, so that the last ones the statistics read come first, while
-// L2 still holds them; their first copies are on their way before the statistics are waited
-// for (x is no output of that launch, which itself waited for whatever wrote x).
+// Streamed.  Each turn's pieces (a unit's chunk each) are dealt out to the grid; a CTA sums its
+// own, and after the barrier combines the chunks' statistics of its unit (a warp a group, the
+// chunks over its lanes) and writes its own pieces' output, its first copies already on their
+// way.  Turns follow each other without a second barrier: every unit has its own place in part.
 template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
-    gn_fwd_out_kernel(const GnArgs a) {
+    gn_fwd_stream_kernel(const GnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
-  const int tid = threadIdx.x;
-  const Owner o = out_owner(a);
-  const int64_t n = o.n;
-  const int ch = o.slab * s.cs + o.c;
-  const int64_t step = s.lanes * a.s_s;
-  const T* px = static_cast<const T*>(a.x) + n * a.s_n + (o.r0 + o.lane) * a.s_s + ch;
-  Ring<1> ring{smem_u32(smem) + 16u * tid, 16u * s.threads,
-               {reinterpret_cast<const unsigned char*>(px)},
-               {step * static_cast<int64_t>(sizeof(T))}, o.cnt};
-  ring.start();
-  float* w = reinterpret_cast<float*>(smem + gn_stage_bytes(s, false));
-  float* b = w + s.cs;
-  float* c0 = b + s.cs;
-  float* c1 = c0 + s.cs;
-  load_params(a, w, b, o.slab);
-  __syncthreads();
-
-  pdl_wait_prior_grid();
-  pdl_allow_next_grid();
-
+  const Smem m = carve(smem, s, false);
+  const int tid = threadIdx.x, l = tid & 31;
+  const int64_t step = s.lanes * a.s_s, ystep = static_cast<int64_t>(s.lanes) * a.C;
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
   const float cg = static_cast<float>(s.cg);
-  const int l8 = tid & 7;
-  for (int g0 = 4 * (tid >> 5); g0 < s.gs; g0 += s.threads >> 3) {
-    const int g = g0 + ((tid & 31) >> 3);
-    const float2* p = a.part + n * s.chunks * a.G + o.slab * s.gs + g;
-    // about the first chunk's mean, as in cta_stats
-    const int chunks = g < s.gs ? s.chunks : 0;
-    const float ref = g < s.gs ? p[0].x : 0.f;
-    float sum = 0.f, m2 = 0.f;
+  Owner o;
+  set_lane(o, s);
+  const int64_t all = a.N * s.slabs;
+  for (int64_t u0 = 0; u0 < all; u0 += s.units) {
+    const int nu = static_cast<int>(min(static_cast<int64_t>(s.units), all - u0));
+    const int pieces = nu * s.chunks;
+    auto ring_of = [&] {  // piece o's
+      const T* p = static_cast<const T*>(a.x) + o.n * a.s_n + (o.r0 + o.lane) * a.s_s +
+                   o.slab * s.cs + o.c;
+      return Ring<1>{smem_u32(smem) + 16u * tid, 16u * s.threads,
+                     {reinterpret_cast<const unsigned char*>(p)},
+                     {step * static_cast<int64_t>(sizeof(T))}, o.cnt};
+    };
+    Ring<1> ring{};
+    for (int v = blockIdx.x; v < pieces; v += gridDim.x) {
+      set_piece(o, a, u0, nu, v);
+      ring = ring_of();
+      ring.start();
+      ColumnStats<T> st;
+      if (o.cnt > 0) {
+        cp_async_wait(kRingGroups - 2);
+        st.start(lds128_at(ring.slot));
+      }
+      ring.run(o.cnt, [&](uint32_t slot) { st.add(lds128_at(slot)); });
+      __syncthreads();  // red takes the rings' place
+      cta_stats(m, s, o, st);
+      __syncthreads();
+      float2* part = a.part + (o.n * s.chunks + o.chunk) * a.G + o.slab * s.gs;
+      for (int g = tid; g < s.gs; g += s.threads)
+        part[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
+    }
+    // the last piece summed is the first written: o is still its owner
+    int v = blockIdx.x < pieces
+                ? blockIdx.x + (pieces - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) *
+                                   static_cast<int>(gridDim.x)
+                : -1;
+    if (v >= 0) {
+      ring = ring_of();
+      ring.start();
+    }
+    cooperative_groups::this_grid().sync();
+    for (; v >= 0; v -= gridDim.x) {
+      if (v + static_cast<int>(gridDim.x) < pieces) {  // not the one whose copies have started
+        set_piece(o, a, u0, nu, v);
+        ring = ring_of();
+        ring.start();
+      }
+      __syncthreads();  // the piece before is done with w, b, c0, c1
+      load_params(a, m.w, m.b, o.slab);
+      __syncthreads();
+      for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
+        const float2* p = a.part + o.n * s.chunks * a.G + o.slab * s.gs + g;
+        // about the first chunk's mean, as in cta_stats; not through L1, which may hold an
+        // earlier turn's line
+        const float ref = __ldcg(p).x;
+        float sum = 0.f, m2 = 0.f;
 #pragma unroll 4
-    for (int k = l8; k < chunks; k += 8) {
-      const float2 v = p[static_cast<int64_t>(k) * a.G];
-      const float d = v.x - ref;
-      const float nd = static_cast<float>(s.chunk_base + (k < s.chunk_more ? 1 : 0)) * cg * d;
-      sum += nd;
-      m2 += __fmaf_rn(nd, d, v.y);
-    }
-    sum = octet_sum(sum);
-    m2 = octet_sum(m2);
-    const float off = sum / total, mean = ref + off;
-    m2 = __fmaf_rn(-off, sum, m2);
-    if (g < s.gs) {
-      const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
-      for (int i = g * s.cg + l8; i < (g + 1) * s.cg; i += 8) {
-        c0[i] = -mean;
-        c1[i] = rstd * w[i];
+        for (int k = l; k < s.chunks; k += 32) {
+          const float2 x = __ldcg(p + static_cast<int64_t>(k) * a.G);
+          const float d = x.x - ref;
+          const float nd = static_cast<float>(s.chunk_base + (k < s.chunk_more ? 1 : 0)) * cg * d;
+          sum += nd;
+          m2 += __fmaf_rn(nd, d, x.y);
+        }
+        sum = warp_allsum(sum);
+        m2 = warp_allsum(m2);
+        const float off = sum / total, mean = ref + off;
+        m2 = __fmaf_rn(-off, sum, m2);
+        const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
+        set_group(m, s, g, l, 32, mean, rstd);
+        if (l == 0 && o.chunk == 0) {
+          a.mean[o.n * a.G + o.slab * s.gs + g] = mean;
+          a.rstd[o.n * a.G + o.slab * s.gs + g] = rstd;
+        }
       }
-      if (l8 == 0 && o.chunk == 0) {
-        a.mean[n * a.G + o.slab * s.gs + g] = mean;
-        a.rstd[n * a.G + o.slab * s.gs + g] = rstd;
+      __syncthreads();
+      if (o.cnt > 0) {
+        Consts<T> q;
+        q.load(m.c0, m.c1, m.b, o.c);
+        T* py = static_cast<T*>(a.out) + (o.n * a.S + o.r0 + o.lane) * a.C + o.slab * s.cs + o.c;
+        ring.run(o.cnt, [&](uint32_t slot) {  // y is not read here again: it leaves L2 first
+          __stcs(reinterpret_cast<uint4*>(py), q.template norm<kAct>(lds128_at(slot)));
+          py += ystep;
+        });
       }
     }
+    __syncthreads();  // the next turn's sums reuse the shared memory
   }
-  __syncthreads();
-  if (o.cnt == 0) return;
-
-  Consts<T> q;
-  q.load(c0, c1, b, o.c);
-  T* py = static_cast<T*>(a.out) + (n * a.S + o.r0 + o.lane) * a.C + ch;
-  const int64_t ystep = static_cast<int64_t>(s.lanes) * a.C;
-  ring.run(o.cnt, [&](uint32_t slot) {  // y is not read here again: it leaves L2 first
-    __stcs(reinterpret_cast<uint4*>(py), q.template norm<kAct>(lds128_at(slot)));
-    py += ystep;
-  });
 }
 
 namespace {
 
 // The kernel builds for a dtype T, activation and width.
-template <typename T, bool kOnChip, bool kWide>
-const void* pick_stats(int act) {
+template <typename T, bool kWide>
+const void* pick_act(const GnShape& s, int act) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  if constexpr (!kOnChip) {
-    return fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, false, kWide>);  // statistics only
-  } else {
-    return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, true, kWide>)
-           : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_SILU, true, kWide>)
-                                       : fn(&gn_fwd_kernel<T, GROUPNORM_ACT_GELU, true, kWide>);
-  }
+  if (s.on_chip)
+    return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_NONE, kWide>)
+           : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_kernel<T, GROUPNORM_ACT_SILU, kWide>)
+                                       : fn(&gn_fwd_kernel<T, GROUPNORM_ACT_GELU, kWide>);
+  return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_stream_kernel<T, GROUPNORM_ACT_NONE, kWide>)
+         : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_stream_kernel<T, GROUPNORM_ACT_SILU, kWide>)
+                                     : fn(&gn_fwd_stream_kernel<T, GROUPNORM_ACT_GELU, kWide>);
 }
 template <typename T>
 const void* pick_fwd(const GnShape& s, int act) {
-  if (s.vecs > kThreads)
-    return s.on_chip ? pick_stats<T, true, true>(act) : pick_stats<T, false, true>(act);
-  return s.on_chip ? pick_stats<T, true, false>(act) : pick_stats<T, false, false>(act);
-}
-template <typename T, bool kWide>
-const void* pick_act(int act) {
-  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  return act == GROUPNORM_ACT_NONE   ? fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_NONE, kWide>)
-         : act == GROUPNORM_ACT_SILU ? fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_SILU, kWide>)
-                                     : fn(&gn_fwd_out_kernel<T, GROUPNORM_ACT_GELU, kWide>);
-}
-template <typename T>
-const void* pick_out(const GnShape& s, int act) {
-  return s.vecs > kThreads ? pick_act<T, true>(act) : pick_act<T, false>(act);
+  return s.vecs > kThreads ? pick_act<T, true>(s, act) : pick_act<T, false>(s, act);
 }
 
 }  // namespace
@@ -402,14 +399,7 @@ cudaError_t launch_gn_fwd(const GnArgs& a, int dtype, int act, cudaStream_t st) 
   const void* fn = dtype == GROUPNORM_BF16   ? pick_fwd<__nv_bfloat16>(a.s, act)
                    : dtype == GROUPNORM_FP32 ? pick_fwd<float>(a.s, act)
                                              : pick_fwd<__half>(a.s, act);
-  return launch_cluster(fn, gn_stats_ctas(a.s, a.nu), a.s, a, st);
-}
-
-cudaError_t launch_gn_fwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st) {
-  const void* fn = dtype == GROUPNORM_BF16   ? pick_out<__nv_bfloat16>(a.s, act)
-                   : dtype == GROUPNORM_FP32 ? pick_out<float>(a.s, act)
-                                             : pick_out<__half>(a.s, act);
-  return launch_out(fn, a, false, st);
+  return launch_gn(fn, a, st);
 }
 
 }  // namespace gnorm

@@ -8,8 +8,12 @@ namespace gnorm {
 
 // A CTA owns a slab -- whole groups whose channels make whole 16-byte vectors -- of some
 // consecutive places of one sample.  Its threads form `lanes` rows of `vecs` threads; thread
-// (lane, vec) owns 16-byte vector vec of places lane, lane + lanes, ...  `ctas` CTAs of a
-// cluster split a sample's (or a chunk's) places between them.
+// (lane, vec) owns 16-byte vector vec of places lane, lane + lanes, ...
+// Two forms, one launch each:
+//  on chip   `ctas` CTAs of a cluster split a sample's places and keep the slab in shared memory
+//            between the statistics and the output
+//  streamed  a cooperative grid takes units -- slabs of samples -- in turns of as many as L2
+//            holds, each split into `chunks` of places: statistics, a barrier of the grid, output
 struct GnShape {
   int ev;        // elements a 16-byte vector
   int cg;        // channels a group
@@ -19,19 +23,19 @@ struct GnShape {
   int slabs;     // slabs a sample
   int lanes;     // rows of threads
   int threads;   // lanes * vecs, up to whole warps
+  int on_chip;
+  // on chip
   int ctas;      // CTAs a cluster, 1 << ctas_log2
   int ctas_log2;
   int iters;     // most places a thread takes
-  int on_chip;   // the slab stays in shared memory between statistics and output
-  int lanes_n;   // on chip: clusters a slab (each takes samples lane, lane + lanes_n, ...)
-  int stages;    // on chip: samples a cluster has staged or on their way
-  int chunks;    // two launches: chunks of places a sample's statistics are split into: the
-                 // first chunk_more of chunk_base + 1 places, the others of chunk_base
+  int lanes_n;   // clusters a slab (each takes samples lane, lane + lanes_n, ...)
+  int stages;    // samples a cluster has staged or on their way
+  // streamed
+  int units;     // units a turn takes, unit u the slab u % slabs of sample u / slabs
+  int chunks;    // the first chunk_more of chunk_base + 1 places, the others of chunk_base
   int chunk_base, chunk_more;
-  int units;     // two launches: units (slabs of samples) a pair of launches takes
-  int parts;     // two launches: chunks of places of the second launch, alike
-  int part_base, part_more;
-  size_t smem;   // dynamic shared memory of the (first) launch
+  int grid;      // CTAs at most
+  size_t smem;   // dynamic shared memory
 };
 
 struct GnArgs {
@@ -42,15 +46,10 @@ struct GnArgs {
   void* out;             // y, or dx
   float* mean;           // [N, G]; backward: read
   float* rstd;
-  float2* part;          // two launches: [N][chunks][G]: (mean, M2), or (sum g*xhat, sum g)
+  float2* part;          // streamed: [N][chunks][G]: (mean, M2), or (sum g*xhat, sum g)
   float* cols;           // backward: [.][2][C] column sums (dw, then db)
   int64_t s_n, s_s;      // x's strides
   int64_t N;
-  // two launches: units [u0, u0 + nu) of the N * slabs, unit u the slab u % slabs of sample
-  // u / slabs; `early`: x was complete before the launch before this one began
-  int64_t u0;
-  int32_t nu;
-  int32_t early;
   int64_t S;
   int32_t C, G;
   int32_t wb_dtype;
@@ -68,7 +67,7 @@ constexpr int kMaxCluster = 8;
 constexpr int max_threads(bool wide) { return wide ? kWideThreads : kThreads; }
 constexpr int min_ctas(bool wide) { return wide ? 1 : kCtas; }
 
-// Two launches: each thread's copies run through a ring of kRingGroups groups of kRingPlaces
+// Streamed: each thread's copies run through a ring of kRingGroups groups of kRingPlaces
 // places; on chip, `iters` places of each of `stages` samples are staged.
 constexpr int kRingGroups = 4, kRingPlaces = 2;
 // Bytes of one staged sample, or of the ring.
@@ -76,14 +75,14 @@ inline __host__ __device__ size_t gn_stage_bytes(const GnShape& s, bool bwd) {
   return static_cast<size_t>(bwd ? 2 : 1) * (s.on_chip ? s.iters : kRingGroups * kRingPlaces) *
          s.threads * 16;
 }
-// Shared memory of the statistics kernels behind the staged vectors, in floats:
+// Shared memory of the kernels behind the staged vectors, in floats:
 //   w, b  cs parameters each
 //   c0, c1  cs channel constants each (forward: -mean and rstd * w; backward: nc1 and nc2)
 //   col   2 * cs column values; on chip backward: + 4 * cs running totals (sum, compensation)
 //   gm    2 * gs: the CTA's group values
 //   red   2 planes [lanes][red_stride]: per-thread column values on their way to column sums
-//         (forward: mean and M2; backward: A and B); two launches: over the ring, which is
-//         done by then
+//         (forward: mean and M2; backward: A and B); streamed: over the ring, which is empty
+//         then
 // A row of red is padded so that four rows of eight columns fall on 32 different banks wherever
 // the slab is a multiple of 32 channels.
 inline __host__ __device__ int red_stride(const GnShape& s) { return s.cs + (s.cs % 32 ? 0 : 8); }
@@ -100,30 +99,17 @@ inline __host__ __device__ size_t gn_stats_smem(const GnShape& s, bool bwd) {
                    (2 * static_cast<size_t>(s.gs) + 3) / 4 * 4;
   return gn_front_bytes(s, bwd) + n * sizeof(float) + (s.on_chip ? gn_red_bytes(s) : 0);
 }
-// Shared memory of the second launch: the ring, then w, b, c0, c1 as above.
-inline __host__ __device__ size_t gn_out_smem(const GnShape& s, bool bwd) {
-  return gn_stage_bytes(s, bwd) + (4 * static_cast<size_t>(s.cs)) * sizeof(float);
+// CTAs of the launch.
+inline int64_t gn_ctas(const GnShape& s) {
+  return s.on_chip ? static_cast<int64_t>(s.slabs) * s.ctas * s.lanes_n : s.grid;
 }
 
-// CTAs of the launches (two launches: over nu units).
-inline int64_t gn_stats_ctas(const GnShape& s, int64_t nu) {
-  return s.on_chip ? static_cast<int64_t>(s.slabs) * s.ctas * s.lanes_n : nu * s.ctas * s.chunks;
-}
-inline int64_t gn_out_ctas(const GnShape& s, int64_t nu) { return nu * s.parts; }
+// Launches fn: in clusters with programmatic dependent launch, or as a cooperative grid.
+cudaError_t launch_gn(const void* fn, const GnArgs& a, cudaStream_t st);
 
-// Launches fn over `ctas` CTAs in clusters of s.ctas, with programmatic dependent launch.
-cudaError_t launch_cluster(const void* fn, int64_t ctas, const GnShape& s, const GnArgs& a,
-                           cudaStream_t st);
-
-// Launches fn, a second launch, over the units of a.
-cudaError_t launch_out(const void* fn, const GnArgs& a, bool bwd, cudaStream_t st);
-
-// Launch the statistics (and, on chip, the output) of a's samples or units; then, for two
-// launches, the output.  dtype and act: GROUPNORM_*.
+// dtype and act: GROUPNORM_*.
 cudaError_t launch_gn_fwd(const GnArgs& a, int dtype, int act, cudaStream_t st);
-cudaError_t launch_gn_fwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st);
 cudaError_t launch_gn_bwd(const GnArgs& a, int dtype, int act, cudaStream_t st);
-cudaError_t launch_gn_bwd_out(const GnArgs& a, int dtype, int act, cudaStream_t st);
 // dw, db = the sums of `rows` column-sum rows [2][C] (rows == 0: zeros).
 cudaError_t launch_gn_finish(const float* cols, float* dw, float* db, int64_t rows, int C,
                              cudaStream_t st);

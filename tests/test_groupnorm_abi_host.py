@@ -70,7 +70,7 @@ SIZES = [
     (dict(N=0), OK),
     (dict(N=0, S=0, x=None, y=None, mean=None, rstd=None), OK),
     (dict(N=0, w=None), INVALID),
-    (dict(S=200000), WORKSPACE),                 # two launches: a workspace is due
+    (dict(S=200000), WORKSPACE),                 # streamed: a workspace is due
     (dict(S=200000, ws=BAD_PTR, wsb=16), WORKSPACE),
     (dict(S=200000, ws=MISALIGNED, wsb=1 << 20), INVALID),
 ])
@@ -131,7 +131,9 @@ def test_plans_fit_the_kernels():
             assert p["channels"] // ev <= p["threads"] <= 512 and p["threads"] % 32 == 0
             assert p["cluster_ctas"] in (1, 2, 4, 8) and p["smem"] <= 227 * 1024
             assert p["ctas"] % p["cluster_ctas"] == 0 and 0 < p["ctas"] < 1 << 31
-            assert p["out_ctas"] < 1 << 31 and (p["out_ctas"] == 0) == (p["on_chip"] == 1)
+            assert 1 <= p["chunks"] <= S and (p["on_chip"] == 0 or p["chunks"] == 1)
+            assert p["units"] * p["chunks"] < 1 << 31 or p["on_chip"]
+            assert p["on_chip"] or p["ctas"] <= 304
             assert 1 <= p["units"] <= n * (C // p["channels"])
             size = (N.groupnorm_train_bwd_workspace_bytes if bwd
                     else N.groupnorm_train_fwd_workspace_bytes)(dtype, n, S, C, G)
@@ -141,7 +143,7 @@ def test_plans_fit_the_kernels():
             assert size <= max(n * S * C * (4 if dtype == 1 else 2), 2432 * 2 * C * 4)
             seen.add((bwd, p["on_chip"], p["cluster_ctas"]))
     assert {(d, 1, k) for d in (False, True) for k in (1, 2, 4, 8)} <= seen
-    assert {(d, 0, 4) for d in (False, True)} <= seen
+    assert {(d, 0, 1) for d in (False, True)} <= seen
 
 
 def test_torch_api_refuses_what_the_kernels_do_not_take():

@@ -54,12 +54,12 @@ def depth(x, groups, bwd):
     if p["on_chip"]:
         rows, chunks = -(-s // p["cluster_ctas"]), 1
     else:
-        chunks = p["ctas"] // (p["units"] * p["cluster_ctas"])
-        rows = -(-s // (chunks * p["cluster_ctas"])) + 1
+        chunks = p["chunks"]
+        rows = -(-s // chunks)
     # a thread's places (at least half the lanes the plan has threads for), four lanes of a
-    # column at a time, eight columns of a group, eight chunks; the trees between
+    # column at a time, eight columns of a group, 32 chunks; the trees between
     places = rows // max(1, (lanes + 1) // 2) + 2
-    return places + lanes / 4 + 3 + c // groups / 8 + 4 + 4 + chunks / 8 + 4
+    return places + lanes / 4 + 3 + c // groups / 8 + 4 + 4 + chunks / 32 + 6
 
 
 def case(seed, n, s, c, dtype, wb=FP, offset=0.0):
@@ -150,7 +150,7 @@ SHAPES = [(1, 1, 64, 1), (3, 1, 256, 4), (2, 7, 8, 1), (2, 37, 64, 64), (3, 33, 
           (2, 130, 24, 8), (5, 50, 320, 32), (1, 3, 4088, 8), (2, 9, 2048, 1), (2, 64, 1280, 32),
           (7, 257, 96, 6), (1, 1023, 640, 32), (2, 1500, 72, 8), (1, 4096, 320, 32),
           (1, 9000, 128, 32), (300, 5, 64, 8)]
-# two launches: samples past a cluster's shared memory, several pairs of launches, wide slabs
+# streamed: samples past a cluster's shared memory, several turns, wide slabs
 LARGE = [(1, 70001, 64, 4), (9, 70001, 64, 4), (1, 20011, 520, 8), (1, 301, 2048, 1)]
 
 
@@ -190,7 +190,7 @@ def test_backward(n, s, c, groups, dtype, kind):
 
 @pytest.mark.parametrize("n,s,c,groups", LARGE)
 @pytest.mark.parametrize("dtype", [BF, FP], ids=str)
-def test_two_launches(n, s, c, groups, dtype):
+def test_streamed(n, s, c, groups, dtype):
     x, dy, w, b = case(n + s, n, s, c, dtype)
     plans = [N.groupnorm_train_launch_plan(GN._DTYPES[dtype], n, s, c, groups, d) for d in (0, 1)]
     assert not plans[1]["on_chip"]
