@@ -34,7 +34,7 @@ constexpr int kSlabBytes = 128, kMinSlabBytes = 32;
 constexpr int kSmallCta = 16 * 1024;  // staged bytes below which a CTA is not split further
 constexpr int kMaxStages = 4;
 // streamed: bytes of x (and dy) a turn may take, to be found in L2 again
-constexpr int64_t kL2Bytes = int64_t{64} << 20;
+constexpr int64_t kL2Bytes = int64_t{80} << 20;
 
 int elem_bytes(int dtype) { return dtype == GROUPNORM_FP32 ? 4 : 2; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -150,13 +150,19 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
   // streamed
   int gs = slab_groups(dtype, C, G, kSlabBytes);
   auto slab_bytes = [&] { return S * gs * (C / G) * elem_bytes(dtype) * (bwd ? 2 : 1); };
-  if (slab_bytes() > kL2Bytes) gs = slab_groups(dtype, C, G, kSlabBytes / 2);
   GnShape s = slab_shape(dtype, C, G, gs, S, 4);
   const int64_t all = N * s.slabs;
-  int64_t units = kL2Bytes / slab_bytes();
+  // whole samples a turn, full lines of memory, unless one is far larger than L2 (measured: half
+  // lines cost more than reading a quarter of the turn twice)
+  const int64_t sample = slab_bytes() * s.slabs;
+  int64_t units = sample <= 2 * kL2Bytes ? (sample < kL2Bytes ? kL2Bytes / sample : 1) * s.slabs
+                                         : kL2Bytes / slab_bytes();
   units = units < 1 ? 1 : (units > all ? all : units);
-  units = ceil_div(all, ceil_div(all, units));  // evened out
-  if (units > INT32_MAX / 2) units = INT32_MAX / 2;
+  if (units >= s.slabs) {  // evened out
+    const int64_t turns = ceil_div(N, units / s.slabs);
+    units = ceil_div(N, turns) * s.slabs;
+  }
+  // (a unit past a cluster's shared memory has 2^15 elements and more, so `all` fits 31 bits)
   s.units = static_cast<int>(units);
   s.grid = kSMs * min_ctas(s.vecs > kThreads);
   // a piece a CTA, each thread 4 to 256 places

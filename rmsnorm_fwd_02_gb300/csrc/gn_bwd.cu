@@ -18,13 +18,14 @@ template <typename T>
 struct Consts {
   static constexpr int kPairs = VecOf<T>::kPairs;
   f2 nm[kPairs], scale[kPairs], bias[kPairs];
-  // w, b: the slab's parameters in shared memory; mean, rstd: the sample's group values from the
-  // slab's first group on; c: the thread's first channel, place r of group g
+  // w, b: the slab's parameters in shared memory; mean, rstd: the sample's group values, `gap`
+  // floats apart, from the slab's first group on; c: the thread's first channel, place r of
+  // group g
   __device__ __forceinline__ void load(const float* w, const float* b, const float* mean,
-                                       const float* rstd, int cg, int c, int g, int r) {
+                                       const float* rstd, int gap, int cg, int c, int g, int r) {
     lds_pairs<kPairs>(w + c, scale);
     lds_pairs<kPairs>(b + c, bias);
-    float m = mean[g], q = rstd[g];
+    float m = mean[gap * g], q = rstd[gap * g];
     float v[2 * kPairs], u[2 * kPairs];
 #pragma unroll
     for (int j = 0; j < 2 * kPairs; ++j) {
@@ -33,8 +34,8 @@ struct Consts {
       if (j + 1 < 2 * kPairs && ++r == cg) {
         r = 0;
         ++g;
-        m = mean[g];
-        q = rstd[g];
+        m = mean[gap * g];
+        q = rstd[gap * g];
       }
     }
 #pragma unroll
@@ -111,12 +112,13 @@ struct ColumnSums {
 
 // Column sums over the CTA's places from its threads': A * rstd (= sum of dz * xhat) to
 // m.col[0, cs), B to [cs, 2 cs).  A warp takes eight quads of columns, four lanes of each at a
-// time; each value also goes to sink(half, column of the slab, value).  Then the CTA's group sums
+// time; each value also goes to sink(half, column of the slab, value); rstd: the groups' values,
+// `gap` floats apart.  Then the CTA's group sums
 // of w * A and w * B to m.gm, an octet of threads a group.
 template <typename T, int kAct, typename F>
 __device__ __forceinline__ void cta_sums(const Smem& m, const GnShape& s, const Owner& o,
                                          const ColumnSums<T, kAct>& sum, const float* rstd,
-                                         F sink) {
+                                         int gap, F sink) {
   constexpr int NP = VecOf<T>::kPairs;
   const int w = threadIdx.x >> 5, nw = s.threads >> 5, l8 = threadIdx.x & 7;
   const int oct = (threadIdx.x & 31) >> 3;
@@ -146,7 +148,7 @@ __device__ __forceinline__ void cta_sums(const Smem& m, const GnShape& s, const 
                        : oct == 1 ? f2_hi(v[0]) : (oct == 2 ? f2_lo(v[1]) : f2_hi(v[1]));
     if (c < s.cs) {
       const int cc = c + oct;
-      const float val = half == 0 ? mine * rstd[cc / s.cg] : mine;
+      const float val = half == 0 ? mine * rstd[gap * (cc / s.cg)] : mine;
       m.col[half * s.cs + cc] = val;
       sink(half, cc, val);
     }
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     const uint32_t mine = stage + 2 * k * s.iters * stride;
     auto add = [&](const uint4& xu, const uint4& du) { sum.add(q, xu, du); };
     if (s.stages == 1) {  // the sums follow the copies, batch by batch
-      if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
+      if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, 1, s.cg, o.c, og, orr);
       for (int b = 0; b < kBatches; ++b) {
         cp_async_wait(kBatches - 1 - b);
         for_staged2(mine, dy_off, b * per, min(o.cnt, (b + 1) * per), stride, add);
@@ -245,11 +247,11 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       const int ahead = s.stages - 1;
       stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
                    0, s.iters);
-      if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, s.cg, o.c, og, orr);
+      if (o.cnt > 0) q.load(m.w, m.b, mean, rstd, 1, s.cg, o.c, og, orr);
       cp_async_wait(ahead);
       for_staged2(mine, dy_off, 0, o.cnt, stride, add);
     }
-    cta_sums(m, s, o, sum, rstd, [&](int half, int c, float v) {
+    cta_sums(m, s, o, sum, rstd, 1, [&](int half, int c, float v) {
       float* run = m.run + 2 * (half * s.cs + c);  // Kahan's running sum over the samples
       const float y = __fsub_rn(v, run[1]);
       const float r = __fadd_rn(run[0], y);
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     out[t < s.cs ? t : a.C + t - s.cs] = m.run[2 * t];
 }
 
-// Streamed, as the forward's (gn_fwd.cu): a turn's sums, the barrier, its dx.
+// Streamed, as the forward's (gn_fwd.cu): the sums of turn t + 1, the barrier, dx of turn t.
 template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     gn_bwd_stream_kernel(const GnArgs a) {
@@ -311,31 +313,37 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   Owner o;
   set_lane(o, s);
   const int og = o.c / s.cg, orr = o.c - og * s.cg;
-  const int64_t all = a.N * s.slabs;
-  for (int64_t u0 = 0; u0 < all; u0 += s.units) {
-    const int nu = static_cast<int>(min(static_cast<int64_t>(s.units), all - u0));
-    const int pieces = nu * s.chunks;
-    auto place = [&] { return (o.n * a.S + o.r0 + o.lane) * a.C + o.slab * s.cs + o.c; };
-    auto ring_of = [&] {  // piece o's
-      const T* p = static_cast<const T*>(a.x) + o.n * a.s_n + (o.r0 + o.lane) * a.s_s +
-                   o.slab * s.cs + o.c;
-      return Ring<2>{smem_u32(smem) + 16u * tid, stride,
-                     {reinterpret_cast<const unsigned char*>(p),
-                      reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.dy) + place())},
-                     {step * static_cast<int64_t>(sizeof(T)),
-                      dstep * static_cast<int64_t>(sizeof(T))}, o.cnt};
-    };
-    Ring<2> ring{};
-    Consts<T> q;
-    for (int v = blockIdx.x; v < pieces; v += gridDim.x) {
+  const int all = static_cast<int>(a.N) * s.slabs;
+  auto units_at = [&](int u0) { return min(s.units, all - u0); };
+  auto place = [&] { return (o.n * a.S + o.r0 + o.lane) * a.C + o.slab * s.cs + o.c; };
+  auto ring_of = [&](bool back) {  // piece o's, from its last place if back
+    const int64_t last = back ? o.cnt - 1 : 0, es = back ? -int64_t{sizeof(T)} : int64_t{sizeof(T)};
+    const T* p = static_cast<const T*>(a.x) + o.n * a.s_n + (o.r0 + o.lane) * a.s_s +
+                 o.slab * s.cs + o.c + last * step;
+    const T* d = static_cast<const T*>(a.dy) + place() + last * dstep;
+    return Ring<2>{smem_u32(smem) + 16u * tid, stride,
+                   {reinterpret_cast<const unsigned char*>(p),
+                    reinterpret_cast<const unsigned char*>(d)}, {step * es, dstep * es}, o.cnt};
+  };
+  // piece o's parameters and statistics to shared memory (its copies have started)
+  auto load_piece = [&] {
+    __syncthreads();  // the piece before is done with them
+    load_params(a, m.w, m.b, o.slab);
+    for (int g = tid; g < s.gs; g += s.threads) {
+      m.ms[2 * g] = a.mean[o.n * a.G + o.slab * s.gs + g];
+      m.ms[2 * g + 1] = a.rstd[o.n * a.G + o.slab * s.gs + g];
+    }
+  };
+  auto sum_turn = [&](int u0) {
+    const int nu = units_at(u0);
+    for (int v = blockIdx.x; v < nu * s.chunks; v += gridDim.x) {
       set_piece(o, a, u0, nu, v);
-      ring = ring_of();
+      Ring<2> ring = ring_of(false);
       ring.start();
-      load_params(a, m.w, m.b, o.slab);
+      load_piece();
       __syncthreads();
-      const float* const rstd = a.rstd + o.n * a.G + o.slab * s.gs;
-      if (o.cnt > 0)
-        q.load(m.w, m.b, a.mean + o.n * a.G + o.slab * s.gs, rstd, s.cg, o.c, og, orr);
+      Consts<T> q;
+      if (o.cnt > 0) q.load(m.w, m.b, m.ms, m.ms + 1, 2, s.cg, o.c, og, orr);
       ColumnSums<T, kAct> sum;
       sum.clear();
       ring.run(o.cnt, [&](uint32_t slot) {
@@ -343,39 +351,33 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       });
       __syncthreads();  // red takes the rings' place
       float* cols = a.cols + (o.n * s.chunks + o.chunk) * 2 * a.C + o.slab * s.cs;
-      cta_sums(m, s, o, sum, rstd,
+      cta_sums(m, s, o, sum, m.ms + 1, 2,
                [&](int half, int c, float val) { cols[half * a.C + c] = val; });
       __syncthreads();
       float2* part = a.part + (o.n * s.chunks + o.chunk) * a.G + o.slab * s.gs;
       for (int g = tid; g < s.gs; g += s.threads)
         part[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
     }
-    // the last piece summed is the first written: o is still its owner, q its constants
-    int v = blockIdx.x < pieces
-                ? blockIdx.x + (pieces - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) *
-                                   static_cast<int>(gridDim.x)
-                : -1;
-    if (v >= 0) {
-      ring = ring_of();
+  };
+
+  auto grid = cooperative_groups::this_grid();
+  sum_turn(0);
+  auto token = grid.barrier_arrive();
+  for (int u0 = 0; u0 < all; u0 += s.units) {
+    const bool more = u0 + s.units < all;
+    if (more) sum_turn(u0 + s.units);
+    grid.barrier_wait(std::move(token));
+    if (more) token = grid.barrier_arrive();
+    const int nu = units_at(u0);
+    for (int v = blockIdx.x; v < nu * s.chunks; v += gridDim.x) {
+      set_piece(o, a, u0, nu, v);
+      Ring<2> ring = ring_of(true);
       ring.start();
-    }
-    cooperative_groups::this_grid().sync();
-    for (; v >= 0; v -= gridDim.x) {
-      if (v + static_cast<int>(gridDim.x) < pieces) {  // not the one whose copies have started
-        set_piece(o, a, u0, nu, v);
-        ring = ring_of();
-        ring.start();
-        __syncthreads();  // the piece before is done with w, b, c0, c1
-        load_params(a, m.w, m.b, o.slab);
-        __syncthreads();
-        if (o.cnt > 0)
-          q.load(m.w, m.b, a.mean + o.n * a.G + o.slab * s.gs, a.rstd + o.n * a.G + o.slab * s.gs,
-                 s.cg, o.c, og, orr);
-      }
+      load_piece();
       for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
         const float2* p = a.part + o.n * s.chunks * a.G + o.slab * s.gs + g;
         float sa = 0.f, sb = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = l; k < s.chunks; k += 32) {  // not through L1 (gn_fwd.cu)
           const float2 x = __ldcg(p + static_cast<int64_t>(k) * a.G);
           sa += x.x;
@@ -383,21 +385,33 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         }
         sa = warp_allsum(sa);
         sb = warp_allsum(sb);
-        set_group(m, s, g, l, 32, a.rstd[o.n * a.G + o.slab * s.gs + g], sa, sb, total);
+        if (l == 0) {
+          m.gm[2 * g] = sa / total;
+          m.gm[2 * g + 1] = sb / total;
+        }
       }
+      __syncthreads();
+      for (int c = tid; c < s.cs; c += s.threads) {
+        const int g = c / s.cg;
+        const float r = m.ms[2 * g + 1];
+        m.c0[c] = -r * m.gm[2 * g + 1];
+        m.c1[c] = -r * r * m.gm[2 * g];
+      }
+      Consts<T> q;
+      if (o.cnt > 0) q.load(m.w, m.b, m.ms, m.ms + 1, 2, s.cg, o.c, og, orr);
       __syncthreads();
       if (o.cnt > 0) {
         GroupTerms<T> t;
         t.load(m.c0, m.c1, o.c);
-        T* po = static_cast<T*>(a.out) + place();
+        T* po = static_cast<T*>(a.out) + place() + (o.cnt - 1) * dstep;
         ring.run(o.cnt, [&](uint32_t slot) {  // dx is not read here again: it leaves L2 first
           __stcs(reinterpret_cast<uint4*>(po),
                  dx_vec<T, kAct>(q, t, lds128_at(slot), lds128_at(slot + kRingSlots * stride)));
-          po += dstep;
+          po -= dstep;
         });
       }
     }
-    __syncthreads();  // the next turn's sums reuse the shared memory
+    __syncthreads();  // the sums reuse the shared memory
   }
 }
 

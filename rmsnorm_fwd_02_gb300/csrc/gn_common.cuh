@@ -4,6 +4,8 @@
 
 #include <cooperative_groups.h>
 
+#include <utility>
+
 #include "gn_launch.h"
 #include "groupnorm_train.h"
 #include "ln_common.cuh"
@@ -207,6 +209,7 @@ __device__ __forceinline__ int rank_start(int places, int k, const GnShape& s) {
 struct Smem {
   float* red;   // [2][lanes][red_stride]
   float* gm;    // [gs][2]
+  float* ms;    // [gs][2]
   float* w;     // [cs]
   float* b;     // [cs]
   float* c0;    // [cs]
@@ -224,7 +227,8 @@ __device__ __forceinline__ Smem carve(unsigned char* base, const GnShape& s, boo
   m.col = m.c1 + s.cs;
   m.run = m.col + 2 * s.cs;
   m.gm = m.run + (bwd && s.on_chip ? 4 * s.cs : 0);
-  m.red = s.on_chip ? m.gm + (2 * s.gs + 3) / 4 * 4 : reinterpret_cast<float*>(base);
+  m.ms = m.gm + 2 * s.gs;
+  m.red = s.on_chip ? m.gm + 4 * s.gs : reinterpret_cast<float*>(base);
   return m;
 }
 // The slab's parameters to shared memory (no synchronization).
@@ -270,13 +274,13 @@ __device__ __forceinline__ Owner on_chip_owner(const GnArgs& a) {
 }
 // Piece v of a turn that starts at unit u0 and takes nu: neighbouring pieces are neighbouring
 // slabs of the same places.
-__device__ __forceinline__ void set_piece(Owner& o, const GnArgs& a, int64_t u0, int nu, int v) {
+__device__ __forceinline__ void set_piece(Owner& o, const GnArgs& a, int u0, int nu, int v) {
   const GnShape& s = a.s;
   o.rank = 0;
   o.chunk = v / nu;
-  const int64_t u = u0 + (v - o.chunk * nu);
-  o.n = u / s.slabs;
-  o.slab = static_cast<int>(u - o.n * s.slabs);
+  const int u = u0 + (v - o.chunk * nu), n = u / s.slabs;
+  o.n = n;
+  o.slab = u - n * s.slabs;
   o.len = o.rows = s.chunk_base + (o.chunk < s.chunk_more ? 1 : 0);
   o.r0 = static_cast<int64_t>(o.chunk) * s.chunk_base + min(o.chunk, s.chunk_more);
   set_count(o, s);
@@ -284,8 +288,7 @@ __device__ __forceinline__ void set_piece(Owner& o, const GnArgs& a, int64_t u0,
 
 // A thread's own copies through its ring: kTensors 16-byte vectors a place (tensor t's slots
 // kRingSlots strides behind tensor t - 1's), kRingPlaces places a copy group, kRingGroups - 1
-// groups on their way while one is used.  One turn of the ring is unrolled, so that slots are
-// fixed offsets.
+// groups on their way while one is used.
 constexpr int kRingSlots = kRingGroups * kRingPlaces;
 template <int kTensors>
 struct Ring {
@@ -295,38 +298,48 @@ struct Ring {
   int64_t step[kTensors];  // bytes from place to place
   int left;                // places not issued yet
 
-  __device__ __forceinline__ void issue(int group) {
+  __device__ __forceinline__ void copy(uint32_t d) {
 #pragma unroll
-    for (int j = 0; j < kRingPlaces; ++j) {
-      if (left > 0) {
-#pragma unroll
-        for (int t = 0; t < kTensors; ++t) {
-          cp_async_16(slot + (group * kRingPlaces + j + t * kRingSlots) * stride, p[t]);
-          p[t] += step[t];
-        }
-        --left;
-      }
+    for (int t = 0; t < kTensors; ++t) {
+      cp_async_16(d + t * kRingSlots * stride, p[t]);
+      p[t] += step[t];
     }
+  }
+  __device__ __forceinline__ void issue(uint32_t d) {  // a group that may pass the end
+#pragma unroll
+    for (int j = 0; j < kRingPlaces; ++j)
+      if (left > j) copy(d + j * stride);
+    left -= kRingPlaces;
     cp_async_commit();
   }
   __device__ __forceinline__ void start() {
 #pragma unroll
-    for (int g = 0; g + 1 < kRingGroups; ++g) issue(g);
+    for (int g = 0; g + 1 < kRingGroups; ++g) issue(slot + g * kRingPlaces * stride);
   }
   // f(its slot) for each of the thread's cnt places in order
   template <typename F>
   __device__ __forceinline__ void run(int cnt, F f) {
-    for (int i = 0; i < cnt; i += kRingSlots) {
+    const uint32_t group = kRingPlaces * stride, end = slot + kRingSlots * stride;
+    uint32_t rd = slot, wr = end - group;
+    int i = 0;
+    for (; left >= kRingPlaces; left -= kRingPlaces, i += kRingPlaces) {  // whole groups
 #pragma unroll
-      for (int g = 0; g < kRingGroups; ++g) {
-        if (i + g * kRingPlaces < cnt) {
-          issue((g + kRingGroups - 1) % kRingGroups);
-          cp_async_wait(kRingGroups - 1);
+      for (int j = 0; j < kRingPlaces; ++j) copy(wr + j * stride);
+      cp_async_commit();
+      wr = wr + group == end ? slot : wr + group;
+      cp_async_wait(kRingGroups - 1);
 #pragma unroll
-          for (int j = 0; j < kRingPlaces; ++j)
-            if (i + g * kRingPlaces + j < cnt) f(slot + (g * kRingPlaces + j) * stride);
-        }
-      }
+      for (int j = 0; j < kRingPlaces; ++j) f(rd + j * stride);
+      rd = rd + group == end ? slot : rd + group;
+    }
+    for (; i < cnt; i += kRingPlaces) {
+      issue(wr);
+      wr = wr + group == end ? slot : wr + group;
+      cp_async_wait(kRingGroups - 1);
+#pragma unroll
+      for (int j = 0; j < kRingPlaces; ++j)
+        if (i + j < cnt) f(rd + j * stride);
+      rd = rd + group == end ? slot : rd + group;
     }
   }
 };

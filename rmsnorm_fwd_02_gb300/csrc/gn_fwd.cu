@@ -270,10 +270,12 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   }
 }
 
-// Streamed.  Each turn's pieces (a unit's chunk each) are dealt out to the grid; a CTA sums its
-// own, and after the barrier combines the chunks' statistics of its unit (a warp a group, the
-// chunks over its lanes) and writes its own pieces' output, its first copies already on their
-// way.  Turns follow each other without a second barrier: every unit has its own place in part.
+// Streamed.  Each turn's pieces (a unit's chunk each) are dealt out to the grid.  A CTA sums its
+// pieces of turn t + 1 before it waits for every CTA's sums of turn t and writes its pieces of
+// that one, so the grid's barrier and the CTAs' unevenness hide behind a turn's sums; L2 holds
+// both turns.  Before the output a unit's chunks combine (a warp a group, the chunks over its
+// lanes).  A piece is written from its last place back, so that of a turn larger than L2 the
+// part still held is read first.  Every unit has its own place in part.
 template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     gn_fwd_stream_kernel(const GnArgs a) {
@@ -286,21 +288,20 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   const float cg = static_cast<float>(s.cg);
   Owner o;
   set_lane(o, s);
-  const int64_t all = a.N * s.slabs;
-  for (int64_t u0 = 0; u0 < all; u0 += s.units) {
-    const int nu = static_cast<int>(min(static_cast<int64_t>(s.units), all - u0));
-    const int pieces = nu * s.chunks;
-    auto ring_of = [&] {  // piece o's
-      const T* p = static_cast<const T*>(a.x) + o.n * a.s_n + (o.r0 + o.lane) * a.s_s +
-                   o.slab * s.cs + o.c;
-      return Ring<1>{smem_u32(smem) + 16u * tid, 16u * s.threads,
-                     {reinterpret_cast<const unsigned char*>(p)},
-                     {step * static_cast<int64_t>(sizeof(T))}, o.cnt};
-    };
-    Ring<1> ring{};
-    for (int v = blockIdx.x; v < pieces; v += gridDim.x) {
+  const int all = static_cast<int>(a.N) * s.slabs;
+  auto units_at = [&](int u0) { return min(s.units, all - u0); };
+  auto ring_of = [&](bool back) {  // piece o's, from its last place if back
+    const T* p = static_cast<const T*>(a.x) + o.n * a.s_n + (o.r0 + o.lane) * a.s_s +
+                 o.slab * s.cs + o.c + (back ? (o.cnt - 1) * step : 0);
+    return Ring<1>{smem_u32(smem) + 16u * tid, 16u * s.threads,
+                   {reinterpret_cast<const unsigned char*>(p)},
+                   {(back ? -step : step) * static_cast<int64_t>(sizeof(T))}, o.cnt};
+  };
+  auto sum_turn = [&](int u0) {
+    const int nu = units_at(u0);
+    for (int v = blockIdx.x; v < nu * s.chunks; v += gridDim.x) {
       set_piece(o, a, u0, nu, v);
-      ring = ring_of();
+      Ring<1> ring = ring_of(false);
       ring.start();
       ColumnStats<T> st;
       if (o.cnt > 0) {
@@ -315,32 +316,31 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       for (int g = tid; g < s.gs; g += s.threads)
         part[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
     }
-    // the last piece summed is the first written: o is still its owner
-    int v = blockIdx.x < pieces
-                ? blockIdx.x + (pieces - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) *
-                                   static_cast<int>(gridDim.x)
-                : -1;
-    if (v >= 0) {
-      ring = ring_of();
+  };
+
+  auto grid = cooperative_groups::this_grid();
+  sum_turn(0);
+  auto token = grid.barrier_arrive();
+  for (int u0 = 0; u0 < all; u0 += s.units) {
+    const bool more = u0 + s.units < all;
+    if (more) sum_turn(u0 + s.units);
+    grid.barrier_wait(std::move(token));
+    if (more) token = grid.barrier_arrive();
+    const int nu = units_at(u0);
+    for (int v = blockIdx.x; v < nu * s.chunks; v += gridDim.x) {
+      set_piece(o, a, u0, nu, v);
+      Ring<1> ring = ring_of(true);
       ring.start();
-    }
-    cooperative_groups::this_grid().sync();
-    for (; v >= 0; v -= gridDim.x) {
-      if (v + static_cast<int>(gridDim.x) < pieces) {  // not the one whose copies have started
-        set_piece(o, a, u0, nu, v);
-        ring = ring_of();
-        ring.start();
-      }
       __syncthreads();  // the piece before is done with w, b, c0, c1
+      // one round trip to memory: the parameters and the chunks' statistics
       load_params(a, m.w, m.b, o.slab);
-      __syncthreads();
       for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
         const float2* p = a.part + o.n * s.chunks * a.G + o.slab * s.gs + g;
         // about the first chunk's mean, as in cta_stats; not through L1, which may hold an
         // earlier turn's line
         const float ref = __ldcg(p).x;
         float sum = 0.f, m2 = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = l; k < s.chunks; k += 32) {
           const float2 x = __ldcg(p + static_cast<int64_t>(k) * a.G);
           const float d = x.x - ref;
@@ -350,27 +350,37 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         }
         sum = warp_allsum(sum);
         m2 = warp_allsum(m2);
-        const float off = sum / total, mean = ref + off;
-        m2 = __fmaf_rn(-off, sum, m2);
-        const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
-        set_group(m, s, g, l, 32, mean, rstd);
-        if (l == 0 && o.chunk == 0) {
-          a.mean[o.n * a.G + o.slab * s.gs + g] = mean;
-          a.rstd[o.n * a.G + o.slab * s.gs + g] = rstd;
+        if (l == 0) {
+          const float off = sum / total, mean = ref + off;
+          m2 = __fmaf_rn(-off, sum, m2);
+          const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
+          m.gm[2 * g] = mean;
+          m.gm[2 * g + 1] = rstd;
+          if (o.chunk == 0) {
+            a.mean[o.n * a.G + o.slab * s.gs + g] = mean;
+            a.rstd[o.n * a.G + o.slab * s.gs + g] = rstd;
+          }
         }
+      }
+      __syncthreads();
+      for (int c = tid; c < s.cs; c += s.threads) {
+        const int g = c / s.cg;
+        m.c0[c] = -m.gm[2 * g];
+        m.c1[c] = m.gm[2 * g + 1] * m.w[c];
       }
       __syncthreads();
       if (o.cnt > 0) {
         Consts<T> q;
         q.load(m.c0, m.c1, m.b, o.c);
-        T* py = static_cast<T*>(a.out) + (o.n * a.S + o.r0 + o.lane) * a.C + o.slab * s.cs + o.c;
+        T* py = static_cast<T*>(a.out) + (o.n * a.S + o.r0 + o.lane) * a.C + o.slab * s.cs + o.c +
+                (o.cnt - 1) * ystep;
         ring.run(o.cnt, [&](uint32_t slot) {  // y is not read here again: it leaves L2 first
           __stcs(reinterpret_cast<uint4*>(py), q.template norm<kAct>(lds128_at(slot)));
-          py += ystep;
+          py -= ystep;
         });
       }
     }
-    __syncthreads();  // the next turn's sums reuse the shared memory
+    __syncthreads();  // the sums reuse the shared memory
   }
 }
 

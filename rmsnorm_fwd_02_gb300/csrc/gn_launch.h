@@ -80,6 +80,7 @@ inline __host__ __device__ size_t gn_stage_bytes(const GnShape& s, bool bwd) {
 //   c0, c1  cs channel constants each (forward: -mean and rstd * w; backward: nc1 and nc2)
 //   col   2 * cs column values; on chip backward: + 4 * cs running totals (sum, compensation)
 //   gm    2 * gs: the CTA's group values
+//   ms    2 * gs: backward, the sample's mean and rstd of the slab's groups
 //   red   2 planes [lanes][red_stride]: per-thread column values on their way to column sums
 //         (forward: mean and M2; backward: A and B); streamed: over the ring, which is empty
 //         then
@@ -96,7 +97,7 @@ inline __host__ __device__ size_t gn_front_bytes(const GnShape& s, bool bwd) {  
 }
 inline __host__ __device__ size_t gn_stats_smem(const GnShape& s, bool bwd) {
   const size_t n = 6 * static_cast<size_t>(s.cs) + (bwd && s.on_chip ? 4 * s.cs : 0) +
-                   (2 * static_cast<size_t>(s.gs) + 3) / 4 * 4;
+                   4 * static_cast<size_t>(s.gs);
   return gn_front_bytes(s, bwd) + n * sizeof(float) + (s.on_chip ? gn_red_bytes(s) : 0);
 }
 // CTAs of the launch.

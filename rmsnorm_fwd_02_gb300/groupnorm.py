@@ -14,6 +14,7 @@ are float32 [N, groups]; dw, db float32 [C].  All results are bit-reproducible.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -39,6 +40,8 @@ def _places(x: torch.Tensor, groups: int):
         raise ValueError(f"{c} channels do not divide into {groups} groups")
     if x.stride(-1) != 1 and c > 1:
         raise ValueError("the channels must be contiguous (channels last)")
+    if x.is_contiguous():
+        return dtype, n, s, c, s * c, c
     try:
         v = x.view(n, s, c)
     except RuntimeError:
@@ -63,6 +66,13 @@ def _act(act: str) -> int:
     return _ACTS[act]
 
 
+# functions of the shape alone
+_fwd_bytes = functools.lru_cache(maxsize=4096)(
+    lambda *shape: N.groupnorm_train_fwd_workspace_bytes(*shape))
+_bwd_bytes = functools.lru_cache(maxsize=4096)(
+    lambda *shape: N.groupnorm_train_bwd_workspace_bytes(*shape))
+
+
 def _workspace(nbytes: int, x: torch.Tensor):
     return torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
 
@@ -74,7 +84,7 @@ def groupnorm_fwd(x, w, b, groups, eps=EPS, act="none"):
     mean = torch.empty((n, groups), dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
     with _on(x):
-        nbytes = N.groupnorm_train_fwd_workspace_bytes(dtype, n, s, c, groups)
+        nbytes = _fwd_bytes(dtype, n, s, c, groups)
         N.groupnorm_train_fwd(x, dtype, w.contiguous(), b.contiguous(), wb, y, mean, rstd,
                               _workspace(nbytes, x), nbytes, n, s, c, groups, s_n, s_s,
                               float(eps), code)
@@ -93,7 +103,7 @@ def groupnorm_bwd(dy, x, mean, rstd, w, b, groups, act="none"):
     dw = torch.empty(c, dtype=torch.float32, device=x.device)
     db = torch.empty_like(dw)
     with _on(x):
-        nbytes = N.groupnorm_train_bwd_workspace_bytes(dtype, n, s, c, groups)
+        nbytes = _bwd_bytes(dtype, n, s, c, groups)
         N.groupnorm_train_bwd(x, dy.contiguous(), dtype, mean.contiguous(), rstd.contiguous(),
                               w.contiguous(), b.contiguous(), wb, dx, dw, db,
                               _workspace(nbytes, x), nbytes, n, s, c, groups, s_n, s_s, code)

@@ -151,7 +151,8 @@ SHAPES = [(1, 1, 64, 1), (3, 1, 256, 4), (2, 7, 8, 1), (2, 37, 64, 64), (3, 33, 
           (7, 257, 96, 6), (1, 1023, 640, 32), (2, 1500, 72, 8), (1, 4096, 320, 32),
           (1, 9000, 128, 32), (300, 5, 64, 8)]
 # streamed: samples past a cluster's shared memory, several turns, wide slabs
-LARGE = [(1, 70001, 64, 4), (9, 70001, 64, 4), (1, 20011, 520, 8), (1, 301, 2048, 1)]
+LARGE = [(1, 70001, 64, 4), (13, 70001, 64, 4), (1, 20011, 520, 8), (1, 301, 2048, 1),
+         (1, 350001, 128, 32)]
 
 
 def too_wide(dtype, c, groups):
@@ -196,6 +197,8 @@ def test_streamed(n, s, c, groups, dtype):
     assert not plans[1]["on_chip"]
     if n > 1:
         assert not plans[0]["on_chip"] and plans[0]["units"] < n * c // plans[0]["channels"]
+    if s > 300000:  # a sample too large for one turn
+        assert plans[1]["units"] < c // plans[1]["channels"]
     got = check_fwd(x, w, b, groups, "silu")
     grads = check_bwd(dy, x, w, b, groups, "silu")
     assert all(torch.equal(p, q) for p, q in zip(got, R.groupnorm_fwd(x, w, b, groups, EPS, "silu")))
