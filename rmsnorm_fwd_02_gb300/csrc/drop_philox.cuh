@@ -48,22 +48,19 @@ __device__ __forceinline__ bool drop_keep_hi(const DropParams& d, uint32_t w) {
   return w > d.drop_below;
 }
 
-// A group's keep bits, element j in bit j (all set when nothing is dropped).
-__device__ __forceinline__ uint32_t drop_keep8(const DropParams& d, const uint4& b) {
-  uint32_t m = d.active ? 0u : 0xffu;
+// The masks of a group's four words of 16-bit elements (all ones under a kept element, zeros
+// under a dropped one).
+__device__ __forceinline__ uint4 drop_masks(const DropParams& d, const uint4& b) {
+  const uint32_t all = d.active ? 0u : 0xffffffffu;
   const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+  uint32_t m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (drop_keep_lo(d, w[i])) m |= 1u << (2 * i);
-    if (drop_keep_hi(d, w[i])) m |= 2u << (2 * i);
+    m[i] = drop_keep_hi(d, w[i]) ? 0xffff0000u : 0u;
+    if (drop_keep_lo(d, w[i])) m[i] |= 0x0000ffffu;
+    m[i] |= all;
   }
-  return m;
-}
-
-// The mask of word i (elements 2i and 2i + 1 in its halves) of a group of 16-bit elements
-// under keep bits m.
-__device__ __forceinline__ uint32_t drop_word_mask(uint32_t m, int i) {
-  return ((m >> (2 * i)) & 1u ? 0x0000ffffu : 0u) | ((m >> (2 * i)) & 2u ? 0xffff0000u : 0u);
+  return make_uint4(m[0], m[1], m[2], m[3]);
 }
 
 }  // namespace rmsn

@@ -415,14 +415,16 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   }
 }
 
-constexpr int kFinishCols = 32, kFinishSlices = 32;
+constexpr int kFinishCols = 32;
 
-// dw_c and db_c: column t of the [rows][2 C] sums, 32 slices of rows a column, each added in
-// row order (loads a few rows ahead) and then in slice order, with TwoSum's error terms beside.
-__global__ void __launch_bounds__(kFinishCols* kFinishSlices)
+// dw_c and db_c: column t of the [rows][2 C] sums.  kSlices slices of rows a column, each added
+// in row order (loads a few rows ahead), then joined pairwise in slice order; TwoSum keeps the
+// additions' errors beside.  Few rows take eight slices: the joins are what such a call waits on.
+template <int kSlices>
+__global__ void __launch_bounds__(kFinishCols* kSlices)
     gn_finish_kernel(const float* __restrict__ cols, float* __restrict__ dw,
                      float* __restrict__ db, int64_t rows, int C) {
-  __shared__ float sh[kFinishSlices][kFinishCols + 1], se[kFinishSlices][kFinishCols + 1];
+  __shared__ float sh[kSlices][kFinishCols], se[kSlices][kFinishCols];
   const int x = threadIdx.x % kFinishCols, y = threadIdx.x / kFinishCols;
   const int t = blockIdx.x * kFinishCols + x;
   pdl_wait_prior_grid();
@@ -434,8 +436,8 @@ __global__ void __launch_bounds__(kFinishCols* kFinishSlices)
     sum = r;
   };
   if (t < 2 * C) {
-    const int64_t end = rows * (y + 1) / kFinishSlices;
-    int64_t r = rows * y / kFinishSlices;
+    const int64_t end = rows * (y + 1) / kSlices;
+    int64_t r = rows * y / kSlices;
     const float* p = cols + r * 2 * C + t;
     constexpr int kU = 8;
     for (; r + kU <= end; r += kU, p += static_cast<int64_t>(kU) * 2 * C) {
@@ -449,14 +451,17 @@ __global__ void __launch_bounds__(kFinishCols* kFinishSlices)
   }
   sh[y][x] = sum;
   se[y][x] = err;
-  __syncthreads();
-  if (y == 0 && t < 2 * C) {
-    for (int i = 1; i < kFinishSlices; ++i) {
-      err += se[i][x];
-      add(sh[i][x]);
+#pragma unroll
+  for (int stride = kSlices / 2; stride > 0; stride >>= 1) {
+    __syncthreads();
+    if (y < stride) {
+      err += se[y + stride][x];
+      add(sh[y + stride][x]);
+      sh[y][x] = sum;
+      se[y][x] = err;
     }
-    (t < C ? dw : db)[t < C ? t : t - C] = sum + err;
   }
+  if (y == 0 && t < 2 * C) (t < C ? dw : db)[t < C ? t : t - C] = sum + err;
 }
 
 namespace {
@@ -490,9 +495,11 @@ cudaError_t launch_gn_bwd(const GnArgs& a, int dtype, int act, cudaStream_t st) 
 cudaError_t launch_gn_finish(const float* cols, float* dw, float* db, int64_t rows, int C,
                              cudaStream_t st) {
   void* args[] = {&cols, &dw, &db, &rows, &C};
-  return launch_pdl(reinterpret_cast<const void*>(&gn_finish_kernel),
-                    dim3(static_cast<unsigned>((2 * C + kFinishCols - 1) / kFinishCols)),
-                    dim3(kFinishCols * kFinishSlices), 0, st, args);
+  const bool few = rows <= 64;
+  const void* fn = few ? reinterpret_cast<const void*>(&gn_finish_kernel<8>)
+                       : reinterpret_cast<const void*>(&gn_finish_kernel<32>);
+  return launch_pdl(fn, dim3(static_cast<unsigned>((2 * C + kFinishCols - 1) / kFinishCols)),
+                    dim3(static_cast<unsigned>(kFinishCols * (few ? 8 : 32))), 0, st, args);
 }
 
 }  // namespace gnorm

@@ -428,10 +428,9 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
           f2 wl[4];
           wvec(v, c, wl);
           uint32_t o[4], od[4];
-          uint32_t k8 = 0u;
+          uint4 keep = make_uint4(0u, 0u, 0u, 0u);
           if constexpr (kDrop)
-            k8 = drop_keep8(a.drop,
-                            drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
+            keep = drop_masks(a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 x2 = bf2_to_f2(u4_get(xv, q));
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
             if constexpr (kDh) d = f2_add(d, bf2_to_f2(u4_get(hv, q)));
             o[q] = f2_to_bf2(d);
             if constexpr (kDrop)
-              od[q] = f2_to_bf2(f2_mul(d, f2_splat(a.drop.scale))) & drop_word_mask(k8, q);
+              od[q] = f2_to_bf2(f2_mul(d, f2_splat(a.drop.scale))) & u4_get(keep, q);
             dyx[q] = f2_mul(d2, x2);
             if constexpr (!kTm) {
               // dw: running sum of the exact products dy*x*rs_hi with a Fast2Sum

@@ -49,14 +49,19 @@ __device__ __forceinline__ uint4 residual_sum8(const uint4& u, const uint4& q) {
 
 // h = BF16(keep * x_in * scale + residual) for one 16-byte vector: dropped halves of x_in's
 // words are cleared (so an infinity or NaN there does not pass), then one fma an element.
-__device__ __forceinline__ uint4 dropped_sum8(const uint4& u, const uint4& q, uint32_t keep,
+__device__ __forceinline__ uint4 dropped_sum8(const uint4& u, const uint4& q, const uint4& keep,
                                               f2 scale) {
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    r[i] = f2_to_bf2(f2_fma(bf2_to_f2(u4_get(u, i) & drop_word_mask(keep, i)), scale,
+    r[i] = f2_to_bf2(f2_fma(bf2_to_f2(u4_get(u, i) & u4_get(keep, i)), scale,
                             bf2_to_f2(u4_get(q, i))));
   return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Orders this thread's stores to shared memory before later bulk copies into it.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Launch bounds per shape class (rmsn_launch.h): kFwdPair, at most 256 consumers (G*NTg)
@@ -65,8 +70,9 @@ __device__ __forceinline__ uint4 dropped_sum8(const uint4& u, const uint4& q, ui
 // Narrow rows use sub-warp groups of 8 or 16 lanes (several rows a warp, reduced by
 // shuffles alone).
 //
-// kDrop (with kRes): phase A draws the row's keep bits, a byte a vector, and carries them to
-// phase B of the same row in registers, so each block of the generator is computed once.
+// kDrop (with kRes): phase A leaves h in the staged x's place for phase B of the same thread, so
+// each block of the generator is computed once; a proxy fence orders those stores before the
+// bulk copy that refills the stage.
 template <int VPT, int kCls, bool kFp32W, bool kRes, bool kDrop>
 __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_per_sm(kCls))
     rmsn_fwd_kernel(const std::conditional_t<kDrop, FwdDropArgs, FwdArgs> a) {
@@ -150,8 +156,6 @@ __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_
   const int g0 = red_smem ? g : (tid & ~31) / NTg;
   const int32_t ng = (r1 - r0 > g0) ? (r1 - r0 - g0 + G - 1) / G : 0;
 
-  constexpr int kKeepWords = kDrop ? (VPT + 3) / 4 : 1;  // four vectors' keep bytes a word
-  uint32_t keep[kKeepWords] = {}, keep_prev[kKeepWords] = {};
   f2 scale2 = f2_splat(1.f);
   uint2 ctr = make_uint2(0u, 0u);
   if constexpr (kDrop) {
@@ -164,19 +168,12 @@ __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_
   uint32_t ph = 0;            // no division by the runtime ring depth)
   for (int32_t j = 0; j <= ng; ++j) {
     float part = 0.f;
-    if constexpr (kDrop) {
-#pragma unroll
-      for (int i = 0; i < kKeepWords; ++i) {
-        keep_prev[i] = keep[i];
-        keep[i] = 0u;
-      }
-    }
     // ---- phase A, row j: this thread's partial sum of squares (and h, residual form) ----
     if (j < ng) {
       const int32_t row = r0 + j * G + g;
       const int s = s_cur;
       mbar_wait_bounded(&full[s], ph, abort_flag, a.err, kErrConsumerWait);
-      const __nv_bfloat16* xs = ring + s * stage_elems + static_cast<size_t>(g) * H;
+      __nv_bfloat16* xs = ring + s * stage_elems + static_cast<size_t>(g) * H;
       f2 ss0 = f2_splat(0.f), ss1 = f2_splat(0.f);  // two chains, fixed combine order
       if (row < r1) {
 #pragma unroll
@@ -187,10 +184,11 @@ __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_
             if constexpr (kRes) {
               const uint4 q = lds128(xs + static_cast<size_t>(G) * H + c * 8);
               if constexpr (kDrop) {
-                const uint32_t k8 = drop_keep8(
-                    a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
-                keep[v >> 2] |= k8 << (8 * (v & 3));
-                u = dropped_sum8(u, q, k8, scale2);
+                u = dropped_sum8(u, q,
+                                 drop_masks(a.drop, drop_block(a.drop, ctr,
+                                                               static_cast<uint64_t>(row) * NV + c)),
+                                 scale2);
+                stg128(xs + c * 8, u);
               } else {
                 u = residual_sum8(u, q);
               }
@@ -226,15 +224,11 @@ __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_
         hv[v] = make_uint4(0u, 0u, 0u, 0u);
         if (valid && c < NV) {
           hv[v] = lds128(xs + c * 8);
-          if constexpr (kRes) {
-            const uint4 q = lds128(xs + static_cast<size_t>(G) * H + c * 8);
-            if constexpr (kDrop)
-              hv[v] = dropped_sum8(hv[v], q, (keep_prev[v >> 2] >> (8 * (v & 3))) & 0xffu, scale2);
-            else
-              hv[v] = residual_sum8(hv[v], q);
-          }
+          if constexpr (kRes && !kDrop)
+            hv[v] = residual_sum8(hv[v], lds128(xs + static_cast<size_t>(G) * H + c * 8));
         }
       }
+      if constexpr (kDrop) fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);  // this warp has its vectors of the stage
       float ss = ss_carry;

@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kSmallThreads)
         if constexpr (kDh)
           hv = *reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(row) * H + c * 8);
         uint32_t o[4], od[4];
-        uint32_t k8 = 0u;
+        uint4 keep = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (kDrop)
-          k8 = drop_keep8(a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
+          keep = drop_masks(a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f2 gw = f2_mul(bf2_to_f2(u4_get(dv[v], q)), wv[v][q]);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kSmallThreads)
           if constexpr (kDh) d = f2_add(d, bf2_to_f2(u4_get(hv, q)));
           o[q] = f2_to_bf2(d);
           if constexpr (kDrop)
-            od[q] = f2_to_bf2(f2_mul(d, f2_splat(a.drop.scale))) & drop_word_mask(k8, q);
+            od[q] = f2_to_bf2(f2_mul(d, f2_splat(a.drop.scale))) & u4_get(keep, q);
         }
         stg128(a.dx + static_cast<size_t>(row) * H + c * 8, make_uint4(o[0], o[1], o[2], o[3]));
         if constexpr (kDrop)
