@@ -346,3 +346,16 @@ def test_side_stream():
     for i in range(8):
         want = R.dropout_fwd(want, 0.1, 3, i)
     assert torch.equal(y, want)
+
+
+def test_rmsnorm_dropout_elements_past_32_bits():
+    T, H, p = (1 << 20) + 9, 4096, 0.5
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_()
+    res = torch.empty_like(x).normal_()
+    w = torch.ones(H, device=DEV)
+    y, rstd, h = R.rmsnorm_dropout_fwd(x, res, w, p, 5, 6)
+    assert torch.equal(h[-64:], R.dropout_fwd(x, p, 5, 6, residual=res)[-64:])
+    k = torch.from_numpy(OD.keep(64 * H, p, 5, 6, (T - 64) * H)).to(DEV).view(64, H)
+    del x, res
+    dx, dres, _ = R.rmsnorm_dropout_bwd(y, h, rstd, w, p, 5, 6)
+    assert torch.equal(dx[-64:] != 0, k & (dres[-64:] != 0))

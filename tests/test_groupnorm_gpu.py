@@ -459,3 +459,41 @@ def test_block_of_all_the_operators():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(g, e) for g, e in zip(captured, got))
+
+
+def test_elements_past_32_bits():
+    # 3.2e9 elements (and byte offsets past 2^32): the last sample as when it is alone
+    n, s, c, groups = 3, 1 << 20, 1024, 32
+    x = torch.empty(n, s, c, dtype=BF, device=DEV).normal_()
+    dy = torch.empty_like(x).normal_()
+    w, b = 1 + 0.1 * randn(1, c), 0.1 * randn(2, c)
+    y, mean, rstd = R.groupnorm_fwd(x, w, b, groups, act="silu")
+    y1, mean1, rstd1 = R.groupnorm_fwd(x[2:], w, b, groups, act="silu")
+    dx, dw, db = R.groupnorm_bwd(dy, x, mean, rstd, w, b, groups, "silu")
+    parts = [R.groupnorm_bwd(dy[i:i + 1], x[i:i + 1], mean[i:i + 1], rstd[i:i + 1], w, b, groups,
+                             "silu") for i in range(n)]
+    # the same sums in other orders: 2^-24 a step, well under a bf16 rounding; an output differs
+    # where that tips it, by one bf16 step (2^-7 of the value, 2^-20 of the scale near zero)
+    assert (mean[2:] - mean1).abs().max() < 1e-6 and (rstd[2:] / rstd1 - 1).abs().max() < 1e-5
+    for at in (0, s // 2, s - 4096):
+        part = slice(at, at + 4096)
+        for got, want in ((y[2, part], y1[0, part]), (dx[2, part], parts[2][0][0, part])):
+            got, want = got.float(), want.float()
+            assert ((got - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -20).all()
+    for got, i in ((dw, 1), (db, 2)):
+        want = sum(p[i].double() for p in parts)
+        # n * s terms of about one each: sums of absolute values near n s, in 2^-24 steps
+        assert (got.double() - want).abs().max() < 64 * U * n * s
+
+
+def test_strides_past_32_bits():
+    buf = torch.empty((1 << 32) + 64 * 64, dtype=BF, device=DEV)
+    x = buf.as_strided((2, 64, 64), (1 << 32, 64, 1))
+    x.copy_(randn(1, 2, 64, 64))
+    w, b = 1 + 0.1 * randn(2, 64), 0.1 * randn(3, 64)
+    got = R.groupnorm_fwd(x, w, b, 8)
+    want = R.groupnorm_fwd(x.contiguous(), w, b, 8)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    for p, q in zip(R.groupnorm_bwd(want[0], x, *got[1:], w, b, 8),
+                    R.groupnorm_bwd(want[0], x.contiguous(), *got[1:], w, b, 8)):
+        assert torch.equal(p, q)
