@@ -28,21 +28,17 @@ __device__ __forceinline__ float rcp_approx(float a) {
   return r;
 }
 
-// s = 1 / (1 + exp(-z)) of pairs, to a few FP32 roundings.  A reciprocal takes the
-// special-function unit twice as long as an exponential, so the two values of a pair share one
-// (1/a = b * 1/(ab)).  exp(-z) is held to 2^62, which keeps ab finite and leaves a sigmoid below
-// 2^-62 there; the smaller of a NaN and 62 is 62, so a NaN (it stays in z) does not reach the
-// pair's other value.
+// s = 1 / (1 + exp(-z)) of pairs, to a few FP32 roundings; far below zero exp(-z) is infinite and
+// s is 0.  (Two values can share a reciprocal, 1/a = b * 1/(ab), if exp(-z) is held to 2^62 so
+// that ab stays finite: the clamp costs what the reciprocal saves, 2 % either way, and leaves
+// z * 2^-62 where the product should vanish.)
 template <int kPairs>
 __device__ __forceinline__ void sigmoid_vec(const f2 (&z)[kPairs], f2 (&s)[kPairs]) {
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
     const f2 t = f2_mul(z[i], f2_splat(-1.44269504088896340736f));
-    const f2 d = f2_add(f2_make(ex2_approx(fminf(f2_lo(t), 62.f)),
-                                ex2_approx(fminf(f2_hi(t), 62.f))),
-                        f2_splat(1.f));
-    const float r = rcp_approx(f2_lo(d) * f2_hi(d));
-    s[i] = f2_make(r * f2_hi(d), r * f2_lo(d));
+    const f2 d = f2_add(f2_make(ex2_approx(f2_lo(t)), ex2_approx(f2_hi(t))), f2_splat(1.f));
+    s[i] = f2_make(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
   }
 }
 
@@ -73,12 +69,14 @@ __device__ __forceinline__ void act_vec(f2 (&z)[kPairs]) {
 // dy becomes dy * act'(z).
 template <int kAct, int kPairs>
 __device__ __forceinline__ void act_grad_vec(const f2 (&z)[kPairs], f2 (&dy)[kPairs]) {
-  if constexpr (kAct == GROUPNORM_ACT_SILU) {  // s + z s (1 - s)
+  if constexpr (kAct == GROUPNORM_ACT_SILU) {  // s + z (s - s^2)
     f2 s[kPairs];
     sigmoid_vec(z, s);
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      dy[i] = f2_mul(dy[i], f2_fma(f2_mul(z[i], s[i]), f2_sub(f2_splat(1.f), s[i]), s[i]));
+    for (int i = 0; i < kPairs; ++i) {
+      const f2 v = f2_fma(f2_mul(s[i], f2_splat(-1.f)), s[i], s[i]);
+      dy[i] = f2_mul(dy[i], f2_fma(z[i], v, s[i]));
+    }
   } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i)
