@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       float* run = m.run + 2 * (half * s.cs + c);  // Kahan's running sum over the samples
       const float y = __fsub_rn(v, run[1]);
       const float r = __fadd_rn(run[0], y);
-      run[1] = __fsub_rn(__fsub_rn(r, run[0]), y);
+      run[1] = isinf(r) ? 0.f : __fsub_rn(__fsub_rn(r, run[0]), y);
       run[0] = r;
     });
     // the cluster's: an octet of threads a group, a CTA a thread
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kFinishCols* kSlices)
       se[y][x] = err;
     }
   }
-  if (y == 0 && t < 2 * C) (t < C ? dw : db)[t < C ? t : t - C] = sum + err;
+  if (y == 0 && t < 2 * C) (t < C ? dw : db)[t < C ? t : t - C] = isinf(sum) ? sum : sum + err;
 }
 
 namespace {

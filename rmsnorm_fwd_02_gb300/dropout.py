@@ -21,8 +21,9 @@ backward: autograd refuses a step changed in between).  Calls whose masks have t
 independent need different seeds, or different offset + step.
 
 dropout_*: contiguous CUDA tensors of any shape, bfloat16, float16 or float32; residual has x's
-shape and dtype.  rmsnorm_dropout_*: as rmsnorm_fwd with a residual; h is contiguous.  All
-tensors of a call are on one device.
+shape and dtype.  rmsnorm_dropout_*: as rmsnorm_fwd with a residual; h is contiguous.  The
+kernels read whole 16-byte vectors: an x that starts between two is refused, a gradient (or
+dropout_fwd's residual) is copied first.  All tensors of a call are on one device.
 """
 from __future__ import annotations
 
@@ -56,6 +57,13 @@ def _like(x: torch.Tensor, name: str, t):
         raise ValueError(f"{name} must have shape {tuple(x.shape)} and dtype {x.dtype}")
 
 
+def _flat(t):
+    """t, or a copy, contiguous and at a 16-byte boundary: a gradient can be a slice of another
+    tensor that starts anywhere."""
+    t = t.contiguous()
+    return t.clone(memory_format=torch.contiguous_format) if t.data_ptr() & 15 else t
+
+
 def _generator(p, seed, offset, step, x):
     p = float(p)
     if not 0.0 <= p <= 1.0:
@@ -84,7 +92,7 @@ def dropout_fwd(x, p, seed, offset=0, step=None, residual=None):
     if residual is not None:
         _like(x, "residual", residual)
         _same_device(x, residual)
-        residual = residual.contiguous()
+        residual = _flat(residual)
     y = torch.empty_like(x)
     with _on(x):
         N.dropout_train_fwd(x, residual, y, dtype, x.numel(), *gen)
@@ -94,7 +102,7 @@ def dropout_fwd(x, p, seed, offset=0, step=None, residual=None):
 def dropout_bwd(dy, p, seed, offset=0, step=None):
     dtype = _activation(dy, "dy")
     gen = _generator(p, seed, offset, step, dy)
-    dy = dy.contiguous()
+    dy = _flat(dy)
     dx = torch.empty_like(dy)
     with _on(dy):
         N.dropout_train_bwd(dy, dx, dtype, dy.numel(), *gen)
@@ -150,13 +158,13 @@ def rmsnorm_dropout_bwd(dy, h, rstd, w, p, seed, offset=0, step=None, determinis
     _like(h, "dy", dy)
     if dh is not None:
         _like(h, "dh", dh)
-        dh = dh.contiguous()
+        dh = _flat(dh)
     if rstd.shape != h.shape[:-1] or rstd.dtype != torch.float32:
         raise ValueError(f"rstd must have shape {tuple(h.shape[:-1])} and dtype float32")
     if w.shape != (H,):
         raise ValueError(f"w must have shape ({H},)")
     _same_device(h, dy, dh, rstd, w)
-    dy = dy.contiguous()
+    dy = _flat(dy)
     w = w.contiguous()
     dx = torch.empty_like(h)
     dres = torch.empty_like(h)

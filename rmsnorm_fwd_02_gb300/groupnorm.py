@@ -7,10 +7,11 @@ outputs and workspace with torch, then calls the C ABI (include/groupnorm_train.
 
 x is a CUDA bfloat16, float16 or float32 tensor [N, ..., C] with the channels last (an
 [N, C, H, W] tensor in torch's channels_last format is x.permute(0, 2, 3, 1) here); N and the
-merged places between may be strided, in whole 16-byte steps.  C is a multiple of 8 and of
-groups, up to 4096.  w and b are both bfloat16, float16 or float32 [C].  act is "none", "silu"
-or "gelu" (the exact form).  y, dx have x's shape and dtype and are contiguous; mean and rstd
-are float32 [N, groups]; dw, db float32 [C].  All results are bit-reproducible.
+merged places between may be strided, in whole 16-byte steps from a 16-byte boundary on.  C is
+a multiple of 8 and of groups, up to 4096.  w and b are both bfloat16, float16 or float32 [C].
+act is "none", "silu" or "gelu" (the exact form).  y, dx have x's shape and dtype and are
+contiguous; mean and rstd are float32 [N, groups]; dw, db float32 [C].  All results are
+bit-reproducible.
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .dropout import _DTYPES, _activation, _like, _on, _same_device
+from .dropout import _DTYPES, _activation, _flat, _like, _on, _same_device
 
 EPS = 1e-5
 
@@ -104,7 +105,7 @@ def groupnorm_bwd(dy, x, mean, rstd, w, b, groups, act="none"):
     db = torch.empty_like(dw)
     with _on(x):
         nbytes = _bwd_bytes(dtype, n, s, c, groups)
-        N.groupnorm_train_bwd(x, dy.contiguous(), dtype, mean.contiguous(), rstd.contiguous(),
+        N.groupnorm_train_bwd(x, _flat(dy), dtype, mean.contiguous(), rstd.contiguous(),
                               w.contiguous(), b.contiguous(), wb, dx, dw, db,
                               _workspace(nbytes, x), nbytes, n, s, c, groups, s_n, s_s, code)
     return dx, dw, db

@@ -117,6 +117,41 @@ def test_shapes_and_empty_tensors():
     assert torch.equal(R.dropout_bwd(t.t(), 0.5, 1), R.dropout_bwd(t.t().contiguous(), 0.5, 1))
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_tensors_at_any_address(dtype):
+    # a gradient that is a slice of another tensor starts anywhere: the same values
+    at = lambda t: torch.cat([t.new_zeros(1), t])[1:]  # noqa: E731
+    x, res = (normal(i, 1003, dtype=dtype) for i in (1, 2))
+    assert at(x).is_contiguous() and at(x).data_ptr() % 16
+    assert torch.equal(R.dropout_fwd(x, 0.3, 4, residual=at(res)),
+                       R.dropout_fwd(x, 0.3, 4, residual=res))
+    assert torch.equal(R.dropout_bwd(at(x), 0.3, 4), R.dropout_bwd(x, 0.3, 4))
+    x.requires_grad_()
+    y = torch.cat([res[:5], R.dropout_train(x, 0.3, 4)])
+    g = normal(3, 1008, dtype=dtype)
+    y.backward(g)
+    assert torch.equal(x.grad, R.dropout_bwd(g[5:].clone(), 0.3, 4))
+
+
+def test_rmsnorm_dropout_gradients_at_any_address():
+    at = lambda t: torch.cat([t.new_zeros(5), t.flatten()])[5:].view_as(t)  # noqa: E731
+    x, res, dy, dh, w = rms_case(300, 264, 8, torch.float32)
+    y, rstd, h = R.rmsnorm_dropout_fwd(x, res, w, 0.2, 6)
+    for p, q in zip(R.rmsnorm_dropout_bwd(at(dy), h, rstd, w, 0.2, 6, dh=at(dh)),
+                    R.rmsnorm_dropout_bwd(dy, h, rstd, w, 0.2, 6, dh=dh)):
+        assert torch.equal(p, q)
+
+
+def test_residual_that_is_x():
+    x = normal(5, 777)
+    x.requires_grad_()
+    y = R.dropout_train(x, 0.4, 9, residual=x)
+    y.backward(torch.ones_like(y))
+    assert torch.equal(y.detach(), R.dropout_fwd(x.detach(), 0.4, 9, residual=x.detach().clone()))
+    one = R.dropout_bwd(torch.ones_like(y), 0.4, 9)
+    assert torch.equal(x.grad, one + 1)
+
+
 def test_dropout_autograd():
     x = normal(4, 33, 65).requires_grad_()
     r = normal(5, 33, 65).requires_grad_()

@@ -437,6 +437,57 @@ def test_two_streams_at_once():
             assert all(torch.equal(p, q) for p, q in zip(got[1:], grads[i]))
 
 
+def test_two_graphs_at_once():
+    # each has its own workspace; the streamed form's grids wait for each other's SMs at most
+    cases = [case(60 + i, 2, 70001, 64, BF) for i in range(2)]
+
+    def step(x, dy, w, b):
+        y, mean, rstd = R.groupnorm_fwd(x, w, b, 4, act="silu")
+        return (y,) + R.groupnorm_bwd(dy, x, mean, rstd, w, b, 4, "silu")
+
+    want = [step(*c) for c in cases]
+    torch.cuda.synchronize()
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in cases]
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(step(*c))
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for p, q in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(p, q))
+
+
+@pytest.mark.parametrize("n,s", [(2, 300), (6000, 3), (2, 70001)])
+def test_an_infinite_gradient_stays_infinite_in_its_sums(n, s):
+    # one channel's gradient overflows: its db is infinite, dw too, the other channels' as before
+    x, dy, w, b = case(70, n, s, 64, FP)
+    _, mean, rstd = R.groupnorm_fwd(x, w, b, 8)
+    want = R.groupnorm_bwd(dy, x, mean, rstd, w, b, 8)
+    dy[0, 1, 5] = float("inf")
+    got = R.groupnorm_bwd(dy, x, mean, rstd, w, b, 8)
+    xhat = (x[0, 1, 5] - mean[0, 0]).sign()
+    assert got[2][5] == float("inf") and got[1][5] == float("inf") * xhat
+    rest = torch.arange(64, device=DEV) != 5
+    for g, e in zip(got[1:], want[1:]):
+        assert torch.equal(g[rest], e[rest])
+
+
+def test_gradient_at_any_address():
+    x, dy, w, b = case(71, 2, 50, 64, BF)
+    _, mean, rstd = R.groupnorm_fwd(x, w, b, 8)
+    off = torch.cat([dy.new_zeros(3), dy.flatten()])[3:].view_as(dy)
+    assert off.is_contiguous() and off.data_ptr() % 16
+    for p, q in zip(R.groupnorm_bwd(off, x, mean, rstd, w, b, 8),
+                    R.groupnorm_bwd(dy, x, mean, rstd, w, b, 8)):
+        assert torch.equal(p, q)
+    with pytest.raises(N.RmsnError):
+        R.groupnorm_fwd(off, w, b, 8)
+
+
 def test_block_of_all_the_operators():
     """A residual block as a training step runs it, eagerly and captured: group norm with SiLU,
     dropout, a projection, dropout with the residual RMSNorm; gradients against the same block
