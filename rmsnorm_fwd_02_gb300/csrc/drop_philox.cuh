@@ -38,6 +38,13 @@ __device__ __forceinline__ uint4 drop_block(const DropParams& d, uint2 c, uint64
   return make_uint4(a0, a1, a2, a3);
 }
 
+// The eight-element group of vector c of a row of `vecs` vectors (row and vecs below 2^31; in
+// 32-bit factors, which takes fewer registers than a 64-bit product).
+__device__ __forceinline__ uint64_t drop_group(int32_t row, int vecs, int c) {
+  return static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(vecs) +
+         static_cast<uint32_t>(c);
+}
+
 // Whether elements 2i (lo) and 2i+1 (hi) of a group are kept, from the block's word i.
 // drop_below = 65536 t - 1 (modulo 2^32): for 1 <= t <= 65536 a 16-bit number u is at least
 // t exactly when u * 65536 > drop_below, and the bits under an upper half do not matter.

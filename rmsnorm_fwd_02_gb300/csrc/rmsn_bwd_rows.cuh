@@ -100,8 +100,11 @@ struct RowSums {
 // kDrop: the row's gradient (total, dh included) is the residual's, written to a.dx; the
 // gradient of the added branch before its dropout, keep * scale * total rounded once from
 // FP32, goes to a.dx_drop, with the keep bits drawn here again.
-template <int VPT, int kCls, bool kFp32W, bool kDh, bool kRc, bool kDrop>
-__global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_per_sm(kCls))
+//
+// kSlim: a build for CTAs of at most bwd_slim_threads threads.
+template <int VPT, int kCls, bool kFp32W, bool kDh, bool kRc, bool kDrop, bool kSlim>
+__global__ void __launch_bounds__(kSlim ? bwd_slim_threads(VPT) : bwd_max_threads(kCls, VPT),
+                                  bwd_design_blocks_per_sm(kCls))
     rmsn_bwd_rows_kernel(const std::conditional_t<kDrop, BwdDropArgs, BwdArgs> a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int NT = kDh ? 3 : 2;  // staged tensors: x, dy [, dh]
@@ -421,6 +424,9 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
         if constexpr (kTm) tmem_ld16(tm + 16u * v, tv);
         f2 dyx[4];
         if (live) {
+          uint4 keep = make_uint4(0u, 0u, 0u, 0u);  // before the loads: fewer live registers
+          if constexpr (kDrop)
+            keep = drop_masks(a.drop, drop_block(a.drop, ctr, drop_group(row, NV, c)));
           const uint4 xv = lds128_at(st + 16u * c);
           const uint4 dv = lds128_at(st + dy_off + 16u * c);
           uint4 hv = make_uint4(0u, 0u, 0u, 0u);
@@ -428,9 +434,6 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
           f2 wl[4];
           wvec(v, c, wl);
           uint32_t o[4], od[4];
-          uint4 keep = make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (kDrop)
-            keep = drop_masks(a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 x2 = bf2_to_f2(u4_get(xv, q));
@@ -636,14 +639,30 @@ __global__ void __launch_bounds__(bwd_max_threads(kCls, VPT), bwd_design_blocks_
 // instantiates only its own builds.  (bwd_shape gives 1-vector lanes the narrow class, 2-
 // and 4-vector threads the multi, tensor-memory or wide class, 3-vector threads the multi
 // or tensor-memory class.)
+template <int VPT, int kCls, bool kRc, bool kDrop, bool kSlim = false>
+const void* rows_kernel_of(bool fp32w, bool dh) {
+  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+  return fp32w ? (dh ? fn(&rmsn_bwd_rows_kernel<VPT, kCls, true, true, kRc, kDrop, kSlim>)
+                     : fn(&rmsn_bwd_rows_kernel<VPT, kCls, true, false, kRc, kDrop, kSlim>))
+               : (dh ? fn(&rmsn_bwd_rows_kernel<VPT, kCls, false, true, kRc, kDrop, kSlim>)
+                     : fn(&rmsn_bwd_rows_kernel<VPT, kCls, false, false, kRc, kDrop, kSlim>));
+}
 template <bool kRc, bool kDrop = false>
 const void* pick_rows_kernel(const Shape& s, bool fp32w, bool dh) {
-  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-#define RMSN_PICK(V, C)                                                               \
-  (fp32w ? (dh ? fn(&rmsn_bwd_rows_kernel<V, C, true, true, kRc, kDrop>)              \
-               : fn(&rmsn_bwd_rows_kernel<V, C, true, false, kRc, kDrop>))            \
-         : (dh ? fn(&rmsn_bwd_rows_kernel<V, C, false, true, kRc, kDrop>)             \
-               : fn(&rmsn_bwd_rows_kernel<V, C, false, false, kRc, kDrop>)))
+  // The dropout builds work on more values at a time than the others; bounds nearer the CTA's
+  // own threads let the compiler order them better (65536 rows: H = 4096 with dh 467 -> 409 us,
+  // without 380 -> 341; H = 1536 with dh 174 -> 166; H = 512 with dh 63.6 -> 61.5).
+  if constexpr (kDrop) {
+    if (s.threads <= bwd_slim_threads(s.vpt)) {
+      if (s.cls == kBwdMulti && s.vpt == 3)
+        return rows_kernel_of<3, kBwdMulti, kRc, true, true>(fp32w, dh);
+      if (s.cls == kBwdMulti && s.vpt == 4)
+        return rows_kernel_of<4, kBwdMulti, kRc, true, true>(fp32w, dh);
+      if (s.cls == kBwdTm && s.vpt == 4)
+        return rows_kernel_of<4, kBwdTm, kRc, true, true>(fp32w, dh);
+    }
+  }
+#define RMSN_PICK(V, C) rows_kernel_of<V, C, kRc, kDrop>(fp32w, dh)
   if (s.cls == kBwdTm)
     return s.vpt == 2 ? RMSN_PICK(2, kBwdTm)
                       : (s.vpt == 3 ? RMSN_PICK(3, kBwdTm) : RMSN_PICK(4, kBwdTm));

@@ -185,8 +185,7 @@ __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_
               const uint4 q = lds128(xs + static_cast<size_t>(G) * H + c * 8);
               if constexpr (kDrop) {
                 u = dropped_sum8(u, q,
-                                 drop_masks(a.drop, drop_block(a.drop, ctr,
-                                                               static_cast<uint64_t>(row) * NV + c)),
+                                 drop_masks(a.drop, drop_block(a.drop, ctr, drop_group(row, NV, c))),
                                  scale2);
                 stg128(xs + c * 8, u);
               } else {

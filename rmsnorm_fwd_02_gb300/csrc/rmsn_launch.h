@@ -224,6 +224,9 @@ __host__ __device__ constexpr int bwd_tm_cols(int cons_warps, int vpt) {
 // minimum), a compile-time property of the shape class.
 constexpr int bwd_design_blocks_per_sm(int cls) { return cls == kBwdNarrow ? 2 : 1; }
 
+// Most threads of the CTAs that the dropout backward has slim builds for (rmsn_bwd_rows.cuh).
+constexpr int bwd_slim_threads(int vpt) { return vpt == 3 ? 480 : 416; }
+
 // Threads a backward CTA of the class may have (its launch bounds' maximum).
 constexpr int bwd_max_threads(int cls, int vpt) {
   return kProducerThreads +

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         uint32_t o[4], od[4];
         uint4 keep = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (kDrop)
-          keep = drop_masks(a.drop, drop_block(a.drop, ctr, static_cast<uint64_t>(row) * NV + c));
+          keep = drop_masks(a.drop, drop_block(a.drop, ctr, drop_group(row, NV, c)));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f2 gw = f2_mul(bf2_to_f2(u4_get(dv[v], q)), wv[v][q]);
