@@ -28,6 +28,7 @@ dropout_fwd's residual) is copied first.  All tensors of a call are on one devic
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -37,6 +38,31 @@ from .ops import EPS, _view, _wdtype
 
 _DTYPES = {torch.bfloat16: N.DROPOUT_BF16, torch.float32: N.DROPOUT_FP32,
            torch.float16: N.DROPOUT_FP16}
+
+
+# torch's allocation of a CUDA tensor past the dispatcher, where this torch has it: through
+# torch.empty, the allocations of a small call take longer than its launch (three of them and
+# the launch 16 us, against 10).
+try:
+    _empty_strided = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    def _empty_strided(shape, stride, dtype):
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
+
+@functools.lru_cache(maxsize=4096)
+def _layout(shape):
+    """shape and its contiguous strides as plain tuples."""
+    stride, n = [], 1
+    for k in reversed(shape):
+        stride.append(n)
+        n *= k if k > 1 else 1
+    return tuple(shape), tuple(reversed(stride))
+
+
+def _empty(shape, dtype: torch.dtype) -> torch.Tensor:
+    """An uninitialized contiguous tensor on the current device."""
+    return _empty_strided(*_layout(shape), dtype)
 
 
 def _on(x: torch.Tensor):
@@ -93,8 +119,8 @@ def dropout_fwd(x, p, seed, offset=0, step=None, residual=None):
         _like(x, "residual", residual)
         _same_device(x, residual)
         residual = _flat(residual)
-    y = torch.empty_like(x)
     with _on(x):
+        y = _empty(x.shape, x.dtype)
         N.dropout_train_fwd(x, residual, y, dtype, x.numel(), *gen)
     return y
 
@@ -103,8 +129,8 @@ def dropout_bwd(dy, p, seed, offset=0, step=None):
     dtype = _activation(dy, "dy")
     gen = _generator(p, seed, offset, step, dy)
     dy = _flat(dy)
-    dx = torch.empty_like(dy)
     with _on(dy):
+        dx = _empty(dy.shape, dy.dtype)
         N.dropout_train_bwd(dy, dx, dtype, dy.numel(), *gen)
     return dx
 
@@ -140,10 +166,10 @@ def rmsnorm_dropout_fwd(x, residual, w, p, seed, offset=0, step=None, eps=EPS):
         raise ValueError(f"w must have shape ({H},)")
     _same_device(x, residual, w)
     w = w.contiguous()
-    y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    h = torch.empty_like(y)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     with _on(x):
+        y = _empty(x.shape, torch.bfloat16)
+        h = _empty(x.shape, torch.bfloat16)
+        rstd = _empty(x.shape[:-1], torch.float32)
         N.rmsnorm_dropout_train_fwd(x, residual, w, _wdtype(w), y, h, rstd, T, nh, H, s_tok,
                                     s_head, float(eps), *gen)
     return y, rstd, h
@@ -166,12 +192,12 @@ def rmsnorm_dropout_bwd(dy, h, rstd, w, p, seed, offset=0, step=None, determinis
     _same_device(h, dy, dh, rstd, w)
     dy = _flat(dy)
     w = w.contiguous()
-    dx = torch.empty_like(h)
-    dres = torch.empty_like(h)
-    dw = torch.empty(H, dtype=torch.float32, device=h.device)
     with _on(h):
+        dx = _empty(h.shape, torch.bfloat16)
+        dres = _empty(h.shape, torch.bfloat16)
+        dw = _empty((H,), torch.float32)
         nbytes = N.rmsnorm_train_bwd_workspace_bytes(T, nh, H, deterministic)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=h.device) if nbytes else None
+        ws = _empty((nbytes,), torch.uint8) if nbytes else None
         N.rmsnorm_dropout_train_bwd(h, dy, dh, rstd.contiguous(), w, _wdtype(w), dx, dres, dw,
                                     ws, nbytes, T, nh, H, *gen, deterministic)
     return dx, dres, dw

@@ -22,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .dropout import _DTYPES, _activation, _flat, _like, _on, _same_device
+from .dropout import _DTYPES, _activation, _empty, _flat, _like, _on, _same_device
 
 EPS = 1e-5
 
@@ -74,20 +74,20 @@ _bwd_bytes = functools.lru_cache(maxsize=4096)(
     lambda *shape: N.groupnorm_train_bwd_workspace_bytes(*shape))
 
 
-def _workspace(nbytes: int, x: torch.Tensor):
-    return torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+def _workspace(nbytes: int):
+    return _empty((nbytes,), torch.uint8) if nbytes else None
 
 
 def groupnorm_fwd(x, w, b, groups, eps=EPS, act="none"):
     dtype, n, s, c, s_n, s_s = _places(x, groups)
     wb, code = _params(x, w, b, c), _act(act)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    mean = torch.empty((n, groups), dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
     with _on(x):
+        y = _empty(x.shape, x.dtype)
+        mean = _empty((n, groups), torch.float32)
+        rstd = _empty((n, groups), torch.float32)
         nbytes = _fwd_bytes(dtype, n, s, c, groups)
         N.groupnorm_train_fwd(x, dtype, w.contiguous(), b.contiguous(), wb, y, mean, rstd,
-                              _workspace(nbytes, x), nbytes, n, s, c, groups, s_n, s_s,
+                              _workspace(nbytes), nbytes, n, s, c, groups, s_n, s_s,
                               float(eps), code)
     return y, mean, rstd
 
@@ -100,14 +100,14 @@ def groupnorm_bwd(dy, x, mean, rstd, w, b, groups, act="none"):
         if t.shape != (n, groups) or t.dtype != torch.float32:
             raise ValueError(f"{name} must have shape ({n}, {groups}) and dtype float32")
     _same_device(x, dy, mean, rstd)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = torch.empty(c, dtype=torch.float32, device=x.device)
-    db = torch.empty_like(dw)
     with _on(x):
+        dx = _empty(x.shape, x.dtype)
+        dw = _empty((c,), torch.float32)
+        db = _empty((c,), torch.float32)
         nbytes = _bwd_bytes(dtype, n, s, c, groups)
         N.groupnorm_train_bwd(x, _flat(dy), dtype, mean.contiguous(), rstd.contiguous(),
                               w.contiguous(), b.contiguous(), wb, dx, dw, db,
-                              _workspace(nbytes, x), nbytes, n, s, c, groups, s_n, s_s, code)
+                              _workspace(nbytes), nbytes, n, s, c, groups, s_n, s_s, code)
     return dx, dw, db
 
 
