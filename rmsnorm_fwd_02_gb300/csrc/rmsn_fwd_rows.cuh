@@ -73,6 +73,8 @@ __device__ __forceinline__ void fence_proxy_async() {
 // kDrop (with kRes): phase A leaves h in the staged x's place for phase B of the same thread, so
 // each block of the generator is computed once; a proxy fence orders those stores before the
 // bulk copy that refills the stage.
+// (30720 rows of 6144: 267 us with the masks carried between the phases as bits, 235 with h left
+// in place, 94 % of a plain copy's rate.)
 template <int VPT, int kCls, bool kFp32W, bool kRes, bool kDrop>
 __global__ void __launch_bounds__(fwd_max_threads(kCls, VPT), fwd_design_blocks_per_sm(kCls))
     rmsn_fwd_kernel(const std::conditional_t<kDrop, FwdDropArgs, FwdArgs> a) {
