@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       ColumnSums<T, kAct> sum;
       sum.clear();
       ring.run(o.cnt, [&](uint32_t slot) {
-        sum.add(q, lds128_at(slot), lds128_at(slot + kRingSlots * stride));
+        sum.add(q, lds128_at(slot), lds128_at(slot + Ring<2>::kSlots * stride));
       });
       __syncthreads();  // red takes the rings' place
       float* cols = a.cols + (o.n * s.chunks + o.chunk) * 2 * a.C + o.slab * s.cs;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         T* po = static_cast<T*>(a.out) + place() + (o.cnt - 1) * dstep;
         ring.run(o.cnt, [&](uint32_t slot) {  // dx is not read here again: it leaves L2 first
           __stcs(reinterpret_cast<uint4*>(po),
-                 dx_vec<T, kAct>(q, t, lds128_at(slot), lds128_at(slot + kRingSlots * stride)));
+                 dx_vec<T, kAct>(q, t, lds128_at(slot), lds128_at(slot + Ring<2>::kSlots * stride)));
           po -= dstep;
         });
       }

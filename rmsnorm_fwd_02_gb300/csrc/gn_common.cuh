@@ -109,6 +109,10 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait_n() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 // Waits until at most `left` (0 .. 3) of this thread's latest groups are in flight.
 __device__ __forceinline__ void cp_async_wait(int left) {
   if (left >= 3)
@@ -285,11 +289,11 @@ __device__ __forceinline__ void set_piece(Owner& o, const GnArgs& a, int u0, int
 }
 
 // A thread's own copies through its ring: kTensors 16-byte vectors a place (tensor t's slots
-// kRingSlots strides behind tensor t - 1's), kRingPlaces places a copy group, kRingGroups - 1
-// groups on their way while one is used.
-constexpr int kRingSlots = kRingGroups * kRingPlaces;
+// kSlots strides behind tensor t - 1's), kRingPlaces places a copy group, kGroups - 1 groups on
+// their way while one is used.
 template <int kTensors>
 struct Ring {
+  static constexpr int kGroups = ring_groups(kTensors), kSlots = ring_slots(kTensors);
   uint32_t slot;           // this thread's first slot (shared window)
   uint32_t stride;         // bytes from slot to slot
   const unsigned char* p[kTensors];
@@ -299,7 +303,7 @@ struct Ring {
   __device__ __forceinline__ void copy(uint32_t d) {
 #pragma unroll
     for (int t = 0; t < kTensors; ++t) {
-      cp_async_16(d + t * kRingSlots * stride, p[t]);
+      cp_async_16(d + t * kSlots * stride, p[t]);
       p[t] += step[t];
     }
   }
@@ -312,12 +316,12 @@ struct Ring {
   }
   __device__ __forceinline__ void start() {
 #pragma unroll
-    for (int g = 0; g + 1 < kRingGroups; ++g) issue(slot + g * kRingPlaces * stride);
+    for (int g = 0; g + 1 < kGroups; ++g) issue(slot + g * kRingPlaces * stride);
   }
   // f(its slot) for each of the thread's cnt places in order
   template <typename F>
   __device__ __forceinline__ void run(int cnt, F f) {
-    const uint32_t group = kRingPlaces * stride, end = slot + kRingSlots * stride;
+    const uint32_t group = kRingPlaces * stride, end = slot + kSlots * stride;
     uint32_t rd = slot, wr = end - group;
     int i = 0;
     for (; left >= kRingPlaces; left -= kRingPlaces, i += kRingPlaces) {  // whole groups
@@ -325,7 +329,7 @@ struct Ring {
       for (int j = 0; j < kRingPlaces; ++j) copy(wr + j * stride);
       cp_async_commit();
       wr = wr + group == end ? slot : wr + group;
-      cp_async_wait(kRingGroups - 1);
+      cp_async_wait_n<kGroups - 1>();
 #pragma unroll
       for (int j = 0; j < kRingPlaces; ++j) f(rd + j * stride);
       rd = rd + group == end ? slot : rd + group;
@@ -333,7 +337,7 @@ struct Ring {
     for (; i < cnt; i += kRingPlaces) {
       issue(wr);
       wr = wr + group == end ? slot : wr + group;
-      cp_async_wait(kRingGroups - 1);
+      cp_async_wait_n<kGroups - 1>();
 #pragma unroll
       for (int j = 0; j < kRingPlaces; ++j)
         if (i + j < cnt) f(rd + j * stride);

@@ -67,13 +67,21 @@ constexpr int kMaxCluster = 8;
 constexpr int max_threads(bool wide) { return wide ? kWideThreads : kThreads; }
 constexpr int min_ctas(bool wide) { return wide ? 1 : kCtas; }
 
-// Streamed: each thread's copies run through a ring of kRingGroups groups of kRingPlaces
-// places; on chip, `iters` places of each of `stages` samples are staged.
-constexpr int kRingGroups = 4, kRingPlaces = 2;
+// Streamed: each thread's copies run through a ring of ring_groups groups of kRingPlaces places;
+// on chip, `iters` places of each of `stages` samples are staged.  (Forward, bf16: 4 groups 135 us
+// at 8 x 65536 x 256 and 90.8 at 64 x 4096 x 320, 6 groups 129 and 87.6, 8 groups 130 and 86.4 but
+// 4 % more on the smallest streamed calls; backward, two tensors: 4 groups 227 and 155, 6 groups
+// 235 and 159.)
+constexpr int kRingPlaces = 2;
+inline __host__ __device__ constexpr int ring_groups(int tensors) { return tensors == 1 ? 6 : 4; }
+inline __host__ __device__ constexpr int ring_slots(int tensors) {
+  return ring_groups(tensors) * kRingPlaces;
+}
 // Bytes of one staged sample, or of the ring.
 inline __host__ __device__ size_t gn_stage_bytes(const GnShape& s, bool bwd) {
-  return static_cast<size_t>(bwd ? 2 : 1) * (s.on_chip ? s.iters : kRingGroups * kRingPlaces) *
-         s.threads * 16;
+  const int tensors = bwd ? 2 : 1;
+  return static_cast<size_t>(tensors) * (s.on_chip ? s.iters : ring_slots(tensors)) * s.threads *
+         16;
 }
 // Shared memory of the kernels behind the staged vectors, in floats:
 //   w, b  cs parameters each
