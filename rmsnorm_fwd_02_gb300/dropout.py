@@ -65,16 +65,20 @@ def _empty(shape, dtype: torch.dtype) -> torch.Tensor:
     return _empty_strided(*_layout(shape), dtype)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(x: torch.Tensor):
     """A context in which x's device is the current one (the C ABI works on that)."""
-    if x.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if x.get_device() == torch.cuda.current_device():
+        return _HERE
     return torch.cuda.device(x.device)
 
 
 def _same_device(x: torch.Tensor, *others):
+    dev = x.get_device()
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
 
 

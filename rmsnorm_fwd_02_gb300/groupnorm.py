@@ -33,16 +33,17 @@ def _places(x: torch.Tensor, groups: int):
     dtype = _activation(x, "x")
     if x.dim() < 2:
         raise ValueError("x must be [N, ..., C]")
-    n, c = x.shape[0], x.shape[-1]
-    s = math.prod(x.shape[1:-1])
+    shape = x.shape
+    n, c = shape[0], shape[-1]
+    s = shape[1] if len(shape) == 3 else math.prod(shape[1:-1])
     if n > 0 and s == 0:
         raise ValueError("x has samples without places")
     if groups < 1 or c % groups:
         raise ValueError(f"{c} channels do not divide into {groups} groups")
-    if x.stride(-1) != 1 and c > 1:
-        raise ValueError("the channels must be contiguous (channels last)")
     if x.is_contiguous():
         return dtype, n, s, c, s * c, c
+    if x.stride(-1) != 1 and c > 1:
+        raise ValueError("the channels must be contiguous (channels last)")
     try:
         v = x.view(n, s, c)
     except RuntimeError:
@@ -96,9 +97,9 @@ def groupnorm_bwd(dy, x, mean, rstd, w, b, groups, act="none"):
     dtype, n, s, c, s_n, s_s = _places(x, groups)
     wb, code = _params(x, w, b, c), _act(act)
     _like(x, "dy", dy)
-    for name, t in (("mean", mean), ("rstd", rstd)):
+    for t in (mean, rstd):
         if t.shape != (n, groups) or t.dtype != torch.float32:
-            raise ValueError(f"{name} must have shape ({n}, {groups}) and dtype float32")
+            raise ValueError(f"mean and rstd must have shape ({n}, {groups}) and dtype float32")
     _same_device(x, dy, mean, rstd)
     with _on(x):
         dx = _empty(x.shape, x.dtype)
