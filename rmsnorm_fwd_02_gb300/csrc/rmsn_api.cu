@@ -49,16 +49,28 @@ constexpr int kDetSMs = 152;
 constexpr int kMinStagesPerCta = 1;
 
 std::mutex g_mu;
-std::unordered_map<uint64_t, int> g_occ;       // (device, fn, threads, smem) -> blocks/SM
-std::unordered_map<uint64_t, bool> g_prepared; // (device, fn) -> smem attribute set
+// A kernel on a device, and for its occupancy a launch shape (0 where only the kernel counts).
+struct KernelKey {
+  int dev;
+  const void* fn;
+  uint64_t threads_smem;
+  bool operator==(const KernelKey& o) const {
+    return dev == o.dev && fn == o.fn && threads_smem == o.threads_smem;
+  }
+};
+struct KernelKeyHash {
+  size_t operator()(const KernelKey& k) const;
+};
+std::unordered_map<KernelKey, int, KernelKeyHash> g_occ;        // -> blocks/SM
+std::unordered_map<KernelKey, bool, KernelKeyHash> g_prepared;  // -> smem attribute set
 unsigned* g_err_ptr[kMaxDevices] = {};
 int g_sms[kMaxDevices] = {};
 
-uint64_t key(int dev, const void* fn, uint64_t extra) {
-  uint64_t h = reinterpret_cast<uint64_t>(fn);
-  h ^= (static_cast<uint64_t>(dev) + 0x9e3779b97f4a7c15ull) + (h << 6) + (h >> 2);
-  h ^= extra + 0x9e3779b97f4a7c15ull + (h << 6) + (h >> 2);
-  return h;
+size_t KernelKeyHash::operator()(const KernelKey& k) const {
+  uint64_t h = reinterpret_cast<uint64_t>(k.fn);
+  h ^= (static_cast<uint64_t>(k.dev) + 0x9e3779b97f4a7c15ull) + (h << 6) + (h >> 2);
+  h ^= k.threads_smem + 0x9e3779b97f4a7c15ull + (h << 6) + (h >> 2);
+  return static_cast<size_t>(h);
 }
 
 size_t shared_bytes(const Shape& s, int H, bool bwd) {
@@ -320,7 +332,7 @@ cudaError_t prepare_kernel(const void* fn, size_t smem) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t k = key(dev, fn, 0);
+  const KernelKey k{dev, fn, 0};
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (g_prepared.count(k)) return cudaSuccess;
@@ -337,7 +349,7 @@ cudaError_t prepare_kernel(const void* fn, size_t smem) {
 int blocks_per_sm(const void* fn, int threads, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  const uint64_t k = key(dev, fn, (static_cast<uint64_t>(threads) << 32) ^ smem);
+  const KernelKey k{dev, fn, (static_cast<uint64_t>(threads) << 32) | smem};
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_occ.find(k);
