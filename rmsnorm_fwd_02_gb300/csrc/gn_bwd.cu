@@ -310,7 +310,9 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const Smem m = carve(smem, s, true);
-  const int tid = threadIdx.x, l = tid & 31;
+  const int tid = threadIdx.x;
+  const int join_log2 = join_lanes_log2(s), jl = tid & ((1 << join_log2) - 1);
+  const int gs_up = join_groups(s, join_log2);
   const int64_t step = s.lanes * a.s_s, dstep = static_cast<int64_t>(s.lanes) * a.C;
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
   const uint32_t stride = 16u * s.threads;
@@ -378,18 +380,19 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       Ring<2> ring = ring_of(true);
       ring.start();
       load_piece();
-      for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
+      for (int g0 = tid >> join_log2; g0 < gs_up; g0 += s.threads >> join_log2) {
+        const int g = min(g0, s.gs - 1);  // whole warps: the shuffles need them
         const float2* p = a.part + o.n * s.chunks * a.G + o.slab * s.gs + g;
         float sa = 0.f, sb = 0.f;
 #pragma unroll 8
-        for (int k = l; k < s.chunks; k += 32) {  // not through L1 (gn_fwd.cu)
+        for (int k = jl; k < s.chunks; k += 1 << join_log2) {  // not through L1 (gn_fwd.cu)
           const float2 x = __ldcg(p + static_cast<int64_t>(k) * a.G);
           sa += x.x;
           sb += x.y;
         }
-        sa = warp_allsum(sa);
-        sb = warp_allsum(sb);
-        if (l == 0) {
+        sa = join_sum(sa, join_log2);
+        sb = join_sum(sb, join_log2);
+        if (jl == 0 && g0 < s.gs) {
           m.gm[2 * g] = sa / total;
           m.gm[2 * g + 1] = sb / total;
         }

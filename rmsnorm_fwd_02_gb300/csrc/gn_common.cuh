@@ -166,6 +166,22 @@ __device__ __forceinline__ float across_octets(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
+// Streamed: the lanes of a warp that join the chunks of a group: 32, fewer where the slab has more
+// groups than the CTA has warps, so that a warp waits for several groups' loads at once.
+__device__ __forceinline__ int join_lanes_log2(const GnShape& s) {
+  const int warps = s.threads >> 5;
+  return s.gs <= warps ? 5 : (s.gs <= 2 * warps ? 4 : 3);
+}
+// The slab's groups, up to whole warps of joining lanes.
+__device__ __forceinline__ int join_groups(const GnShape& s, int lanes_log2) {
+  const int a_warp = 32 >> lanes_log2;
+  return (s.gs + a_warp - 1) & ~(a_warp - 1);
+}
+__device__ __forceinline__ float join_sum(float v, int lanes_log2) {
+  for (int o = 1 << (lanes_log2 - 1); o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 __device__ __forceinline__ f2 across_octets(f2 v) {
   return f2_make(across_octets(f2_lo(v)), across_octets(f2_hi(v)));
 }

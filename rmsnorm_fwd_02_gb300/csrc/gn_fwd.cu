@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
 // Streamed.  Each turn's pieces (a unit's chunk each) are dealt out to the grid.  A CTA sums its
 // pieces of turn t + 1 before it waits for every CTA's sums of turn t and writes its pieces of
 // that one, so the grid's barrier and the CTAs' unevenness hide behind a turn's sums; L2 holds
-// both turns.  Before the output a unit's chunks combine (a warp a group, the chunks over its
-// lanes).  A piece is written from its last place back, so that of a turn larger than L2 the
+// both turns.  Before the output a unit's chunks combine (some lanes of a warp a group, the
+// chunks over them).  A piece is written from its last place back, so that of a turn larger than L2 the
 // part still held is read first.  Every unit has its own place in part.
 template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   extern __shared__ __align__(128) unsigned char smem[];
   const GnShape& s = a.s;
   const Smem m = carve(smem, s, false);
-  const int tid = threadIdx.x, l = tid & 31;
+  const int tid = threadIdx.x;
+  const int join_log2 = join_lanes_log2(s), jl = tid & ((1 << join_log2) - 1);
+  const int gs_up = join_groups(s, join_log2);
   const int64_t step = s.lanes * a.s_s, ystep = static_cast<int64_t>(s.lanes) * a.C;
   const float total = static_cast<float>(a.S) * static_cast<float>(s.cg);
   const float cg = static_cast<float>(s.cg);
@@ -338,23 +340,24 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       __syncthreads();  // the piece before is done with w, b, c0, c1
       // one round trip to memory: the parameters and the chunks' statistics
       load_params(a, m.w, m.b, o.slab);
-      for (int g = tid >> 5; g < s.gs; g += s.threads >> 5) {
+      for (int g0 = tid >> join_log2; g0 < gs_up; g0 += s.threads >> join_log2) {
+        const int g = min(g0, s.gs - 1);  // whole warps: the shuffles need them
         const float2* p = a.part + o.n * s.chunks * a.G + o.slab * s.gs + g;
         // about the first chunk's mean, as in cta_stats; not through L1, which may hold an
         // earlier turn's line
         const float ref = __ldcg(p).x;
         float sum = 0.f, m2 = 0.f;
 #pragma unroll 8
-        for (int k = l; k < s.chunks; k += 32) {
+        for (int k = jl; k < s.chunks; k += 1 << join_log2) {
           const float2 x = __ldcg(p + static_cast<int64_t>(k) * a.G);
           const float d = x.x - ref;
           const float nd = static_cast<float>(s.chunk_base + (k < s.chunk_more ? 1 : 0)) * cg * d;
           sum += nd;
           m2 += __fmaf_rn(nd, d, x.y);
         }
-        sum = warp_allsum(sum);
-        m2 = warp_allsum(m2);
-        if (l == 0) {
+        sum = join_sum(sum, join_log2);
+        m2 = join_sum(m2, join_log2);
+        if (jl == 0 && g0 < s.gs) {
           const float off = sum / total, mean = ref + off;
           m2 = __fmaf_rn(-off, sum, m2);
           const float rstd = __frsqrt_rn(__fadd_rn(clamp_below(m2 / total), a.eps));
