@@ -13,7 +13,8 @@
  *   backward  xhat = (x - mean) * rstd,  dz = dy * act'(z),  g = dz * w_c
  *             dx = rstd * (g - mean(g) - xhat * mean(g * xhat))       (means over the group)
  *             dw_c = sum over n, s of dz * xhat,   db_c = sum over n, s of dz
- *   act       identity; SiLU z / (1 + exp(-z)); GELU z * Phi(z) (the exact form, by erf)
+ *   act       identity; SiLU z / (1 + exp(-z)); GELU z * Phi(z) (the exact form;
+ *             for the 16-bit types Phi is within 2e-7)
  *
  * Statistics, sums and arithmetic are FP32, with one rounding to the output type.  The variance
  * is formed from values shifted by one of their own, so a mean far from zero costs it nothing

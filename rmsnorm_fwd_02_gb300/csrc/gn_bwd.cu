@@ -11,7 +11,7 @@
 // adds them in a fixed order.
 //
 // Measured (SiLU): on chip 5 x 1023 x 640 fp16 15.6 us, two launches; streamed
-// 2 x 262144 x 128 bf16 122 us: x and dy of a sample, 134 MB, are more than L2 gives back, so
+// 2 x 262144 x 128 bf16 118 us: x and dy of a sample, 134 MB, are more than L2 gives back, so
 // both passes read memory, 98.7 us at a copy's rate.
 #include "gn_common.cuh"
 
@@ -59,7 +59,7 @@ struct Consts {
       z[i] = f2_fma(d[i], scale[h + i], bias[h + i]);
       out[i] = VecOf<T>::pair(du, h + i);
     }
-    act_grad_vec<kAct>(z, out);
+    act_grad_vec<T, kAct>(z, out);
   }
 };
 

@@ -51,8 +51,47 @@ __device__ __forceinline__ float gelu_slope(float z) {
                    normal_cdf(z));
 }
 
-// z becomes act(z).
-template <int kAct, int kPairs>
+// For 16-bit outputs, pairs: a = |z|, e = exp(-z^2/2) and q = Phi(-a) = e t R(t) with
+// t = 1 / (1 + 0.35 a).  R is a polynomial fitted to erfcx(a / sqrt 2) / (2 t) for this, keeping
+// the largest (1 + a) e times its error small (least squares, weights raised where the error is
+// largest): q is within 2.5e-8, and 1.5e-7 with the FP32 roundings, and relative to its own size
+// within 2e-5 up to a = 5 -- far below a 16-bit rounding, where 1 + erf loses the tail.  The
+// derivative's phi takes e again.  (erff instead: 1 x 232341 x 96 bf16, backward, 75.8 against
+// 58.4 us; 38 x 979 x 480 bf16, forward, 34.9 against 28.0.  FP32 outputs keep erff.)
+struct NormalTail {
+  f2 a, e, q;
+};
+__device__ __forceinline__ NormalTail normal_tail(f2 z) {
+  NormalTail n;
+  n.a = f2_make(fabsf(f2_lo(z)), fabsf(f2_hi(z)));
+  const f2 d = f2_fma(n.a, f2_splat(0.35f), f2_splat(1.f));
+  const f2 t = f2_make(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
+  const f2 x = f2_mul(f2_mul(z, z), f2_splat(-0.72134752044448170368f));
+  n.e = f2_make(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
+  f2 r = f2_fma(t, f2_splat(0.040748097002506256f), f2_splat(-0.16716481745243073f));
+  r = f2_fma(r, t, f2_splat(0.17960256338119507f));
+  r = f2_fma(r, t, f2_splat(0.03882385790348053f));
+  r = f2_fma(r, t, f2_splat(0.12764227390289307f));
+  r = f2_fma(r, t, f2_splat(0.14100906252861023f));
+  r = f2_fma(r, t, f2_splat(0.13933898508548737f));
+  n.q = f2_mul(f2_mul(r, t), n.e);
+  return n;
+}
+// z Phi(z) = max(z, 0) - a q
+__device__ __forceinline__ f2 gelu_pair(f2 z) {
+  const NormalTail n = normal_tail(z);
+  return f2_sub(f2_make(fmaxf(f2_lo(z), 0.f), fmaxf(f2_hi(z), 0.f)), f2_mul(n.a, n.q));
+}
+__device__ __forceinline__ f2 gelu_slope_pair(f2 z) {
+  const NormalTail n = normal_tail(z);
+  const f2 u = f2_sub(f2_splat(1.f), n.q);
+  const f2 cdf = f2_make(f2_lo(z) < 0.f ? f2_lo(n.q) : f2_lo(u),
+                         f2_hi(z) < 0.f ? f2_hi(n.q) : f2_hi(u));
+  return f2_fma(f2_mul(z, f2_splat(0.39894228040143267794f)), n.e, cdf);
+}
+
+// z becomes act(z); T is the output's type.
+template <typename T, int kAct, int kPairs>
 __device__ __forceinline__ void act_vec(f2 (&z)[kPairs]) {
   if constexpr (kAct == GROUPNORM_ACT_SILU) {
     f2 s[kPairs];
@@ -62,12 +101,14 @@ __device__ __forceinline__ void act_vec(f2 (&z)[kPairs]) {
   } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i)
-      z[i] = f2_make(f2_lo(z[i]) * normal_cdf(f2_lo(z[i])), f2_hi(z[i]) * normal_cdf(f2_hi(z[i])));
+      z[i] = sizeof(T) == 2 ? gelu_pair(z[i])
+                            : f2_make(f2_lo(z[i]) * normal_cdf(f2_lo(z[i])),
+                                      f2_hi(z[i]) * normal_cdf(f2_hi(z[i])));
   }
 }
 
 // dy becomes dy * act'(z).
-template <int kAct, int kPairs>
+template <typename T, int kAct, int kPairs>
 __device__ __forceinline__ void act_grad_vec(const f2 (&z)[kPairs], f2 (&dy)[kPairs]) {
   if constexpr (kAct == GROUPNORM_ACT_SILU) {  // s + z (s - s^2)
     f2 s[kPairs];
@@ -80,7 +121,9 @@ __device__ __forceinline__ void act_grad_vec(const f2 (&z)[kPairs], f2 (&dy)[kPa
   } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i)
-      dy[i] = f2_mul(dy[i], f2_make(gelu_slope(f2_lo(z[i])), gelu_slope(f2_hi(z[i]))));
+      dy[i] = f2_mul(dy[i], sizeof(T) == 2
+                                ? gelu_slope_pair(z[i])
+                                : f2_make(gelu_slope(f2_lo(z[i])), gelu_slope(f2_hi(z[i]))));
   }
 }
 

@@ -66,7 +66,7 @@ struct Consts {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         v[i] = f2_fma(VecOf<T>::plus(u, h + i, nm[h + i]), scale[h + i], bias[h + i]);
-      act_vec<kAct>(v);
+      act_vec<T, kAct>(v);
       z[h] = v[0];
       z[h + 1] = v[1];
     }

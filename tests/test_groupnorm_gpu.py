@@ -302,6 +302,28 @@ def test_activations_far_out(dtype, kind):
     assert dx.isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FP], ids=str)
+def test_gelu_along_its_argument(dtype):
+    # w = 0: z is b, one value a channel; with dy = 1 db is the slope, in FP32
+    c, groups = 4096, 64
+    z = torch.linspace(-12, 12, c, device=DEV)
+    x, w = randn(1, 1, 1, c).to(dtype), torch.zeros(c, device=DEV)
+    y, mean, rstd = R.groupnorm_fwd(x, w, z, groups, act="gelu")
+    dx, dw, db = R.groupnorm_bwd(torch.ones_like(x), x, mean, rstd, w, z, groups, "gelu")
+    z64 = z.double()
+    y64, a = OG.act(z64, "gelu"), z64.abs()
+    # Phi(-a) within 1.5e-7, below a = 5 also within 2e-5 of itself; the rounded exponent adds
+    # 2^-23 z^2 / 2 and the approximate functions 2^-21 (FP32: erf's 2^-22)
+    q = 0.5 * torch.erfc(a / math.sqrt(2))
+    tail = torch.where(a < 5, q * (2e-5 + 2.0 ** -23 * a * a / 2 + 2.0 ** -21), q + 1.5e-7)
+    dq = torch.full_like(q, 2.0 ** -22) if dtype == FP else tail.clamp(max=2e-7)
+    e = a * dq + 2.0 ** -23 * y64.abs()
+    assert ((y[0, 0].double() - y64).abs() <= e + half_step(y64.abs() + e, dtype)).all()
+    # the slope: 1 - Phi's rounding, phi's argument, and dq
+    assert ((db.double() - OG.slope(z64, "gelu")).abs() <= 2e-7 + 2.0 ** -21).all()
+    assert not dx.any()
+
+
 def test_strided_input():
     wide = randn(1, 3, 40, 256).to(BF)
     w, b = 1 + 0.1 * randn(2, 64), 0.1 * randn(3, 64)
