@@ -10,7 +10,7 @@
 // their ramps, cost 5 us each more.)
 //
 // Measured (SiLU): on chip 8 x 4096 x 320 bf16 14.5 us, of which about 5 are the launch's ramp
-// and 6 the bandwidth's; streamed 1 x 262144 x 128 fp32 66 us, where L2 gives back 54 MB of the
+// and 6 the bandwidth's; streamed 1 x 262144 x 128 fp32 66 us, where L2 gives back 58 MB of the
 // 134 and the rest of x is read twice (60 us at a copy's rate).
 //
 // Statistics: each thread sums its channels' values less the first of them, K (sum d and
