@@ -77,10 +77,11 @@ __device__ __forceinline__ NormalTail normal_tail(f2 z) {
   n.q = f2_mul(f2_mul(r, t), n.e);
   return n;
 }
-// z Phi(z) = max(z, 0) - a q
+// z Phi(z) = max(z, 0) - a q (a q is 0 long before the bound on a, which an infinite z needs)
 __device__ __forceinline__ f2 gelu_pair(f2 z) {
   const NormalTail n = normal_tail(z);
-  return f2_sub(f2_make(fmaxf(f2_lo(z), 0.f), fmaxf(f2_hi(z), 0.f)), f2_mul(n.a, n.q));
+  const f2 a = f2_make(fminf(f2_lo(n.a), 1024.f), fminf(f2_hi(n.a), 1024.f));
+  return f2_sub(f2_make(fmaxf(f2_lo(z), 0.f), fmaxf(f2_hi(z), 0.f)), f2_mul(a, n.q));
 }
 __device__ __forceinline__ f2 gelu_slope_pair(f2 z) {
   const NormalTail n = normal_tail(z);

@@ -302,6 +302,16 @@ def test_activations_far_out(dtype, kind):
     assert dx.isfinite().all()
 
 
+@pytest.mark.parametrize("kind", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", [BF, HF, FP], ids=str)
+def test_an_overflowing_norm_is_infinite(dtype, kind):
+    x = torch.zeros(1, 64, 16, device=DEV, dtype=dtype)
+    x[0, ::2] = 1.0
+    w, b = torch.full((16,), 3e38, device=DEV), torch.zeros(16, device=DEV)
+    y, _, _ = R.groupnorm_fwd(x, w, b, 2, act=kind)
+    assert torch.equal(y[0, ::2], torch.full_like(y[0, ::2], float("inf")))
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, FP], ids=str)
 def test_gelu_along_its_argument(dtype):
     # w = 0: z is b, one value a channel; with dy = 1 db is the slope, in FP32
