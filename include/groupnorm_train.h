@@ -14,7 +14,8 @@
  *             dx = rstd * (g - mean(g) - xhat * mean(g * xhat))       (means over the group)
  *             dw_c = sum over n, s of dz * xhat,   db_c = sum over n, s of dz
  *   act       identity; SiLU z / (1 + exp(-z)); GELU z * Phi(z) (the exact form;
- *             for the 16-bit types Phi is within 2e-7)
+ *             for the 16-bit types Phi is within 2e-7, for FP32 Phi(z), z < 0, within 1e-6 of
+ *             itself, so its tail is kept)
  *
  * Statistics, sums and arithmetic are FP32, with one rounding to the output type.  The variance
  * is formed from values shifted by one of their own, so a mean far from zero costs it nothing

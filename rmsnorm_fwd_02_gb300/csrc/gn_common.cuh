@@ -42,25 +42,17 @@ __device__ __forceinline__ void sigmoid_vec(const f2 (&z)[kPairs], f2 (&s)[kPair
   }
 }
 
-__device__ __forceinline__ float normal_cdf(float z) {
-  return 0.5f * (1.f + erff(z * 0.70710678118654752440f));
-}
-__device__ __forceinline__ float gelu_slope(float z) {
-  // Phi(z) + z * phi(z)
-  return __fmaf_rn(z * 0.39894228040143267794f, ex2_approx(z * z * -0.72134752044448170368f),
-                   normal_cdf(z));
-}
-
-// For 16-bit outputs, pairs: a = |z|, e = exp(-z^2/2) and q = Phi(-a) = e t R(t) with
-// t = 1 / (1 + 0.35 a).  R is a polynomial fitted to erfcx(a / sqrt 2) / (2 t) for this, keeping
-// the largest (1 + a) e times its error small (least squares, weights raised where the error is
-// largest): q is within 2.5e-8, and 1.5e-7 with the FP32 roundings, and relative to its own size
-// within 2e-5 up to a = 5 -- far below a 16-bit rounding, where 1 + erf loses the tail.  The
-// derivative's phi takes e again.  (erff instead: 1 x 232341 x 96 bf16, backward, 75.8 against
-// 58.4 us; 38 x 979 x 480 bf16, forward, 34.9 against 28.0.  FP32 outputs keep erff.)
+// GELU, pairs, by the normal distribution's tail: a = |z|, e = exp(-z^2/2) and q = Phi(-a) =
+// e t R(t) with t = 1 / (1 + 0.35 a), R a polynomial fitted to erfcx(a / sqrt 2) / (2 t) for this
+// (least squares, weights raised where the error is largest).  The derivative's phi takes e again.
+// (1 + erf loses the tail: all of it at z = -6 in FP32.)
 struct NormalTail {
   f2 a, e, q;
 };
+// For 16-bit outputs: R keeps the largest (1 + a) e times its error small.  q is within 2.7e-8, and
+// 1.5e-7 with the FP32 roundings, and relative to its own size within 2e-5 up to a = 5 -- far below
+// a 16-bit rounding.  (erff instead: 1 x 232341 x 96 bf16, backward, 75.8 against 58.4 us;
+// 38 x 979 x 480 bf16, forward, 34.9 against 28.0.)
 __device__ __forceinline__ NormalTail normal_tail(f2 z) {
   NormalTail n;
   n.a = f2_make(fabsf(f2_lo(z)), fabsf(f2_hi(z)));
@@ -77,14 +69,55 @@ __device__ __forceinline__ NormalTail normal_tail(f2 z) {
   n.q = f2_mul(f2_mul(r, t), n.e);
   return n;
 }
-// z Phi(z) = max(z, 0) - a q (a q is 0 long before the bound on a, which an infinite z needs)
-__device__ __forceinline__ f2 gelu_pair(f2 z) {
-  const NormalTail n = normal_tail(z);
-  const f2 a = f2_make(fminf(f2_lo(n.a), 1024.f), fminf(f2_hi(n.a), 1024.f));
-  return f2_sub(f2_make(fmaxf(f2_lo(z), 0.f), fmaxf(f2_hi(z), 0.f)), f2_mul(a, n.q));
+// For FP32 outputs: R's relative error is 1.4e-8, and exp's argument is formed to twice FP32's
+// length (a rounded one costs z^2 / 2 roundings of e): q within 2^-20.5 of itself at every a.
+// a ends at 32, where e is 0: a * a stays finite.
+__device__ __forceinline__ NormalTail normal_tail_fp32(f2 z) {
+  constexpr float kLog2e2 = 0.72134752044448170368f;  // log2(e) / 2
+  constexpr float kRest = static_cast<float>(0.72134752044448170368 - double{kLog2e2});
+  NormalTail n;
+  n.a = f2_make(fminf(fabsf(f2_lo(z)), 32.f), fminf(fabsf(f2_hi(z)), 32.f));
+  const f2 d = f2_fma(n.a, f2_splat(0.35f), f2_splat(1.f));
+  const f2 t = f2_make(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
+  const f2 minus = f2_splat(-1.f);
+  const f2 s = f2_mul(n.a, n.a), s_low = f2_fma(n.a, n.a, f2_mul(s, minus));
+  const f2 x = f2_mul(s, f2_splat(-kLog2e2));
+  f2 low = f2_fma(s, f2_splat(-kLog2e2), f2_mul(x, minus));
+  low = f2_fma(s_low, f2_splat(-kLog2e2), low);
+  low = f2_fma(s, f2_splat(-kRest), low);
+  n.e = f2_make(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
+  n.e = f2_fma(f2_mul(low, f2_splat(0.69314718055994530942f)), n.e, n.e);
+  f2 r = f2_fma(t, f2_splat(0.019322199746966362f), f2_splat(-0.10849655419588089f));
+  r = f2_fma(r, t, f2_splat(0.235971599817276f));
+  r = f2_fma(r, t, f2_splat(-0.22601933777332306f));
+  r = f2_fma(r, t, f2_splat(0.06964033335447311f));
+  r = f2_fma(r, t, f2_splat(-0.02842709608376026f));
+  r = f2_fma(r, t, f2_splat(0.04841167479753494f));
+  r = f2_fma(r, t, f2_splat(0.08778508752584457f));
+  r = f2_fma(r, t, f2_splat(0.1225530356168747f));
+  r = f2_fma(r, t, f2_splat(0.13962922990322113f));
+  r = f2_fma(r, t, f2_splat(0.1396297961473465f));
+  n.q = f2_mul(f2_mul(r, t), n.e);
+  return n;
 }
+// z Phi(z) = max(z, 0) - a q (a q is 0 long before the bound on a, which an infinite z needs)
+template <typename T>
+__device__ __forceinline__ f2 gelu_pair(f2 z) {
+  if constexpr (sizeof(T) == 2) {
+    const NormalTail n = normal_tail(z);
+    const f2 a = f2_make(fminf(f2_lo(n.a), 1024.f), fminf(f2_hi(n.a), 1024.f));
+    return f2_sub(f2_make(fmaxf(f2_lo(z), 0.f), fmaxf(f2_hi(z), 0.f)), f2_mul(a, n.q));
+  } else {
+    const NormalTail n = normal_tail_fp32(z);
+    // (a NaN is not below 0 and stays)
+    const f2 up = f2_make(f2_lo(z) < 0.f ? 0.f : f2_lo(z), f2_hi(z) < 0.f ? 0.f : f2_hi(z));
+    return f2_fma(f2_mul(n.a, f2_splat(-1.f)), n.q, up);
+  }
+}
+// Phi(z) + z phi(z)
+template <typename T>
 __device__ __forceinline__ f2 gelu_slope_pair(f2 z) {
-  const NormalTail n = normal_tail(z);
+  const NormalTail n = sizeof(T) == 2 ? normal_tail(z) : normal_tail_fp32(z);
   const f2 u = f2_sub(f2_splat(1.f), n.q);
   const f2 cdf = f2_make(f2_lo(z) < 0.f ? f2_lo(n.q) : f2_lo(u),
                          f2_hi(z) < 0.f ? f2_hi(n.q) : f2_hi(u));
@@ -101,10 +134,7 @@ __device__ __forceinline__ void act_vec(f2 (&z)[kPairs]) {
     for (int i = 0; i < kPairs; ++i) z[i] = f2_mul(z[i], s[i]);
   } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      z[i] = sizeof(T) == 2 ? gelu_pair(z[i])
-                            : f2_make(f2_lo(z[i]) * normal_cdf(f2_lo(z[i])),
-                                      f2_hi(z[i]) * normal_cdf(f2_hi(z[i])));
+    for (int i = 0; i < kPairs; ++i) z[i] = gelu_pair<T>(z[i]);
   }
 }
 
@@ -122,9 +152,7 @@ __device__ __forceinline__ void act_grad_vec(const f2 (&z)[kPairs], f2 (&dy)[kPa
   } else if constexpr (kAct == GROUPNORM_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i)
-      dy[i] = f2_mul(dy[i], sizeof(T) == 2
-                                ? gelu_slope_pair(z[i])
-                                : f2_make(gelu_slope(f2_lo(z[i])), gelu_slope(f2_hi(z[i]))));
+      dy[i] = f2_mul(dy[i], gelu_slope_pair<T>(z[i]));
   }
 }
 
