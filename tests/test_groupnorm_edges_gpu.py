@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import rmsnorm_fwd_02_gb300 as R
-from test_groupnorm_gpu import DEV, randn
+from oracle import groupnorm as OG
+from test_groupnorm_gpu import BF, DEV, EPS, FP, U, case, depth, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,29 @@ def test_fp32_gelu_keeps_its_tail():
     e = (2.0 ** -21 * z64.abs() * phi + 2.0 ** -20 * cdf
          + 2.0 ** -23 * (cdf + z64 * phi).abs())
     assert ((db.double() - (cdf + z64 * phi)).abs() <= e).all()
+
+
+# on chip (several stages, one stage), streamed, one thread a column, 256 lanes of it; threads
+# with up to 256 places
+@pytest.mark.parametrize("n,s,c,groups", [(2, 700, 64, 4), (1, 4096, 320, 32),
+                                          (1, 262144, 128, 32), (1, 100000, 512, 512),
+                                          (1, 20011, 2048, 1), (200, 100, 64, 8), (1, 1023, 8, 1),
+                                          (2, 9, 1024, 4)])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=str)
+@pytest.mark.parametrize("place", [0, 1, -1])
+def test_one_value_far_from_the_others(n, s, c, groups, dtype, place):
+    x, _, w, b = case(17, n, s, c, FP)
+    x[:, place, ::c // groups] = 1000.0
+    x = x.to(dtype)
+    _, mean, rstd = R.groupnorm_fwd(x, w, b, groups)
+    x64 = x.double()
+    m64, r64 = OG.stats(x64, groups, EPS)
+    # One value carries most of a group's sum of squares, and the others are near the values that
+    # sums are shifted by, so nothing larger is ever added up: each of the depth's additions and
+    # the products around them round within U of it; and mean's own error, squared (D U of the
+    # largest value at most, over the s places that one is averaged with).
+    D = depth(x, groups, False)
+    big = x64.view(n, s, groups, -1).abs().amax((1, 3))
+    rel = 2 * (D + 8) * U + (D * U * big * r64).square() / s + 4 * 2.0 ** -22 * m64.abs() * r64
+    err = (rstd.double() - r64).abs() / r64
+    assert (err <= 0.5 * rel + 2.0 ** -22).all(), (err / (0.5 * rel + 2.0 ** -22)).max()
