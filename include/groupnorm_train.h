@@ -20,7 +20,9 @@
  * Statistics, sums and arithmetic are FP32, with one rounding to the output type.  The variance
  * is formed from values shifted by one of their own, so a mean far from zero costs it nothing
  * beyond what FP32 holds of mean itself.  Every order of summation is a function of the shape
- * and dtype alone: results are bit-reproducible run to run and on GPUs of any SM count.
+ * and dtype alone: results are bit-reproducible run to run and on GPUs of any SM count.  A group's
+ * sum of squared deviations has to stay within FP32's range, and its variance, where eps is 0,
+ * within FP32's normal numbers; the backward takes any finite rstd.
  *
  * Layout: x is read through strides (elements): place s of sample n starts at n*s_n + s*s_s,
  * its C channels side by side.  y, dy and dx are contiguous [N, S, C]; mean and rstd [N, G]

@@ -17,11 +17,18 @@
 
 namespace gnorm {
 
+// Whether rstd^2 stays well inside FP32's range (false for NaN).  Past it, groups of values around
+// 1e-20 or 1e20, the factor rstd^2 of dx's last term is applied in two steps.
+__device__ __forceinline__ bool rstd_is_near(float rstd) {
+  return rstd >= 0x1p-40f && rstd <= 0x1p40f;
+}
+
 // A thread's constants for its channels: d = x - mean, z = d * scale + bias, scale = rstd * w.
 template <typename T>
 struct Consts {
   static constexpr int kPairs = VecOf<T>::kPairs;
   f2 nm[kPairs], scale[kPairs], bias[kPairs];
+  bool far;  // some group's rstd is not near
   // w, b: the slab's parameters in shared memory; mean, rstd: the sample's group values, `gap`
   // floats apart, from the slab's first group on; c: the thread's first channel, place r of
   // group g
@@ -31,6 +38,7 @@ struct Consts {
     lds_pairs<kPairs>(b + c, bias);
     float m = mean[gap * g], q = rstd[gap * g];
     float v[2 * kPairs], u[2 * kPairs];
+    far = !rstd_is_near(q);
 #pragma unroll
     for (int j = 0; j < 2 * kPairs; ++j) {
       v[j] = -m;
@@ -40,6 +48,7 @@ struct Consts {
         ++g;
         m = mean[gap * g];
         q = rstd[gap * g];
+        far = far || !rstd_is_near(q);
       }
     }
 #pragma unroll
@@ -64,7 +73,11 @@ struct Consts {
 };
 
 // The group terms of dx = scale * dz + nc1 + d * nc2, with nc1 = -rstd * mean(g) and
-// nc2 = -rstd^2 * mean(g * xhat).
+// nc2 = -rstd^2 * mean(g * xhat); of a far group, dx = scale * dz + nc1 + (d * rstd) * nc2 with
+// nc2 = -rstd * mean(g * xhat).
+__device__ __forceinline__ float group_nc2(float rstd, float mean) {
+  return (rstd_is_near(rstd) ? -rstd * rstd : -rstd) * mean;
+}
 template <typename T>
 struct GroupTerms {
   static constexpr int kPairs = VecOf<T>::kPairs;
@@ -75,15 +88,35 @@ struct GroupTerms {
   }
 };
 
-template <typename T, int kAct>
+// d of two pairs from channel c of the slab on, times rstd where the group is far; rstd: the groups'
+// values, `gap` floats apart.
+__device__ __forceinline__ void scale_far(const float* rstd, int gap, int cg, int c, f2 (&d)[2]) {
+  int g = c / cg, r = c - g * cg;
+  float v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float q = rstd[gap * g];
+    v[j] = rstd_is_near(q) ? 1.f : q;
+    if (j < 3 && ++r == cg) {
+      r = 0;
+      ++g;
+    }
+  }
+  d[0] = f2_mul(d[0], f2_make(v[0], v[1]));
+  d[1] = f2_mul(d[1], f2_make(v[2], v[3]));
+}
+
+// far(pair, d): what is done to d of two pairs before the group's term
+template <typename T, int kAct, typename F>
 __device__ __forceinline__ uint4 dx_vec(const Consts<T>& k, const GroupTerms<T>& t,
-                                        const uint4& xu, const uint4& du) {
+                                        const uint4& xu, const uint4& du, F far) {
   constexpr int NP = VecOf<T>::kPairs;
   f2 v[NP];
 #pragma unroll
   for (int h = 0; h < NP; h += 2) {
     f2 d[2], dz[2];
     k.template dz<kAct>(xu, du, h, d, dz);
+    far(h, d);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       v[h + i] = f2_fma(dz[i], k.scale[h + i], f2_fma(d[i], t.nc2[h + i], t.nc1[h + i]));
@@ -179,7 +212,7 @@ __device__ __forceinline__ void cta_sums(const Smem& m, const GnShape& s, const 
 // of `lanes` threads.
 __device__ __forceinline__ void set_group(const Smem& m, const GnShape& s, int g, int k, int lanes,
                                           float rstd, float sa, float sb, float total) {
-  const float nc1 = -rstd * (sb / total), nc2 = -rstd * rstd * (sa / total);
+  const float nc1 = -rstd * (sb / total), nc2 = group_nc2(rstd, sa / total);
   for (int i = g * s.cg + k; i < (g + 1) * s.cg; i += lanes) {
     m.c0[i] = nc1;
     m.c1[i] = nc2;
@@ -284,10 +317,20 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       GroupTerms<T> t;
       t.load(m.c0, m.c1, o.c);
       T* po = static_cast<T*>(a.out) + n * a.S * a.C + at0;
-      for_staged2(mine, dy_off, 0, o.cnt, stride, [&](const uint4& xu, const uint4& du) {
-        stg128(po, dx_vec<T, kAct>(q, t, xu, du));
-        po += dstep;
-      });
+      if (!q.far) {
+        for_staged2(mine, dy_off, 0, o.cnt, stride, [&](const uint4& xu, const uint4& du) {
+          stg128(po, dx_vec<T, kAct>(q, t, xu, du, [](int, f2 (&)[2]) {}));
+          po += dstep;
+        });
+      } else {  // (a branch inside the loop costs up to 5 % of small samples)
+        for (int i = 0; i < o.cnt; ++i, po += dstep) {
+          const uint32_t p = mine + i * stride;
+          stg128(po, dx_vec<T, kAct>(q, t, lds128_at(p), lds128_at(p + dy_off),
+                                     [&](int h, f2 (&d)[2]) {
+                                       scale_far(rstd, 1, s.cg, o.c + 2 * h, d);
+                                     }));
+        }
+      }
     }
     if (s.stages == 1) {
       for (int b = 0; b < kBatches; ++b) stage_places(n + s.lanes_n, 0, b * per, (b + 1) * per);
@@ -402,7 +445,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         const int g = c / s.cg;
         const float r = m.ms[2 * g + 1];
         m.c0[c] = -r * m.gm[2 * g + 1];
-        m.c1[c] = -r * r * m.gm[2 * g];
+        m.c1[c] = group_nc2(r, m.gm[2 * g]);
       }
       Consts<T> q;
       if (o.cnt > 0) q.load(m.w, m.b, m.ms, m.ms + 1, 2, s.cg, o.c, og, orr);
@@ -412,8 +455,16 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
         t.load(m.c0, m.c1, o.c);
         T* po = static_cast<T*>(a.out) + place() + (o.cnt - 1) * dstep;
         ring.run(o.cnt, [&](uint32_t slot) {  // dx is not read here again: it leaves L2 first
-          __stcs(reinterpret_cast<uint4*>(po),
-                 dx_vec<T, kAct>(q, t, lds128_at(slot), lds128_at(slot + Ring<2>::kSlots * stride)));
+          const uint4 xu = lds128_at(slot), du = lds128_at(slot + Ring<2>::kSlots * stride);
+          uint4 v;
+          if (__builtin_expect(!q.far, 1)) {
+            v = dx_vec<T, kAct>(q, t, xu, du, [](int, f2 (&)[2]) {});
+          } else {
+            v = dx_vec<T, kAct>(q, t, xu, du, [&](int h, f2 (&d)[2]) {
+              scale_far(m.ms + 1, 2, s.cg, o.c + 2 * h, d);
+            });
+          }
+          __stcs(reinterpret_cast<uint4*>(po), v);
           po -= dstep;
         });
       }

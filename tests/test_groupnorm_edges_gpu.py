@@ -10,7 +10,7 @@ import torch
 
 import rmsnorm_fwd_02_gb300 as R
 from oracle import groupnorm as OG
-from test_groupnorm_gpu import BF, DEV, EPS, FP, U, case, depth, randn
+from test_groupnorm_gpu import BF, DEV, EPS, FP, U, case, check_bwd, depth, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,17 @@ def test_one_value_far_from_the_others(n, s, c, groups, dtype, place):
     rel = 2 * (D + 8) * U + (D * U * big * r64).square() / s + 4 * 2.0 ** -22 * m64.abs() * r64
     err = (rstd.double() - r64).abs() / r64
     assert (err <= 0.5 * rel + 2.0 ** -22).all(), (err / (0.5 * rel + 2.0 ** -22)).max()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=str)
+@pytest.mark.parametrize("kind", ["none", "silu"])
+@pytest.mark.parametrize("n,s,c,groups", [(2, 50, 64, 8), (2, 60, 40, 8), (1, 9000, 128, 32),
+                                          (2, 70001, 64, 4), (700, 3, 64, 8)])
+@pytest.mark.parametrize("log2", [-66, 66])
+def test_gradient_of_groups_of_any_scale(n, s, c, groups, kind, dtype, log2):
+    # rstd^2 passes FP32's range at either end, rstd and dx do not; groups of 1 between them
+    x, dy, w, b = case(19, n, s, c, dtype)
+    scale = torch.ones(c, device=DEV)
+    scale.view(groups, -1)[::2] = 2.0 ** log2
+    x = (x * scale).to(dtype)
+    check_bwd(dy, x, w, b, groups, kind, eps=0.0)
