@@ -78,7 +78,7 @@ int slab_groups(int dtype, int C, int G, int bytes) {
 }
 
 // One launch with the slab on chip: the fewest CTAs a cluster that let two CTAs share an SM
-// (else one), more while the GPU has idle SMs and the CTAs are not small; threads == 0 if a
+// (else one, which plan() takes for one place a sample alone), more while the GPU has idle SMs and the CTAs are not small; threads == 0 if a
 // cluster of kMaxCluster cannot hold the slab.
 GnShape on_chip_shape(int dtype, int64_t N, int64_t S, int C, int G, int gs, bool bwd) {
   GnShape best{};
@@ -143,11 +143,15 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
     }
     if (gs == gs0 || one >= bytes) break;  // no narrower slab
   }
-  if (chip.threads != 0 && chip.smem <= kHalfSmem) {
+  // A backward over one place a sample stays on chip at one CTA an SM too, where the slab's constants
+  // fill half an SM: streamed, it would have a row of sums a sample (65536 x 1 x 4096 bf16, one
+  // group: 6.7 ms against 10.2).
+  const bool one_place = bwd && S == 1;
+  if (chip.threads != 0 && (chip.smem <= kHalfSmem || one_place)) {
     on_chip_loop(&chip, N, bwd);
     // a loop over samples has to have the next ones on their way: at 64 x 4096 x 320 bf16,
     // forward, one stage took 108 us and streaming 90
-    if (chip.lanes_n == N || chip.stages > 1) return chip;
+    if (chip.lanes_n == N || chip.stages > 1 || one_place) return chip;
   }
   // streamed
   int gs = slab_groups(dtype, C, G, kSlabBytes);
@@ -164,7 +168,9 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
     const int64_t turns = ceil_div(N, units / s.slabs);
     units = ceil_div(N, turns) * s.slabs;
   }
-  // (a unit past a cluster's shared memory has 2^15 elements and more, so `all` fits 31 bits)
+  // (`all` fits 31 bits: N * S * C is below 2^40 and a streamed unit has more than 2^9 elements --
+  // up to that, staged vectors, constants and partial sums are below 60 KB, so two CTAs share an
+  // SM and stage several samples each)
   s.units = static_cast<int>(units);
   s.grid = kSMs * min_ctas(s.vecs > kThreads);
   // a piece a CTA, each thread 4 to 256 places
@@ -175,6 +181,10 @@ GnShape plan(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
   s.chunks = static_cast<int>(chunks);
   s.chunk_base = static_cast<int>(S / chunks);
   s.chunk_more = static_cast<int>(S % chunks);
+  // A row of column sums a piece would be more than the piece itself (a few places in a wide slab):
+  // a fixed number of sequences of pieces add theirs up, whatever grid runs them.
+  if (bwd && S * elem_bytes(dtype) < 2 * static_cast<int64_t>(sizeof(float)) && N * chunks > s.grid)
+    s.seqs = s.grid;
   if (units * chunks < s.grid) s.grid = static_cast<int>(units * chunks);
   s.iters = 0;  // nothing stays staged
   s.smem = gn_stats_smem(s, bwd);
@@ -198,13 +208,17 @@ size_t part_bytes(const GnShape& s, int64_t N, int G) {
   const size_t n = static_cast<size_t>(N) * s.chunks * G * sizeof(float2);
   return (n + 15) & ~static_cast<size_t>(15);
 }
+// Rows of column sums, and their bytes (those of sequences have compensations behind them).
 int64_t col_rows(const GnShape& s, int64_t N) {
-  return s.on_chip ? static_cast<int64_t>(s.lanes_n) * s.ctas : N * s.chunks;
+  if (s.on_chip) return static_cast<int64_t>(s.lanes_n) * s.ctas;
+  return s.seqs > 0 ? s.seqs : N * s.chunks;
+}
+size_t col_bytes(const GnShape& s, int64_t N, int C) {
+  return static_cast<size_t>(col_rows(s, N)) * (s.seqs > 0 ? 2 : 1) * 2 * C * sizeof(float);
 }
 size_t workspace_bytes(int dtype, int64_t N, int64_t S, int C, int G, bool bwd) {
   const GnShape s = plan(dtype, N, S, C, G, bwd);
-  return part_bytes(s, N, G) +
-         (bwd ? static_cast<size_t>(col_rows(s, N)) * 2 * C * sizeof(float) : 0);
+  return part_bytes(s, N, G) + (bwd ? col_bytes(s, N, C) : 0);
 }
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -341,7 +355,7 @@ int groupnorm_train_bwd(const void* x, const void* dy, int dtype, const float* m
   if (N > 0) {
     s = plan(dtype, N, S, C, G, true);
     rows = col_rows(s, N);
-    const size_t need = part_bytes(s, N, G) + static_cast<size_t>(rows) * 2 * C * sizeof(float);
+    const size_t need = part_bytes(s, N, G) + col_bytes(s, N, C);
     if (workspace == nullptr || workspace_bytes < need) return RMSN_ERR_WORKSPACE;
   }
   if ((st = rmsn::check_device()) != RMSN_OK) return st;

@@ -7,8 +7,8 @@
 // between the sums and dx where a cluster's shared memory holds them, and are streamed by a
 // cooperative grid, twice through L2, where not.  dz is formed twice from x and dy rather than
 // kept (keeping it in FP32 would double the staged bytes).  The column sums of each CTA (on
-// chip: over all the samples it takes, compensated) go to the workspace, and a finishing kernel
-// adds them in a fixed order.
+// chip, and for pieces of a few places: over all that it takes, compensated; else of each piece)
+// go to the workspace, and a finishing kernel adds them in a fixed order.
 //
 // Measured (SiLU): on chip 5 x 1023 x 640 fp16 15.6 us, two launches; streamed
 // 2 x 262144 x 128 bf16 118 us: x and dy of a sample, 134 MB, are more than L2 gives back, so
@@ -219,6 +219,32 @@ __device__ __forceinline__ void set_group(const Smem& m, const GnShape& s, int g
   }
 }
 
+// Kahan's running sum; an infinite one stays infinite.
+__device__ __forceinline__ void running_add(float* sum, float* comp, float v) {
+  const float s = *sum, y = __fsub_rn(v, *comp);
+  const float r = __fadd_rn(s, y);
+  *comp = isinf(r) ? 0.f : __fsub_rn(__fsub_rn(r, s), y);
+  *sum = r;
+}
+
+// The piece's column sums col [2][cs] into a row of running ones, their compensations `gap` floats
+// behind them: four columns a thread, all of a round's loads on their way together.
+__device__ __forceinline__ void add_to_row(const float* col, float* row, int64_t gap, int C,
+                                           const GnShape& s) {
+#pragma unroll 4
+  for (int i = 4 * threadIdx.x; i < 2 * s.cs; i += 4 * s.threads) {
+    float* p = row + (i < s.cs ? i : C + i - s.cs);
+    float4 sum = *reinterpret_cast<float4*>(p), comp = *reinterpret_cast<float4*>(p + gap);
+    const float4 v = *reinterpret_cast<const float4*>(col + i);
+    running_add(&sum.x, &comp.x, v.x);
+    running_add(&sum.y, &comp.y, v.y);
+    running_add(&sum.z, &comp.z, v.z);
+    running_add(&sum.w, &comp.w, v.w);
+    *reinterpret_cast<float4*>(p) = sum;
+    *reinterpret_cast<float4*>(p + gap) = comp;
+  }
+}
+
 template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     gn_bwd_kernel(const GnArgs a) {
@@ -289,11 +315,8 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       for_staged2(mine, dy_off, 0, o.cnt, stride, add);
     }
     cta_sums(m, s, o, sum, rstd, 1, [&](int half, int c, float v) {
-      float* run = m.run + 2 * (half * s.cs + c);  // Kahan's running sum over the samples
-      const float y = __fsub_rn(v, run[1]);
-      const float r = __fadd_rn(run[0], y);
-      run[1] = isinf(r) ? 0.f : __fsub_rn(__fsub_rn(r, run[0]), y);
-      run[0] = r;
+      float* run = m.run + 2 * (half * s.cs + c);  // over the samples
+      running_add(run, run + 1, v);
     });
     // the cluster's: an octet of threads a group, a CTA a thread
     if (s.ctas > 1) {
@@ -383,31 +406,43 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       m.ms[2 * g + 1] = a.rstd[o.n * a.G + o.slab * s.gs + g];
     }
   };
+  // (a sequence a CTA, unless a smaller grid runs them)
+  const int ways = s.seqs > 0 ? s.seqs : static_cast<int>(gridDim.x);
   auto sum_turn = [&](int u0) {
     const int nu = units_at(u0);
-    for (int v = blockIdx.x; v < nu * s.chunks; v += gridDim.x) {
-      set_piece(o, a, u0, nu, v);
-      Ring<2> ring = ring_of(false);
-      ring.start();
-      load_piece();
-      __syncthreads();
-      Consts<T> q;
-      if (o.cnt > 0) q.load(m.w, m.b, m.ms, m.ms + 1, 2, s.cg, o.c, og, orr);
-      ColumnSums<T, kAct> sum;
-      sum.clear();
-      ring.run(o.cnt, [&](uint32_t slot) {
-        sum.add(q, lds128_at(slot), lds128_at(slot + Ring<2>::kSlots * stride));
-      });
-      __syncthreads();  // red takes the rings' place
-      float* cols = a.cols + (o.n * s.chunks + o.chunk) * 2 * a.C + o.slab * s.cs;
-      cta_sums(m, s, o, sum, m.ms + 1, 2,
-               [&](int half, int c, float val) { cols[half * a.C + c] = val; });
-      __syncthreads();
-      float2* part = a.part + (o.n * s.chunks + o.chunk) * a.G + o.slab * s.gs;
-      for (int g = tid; g < s.gs; g += s.threads)
-        part[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
-    }
+    for (int w = blockIdx.x; w < ways; w += gridDim.x)
+      for (int v = w; v < nu * s.chunks; v += ways) {
+        set_piece(o, a, u0, nu, v);
+        Ring<2> ring = ring_of(false);
+        ring.start();
+        load_piece();
+        __syncthreads();
+        Consts<T> q;
+        if (o.cnt > 0) q.load(m.w, m.b, m.ms, m.ms + 1, 2, s.cg, o.c, og, orr);
+        ColumnSums<T, kAct> sum;
+        sum.clear();
+        ring.run(o.cnt, [&](uint32_t slot) {
+          sum.add(q, lds128_at(slot), lds128_at(slot + Ring<2>::kSlots * stride));
+        });
+        __syncthreads();  // red takes the rings' place
+        const int64_t row = s.seqs > 0 ? w : o.n * s.chunks + o.chunk;
+        float* cols = a.cols + row * 2 * a.C + o.slab * s.cs;
+        cta_sums(m, s, o, sum, m.ms + 1, 2, [&](int half, int c, float val) {
+          if (s.seqs == 0) cols[half * a.C + c] = val;
+        });
+        __syncthreads();
+        if (s.seqs > 0) add_to_row(m.col, cols, static_cast<int64_t>(s.seqs) * 2 * a.C, a.C, s);
+        float2* part = a.part + (o.n * s.chunks + o.chunk) * a.G + o.slab * s.gs;
+        for (int g = tid; g < s.gs; g += s.threads)
+          part[g] = make_float2(m.gm[2 * g], m.gm[2 * g + 1]);
+      }
   };
+  // this CTA's sequences: sums and compensations
+  for (int w = blockIdx.x; w < s.seqs; w += gridDim.x)
+    for (int t = tid; t < 2 * a.C; t += s.threads) {
+      float* p = a.cols + static_cast<int64_t>(w) * 2 * a.C + t;
+      p[0] = p[static_cast<int64_t>(s.seqs) * 2 * a.C] = 0.f;
+    }
 
   auto grid = cooperative_groups::this_grid();
   sum_turn(0);

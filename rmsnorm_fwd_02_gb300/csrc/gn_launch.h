@@ -34,6 +34,7 @@ struct GnShape {
   int units;     // units a turn takes, unit u the slab u % slabs of sample u / slabs
   int chunks;    // the first chunk_more of chunk_base + 1 places, the others of chunk_base
   int chunk_base, chunk_more;
+  int seqs;      // backward: sequences of pieces that share a row of column sums (0: a row a piece)
   int grid;      // CTAs at most
   size_t smem;   // dynamic shared memory
 };
@@ -47,7 +48,8 @@ struct GnArgs {
   float* mean;           // [N, G]; backward: read
   float* rstd;
   float2* part;          // streamed: [N][chunks][G]: (mean, M2), or (sum g*xhat, sum g)
-  float* cols;           // backward: [.][2][C] column sums (dw, then db)
+  float* cols;           // backward: [.][2][C] column sums (dw, then db); of sequences, their
+                         // compensations behind them
   int64_t s_n, s_s;      // x's strides
   int64_t N;
   int64_t S;

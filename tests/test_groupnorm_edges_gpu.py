@@ -10,7 +10,7 @@ import torch
 
 import rmsnorm_fwd_02_gb300 as R
 from oracle import groupnorm as OG
-from test_groupnorm_gpu import BF, DEV, EPS, FP, U, case, check_bwd, depth, randn
+from test_groupnorm_gpu import BF, DEV, EPS, FP, HF, U, case, check_bwd, check_fwd, depth, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,17 @@ def test_gradient_of_groups_of_any_scale(n, s, c, groups, kind, dtype, log2):
     scale.view(groups, -1)[::2] = 2.0 ** log2
     x = (x * scale).to(dtype)
     check_bwd(dy, x, w, b, groups, kind, eps=0.0)
+
+
+# one to three places a sample and every channel in one slab
+@pytest.mark.parametrize("dtype,n,s,c,groups", [
+    (BF, 3000, 1, 2048, 1), (HF, 700, 2, 2048, 1), (BF, 333, 3, 2048, 1), (BF, 1200, 1, 4096, 1),
+    (HF, 500, 2, 4096, 1), (BF, 401, 3, 4096, 1), (BF, 700, 1, 3000, 8), (FP, 900, 1, 2048, 1),
+    (BF, 64, 1, 4096, 1), (BF, 5, 3, 4088, 8)], ids=str)
+def test_few_places_of_wide_slabs(dtype, n, s, c, groups):
+    x, dy, w, b = case(37, n, s, c, dtype)
+    check_fwd(x, w, b, groups, "silu")
+    got = check_bwd(dy, x, w, b, groups, "silu")
+    mean, rstd = (t.float() for t in OG.stats(x.double(), groups, EPS))
+    again = R.groupnorm_bwd(dy, x, mean, rstd, w, b, groups, "silu")
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
