@@ -13,13 +13,14 @@
 // and 6 the bandwidth's; streamed 1 x 262144 x 128 fp32 66 us, where L2 gives back 58 MB of the
 // 134 and the rest of x is read twice (60 us at a copy's rate).
 //
-// Statistics: each thread sums its channels' values less K, the middle one of its first three
-// (sum d and sum d^2 of d = x - K), so neither sum cancels when the mean is far from zero; a
-// column's mean is K + sum d / n and its M2 = sum d^2 - (sum d)^2 / n.  (The first value alone as K:
-// one value a thousand times the others' spread there, as activations at place 0 can be, leaves
-// n (x - K)^2 to cancel -- 2.7e-5 of rstd lost at 1 x 262144 x 128 fp32.)  Means combine weighted by their
-// counts, and M2 about the combined mean: M2 = sum of M2_i + n_i (mean_i - mean)^2 -- from
-// threads to columns, groups, the cluster or the chunks.
+// Statistics: each thread sums its channels' values less K, the middle one of its first three (of
+// kFewPlaces and fewer, the first): sum d and sum d^2 of d = x - K, so neither sum cancels when the
+// mean is far from zero.  A column's mean is K + sum d / n and its M2 = sum d^2 - (sum d)^2 / n.
+// (With the first value as K everywhere, one value a thousand times the others' spread there, as
+// an activation at place 0 can be, leaves n (x - K)^2 to cancel: 2.7e-5 of rstd lost at
+// 1 x 262144 x 128 fp32.)  Means combine weighted by their counts, and M2 about the combined mean:
+// M2 = sum of M2_i + n_i (mean_i - mean)^2 -- from threads to columns, groups, the cluster or the
+// chunks.
 #include "gn_common.cuh"
 
 namespace gnorm {
@@ -32,21 +33,28 @@ __device__ __forceinline__ f2 middle(f2 a, f2 b, f2 c) {
   return f2_make(middle(f2_lo(a), f2_lo(b), f2_lo(c)), middle(f2_hi(a), f2_hi(b), f2_hi(c)));
 }
 
+// Places a thread up to which K is its first value: n (x - K)^2 of so few costs 1e-6 of rstd at
+// most, and small samples feel two loads more (3 % at 1024 x 49 x 512).
+constexpr int kFewPlaces = 8;
+
 template <typename T>
 struct ColumnStats {
   static constexpr int kPairs = VecOf<T>::kPairs;
   f2 nk[kPairs], s[kPairs], q[kPairs];  // -K, sum d, sum d^2
-  // from the thread's first `have` staged places, `stride` bytes apart from `slot` on; one or two
-  // places are taken as they are
-  __device__ __forceinline__ void start(uint32_t slot, uint32_t stride, int have) {
-    const uint32_t step = have >= 3 ? stride : 0u;
-    f2 x0[kPairs], x1[kPairs], x2[kPairs];
-    VecOf<T>::unpack(lds128_at(slot), x0);
-    VecOf<T>::unpack(lds128_at(slot + step), x1);
-    VecOf<T>::unpack(lds128_at(slot + 2u * step), x2);
+  // K from the thread's first place, or its first three, `stride` bytes apart
+  __device__ __forceinline__ void start(uint32_t slot, uint32_t stride, bool three) {
+    f2 k[kPairs];
+    VecOf<T>::unpack(lds128_at(slot), k);
+    if (three) {
+      f2 x1[kPairs], x2[kPairs];
+      VecOf<T>::unpack(lds128_at(slot + stride), x1);
+      VecOf<T>::unpack(lds128_at(slot + 2u * stride), x2);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) k[i] = middle(k[i], x1[i], x2[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      nk[i] = f2_mul(middle(x0[i], x1[i], x2[i]), f2_splat(-1.f));
+      nk[i] = f2_mul(k[i], f2_splat(-1.f));
       s[i] = q[i] = f2_splat(0.f);
     }
   }
@@ -101,8 +109,10 @@ __device__ __forceinline__ void set_group(const Smem& m, const GnShape& s, int g
 // The CTA's group values (mean, M2) to m.gm from its threads' statistics: columns over the
 // lanes, then groups over their columns (an octet of threads a group).  A warp takes eight
 // quads of columns, four lanes of each at a time: wide loads, and the other warps' issue slots
-// stay free.  A column's lanes combine about r, the middle one of the first three lanes' means: with
-// d = mean_l - r, mean = r + sum n_l d / n and M2 = sum (M2_l + n_l d^2) - (sum n_l d)^2 / n.
+// stay free.  A column's lanes combine about r, the mean of one of them in the middle (not that with
+// place 0): with d = mean_l - r, mean = r + sum n_l d / n and
+// M2 = sum (M2_l + n_l d^2) - (sum n_l d)^2 / n; what that can cancel is at most the lanes over a
+// lane's places times the rest.
 template <typename T>
 __device__ __forceinline__ void cta_stats(const Smem& m, const GnShape& s, const Owner& o,
                                           const ColumnStats<T>& st) {
@@ -130,15 +140,7 @@ __device__ __forceinline__ void cta_stats(const Smem& m, const GnShape& s, const
     const int c = 4 * (8 * t + l8);
     const float* p = m.red + (c < s.cs ? c : 0);
     f2 ref[2], sum[2], q[2];
-    {
-      const int next = o.rows >= 3 && s.lanes >= 3 ? rs : 0;  // lanes that have places
-      f2 r1[2], r2[2];
-      lds_quad(p, ref);
-      lds_quad(p + next, r1);
-      lds_quad(p + 2 * next, r2);
-      ref[0] = middle(ref[0], r1[0], r2[0]);
-      ref[1] = middle(ref[1], r1[1], r2[1]);
-    }
+    lds_quad(p + (min(s.lanes, o.rows) >> 1) * rs, ref);
     sum[0] = sum[1] = q[0] = q[1] = f2_splat(0.f);
 #pragma unroll 2
     for (int l = oct; l < s.lanes; l += 4) {
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
   };
   constexpr int kBatches = 4;  // of a single-stage sample
   const int per = (s.iters + kBatches - 1) / kBatches;
+  const bool three = o.cnt > kFewPlaces;
   int64_t n = o.n;
   if (s.stages == 1)
     for (int b = 0; b < kBatches; ++b) stage_places(n, 0, b * per, (b + 1) * per);
@@ -236,8 +239,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     if (s.stages == 1) {  // the sums follow the copies, batch by batch
       for (int b = 0; b < kBatches; ++b) {
         cp_async_wait(kBatches - 1 - b);
-        // (batches of one or two places: up to eight a thread, which cancel next to nothing)
-        if (b == 0 && o.cnt > 0) st.start(mine, stride, min(o.cnt, per));
+        if (b == 0 && o.cnt > 0) st.start(mine, stride, three);  // (then per is three at least)
         for_staged(mine, b * per, min(o.cnt, (b + 1) * per), stride,
                    [&](const uint4& u) { st.add(u); });
       }
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       stage_places(n + ahead * s.lanes_n, k + ahead < s.stages ? k + ahead : k + ahead - s.stages,
                    0, s.iters);
       cp_async_wait(ahead);
-      if (o.cnt > 0) st.start(mine, stride, o.cnt);
+      if (o.cnt > 0) st.start(mine, stride, three);
       for_staged(mine, 0, o.cnt, stride, [&](const uint4& u) { st.add(u); });
     }
     cta_stats(m, s, o, st);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
       if (o.cnt > 0) {
         static_assert(2 * kRingPlaces >= 3 && Ring<1>::kGroups >= 3, "three places have arrived");
         cp_async_wait_n<Ring<1>::kGroups - 3>();
-        st.start(ring.slot, ring.stride, o.cnt);
+        st.start(ring.slot, ring.stride, o.cnt > kFewPlaces);
       }
       ring.run(o.cnt, [&](uint32_t slot) { st.add(lds128_at(slot)); });
       __syncthreads();  // red takes the rings' place
