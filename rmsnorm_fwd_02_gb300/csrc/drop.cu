@@ -115,15 +115,17 @@ __global__ void __launch_bounds__(kDropThreads)
   const int tail = static_cast<int>(n & 7);
   if (blockIdx.x == gridDim.x - 1 && static_cast<int>(threadIdx.x) < tail) {
     const int64_t at = whole * 8 + threadIdx.x;
-    const float v = widen1(x[at]);
+    float v = widen1(x[at]);
     const float r = kRes ? widen1(res[at]) : 0.f;
-    bool keep = true;
-    if constexpr (kDrop) {
+    if constexpr (kDrop) {  // as drop_pairs, an element at a time (no + 0: a kept -0 stays)
       const uint4 bits = drop_block(d, c, static_cast<uint64_t>(whole));
       const uint32_t w = u4_get(bits, threadIdx.x >> 1);
-      keep = (threadIdx.x & 1) ? drop_keep_hi(d, w) : drop_keep_lo(d, w);
+      const bool keep = (threadIdx.x & 1) ? drop_keep_hi(d, w) : drop_keep_lo(d, w);
+      v = keep ? (kRes ? __fmaf_rn(v, d.scale, r) : v * d.scale) : r;
+    } else if constexpr (kRes) {
+      v += r;
     }
-    narrow1(keep ? __fmaf_rn(v, d.scale, r) : r, y + at);
+    narrow1(v, y + at);
   }
 }
 
