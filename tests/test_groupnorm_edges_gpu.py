@@ -10,6 +10,8 @@ import torch
 
 import rmsnorm_fwd_02_gb300 as R
 from oracle import groupnorm as OG
+from rmsnorm_fwd_02_gb300 import _native as N
+from rmsnorm_fwd_02_gb300 import groupnorm as GN
 from test_groupnorm_gpu import BF, DEV, EPS, FP, HF, U, case, check_bwd, check_fwd, depth, randn
 
 pytestmark = pytest.mark.gpu
@@ -71,6 +73,72 @@ def test_gradient_of_groups_of_any_scale(n, s, c, groups, kind, dtype, log2):
     scale.view(groups, -1)[::2] = 2.0 ** log2
     x = (x * scale).to(dtype)
     check_bwd(dy, x, w, b, groups, kind, eps=0.0)
+
+
+@pytest.mark.parametrize("c,groups", [(40, 8), (64, 4), (24, 8)])
+@pytest.mark.parametrize("s", [60, 3000, 70001])
+@pytest.mark.parametrize("kind", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=str)
+def test_nan_and_infinity_leave_the_other_groups_their_bits(c, groups, s, kind, dtype):
+    x, dy, w, b = case(23, 2, s, c, dtype)
+    per = c // groups
+    clean = R.groupnorm_fwd(x, w, b, groups, EPS, kind)
+    gclean = R.groupnorm_bwd(dy, x, clean[1], clean[2], w, b, groups, kind)
+    bad = x.clone()
+    bad[1, s // 2, 2 * per] = float("nan")
+    bad[0, 0, per - 1] = float("-inf")
+    y, mean, rstd = R.groupnorm_fwd(bad, w, b, groups, EPS, kind)
+    dx, dw, db = R.groupnorm_bwd(dy, bad, mean, rstd, w, b, groups, kind)
+    hit = torch.zeros(2, groups, dtype=torch.bool, device=DEV)
+    hit[1, 2] = hit[0, 0] = True
+    assert torch.equal(~rstd.isfinite(), hit)
+    wide = hit.repeat_interleave(per, 1)[:, None].expand(x.shape)
+    cols = hit.any(0).repeat_interleave(per)
+    assert y[wide].isnan().all() and dx[wide].isnan().all() and dw[cols].isnan().all()
+    for got, want in ((y[~wide], clean[0][~wide]), (dx[~wide], gclean[0][~wide]),
+                      (dw[~cols], gclean[1][~cols]), (db[~cols], gclean[2][~cols])):
+        assert torch.equal(got, want)
+
+
+# clusters of 2, 4 and 8 CTAs that take 1.5 to 8 samples each
+FWD_CLUSTERS = [(HF, 114, 6, 2296, 2), (BF, 124, 6, 2344, 2), (FP, 25, 22, 2104, 2),
+                (BF, 75, 342, 72, 6), (FP, 11, 14, 2152, 2), (HF, 37, 622, 72, 8),
+                (BF, 64, 8, 2168, 1)]
+BWD_CLUSTERS = [(FP, 160, 3, 1576, 1), (FP, 212, 221, 56, 8), (BF, 52, 4, 2104, 2),
+                (FP, 156, 7, 1384, 173), (FP, 11, 11, 2104, 8), (HF, 37, 622, 72, 8),
+                (BF, 119, 8, 2128, 1)]
+
+
+def several_samples_a_cluster(dtype, n, s, c, groups, bwd):
+    p = N.groupnorm_train_launch_plan(GN._DTYPES[dtype], n, s, c, groups, bwd)
+    return p["on_chip"] and p["cluster_ctas"] > 1 and p["ctas"] < p["units"] * p["cluster_ctas"]
+
+
+@pytest.mark.parametrize("dtype,n,s,c,groups", FWD_CLUSTERS, ids=str)
+def test_clusters_go_on_to_further_samples_forward(dtype, n, s, c, groups):
+    assert several_samples_a_cluster(dtype, n, s, c, groups, 0)
+    x, _, w, b = case(29, n, s, c, dtype)
+    got = check_fwd(x, w, b, groups, "silu")
+    for _ in range(3):
+        again = R.groupnorm_fwd(x, w, b, groups, EPS, "silu")
+        assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+@pytest.mark.parametrize("dtype,n,s,c,groups", BWD_CLUSTERS, ids=str)
+def test_clusters_go_on_to_further_samples_backward(dtype, n, s, c, groups):
+    assert several_samples_a_cluster(dtype, n, s, c, groups, 1)
+    x, dy, w, b = case(31, n, s, c, dtype)
+    got = check_bwd(dy, x, w, b, groups, "silu")
+    mean, rstd = (t.float() for t in OG.stats(x.double(), groups, EPS))
+    for _ in range(3):
+        again = R.groupnorm_bwd(dy, x, mean, rstd, w, b, groups, "silu")
+        assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+def test_forms_of_many_small_samples():
+    # forward on chip, backward streamed in one piece a sample
+    p = [N.groupnorm_train_launch_plan(N.GROUPNORM_FP32, 700, 300, 64, 8, d) for d in (0, 1)]
+    assert p[0]["on_chip"] and not p[1]["on_chip"] and p[1]["chunks"] == 1
 
 
 # one to three places a sample and every channel in one slab
