@@ -115,9 +115,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _raw_stream_object(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the current stream's handle alone, without a Stream object around it (2.5 us a call), where
+# this torch has that (a private name)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream_object)
+
+
 def _stream(stream):
-    if stream is None:  # the handle alone, without a Stream object around it (2.5 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -40,14 +40,19 @@ _DTYPES = {torch.bfloat16: N.DROPOUT_BF16, torch.float32: N.DROPOUT_FP32,
            torch.float16: N.DROPOUT_FP16}
 
 
-# torch's allocation of a CUDA tensor past the dispatcher, where this torch has it: through
-# torch.empty, the allocations of a small call take longer than its launch (three of them and
-# the launch 16 us, against 10).
+def _empty_strided_dispatched(shape, stride, dtype):
+    return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
+
+# Outputs and workspaces, which the kernels write whole, come from torch's allocation of a CUDA
+# tensor past the dispatcher, where this torch has it (a private name): through torch.empty, the
+# allocations of a small call take longer than its launch (three of them and the launch 16 us,
+# against 10).  Dispatch modes and torch's filling of uninitialized memory do not see them; the
+# caching allocator, its pools and its streams are the same.
 try:
     _empty_strided = torch._C._dynamo.guards._empty_strided_cuda
 except AttributeError:
-    def _empty_strided(shape, stride, dtype):
-        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+    _empty_strided = _empty_strided_dispatched
 
 
 @functools.lru_cache(maxsize=4096)

@@ -7,6 +7,7 @@ import torch
 
 import rmsnorm_fwd_02_gb300 as R
 from rmsnorm_fwd_02_gb300 import _native as N
+from rmsnorm_fwd_02_gb300 import dropout as D
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,29 @@ def test_rings_that_go_round(T, H, with_dh):
             tol = off + half_step(want.abs() + off)
             assert ((got - want).abs() <= tol)[k].all()
     assert N.rmsnorm_train_device_error(reset=True) == 0
+
+
+def test_allocation_through_the_dispatcher(monkeypatch):
+    # what a torch without the direct allocation and stream calls runs
+    x, res, dy = (randn(i, 300, 264).bfloat16() for i in range(3))
+    w, b = 1 + 0.1 * randn(4, 264), randn(5, 264)
+
+    def step():
+        y, rstd, h = R.rmsnorm_dropout_fwd(x, res, w, 0.2, 6)
+        g, mean, grstd = R.groupnorm_fwd(x, w, b, 8)
+        return (y, rstd, h, g, R.dropout_fwd(x, 0.2, 6), R.dropout_bwd(dy, 0.2, 6),
+                *R.rmsnorm_dropout_bwd(dy, h, rstd, w, 0.2, 6),
+                *R.groupnorm_bwd(dy, x, mean, grstd, w, b, 8))
+
+    want = step()
+    monkeypatch.setattr(D, "_empty_strided", D._empty_strided_dispatched)
+    monkeypatch.setattr(N, "_raw_stream", N._raw_stream_object)
+    got = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        aside = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for t, u, v in zip(got, aside, want):
+        assert t.stride() == v.stride() and t.dtype == v.dtype
+        assert torch.equal(t, v) and torch.equal(u, v)
