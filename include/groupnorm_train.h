@@ -94,7 +94,7 @@ int groupnorm_train_bwd(const void* x, const void* dy, int dtype, const float* m
 /*
  * How the library runs a shape (host-only): writes min(n_out, GROUPNORM_PLAN_FIELDS) values to
  * `out` (host memory): 1 if samples stay on chip between the statistics and the output (one
- * pass over memory; else a cooperative grid streams them, twice through L2), channels a CTA
+ * pass over memory; else a cooperative grid streams them, twice), channels a CTA
  * takes (its slab), threads a CTA, CTAs a cluster, CTAs of the launch at most, its dynamic
  * shared memory bytes, units -- slabs of samples -- taken at a time, chunks a unit's places are
  * split into (1 on chip).  backward: 0 or 1.

@@ -5,13 +5,13 @@
 // mean(g * xhat) and mean(g) are w-weighted sums of them, and dw_c, db_c their sums over the
 // samples -- one set of sums serves all.  As the forward (gn_fwd.cu): x and dy stay on chip
 // between the sums and dx where a cluster's shared memory holds them, and are streamed by a
-// cooperative grid, twice through L2, where not.  dz is formed twice from x and dy rather than
+// cooperative grid, twice, where not.  dz is formed twice from x and dy rather than
 // kept (keeping it in FP32 would double the staged bytes).  The column sums of each CTA (on
 // chip, and for pieces of a few places: over all that it takes, compensated; else of each piece)
 // go to the workspace, and a finishing kernel adds them in a fixed order.
 //
-// Measured (SiLU): on chip 5 x 1023 x 640 fp16 15.6 us, two launches; streamed
-// 2 x 262144 x 128 bf16 118 us: x and dy of a sample, 134 MB, are more than L2 gives back, so
+// Measured (SiLU): on chip 5 x 1023 x 640 fp16 15.5 us, two launches; streamed
+// 2 x 262144 x 128 bf16 117 us: x and dy of a sample, 134 MB, are more than L2 gives back, so
 // both passes read memory, 98.7 us at a copy's rate.
 #include "gn_common.cuh"
 

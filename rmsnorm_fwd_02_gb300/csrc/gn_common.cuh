@@ -28,10 +28,11 @@ __device__ __forceinline__ float rcp_approx(float a) {
   return r;
 }
 
-// s = 1 / (1 + exp(-z)) of pairs, to a few FP32 roundings; far below zero exp(-z) is infinite and
-// s is 0.  (Two values can share a reciprocal, 1/a = b * 1/(ab), if exp(-z) is held to 2^62 so
-// that ab stays finite: the clamp costs what the reciprocal saves, 2 % either way, and leaves
-// z * 2^-62 where the product should vanish.)
+// s = 1 / (1 + exp(-z)) of pairs, within 2^-21 of itself and, below zero, 1.25 |z| FP32 roundings
+// more (the exponential's argument's); far below zero exp(-z) is infinite and s is 0.  (Two values
+// can share a reciprocal, 1/a = b * 1/(ab), if exp(-z) is held to 2^62 so that ab stays finite: the
+// clamp costs what the reciprocal saves, 2 % either way, and leaves z * 2^-62 where the product
+// should vanish.)
 template <int kPairs>
 __device__ __forceinline__ void sigmoid_vec(const f2 (&z)[kPairs], f2 (&s)[kPairs]) {
 #pragma unroll

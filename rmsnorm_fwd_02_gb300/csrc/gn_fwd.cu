@@ -5,11 +5,11 @@
 // a sample's slab (gn_launch.h), x is read once: asynchronous 16-byte copies stage each
 // thread's own vectors (the next samples' on their way meanwhile), the cluster's CTAs exchange
 // a few floats a group, and the staged vectors are normalized and written.  Larger samples are
-// streamed: a cooperative grid takes as many of their slabs at a time as L2 holds, sums them,
-// meets at a barrier, and reads x again from L2 for the output.  (Two launches instead, with
-// their ramps, cost 5 us each more.)
+// streamed: a cooperative grid takes some tens of megabytes of their slabs at a time, sums them,
+// meets at a barrier, and reads x again, as far as it goes from L2, for the output.  (Two launches
+// instead, with their ramps, cost 5 us each more.)
 //
-// Measured (SiLU): on chip 8 x 4096 x 320 bf16 14.5 us, of which about 5 are the launch's ramp
+// Measured (SiLU): on chip 8 x 4096 x 320 bf16 14.6 us, of which about 5 are the launch's ramp
 // and 6 the bandwidth's; streamed 1 x 262144 x 128 fp32 66 us, where L2 gives back 58 MB of the
 // 134 and the rest of x is read twice (60 us at a copy's rate).
 //
@@ -301,10 +301,10 @@ __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
 
 // Streamed.  Each turn's pieces (a unit's chunk each) are dealt out to the grid.  A CTA sums its
 // pieces of turn t + 1 before it waits for every CTA's sums of turn t and writes its pieces of
-// that one, so the grid's barrier and the CTAs' unevenness hide behind a turn's sums; L2 holds
-// both turns.  Before the output a unit's chunks combine (some lanes of a warp a group, the
-// chunks over them).  A piece is written from its last place back, so that of a turn larger than L2 the
-// part still held is read first.  Every unit has its own place in part.
+// that one, so the grid's barrier and the CTAs' unevenness hide behind a turn's sums (L2 holds
+// part of the two turns that are live).  Before the output a unit's chunks combine (some lanes of
+// a warp a group, the chunks over them).  A piece is written from its last place back, so that the
+// part L2 still holds is read first.  Every unit has its own place in part.
 template <typename T, int kAct, bool kWide>
 __global__ void __launch_bounds__(max_threads(kWide), min_ctas(kWide))
     gn_fwd_stream_kernel(const GnArgs a) {

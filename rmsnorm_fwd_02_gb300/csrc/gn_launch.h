@@ -12,8 +12,8 @@ namespace gnorm {
 // Two forms, one launch each:
 //  on chip   `ctas` CTAs of a cluster split a sample's places and keep the slab in shared memory
 //            between the statistics and the output
-//  streamed  a cooperative grid takes units -- slabs of samples -- in turns of as many as L2
-//            holds, each split into `chunks` of places: statistics, a barrier of the grid, output
+//  streamed  a cooperative grid takes units -- slabs of samples -- in turns of some tens of
+//            megabytes, each split into `chunks` of places: statistics, a barrier of the grid, output
 struct GnShape {
   int ev;        // elements a 16-byte vector
   int cg;        // channels a group
