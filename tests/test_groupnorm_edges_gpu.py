@@ -153,3 +153,40 @@ def test_few_places_of_wide_slabs(dtype, n, s, c, groups):
     mean, rstd = (t.float() for t in OG.stats(x.double(), groups, EPS))
     again = R.groupnorm_bwd(dy, x, mean, rstd, w, b, groups, "silu")
     assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+# sequences of pieces that share a row of sums, and one place a sample on chip
+@pytest.mark.parametrize("dtype,n,s,c", [(BF, 1300, 2, 2048), (HF, 401, 3, 4096), (BF, 900, 1, 4096)],
+                         ids=str)
+def test_few_places_of_wide_slabs_captured_and_side_by_side(dtype, n, s, c):
+    cases = [case(41 + i, n, s, c, dtype) for i in range(2)]
+
+    def step(x, dy, w, b):
+        _, mean, rstd = R.groupnorm_fwd(x, w, b, 1, act="silu")
+        return R.groupnorm_bwd(dy, x, mean, rstd, w, b, 1, "silu")
+
+    want = [step(*args) for args in cases]
+    torch.cuda.synchronize()
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in cases]
+    for args in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(step(*args))
+    for _ in range(4):                            # each finds the last replay's sums in its workspace
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for p, q in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(p, q))
+    # one infinite gradient: its channel's sums are infinite, the other channels' as before
+    x, dy, w, b = cases[0]
+    _, mean, rstd = R.groupnorm_fwd(x, w, b, 1)
+    clean = R.groupnorm_bwd(dy, x, mean, rstd, w, b, 1)
+    dy[n // 2, s - 1, 5] = float("inf")
+    dx, dw, db = R.groupnorm_bwd(dy, x, mean, rstd, w, b, 1)
+    assert db[5] == float("inf") and dw[5].isinf()
+    rest = torch.arange(c, device=DEV) != 5
+    assert torch.equal(dw[rest], clean[1][rest]) and torch.equal(db[rest], clean[2][rest])
+    rows = torch.arange(n, device=DEV) != n // 2
+    assert torch.equal(dx[rows], clean[0][rows])
