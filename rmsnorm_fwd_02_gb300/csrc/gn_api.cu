@@ -81,8 +81,8 @@ int slab_groups(int dtype, int C, int G, int bytes) {
 }
 
 // One launch with the slab on chip: the fewest CTAs a cluster that let two CTAs share an SM
-// (else one, which plan() takes for one place a sample alone), more while the GPU has idle SMs and the CTAs are not small; threads == 0 if a
-// cluster of kMaxCluster cannot hold the slab.
+// (else one, which plan() takes for one place a sample alone), more while the GPU has idle SMs
+// and the CTAs are not small; threads == 0 if a cluster of kMaxCluster cannot hold the slab.
 GnShape on_chip_shape(int dtype, int64_t N, int64_t S, int C, int G, int gs, bool bwd) {
   GnShape best{};
   for (int k = 1; k <= kMaxCluster; k *= 2) {
