@@ -1,9 +1,13 @@
-"""GB300 (sm_103a) RMSNorm for training, and LayerNorm, dropout and group norm beside it: a
-C-ABI CUDA library plus a thin torch binding.
+"""GB300 (sm_103a) RMSNorm for training, and LayerNorm, dropout, group norm, a block's boundary and
+activations kept in 8 bits beside it: a C-ABI CUDA library plus a thin torch binding.
 
 The CUDA library is loaded lazily on the first call; importing the package needs no GPU
 (so the input generator ``synth`` is usable on any host).  There is no CPU fallback.
 """
+from .act8 import (RMSNormAct8Train, act8_pack, act8_row_bytes, act8_unpack,  # noqa: F401
+                   rmsnorm_act8_bwd, rmsnorm_act8_fwd, rmsnorm_act8_train)
+from .block import (RMSNormBlockTrain, rmsnorm_block_bwd, rmsnorm_block_fwd,  # noqa: F401
+                    rmsnorm_block_train)
 from .dropout import (DropoutTrain, RMSNormDropoutTrain, dropout_bwd, dropout_fwd,  # noqa: F401
                       dropout_train, rmsnorm_dropout_bwd, rmsnorm_dropout_fwd,
                       rmsnorm_dropout_train)
@@ -18,4 +22,7 @@ __all__ = ["rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_recompute", "rmsnorm_train
            "dropout_fwd", "dropout_bwd", "dropout_train", "DropoutTrain",
            "rmsnorm_dropout_fwd", "rmsnorm_dropout_bwd", "rmsnorm_dropout_train",
            "RMSNormDropoutTrain",
-           "groupnorm_fwd", "groupnorm_bwd", "groupnorm_train", "GroupNormTrain"]
+           "groupnorm_fwd", "groupnorm_bwd", "groupnorm_train", "GroupNormTrain",
+           "act8_pack", "act8_unpack", "act8_row_bytes", "rmsnorm_act8_fwd", "rmsnorm_act8_bwd",
+           "rmsnorm_act8_train", "RMSNormAct8Train",
+           "rmsnorm_block_fwd", "rmsnorm_block_bwd", "rmsnorm_block_train", "RMSNormBlockTrain"]

@@ -1,5 +1,6 @@
 """ctypes binding of ``librmsnorm_train.so`` with the C ABI's names (include/rmsnorm_train.h,
-include/layernorm_train.h, include/dropout_train.h and include/groupnorm_train.h).
+include/layernorm_train.h, include/dropout_train.h, include/groupnorm_train.h,
+include/act8_train.h and include/block_train.h).
 
 Argument marshalling only: tensors become device pointers, the current torch stream
 becomes the ``cudaStream_t``, sizes and strides are passed through, and a nonzero status
@@ -61,6 +62,26 @@ SIGNATURES = {
                                    _size, _i64, _i64, _i32, _i32, _i64, _i64, _int, _vp]),
     "groupnorm_train_launch_plan": (_int, [_int, _i64, _i64, _i32, _i32, _int,
                                            C.POINTER(C.c_int64), _int]),
+    # include/act8_train.h
+    "act8_train_row_bytes": (_i64, [_i64]),
+    "act8_train_pack": (_int, [_vp, _int, _vp, _i64, _i64, _i64, _vp]),
+    "act8_train_unpack": (_int, [_vp, _vp, _int, _i64, _i64, _vp]),
+    "rmsnorm_act8_train_fwd": (_int, [_vp, _vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i32,
+                                      _i64, _i64, _f32, _vp]),
+    "rmsnorm_act8_train_bwd_workspace_bytes": (_size, [_i64, _i32]),
+    "rmsnorm_act8_train_bwd": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _int, _vp, _vp, _vp, _size,
+                                      _i64, _i32, _vp]),
+    # include/block_train.h
+    "rmsnorm_block_train_fwd": (_int, [_vp, _vp, _int, _vp, _vp, _int, _vp, _int, _i64, _vp, _vp,
+                                       _vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _f32, _f32,
+                                       _f32, _vp]),
+    "rmsnorm_block_train_bwd_workspace_bytes": (_size, [_i64, _i32, _i64]),
+    "rmsnorm_block_train_bwd": (_int, [_vp, _vp, _vp, _vp, _int, _int, _vp, _vp, _vp, _vp, _int,
+                                       _vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _size, _i64,
+                                       _i32, _i64, _f32, _f32, _vp]),
+    "rmsnorm_block_train_launch_plan": (_int, [_i64, _i32, _i64, _int, _int, C.POINTER(C.c_int64),
+                                               _int]),
+    "rmsnorm_block_train_device_error": (_int, [C.POINTER(C.c_uint), _int]),
 }
 
 DROPOUT_BF16, DROPOUT_FP32, DROPOUT_FP16 = 0, 1, 2
@@ -68,6 +89,8 @@ GROUPNORM_BF16, GROUPNORM_FP32, GROUPNORM_FP16 = 0, 1, 2
 GROUPNORM_ACT_NONE, GROUPNORM_ACT_SILU, GROUPNORM_ACT_GELU = 0, 1, 2
 GROUPNORM_PLAN_FIELDS = ("on_chip", "channels", "threads", "cluster_ctas", "ctas", "smem",
                          "units", "chunks")
+ACT8_BF16, ACT8_FP32, ACT8_FP16 = 0, 1, 2
+BLOCK_PLAN_FIELDS = ("vectors", "row_threads", "teams", "rows", "stages", "threads", "ctas", "smem")
 
 PLAN_FWD, PLAN_FWD_RESIDUAL, PLAN_BWD, PLAN_BWD_DH, PLAN_BWD_ND, PLAN_BWD_ND_DH = 0, 1, 2, 3, 4, 5
 LN_PLAN_FWD, LN_PLAN_BWD = 0, 1
@@ -308,3 +331,92 @@ def groupnorm_train_launch_plan(dtype, N, S, C_, G, backward):
     if st != RMSN_OK:
         raise RmsnError("groupnorm_train_launch_plan", st)
     return dict(zip(GROUPNORM_PLAN_FIELDS, (int(v) for v in out)))
+
+
+# ---- activations in 8 bits (include/act8_train.h) ---------------------------------------
+
+def act8_train_row_bytes(H):
+    return int(lib().act8_train_row_bytes(H))
+
+
+def act8_train_pack(x, dtype, packed, R, H, s_row, stream=None):
+    st = lib().act8_train_pack(_ptr(x), dtype, _ptr(packed), R, H, s_row, _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("act8_train_pack", st)
+
+
+def act8_train_unpack(packed, y, dtype, R, H, stream=None):
+    st = lib().act8_train_unpack(_ptr(packed), _ptr(y), dtype, R, H, _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("act8_train_unpack", st)
+
+
+def rmsnorm_act8_train_fwd(x, residual, dtype, w, w_dtype, y, h_out, rstd, packed, R, H, s_x, s_res,
+                           eps, stream=None):
+    st = lib().rmsnorm_act8_train_fwd(_ptr(x), _ptr(residual), dtype, _ptr(w), w_dtype, _ptr(y),
+                                      _ptr(h_out), _ptr(rstd), _ptr(packed), R, H, s_x, s_res, eps,
+                                      _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_act8_train_fwd", st)
+
+
+def rmsnorm_act8_train_bwd_workspace_bytes(R, H):
+    return int(lib().rmsnorm_act8_train_bwd_workspace_bytes(R, H))
+
+
+def rmsnorm_act8_train_bwd(packed, dy, dh, dtype, rstd, w, w_dtype, dx, dw, workspace,
+                           workspace_bytes, R, H, stream=None):
+    st = lib().rmsnorm_act8_train_bwd(_ptr(packed), _ptr(dy), _ptr(dh), dtype, _ptr(rstd), _ptr(w),
+                                      w_dtype, _ptr(dx), _ptr(dw), _ptr(workspace),
+                                      workspace_bytes, R, H, _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_act8_train_bwd", st)
+
+
+# ---- a block's boundary (include/block_train.h) -----------------------------------------
+
+def rmsnorm_block_train_fwd(x, residual, dtype, w_pre, w_post, w_dtype, gate, gate_dtype, N, y, h,
+                            rstd_pre, rstd_post, x8, h8, R, H, s_x, s_res, scale, residual_scale,
+                            eps, stream=None):
+    st = lib().rmsnorm_block_train_fwd(_ptr(x), _ptr(residual), dtype, _ptr(w_pre), _ptr(w_post),
+                                       w_dtype, _ptr(gate), gate_dtype, N, _ptr(y), _ptr(h),
+                                       _ptr(rstd_pre), _ptr(rstd_post), _ptr(x8), _ptr(h8), R, H,
+                                       s_x, s_res, scale, residual_scale, eps, _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_block_train_fwd", st)
+
+
+def rmsnorm_block_train_bwd_workspace_bytes(R, H, N):
+    return int(lib().rmsnorm_block_train_bwd_workspace_bytes(R, H, N))
+
+
+def rmsnorm_block_train_bwd(dy, dh, x, h, packed, dtype, rstd_pre, rstd_post, w_pre, w_post,
+                            w_dtype, gate, gate_dtype, N, dx, dresidual, dw_pre, dw_post, dgate,
+                            workspace, workspace_bytes, R, H, s_x, scale, residual_scale,
+                            stream=None):
+    st = lib().rmsnorm_block_train_bwd(_ptr(dy), _ptr(dh), _ptr(x), _ptr(h), int(packed), dtype,
+                                       _ptr(rstd_pre), _ptr(rstd_post), _ptr(w_pre),
+                                       _ptr(w_post), w_dtype, _ptr(gate), gate_dtype, N, _ptr(dx),
+                                       _ptr(dresidual), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate),
+                                       _ptr(workspace), workspace_bytes, R, H, s_x, scale,
+                                       residual_scale, _stream(stream))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_block_train_bwd", st)
+
+
+def rmsnorm_block_train_launch_plan(R, H, N, backward, packed):
+    """The library's launch plan of a block's boundary with both norms for a shape, as a dict."""
+    out = (C.c_int64 * len(BLOCK_PLAN_FIELDS))()
+    st = lib().rmsnorm_block_train_launch_plan(R, H, N, int(backward), int(packed), out,
+                                               len(BLOCK_PLAN_FIELDS))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_block_train_launch_plan", st)
+    return dict(zip(BLOCK_PLAN_FIELDS, (int(v) for v in out)))
+
+
+def rmsnorm_block_train_device_error(reset=True):
+    flags = C.c_uint(0)
+    st = lib().rmsnorm_block_train_device_error(C.byref(flags), int(reset))
+    if st != RMSN_OK:
+        raise RmsnError("rmsnorm_block_train_device_error", st)
+    return int(flags.value)

@@ -20,11 +20,14 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librmsnorm_train.so")
 SOURCES = ["rmsn_api.cu", "rmsn_fwd.cu", "rmsn_bwd.cu", "rmsn_bwd_rc.cu", "rmsn_small.cu",
            "rmsn_drop_fwd.cu", "rmsn_drop_bwd.cu", "drop.cu", "gn_api.cu",
-           "gn_fwd.cu", "gn_bwd.cu", "ln_api.cu", "ln_fwd.cu", "ln_bwd.cu"]
+           "gn_fwd.cu", "gn_bwd.cu", "ln_api.cu", "ln_fwd.cu", "ln_bwd.cu", "act8.cu",
+           "blk_api.cu", "blk_finish.cu", "blk_fwd_bf16.cu", "blk_fwd_fp16.cu",
+           "blk_bwd_bf16.cu", "blk_bwd_fp16.cu"]
 HEADERS = ["rmsn_common.cuh", "rmsn_launch.h", "rmsn_fwd_rows.cuh", "rmsn_bwd_rows.cuh",
            "rmsn_tmem.cuh", "drop_launch.h", "drop_philox.cuh", "types.cuh", "gn_launch.h",
            "gn_common.cuh", "ln_launch.h",
-           "ln_common.cuh"]
+           "ln_common.cuh", "act8.cuh", "blk_launch.h", "blk_common.cuh", "blk_fwd.cuh",
+           "blk_bwd.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +41,8 @@ def _nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
     files += [os.path.join(ROOT, "include", h) for h in ("rmsnorm_train.h", "layernorm_train.h",
-                                                    "dropout_train.h", "groupnorm_train.h")]
+                                                    "dropout_train.h", "groupnorm_train.h",
+                                                    "act8_train.h", "block_train.h")]
     return files
 
 

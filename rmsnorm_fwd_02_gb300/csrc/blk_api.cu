@@ -1,0 +1,545 @@
+// blk_api.cu -- the C ABI of a block's boundary (include/block_train.h) and of the norm that keeps
+// its input in 8 bits (include/act8_train.h): argument checks, launch shapes and launches.  Never
+// allocates, frees or synchronizes (except the diagnostic rmsnorm_block_train_device_error); every
+// launch goes on the caller's stream.
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "act8.cuh"
+#include "blk_launch.h"
+#include "block_train.h"  // include/ (on the include path)
+
+namespace blk {
+
+// Device error word of these kernels' bounded waits, one per device.
+__device__ unsigned g_blk_err_word = 0u;
+
+template <typename T>
+cudaError_t launch_fwd_t(const FwdArgs& a, const Shape& s, int form, bool pack, cudaStream_t st);
+template <typename T>
+cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st);
+
+cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int dtype, int form, bool pack,
+                       cudaStream_t st) {
+  return dtype == ACT8_BF16 ? launch_fwd_t<__nv_bfloat16>(a, s, form, pack, st)
+                            : launch_fwd_t<__half>(a, s, form, pack, st);
+}
+cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int dtype, int form, bool packed,
+                       cudaStream_t st) {
+  return dtype == ACT8_BF16 ? launch_bwd_t<__nv_bfloat16>(a, s, form, packed, st)
+                            : launch_bwd_t<__half>(a, s, form, packed, st);
+}
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - (int64_t{1} << 16);
+constexpr size_t kSmemBytes = 226 * 1024;  // of the 227 KB that a CTA may take
+constexpr size_t kCopyBytes = 2048;  // least bytes of a copy, where rows are narrow
+constexpr int kMaxStages = 8;
+
+std::mutex g_mu;
+unsigned* g_err_ptr[kMaxDevices] = {};
+
+// The error word's address on the current device, after the checks of every launch.
+int device_setup(unsigned** err) {
+  int st = rmsn::check_device();
+  if (st != RMSN_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RMSN_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices) return RMSN_ERR_DEVICE;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_err_ptr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_blk_err_word) != cudaSuccess || p == nullptr)
+      return RMSN_ERR_CUDA;
+    g_err_ptr[dev] = static_cast<unsigned*>(p);
+  }
+  *err = g_err_ptr[dev];
+  return RMSN_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Threads a row, vectors a thread and teams a CTA: functions of H (and of whether a warp may share
+// rows between its threads).
+Shape team_shape(int H, bool whole_warps) {
+  Shape s{};
+  const int nv = H / 8;
+  s.vpt = nv <= 32 ? 1 : 2;
+  const int per = (nv + s.vpt - 1) / s.vpt;
+  s.ntg = per <= 8 && !whole_warps    ? 8
+          : per <= 16 && !whole_warps ? 16
+                                      : static_cast<int>(ceil_div(per, 32)) * 32;
+  const int team = s.ntg < 32 ? 32 : s.ntg;
+  s.teams = kThreads / team;
+  if (s.teams > kMaxTeams) s.teams = kMaxTeams;
+  return s;
+}
+
+// Teams a CTA and CTAs for R rows: a row (or a warp's rows) a team at least, spread over the CTAs
+// first.  A function of (R, H, whole_warps) alone.
+void spread(Shape& s, int64_t R) {
+  const int side = s.ntg < 32 ? 32 / s.ntg : 1;
+  const int64_t takes = ceil_div(R, side);
+  const int64_t per = ceil_div(takes, kPartSMs);
+  if (per < s.teams) s.teams = static_cast<int>(per < 1 ? 1 : per);
+  const int64_t ctas = ceil_div(takes, s.teams);
+  s.P = static_cast<int>(ctas < kPartSMs ? ctas : kPartSMs);
+  s.threads = s.teams * (s.ntg < 32 ? 32 : s.ntg);
+}
+
+}  // namespace
+
+size_t smem_bytes(const Shape& s) {
+  const size_t n = static_cast<size_t>(s.teams) * s.stages;
+  return n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 32 * static_cast<size_t>(s.teams) + 16;
+}
+
+namespace {
+
+// The ring for staged rows of `row` bytes, of which a copy moves at least `least` at once.
+void ring(Shape& s, size_t row, size_t least) {
+  const int side = s.ntg < 32 ? 32 / s.ntg : 1;
+  int steps = 1;
+  if (s.ntg <= 32)
+    while (steps * side * least < kCopyBytes && steps < 64) steps *= 2;
+  for (;; steps /= 2) {
+    s.rows = steps * side;
+    s.slot = row * s.rows;
+    for (s.stages = kMaxStages; s.stages > 1 && smem_bytes(s) > kSmemBytes; --s.stages) {
+    }
+    if (steps == 1 || (s.stages >= 3 && smem_bytes(s) <= kSmemBytes)) break;
+  }
+  s.smem = smem_bytes(s);
+}
+
+Shape plan(int H, int64_t R, bool whole_warps, size_t row, size_t least) {
+  Shape s = team_shape(H, whole_warps);
+  spread(s, R);
+  ring(s, row, least);
+  return s;
+}
+
+int64_t all_teams(int64_t R, int32_t H, bool whole_warps) {
+  Shape s = team_shape(H, whole_warps);
+  spread(s, R);
+  return static_cast<int64_t>(s.P) * s.teams;
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool type_ok(int dtype, bool activation) {
+  return dtype == ACT8_BF16 || dtype == ACT8_FP16 || (!activation && dtype == ACT8_FP32);
+}
+
+int check_sizes(int64_t R, int32_t H, int64_t N) {
+  if (R < 0 || H <= 0 || H % 8 != 0 || N < 1) return RMSN_ERR_INVALID_ARG;
+  if (H > kMaxH || R > kMaxRows) return RMSN_ERR_UNSUPPORTED;
+  if (R % N != 0) return RMSN_ERR_INVALID_ARG;
+  if (N > kMaxRows) return RMSN_ERR_UNSUPPORTED;
+  return RMSN_OK;
+}
+
+bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+
+void set_common(Args& a, const Shape& s, int64_t R, int32_t H, int64_t N, unsigned* err) {
+  a.R = static_cast<int32_t>(R);
+  a.H = H;
+  a.samples = static_cast<int32_t>(N);
+  a.L = static_cast<int32_t>(R / N);
+  a.ntg = s.ntg;
+  a.teams = s.teams;
+  a.rows = s.rows;
+  a.stages = s.stages;
+  a.slot = static_cast<uint32_t>(s.slot);
+  a.err = err;
+}
+
+// Places the staged tensors in a slot of `rows` rows.
+void set_offsets(Args& a) {
+  uint32_t off = 0;
+  for (Staged& in : a.in) {
+    if (in.p == nullptr) continue;
+    in.off = off;
+    off += in.bytes * static_cast<uint32_t>(a.rows);
+  }
+}
+
+Staged staged(const void* p, int64_t stride_bytes, int64_t bytes) {
+  return Staged{static_cast<const unsigned char*>(p), stride_bytes, static_cast<uint32_t>(bytes), 0};
+}
+
+struct Fwd {
+  const void *x, *residual, *w_pre, *w_post, *gate;
+  int dtype, w_dtype, gate_dtype, form;
+  int64_t N, R;
+  void *y, *h;
+  float *rstd_pre, *rstd_post;
+  void *x8, *h8;
+  int32_t H;
+  int64_t s_x, s_res;
+  float scale, residual_scale, eps;
+};
+
+int run_fwd(const Fwd& f, void* stream) {
+  unsigned* err = nullptr;
+  const int st = device_setup(&err);
+  if (st != RMSN_OK) return st;
+  FwdArgs a{};
+  const size_t row = 2 * static_cast<size_t>(f.H);
+  const Shape s = plan(f.H, f.R, false, f.residual != nullptr ? 2 * row : row, row);
+  set_common(a, s, f.R, f.H, f.N, err);
+  a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
+  if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
+  set_offsets(a);
+  a.w_pre = f.w_pre;
+  a.w_post = f.w_post;
+  a.gate = f.gate;
+  a.w_dtype = f.w_dtype;
+  a.gate_dtype = f.gate_dtype;
+  a.scale = f.scale;
+  a.residual_scale = f.residual_scale;
+  a.eps = f.eps;
+  a.y = f.y;
+  a.h = f.h;
+  a.rstd_pre = f.rstd_pre;
+  a.rstd_post = f.rstd_post;
+  a.x8 = static_cast<unsigned char*>(f.x8);
+  a.h8 = static_cast<unsigned char*>(f.h8);
+  return launch_fwd(a, s, f.dtype, f.form, f.x8 != nullptr || f.h8 != nullptr,
+                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RMSN_OK
+             : RMSN_ERR_CUDA;
+}
+
+struct Bwd {
+  const void *dy, *dh, *x, *h;
+  bool packed;
+  int dtype, form;
+  const float *rstd_pre, *rstd_post;
+  const void *w_pre, *w_post, *gate;
+  int w_dtype, gate_dtype;
+  int64_t N, R;
+  void *dx, *dres;
+  float *dw_pre, *dw_post, *dgate;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t H;
+  int64_t s_x;
+  float scale, residual_scale;
+};
+
+// Floats of the sums' rows: a row a team for dw_pre, a row a team and sample for S.
+size_t part_floats(int64_t teams, int32_t H) { return static_cast<size_t>(teams) * H; }
+size_t s_floats(int64_t teams, int32_t H, int64_t N) {
+  return static_cast<size_t>(teams + N - 1) * H;
+}
+size_t workspace_bytes(int64_t R, int32_t H, int64_t N) {
+  const int64_t teams = all_teams(R, H, N > 1);
+  return sizeof(float) * (part_floats(teams, H) + s_floats(teams, H, N));
+}
+
+int run_bwd(const Bwd& b, void* stream) {
+  const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  const bool pre = b.form != kPost, s_sums = b.form != kKeep;
+  unsigned* err = nullptr;
+  const int st = device_setup(&err);
+  if (st != RMSN_OK) return st;
+  if (b.R == 0) {
+    for (float* p : {b.dw_pre, b.dw_post})
+      if (p != nullptr && cudaMemsetAsync(p, 0, sizeof(float) * b.H, stream_) != cudaSuccess)
+        return RMSN_ERR_CUDA;
+    if (b.dgate != nullptr &&
+        cudaMemsetAsync(b.dgate, 0, sizeof(float) * b.N * b.H, stream_) != cudaSuccess)
+      return RMSN_ERR_CUDA;
+    return RMSN_OK;
+  }
+  BwdArgs a{};
+  const bool whole_warps = s_sums && b.N > 1;  // a warp's rows are then of one sample
+  const int64_t wide = 2 * static_cast<int64_t>(b.H);
+  const int64_t saved = b.packed ? rmsn::act8_row_size(b.H) : wide;
+  if (pre) {
+    a.in[0] = staged(b.h, saved, saved);
+    a.in[1] = staged(b.dy, wide, wide);
+  }
+  if (b.dh != nullptr) a.in[2] = staged(b.dh, wide, wide);
+  if (s_sums) a.in[3] = staged(b.x, b.packed || b.R == 1 ? saved : 2 * b.s_x, saved);
+  size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
+  for (const Staged& in : a.in)
+    if (in.p != nullptr) row += in.bytes;
+  const Shape s = plan(b.H, b.R, whole_warps, row, least);
+  set_common(a, s, b.R, b.H, b.N, err);
+  set_offsets(a);
+  const int64_t teams = static_cast<int64_t>(s.P) * s.teams;
+  const size_t need = sizeof(float) * ((pre ? part_floats(teams, b.H) : 0) +
+                                       (s_sums ? s_floats(teams, b.H, b.N) : 0));
+  if (b.workspace == nullptr || b.workspace_bytes < need) return RMSN_ERR_WORKSPACE;
+  float* ws = static_cast<float*>(b.workspace);
+  a.w_pre = b.w_pre;
+  a.w_post = b.w_post;
+  a.gate = b.gate;
+  a.w_dtype = b.w_dtype;
+  a.gate_dtype = b.gate_dtype;
+  a.scale = b.scale;
+  a.residual_scale = b.residual_scale;
+  a.rstd_pre = b.rstd_pre;
+  a.rstd_post = b.rstd_post;
+  a.dx = b.dx;
+  a.dres = b.dres;
+  a.part_pre = pre ? ws : nullptr;
+  a.part_s = s_sums ? ws + (pre ? part_floats(teams, b.H) : 0) : nullptr;
+  if (launch_bwd(a, s, b.dtype, b.form, b.packed, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
+  FinishArgs f{};
+  f.part_pre = a.part_pre;
+  f.part_s = a.part_s;
+  f.teams = teams;
+  f.R = a.R;
+  f.H = b.H;
+  f.samples = a.samples;
+  f.w_post = b.w_post;
+  f.gate = b.gate;
+  f.w_dtype = b.w_dtype;
+  f.gate_dtype = b.gate_dtype;
+  f.scale = b.scale;
+  f.dw_pre = b.dw_pre;
+  f.dw_post = b.dw_post;
+  f.dgate = b.dgate;
+  return launch_finish(f, stream_) == cudaSuccess ? RMSN_OK : RMSN_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace blk
+
+using namespace blk;
+
+extern "C" {
+
+int rmsnorm_act8_train_fwd(const void* x, const void* residual, int dtype, const void* w,
+                           int w_dtype, void* y, void* h_out, float* rstd, void* packed,
+                           int64_t R, int32_t H, int64_t s_x, int64_t s_res, float eps,
+                           void* stream) {
+  const int st = check_sizes(R, H, 1);
+  if (st != RMSN_OK) return st;
+  if (!type_ok(dtype, true) || !type_ok(w_dtype, false) || !stride_ok(s_x) ||
+      (residual != nullptr && !stride_ok(s_res)))
+    return RMSN_ERR_INVALID_ARG;
+  if (!w || (residual == nullptr && h_out != nullptr)) return RMSN_ERR_INVALID_ARG;
+  if (R > 0 && (!x || !y || !rstd || !packed || (residual != nullptr && h_out == nullptr)))
+    return RMSN_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, w, static_cast<const void*>(y), static_cast<const void*>(h_out),
+                        static_cast<const void*>(packed)})
+    if (!aligned(p, 16)) return RMSN_ERR_INVALID_ARG;
+  if (!aligned(rstd, 4) || !std::isfinite(eps) || eps < 0.f) return RMSN_ERR_INVALID_ARG;
+  if (R == 0) return RMSN_OK;
+  Fwd f{};
+  f.x = x;
+  f.residual = residual;
+  f.w_pre = w;
+  f.dtype = dtype;
+  f.w_dtype = w_dtype;
+  f.form = kKeep;
+  f.N = 1;
+  f.R = R;
+  f.y = y;
+  f.h = h_out;
+  f.rstd_pre = rstd;
+  f.h8 = packed;
+  f.H = H;
+  f.s_x = s_x;
+  f.s_res = s_res;
+  f.eps = eps;
+  return run_fwd(f, stream);
+}
+
+size_t rmsnorm_act8_train_bwd_workspace_bytes(int64_t R, int32_t H) {
+  if (check_sizes(R, H, 1) != RMSN_OK || R == 0) return 0;
+  return sizeof(float) * part_floats(all_teams(R, H, false), H);
+}
+
+int rmsnorm_act8_train_bwd(const void* packed, const void* dy, const void* dh, int dtype,
+                           const float* rstd, const void* w, int w_dtype, void* dx, float* dw,
+                           void* workspace, size_t workspace_bytes, int64_t R, int32_t H,
+                           void* stream) {
+  const int st = check_sizes(R, H, 1);
+  if (st != RMSN_OK) return st;
+  if (!type_ok(dtype, true) || !type_ok(w_dtype, false)) return RMSN_ERR_INVALID_ARG;
+  if (!w || !dw || (R > 0 && (!packed || !dy || !rstd || !dx))) return RMSN_ERR_INVALID_ARG;
+  for (const void* p : {packed, dy, dh, w, static_cast<const void*>(dx),
+                        static_cast<const void*>(workspace)})
+    if (!aligned(p, 16)) return RMSN_ERR_INVALID_ARG;
+  if (!aligned(rstd, 4) || !aligned(dw, 4)) return RMSN_ERR_INVALID_ARG;
+  Bwd b{};
+  b.dy = dy;
+  b.dh = dh;
+  b.h = packed;
+  b.packed = true;
+  b.dtype = dtype;
+  b.form = kKeep;
+  b.rstd_pre = rstd;
+  b.w_pre = w;
+  b.w_dtype = w_dtype;
+  b.N = 1;
+  b.R = R;
+  b.dres = dx;
+  b.dw_pre = dw;
+  b.workspace = workspace;
+  b.workspace_bytes = workspace_bytes;
+  b.H = H;
+  b.scale = b.residual_scale = 1.f;
+  return run_bwd(b, stream);
+}
+
+int rmsnorm_block_train_fwd(const void* x, const void* residual, int dtype, const void* w_pre,
+                            const void* w_post, int w_dtype, const void* gate, int gate_dtype,
+                            int64_t N, void* y, void* h, float* rstd_pre, float* rstd_post,
+                            void* x8, void* h8, int64_t R, int32_t H, int64_t s_x, int64_t s_res,
+                            float scale, float residual_scale, float eps, void* stream) {
+  const int st = check_sizes(R, H, N);
+  if (st != RMSN_OK) return st;
+  if (!type_ok(dtype, true) || !type_ok(w_dtype, false) ||
+      (gate != nullptr ? !type_ok(gate_dtype, false) : N != 1) || !stride_ok(s_x) ||
+      !stride_ok(s_res) || (!w_pre && !w_post))
+    return RMSN_ERR_INVALID_ARG;
+  if (R > 0 && (!x || !residual || !h || (w_pre != nullptr) != (y != nullptr) ||
+                (w_pre != nullptr) != (rstd_pre != nullptr) ||
+                (w_post != nullptr) != (rstd_post != nullptr)))
+    return RMSN_ERR_INVALID_ARG;
+  // in 8 bits: all that the backward reads, or nothing
+  const bool reads_x = w_post != nullptr || gate != nullptr, reads_h = w_pre != nullptr;
+  if ((x8 != nullptr && !reads_x) || (h8 != nullptr && !reads_h) ||
+      (reads_x && reads_h && (x8 != nullptr) != (h8 != nullptr)))
+    return RMSN_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, w_pre, w_post, gate, static_cast<const void*>(y),
+                        static_cast<const void*>(h), static_cast<const void*>(x8),
+                        static_cast<const void*>(h8)})
+    if (!aligned(p, 16)) return RMSN_ERR_INVALID_ARG;
+  if (!aligned(rstd_pre, 4) || !aligned(rstd_post, 4) || !std::isfinite(scale) ||
+      !std::isfinite(residual_scale) || !std::isfinite(eps) || eps < 0.f)
+    return RMSN_ERR_INVALID_ARG;
+  if (R == 0) return RMSN_OK;
+  Fwd f{};
+  f.x = x;
+  f.residual = residual;
+  f.w_pre = w_pre;
+  f.w_post = w_post;
+  f.gate = gate;
+  f.dtype = dtype;
+  f.w_dtype = w_dtype;
+  f.gate_dtype = gate_dtype;
+  f.form = w_post == nullptr ? kPre : (w_pre != nullptr ? kBoth : kPost);
+  f.N = N;
+  f.R = R;
+  f.y = y;
+  f.h = h;
+  f.rstd_pre = rstd_pre;
+  f.rstd_post = rstd_post;
+  f.x8 = x8;
+  f.h8 = h8;
+  f.H = H;
+  f.s_x = s_x;
+  f.s_res = s_res;
+  f.scale = scale;
+  f.residual_scale = residual_scale;
+  f.eps = eps;
+  return run_fwd(f, stream);
+}
+
+size_t rmsnorm_block_train_bwd_workspace_bytes(int64_t R, int32_t H, int64_t N) {
+  if (check_sizes(R, H, N) != RMSN_OK || R == 0) return 0;
+  return workspace_bytes(R, H, N);
+}
+
+int rmsnorm_block_train_bwd(const void* dy, const void* dh, const void* x, const void* h,
+                            int packed, int dtype, const float* rstd_pre, const float* rstd_post,
+                            const void* w_pre, const void* w_post, int w_dtype, const void* gate,
+                            int gate_dtype, int64_t N, void* dx, void* dresidual, float* dw_pre,
+                            float* dw_post, float* dgate, void* workspace, size_t workspace_bytes,
+                            int64_t R, int32_t H, int64_t s_x, float scale, float residual_scale,
+                            void* stream) {
+  const int st = check_sizes(R, H, N);
+  if (st != RMSN_OK) return st;
+  const bool pre = w_pre != nullptr, post = w_post != nullptr, gated = gate != nullptr;
+  if (!type_ok(dtype, true) || !type_ok(w_dtype, false) ||
+      (gated ? !type_ok(gate_dtype, false) : N != 1) || (packed != 0 && packed != 1) ||
+      !stride_ok(s_x) || (!pre && !post))
+    return RMSN_ERR_INVALID_ARG;
+  if (pre != (dw_pre != nullptr) || post != (dw_post != nullptr) || gated != (dgate != nullptr))
+    return RMSN_ERR_INVALID_ARG;
+  if (R > 0 && (pre != (dy != nullptr) || (!pre && !dh) || (pre && (!h || !rstd_pre)) ||
+                ((post || gated) && !x) || (post && !rstd_post) || !dx || !dresidual))
+    return RMSN_ERR_INVALID_ARG;
+  for (const void* p : {dy, dh, x, h, w_pre, w_post, gate, static_cast<const void*>(dx),
+                        static_cast<const void*>(dresidual), static_cast<const void*>(workspace)})
+    if (!aligned(p, 16)) return RMSN_ERR_INVALID_ARG;
+  for (const float* p : {rstd_pre, rstd_post, static_cast<const float*>(dw_pre),
+                         static_cast<const float*>(dw_post), static_cast<const float*>(dgate)})
+    if (!aligned(p, 4)) return RMSN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(residual_scale)) return RMSN_ERR_INVALID_ARG;
+  Bwd b{};
+  b.dy = dy;
+  b.dh = dh;
+  b.x = x;
+  b.h = h;
+  b.packed = packed != 0;
+  b.dtype = dtype;
+  b.form = !post ? (gated ? kPre : kKeep) : (pre ? kBoth : kPost);
+  b.rstd_pre = rstd_pre;
+  b.rstd_post = rstd_post;
+  b.w_pre = w_pre;
+  b.w_post = w_post;
+  b.gate = gate;
+  b.w_dtype = w_dtype;
+  b.gate_dtype = gate_dtype;
+  b.N = N;
+  b.R = R;
+  b.dx = dx;
+  b.dres = dresidual;
+  b.dw_pre = dw_pre;
+  b.dw_post = dw_post;
+  b.dgate = dgate;
+  b.workspace = workspace;
+  b.workspace_bytes = workspace_bytes;
+  b.H = H;
+  b.s_x = s_x;
+  b.scale = scale;
+  b.residual_scale = residual_scale;
+  return run_bwd(b, stream);
+}
+
+int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backward, int packed,
+                                    int64_t* out, int n_out) {
+  if (!out || n_out < 0 || (backward != 0 && backward != 1) || (packed != 0 && packed != 1))
+    return RMSN_ERR_INVALID_ARG;
+  const int st = check_sizes(R, H, N);
+  if (st != RMSN_OK) return st;
+  if (R == 0) return RMSN_ERR_INVALID_ARG;
+  const size_t wide = 2 * static_cast<size_t>(H);
+  const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
+  const Shape s = backward ? plan(H, R, N > 1, 2 * wide + 2 * saved, wide < saved ? wide : saved)
+                           : plan(H, R, false, 2 * wide, wide);
+  const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
+                                        s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
+  for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];
+  return RMSN_OK;
+}
+
+int rmsnorm_block_train_device_error(unsigned int* flags, int reset) {
+  if (!flags) return RMSN_ERR_INVALID_ARG;
+  unsigned* err = nullptr;
+  const int st = device_setup(&err);
+  if (st != RMSN_OK) return st;
+  if (cudaDeviceSynchronize() != cudaSuccess) return RMSN_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(flags, g_blk_err_word, sizeof(unsigned)) != cudaSuccess)
+    return RMSN_ERR_CUDA;
+  if (reset) {
+    const unsigned zero = 0u;
+    if (cudaMemcpyToSymbol(g_blk_err_word, &zero, sizeof(unsigned)) != cudaSuccess)
+      return RMSN_ERR_CUDA;
+  }
+  return RMSN_OK;
+}
+
+}  // extern "C"

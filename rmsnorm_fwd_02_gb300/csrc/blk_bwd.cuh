@@ -1,0 +1,263 @@
+// blk_bwd.cuh -- the backward of a block's boundary for sm_103a (include/block_train.h), and of
+// the norm that keeps its input in 8 bits (include/act8_train.h).  Included by the translation
+// units of the two activation types.
+//
+// HBM-bound: up to 12 bytes an element (h, dy, dh, x; dx, dresidual; h and x 1.03 each where they are
+// kept in 8 bits).  Two row sums follow one another: of dy w_pre h for the gradient t of h, then of
+// the branch's gradient times x for dx; t waits between them in registers.  One column sum serves
+// both dw_post and the gate's gradient: S = sum of t * xhat over a sample's rows, of which dgate is
+// scale * w_post * S and dw_post the sum over samples of scale * gate * S.
+//
+// A team sums its columns in FP32 registers over its rows; it writes a row of S whenever its
+// rows pass into another sample (row k + n for team k and sample n: teams and samples both go
+// forward, so no two share one) and a row of dw_pre's sums at the end.  The finish adds these rows
+// in a fixed order.
+#pragma once
+
+#include "blk_common.cuh"
+
+namespace blk {
+
+// Vector c of a staged row: 16-bit values, or 8-bit numbers with their block's scale.
+template <typename T, bool kPacked>
+__device__ __forceinline__ void load_saved(const Args& a, uint32_t at, int c, f2 (&v)[4]) {
+  if constexpr (kPacked) {
+    const uint2 q = lds64_at(at + 8u * c);
+    const uint32_t s = lds8_at(at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2));
+    act8_unpack8(q, act8_unit(s), v);
+  } else {
+    VecOf<T>::unpack(lds128_at(at + 16u * c), v);
+  }
+}
+
+// A team's sums of its columns to a row of partials, and back to zero.
+template <int VPT>
+__device__ __forceinline__ void write_sums(const Args& a, const Team& t, float* out, f2 (&acc)[VPT][4]) {
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = t.lt + v * a.ntg;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // rows side by side in a warp
+      for (int o = a.ntg; o < 32; o <<= 1) {
+        const float lo = __shfl_xor_sync(0xffffffffu, f2_lo(acc[v][q]), o);
+        const float hi = __shfl_xor_sync(0xffffffffu, f2_hi(acc[v][q]), o);
+        acc[v][q] = f2_add(acc[v][q], f2_make(lo, hi));
+      }
+    }
+    if (8 * c < a.H && t.sub == 0) {
+      float4* p = reinterpret_cast<float4*>(out) + 2 * c;
+      p[0] = make_float4(f2_lo(acc[v][0]), f2_hi(acc[v][0]), f2_lo(acc[v][1]), f2_hi(acc[v][1]));
+      p[1] = make_float4(f2_lo(acc[v][2]), f2_hi(acc[v][2]), f2_lo(acc[v][3]), f2_hi(acc[v][3]));
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[v][q] = f2_splat(0.f);
+  }
+}
+
+template <typename T, int VPT, int kForm, bool kPacked>
+__global__ void __launch_bounds__(kThreads, 1) blk_bwd_kernel(const BwdArgs a) {
+  constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
+  constexpr bool kX = kForm != kKeep;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint64_t pol = l2_evict_first_policy();
+  Team t = team_begin<4>(a, smem, pol);
+  const int NV = a.H >> 3;
+  f2 w[VPT][4], k1[VPT][4], sum_pre[VPT][4], sum_s[VPT][4];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = t.lt + v * a.ntg;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      sum_pre[v][q] = f2_splat(0.f);
+      sum_s[v][q] = f2_splat(0.f);
+    }
+    if constexpr (kPreN) {
+      if (c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
+    }
+  }
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  const f2 rscale = f2_splat(a.residual_scale);
+  const int step = a.ntg < 32 ? 32 / a.ntg : 1;
+  const bool has_dh = a.in[2].p != nullptr;
+  int32_t sample = kX ? t.r0 / a.L : 0;
+  int32_t next_sample = (sample + 1) * a.L;  // the row from which k1 and S are another sample's
+  if constexpr (kX) {
+    if (t.r0 < t.r1) load_factor<VPT, kPostN>(a, sample, t.lt, k1);
+  }
+  // the r's of the row ahead, so that no row waits for them
+  float r1_next = 0.f, r2_next = 0.f;
+  auto fetch = [&](int32_t row) {
+    if (row < t.r1) {
+      if constexpr (kPreN) r2_next = __ldg(a.rstd_pre + row);
+      if constexpr (kPostN) r1_next = __ldg(a.rstd_post + row);
+    }
+  };
+  fetch(t.r0 + t.sub);
+  int s = 0;
+  uint32_t parity = 0;
+  for (int32_t j = 0; j < t.nslots; ++j) {
+    wait_slot(a, t, s, parity);
+    const int32_t ra = t.r0 + j * a.rows;
+    const int32_t n = min(a.rows, t.r1 - ra);
+    for (int32_t i = 0; i < n; i += step) {
+      const int32_t row = ra + i + t.sub;
+      const bool valid = i + t.sub < n;
+      const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
+      const uint32_t at = static_cast<uint32_t>(i + t.sub);
+      const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
+      const uint32_t dys = base + a.in[1].off + at * a.in[1].bytes;
+      const uint32_t dhs = base + a.in[2].off + at * a.in[2].bytes;
+      const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
+      if constexpr (kX) {
+        // (gates of several samples: a team's rows are one at a time, so this is uniform)
+        if (row >= next_sample && a.samples > 1) {
+          write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
+          sample = row / a.L;
+          next_sample = (sample + 1) * a.L;
+          load_factor<VPT, kPostN>(a, sample, t.lt, k1);
+        }
+      }
+      const float r1 = r1_next, r2 = r2_next;
+      fetch(i + step < n ? row + step : ra + a.rows + t.sub);
+      f2 ncr2 = f2_splat(0.f);
+      const f2 r2v = f2_splat(r2);
+      if constexpr (kPreN) {
+        f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const int c = t.lt + v * a.ntg;
+          if (c < NV && valid) {
+            f2 h[4], dy[4];
+            load_saved<T, kPacked>(a, hs, c, h);
+            VecOf<T>::unpack(lds128_at(dys + 16u * c), dy);
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              dot0 = f2_fma(f2_mul(dy[q], w[v][q]), h[q], dot0);
+              dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), h[q + 1], dot1);
+            }
+          }
+        }
+        const f2 d = f2_add(dot0, dot1);
+        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
+        if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+          issue<4>(a, t, j - 1 + a.stages, pol);
+        // t = r2 (dy w - h (mean r2^2)): the mean's factor times r2, on t's scale
+        ncr2 = f2_splat(-(dot * (r2 * inv_h)) * r2);
+      }
+      f2 m[VPT][4];
+      const f2 r1v = f2_splat(r1);
+      f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = t.lt + v * a.ntg;
+        if (c < NV && valid) {
+          f2 g[4];
+          if constexpr (kPreN) {
+            f2 h[4], dy[4];
+            load_saved<T, kPacked>(a, hs, c, h);
+            VecOf<T>::unpack(lds128_at(dys + 16u * c), dy);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              g[q] = f2_mul(f2_fma(h[q], ncr2, f2_mul(dy[q], w[v][q])), r2v);
+              sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], r2v), sum_pre[v][q]);
+            }
+          }
+          if (!kPreN || has_dh) {
+            f2 dh[4];
+            VecOf<T>::unpack(lds128_at(dhs + 16u * c), dh);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_add(g[q], dh[q]) : dh[q];
+          }
+          f2 o[4];
+          const size_t out = static_cast<size_t>(row) * a.H + 8 * c;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], rscale);
+          stg128(static_cast<T*>(a.dres) + out, VecOf<T>::pack(o));
+          if constexpr (kX) {
+            f2 x[4];
+            load_saved<T, kPacked>(a, xs, c, x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f2 xh = kPostN ? f2_mul(x[q], r1v) : x[q];
+              sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
+              m[v][q] = f2_mul(g[q], k1[v][q]);
+              if constexpr (kPostN) {
+                if (q & 1)
+                  dot1 = f2_fma(m[v][q], x[q], dot1);
+                else
+                  dot0 = f2_fma(m[v][q], x[q], dot0);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m[v][q] = f2_mul(g[q], f2_splat(a.scale));
+          }
+          if (!kPostN && a.dx != nullptr)
+            stg128(static_cast<T*>(a.dx) + out, VecOf<T>::pack(m[v]));
+        }
+      }
+      if constexpr (kPostN) {
+        const f2 d = f2_add(dot0, dot1);
+        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
+        if (!kPreN && i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+          issue<4>(a, t, j - 1 + a.stages, pol);
+        const f2 ncr1 = f2_splat(-(dot * (r1 * inv_h)) * r1);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const int c = t.lt + v * a.ntg;
+          if (c < NV && valid) {
+            f2 x[4], o[4];
+            load_saved<T, kPacked>(a, xs, c, x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], ncr1, m[v][q]), r1v);
+            stg128(static_cast<T*>(a.dx) + static_cast<size_t>(row) * a.H + 8 * c, VecOf<T>::pack(o));
+          }
+        }
+      }
+    }
+    if (t.warps == 1) {
+      __syncwarp();
+      if (t.leader && j + a.stages < t.nslots) issue<4>(a, t, j + a.stages, pol);
+    }
+    if (++s == a.stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+  drain(a, t);
+  if constexpr (kPreN) write_sums<VPT>(a, t, a.part_pre + t.k * a.H, sum_pre);
+  // (a team without rows writes zeros: it lies among the teams of its first row's sample)
+  if constexpr (kX) write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
+}
+
+template <typename T, int VPT>
+const void* pick_bwd(int form, bool packed) {
+  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+  switch (form) {
+    case kKeep:
+      return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true>)
+                    : fn(&blk_bwd_kernel<T, VPT, kKeep, false>);
+    case kPre:
+      return packed ? fn(&blk_bwd_kernel<T, VPT, kPre, true>)
+                    : fn(&blk_bwd_kernel<T, VPT, kPre, false>);
+    case kBoth:
+      return packed ? fn(&blk_bwd_kernel<T, VPT, kBoth, true>)
+                    : fn(&blk_bwd_kernel<T, VPT, kBoth, false>);
+    default:
+      return packed ? fn(&blk_bwd_kernel<T, VPT, kPost, true>)
+                    : fn(&blk_bwd_kernel<T, VPT, kPost, false>);
+  }
+}
+
+template <typename T>
+cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
+  const void* fn = s.vpt == 1 ? pick_bwd<T, 1>(form, packed) : pick_bwd<T, 2>(form, packed);
+  const cudaError_t e = prepare_kernel(fn, s.smem);
+  if (e != cudaSuccess) return e;
+  BwdArgs copy = a;
+  void* args[] = {&copy};
+  return launch_pdl(fn, dim3(static_cast<unsigned>(s.P)), dim3(static_cast<unsigned>(s.threads)),
+                    s.smem, st, args);
+}
+
+}  // namespace blk

@@ -1,0 +1,196 @@
+// blk_common.cuh -- device code shared by the forward and backward kernels of a block's boundary.
+//
+// Staging: a CTA is a number of teams, each with a contiguous run of rows and a ring of its own
+// in shared memory that bulk asynchronous copies fill; the team's first thread starts a slot's
+// next copies as soon as the team is known to be done with it: one-warp teams after a __syncwarp
+// behind the slot, others behind the next slot's first reduction, whose barrier every warp reaches
+// only after its last read.  There is no producer warp, so 16 warps of 128 registers fill an SM, and
+// a slot is held for one row's work only: the rest of the ring is on its way.
+#pragma once
+
+#include "act8.cuh"
+#include "blk_launch.h"
+#include "types.cuh"
+
+namespace blk {
+
+using namespace rmsn;  // f2, the barriers and copies of rmsn_common.cuh, VecOf
+
+// The 8 values from element 8 * c on of a vector of dtype code 0 (BF16), 1 (FP32) or 2 (FP16).
+__device__ __forceinline__ void load8(const void* p, int code, int64_t c, f2 (&f)[4]) {
+  if (code == 1) {
+    const float4* q = static_cast<const float4*>(p) + 2 * c;
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    f[0] = f2_make(a.x, a.y);
+    f[1] = f2_make(a.z, a.w);
+    f[2] = f2_make(b.x, b.y);
+    f[3] = f2_make(b.z, b.w);
+  } else {
+    const uint4 u = __ldg(static_cast<const uint4*>(p) + c);
+    if (code == 0)
+      VecOf<__nv_bfloat16>::unpack(u, f);
+    else
+      VecOf<__half>::unpack(u, f);
+  }
+}
+__device__ __forceinline__ float load1(const void* p, int code, int64_t i) {
+  if (code == 1) return static_cast<const float*>(p)[i];
+  return code == 0 ? widen1(static_cast<const __nv_bfloat16*>(p)[i])
+                   : widen1(static_cast<const __half*>(p)[i]);
+}
+
+// scale * gate * w_post of a thread's columns (each factor where it is there), sample n's gate.
+template <int VPT, bool kPostW>
+__device__ __forceinline__ void load_factor(const Args& a, int32_t n, int lt, f2 (&k1)[VPT][4]) {
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = lt + v * a.ntg;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) k1[v][q] = f2_splat(a.scale);
+    if (8 * c < a.H) {
+      f2 t[4];
+      if (a.gate != nullptr) {
+        load8(a.gate, a.gate_dtype, static_cast<int64_t>(n) * (a.H >> 3) + c, t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) k1[v][q] = f2_mul(k1[v][q], t[q]);
+      }
+      if constexpr (kPostW) {
+        load8(a.w_post, a.w_dtype, c, t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) k1[v][q] = f2_mul(k1[v][q], t[q]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float sum8(const f2 (&f)[4]) {
+  const f2 s = f2_add(f2_add(f[0], f[1]), f2_add(f[2], f[3]));
+  return f2_lo(s) + f2_hi(s);
+}
+
+// A thread's place in its CTA, its team's rows, ring and reductions.
+struct Team {
+  uint32_t ring;        // shared address of the team's slots
+  uint64_t* full;       // its barriers
+  float* red;           // [2][16]: warp sums, taken in turns
+  volatile int* abort_flag;
+  int32_t r0, r1;       // rows
+  int32_t nslots;
+  int64_t k;            // among all teams
+  int lt;               // thread of the row
+  int sub;              // row of the warp (teams of a part of a warp)
+  int team;             // of the CTA
+  int warps;            // of the team
+  int turn;             // of red
+  int32_t issued;       // slots (the leader's)
+  bool leader;
+};
+
+// bulk_g2s with the shared address as such.
+__device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint32_t bytes,
+                                            uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint2 lds64_at(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8_at(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// The copies of slot j of the team's rows (its leader; nothing once a wait has given up).
+template <int kTensors>
+__device__ __forceinline__ void issue(const Args& a, Team& t, int32_t j, uint64_t pol) {
+  if (*t.abort_flag) return;
+  t.issued = j + 1;
+  const int s = j % a.stages;
+  const int32_t ra = t.r0 + j * a.rows;
+  const int32_t n = min(a.rows, t.r1 - ra);
+  uint32_t row = 0;
+#pragma unroll
+  for (int i = 0; i < kTensors; ++i)
+    if (a.in[i].p != nullptr) row += a.in[i].bytes;
+  mbar_arrive_expect_tx(&t.full[s], row * static_cast<uint32_t>(n));
+  const uint32_t dst = t.ring + static_cast<uint32_t>(s) * a.slot;
+#pragma unroll
+  for (int i = 0; i < kTensors; ++i) {
+    const Staged& in = a.in[i];
+    if (in.p == nullptr) continue;
+    const unsigned char* src = in.p + static_cast<int64_t>(ra) * in.stride;
+    if (in.stride == in.bytes) {
+      bulk_g2s_at(dst + in.off, src, in.bytes * static_cast<uint32_t>(n), &t.full[s], pol);
+    } else {
+      for (int32_t r = 0; r < n; ++r)
+        bulk_g2s_at(dst + in.off + static_cast<uint32_t>(r) * in.bytes, src + r * in.stride, in.bytes,
+                    &t.full[s], pol);
+    }
+  }
+}
+
+// Sets the CTA up; returns with the team's first slots on their way.
+template <int kTensors>
+__device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, uint64_t pol) {
+  Team t;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int per = a.ntg < 32 ? 32 : a.ntg;  // threads of a team
+  t.team = tid / per;
+  const int in_team = tid - t.team * per;
+  t.lt = a.ntg < 32 ? in_team % a.ntg : in_team;
+  t.sub = a.ntg < 32 ? in_team / a.ntg : 0;
+  t.warps = per >> 5;
+  t.turn = 0;
+  t.issued = 0;
+  t.leader = in_team == 0;
+  const size_t ring = static_cast<size_t>(a.stages) * a.slot;
+  unsigned char* behind = smem + ring * a.teams;
+  t.ring = smem_u32(smem + ring * t.team);
+  uint64_t* full = reinterpret_cast<uint64_t*>(behind);
+  t.full = full + t.team * a.stages;
+  float* red = reinterpret_cast<float*>(behind + ((8 * a.teams * a.stages + 15) & ~15));
+  t.red = red + 32 * t.team;
+  t.abort_flag = reinterpret_cast<volatile int*>(red + 32 * a.teams);
+  for (int i = tid; i < a.teams * a.stages; i += static_cast<int>(blockDim.x)) mbar_init(&full[i], 1u);
+  if (tid == 0) *t.abort_flag = 0;
+  fence_barrier_init();
+  __syncthreads();
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
+  t.k = static_cast<int64_t>(blockIdx.x) * a.teams + t.team;
+  t.r0 = team_row(t.k, a.R, all);
+  t.r1 = team_row(t.k + 1, a.R, all);
+  t.nslots = (t.r1 - t.r0 + a.rows - 1) / a.rows;
+  if (t.leader)
+    for (int32_t j = 0; j < a.stages && j < t.nslots; ++j) issue<kTensors>(a, t, j, pol);
+  return t;
+}
+
+__device__ __forceinline__ void wait_slot(const Args& a, const Team& t, int s, uint32_t parity) {
+  mbar_wait_bounded(&t.full[s], parity, t.abort_flag, a.err, kErrConsumerWait);
+}
+
+// After a wait that gave up: no copy may still write this CTA's shared memory when it exits.
+__device__ __forceinline__ void drain(const Args& a, const Team& t) {
+  if (*t.abort_flag && t.leader) mbar_drain(t.full, a.stages, t.issued);
+}
+
+// Sum over the threads of a row; every one of them gets the same bits.
+__device__ __forceinline__ float row_sum(const Args& a, Team& t, float v) {
+  if (a.ntg <= 32) return subwarp_allsum(v, a.ntg);
+  v = warp_allsum(v);
+  float* red = t.red + 16 * t.turn;
+  t.turn ^= 1;
+  if ((threadIdx.x & 31) == 0) red[t.lt >> 5] = v;
+  named_bar_sync(static_cast<uint32_t>(t.team) + 1u, static_cast<uint32_t>(a.ntg));
+  return slot_sum(red, t.warps);
+}
+
+}  // namespace blk

@@ -1,0 +1,197 @@
+// blk_fwd.cuh -- the forward of a block's boundary for sm_103a (include/block_train.h), and of
+// the norm that keeps its input in 8 bits (include/act8_train.h).  Included by the translation
+// units of the two activation types.
+//
+// HBM-bound: 8 bytes an element (x, residual; h, y) and 1.03 for each tensor kept in 8 bits, for
+// some 20 instructions.  Two row sums follow one another, of x^2 and, through rstd, of h^2, so a
+// row cannot be streamed; it waits in shared memory, h between the sums in registers.
+#pragma once
+
+#include "blk_common.cuh"
+
+namespace blk {
+
+// One 16-byte vector's values, packed into its row; every lane of the warp takes part (`live`:
+// the vector exists).
+__device__ __forceinline__ void keep8(const Args& a, unsigned char* packed, int64_t row, int c,
+                                      bool live, const f2 (&v)[4]) {
+  const uint32_t amax = act8_max_block(live ? act8_max8(v) : 0u);
+  const uint32_t s = act8_scale_byte(amax);
+  if (packed == nullptr) return;
+  unsigned char* p = packed + row * act8_row_size(a.H);
+  const int first = static_cast<int>(act8_scale_offset(a.H));
+  if (live) *reinterpret_cast<uint2*>(p + 8 * c) = act8_pack8(v, amax, s);
+  if (live && (c & 3) == 0) p[first + (c >> 2)] = static_cast<unsigned char>(s);
+}
+// A packed row's padding (one thread).
+__device__ __forceinline__ void keep8_padding(const Args& a, unsigned char* packed, int64_t row) {
+  unsigned char* p = packed + row * act8_row_size(a.H);
+  const int first = static_cast<int>(act8_scale_offset(a.H));
+  for (int i = a.H; i < first; ++i) p[i] = 0;
+  const int end = static_cast<int>(act8_row_size(a.H));
+  for (int i = first + (a.H + kAct8Block - 1) / kAct8Block; i < end; ++i) p[i] = 0;
+}
+
+template <typename T, int VPT, int kForm, bool kPack>
+__global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
+  constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint64_t pol = l2_evict_first_policy();
+  Team t = team_begin<2>(a, smem, pol);
+  const int NV = a.H >> 3;
+  f2 w[VPT][4];   // w_pre
+  f2 k1[VPT][4];  // scale * gate * w_post
+  if constexpr (kPreN) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = t.lt + v * a.ntg;
+      if (c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
+    }
+  }
+  int32_t next_sample = 0;  // the row from which k1 is another sample's
+  const float hf = static_cast<float>(a.H);
+  const f2 rscale = f2_splat(a.residual_scale);
+  const int step = a.ntg < 32 ? 32 / a.ntg : 1;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int32_t j = 0; j < t.nslots; ++j) {
+    wait_slot(a, t, s, parity);
+    const int32_t ra = t.r0 + j * a.rows;
+    const int32_t n = min(a.rows, t.r1 - ra);
+    for (int32_t i = 0; i < n; i += step) {
+      const int32_t row = ra + i + t.sub;
+      const bool valid = i + t.sub < n;
+      const uint32_t slot = t.ring + static_cast<uint32_t>(s) * a.slot +
+                            static_cast<uint32_t>(i + t.sub) * (static_cast<uint32_t>(a.H) * 2u);
+      const uint32_t xs = slot + a.in[0].off, rs = slot + a.in[1].off;
+      if constexpr (kForm != kKeep) {
+        if (valid && row >= next_sample) {
+          const int32_t sample = row / a.L;
+          load_factor<VPT, kPostN>(a, sample, t.lt, k1);
+          next_sample = (sample + 1) * a.L;
+        }
+      }
+      f2 r1 = f2_splat(1.f);
+      if constexpr (kPostN) {
+        f2 ss = f2_splat(0.f);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const int c = t.lt + v * a.ntg;
+          if (c < NV) {
+            f2 x[4];
+            VecOf<T>::unpack(lds128_at(xs + 16u * c), x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ss = f2_fma(x[q], x[q], ss);
+          }
+        }
+        const float sum = row_sum(a, t, f2_lo(ss) + f2_hi(ss));
+        if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+          issue<2>(a, t, j - 1 + a.stages, pol);
+        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, hf), a.eps));
+        if (valid && t.lt == 0) a.rstd_post[row] = r;
+        r1 = f2_splat(r);
+      }
+      f2 h[VPT][4];
+      f2 ss = f2_splat(0.f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = t.lt + v * a.ntg;
+        const bool live = valid && c < NV;
+        f2 x[4], written[4];
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (c < NV) {
+          VecOf<T>::unpack(lds128_at(xs + 16u * c), x);
+          f2 res[4];
+          if (kForm != kKeep || a.in[1].p != nullptr) VecOf<T>::unpack(lds128_at(rs + 16u * c), res);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (kForm == kKeep) {
+              h[v][q] = a.in[1].p != nullptr ? f2_add(x[q], res[q]) : x[q];
+            } else {
+              const f2 p = kPostN ? f2_mul(x[q], r1) : x[q];
+              h[v][q] = f2_fma(p, k1[v][q], f2_mul(res[q], rscale));
+            }
+          }
+          o = VecOf<T>::pack(h[v]);
+          VecOf<T>::unpack(o, written);
+          if constexpr (kForm == kKeep) {  // the norm is taken of h as it is written
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[v][q] = written[q];
+          }
+          if constexpr (kPreN) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ss = f2_fma(h[v][q], h[v][q], ss);
+          }
+          if (live && a.h != nullptr)
+            stg128(static_cast<T*>(a.h) + static_cast<size_t>(row) * a.H + 8 * c, o);
+        }
+        if constexpr (kPack) {
+          if constexpr (kForm != kKeep) keep8(a, a.x8, row, c, live, x);
+          if constexpr (kPreN) keep8(a, a.h8, row, c, live, written);
+        }
+      }
+      if constexpr (kPack) {
+        if (valid && t.lt == 0) {
+          if (kForm != kKeep && a.x8 != nullptr) keep8_padding(a, a.x8, row);
+          if (kPreN) keep8_padding(a, a.h8, row);
+        }
+      }
+      if constexpr (kPreN) {
+        const float sum = row_sum(a, t, f2_lo(ss) + f2_hi(ss));
+        if (!kPostN && i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+          issue<2>(a, t, j - 1 + a.stages, pol);
+        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, hf), a.eps));
+        if (valid && t.lt == 0) a.rstd_pre[row] = r;
+        const f2 r2 = f2_splat(r);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const int c = t.lt + v * a.ntg;
+          if (valid && c < NV) {
+            f2 y[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = f2_mul(f2_mul(h[v][q], r2), w[v][q]);
+            stg128(static_cast<T*>(a.y) + static_cast<size_t>(row) * a.H + 8 * c, VecOf<T>::pack(y));
+          }
+        }
+      }
+    }
+    if (t.warps == 1) {
+      __syncwarp();
+      if (t.leader && j + a.stages < t.nslots) issue<2>(a, t, j + a.stages, pol);
+    }
+    if (++s == a.stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+  drain(a, t);
+}
+
+template <typename T, int VPT>
+const void* pick_fwd(int form, bool pack) {
+  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+  switch (form) {
+    case kKeep: return fn(&blk_fwd_kernel<T, VPT, kKeep, true>);
+    case kPre:
+      return pack ? fn(&blk_fwd_kernel<T, VPT, kPre, true>) : fn(&blk_fwd_kernel<T, VPT, kPre, false>);
+    case kBoth:
+      return pack ? fn(&blk_fwd_kernel<T, VPT, kBoth, true>)
+                  : fn(&blk_fwd_kernel<T, VPT, kBoth, false>);
+    default:
+      return pack ? fn(&blk_fwd_kernel<T, VPT, kPost, true>)
+                  : fn(&blk_fwd_kernel<T, VPT, kPost, false>);
+  }
+}
+
+template <typename T>
+cudaError_t launch_fwd_t(const FwdArgs& a, const Shape& s, int form, bool pack, cudaStream_t st) {
+  const void* fn = s.vpt == 1 ? pick_fwd<T, 1>(form, pack) : pick_fwd<T, 2>(form, pack);
+  const cudaError_t e = prepare_kernel(fn, s.smem);
+  if (e != cudaSuccess) return e;
+  FwdArgs copy = a;
+  void* args[] = {&copy};
+  return launch_pdl(fn, dim3(static_cast<unsigned>(s.P)), dim3(static_cast<unsigned>(s.threads)),
+                    s.smem, st, args);
+}
+
+}  // namespace blk

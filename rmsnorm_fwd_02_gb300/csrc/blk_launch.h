@@ -1,0 +1,119 @@
+// blk_launch.h -- argument blocks, launch shapes and launchers of a block's boundary
+// (include/block_train.h) and of the norms that keep 8-bit activations (include/act8_train.h).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace blk {
+
+constexpr int kMaxH = 8192;
+constexpr int kThreads = 512;     // most threads of a CTA, one CTA an SM: 128 registers a thread
+constexpr int kMaxTeams = 16;
+constexpr int kMaxTensors = 4;    // staged
+// CTAs of the backward at most, whatever the GPU: the rows' partition, and with it the order of
+// every sum, is a function of the shape.  GB300 has 152 SMs: there it is one wave.
+constexpr int kPartSMs = 152;
+constexpr int kFinishCols = 32;
+constexpr int kFinishSlices = 32;
+
+// What a kernel computes.
+//   kKeep  h = x [+ residual], rounded; norm before; h held in 8 bits    (rmsnorm_act8)
+//   kPre   scales and gate, norm before
+//   kBoth  norm behind, scales and gate, norm before
+//   kPost  norm behind, scales and gate
+// The backward has three forms with a norm before: kKeep (no x: no gate), kPre (x for the gate's
+// gradient), kBoth; and kPost.
+enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
+
+// A team of ntg threads (8, 16: part of a warp, 32 / ntg rows side by side; 32; or several whole
+// warps) takes one row (or those of its warp) at a time from its own ring of `stages` slots, each
+// of `steps` such takes.
+struct Shape {
+  int vpt;      // 16-byte vectors (8 elements) a thread: 1 or 2
+  int ntg;      // threads a row
+  int teams;    // teams (of whole warps) a CTA
+  int rows;     // rows a slot
+  int stages;   // slots a team
+  int threads;  // a CTA
+  int P;        // CTAs
+  size_t slot;  // bytes
+  size_t smem;  // bytes
+};
+
+struct Staged {
+  const unsigned char* p;  // null: not staged
+  int64_t stride;          // bytes between rows
+  uint32_t bytes;          // of a row
+  uint32_t off;            // within a slot
+};
+
+struct Args {
+  Staged in[kMaxTensors];
+  int32_t R, H;
+  int32_t L;               // rows a sample
+  int32_t samples;         // N
+  const void* w_pre;
+  const void* w_post;
+  const void* gate;
+  int32_t w_dtype, gate_dtype;
+  float scale, residual_scale, eps;
+  int32_t ntg, teams, rows, stages;
+  uint32_t slot;
+  unsigned* err;
+};
+
+// Forward: staged x, residual.
+struct FwdArgs : Args {
+  void* y;
+  void* h;
+  float* rstd_pre;
+  float* rstd_post;
+  unsigned char* x8;
+  unsigned char* h8;
+};
+
+// Backward: staged h, dy, dh, x.
+struct BwdArgs : Args {
+  const float* rstd_pre;
+  const float* rstd_post;
+  void* dx;
+  void* dres;
+  float* part_pre;    // [P * teams][H]: sums of dy * hhat, a row a team
+  float* part_s;      // [P * teams + N - 1][H]: sums of t * xhat, a row a team and sample
+};
+
+// First row of team k of n.
+__host__ __device__ inline int32_t team_row(int64_t k, int64_t R, int64_t n) {
+  return static_cast<int32_t>(k * R / n);
+}
+// The team that takes row r.
+__host__ __device__ inline int64_t row_team(int64_t r, int64_t R, int64_t n) {
+  return ((r + 1) * n - 1) / R;
+}
+
+size_t smem_bytes(const Shape& s);
+
+cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int dtype, int form, bool pack,
+                       cudaStream_t st);
+cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int dtype, int form, bool packed,
+                       cudaStream_t st);
+
+// The sums' last step.
+struct FinishArgs {
+  const float* part_pre;   // null: no norm before
+  float* part_s;           // null: neither norm behind nor gate
+  int64_t teams;
+  int32_t R, H, samples;
+  const void* w_post;
+  const void* gate;
+  int32_t w_dtype, gate_dtype;
+  float scale;
+  float* dw_pre;
+  float* dw_post;          // null: no norm behind
+  float* dgate;            // null: no gate
+};
+cudaError_t launch_finish(const FinishArgs& a, cudaStream_t st);
+
+}  // namespace blk
