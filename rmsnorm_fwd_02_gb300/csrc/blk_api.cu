@@ -64,17 +64,19 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Threads a row, vectors a thread and teams a CTA: functions of H (and of whether a warp may share
 // rows between its threads).
-Shape team_shape(int H, bool whole_warps) {
+Shape team_shape(int H, bool bwd, bool whole_warps) {
   Shape s{};
   const int nv = H / 8;
-  s.vpt = nv <= 32 ? 1 : 2;
-  const int per = (nv + s.vpt - 1) / s.vpt;
-  s.ntg = per <= 8 && !whole_warps    ? 8
-          : per <= 16 && !whole_warps ? 16
-                                      : static_cast<int>(ceil_div(per, 32)) * 32;
-  const int team = s.ntg < 32 ? 32 : s.ntg;
-  s.teams = kThreads / team;
-  if (s.teams > kMaxTeams) s.teams = kMaxTeams;
+  auto threads = [&](int vpt) {
+    const int per = (nv + vpt - 1) / vpt;
+    return per <= 8 && !whole_warps    ? 8
+           : per <= 16 && !whole_warps ? 16
+                                       : static_cast<int>(ceil_div(per, 32)) * 32;
+  };
+  // four vectors a thread, three where fewer places then stay empty; narrow rows one
+  s.vpt = nv <= 16 ? 1 : (3 * threads(3) < 4 * threads(4) ? 3 : 4);
+  s.ntg = threads(s.vpt);
+  s.teams = (bwd ? kBwdThreads : kFwdThreads) / (s.ntg < 32 ? 32 : s.ntg);
   return s;
 }
 
@@ -94,7 +96,7 @@ void spread(Shape& s, int64_t R) {
 
 size_t smem_bytes(const Shape& s) {
   const size_t n = static_cast<size_t>(s.teams) * s.stages;
-  return n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 32 * static_cast<size_t>(s.teams) + 16;
+  return n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 16;
 }
 
 namespace {
@@ -115,15 +117,16 @@ void ring(Shape& s, size_t row, size_t least) {
   s.smem = smem_bytes(s);
 }
 
-Shape plan(int H, int64_t R, bool whole_warps, size_t row, size_t least) {
-  Shape s = team_shape(H, whole_warps);
+Shape plan(int H, int64_t R, bool bwd, bool whole_warps, size_t row, size_t least) {
+  Shape s = team_shape(H, bwd, whole_warps);
   spread(s, R);
   ring(s, row, least);
   return s;
 }
 
+// Teams of the backward.
 int64_t all_teams(int64_t R, int32_t H, bool whole_warps) {
-  Shape s = team_shape(H, whole_warps);
+  Shape s = team_shape(H, true, whole_warps);
   spread(s, R);
   return static_cast<int64_t>(s.P) * s.teams;
 }
@@ -189,7 +192,7 @@ int run_fwd(const Fwd& f, void* stream) {
   if (st != RMSN_OK) return st;
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
-  const Shape s = plan(f.H, f.R, false, f.residual != nullptr ? 2 * row : row, row);
+  const Shape s = plan(f.H, f.R, false, false, f.residual != nullptr ? 2 * row : row, row);
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -269,7 +272,7 @@ int run_bwd(const Bwd& b, void* stream) {
   size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
-  const Shape s = plan(b.H, b.R, whole_warps, row, least);
+  const Shape s = plan(b.H, b.R, true, whole_warps, row, least);
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
   const int64_t teams = static_cast<int64_t>(s.P) * s.teams;
@@ -518,8 +521,9 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   if (R == 0) return RMSN_ERR_INVALID_ARG;
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
-  const Shape s = backward ? plan(H, R, N > 1, 2 * wide + 2 * saved, wide < saved ? wide : saved)
-                           : plan(H, R, false, 2 * wide, wide);
+  const Shape s = backward ? plan(H, R, true, N > 1, 2 * wide + 2 * saved,
+                                  wide < saved ? wide : saved)
+                           : plan(H, R, false, false, 2 * wide, wide);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

@@ -18,15 +18,16 @@
 
 namespace blk {
 
-// Vector c of a staged row: 16-bit values, or 8-bit numbers with their block's scale.
+// Vector c of a staged row: 16-bit values, or 8-bit numbers; their values are v * the unit that is
+// returned (a vector lies in one block, so the unit can go to what the numbers are multiplied by).
 template <typename T, bool kPacked>
-__device__ __forceinline__ void load_saved(const Args& a, uint32_t at, int c, f2 (&v)[4]) {
+__device__ __forceinline__ float load_saved(const Args& a, uint32_t at, int c, f2 (&v)[4]) {
   if constexpr (kPacked) {
-    const uint2 q = lds64_at(at + 8u * c);
-    const uint32_t s = lds8_at(at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2));
-    act8_unpack8(q, act8_unit(s), v);
+    act8_numbers8(lds64_at(at + 8u * c), v);
+    return act8_unit(lds8_at(at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2)));
   } else {
     VecOf<T>::unpack(lds128_at(at + 16u * c), v);
+    return 1.f;
   }
 }
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ void write_sums(const Args& a, const Team& t, float* 
 }
 
 template <typename T, int VPT, int kForm, bool kPacked>
-__global__ void __launch_bounds__(kThreads, 1) blk_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   constexpr bool kX = kForm != kKeep;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -119,33 +120,53 @@ __global__ void __launch_bounds__(kThreads, 1) blk_bwd_kernel(const BwdArgs a) {
       }
       const float r1 = r1_next, r2 = r2_next;
       fetch(i + step < n ? row + step : ra + a.rows + t.sub);
-      f2 ncr2 = f2_splat(0.f);
-      const f2 r2v = f2_splat(r2);
+      // Packed vectors stay in registers between the passes over a row (h, then x in its place):
+      // their unpacking is three times that of 16-bit values, which are read again.
+      f2 kept[kPacked ? VPT : 1][4];
+      float unit[kPacked ? VPT : 1];
+      f2 nc2 = f2_splat(0.f);
       if constexpr (kPreN) {
+        float dot = 0.f;
         f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
           if (c < NV && valid) {
             f2 h[4], dy[4];
-            load_saved<T, kPacked>(a, hs, c, h);
+            const float u = load_saved<T, kPacked>(a, hs, c, h);
             VecOf<T>::unpack(lds128_at(dys + 16u * c), dy);
+            if constexpr (kPacked) {
+              dot0 = f2_mul(f2_mul(dy[0], w[v][0]), h[0]);
+              dot1 = f2_mul(f2_mul(dy[1], w[v][1]), h[1]);
+              dot0 = f2_fma(f2_mul(dy[2], w[v][2]), h[2], dot0);
+              dot1 = f2_fma(f2_mul(dy[3], w[v][3]), h[3], dot1);
+              const f2 d = f2_add(dot0, dot1);
+              dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
+              unit[v] = u;
 #pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              dot0 = f2_fma(f2_mul(dy[q], w[v][q]), h[q], dot0);
-              dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), h[q + 1], dot1);
+              for (int q = 0; q < 4; ++q) kept[v][q] = h[q];
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                dot0 = f2_fma(f2_mul(dy[q], w[v][q]), h[q], dot0);
+                dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), h[q + 1], dot1);
+              }
             }
           }
         }
-        const f2 d = f2_add(dot0, dot1);
-        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
+        if constexpr (!kPacked) {
+          const f2 d = f2_add(dot0, dot1);
+          dot = f2_lo(d) + f2_hi(d);
+        }
+        dot = row_sum(a, t, dot);
         if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<4>(a, t, j - 1 + a.stages, pol);
         // t = r2 (dy w - h (mean r2^2)): the mean's factor times r2, on t's scale
-        ncr2 = f2_splat(-(dot * (r2 * inv_h)) * r2);
+        nc2 = f2_splat(-(dot * (r2 * inv_h)) * r2);
       }
+      const f2 r2v = f2_splat(r2), r1v = f2_splat(r1);
       f2 m[VPT][4];
-      const f2 r1v = f2_splat(r1);
+      float dot = 0.f;
       f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
@@ -154,12 +175,20 @@ __global__ void __launch_bounds__(kThreads, 1) blk_bwd_kernel(const BwdArgs a) {
           f2 g[4];
           if constexpr (kPreN) {
             f2 h[4], dy[4];
-            load_saved<T, kPacked>(a, hs, c, h);
+            f2 nc = nc2, rh = r2v;
+            if constexpr (kPacked) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) h[q] = kept[v][q];
+              nc = f2_mul(nc2, f2_splat(unit[v]));
+              rh = f2_mul(r2v, f2_splat(unit[v]));
+            } else {
+              load_saved<T, kPacked>(a, hs, c, h);
+            }
             VecOf<T>::unpack(lds128_at(dys + 16u * c), dy);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              g[q] = f2_mul(f2_fma(h[q], ncr2, f2_mul(dy[q], w[v][q])), r2v);
-              sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], r2v), sum_pre[v][q]);
+              g[q] = f2_mul(f2_fma(h[q], nc, f2_mul(dy[q], w[v][q])), r2v);
+              sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
             }
           }
           if (!kPreN || has_dh) {
@@ -175,17 +204,30 @@ __global__ void __launch_bounds__(kThreads, 1) blk_bwd_kernel(const BwdArgs a) {
           stg128(static_cast<T*>(a.dres) + out, VecOf<T>::pack(o));
           if constexpr (kX) {
             f2 x[4];
-            load_saved<T, kPacked>(a, xs, c, x);
+            const float u = load_saved<T, kPacked>(a, xs, c, x);
+            f2 rx = kPostN ? r1v : f2_splat(1.f);
+            if constexpr (kPacked) rx = f2_mul(rx, f2_splat(u));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const f2 xh = kPostN ? f2_mul(x[q], r1v) : x[q];
+              const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
               sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
               m[v][q] = f2_mul(g[q], k1[v][q]);
-              if constexpr (kPostN) {
-                if (q & 1)
-                  dot1 = f2_fma(m[v][q], x[q], dot1);
-                else
-                  dot0 = f2_fma(m[v][q], x[q], dot0);
+            }
+            if constexpr (kPostN && kPacked) {
+              dot0 = f2_mul(m[v][0], x[0]);
+              dot1 = f2_mul(m[v][1], x[1]);
+              dot0 = f2_fma(m[v][2], x[2], dot0);
+              dot1 = f2_fma(m[v][3], x[3], dot1);
+              const f2 d = f2_add(dot0, dot1);
+              dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
+              unit[v] = u;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) kept[v][q] = x[q];
+            } else if constexpr (kPostN) {
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                dot0 = f2_fma(m[v][q], x[q], dot0);
+                dot1 = f2_fma(m[v][q + 1], x[q + 1], dot1);
               }
             }
           } else {
@@ -197,19 +239,29 @@ __global__ void __launch_bounds__(kThreads, 1) blk_bwd_kernel(const BwdArgs a) {
         }
       }
       if constexpr (kPostN) {
-        const f2 d = f2_add(dot0, dot1);
-        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
+        if constexpr (!kPacked) {
+          const f2 d = f2_add(dot0, dot1);
+          dot = f2_lo(d) + f2_hi(d);
+        }
+        dot = row_sum(a, t, dot);
         if (!kPreN && i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<4>(a, t, j - 1 + a.stages, pol);
-        const f2 ncr1 = f2_splat(-(dot * (r1 * inv_h)) * r1);
+        const f2 nc1 = f2_splat(-(dot * (r1 * inv_h)) * r1);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
           if (c < NV && valid) {
             f2 x[4], o[4];
-            load_saved<T, kPacked>(a, xs, c, x);
+            f2 nc = nc1;
+            if constexpr (kPacked) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], ncr1, m[v][q]), r1v);
+              for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
+              nc = f2_mul(nc1, f2_splat(unit[v]));
+            } else {
+              load_saved<T, kPacked>(a, xs, c, x);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc, m[v][q]), r1v);
             stg128(static_cast<T*>(a.dx) + static_cast<size_t>(row) * a.H + 8 * c, VecOf<T>::pack(o));
           }
         }
@@ -251,7 +303,9 @@ const void* pick_bwd(int form, bool packed) {
 
 template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
-  const void* fn = s.vpt == 1 ? pick_bwd<T, 1>(form, packed) : pick_bwd<T, 2>(form, packed);
+  const void* fn = s.vpt == 1   ? pick_bwd<T, 1>(form, packed)
+                   : s.vpt == 3 ? pick_bwd<T, 3>(form, packed)
+                                : pick_bwd<T, 4>(form, packed);
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   BwdArgs copy = a;

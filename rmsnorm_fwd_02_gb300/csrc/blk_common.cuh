@@ -4,7 +4,7 @@
 // in shared memory that bulk asynchronous copies fill; the team's first thread starts a slot's
 // next copies as soon as the team is known to be done with it: one-warp teams after a __syncwarp
 // behind the slot, others behind the next slot's first reduction, whose barrier every warp reaches
-// only after its last read.  There is no producer warp, so 16 warps of 128 registers fill an SM, and
+// only after its last read.  There is no producer warp, and
 // a slot is held for one row's work only: the rest of the ring is on its way.
 #pragma once
 
@@ -72,7 +72,7 @@ __device__ __forceinline__ float sum8(const f2 (&f)[4]) {
 struct Team {
   uint32_t ring;        // shared address of the team's slots
   uint64_t* full;       // its barriers
-  float* red;           // [2][16]: warp sums, taken in turns
+  float* red;           // [2][12]: warp sums, taken in turns
   volatile int* abort_flag;
   int32_t r0, r1;       // rows
   int32_t nslots;
@@ -155,8 +155,9 @@ __device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, u
   uint64_t* full = reinterpret_cast<uint64_t*>(behind);
   t.full = full + t.team * a.stages;
   float* red = reinterpret_cast<float*>(behind + ((8 * a.teams * a.stages + 15) & ~15));
-  t.red = red + 32 * t.team;
-  t.abort_flag = reinterpret_cast<volatile int*>(red + 32 * a.teams);
+  t.red = red + 2 * kMaxWarps * t.team;
+  t.abort_flag = reinterpret_cast<volatile int*>(red + 2 * kMaxWarps * a.teams);
+  for (int i = tid; i < 2 * kMaxWarps * a.teams; i += static_cast<int>(blockDim.x)) red[i] = 0.f;
   for (int i = tid; i < a.teams * a.stages; i += static_cast<int>(blockDim.x)) mbar_init(&full[i], 1u);
   if (tid == 0) *t.abort_flag = 0;
   fence_barrier_init();
@@ -186,11 +187,33 @@ __device__ __forceinline__ void drain(const Args& a, const Team& t) {
 __device__ __forceinline__ float row_sum(const Args& a, Team& t, float v) {
   if (a.ntg <= 32) return subwarp_allsum(v, a.ntg);
   v = warp_allsum(v);
-  float* red = t.red + 16 * t.turn;
+  float* red = t.red + kMaxWarps * t.turn;
   t.turn ^= 1;
   if ((threadIdx.x & 31) == 0) red[t.lt >> 5] = v;
   named_bar_sync(static_cast<uint32_t>(t.team) + 1u, static_cast<uint32_t>(a.ntg));
-  return slot_sum(red, t.warps);
+  // places behind the team's warps hold zeros
+  const float4* q = reinterpret_cast<const float4*>(red);
+  float4 s = q[0];
+  v = (s.x + s.y) + (s.z + s.w);
+  if (t.warps > 4) {
+    s = q[1];
+    v += (s.x + s.y) + (s.z + s.w);
+    if (t.warps > 8) {
+      s = q[2];
+      v += (s.x + s.y) + (s.z + s.w);
+    }
+  }
+  return v;
+}
+
+// 1 / sqrt(sum / H + eps): the hardware's estimate and one Newton step, within two units of the
+// last place (the correctly rounded root takes some twenty instructions a row and thread more).
+// A mean of 0 (with eps 0), infinity or NaN keeps the estimate: infinity, 0, NaN.
+__device__ __forceinline__ float row_rstd(float sum, float inv_h, float eps) {
+  const float m = __fmaf_rn(sum, inv_h, eps);
+  const float y = rsqrtf(m);
+  const float e = __fmaf_rn(-m * y, y, 1.f);
+  return e == e && fabsf(e) < 1.f ? __fmaf_rn(0.5f * y, e, y) : y;
 }
 
 }  // namespace blk

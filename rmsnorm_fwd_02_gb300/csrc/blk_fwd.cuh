@@ -11,21 +11,20 @@
 
 namespace blk {
 
-// One 16-byte vector's values, packed into its row; every lane of the warp takes part (`live`:
-// the vector exists).
-__device__ __forceinline__ void keep8(const Args& a, unsigned char* packed, int64_t row, int c,
-                                      bool live, const f2 (&v)[4]) {
-  const uint32_t amax = act8_max_block(live ? act8_max8(v) : 0u);
+// One 16-byte vector, packed into its row; every lane of the warp takes part (`live`: the vector
+// exists).
+template <typename T>
+__device__ __forceinline__ void keep8(unsigned char* packed_row, int first_scale, int c, bool live,
+                                      const uint4& u) {
+  const uint4 one[1] = {u};
+  const uint32_t amax = act8_max_block(live ? act8_max8<T>(one) : 0u);
+  if (!live) return;
   const uint32_t s = act8_scale_byte(amax);
-  if (packed == nullptr) return;
-  unsigned char* p = packed + row * act8_row_size(a.H);
-  const int first = static_cast<int>(act8_scale_offset(a.H));
-  if (live) *reinterpret_cast<uint2*>(p + 8 * c) = act8_pack8(v, amax, s);
-  if (live && (c & 3) == 0) p[first + (c >> 2)] = static_cast<unsigned char>(s);
+  *reinterpret_cast<uint2*>(packed_row + 8 * c) = act8_pack8<T>(u, amax, s);
+  if ((c & 3) == 0) packed_row[first_scale + (c >> 2)] = static_cast<unsigned char>(s);
 }
 // A packed row's padding (one thread).
-__device__ __forceinline__ void keep8_padding(const Args& a, unsigned char* packed, int64_t row) {
-  unsigned char* p = packed + row * act8_row_size(a.H);
+__device__ __forceinline__ void keep8_padding(const Args& a, unsigned char* p) {
   const int first = static_cast<int>(act8_scale_offset(a.H));
   for (int i = a.H; i < first; ++i) p[i] = 0;
   const int end = static_cast<int>(act8_row_size(a.H));
@@ -33,7 +32,7 @@ __device__ __forceinline__ void keep8_padding(const Args& a, unsigned char* pack
 }
 
 template <typename T, int VPT, int kForm, bool kPack>
-__global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint64_t pol = l2_evict_first_policy();
@@ -49,9 +48,12 @@ __global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
     }
   }
   int32_t next_sample = 0;  // the row from which k1 is another sample's
-  const float hf = static_cast<float>(a.H);
+  const float inv_h = 1.f / static_cast<float>(a.H);
   const f2 rscale = f2_splat(a.residual_scale);
   const int step = a.ntg < 32 ? 32 / a.ntg : 1;
+  const int64_t packed_row = act8_row_size(a.H);
+  const int first_scale = static_cast<int>(act8_scale_offset(a.H));
+  const bool padded = a.H % 512 != 0;  // numbers and scales are not both whole 16 bytes
   int s = 0;
   uint32_t parity = 0;
   for (int32_t j = 0; j < t.nslots; ++j) {
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
         const float sum = row_sum(a, t, f2_lo(ss) + f2_hi(ss));
         if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<2>(a, t, j - 1 + a.stages, pol);
-        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, hf), a.eps));
+        const float r = row_rstd(sum, inv_h, a.eps);
         if (valid && t.lt == 0) a.rstd_post[row] = r;
         r1 = f2_splat(r);
       }
@@ -97,10 +99,11 @@ __global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
       for (int v = 0; v < VPT; ++v) {
         const int c = t.lt + v * a.ntg;
         const bool live = valid && c < NV;
-        f2 x[4], written[4];
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        uint4 xw = make_uint4(0u, 0u, 0u, 0u), o = xw;
         if (c < NV) {
-          VecOf<T>::unpack(lds128_at(xs + 16u * c), x);
+          f2 x[4];
+          xw = lds128_at(xs + 16u * c);
+          VecOf<T>::unpack(xw, x);
           f2 res[4];
           if (kForm != kKeep || a.in[1].p != nullptr) VecOf<T>::unpack(lds128_at(rs + 16u * c), res);
 #pragma unroll
@@ -113,11 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
             }
           }
           o = VecOf<T>::pack(h[v]);
-          VecOf<T>::unpack(o, written);
-          if constexpr (kForm == kKeep) {  // the norm is taken of h as it is written
-#pragma unroll
-            for (int q = 0; q < 4; ++q) h[v][q] = written[q];
-          }
+          if constexpr (kForm == kKeep) VecOf<T>::unpack(o, h[v]);  // the norm of h as it is written
           if constexpr (kPreN) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) ss = f2_fma(h[v][q], h[v][q], ss);
@@ -126,21 +125,22 @@ __global__ void __launch_bounds__(kThreads, 1) blk_fwd_kernel(const FwdArgs a) {
             stg128(static_cast<T*>(a.h) + static_cast<size_t>(row) * a.H + 8 * c, o);
         }
         if constexpr (kPack) {
-          if constexpr (kForm != kKeep) keep8(a, a.x8, row, c, live, x);
-          if constexpr (kPreN) keep8(a, a.h8, row, c, live, written);
+          if (kForm != kKeep && a.x8 != nullptr)
+            keep8<T>(a.x8 + row * packed_row, first_scale, c, live, xw);
+          if constexpr (kPreN) keep8<T>(a.h8 + row * packed_row, first_scale, c, live, o);
         }
       }
       if constexpr (kPack) {
-        if (valid && t.lt == 0) {
-          if (kForm != kKeep && a.x8 != nullptr) keep8_padding(a, a.x8, row);
-          if (kPreN) keep8_padding(a, a.h8, row);
+        if (padded && valid && t.lt == 0) {
+          if (kForm != kKeep && a.x8 != nullptr) keep8_padding(a, a.x8 + row * packed_row);
+          if (kPreN) keep8_padding(a, a.h8 + row * packed_row);
         }
       }
       if constexpr (kPreN) {
         const float sum = row_sum(a, t, f2_lo(ss) + f2_hi(ss));
         if (!kPostN && i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<2>(a, t, j - 1 + a.stages, pol);
-        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, hf), a.eps));
+        const float r = row_rstd(sum, inv_h, a.eps);
         if (valid && t.lt == 0) a.rstd_pre[row] = r;
         const f2 r2 = f2_splat(r);
 #pragma unroll
@@ -185,7 +185,9 @@ const void* pick_fwd(int form, bool pack) {
 
 template <typename T>
 cudaError_t launch_fwd_t(const FwdArgs& a, const Shape& s, int form, bool pack, cudaStream_t st) {
-  const void* fn = s.vpt == 1 ? pick_fwd<T, 1>(form, pack) : pick_fwd<T, 2>(form, pack);
+  const void* fn = s.vpt == 1   ? pick_fwd<T, 1>(form, pack)
+                   : s.vpt == 3 ? pick_fwd<T, 3>(form, pack)
+                                : pick_fwd<T, 4>(form, pack);
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   FwdArgs copy = a;

@@ -9,8 +9,13 @@
 namespace blk {
 
 constexpr int kMaxH = 8192;
-constexpr int kThreads = 512;     // most threads of a CTA, one CTA an SM: 128 registers a thread
-constexpr int kMaxTeams = 16;
+// Most threads of a CTA, one CTA an SM.  A row costs a thread some 150 instructions (its waits,
+// the two sums' reduction, rstd, addresses) whatever its share of the row, so threads own 32
+// elements where the row has them, with the registers that takes: 168 in the forward, 255 in the
+// backward, whose column sums, weights and waiting gradient are 160.
+constexpr int kFwdThreads = 384;
+constexpr int kBwdThreads = 256;
+constexpr int kMaxWarps = kFwdThreads / 32;
 constexpr int kMaxTensors = 4;    // staged
 // CTAs of the backward at most, whatever the GPU: the rows' partition, and with it the order of
 // every sum, is a function of the shape.  GB300 has 152 SMs: there it is one wave.
@@ -31,7 +36,7 @@ enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
 // warps) takes one row (or those of its warp) at a time from its own ring of `stages` slots, each
 // of `steps` such takes.
 struct Shape {
-  int vpt;      // 16-byte vectors (8 elements) a thread: 1 or 2
+  int vpt;      // 16-byte vectors (8 elements) a thread: 1, 3 or 4
   int ntg;      // threads a row
   int teams;    // teams (of whole warps) a CTA
   int rows;     // rows a slot
