@@ -64,7 +64,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Threads a row, vectors a thread and teams a CTA: functions of H (and of whether a warp may share
 // rows between its threads).
-Shape team_shape(int H, bool bwd, bool whole_warps) {
+Shape team_shape(int H, int threads_cta, bool whole_warps) {
   Shape s{};
   const int nv = H / 8;
   auto threads = [&](int vpt) {
@@ -76,7 +76,7 @@ Shape team_shape(int H, bool bwd, bool whole_warps) {
   // four vectors a thread, three where fewer places then stay empty; narrow rows one
   s.vpt = nv <= 16 ? 1 : (3 * threads(3) < 4 * threads(4) ? 3 : 4);
   s.ntg = threads(s.vpt);
-  s.teams = (bwd ? kBwdThreads : kFwdThreads) / (s.ntg < 32 ? 32 : s.ntg);
+  s.teams = threads_cta / (s.ntg < 32 ? 32 : s.ntg);
   return s;
 }
 
@@ -117,16 +117,16 @@ void ring(Shape& s, size_t row, size_t least) {
   s.smem = smem_bytes(s);
 }
 
-Shape plan(int H, int64_t R, bool bwd, bool whole_warps, size_t row, size_t least) {
-  Shape s = team_shape(H, bwd, whole_warps);
+Shape plan(int H, int64_t R, int threads_cta, bool whole_warps, size_t row, size_t least) {
+  Shape s = team_shape(H, threads_cta, whole_warps);
   spread(s, R);
   ring(s, row, least);
   return s;
 }
 
-// Teams of the backward.
-int64_t all_teams(int64_t R, int32_t H, bool whole_warps) {
-  Shape s = team_shape(H, true, whole_warps);
+// Teams of the backward's form.
+int64_t all_teams(int64_t R, int32_t H, int form, bool whole_warps) {
+  Shape s = team_shape(H, bwd_threads(form), whole_warps);
   spread(s, R);
   return static_cast<int64_t>(s.P) * s.teams;
 }
@@ -192,7 +192,7 @@ int run_fwd(const Fwd& f, void* stream) {
   if (st != RMSN_OK) return st;
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
-  const Shape s = plan(f.H, f.R, false, false, f.residual != nullptr ? 2 * row : row, row);
+  const Shape s = plan(f.H, f.R, kFwdThreads, false, f.residual != nullptr ? 2 * row : row, row);
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -240,8 +240,9 @@ size_t s_floats(int64_t teams, int32_t H, int64_t N) {
   return static_cast<size_t>(teams + N - 1) * H;
 }
 size_t workspace_bytes(int64_t R, int32_t H, int64_t N) {
-  const int64_t teams = all_teams(R, H, N > 1);
-  return sizeof(float) * (part_floats(teams, H) + s_floats(teams, H, N));
+  const int64_t teams = all_teams(R, H, kBoth, N > 1), keep = all_teams(R, H, kKeep, false);
+  const size_t both = part_floats(teams, H) + s_floats(teams, H, N), one = part_floats(keep, H);
+  return sizeof(float) * (both > one ? both : one);
 }
 
 int run_bwd(const Bwd& b, void* stream) {
@@ -272,7 +273,7 @@ int run_bwd(const Bwd& b, void* stream) {
   size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
-  const Shape s = plan(b.H, b.R, true, whole_warps, row, least);
+  const Shape s = plan(b.H, b.R, bwd_threads(b.form), whole_warps, row, least);
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
   const int64_t teams = static_cast<int64_t>(s.P) * s.teams;
@@ -359,7 +360,7 @@ int rmsnorm_act8_train_fwd(const void* x, const void* residual, int dtype, const
 
 size_t rmsnorm_act8_train_bwd_workspace_bytes(int64_t R, int32_t H) {
   if (check_sizes(R, H, 1) != RMSN_OK || R == 0) return 0;
-  return sizeof(float) * part_floats(all_teams(R, H, false), H);
+  return sizeof(float) * part_floats(all_teams(R, H, kKeep, false), H);
 }
 
 int rmsnorm_act8_train_bwd(const void* packed, const void* dy, const void* dh, int dtype,
@@ -521,9 +522,9 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   if (R == 0) return RMSN_ERR_INVALID_ARG;
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
-  const Shape s = backward ? plan(H, R, true, N > 1, 2 * wide + 2 * saved,
+  const Shape s = backward ? plan(H, R, bwd_threads(kBoth), N > 1, 2 * wide + 2 * saved,
                                   wide < saved ? wide : saved)
-                           : plan(H, R, false, false, 2 * wide, wide);
+                           : plan(H, R, kFwdThreads, false, 2 * wide, wide);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

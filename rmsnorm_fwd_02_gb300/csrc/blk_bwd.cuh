@@ -20,13 +20,19 @@ namespace blk {
 
 // Vector c of a staged row: 16-bit values, or 8-bit numbers; their values are v * the unit that is
 // returned (a vector lies in one block, so the unit can go to what the numbers are multiplied by).
-template <typename T, bool kPacked>
-__device__ __forceinline__ float load_saved(const Args& a, uint32_t at, int c, f2 (&v)[4]) {
+template <typename T, bool kPacked, bool kEven>
+__device__ __forceinline__ float load_saved(const Args& a, uint32_t at, int c, bool live, f2 (&v)[4]) {
   if constexpr (kPacked) {
-    act8_numbers8(lds64_at(at + 8u * c), v);
-    return act8_unit(lds8_at(at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2)));
+    uint2 q = make_uint2(0u, 0u);
+    uint32_t scale = 0u;
+    if (kEven || live) {
+      q = lds64_at(at + 8u * c);
+      scale = lds8_at(at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2));
+    }
+    act8_numbers8(q, v);
+    return act8_unit(scale);
   } else {
-    VecOf<T>::unpack(lds128_at(at + 16u * c), v);
+    VecOf<T>::unpack(lds128_if<kEven>(at + 16u * c, live), v);
     return 1.f;
   }
 }
@@ -55,8 +61,8 @@ __device__ __forceinline__ void write_sums(const Args& a, const Team& t, float* 
   }
 }
 
-template <typename T, int VPT, int kForm, bool kPacked>
-__global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a) {
+template <typename T, int VPT, int kForm, bool kPacked, bool kEven>
+__global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const BwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   constexpr bool kX = kForm != kKeep;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -73,7 +79,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a
       sum_s[v][q] = f2_splat(0.f);
     }
     if constexpr (kPreN) {
-      if (c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[v][q] = f2_splat(0.f);
+      if (kEven || c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
     }
   }
   const float inv_h = 1.f / static_cast<float>(a.H);
@@ -102,7 +110,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a
     const int32_t n = min(a.rows, t.r1 - ra);
     for (int32_t i = 0; i < n; i += step) {
       const int32_t row = ra + i + t.sub;
-      const bool valid = i + t.sub < n;
+      const bool valid = kEven || i + t.sub < n;
       const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
       const uint32_t at = static_cast<uint32_t>(i + t.sub);
       const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
@@ -131,26 +139,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
-          if (c < NV && valid) {
-            f2 h[4], dy[4];
-            const float u = load_saved<T, kPacked>(a, hs, c, h);
-            VecOf<T>::unpack(lds128_at(dys + 16u * c), dy);
-            if constexpr (kPacked) {
-              dot0 = f2_mul(f2_mul(dy[0], w[v][0]), h[0]);
-              dot1 = f2_mul(f2_mul(dy[1], w[v][1]), h[1]);
-              dot0 = f2_fma(f2_mul(dy[2], w[v][2]), h[2], dot0);
-              dot1 = f2_fma(f2_mul(dy[3], w[v][3]), h[3], dot1);
-              const f2 d = f2_add(dot0, dot1);
-              dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
-              unit[v] = u;
+          const bool live = kEven || (valid && c < NV);
+          f2 h[4], dy[4];
+          const float u = load_saved<T, kPacked, kEven>(a, hs, c, live, h);
+          VecOf<T>::unpack(lds128_if<kEven>(dys + 16u * c, live), dy);
+          if constexpr (kPacked) {
+            dot0 = f2_mul(f2_mul(dy[0], w[v][0]), h[0]);
+            dot1 = f2_mul(f2_mul(dy[1], w[v][1]), h[1]);
+            dot0 = f2_fma(f2_mul(dy[2], w[v][2]), h[2], dot0);
+            dot1 = f2_fma(f2_mul(dy[3], w[v][3]), h[3], dot1);
+            const f2 d = f2_add(dot0, dot1);
+            dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
+            unit[v] = u;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) kept[v][q] = h[q];
-            } else {
+            for (int q = 0; q < 4; ++q) kept[v][q] = h[q];
+          } else {
 #pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                dot0 = f2_fma(f2_mul(dy[q], w[v][q]), h[q], dot0);
-                dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), h[q + 1], dot1);
-              }
+            for (int q = 0; q < 4; q += 2) {
+              dot0 = f2_fma(f2_mul(dy[q], w[v][q]), h[q], dot0);
+              dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), h[q + 1], dot1);
             }
           }
         }
@@ -168,75 +175,78 @@ __global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a
       f2 m[VPT][4];
       float dot = 0.f;
       f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
+      const size_t out_row = static_cast<size_t>(row) * a.H;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = t.lt + v * a.ntg;
-        if (c < NV && valid) {
-          f2 g[4];
-          if constexpr (kPreN) {
-            f2 h[4], dy[4];
-            f2 nc = nc2, rh = r2v;
-            if constexpr (kPacked) {
+        const bool live = kEven || (valid && c < NV);
+        f2 g[4];
+        if constexpr (kPreN) {
+          f2 h[4], dy[4];
+          f2 nc = nc2, rh = r2v;
+          if constexpr (kPacked) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) h[q] = kept[v][q];
-              nc = f2_mul(nc2, f2_splat(unit[v]));
-              rh = f2_mul(r2v, f2_splat(unit[v]));
-            } else {
-              load_saved<T, kPacked>(a, hs, c, h);
-            }
-            VecOf<T>::unpack(lds128_at(dys + 16u * c), dy);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              g[q] = f2_mul(f2_fma(h[q], nc, f2_mul(dy[q], w[v][q])), r2v);
-              sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
-            }
-          }
-          if (!kPreN || has_dh) {
-            f2 dh[4];
-            VecOf<T>::unpack(lds128_at(dhs + 16u * c), dh);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_add(g[q], dh[q]) : dh[q];
-          }
-          f2 o[4];
-          const size_t out = static_cast<size_t>(row) * a.H + 8 * c;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], rscale);
-          stg128(static_cast<T*>(a.dres) + out, VecOf<T>::pack(o));
-          if constexpr (kX) {
-            f2 x[4];
-            const float u = load_saved<T, kPacked>(a, xs, c, x);
-            f2 rx = kPostN ? r1v : f2_splat(1.f);
-            if constexpr (kPacked) rx = f2_mul(rx, f2_splat(u));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
-              sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
-              m[v][q] = f2_mul(g[q], k1[v][q]);
-            }
-            if constexpr (kPostN && kPacked) {
-              dot0 = f2_mul(m[v][0], x[0]);
-              dot1 = f2_mul(m[v][1], x[1]);
-              dot0 = f2_fma(m[v][2], x[2], dot0);
-              dot1 = f2_fma(m[v][3], x[3], dot1);
-              const f2 d = f2_add(dot0, dot1);
-              dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
-              unit[v] = u;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) kept[v][q] = x[q];
-            } else if constexpr (kPostN) {
-#pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                dot0 = f2_fma(m[v][q], x[q], dot0);
-                dot1 = f2_fma(m[v][q + 1], x[q + 1], dot1);
-              }
-            }
+            for (int q = 0; q < 4; ++q) h[q] = kept[v][q];
+            nc = f2_mul(nc2, f2_splat(unit[v]));
+            rh = f2_mul(r2v, f2_splat(unit[v]));
           } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m[v][q] = f2_mul(g[q], f2_splat(a.scale));
+            load_saved<T, kPacked, kEven>(a, hs, c, live, h);
           }
-          if (!kPostN && a.dx != nullptr)
-            stg128(static_cast<T*>(a.dx) + out, VecOf<T>::pack(m[v]));
+          VecOf<T>::unpack(lds128_if<kEven>(dys + 16u * c, live), dy);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            g[q] = f2_mul(f2_fma(h[q], nc, f2_mul(dy[q], w[v][q])), r2v);
+            const f2 sum = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
+            if (live) sum_pre[v][q] = sum;
+          }
         }
+        if (!kPreN || has_dh) {
+          f2 dh[4];
+          VecOf<T>::unpack(lds128_if<kEven>(dhs + 16u * c, live), dh);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_add(g[q], dh[q]) : dh[q];
+        }
+        f2 o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], rscale);
+        if (live) stg128(static_cast<T*>(a.dres) + out_row + 8 * c, VecOf<T>::pack(o));
+        if constexpr (kX) {
+          f2 x[4];
+          const float u = load_saved<T, kPacked, kEven>(a, xs, c, live, x);
+          f2 rx = kPostN ? r1v : f2_splat(1.f);
+          if constexpr (kPacked) rx = f2_mul(rx, f2_splat(u));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
+            const f2 sum = f2_fma(g[q], xh, sum_s[v][q]);
+            if (live) sum_s[v][q] = sum;
+            m[v][q] = f2_mul(g[q], k1[v][q]);
+            // (a row's infinities and NaN stay in it: vectors that are not there add nothing)
+            if (!live) m[v][q] = f2_splat(0.f);
+          }
+          if constexpr (kPostN && kPacked) {
+            dot0 = f2_mul(m[v][0], x[0]);
+            dot1 = f2_mul(m[v][1], x[1]);
+            dot0 = f2_fma(m[v][2], x[2], dot0);
+            dot1 = f2_fma(m[v][3], x[3], dot1);
+            const f2 d = f2_add(dot0, dot1);
+            dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
+            unit[v] = u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) kept[v][q] = x[q];
+          } else if constexpr (kPostN) {
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              dot0 = f2_fma(m[v][q], x[q], dot0);
+              dot1 = f2_fma(m[v][q + 1], x[q + 1], dot1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) m[v][q] = f2_mul(g[q], f2_splat(a.scale));
+        }
+        if (!kPostN && live && (kX || a.dx != nullptr))
+          stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(m[v]));
       }
       if constexpr (kPostN) {
         if constexpr (!kPacked) {
@@ -250,20 +260,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
-          if (c < NV && valid) {
-            f2 x[4], o[4];
-            f2 nc = nc1;
-            if constexpr (kPacked) {
+          const bool live = kEven || (valid && c < NV);
+          f2 x[4], o[4];
+          f2 nc = nc1;
+          if constexpr (kPacked) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
-              nc = f2_mul(nc1, f2_splat(unit[v]));
-            } else {
-              load_saved<T, kPacked>(a, xs, c, x);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc, m[v][q]), r1v);
-            stg128(static_cast<T*>(a.dx) + static_cast<size_t>(row) * a.H + 8 * c, VecOf<T>::pack(o));
+            for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
+            nc = f2_mul(nc1, f2_splat(unit[v]));
+          } else {
+            load_saved<T, kPacked, kEven>(a, xs, c, live, x);
           }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc, m[v][q]), r1v);
+          if (live) stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(o));
         }
       }
     }
@@ -282,30 +291,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) blk_bwd_kernel(const BwdArgs a
   if constexpr (kX) write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, bool kEven>
 const void* pick_bwd(int form, bool packed) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+#define BLK_PICK(F)                                              \
+  (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven>)          \
+          : fn(&blk_bwd_kernel<T, VPT, F, false, kEven>))
   switch (form) {
-    case kKeep:
-      return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true>)
-                    : fn(&blk_bwd_kernel<T, VPT, kKeep, false>);
-    case kPre:
-      return packed ? fn(&blk_bwd_kernel<T, VPT, kPre, true>)
-                    : fn(&blk_bwd_kernel<T, VPT, kPre, false>);
-    case kBoth:
-      return packed ? fn(&blk_bwd_kernel<T, VPT, kBoth, true>)
-                    : fn(&blk_bwd_kernel<T, VPT, kBoth, false>);
-    default:
-      return packed ? fn(&blk_bwd_kernel<T, VPT, kPost, true>)
-                    : fn(&blk_bwd_kernel<T, VPT, kPost, false>);
+    case kKeep: return BLK_PICK(kKeep);
+    case kPre: return BLK_PICK(kPre);
+    case kBoth: return BLK_PICK(kBoth);
+    default: return BLK_PICK(kPost);
   }
+#undef BLK_PICK
 }
 
 template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
-  const void* fn = s.vpt == 1   ? pick_bwd<T, 1>(form, packed)
-                   : s.vpt == 3 ? pick_bwd<T, 3>(form, packed)
-                                : pick_bwd<T, 4>(form, packed);
+  const bool even = even_rows(a.H, s.vpt, s.ntg);
+  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed)
+                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed)
+                                        : pick_bwd<T, 3, false>(form, packed))
+                                : (even ? pick_bwd<T, 4, true>(form, packed)
+                                        : pick_bwd<T, 4, false>(form, packed));
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   BwdArgs copy = a;

@@ -39,6 +39,27 @@ __device__ __forceinline__ float load1(const void* p, int code, int64_t i) {
                    : widen1(static_cast<const __half*>(p)[i]);
 }
 
+// Whether every thread of a row has all its vectors, and every row of a warp is there: kernels are
+// built for that case apart, without a predicate on any vector.
+__host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
+  return ntg >= 32 && H == 8 * vpt * ntg;
+}
+
+// A 16-byte vector of shared memory; without kEven, zeros where it is not `live` (`at` is then not
+// read).
+template <bool kEven>
+__device__ __forceinline__ uint4 lds128_if(uint32_t at, bool live) {
+  if constexpr (kEven) return lds128_at(at);
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "r"(at), "r"(static_cast<uint32_t>(live)));
+  return v;
+}
+
 // scale * gate * w_post of a thread's columns (each factor where it is there), sample n's gate.
 template <int VPT, bool kPostW>
 __device__ __forceinline__ void load_factor(const Args& a, int32_t n, int lt, f2 (&k1)[VPT][4]) {

@@ -31,7 +31,7 @@ __device__ __forceinline__ void keep8_padding(const Args& a, unsigned char* p) {
   for (int i = first + (a.H + kAct8Block - 1) / kAct8Block; i < end; ++i) p[i] = 0;
 }
 
-template <typename T, int VPT, int kForm, bool kPack>
+template <typename T, int VPT, int kForm, bool kPack, bool kEven>
 __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -44,7 +44,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = t.lt + v * a.ntg;
-      if (c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[v][q] = f2_splat(0.f);
+      if (kEven || c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
     }
   }
   int32_t next_sample = 0;  // the row from which k1 is another sample's
@@ -62,7 +64,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
     const int32_t n = min(a.rows, t.r1 - ra);
     for (int32_t i = 0; i < n; i += step) {
       const int32_t row = ra + i + t.sub;
-      const bool valid = i + t.sub < n;
+      const bool valid = kEven || i + t.sub < n;
       const uint32_t slot = t.ring + static_cast<uint32_t>(s) * a.slot +
                             static_cast<uint32_t>(i + t.sub) * (static_cast<uint32_t>(a.H) * 2u);
       const uint32_t xs = slot + a.in[0].off, rs = slot + a.in[1].off;
@@ -79,12 +81,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
-          if (c < NV) {
-            f2 x[4];
-            VecOf<T>::unpack(lds128_at(xs + 16u * c), x);
+          f2 x[4];
+          VecOf<T>::unpack(lds128_if<kEven>(xs + 16u * c, c < NV), x);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ss = f2_fma(x[q], x[q], ss);
-          }
+          for (int q = 0; q < 4; ++q) ss = f2_fma(x[q], x[q], ss);
         }
         const float sum = row_sum(a, t, f2_lo(ss) + f2_hi(ss));
         if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
@@ -98,32 +98,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = t.lt + v * a.ntg;
-        const bool live = valid && c < NV;
-        uint4 xw = make_uint4(0u, 0u, 0u, 0u), o = xw;
-        if (c < NV) {
-          f2 x[4];
-          xw = lds128_at(xs + 16u * c);
-          VecOf<T>::unpack(xw, x);
-          f2 res[4];
-          if (kForm != kKeep || a.in[1].p != nullptr) VecOf<T>::unpack(lds128_at(rs + 16u * c), res);
+        const bool there = kEven || c < NV, live = valid && there;
+        f2 x[4], res[4];
+        const uint4 xw = lds128_if<kEven>(xs + 16u * c, there);
+        VecOf<T>::unpack(xw, x);
+        const bool add = kForm != kKeep || a.in[1].p != nullptr;
+        if (add) VecOf<T>::unpack(lds128_if<kEven>(rs + 16u * c, there), res);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (kForm == kKeep) {
-              h[v][q] = a.in[1].p != nullptr ? f2_add(x[q], res[q]) : x[q];
-            } else {
-              const f2 p = kPostN ? f2_mul(x[q], r1) : x[q];
-              h[v][q] = f2_fma(p, k1[v][q], f2_mul(res[q], rscale));
-            }
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (kForm == kKeep) {
+            h[v][q] = add ? f2_add(x[q], res[q]) : x[q];
+          } else {
+            const f2 p = kPostN ? f2_mul(x[q], r1) : x[q];
+            h[v][q] = f2_fma(p, k1[v][q], f2_mul(res[q], rscale));
           }
-          o = VecOf<T>::pack(h[v]);
-          if constexpr (kForm == kKeep) VecOf<T>::unpack(o, h[v]);  // the norm of h as it is written
-          if constexpr (kPreN) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ss = f2_fma(h[v][q], h[v][q], ss);
-          }
-          if (live && a.h != nullptr)
-            stg128(static_cast<T*>(a.h) + static_cast<size_t>(row) * a.H + 8 * c, o);
         }
+        const uint4 o = VecOf<T>::pack(h[v]);
+        if constexpr (kForm == kKeep) VecOf<T>::unpack(o, h[v]);  // the norm of h as it is written
+        if constexpr (kPreN) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ss = f2_fma(h[v][q], h[v][q], ss);
+        }
+        if (live && (kForm != kKeep || add))
+          stg128(static_cast<T*>(a.h) + static_cast<size_t>(row) * a.H + 8 * c, o);
         if constexpr (kPack) {
           if (kForm != kKeep && a.x8 != nullptr)
             keep8<T>(a.x8 + row * packed_row, first_scale, c, live, xw);
@@ -146,12 +143,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
-          if (valid && c < NV) {
-            f2 y[4];
+          f2 y[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) y[q] = f2_mul(f2_mul(h[v][q], r2), w[v][q]);
+          for (int q = 0; q < 4; ++q) y[q] = f2_mul(f2_mul(h[v][q], r2), w[v][q]);
+          if (kEven || (valid && c < NV))
             stg128(static_cast<T*>(a.y) + static_cast<size_t>(row) * a.H + 8 * c, VecOf<T>::pack(y));
-          }
         }
       }
     }
@@ -167,27 +163,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
   drain(a, t);
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, bool kEven>
 const void* pick_fwd(int form, bool pack) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+#define BLK_PICK(F)                                            \
+  (pack ? fn(&blk_fwd_kernel<T, VPT, F, true, kEven>)          \
+        : fn(&blk_fwd_kernel<T, VPT, F, false, kEven>))
   switch (form) {
-    case kKeep: return fn(&blk_fwd_kernel<T, VPT, kKeep, true>);
-    case kPre:
-      return pack ? fn(&blk_fwd_kernel<T, VPT, kPre, true>) : fn(&blk_fwd_kernel<T, VPT, kPre, false>);
-    case kBoth:
-      return pack ? fn(&blk_fwd_kernel<T, VPT, kBoth, true>)
-                  : fn(&blk_fwd_kernel<T, VPT, kBoth, false>);
-    default:
-      return pack ? fn(&blk_fwd_kernel<T, VPT, kPost, true>)
-                  : fn(&blk_fwd_kernel<T, VPT, kPost, false>);
+    case kKeep: return fn(&blk_fwd_kernel<T, VPT, kKeep, true, kEven>);
+    case kPre: return BLK_PICK(kPre);
+    case kBoth: return BLK_PICK(kBoth);
+    default: return BLK_PICK(kPost);
   }
+#undef BLK_PICK
 }
 
 template <typename T>
 cudaError_t launch_fwd_t(const FwdArgs& a, const Shape& s, int form, bool pack, cudaStream_t st) {
-  const void* fn = s.vpt == 1   ? pick_fwd<T, 1>(form, pack)
-                   : s.vpt == 3 ? pick_fwd<T, 3>(form, pack)
-                                : pick_fwd<T, 4>(form, pack);
+  const bool even = even_rows(a.H, s.vpt, s.ntg);
+  const void* fn = s.vpt == 1   ? pick_fwd<T, 1, false>(form, pack)
+                   : s.vpt == 3 ? (even ? pick_fwd<T, 3, true>(form, pack)
+                                        : pick_fwd<T, 3, false>(form, pack))
+                                : (even ? pick_fwd<T, 4, true>(form, pack)
+                                        : pick_fwd<T, 4, false>(form, pack));
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   FwdArgs copy = a;

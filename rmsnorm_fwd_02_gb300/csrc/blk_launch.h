@@ -10,12 +10,12 @@ namespace blk {
 
 constexpr int kMaxH = 8192;
 // Most threads of a CTA, one CTA an SM.  A row costs a thread some 150 instructions (its waits,
-// the two sums' reduction, rstd, addresses) whatever its share of the row, so threads own 32
-// elements where the row has them, with the registers that takes: 168 in the forward, 255 in the
-// backward, whose column sums, weights and waiting gradient are 160.
+// the sums' reduction, rstd, addresses) whatever its share of the row, so threads own 32 elements
+// where the row has them, with the registers that takes.
+enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
 constexpr int kFwdThreads = 384;
-constexpr int kBwdThreads = 256;
-constexpr int kMaxWarps = kFwdThreads / 32;
+constexpr int bwd_threads(int form) { return form == kKeep ? 384 : 256; }
+constexpr int kMaxWarps = 12;
 constexpr int kMaxTensors = 4;    // staged
 // CTAs of the backward at most, whatever the GPU: the rows' partition, and with it the order of
 // every sum, is a function of the shape.  GB300 has 152 SMs: there it is one wave.
@@ -23,14 +23,13 @@ constexpr int kPartSMs = 152;
 constexpr int kFinishCols = 32;
 constexpr int kFinishSlices = 32;
 
-// What a kernel computes.
+// What a kernel computes (the enumeration above).
 //   kKeep  h = x [+ residual], rounded; norm before; h held in 8 bits    (rmsnorm_act8)
 //   kPre   scales and gate, norm before
 //   kBoth  norm behind, scales and gate, norm before
 //   kPost  norm behind, scales and gate
 // The backward has three forms with a norm before: kKeep (no x: no gate), kPre (x for the gate's
 // gradient), kBoth; and kPost.
-enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
 
 // A team of ntg threads (8, 16: part of a warp, 32 / ntg rows side by side; 32; or several whole
 // warps) takes one row (or those of its warp) at a time from its own ring of `stages` slots, each
