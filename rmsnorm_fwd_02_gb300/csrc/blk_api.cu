@@ -62,27 +62,24 @@ int device_setup(unsigned** err) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads a row, vectors a thread and teams a CTA: functions of H (and of whether a warp may share
-// rows between its threads).
-Shape team_shape(int H, int threads_cta, bool whole_warps) {
+// Threads a row, vectors a thread, teams a CTA and CTAs: functions of R and H (and of the kernel's
+// threads).
+Shape team_shape(int64_t R, int H, int threads_cta) {
   Shape s{};
   const int nv = H / 8;
   auto threads = [&](int vpt) {
     const int per = (nv + vpt - 1) / vpt;
-    return per <= 8 && !whole_warps    ? 8
-           : per <= 16 && !whole_warps ? 16
-                                       : static_cast<int>(ceil_div(per, 32)) * 32;
+    return per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 ? 16 : static_cast<int>(ceil_div(per, 32)) * 32;
   };
-  // four vectors a thread, three where fewer places then stay empty; narrow rows one
-  s.vpt = nv <= 16 ? 1 : (3 * threads(3) < 4 * threads(4) ? 3 : 4);
+  auto teams = [&](int ntg) { return threads_cta / (ntg < 32 ? 32 : ntg); };
+  // four vectors a thread, three where fewer places then stay empty, fewer in narrow rows; one
+  // where the rows are so few that each then has a team at once: the shortest way through a row
+  s.vpt = nv <= 4 ? 1 : nv <= 8 ? 2 : (threads(3) <= threads_cta && 3 * threads(3) < 4 * threads(4) ? 3
+                                                                                  : 4);
+  if (nv > 16 && threads(1) <= threads_cta && R <= int64_t{kPartSMs} * teams(threads(1))) s.vpt = 1;
   s.ntg = threads(s.vpt);
-  s.teams = threads_cta / (s.ntg < 32 ? 32 : s.ntg);
-  return s;
-}
-
-// Teams a CTA and CTAs for R rows: a row (or a warp's rows) a team at least, spread over the CTAs
-// first.  A function of (R, H, whole_warps) alone.
-void spread(Shape& s, int64_t R) {
+  s.teams = teams(s.ntg);
+  // a row (or a warp's rows) a team at least, spread over the CTAs first
   const int side = s.ntg < 32 ? 32 / s.ntg : 1;
   const int64_t takes = ceil_div(R, side);
   const int64_t per = ceil_div(takes, kPartSMs);
@@ -90,6 +87,7 @@ void spread(Shape& s, int64_t R) {
   const int64_t ctas = ceil_div(takes, s.teams);
   s.P = static_cast<int>(ctas < kPartSMs ? ctas : kPartSMs);
   s.threads = s.teams * (s.ntg < 32 ? 32 : s.ntg);
+  return s;
 }
 
 }  // namespace
@@ -101,8 +99,9 @@ size_t smem_bytes(const Shape& s) {
 
 namespace {
 
-// The ring for staged rows of `row` bytes, of which a copy moves at least `least` at once.
-void ring(Shape& s, size_t row, size_t least) {
+// The ring for staged rows of `row` bytes, of which a copy moves at least `least` at once; the
+// backward's teams' sums take its place in the end (`sums` rows a team).
+void ring(Shape& s, int H, size_t row, size_t least, int sums) {
   const int side = s.ntg < 32 ? 32 / s.ntg : 1;
   int steps = 1;
   if (s.ntg <= 32)
@@ -115,20 +114,14 @@ void ring(Shape& s, size_t row, size_t least) {
     if (steps == 1 || (s.stages >= 3 && smem_bytes(s) <= kSmemBytes)) break;
   }
   s.smem = smem_bytes(s);
+  const size_t join = s.teams > 1 ? sizeof(float) * sums * s.teams * H : 0;
+  if (s.smem < join) s.smem = join;
 }
 
-Shape plan(int H, int64_t R, int threads_cta, bool whole_warps, size_t row, size_t least) {
-  Shape s = team_shape(H, threads_cta, whole_warps);
-  spread(s, R);
-  ring(s, row, least);
+Shape plan(int64_t R, int H, int threads_cta, size_t row, size_t least, int sums) {
+  Shape s = team_shape(R, H, threads_cta);
+  ring(s, H, row, least, sums);
   return s;
-}
-
-// Teams of the backward's form.
-int64_t all_teams(int64_t R, int32_t H, int form, bool whole_warps) {
-  Shape s = team_shape(H, bwd_threads(form), whole_warps);
-  spread(s, R);
-  return static_cast<int64_t>(s.P) * s.teams;
 }
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -192,7 +185,7 @@ int run_fwd(const Fwd& f, void* stream) {
   if (st != RMSN_OK) return st;
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
-  const Shape s = plan(f.H, f.R, kFwdThreads, false, f.residual != nullptr ? 2 * row : row, row);
+  const Shape s = plan(f.R, f.H, kFwdThreads, f.residual != nullptr ? 2 * row : row, row, 0);
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -234,14 +227,15 @@ struct Bwd {
   float scale, residual_scale;
 };
 
-// Floats of the sums' rows: a row a team for dw_pre, a row a team and sample for S.
-size_t part_floats(int64_t teams, int32_t H) { return static_cast<size_t>(teams) * H; }
-size_t s_floats(int64_t teams, int32_t H, int64_t N) {
-  return static_cast<size_t>(teams + N - 1) * H;
+// Floats of the sums' rows: of dw_pre's, a row a CTA; of S, too, or a row a team and sample.
+size_t pre_floats(const Shape& s, int32_t H) { return static_cast<size_t>(s.P) * H; }
+size_t s_floats(const Shape& s, int32_t H, int64_t N) {
+  const int64_t rows = N == 1 ? s.P : static_cast<int64_t>(s.P) * s.teams + N - 1;
+  return static_cast<size_t>(rows) * H;
 }
 size_t workspace_bytes(int64_t R, int32_t H, int64_t N) {
-  const int64_t teams = all_teams(R, H, kBoth, N > 1), keep = all_teams(R, H, kKeep, false);
-  const size_t both = part_floats(teams, H) + s_floats(teams, H, N), one = part_floats(keep, H);
+  const Shape s = team_shape(R, H, bwd_threads(kBoth)), keep = team_shape(R, H, bwd_threads(kKeep));
+  const size_t both = pre_floats(s, H) + s_floats(s, H, N), one = pre_floats(keep, H);
   return sizeof(float) * (both > one ? both : one);
 }
 
@@ -261,7 +255,6 @@ int run_bwd(const Bwd& b, void* stream) {
     return RMSN_OK;
   }
   BwdArgs a{};
-  const bool whole_warps = s_sums && b.N > 1;  // a warp's rows are then of one sample
   const int64_t wide = 2 * static_cast<int64_t>(b.H);
   const int64_t saved = b.packed ? rmsn::act8_row_size(b.H) : wide;
   if (pre) {
@@ -273,12 +266,12 @@ int run_bwd(const Bwd& b, void* stream) {
   size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
-  const Shape s = plan(b.H, b.R, bwd_threads(b.form), whole_warps, row, least);
+  const Shape s = plan(b.R, b.H, bwd_threads(b.form), row, least,
+                       (pre ? 1 : 0) + (s_sums ? 1 : 0));
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
-  const int64_t teams = static_cast<int64_t>(s.P) * s.teams;
-  const size_t need = sizeof(float) * ((pre ? part_floats(teams, b.H) : 0) +
-                                       (s_sums ? s_floats(teams, b.H, b.N) : 0));
+  const size_t need = sizeof(float) * ((pre ? pre_floats(s, b.H) : 0) +
+                                       (s_sums ? s_floats(s, b.H, b.N) : 0));
   if (b.workspace == nullptr || b.workspace_bytes < need) return RMSN_ERR_WORKSPACE;
   float* ws = static_cast<float*>(b.workspace);
   a.w_pre = b.w_pre;
@@ -293,12 +286,13 @@ int run_bwd(const Bwd& b, void* stream) {
   a.dx = b.dx;
   a.dres = b.dres;
   a.part_pre = pre ? ws : nullptr;
-  a.part_s = s_sums ? ws + (pre ? part_floats(teams, b.H) : 0) : nullptr;
+  a.part_s = s_sums ? ws + (pre ? pre_floats(s, b.H) : 0) : nullptr;
   if (launch_bwd(a, s, b.dtype, b.form, b.packed, stream_) != cudaSuccess) return RMSN_ERR_CUDA;
   FinishArgs f{};
   f.part_pre = a.part_pre;
   f.part_s = a.part_s;
-  f.teams = teams;
+  f.ctas = s.P;
+  f.teams = static_cast<int64_t>(s.P) * s.teams;
   f.R = a.R;
   f.H = b.H;
   f.samples = a.samples;
@@ -360,7 +354,7 @@ int rmsnorm_act8_train_fwd(const void* x, const void* residual, int dtype, const
 
 size_t rmsnorm_act8_train_bwd_workspace_bytes(int64_t R, int32_t H) {
   if (check_sizes(R, H, 1) != RMSN_OK || R == 0) return 0;
-  return sizeof(float) * part_floats(all_teams(R, H, kKeep, false), H);
+  return sizeof(float) * pre_floats(team_shape(R, H, bwd_threads(kKeep)), H);
 }
 
 int rmsnorm_act8_train_bwd(const void* packed, const void* dy, const void* dh, int dtype,
@@ -522,9 +516,9 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   if (R == 0) return RMSN_ERR_INVALID_ARG;
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
-  const Shape s = backward ? plan(H, R, bwd_threads(kBoth), N > 1, 2 * wide + 2 * saved,
-                                  wide < saved ? wide : saved)
-                           : plan(H, R, kFwdThreads, false, 2 * wide, wide);
+  const Shape s = backward ? plan(R, H, bwd_threads(kBoth), 2 * wide + 2 * saved,
+                                  wide < saved ? wide : saved, 2)
+                           : plan(R, H, kFwdThreads, 2 * wide, wide, 0);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

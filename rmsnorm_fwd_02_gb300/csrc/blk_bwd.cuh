@@ -8,10 +8,10 @@
 // both dw_post and the gate's gradient: S = sum of t * xhat over a sample's rows, of which dgate is
 // scale * w_post * S and dw_post the sum over samples of scale * gate * S.
 //
-// A team sums its columns in FP32 registers over its rows; it writes a row of S whenever its
-// rows pass into another sample (row k + n for team k and sample n: teams and samples both go
-// forward, so no two share one) and a row of dw_pre's sums at the end.  The finish adds these rows
-// in a fixed order.
+// A team sums its columns in FP32 registers over its rows, a CTA its teams' sums, which it writes as
+// one row of partials; the finish adds these in a fixed order.  With a gate for each of several
+// samples, a team writes its S whenever its rows pass into another sample (row k + n for team k and
+// sample n: teams and samples both go forward, so no two share one).
 #pragma once
 
 #include "blk_common.cuh"
@@ -37,14 +37,15 @@ __device__ __forceinline__ float load_saved(const Args& a, uint32_t at, int c, b
   }
 }
 
-// A team's sums of its columns to a row of partials, and back to zero.
+// A team's sums of its columns to row `out` (rows side by side in a warp are added), and back to
+// zero.
 template <int VPT>
 __device__ __forceinline__ void write_sums(const Args& a, const Team& t, float* out, f2 (&acc)[VPT][4]) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = t.lt + v * a.ntg;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {  // rows side by side in a warp
+    for (int q = 0; q < 4; ++q) {
       for (int o = a.ntg; o < 32; o <<= 1) {
         const float lo = __shfl_xor_sync(0xffffffffu, f2_lo(acc[v][q]), o);
         const float hi = __shfl_xor_sync(0xffffffffu, f2_hi(acc[v][q]), o);
@@ -58,6 +59,20 @@ __device__ __forceinline__ void write_sums(const Args& a, const Team& t, float* 
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[v][q] = f2_splat(0.f);
+  }
+}
+
+// The teams' rows of sums in shared memory (rows `first` to `first + teams`) to one row of the CTA,
+// in the teams' order, the additions' errors carried along.
+__device__ __forceinline__ void join_teams(const Args& a, const float* rows, float* out) {
+  for (int col = static_cast<int>(threadIdx.x); col < a.H; col += static_cast<int>(blockDim.x)) {
+    float s = 0.f, e = 0.f;
+    for (int k = 0; k < a.teams; ++k) {
+      float err;
+      s = add_exact(s, rows[k * a.H + col], err);
+      e = __fadd_rn(e, err);
+    }
+    out[col] = isfinite(s) ? __fadd_rn(s, e) : s;
   }
 }
 
@@ -86,7 +101,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
   }
   const float inv_h = 1.f / static_cast<float>(a.H);
   const f2 rscale = f2_splat(a.residual_scale);
-  const int step = a.ntg < 32 ? 32 / a.ntg : 1;
+  const int side = a.ntg < 32 ? 32 / a.ntg : 1;  // rows side by side
   const bool has_dh = a.in[2].p != nullptr;
   int32_t sample = kX ? t.r0 / a.L : 0;
   int32_t next_sample = (sample + 1) * a.L;  // the row from which k1 and S are another sample's
@@ -102,32 +117,41 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
     }
   };
   fetch(t.r0 + t.sub);
+  // the rows of one sample that are taken together from row on, of n
+  auto take = [&](int32_t row, int32_t n) {
+    int32_t k = kEven ? 1 : min(side, n);
+    if (kX && !kEven && a.samples > 1) k = min(k, next_sample - row);
+    return k;
+  };
   int s = 0;
   uint32_t parity = 0;
   for (int32_t j = 0; j < t.nslots; ++j) {
     wait_slot(a, t, s, parity);
     const int32_t ra = t.r0 + j * a.rows;
     const int32_t n = min(a.rows, t.r1 - ra);
-    for (int32_t i = 0; i < n; i += step) {
-      const int32_t row = ra + i + t.sub;
-      const bool valid = kEven || i + t.sub < n;
-      const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
-      const uint32_t at = static_cast<uint32_t>(i + t.sub);
-      const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
-      const uint32_t dys = base + a.in[1].off + at * a.in[1].bytes;
-      const uint32_t dhs = base + a.in[2].off + at * a.in[2].bytes;
-      const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
+    for (int32_t i = 0; i < n;) {
       if constexpr (kX) {
-        // (gates of several samples: a team's rows are one at a time, so this is uniform)
-        if (row >= next_sample && a.samples > 1) {
+        if (a.samples > 1 && ra + i >= next_sample) {
           write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
-          sample = row / a.L;
+          sample = (ra + i) / a.L;
           next_sample = (sample + 1) * a.L;
           load_factor<VPT, kPostN>(a, sample, t.lt, k1);
         }
       }
+      const int32_t together = take(ra + i, n - i);
+      const int32_t row = ra + i + t.sub;
+      const bool valid = kEven || t.sub < together;
+      const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
+      // (lanes without a row stay within the slot)
+      const uint32_t at = static_cast<uint32_t>(valid ? i + t.sub : i);
+      const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
+      const uint32_t dys = base + a.in[1].off + at * a.in[1].bytes;
+      const uint32_t dhs = base + a.in[2].off + at * a.in[2].bytes;
+      const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
       const float r1 = r1_next, r2 = r2_next;
-      fetch(i + step < n ? row + step : ra + a.rows + t.sub);
+      fetch(row + together);
+      const bool first = i == 0;
+      i += together;
       // Packed vectors stay in registers between the passes over a row (h, then x in its place):
       // their unpacking is three times that of 16-bit values, which are read again.
       f2 kept[kPacked ? VPT : 1][4];
@@ -166,7 +190,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
           dot = f2_lo(d) + f2_hi(d);
         }
         dot = row_sum(a, t, dot);
-        if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+        if (first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<4>(a, t, j - 1 + a.stages, pol);
         // t = r2 (dy w - h (mean r2^2)): the mean's factor times r2, on t's scale
         nc2 = f2_splat(-(dot * (r2 * inv_h)) * r2);
@@ -254,7 +278,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
           dot = f2_lo(d) + f2_hi(d);
         }
         dot = row_sum(a, t, dot);
-        if (!kPreN && i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+        if (!kPreN && first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<4>(a, t, j - 1 + a.stages, pol);
         const f2 nc1 = f2_splat(-(dot * (r1 * inv_h)) * r1);
 #pragma unroll
@@ -286,9 +310,24 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
     }
   }
   drain(a, t);
-  if constexpr (kPreN) write_sums<VPT>(a, t, a.part_pre + t.k * a.H, sum_pre);
-  // (a team without rows writes zeros: it lies among the teams of its first row's sample)
-  if constexpr (kX) write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
+  if (kX && a.samples > 1) {
+    // (a team without rows writes zeros: it lies among the teams of its first row's sample)
+    write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
+  }
+  const int64_t cta = static_cast<int64_t>(blockIdx.x) * a.H;
+  if (a.teams == 1) {
+    if constexpr (kPreN) write_sums<VPT>(a, t, a.part_pre + cta, sum_pre);
+    if (kX && a.samples == 1) write_sums<VPT>(a, t, a.part_s + cta, sum_s);
+    return;
+  }
+  __syncthreads();  // every team is done with its ring
+  float* rows = reinterpret_cast<float*>(smem);
+  if constexpr (kPreN) write_sums<VPT>(a, t, rows + t.team * a.H, sum_pre);
+  float* rows_s = rows + (kPreN ? a.teams * a.H : 0);
+  if (kX && a.samples == 1) write_sums<VPT>(a, t, rows_s + t.team * a.H, sum_s);
+  __syncthreads();
+  if constexpr (kPreN) join_teams(a, rows, a.part_pre + cta);
+  if (kX && a.samples == 1) join_teams(a, rows_s, a.part_s + cta);
 }
 
 template <typename T, int VPT, bool kEven>
@@ -310,6 +349,7 @@ template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
   const bool even = even_rows(a.H, s.vpt, s.ntg);
   const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed)
+                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed)
                    : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed)
                                         : pick_bwd<T, 3, false>(form, packed))
                                 : (even ? pick_bwd<T, 4, true>(form, packed)

@@ -39,6 +39,15 @@ __device__ __forceinline__ float load1(const void* p, int code, int64_t i) {
                    : widen1(static_cast<const __half*>(p)[i]);
 }
 
+// s + err == a + b exactly (Knuth).
+__device__ __forceinline__ float add_exact(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b);
+  const float bp = __fsub_rn(s, a);
+  const float ap = __fsub_rn(s, bp);
+  err = __fadd_rn(__fsub_rn(a, ap), __fsub_rn(b, bp));
+  return s;
+}
+
 // Whether every thread of a row has all its vectors, and every row of a warp is there: kernels are
 // built for that case apart, without a predicate on any vector.
 __host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {

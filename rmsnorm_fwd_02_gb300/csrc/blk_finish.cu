@@ -6,17 +6,8 @@ namespace blk {
 
 namespace {
 
-// s + err == a + b exactly (Knuth).
-__device__ __forceinline__ float add_exact(float a, float b, float& err) {
-  const float s = __fadd_rn(a, b);
-  const float bp = __fsub_rn(s, a);
-  const float ap = __fsub_rn(s, bp);
-  err = __fadd_rn(__fsub_rn(a, ap), __fsub_rn(b, bp));
-  return s;
-}
-
 // Sum of n values f(0), f(1), ... over kSlices threads a column: each takes a contiguous share,
-// four loads at a time, the shares are then joined pairwise.  The errors of the additions are
+// five loads at a time (the rows of 152 CTAs: two turns), the shares are then joined pairwise.  The errors of the additions are
 // carried along.  Every thread of the block calls it; the result is thread 0's of the column.
 template <int kSlices, typename F>
 __device__ __forceinline__ float column_sum(int64_t n, int sl, int cl, bool live, float* sh, float* se,
@@ -24,12 +15,12 @@ __device__ __forceinline__ float column_sum(int64_t n, int sl, int cl, bool live
   float s = 0.f, e = 0.f;
   if (live) {
     const int64_t i1 = (sl + 1) * n / kSlices;
-    for (int64_t i = sl * n / kSlices; i < i1; i += 4) {
-      float v[4];
+    for (int64_t i = sl * n / kSlices; i < i1; i += 5) {
+      float v[5];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = i + u < i1 ? f(i + u) : 0.f;
+      for (int u = 0; u < 5; ++u) v[u] = i + u < i1 ? f(i + u) : 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 5; ++u) {
         float err;
         s = add_exact(s, v[u], err);
         e = __fadd_rn(e, err);
@@ -87,14 +78,14 @@ __global__ void __launch_bounds__(kFinishCols* kFinishSlices) blk_finish_kernel(
   const bool live = col < a.H;
   if (a.part_pre != nullptr && blockIdx.y == 0) {
     const float* p = a.part_pre + col;
-    const float s = column_sum<kFinishSlices>(a.teams, sl, cl, live, sh, se,
+    const float s = column_sum<kFinishSlices>(a.ctas, sl, cl, live, sh, se,
                                               [&](int64_t i) { return p[i * a.H]; });
     if (sl == 0 && live) a.dw_pre[col] = s;
     return;
   }
   const float* p = a.part_s + col;
   if (a.samples == 1) {
-    const float s = a.scale * column_sum<kFinishSlices>(a.teams, sl, cl, live, sh, se,
+    const float s = a.scale * column_sum<kFinishSlices>(a.ctas, sl, cl, live, sh, se,
                                                         [&](int64_t i) { return p[i * a.H]; });
     if (sl == 0 && live) {
       if (a.dw_post != nullptr)
@@ -121,7 +112,7 @@ cudaError_t launch_finish(const FinishArgs& a, cudaStream_t st) {
   const bool several = a.part_s != nullptr && a.samples > 1;
   if (several) {
     // few teams a sample: few threads a column
-    const bool few = a.teams / a.samples < 8;
+    const bool few = a.teams / a.samples < 40;
     const void* fn = few ? reinterpret_cast<const void*>(&blk_samples_kernel<4>)
                          : reinterpret_cast<const void*>(&blk_samples_kernel<kFinishSlices>);
     const cudaError_t e =

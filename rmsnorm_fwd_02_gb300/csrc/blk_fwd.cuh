@@ -182,6 +182,7 @@ template <typename T>
 cudaError_t launch_fwd_t(const FwdArgs& a, const Shape& s, int form, bool pack, cudaStream_t st) {
   const bool even = even_rows(a.H, s.vpt, s.ntg);
   const void* fn = s.vpt == 1   ? pick_fwd<T, 1, false>(form, pack)
+                   : s.vpt == 2 ? pick_fwd<T, 2, false>(form, pack)
                    : s.vpt == 3 ? (even ? pick_fwd<T, 3, true>(form, pack)
                                         : pick_fwd<T, 3, false>(form, pack))
                                 : (even ? pick_fwd<T, 4, true>(form, pack)

@@ -21,7 +21,7 @@ constexpr int kMaxTensors = 4;    // staged
 // every sum, is a function of the shape.  GB300 has 152 SMs: there it is one wave.
 constexpr int kPartSMs = 152;
 constexpr int kFinishCols = 32;
-constexpr int kFinishSlices = 32;
+constexpr int kFinishSlices = 16;
 
 // What a kernel computes (the enumeration above).
 //   kKeep  h = x [+ residual], rounded; norm before; h held in 8 bits    (rmsnorm_act8)
@@ -31,11 +31,11 @@ constexpr int kFinishSlices = 32;
 // The backward has three forms with a norm before: kKeep (no x: no gate), kPre (x for the gate's
 // gradient), kBoth; and kPost.
 
-// A team of ntg threads (8, 16: part of a warp, 32 / ntg rows side by side; 32; or several whole
-// warps) takes one row (or those of its warp) at a time from its own ring of `stages` slots, each
+// A team of ntg threads (4, 8, 16: part of a warp, 32 / ntg rows side by side; 32; or several
+// whole warps) takes one row (or those of its warp) at a time from its own ring of `stages` slots, each
 // of `steps` such takes.
 struct Shape {
-  int vpt;      // 16-byte vectors (8 elements) a thread: 1, 3 or 4
+  int vpt;      // 16-byte vectors (8 elements) a thread: 1 to 4
   int ntg;      // threads a row
   int teams;    // teams (of whole warps) a CTA
   int rows;     // rows a slot
@@ -84,8 +84,9 @@ struct BwdArgs : Args {
   const float* rstd_post;
   void* dx;
   void* dres;
-  float* part_pre;    // [P * teams][H]: sums of dy * hhat, a row a team
-  float* part_s;      // [P * teams + N - 1][H]: sums of t * xhat, a row a team and sample
+  float* part_pre;    // [P][H]: sums of dy * hhat, a row a CTA
+  float* part_s;      // sums of t * xhat: [P][H], a row a CTA, or with several samples
+                      // [P * teams + N - 1][H], a row a team and sample
 };
 
 // First row of team k of n.
@@ -108,7 +109,7 @@ cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int dtype, int form, bo
 struct FinishArgs {
   const float* part_pre;   // null: no norm before
   float* part_s;           // null: neither norm behind nor gate
-  int64_t teams;
+  int64_t ctas, teams;     // teams: of all CTAs
   int32_t R, H, samples;
   const void* w_post;
   const void* gate;
