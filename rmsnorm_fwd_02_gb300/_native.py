@@ -334,28 +334,36 @@ def groupnorm_train_launch_plan(dtype, N, S, C_, G, backward):
 
 
 # ---- activations in 8 bits (include/act8_train.h) ---------------------------------------
+#
+# (Tensors that every call has give their pointers here directly: _ptr's tests are a tenth of a
+# microsecond each, and these calls have up to twenty.)
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
 
 def act8_train_row_bytes(H):
     return int(lib().act8_train_row_bytes(H))
 
 
 def act8_train_pack(x, dtype, packed, R, H, s_row, stream=None):
-    st = lib().act8_train_pack(_ptr(x), dtype, _ptr(packed), R, H, s_row, _stream(stream))
+    st = lib().act8_train_pack(x.data_ptr(), dtype, packed.data_ptr(), R, H, s_row,
+                               _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("act8_train_pack", st)
 
 
 def act8_train_unpack(packed, y, dtype, R, H, stream=None):
-    st = lib().act8_train_unpack(_ptr(packed), _ptr(y), dtype, R, H, _stream(stream))
+    st = lib().act8_train_unpack(packed.data_ptr(), y.data_ptr(), dtype, R, H, _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("act8_train_unpack", st)
 
 
 def rmsnorm_act8_train_fwd(x, residual, dtype, w, w_dtype, y, h_out, rstd, packed, R, H, s_x, s_res,
                            eps, stream=None):
-    st = lib().rmsnorm_act8_train_fwd(_ptr(x), _ptr(residual), dtype, _ptr(w), w_dtype, _ptr(y),
-                                      _ptr(h_out), _ptr(rstd), _ptr(packed), R, H, s_x, s_res, eps,
-                                      _stream(stream))
+    st = lib().rmsnorm_act8_train_fwd(x.data_ptr(), _opt(residual), dtype, w.data_ptr(), w_dtype,
+                                      y.data_ptr(), _opt(h_out), rstd.data_ptr(),
+                                      packed.data_ptr(), R, H, s_x, s_res, eps, _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("rmsnorm_act8_train_fwd", st)
 
@@ -366,9 +374,10 @@ def rmsnorm_act8_train_bwd_workspace_bytes(R, H):
 
 def rmsnorm_act8_train_bwd(packed, dy, dh, dtype, rstd, w, w_dtype, dx, dw, workspace,
                            workspace_bytes, R, H, stream=None):
-    st = lib().rmsnorm_act8_train_bwd(_ptr(packed), _ptr(dy), _ptr(dh), dtype, _ptr(rstd), _ptr(w),
-                                      w_dtype, _ptr(dx), _ptr(dw), _ptr(workspace),
-                                      workspace_bytes, R, H, _stream(stream))
+    st = lib().rmsnorm_act8_train_bwd(packed.data_ptr(), dy.data_ptr(), _opt(dh), dtype,
+                                      rstd.data_ptr(), w.data_ptr(), w_dtype, dx.data_ptr(),
+                                      dw.data_ptr(), _opt(workspace), workspace_bytes, R, H,
+                                      _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("rmsnorm_act8_train_bwd", st)
 
@@ -378,10 +387,11 @@ def rmsnorm_act8_train_bwd(packed, dy, dh, dtype, rstd, w, w_dtype, dx, dw, work
 def rmsnorm_block_train_fwd(x, residual, dtype, w_pre, w_post, w_dtype, gate, gate_dtype, N, y, h,
                             rstd_pre, rstd_post, x8, h8, R, H, s_x, s_res, scale, residual_scale,
                             eps, stream=None):
-    st = lib().rmsnorm_block_train_fwd(_ptr(x), _ptr(residual), dtype, _ptr(w_pre), _ptr(w_post),
-                                       w_dtype, _ptr(gate), gate_dtype, N, _ptr(y), _ptr(h),
-                                       _ptr(rstd_pre), _ptr(rstd_post), _ptr(x8), _ptr(h8), R, H,
-                                       s_x, s_res, scale, residual_scale, eps, _stream(stream))
+    st = lib().rmsnorm_block_train_fwd(x.data_ptr(), residual.data_ptr(), dtype, _opt(w_pre),
+                                       _opt(w_post), w_dtype, _opt(gate), gate_dtype, N, _opt(y),
+                                       h.data_ptr(), _opt(rstd_pre), _opt(rstd_post), _opt(x8),
+                                       _opt(h8), R, H, s_x, s_res, scale, residual_scale, eps,
+                                       _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("rmsnorm_block_train_fwd", st)
 
@@ -394,12 +404,13 @@ def rmsnorm_block_train_bwd(dy, dh, x, h, packed, dtype, rstd_pre, rstd_post, w_
                             w_dtype, gate, gate_dtype, N, dx, dresidual, dw_pre, dw_post, dgate,
                             workspace, workspace_bytes, R, H, s_x, scale, residual_scale,
                             stream=None):
-    st = lib().rmsnorm_block_train_bwd(_ptr(dy), _ptr(dh), _ptr(x), _ptr(h), int(packed), dtype,
-                                       _ptr(rstd_pre), _ptr(rstd_post), _ptr(w_pre),
-                                       _ptr(w_post), w_dtype, _ptr(gate), gate_dtype, N, _ptr(dx),
-                                       _ptr(dresidual), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate),
-                                       _ptr(workspace), workspace_bytes, R, H, s_x, scale,
-                                       residual_scale, _stream(stream))
+    st = lib().rmsnorm_block_train_bwd(_opt(dy), _opt(dh), _opt(x), _opt(h), int(packed), dtype,
+                                       _opt(rstd_pre), _opt(rstd_post), _opt(w_pre),
+                                       _opt(w_post), w_dtype, _opt(gate), gate_dtype, N,
+                                       dx.data_ptr(), dresidual.data_ptr(), _opt(dw_pre),
+                                       _opt(dw_post), _opt(dgate), _opt(workspace),
+                                       workspace_bytes, R, H, s_x, scale, residual_scale,
+                                       _stream(stream))
     if st != RMSN_OK:
         raise RmsnError("rmsnorm_block_train_bwd", st)
 

@@ -33,7 +33,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .dropout import _empty, _flat, _like, _on, _same_device
+from .dropout import _empty_strided, _flat, _layout, _like, _on, _same_device
 from .ops import EPS
 
 _CODES = {torch.bfloat16: N.ACT8_BF16, torch.float32: N.ACT8_FP32, torch.float16: N.ACT8_FP16}
@@ -45,6 +45,16 @@ def act8_row_bytes(H: int) -> int:
     if H < 1:
         raise ValueError("a row has at least one value")
     return (H + 15) // 16 * 16 + ((H + 31) // 32 + 15) // 16 * 16
+
+
+@functools.lru_cache(maxsize=4096)
+def _layouts(shape):
+    """Layouts (shape and strides) of tensors of this shape, of its rows' scalars, and of its packed
+    rows."""
+    return _layout(shape), _layout(shape[:-1]), _layout((*shape[:-1], act8_row_bytes(shape[-1])))
+
+
+_WIDTHS = functools.lru_cache(maxsize=4096)(lambda h: _layout((h,)))
 
 
 def _rows(x: torch.Tensor, name: str):
@@ -77,7 +87,7 @@ def _narrow(x: torch.Tensor, name: str) -> int:
 def _row_input(x: torch.Tensor, name: str):
     """_rows of a tensor whose rows the kernels copy in 16-byte pieces."""
     rows, h, stride = _rows(x, name)
-    if h % 8 or h > 8192:
+    if h & 7 or h > 8192:
         raise ValueError(f"{name}'s last axis must be a multiple of 8 up to 8192")
     if stride % 8 or x.data_ptr() % 16:
         raise ValueError(f"{name}'s rows must start at 16-byte boundaries")
@@ -111,7 +121,7 @@ def act8_pack(x):
         raise TypeError("x must be a CUDA bfloat16, float16 or float32 tensor")
     rows, h, stride = _rows(x, "x")
     with _on(x):
-        packed = _empty((*x.shape[:-1], act8_row_bytes(h)), torch.uint8)
+        packed = _empty_strided(*_layouts(x.shape)[2], torch.uint8)
         N.act8_train_pack(x, _CODES[x.dtype], packed, rows, h, stride)
     return packed
 
@@ -124,7 +134,7 @@ def act8_unpack(packed, H, dtype=torch.bfloat16):
     lead = packed.shape[:-1]
     packed = _packed(packed, lead, H, "packed")
     with _on(packed):
-        x = _empty((*lead, H), dtype)
+        x = _empty_strided(*_layout((*lead, H)), dtype)
         N.act8_train_unpack(packed, x, _CODES[dtype], math.prod(lead), H)
     return x
 
@@ -139,11 +149,12 @@ def rmsnorm_act8_fwd(x, w, eps=EPS, residual=None):
         _, _, s_res = _row_input(residual, "residual")
     _same_device(x, residual, w)
     w = _flat(w)
+    full, lead, kept = _layouts(x.shape)
     with _on(x):
-        y = _empty(x.shape, x.dtype)
-        h_out = _empty(x.shape, x.dtype) if residual is not None else None
-        rstd = _empty(x.shape[:-1], torch.float32)
-        packed = _empty((*x.shape[:-1], act8_row_bytes(h)), torch.uint8)
+        y = _empty_strided(*full, x.dtype)
+        h_out = _empty_strided(*full, x.dtype) if residual is not None else None
+        rstd = _empty_strided(*lead, torch.float32)
+        packed = _empty_strided(*kept, torch.uint8)
         N.rmsnorm_act8_train_fwd(x, residual, code, w, w_code, y, h_out, rstd, packed, rows, h, s_x,
                                  s_res, float(eps))
     return (y, rstd, packed) if residual is None else (y, rstd, packed, h_out)
@@ -169,10 +180,10 @@ def rmsnorm_act8_bwd(dy, x8, rstd, w, dh=None):
     _same_device(dy, x8, rstd, w, dh)
     dy, w = _flat(dy), _flat(w)
     with _on(dy):
-        dx = _empty(dy.shape, dy.dtype)
-        dw = _empty((h,), torch.float32)
+        dx = _empty_strided(*_layout(dy.shape), dy.dtype)
+        dw = _empty_strided(*_WIDTHS(h), torch.float32)
         nbytes = _bwd_bytes(rows, h)
-        ws = _empty((nbytes,), torch.uint8) if nbytes else None
+        ws = _empty_strided((nbytes,), (1,), torch.uint8) if nbytes else None
         N.rmsnorm_act8_train_bwd(x8, dy, dh, code, rstd, w, w_code, dx, dw, ws, nbytes, rows, h)
     return dx, dw
 

@@ -35,13 +35,14 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .act8 import (_CODES, _narrow, _packed, _row_input, _row_scalars, _weight, act8_row_bytes)
-from .dropout import _empty, _flat, _like, _on, _same_device
+from .act8 import _CODES, _WIDTHS, _layouts, _narrow, _packed, _row_input, _row_scalars, _weight
+from .dropout import _empty_strided, _flat, _layout, _like, _on, _same_device
 from .ops import EPS
 
 
-def _factors(x, rows: int, h: int, w_pre, w_post, gate, scale, residual_scale):
-    """Checks the weights, the gate and the scales; the weights' and the gate's codes, N."""
+def _factors(x, others, rows: int, h: int, w_pre, w_post, gate, scale, residual_scale):
+    """Checks the weights, the gate and the scales, and that all tensors are on x's device; the
+    weights' and the gate's codes, N."""
     if w_pre is None and w_post is None:
         raise ValueError("one of w_pre and w_post must be given")
     codes = [_weight(w, h, name) for w, name in ((w_pre, "w_pre"), (w_post, "w_post"))
@@ -58,7 +59,7 @@ def _factors(x, rows: int, h: int, w_pre, w_post, gate, scale, residual_scale):
         n = gate.shape[0] if gate.dim() == 2 else 1
         if n < 1 or rows % n:
             raise ValueError(f"{rows} rows do not divide into gate's {n}")
-    _same_device(x, w_pre, w_post, gate)
+    _same_device(x, *others, w_pre, w_post, gate)
     if not (math.isfinite(scale) and math.isfinite(residual_scale)):
         raise ValueError("scale and residual_scale must be finite")
     return codes[0], gate_code, n
@@ -74,19 +75,22 @@ def rmsnorm_block_fwd(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0
     rows, h, s_x = _row_input(x, "x")
     _like(x, "residual", residual)
     _, _, s_res = _row_input(residual, "residual")
-    _same_device(x, residual)
-    w_code, gate_code, n = _factors(x, rows, h, w_pre, w_post, gate, scale, residual_scale)
-    keep_x, keep_h = w_post is not None or gate is not None, w_pre is not None
-    lead, shape = x.shape[:-1], x.shape
+    w_code, gate_code, n = _factors(x, (residual,), rows, h, w_pre, w_post, gate, scale, residual_scale)
+    full, lead, kept = _layouts(x.shape)
+    dtype = x.dtype
     with _on(x):
-        out_h = _empty(shape, x.dtype)
-        y = _empty(shape, x.dtype) if w_pre is not None else None
-        rstd_pre = _empty(lead, torch.float32) if w_pre is not None else None
-        rstd_post = _empty(lead, torch.float32) if w_post is not None else None
-        x8 = h8 = None
+        out_h = _empty_strided(*full, dtype)
+        y = rstd_pre = rstd_post = x8 = h8 = None
+        if w_pre is not None:
+            y = _empty_strided(*full, dtype)
+            rstd_pre = _empty_strided(*lead, torch.float32)
+        if w_post is not None:
+            rstd_post = _empty_strided(*lead, torch.float32)
         if act8:
-            x8 = _empty((*lead, act8_row_bytes(h)), torch.uint8) if keep_x else None
-            h8 = _empty((*lead, act8_row_bytes(h)), torch.uint8) if keep_h else None
+            if w_post is not None or gate is not None:
+                x8 = _empty_strided(*kept, torch.uint8)
+            if w_pre is not None:
+                h8 = _empty_strided(*kept, torch.uint8)
         N.rmsnorm_block_train_fwd(x, residual, code, _opt_flat(w_pre), _opt_flat(w_post), w_code,
                                   _opt_flat(gate), gate_code, n, y, out_h, rstd_pre, rstd_post,
                                   x8, h8, rows, h, s_x, s_res, float(scale),
@@ -127,7 +131,6 @@ def rmsnorm_block_bwd(dy, x, h, rstd_pre, rstd_post, w_pre=None, w_post=None, ga
         _like(grad, "dh", dh)
         dh = _flat(dh)
     dy = _opt_flat(dy)
-    w_code, gate_code, n = _factors(grad, rows, width, w_pre, w_post, gate, scale, residual_scale)
     kinds, s_x = set(), width
     if w_pre is not None:
         h, s_h, packed = _kept(h, grad, width, "h")
@@ -145,15 +148,17 @@ def rmsnorm_block_bwd(dy, x, h, rstd_pre, rstd_post, w_pre=None, w_post=None, ga
     rstd_post = _row_scalars(rstd_post, grad, "rstd_post") if w_post is not None else None
     if len(kinds) > 1:
         raise ValueError("x and h must both be activations or both packed")
-    _same_device(grad, dy, dh, x, h, rstd_pre, rstd_post)
+    w_code, gate_code, n = _factors(grad, (dy, dh, x, h, rstd_pre, rstd_post), rows, width, w_pre,
+                                    w_post, gate, scale, residual_scale)
     with _on(grad):
-        dx = _empty(grad.shape, grad.dtype)
-        dres = _empty(grad.shape, grad.dtype)
-        dw_pre = _empty((width,), torch.float32) if w_pre is not None else None
-        dw_post = _empty((width,), torch.float32) if w_post is not None else None
-        dgate = _empty(gate.shape, torch.float32) if gate is not None else None
+        full, one = _layout(grad.shape), _WIDTHS(width)
+        dx = _empty_strided(*full, grad.dtype)
+        dres = _empty_strided(*full, grad.dtype)
+        dw_pre = _empty_strided(*one, torch.float32) if w_pre is not None else None
+        dw_post = _empty_strided(*one, torch.float32) if w_post is not None else None
+        dgate = _empty_strided(*_layout(gate.shape), torch.float32) if gate is not None else None
         nbytes = _bwd_bytes(rows, width, n)
-        ws = _empty((nbytes,), torch.uint8) if nbytes else None
+        ws = _empty_strided((nbytes,), (1,), torch.uint8) if nbytes else None
         N.rmsnorm_block_train_bwd(dy, dh, x, h, packed, code, rstd_pre, rstd_post,
                                   _opt_flat(w_pre), _opt_flat(w_post), w_code, _opt_flat(gate),
                                   gate_code, n, dx, dres, dw_pre, dw_post, dgate, ws, nbytes, rows,

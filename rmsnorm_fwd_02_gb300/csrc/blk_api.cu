@@ -72,10 +72,12 @@ Shape team_shape(int64_t R, int H, int threads_cta) {
     return per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 ? 16 : static_cast<int>(ceil_div(per, 32)) * 32;
   };
   auto teams = [&](int ntg) { return threads_cta / (ntg < 32 ? 32 : ntg); };
-  // four vectors a thread, three where fewer places then stay empty, fewer in narrow rows; one
-  // where the rows are so few that each then has a team at once: the shortest way through a row
-  s.vpt = nv <= 4 ? 1 : nv <= 8 ? 2 : (threads(3) <= threads_cta && 3 * threads(3) < 4 * threads(4) ? 3
-                                                                                  : 4);
+  // four vectors a thread, three where that keeps more threads busy, fewer in narrow rows; one where the rows are so few that each then has a team at once: the shortest way through a row
+  auto busy = [&](int vpt) {  // threads of a CTA that have vectors
+    const int ntg = threads(vpt), rows = ntg < 32 ? 32 / ntg : 1;
+    return ntg > threads_cta ? 0 : teams(ntg) * rows * ((nv + vpt - 1) / vpt);
+  };
+  s.vpt = nv <= 4 ? 1 : nv <= 8 ? 2 : (busy(3) > busy(4) ? 3 : 4);
   if (nv > 16 && threads(1) <= threads_cta && R <= int64_t{kPartSMs} * teams(threads(1))) s.vpt = 1;
   s.ntg = threads(s.vpt);
   s.teams = teams(s.ntg);
@@ -94,7 +96,7 @@ Shape team_shape(int64_t R, int H, int threads_cta) {
 
 size_t smem_bytes(const Shape& s) {
   const size_t n = static_cast<size_t>(s.teams) * s.stages;
-  return n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 16;
+  return n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 32;
 }
 
 namespace {

@@ -20,19 +20,15 @@ namespace blk {
 
 // Vector c of a staged row: 16-bit values, or 8-bit numbers; their values are v * the unit that is
 // returned (a vector lies in one block, so the unit can go to what the numbers are multiplied by).
-template <typename T, bool kPacked, bool kEven>
-__device__ __forceinline__ float load_saved(const Args& a, uint32_t at, int c, bool live, f2 (&v)[4]) {
+template <typename T, bool kPacked>
+__device__ __forceinline__ float load_saved(const Args& a, const Team& t, uint32_t at, int c, bool live,
+                                            f2 (&v)[4]) {
   if constexpr (kPacked) {
-    uint2 q = make_uint2(0u, 0u);
-    uint32_t scale = 0u;
-    if (kEven || live) {
-      q = lds64_at(at + 8u * c);
-      scale = lds8_at(at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2));
-    }
-    act8_numbers8(q, v);
-    return act8_unit(scale);
+    act8_numbers8(lds64_at(live ? at + 8u * c : t.zero), v);
+    const uint32_t scale = at + ((static_cast<uint32_t>(a.H) + 15u) & ~15u) + (c >> 2);
+    return act8_unit(lds8_at(live ? scale : t.zero));
   } else {
-    VecOf<T>::unpack(lds128_if<kEven>(at + 16u * c, live), v);
+    VecOf<T>::unpack(lds128_at(live ? at + 16u * c : t.zero), v);
     return 1.f;
   }
 }
@@ -142,13 +138,13 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
       const int32_t row = ra + i + t.sub;
       const bool valid = kEven || t.sub < together;
       const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
-      // (lanes without a row stay within the slot)
-      const uint32_t at = static_cast<uint32_t>(valid ? i + t.sub : i);
+      const uint32_t at = static_cast<uint32_t>(i + t.sub);  // (lanes without a row read zeros)
       const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
       const uint32_t dys = base + a.in[1].off + at * a.in[1].bytes;
       const uint32_t dhs = base + a.in[2].off + at * a.in[2].bytes;
       const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
-      const float r1 = r1_next, r2 = r2_next;
+      // (a lane without a row has zeros throughout, and adds zeros to its columns' sums)
+      const float r1 = valid ? r1_next : 0.f, r2 = valid ? r2_next : 0.f;
       fetch(row + together);
       const bool first = i == 0;
       i += together;
@@ -165,8 +161,8 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
           const int c = t.lt + v * a.ntg;
           const bool live = kEven || (valid && c < NV);
           f2 h[4], dy[4];
-          const float u = load_saved<T, kPacked, kEven>(a, hs, c, live, h);
-          VecOf<T>::unpack(lds128_if<kEven>(dys + 16u * c, live), dy);
+          const float u = load_saved<T, kPacked>(a, t, hs, c, live, h);
+          VecOf<T>::unpack(lds128_at(live ? dys + 16u * c : t.zero), dy);
           if constexpr (kPacked) {
             dot0 = f2_mul(f2_mul(dy[0], w[v][0]), h[0]);
             dot1 = f2_mul(f2_mul(dy[1], w[v][1]), h[1]);
@@ -214,19 +210,18 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
             nc = f2_mul(nc2, f2_splat(unit[v]));
             rh = f2_mul(r2v, f2_splat(unit[v]));
           } else {
-            load_saved<T, kPacked, kEven>(a, hs, c, live, h);
+            load_saved<T, kPacked>(a, t, hs, c, live, h);
           }
-          VecOf<T>::unpack(lds128_if<kEven>(dys + 16u * c, live), dy);
+          VecOf<T>::unpack(lds128_at(live ? dys + 16u * c : t.zero), dy);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             g[q] = f2_mul(f2_fma(h[q], nc, f2_mul(dy[q], w[v][q])), r2v);
-            const f2 sum = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
-            if (live) sum_pre[v][q] = sum;
+            sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
           }
         }
         if (!kPreN || has_dh) {
           f2 dh[4];
-          VecOf<T>::unpack(lds128_if<kEven>(dhs + 16u * c, live), dh);
+          VecOf<T>::unpack(lds128_at(live ? dhs + 16u * c : t.zero), dh);
 #pragma unroll
           for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_add(g[q], dh[q]) : dh[q];
         }
@@ -236,17 +231,14 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
         if (live) stg128(static_cast<T*>(a.dres) + out_row + 8 * c, VecOf<T>::pack(o));
         if constexpr (kX) {
           f2 x[4];
-          const float u = load_saved<T, kPacked, kEven>(a, xs, c, live, x);
+          const float u = load_saved<T, kPacked>(a, t, xs, c, live, x);
           f2 rx = kPostN ? r1v : f2_splat(1.f);
           if constexpr (kPacked) rx = f2_mul(rx, f2_splat(u));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
-            const f2 sum = f2_fma(g[q], xh, sum_s[v][q]);
-            if (live) sum_s[v][q] = sum;
+            sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
             m[v][q] = f2_mul(g[q], k1[v][q]);
-            // (a row's infinities and NaN stay in it: vectors that are not there add nothing)
-            if (!live) m[v][q] = f2_splat(0.f);
           }
           if constexpr (kPostN && kPacked) {
             dot0 = f2_mul(m[v][0], x[0]);
@@ -292,7 +284,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
             for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
             nc = f2_mul(nc1, f2_splat(unit[v]));
           } else {
-            load_saved<T, kPacked, kEven>(a, xs, c, live, x);
+            load_saved<T, kPacked>(a, t, xs, c, live, x);
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc, m[v][q]), r1v);

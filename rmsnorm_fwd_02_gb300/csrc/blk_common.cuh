@@ -54,21 +54,6 @@ __host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
   return ntg >= 32 && H == 8 * vpt * ntg;
 }
 
-// A 16-byte vector of shared memory; without kEven, zeros where it is not `live` (`at` is then not
-// read).
-template <bool kEven>
-__device__ __forceinline__ uint4 lds128_if(uint32_t at, bool live) {
-  if constexpr (kEven) return lds128_at(at);
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-      "@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "r"(at), "r"(static_cast<uint32_t>(live)));
-  return v;
-}
-
 // scale * gate * w_post of a thread's columns (each factor where it is there), sample n's gate.
 template <int VPT, bool kPostW>
 __device__ __forceinline__ void load_factor(const Args& a, int32_t n, int lt, f2 (&k1)[VPT][4]) {
@@ -101,6 +86,7 @@ __device__ __forceinline__ float sum8(const f2 (&f)[4]) {
 // A thread's place in its CTA, its team's rows, ring and reductions.
 struct Team {
   uint32_t ring;        // shared address of the team's slots
+  uint32_t zero;        // shared address of 16 bytes of zeros, what vectors that are not there read
   uint64_t* full;       // its barriers
   float* red;           // [2][12]: warp sums, taken in turns
   volatile int* abort_flag;
@@ -186,7 +172,10 @@ __device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, u
   t.full = full + t.team * a.stages;
   float* red = reinterpret_cast<float*>(behind + ((8 * a.teams * a.stages + 15) & ~15));
   t.red = red + 2 * kMaxWarps * t.team;
-  t.abort_flag = reinterpret_cast<volatile int*>(red + 2 * kMaxWarps * a.teams);
+  uint4* zero = reinterpret_cast<uint4*>(red + 2 * kMaxWarps * a.teams);
+  t.zero = smem_u32(zero);
+  t.abort_flag = reinterpret_cast<volatile int*>(zero + 1);
+  if (tid == 0) *zero = make_uint4(0u, 0u, 0u, 0u);
   for (int i = tid; i < 2 * kMaxWarps * a.teams; i += static_cast<int>(blockDim.x)) red[i] = 0.f;
   for (int i = tid; i < a.teams * a.stages; i += static_cast<int>(blockDim.x)) mbar_init(&full[i], 1u);
   if (tid == 0) *t.abort_flag = 0;

@@ -11,13 +11,13 @@
 
 namespace blk {
 
-// One 16-byte vector, packed into its row; every lane of the warp takes part (`live`: the vector
-// exists).
+// One 16-byte vector, packed into its row; every lane of the warp takes part, with zeros where the
+// vector is not there (`live`).
 template <typename T>
 __device__ __forceinline__ void keep8(unsigned char* packed_row, int first_scale, int c, bool live,
                                       const uint4& u) {
   const uint4 one[1] = {u};
-  const uint32_t amax = act8_max_block(live ? act8_max8<T>(one) : 0u);
+  const uint32_t amax = act8_max_block(act8_max8<T>(one));
   if (!live) return;
   const uint32_t s = act8_scale_byte(amax);
   *reinterpret_cast<uint2*>(packed_row + 8 * c) = act8_pack8<T>(u, amax, s);
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
           f2 x[4];
-          VecOf<T>::unpack(lds128_if<kEven>(xs + 16u * c, c < NV), x);
+          VecOf<T>::unpack(lds128_at(kEven || (valid && c < NV) ? xs + 16u * c : t.zero), x);
 #pragma unroll
           for (int q = 0; q < 4; ++q) ss = f2_fma(x[q], x[q], ss);
         }
@@ -98,23 +98,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = t.lt + v * a.ntg;
-        const bool there = kEven || c < NV, live = valid && there;
-        f2 x[4], res[4];
-        const uint4 xw = lds128_if<kEven>(xs + 16u * c, there);
-        VecOf<T>::unpack(xw, x);
+        const bool live = kEven || (valid && c < NV);
         const bool add = kForm != kKeep || a.in[1].p != nullptr;
-        if (add) VecOf<T>::unpack(lds128_if<kEven>(rs + 16u * c, there), res);
+        const uint4 xw = lds128_at(live ? xs + 16u * c : t.zero);
+        uint4 o = xw;
+        if constexpr (kForm == kKeep) {
+          VecOf<T>::unpack(xw, h[v]);
+          if (add) {
+            f2 res[4];
+            VecOf<T>::unpack(lds128_at(live ? rs + 16u * c : t.zero), res);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (kForm == kKeep) {
-            h[v][q] = add ? f2_add(x[q], res[q]) : x[q];
-          } else {
+            for (int q = 0; q < 4; ++q) h[v][q] = f2_add(h[v][q], res[q]);
+            o = VecOf<T>::pack(h[v]);
+            VecOf<T>::unpack(o, h[v]);  // the norm of h as it is written
+          }
+        } else {
+          f2 x[4], res[4];
+          VecOf<T>::unpack(xw, x);
+          VecOf<T>::unpack(lds128_at(live ? rs + 16u * c : t.zero), res);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
             const f2 p = kPostN ? f2_mul(x[q], r1) : x[q];
             h[v][q] = f2_fma(p, k1[v][q], f2_mul(res[q], rscale));
           }
+          o = VecOf<T>::pack(h[v]);
         }
-        const uint4 o = VecOf<T>::pack(h[v]);
-        if constexpr (kForm == kKeep) VecOf<T>::unpack(o, h[v]);  // the norm of h as it is written
         if constexpr (kPreN) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) ss = f2_fma(h[v][q], h[v][q], ss);
