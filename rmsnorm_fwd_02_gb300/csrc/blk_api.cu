@@ -37,7 +37,10 @@ constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - (int64_t{1} << 16);
 constexpr size_t kSmemBytes = 226 * 1024;  // of the 227 KB that a CTA may take
 constexpr size_t kCopyBytes = 2048;  // least bytes of a copy, where rows are narrow
-constexpr int kMaxStages = 8;
+// At most three slots a team: more reads on their way at a time than that needs cost both ways
+// (65536 x 1536 forward: 136 us with three, 142 with four, 149 with two; backward 214 with three, 218
+// with four).
+constexpr int kMaxStages = 3;
 
 std::mutex g_mu;
 unsigned* g_err_ptr[kMaxDevices] = {};
@@ -62,9 +65,9 @@ int device_setup(unsigned** err) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads a row, vectors a thread, teams a CTA and CTAs: functions of R and H (and of the kernel's
-// threads).
-Shape team_shape(int64_t R, int H, int threads_cta) {
+// Threads a row, vectors a thread, teams a CTA and CTAs: functions of R, H and the kernel's threads
+// and form.
+Shape team_shape(int64_t R, int H, int threads_cta, int form) {
   Shape s{};
   const int nv = H / 8;
   auto threads = [&](int vpt) {
@@ -72,12 +75,17 @@ Shape team_shape(int64_t R, int H, int threads_cta) {
     return per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 ? 16 : static_cast<int>(ceil_div(per, 32)) * 32;
   };
   auto teams = [&](int ntg) { return threads_cta / (ntg < 32 ? 32 : ntg); };
-  // four vectors a thread, three where that keeps more threads busy, fewer in narrow rows; one where the rows are so few that each then has a team at once: the shortest way through a row
   auto busy = [&](int vpt) {  // threads of a CTA that have vectors
     const int ntg = threads(vpt), rows = ntg < 32 ? 32 / ntg : 1;
     return ntg > threads_cta ? 0 : teams(ntg) * rows * ((nv + vpt - 1) / vpt);
   };
-  s.vpt = nv <= 4 ? 1 : nv <= 8 ? 2 : (busy(3) > busy(4) ? 3 : 4);
+  // Four vectors a thread, fewer in narrow rows, three where that keeps more threads busy (30720 x
+  // 6144 backward, 256 threads against 192: 385 us against 423) -- but not in the 8-bit norm where
+  // its threads are then uneven (32768 x 8192 backward: 334 us against 296).
+  const bool three = busy(3) > busy(4) && (form != kKeep || nv == 3 * threads(3));
+  s.vpt = nv <= 4 ? 1 : nv <= 8 ? 2 : three ? 3 : 4;
+  // one where the rows are so few that each then has a team at once: the shortest way through a row
+  // (64 x 256 forward: 3.1 us against 5.6)
   if (nv > 16 && threads(1) <= threads_cta && R <= int64_t{kPartSMs} * teams(threads(1))) s.vpt = 1;
   s.ntg = threads(s.vpt);
   s.teams = teams(s.ntg);
@@ -120,8 +128,8 @@ void ring(Shape& s, int H, size_t row, size_t least, int sums) {
   if (s.smem < join) s.smem = join;
 }
 
-Shape plan(int64_t R, int H, int threads_cta, size_t row, size_t least, int sums) {
-  Shape s = team_shape(R, H, threads_cta);
+Shape plan(int64_t R, int H, int threads_cta, int form, size_t row, size_t least, int sums) {
+  Shape s = team_shape(R, H, threads_cta, form);
   ring(s, H, row, least, sums);
   return s;
 }
@@ -187,7 +195,7 @@ int run_fwd(const Fwd& f, void* stream) {
   if (st != RMSN_OK) return st;
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
-  const Shape s = plan(f.R, f.H, kFwdThreads, f.residual != nullptr ? 2 * row : row, row, 0);
+  const Shape s = plan(f.R, f.H, fwd_threads(f.form), f.form, f.residual != nullptr ? 2 * row : row, row, 0);
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -236,7 +244,7 @@ size_t s_floats(const Shape& s, int32_t H, int64_t N) {
   return static_cast<size_t>(rows) * H;
 }
 size_t workspace_bytes(int64_t R, int32_t H, int64_t N) {
-  const Shape s = team_shape(R, H, bwd_threads(kBoth)), keep = team_shape(R, H, bwd_threads(kKeep));
+  const Shape s = team_shape(R, H, bwd_threads(kBoth), kBoth), keep = team_shape(R, H, bwd_threads(kKeep), kKeep);
   const size_t both = pre_floats(s, H) + s_floats(s, H, N), one = pre_floats(keep, H);
   return sizeof(float) * (both > one ? both : one);
 }
@@ -268,7 +276,7 @@ int run_bwd(const Bwd& b, void* stream) {
   size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
-  const Shape s = plan(b.R, b.H, bwd_threads(b.form), row, least,
+  const Shape s = plan(b.R, b.H, bwd_threads(b.form), b.form, row, least,
                        (pre ? 1 : 0) + (s_sums ? 1 : 0));
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
@@ -356,7 +364,7 @@ int rmsnorm_act8_train_fwd(const void* x, const void* residual, int dtype, const
 
 size_t rmsnorm_act8_train_bwd_workspace_bytes(int64_t R, int32_t H) {
   if (check_sizes(R, H, 1) != RMSN_OK || R == 0) return 0;
-  return sizeof(float) * pre_floats(team_shape(R, H, bwd_threads(kKeep)), H);
+  return sizeof(float) * pre_floats(team_shape(R, H, bwd_threads(kKeep), kKeep), H);
 }
 
 int rmsnorm_act8_train_bwd(const void* packed, const void* dy, const void* dh, int dtype,
@@ -518,9 +526,9 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   if (R == 0) return RMSN_ERR_INVALID_ARG;
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
-  const Shape s = backward ? plan(R, H, bwd_threads(kBoth), 2 * wide + 2 * saved,
+  const Shape s = backward ? plan(R, H, bwd_threads(kBoth), kBoth, 2 * wide + 2 * saved,
                                   wide < saved ? wide : saved, 2)
-                           : plan(R, H, kFwdThreads, 2 * wide, wide, 0);
+                           : plan(R, H, fwd_threads(kBoth), kBoth, 2 * wide, wide, 0);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

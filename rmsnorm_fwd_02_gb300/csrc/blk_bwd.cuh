@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
   constexpr bool kX = kForm != kKeep;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint64_t pol = l2_evict_first_policy();
-  Team t = team_begin<4>(a, smem, pol);
+  Team t = team_begin<4>(a, smem, pol, a.samples == 1);
   const int NV = a.H >> 3;
   f2 w[VPT][4], k1[VPT][4], sum_pre[VPT][4], sum_s[VPT][4];
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
   uint32_t parity = 0;
   for (int32_t j = 0; j < t.nslots; ++j) {
     wait_slot(a, t, s, parity);
-    const int32_t ra = t.r0 + j * a.rows;
+    const int32_t ra = t.r0 + j * t.stride;
     const int32_t n = min(a.rows, t.r1 - ra);
     for (int32_t i = 0; i < n;) {
       if constexpr (kX) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
       const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
       // (a lane without a row has zeros throughout, and adds zeros to its columns' sums)
       const float r1 = valid ? r1_next : 0.f, r2 = valid ? r2_next : 0.f;
-      fetch(row + together);
+      fetch(i + together < n ? row + together : ra + t.stride + t.sub);
       const bool first = i == 0;
       i += together;
       // Packed vectors stay in registers between the passes over a row (h, then x in its place):
@@ -160,10 +160,11 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
           const bool live = kEven || (valid && c < NV);
-          f2 h[4], dy[4];
-          const float u = load_saved<T, kPacked>(a, t, hs, c, live, h);
-          VecOf<T>::unpack(lds128_at(live ? dys + 16u * c : t.zero), dy);
+          const uint4 dyw = lds128_at(live ? dys + 16u * c : t.zero);
           if constexpr (kPacked) {
+            f2 h[4], dy[4];
+            const float u = load_saved<T, kPacked>(a, t, hs, c, live, h);
+            VecOf<T>::unpack(dyw, dy);
             dot0 = f2_mul(f2_mul(dy[0], w[v][0]), h[0]);
             dot1 = f2_mul(f2_mul(dy[1], w[v][1]), h[1]);
             dot0 = f2_fma(f2_mul(dy[2], w[v][2]), h[2], dot0);
@@ -174,10 +175,11 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
 #pragma unroll
             for (int q = 0; q < 4; ++q) kept[v][q] = h[q];
           } else {
+            const uint4 hw = lds128_at(live ? hs + 16u * c : t.zero);
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
-              dot0 = f2_fma(f2_mul(dy[q], w[v][q]), h[q], dot0);
-              dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), h[q + 1], dot1);
+              dot0 = f2_fma(mul_exact<T>(u4_get(dyw, q), u4_get(hw, q)), w[v][q], dot0);
+              dot1 = f2_fma(mul_exact<T>(u4_get(dyw, q + 1), u4_get(hw, q + 1)), w[v][q + 1], dot1);
             }
           }
         }

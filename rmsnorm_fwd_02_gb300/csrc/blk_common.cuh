@@ -48,6 +48,42 @@ __device__ __forceinline__ float add_exact(float a, float b, float& err) {
   return s;
 }
 
+// The elementwise products of two words of two 16-bit values each, as an FP32 pair: exact (in BF16 16
+// bits, in FP16 22), by mixed-precision fma that reads the halves without a conversion.
+template <typename T>
+__device__ __forceinline__ f2 mul_exact(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    return bf2_mul_exact(a, b);
+  } else {
+    f2 r;
+    asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\t.reg .f32 p0, p1;\n\t"
+        "mov.b32 {a0, a1}, %1;\n\tmov.b32 {b0, b1}, %2;\n\t"
+        "fma.rn.f32.f16 p0, a0, b0, 0f80000000;\n\t"
+        "fma.rn.f32.f16 p1, a1, b1, 0f80000000;\n\t"
+        "mov.b64 %0, {p0, p1};\n\t}"
+        : "=l"(r.v)
+        : "r"(a), "r"(b));
+    return r;
+  }
+}
+// acc + a * a, likewise (the square is exact).
+template <typename T>
+__device__ __forceinline__ f2 square_onto(uint32_t a, f2 acc) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    return bf2_sq_acc(a, acc);
+  } else {
+    f2 r;
+    asm("{\n\t.reg .b16 a0, a1;\n\t.reg .f32 c0, c1, p0, p1;\n\t"
+        "mov.b32 {a0, a1}, %1;\n\tmov.b64 {c0, c1}, %2;\n\t"
+        "fma.rn.f32.f16 p0, a0, a0, c0;\n\t"
+        "fma.rn.f32.f16 p1, a1, a1, c1;\n\t"
+        "mov.b64 %0, {p0, p1};\n\t}"
+        : "=l"(r.v)
+        : "r"(a), "l"(acc.v));
+    return r;
+  }
+}
+
 // Whether every thread of a row has all its vectors, and every row of a warp is there: kernels are
 // built for that case apart, without a predicate on any vector.
 __host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
@@ -88,11 +124,12 @@ struct Team {
   uint32_t ring;        // shared address of the team's slots
   uint32_t zero;        // shared address of 16 bytes of zeros, what vectors that are not there read
   uint64_t* full;       // its barriers
-  float* red;           // [2][12]: warp sums, taken in turns
+  float* red;           // [2][16]: warp sums, taken in turns
   volatile int* abort_flag;
-  int32_t r0, r1;       // rows
+  int32_t r0, r1;       // first row; end of the rows
+  int32_t stride;       // rows between two of its slots' first
   int32_t nslots;
-  int64_t k;            // among all teams
+  int64_t k;            // among all teams (taking turns: the CTA)
   int lt;               // thread of the row
   int sub;              // row of the warp (teams of a part of a warp)
   int team;             // of the CTA
@@ -128,7 +165,7 @@ __device__ __forceinline__ void issue(const Args& a, Team& t, int32_t j, uint64_
   if (*t.abort_flag) return;
   t.issued = j + 1;
   const int s = j % a.stages;
-  const int32_t ra = t.r0 + j * a.rows;
+  const int32_t ra = t.r0 + j * t.stride;
   const int32_t n = min(a.rows, t.r1 - ra);
   uint32_t row = 0;
 #pragma unroll
@@ -152,8 +189,12 @@ __device__ __forceinline__ void issue(const Args& a, Team& t, int32_t j, uint64_
 }
 
 // Sets the CTA up; returns with the team's first slots on their way.
+// turns: a CTA's teams take the slots of its rows in turns (neighbouring rows at one time are
+// fewer streams of memory: 65536 x 1536 forward 151 us against 157); else each has a run of its
+// own.
 template <int kTensors>
-__device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, uint64_t pol) {
+__device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, uint64_t pol,
+                                           bool turns) {
   Team t;
   const int tid = static_cast<int>(threadIdx.x);
   const int per = a.ntg < 32 ? 32 : a.ntg;  // threads of a team
@@ -183,11 +224,19 @@ __device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, u
   __syncthreads();
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
-  const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
-  t.k = static_cast<int64_t>(blockIdx.x) * a.teams + t.team;
-  t.r0 = team_row(t.k, a.R, all);
-  t.r1 = team_row(t.k + 1, a.R, all);
-  t.nslots = (t.r1 - t.r0 + a.rows - 1) / a.rows;
+  if (turns) {
+    t.k = blockIdx.x;
+    t.stride = a.teams * a.rows;
+    t.r0 = team_row(t.k, a.R, gridDim.x) + t.team * a.rows;
+    t.r1 = team_row(t.k + 1, a.R, gridDim.x);
+  } else {
+    const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
+    t.k = static_cast<int64_t>(blockIdx.x) * a.teams + t.team;
+    t.stride = a.rows;
+    t.r0 = team_row(t.k, a.R, all);
+    t.r1 = team_row(t.k + 1, a.R, all);
+  }
+  t.nslots = t.r1 > t.r0 ? (t.r1 - t.r0 + t.stride - 1) / t.stride : 0;
   if (t.leader)
     for (int32_t j = 0; j < a.stages && j < t.nslots; ++j) issue<kTensors>(a, t, j, pol);
   return t;
@@ -220,6 +269,10 @@ __device__ __forceinline__ float row_sum(const Args& a, Team& t, float v) {
     if (t.warps > 8) {
       s = q[2];
       v += (s.x + s.y) + (s.z + s.w);
+      if (t.warps > 12) {
+        s = q[3];
+        v += (s.x + s.y) + (s.z + s.w);
+      }
     }
   }
   return v;

@@ -23,20 +23,20 @@ __device__ __forceinline__ void keep8(unsigned char* packed_row, int first_scale
   *reinterpret_cast<uint2*>(packed_row + 8 * c) = act8_pack8<T>(u, amax, s);
   if ((c & 3) == 0) packed_row[first_scale + (c >> 2)] = static_cast<unsigned char>(s);
 }
-// A packed row's padding (one thread).
-__device__ __forceinline__ void keep8_padding(const Args& a, unsigned char* p) {
+// A packed row's padding, by the row's threads.
+__device__ __forceinline__ void keep8_padding(const Args& a, int lt, unsigned char* p) {
   const int first = static_cast<int>(act8_scale_offset(a.H));
-  for (int i = a.H; i < first; ++i) p[i] = 0;
+  if (lt == 0 && a.H < first) *reinterpret_cast<uint2*>(p + a.H) = make_uint2(0u, 0u);
   const int end = static_cast<int>(act8_row_size(a.H));
-  for (int i = first + (a.H + kAct8Block - 1) / kAct8Block; i < end; ++i) p[i] = 0;
+  for (int i = first + (a.H + kAct8Block - 1) / kAct8Block + lt; i < end; i += a.ntg) p[i] = 0;
 }
 
 template <typename T, int VPT, int kForm, bool kPack, bool kEven>
-__global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(fwd_threads(kForm), 1) blk_fwd_kernel(const FwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint64_t pol = l2_evict_first_policy();
-  Team t = team_begin<2>(a, smem, pol);
+  Team t = team_begin<2>(a, smem, pol, true);
   const int NV = a.H >> 3;
   f2 w[VPT][4];   // w_pre
   f2 k1[VPT][4];  // scale * gate * w_post
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
   uint32_t parity = 0;
   for (int32_t j = 0; j < t.nslots; ++j) {
     wait_slot(a, t, s, parity);
-    const int32_t ra = t.r0 + j * a.rows;
+    const int32_t ra = t.r0 + j * t.stride;
     const int32_t n = min(a.rows, t.r1 - ra);
     for (int32_t i = 0; i < n; i += step) {
       const int32_t row = ra + i + t.sub;
@@ -81,10 +81,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
-          f2 x[4];
-          VecOf<T>::unpack(lds128_at(kEven || (valid && c < NV) ? xs + 16u * c : t.zero), x);
+          const uint4 xw = lds128_at(kEven || (valid && c < NV) ? xs + 16u * c : t.zero);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) ss = f2_fma(x[q], x[q], ss);
+          for (int q = 0; q < 4; ++q) ss = square_onto<T>(u4_get(xw, q), ss);
         }
         const float sum = row_sum(a, t, f2_lo(ss) + f2_hi(ss));
         if (i == 0 && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
@@ -136,9 +135,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) blk_fwd_kernel(const FwdArgs a
         }
       }
       if constexpr (kPack) {
-        if (padded && valid && t.lt == 0) {
-          if (kForm != kKeep && a.x8 != nullptr) keep8_padding(a, a.x8 + row * packed_row);
-          if (kPreN) keep8_padding(a, a.h8 + row * packed_row);
+        if (padded && valid) {
+          if (kForm != kKeep && a.x8 != nullptr) keep8_padding(a, t.lt, a.x8 + row * packed_row);
+          if (kPreN) keep8_padding(a, t.lt, a.h8 + row * packed_row);
         }
       }
       if constexpr (kPreN) {

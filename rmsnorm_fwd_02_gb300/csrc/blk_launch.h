@@ -11,11 +11,15 @@ namespace blk {
 constexpr int kMaxH = 8192;
 // Most threads of a CTA, one CTA an SM.  A row costs a thread some 150 instructions (its waits,
 // the sums' reduction, rstd, addresses) whatever its share of the row, so threads own 32 elements
-// where the row has them, with the registers that takes.
+// where the row has them, and as many threads run as have the registers for that: the waiting row
+// and one weight in 128 (32768 x 4096 forward: 112 us with 512 threads, 128 with 384), two weights
+// in 168 (with 512 threads of 24 elements 171 us against 177, but from 8 bits 240 against 218); in
+// the backward column sums besides, of which one fits 168, two take 255 (with 512 threads of 16
+// elements 265 us as well as 266, but from 8 bits 302 against 272).
 enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
-constexpr int kFwdThreads = 384;
+constexpr int fwd_threads(int form) { return form == kKeep ? 512 : 384; }
 constexpr int bwd_threads(int form) { return form == kKeep ? 384 : 256; }
-constexpr int kMaxWarps = 12;
+constexpr int kMaxWarps = 16;
 constexpr int kMaxTensors = 4;    // staged
 // CTAs of the backward at most, whatever the GPU: the rows' partition, and with it the order of
 // every sum, is a function of the shape.  GB300 has 152 SMs: there it is one wave.
