@@ -102,9 +102,12 @@ Shape team_shape(int64_t R, int H, int threads_cta, int form) {
 
 }  // namespace
 
+static size_t factor_bytes(const Shape& s) {
+  return 32 * static_cast<size_t>(s.teams) * s.ntg * s.vpt;
+}
 size_t smem_bytes(const Shape& s) {
   const size_t n = static_cast<size_t>(s.teams) * s.stages;
-  return n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 32;
+  return (s.factor ? factor_bytes(s) : 0) + n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 32;
 }
 
 namespace {
@@ -128,8 +131,10 @@ void ring(Shape& s, int H, size_t row, size_t least, int sums) {
   if (s.smem < join) s.smem = join;
 }
 
-Shape plan(int64_t R, int H, int threads_cta, int form, size_t row, size_t least, int sums) {
+Shape plan(int64_t R, int H, int threads_cta, int form, size_t row, size_t least, int sums,
+           bool factor = false) {
   Shape s = team_shape(R, H, threads_cta, form);
+  s.factor = factor;
   ring(s, H, row, least, sums);
   return s;
 }
@@ -277,7 +282,7 @@ int run_bwd(const Bwd& b, void* stream) {
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
   const Shape s = plan(b.R, b.H, bwd_threads(b.form), b.form, row, least,
-                       (pre ? 1 : 0) + (s_sums ? 1 : 0));
+                       (pre ? 1 : 0) + (s_sums ? 1 : 0), factor_in_smem(b.form, b.packed));
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
   const size_t need = sizeof(float) * ((pre ? pre_floats(s, b.H) : 0) +
@@ -293,6 +298,7 @@ int run_bwd(const Bwd& b, void* stream) {
   a.residual_scale = b.residual_scale;
   a.rstd_pre = b.rstd_pre;
   a.rstd_post = b.rstd_post;
+  a.factor_at = static_cast<uint32_t>(smem_bytes(s) - (s.factor ? factor_bytes(s) : 0));
   a.dx = b.dx;
   a.dres = b.dres;
   a.part_pre = pre ? ws : nullptr;
@@ -527,7 +533,7 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
   const Shape s = backward ? plan(R, H, bwd_threads(kBoth), kBoth, 2 * wide + 2 * saved,
-                                  wide < saved ? wide : saved, 2)
+                                  wide < saved ? wide : saved, 2, factor_in_smem(kBoth, packed != 0))
                            : plan(R, H, fwd_threads(kBoth), kBoth, 2 * wide, wide, 0);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};

@@ -80,7 +80,42 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
   const uint64_t pol = l2_evict_first_policy();
   Team t = team_begin<4>(a, smem, pol, a.samples == 1);
   const int NV = a.H >> 3;
-  f2 w[VPT][4], k1[VPT][4], sum_pre[VPT][4], sum_s[VPT][4];
+  // From 8 bits with both norms the factor of the branch lives in shared memory, each thread's part
+  // for itself alone (the rows of a warp share theirs): the sums, w, the kept vectors and m fill the registers.
+  constexpr bool kFactorMem = factor_in_smem(kForm, kPacked);
+  f2 w[VPT][4], k1[kFactorMem ? 1 : VPT][4], sum_pre[VPT][4], sum_s[VPT][4];
+  float4* const k1_mem =
+      reinterpret_cast<float4*>(smem + a.factor_at) + t.team * (2 * VPT * a.ntg) + t.lt;
+  auto set_factor = [&](int32_t n) {
+    if constexpr (kFactorMem) {
+      f2 f[VPT][4];
+      load_factor<VPT, kPostN>(a, n, t.lt, f);
+      __syncwarp();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        if (t.sub != 0) continue;  // (the rows of a warp have one sample)
+        k1_mem[(2 * v) * a.ntg] =
+            make_float4(f2_lo(f[v][0]), f2_hi(f[v][0]), f2_lo(f[v][1]), f2_hi(f[v][1]));
+        k1_mem[(2 * v + 1) * a.ntg] =
+            make_float4(f2_lo(f[v][2]), f2_hi(f[v][2]), f2_lo(f[v][3]), f2_hi(f[v][3]));
+      }
+      __syncwarp();
+    } else {
+      load_factor<VPT, kPostN>(a, n, t.lt, k1);
+    }
+  };
+  auto get_factor = [&](int v, f2 (&f)[4]) {
+    if constexpr (kFactorMem) {
+      const float4 p = k1_mem[(2 * v) * a.ntg], q = k1_mem[(2 * v + 1) * a.ntg];
+      f[0] = f2_make(p.x, p.y);
+      f[1] = f2_make(p.z, p.w);
+      f[2] = f2_make(q.x, q.y);
+      f[3] = f2_make(q.z, q.w);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] = k1[v][q];
+    }
+  };
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = t.lt + v * a.ntg;
@@ -102,7 +137,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
   int32_t sample = kX ? t.r0 / a.L : 0;
   int32_t next_sample = (sample + 1) * a.L;  // the row from which k1 and S are another sample's
   if constexpr (kX) {
-    if (t.r0 < t.r1) load_factor<VPT, kPostN>(a, sample, t.lt, k1);
+    if (t.r0 < t.r1) set_factor(sample);
   }
   // the r's of the row ahead, so that no row waits for them
   float r1_next = 0.f, r2_next = 0.f;
@@ -131,7 +166,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
           write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
           sample = (ra + i) / a.L;
           next_sample = (sample + 1) * a.L;
-          load_factor<VPT, kPostN>(a, sample, t.lt, k1);
+          set_factor(sample);
         }
       }
       const int32_t together = take(ra + i, n - i);
@@ -234,13 +269,14 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
         if constexpr (kX) {
           f2 x[4];
           const float u = load_saved<T, kPacked>(a, t, xs, c, live, x);
-          f2 rx = kPostN ? r1v : f2_splat(1.f);
+          f2 rx = kPostN ? r1v : f2_splat(1.f), f[4];
+          get_factor(v, f);
           if constexpr (kPacked) rx = f2_mul(rx, f2_splat(u));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
             sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
-            m[v][q] = f2_mul(g[q], k1[v][q]);
+            m[v][q] = f2_mul(g[q], f[q]);
           }
           if constexpr (kPostN && kPacked) {
             dot0 = f2_mul(m[v][0], x[0]);

@@ -46,6 +46,7 @@ struct Shape {
   int stages;   // slots a team
   int threads;  // a CTA
   int P;        // CTAs
+  bool factor;  // the branch's factors are in shared memory
   size_t slot;  // bytes
   size_t smem;  // bytes
 };
@@ -88,10 +89,15 @@ struct BwdArgs : Args {
   const float* rstd_post;
   void* dx;
   void* dres;
+  uint32_t factor_at; // where the branch's factors lie in shared memory (factor_in_smem)
   float* part_pre;    // [P][H]: sums of dy * hhat, a row a CTA
   float* part_s;      // sums of t * xhat: [P][H], a row a CTA, or with several samples
                       // [P * teams + N - 1][H], a row a team and sample
 };
+
+// Backward builds whose branch's factor (scale * gate * w_post of a thread's columns) is in shared
+// memory: 4 bytes an element that a team's threads own, after everything else.
+__host__ __device__ constexpr bool factor_in_smem(int form, bool packed) { return form == kBoth && packed; }
 
 // First row of team k of n.
 __host__ __device__ inline int32_t team_row(int64_t k, int64_t R, int64_t n) {
