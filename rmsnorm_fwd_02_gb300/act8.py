@@ -33,10 +33,22 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .dropout import _empty_strided, _flat, _layout, _like, _on, _same_device
+from .dropout import _empty_strided, _flat, _layout, _like, _same_device
 from .ops import EPS
 
 _CODES = {torch.bfloat16: N.ACT8_BF16, torch.float32: N.ACT8_FP32, torch.float16: N.ACT8_FP16}
+_NARROW = {torch.bfloat16: N.ACT8_BF16, torch.float16: N.ACT8_FP16}
+
+# A call's checks, allocations and marshalling take longer than a small call's kernels, so the
+# paths below ask each tensor once for what they need.  The current device comes without torch's
+# lazy initialization (a CUDA tensor is there), where this torch has that (a private name).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(x: torch.Tensor):
+    """A context for x's device where it is not the current one (the C ABI works on that), or
+    None."""
+    return None if x.get_device() == _current_device() else torch.cuda.device(x.device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -54,7 +66,7 @@ def _layouts(shape):
     return _layout(shape), _layout(shape[:-1]), _layout((*shape[:-1], act8_row_bytes(shape[-1])))
 
 
-_WIDTHS = functools.lru_cache(maxsize=4096)(lambda h: _layout((h,)))
+_width = functools.lru_cache(maxsize=4096)(lambda h: _layout((h,)))
 
 
 def _rows(x: torch.Tensor, name: str):
@@ -79,9 +91,10 @@ def _rows(x: torch.Tensor, name: str):
 
 
 def _narrow(x: torch.Tensor, name: str) -> int:
-    if not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float16):
+    code = _NARROW.get(x.dtype)
+    if code is None or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 or float16 tensor")
-    return _CODES[x.dtype]
+    return code
 
 
 def _row_input(x: torch.Tensor, name: str):
@@ -89,40 +102,58 @@ def _row_input(x: torch.Tensor, name: str):
     rows, h, stride = _rows(x, name)
     if h & 7 or h > 8192:
         raise ValueError(f"{name}'s last axis must be a multiple of 8 up to 8192")
-    if stride % 8 or x.data_ptr() % 16:
+    if stride & 7 or x.data_ptr() & 15:
         raise ValueError(f"{name}'s rows must start at 16-byte boundaries")
     return rows, h, stride
 
 
+def _grad_rows(g: torch.Tensor, name: str):
+    """Rows and H of a gradient (of any strides)."""
+    shape = g.shape
+    h = shape[-1] if len(shape) else 0
+    if h < 8 or h & 7 or h > 8192:
+        raise ValueError(f"{name}'s last axis must be a multiple of 8 up to 8192")
+    return (shape[0] if len(shape) == 2 else math.prod(shape[:-1])), h
+
+
 def _weight(w, h: int, name: str) -> int:
-    if w.dtype not in _CODES:
+    code = _CODES.get(w.dtype)
+    if code is None:
         raise TypeError(f"{name} must be bfloat16, float16 or float32")
-    if w.shape != (h,):
+    if w.dim() != 1 or w.numel() != h:
         raise ValueError(f"{name} must have shape ({h},)")
-    return _CODES[w.dtype]
+    return code
 
 
-def _row_scalars(t, x: torch.Tensor, name: str):
-    if t.shape != x.shape[:-1] or t.dtype != torch.float32:
-        raise ValueError(f"{name} must have shape {tuple(x.shape[:-1])} and dtype float32")
-    return t.contiguous()
+def _ready(t):
+    """t, or a copy, contiguous at a 16-byte boundary; None stays."""
+    return t if t is None or (t.is_contiguous() and not t.data_ptr() & 15) else _flat(t)
+
+
+def _row_scalars(t, lead, name: str):
+    if t.shape != lead or t.dtype != torch.float32:
+        raise ValueError(f"{name} must have shape {tuple(lead)} and dtype float32")
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _packed(p, lead, h: int, name: str):
     """A packed tensor of rows [*lead, h], contiguous at a 16-byte boundary."""
-    want = (*lead, act8_row_bytes(h))
-    if p.dtype != torch.uint8 or p.shape != want:
-        raise ValueError(f"{name} must be a packed tensor: uint8 {want}")
-    return _flat(p)
+    if p.dtype != torch.uint8 or p.shape != (*lead, act8_row_bytes(h)):
+        raise ValueError(f"{name} must be a packed tensor: uint8 {(*lead, act8_row_bytes(h))}")
+    return _ready(p)
 
 
 def act8_pack(x):
-    if not x.is_cuda or x.dtype not in _CODES:
+    code = _CODES.get(x.dtype)
+    if code is None or not x.is_cuda:
         raise TypeError("x must be a CUDA bfloat16, float16 or float32 tensor")
     rows, h, stride = _rows(x, "x")
-    with _on(x):
-        packed = _empty_strided(*_layouts(x.shape)[2], torch.uint8)
-        N.act8_train_pack(x, _CODES[x.dtype], packed, rows, h, stride)
+    there = _elsewhere(x)
+    if there is not None:
+        with there:
+            return act8_pack(x)
+    packed = _empty_strided(*_layouts(x.shape)[2], torch.uint8)
+    N.act8_train_pack(x, code, packed, rows, h, stride)
     return packed
 
 
@@ -133,9 +164,12 @@ def act8_unpack(packed, H, dtype=torch.bfloat16):
         raise TypeError("dtype must be bfloat16, float16 or float32")
     lead = packed.shape[:-1]
     packed = _packed(packed, lead, H, "packed")
-    with _on(packed):
-        x = _empty_strided(*_layout((*lead, H)), dtype)
-        N.act8_train_unpack(packed, x, _CODES[dtype], math.prod(lead), H)
+    there = _elsewhere(packed)
+    if there is not None:
+        with there:
+            return act8_unpack(packed, H, dtype)
+    x = _empty_strided(*_layout((*lead, H)), dtype)
+    N.act8_train_unpack(packed, x, _CODES[dtype], math.prod(lead), H)
     return x
 
 
@@ -146,17 +180,20 @@ def rmsnorm_act8_fwd(x, w, eps=EPS, residual=None):
     s_res = h
     if residual is not None:
         _like(x, "residual", residual)
-        _, _, s_res = _row_input(residual, "residual")
+        s_res = _row_input(residual, "residual")[2]
     _same_device(x, residual, w)
-    w = _flat(w)
+    there = _elsewhere(x)
+    if there is not None:
+        with there:
+            return rmsnorm_act8_fwd(x, w, eps, residual)
     full, lead, kept = _layouts(x.shape)
-    with _on(x):
-        y = _empty_strided(*full, x.dtype)
-        h_out = _empty_strided(*full, x.dtype) if residual is not None else None
-        rstd = _empty_strided(*lead, torch.float32)
-        packed = _empty_strided(*kept, torch.uint8)
-        N.rmsnorm_act8_train_fwd(x, residual, code, w, w_code, y, h_out, rstd, packed, rows, h, s_x,
-                                 s_res, float(eps))
+    dtype = x.dtype
+    y = _empty_strided(*full, dtype)
+    h_out = _empty_strided(*full, dtype) if residual is not None else None
+    rstd = _empty_strided(*lead, torch.float32)
+    packed = _empty_strided(*kept, torch.uint8)
+    N.rmsnorm_act8_train_fwd(x, residual, code, _ready(w), w_code, y, h_out, rstd, packed, rows, h,
+                             s_x, s_res, float(eps))
     return (y, rstd, packed) if residual is None else (y, rstd, packed, h_out)
 
 
@@ -167,24 +204,24 @@ _bwd_bytes = functools.lru_cache(maxsize=4096)(
 
 def rmsnorm_act8_bwd(dy, x8, rstd, w, dh=None):
     code = _narrow(dy, "dy")
-    h = dy.shape[-1] if dy.dim() else 0
-    if h < 8 or h % 8 or h > 8192:
-        raise ValueError("dy's last axis must be a multiple of 8 up to 8192")
-    rows = math.prod(dy.shape[:-1])
+    rows, h = _grad_rows(dy, "dy")
+    full, (lead, _), _ = _layouts(dy.shape)
     w_code = _weight(w, h, "w")
-    x8 = _packed(x8, dy.shape[:-1], h, "x8")
-    rstd = _row_scalars(rstd, dy, "rstd")
+    x8 = _packed(x8, lead, h, "x8")
+    rstd = _row_scalars(rstd, lead, "rstd")
     if dh is not None:
         _like(dy, "dh", dh)
-        dh = _flat(dh)
     _same_device(dy, x8, rstd, w, dh)
-    dy, w = _flat(dy), _flat(w)
-    with _on(dy):
-        dx = _empty_strided(*_layout(dy.shape), dy.dtype)
-        dw = _empty_strided(*_WIDTHS(h), torch.float32)
-        nbytes = _bwd_bytes(rows, h)
-        ws = _empty_strided((nbytes,), (1,), torch.uint8) if nbytes else None
-        N.rmsnorm_act8_train_bwd(x8, dy, dh, code, rstd, w, w_code, dx, dw, ws, nbytes, rows, h)
+    there = _elsewhere(dy)
+    if there is not None:
+        with there:
+            return rmsnorm_act8_bwd(dy, x8, rstd, w, dh)
+    dx = _empty_strided(*full, dy.dtype)
+    dw = _empty_strided(*_width(h), torch.float32)
+    nbytes = _bwd_bytes(rows, h)
+    ws = _empty_strided((nbytes,), (1,), torch.uint8) if nbytes else None
+    N.rmsnorm_act8_train_bwd(x8, _ready(dy), _ready(dh), code, rstd, _ready(w), w_code, dx, dw, ws,
+                             nbytes, rows, h)
     return dx, dw
 
 

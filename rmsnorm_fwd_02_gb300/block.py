@@ -35,38 +35,37 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .act8 import _CODES, _WIDTHS, _layouts, _narrow, _packed, _row_input, _row_scalars, _weight
-from .dropout import _empty_strided, _flat, _layout, _like, _on, _same_device
+from .act8 import (_CODES, _elsewhere, _grad_rows, _layouts, _narrow, _packed, _ready, _row_input,
+                   _row_scalars, _weight, _width)
+from .dropout import _empty_strided, _layout, _like, _same_device
 from .ops import EPS
 
 
-def _factors(x, others, rows: int, h: int, w_pre, w_post, gate, scale, residual_scale):
-    """Checks the weights, the gate and the scales, and that all tensors are on x's device; the
-    weights' and the gate's codes, N."""
-    if w_pre is None and w_post is None:
+def _factors(rows: int, h: int, w_pre, w_post, gate, scale, residual_scale):
+    """Checks the weights, the gate and the scales; the weights' and the gate's codes, N."""
+    if w_pre is not None:
+        code = _weight(w_pre, h, "w_pre")
+        if w_post is not None and _weight(w_post, h, "w_post") != code:
+            raise TypeError("w_pre and w_post must have one dtype")
+    elif w_post is not None:
+        code = _weight(w_post, h, "w_post")
+    else:
         raise ValueError("one of w_pre and w_post must be given")
-    codes = [_weight(w, h, name) for w, name in ((w_pre, "w_pre"), (w_post, "w_post"))
-             if w is not None]
-    if codes[0] != codes[-1]:
-        raise TypeError("w_pre and w_post must have one dtype")
     gate_code, n = 0, 1
     if gate is not None:
-        if gate.dtype not in _CODES:
+        gate_code = _CODES.get(gate.dtype)
+        if gate_code is None:
             raise TypeError("gate must be bfloat16, float16 or float32")
-        gate_code = _CODES[gate.dtype]
-        if gate.dim() not in (1, 2) or gate.shape[-1] != h:
+        shape = gate.shape
+        if len(shape) not in (1, 2) or shape[-1] != h:
             raise ValueError(f"gate must be [{h}] or [N, {h}]")
-        n = gate.shape[0] if gate.dim() == 2 else 1
+        if len(shape) == 2:
+            n = shape[0]
         if n < 1 or rows % n:
             raise ValueError(f"{rows} rows do not divide into gate's {n}")
-    _same_device(x, *others, w_pre, w_post, gate)
     if not (math.isfinite(scale) and math.isfinite(residual_scale)):
         raise ValueError("scale and residual_scale must be finite")
-    return codes[0], gate_code, n
-
-
-def _opt_flat(t):
-    return None if t is None else _flat(t)
+    return code, gate_code, n
 
 
 def rmsnorm_block_fwd(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0,
@@ -74,27 +73,32 @@ def rmsnorm_block_fwd(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0
     code = _narrow(x, "x")
     rows, h, s_x = _row_input(x, "x")
     _like(x, "residual", residual)
-    _, _, s_res = _row_input(residual, "residual")
-    w_code, gate_code, n = _factors(x, (residual,), rows, h, w_pre, w_post, gate, scale, residual_scale)
+    s_res = _row_input(residual, "residual")[2]
+    w_code, gate_code, n = _factors(rows, h, w_pre, w_post, gate, scale, residual_scale)
+    _same_device(x, residual, w_pre, w_post, gate)
+    there = _elsewhere(x)
+    if there is not None:
+        with there:
+            return rmsnorm_block_fwd(x, residual, w_pre, w_post, gate, scale, residual_scale, eps,
+                                     act8)
     full, lead, kept = _layouts(x.shape)
     dtype = x.dtype
-    with _on(x):
-        out_h = _empty_strided(*full, dtype)
-        y = rstd_pre = rstd_post = x8 = h8 = None
+    out_h = _empty_strided(*full, dtype)
+    y = rstd_pre = rstd_post = x8 = h8 = None
+    if w_pre is not None:
+        y = _empty_strided(*full, dtype)
+        rstd_pre = _empty_strided(*lead, torch.float32)
+    if w_post is not None:
+        rstd_post = _empty_strided(*lead, torch.float32)
+    if act8:
+        if w_post is not None or gate is not None:
+            x8 = _empty_strided(*kept, torch.uint8)
         if w_pre is not None:
-            y = _empty_strided(*full, dtype)
-            rstd_pre = _empty_strided(*lead, torch.float32)
-        if w_post is not None:
-            rstd_post = _empty_strided(*lead, torch.float32)
-        if act8:
-            if w_post is not None or gate is not None:
-                x8 = _empty_strided(*kept, torch.uint8)
-            if w_pre is not None:
-                h8 = _empty_strided(*kept, torch.uint8)
-        N.rmsnorm_block_train_fwd(x, residual, code, _opt_flat(w_pre), _opt_flat(w_post), w_code,
-                                  _opt_flat(gate), gate_code, n, y, out_h, rstd_pre, rstd_post,
-                                  x8, h8, rows, h, s_x, s_res, float(scale),
-                                  float(residual_scale), float(eps))
+            h8 = _empty_strided(*kept, torch.uint8)
+    N.rmsnorm_block_train_fwd(x, residual, code, _ready(w_pre), _ready(w_post), w_code,
+                              _ready(gate), gate_code, n, y, out_h, rstd_pre, rstd_post, x8, h8,
+                              rows, h, s_x, s_res, float(scale), float(residual_scale),
+                              float(eps))
     out = (y, out_h, rstd_pre, rstd_post)
     return out + (x8, h8) if act8 else out
 
@@ -104,65 +108,63 @@ _bwd_bytes = functools.lru_cache(maxsize=4096)(
     lambda *shape: N.rmsnorm_block_train_bwd_workspace_bytes(*shape))
 
 
-def _kept(t, grad, h: int, name: str):
+def _kept(t, grad, lead, h: int, name: str):
     """A kept activation of grad's rows: (tensor, elements between rows, whether it is packed)."""
     if t is None:
         raise ValueError(f"{name} must be given")
     if t.dtype == torch.uint8:
-        return _packed(t, grad.shape[:-1], h, name), h, True
+        return _packed(t, lead, h, name), h, True
     _like(grad, name, t)
-    _, _, stride = _row_input(t, name)
-    return t, stride, False
+    return t, _row_input(t, name)[2], False
 
 
 def rmsnorm_block_bwd(dy, x, h, rstd_pre, rstd_post, w_pre=None, w_post=None, gate=None, scale=1.0,
                       residual_scale=1.0, dh=None):
     if (dy is None) != (w_pre is None):
         raise ValueError("dy must be given with w_pre, and only then")
-    grad = dh if dy is None else dy
+    grad, name = (dh, "dh") if dy is None else (dy, "dy")
     if grad is None:
         raise ValueError("dh must be given without w_pre")
-    code = _narrow(grad, "dh" if dy is None else "dy")
-    width = grad.shape[-1] if grad.dim() else 0
-    if width < 8 or width % 8 or width > 8192:
-        raise ValueError("the gradients' last axis must be a multiple of 8 up to 8192")
-    rows = math.prod(grad.shape[:-1])
-    if dh is not None:
-        _like(grad, "dh", dh)
-        dh = _flat(dh)
-    dy = _opt_flat(dy)
-    kinds, s_x = set(), width
+    code = _narrow(grad, name)
+    rows, width = _grad_rows(grad, name)
+    full, (lead, _), _ = _layouts(grad.shape)
+    if dh is not None and dy is not None:
+        _like(dy, "dh", dh)
+    w_code, gate_code, n = _factors(rows, width, w_pre, w_post, gate, scale, residual_scale)
+    s_x, packed = width, None
     if w_pre is not None:
-        h, s_h, packed = _kept(h, grad, width, "h")
-        if not packed and s_h != width:
+        h, s_h, packed = _kept(h, grad, lead, width, "h")
+        if s_h != width:
             raise ValueError("h must be contiguous")
-        kinds.add(packed)
-        rstd_pre = _row_scalars(rstd_pre, grad, "rstd_pre")
+        rstd_pre = _row_scalars(rstd_pre, lead, "rstd_pre")
     else:
         h = rstd_pre = None
     if w_post is not None or gate is not None:
-        x, s_x, packed = _kept(x, grad, width, "x")
-        kinds.add(packed)
+        x, s_x, x_packed = _kept(x, grad, lead, width, "x")
+        if packed is not None and packed != x_packed:
+            raise ValueError("x and h must both be activations or both packed")
+        packed = x_packed
     else:
         x = None
-    rstd_post = _row_scalars(rstd_post, grad, "rstd_post") if w_post is not None else None
-    if len(kinds) > 1:
-        raise ValueError("x and h must both be activations or both packed")
-    w_code, gate_code, n = _factors(grad, (dy, dh, x, h, rstd_pre, rstd_post), rows, width, w_pre,
-                                    w_post, gate, scale, residual_scale)
-    with _on(grad):
-        full, one = _layout(grad.shape), _WIDTHS(width)
-        dx = _empty_strided(*full, grad.dtype)
-        dres = _empty_strided(*full, grad.dtype)
-        dw_pre = _empty_strided(*one, torch.float32) if w_pre is not None else None
-        dw_post = _empty_strided(*one, torch.float32) if w_post is not None else None
-        dgate = _empty_strided(*_layout(gate.shape), torch.float32) if gate is not None else None
-        nbytes = _bwd_bytes(rows, width, n)
-        ws = _empty_strided((nbytes,), (1,), torch.uint8) if nbytes else None
-        N.rmsnorm_block_train_bwd(dy, dh, x, h, packed, code, rstd_pre, rstd_post,
-                                  _opt_flat(w_pre), _opt_flat(w_post), w_code, _opt_flat(gate),
-                                  gate_code, n, dx, dres, dw_pre, dw_post, dgate, ws, nbytes, rows,
-                                  width, s_x, float(scale), float(residual_scale))
+    rstd_post = _row_scalars(rstd_post, lead, "rstd_post") if w_post is not None else None
+    _same_device(grad, dy, dh, x, h, rstd_pre, rstd_post, w_pre, w_post, gate)
+    there = _elsewhere(grad)
+    if there is not None:
+        with there:
+            return rmsnorm_block_bwd(dy, x, h, rstd_pre, rstd_post, w_pre, w_post, gate, scale,
+                                     residual_scale, dh)
+    one = _width(width)
+    dx = _empty_strided(*full, grad.dtype)
+    dres = _empty_strided(*full, grad.dtype)
+    dw_pre = _empty_strided(*one, torch.float32) if w_pre is not None else None
+    dw_post = _empty_strided(*one, torch.float32) if w_post is not None else None
+    dgate = _empty_strided(*_layout(gate.shape), torch.float32) if gate is not None else None
+    nbytes = _bwd_bytes(rows, width, n)
+    ws = _empty_strided((nbytes,), (1,), torch.uint8) if nbytes else None
+    N.rmsnorm_block_train_bwd(_ready(dy), _ready(dh), x, h, packed, code, rstd_pre, rstd_post,
+                              _ready(w_pre), _ready(w_post), w_code, _ready(gate), gate_code, n,
+                              dx, dres, dw_pre, dw_post, dgate, ws, nbytes, rows, width, s_x,
+                              float(scale), float(residual_scale))
     return dx, dres, dw_pre, dw_post, dgate
 
 
