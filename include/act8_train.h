@@ -38,15 +38,15 @@ extern "C" {
 #define ACT8_FP32 1
 #define ACT8_FP16 2
 
-/* Bytes of a packed row of H values; 0 unless 1 <= H < 2^31.  Host-only. */
+/* Bytes of a packed row of H values; 0 unless 1 <= H <= 2^30.  Host-only. */
 int64_t act8_train_row_bytes(int64_t H);
 
 /*
  * Packs R rows of H values.
- *   x       dtype ACT8_*, row r at element r * s_row, aligned to its elements (whole 16-byte
- *           vectors are read where pointer and s_row allow it)
+ *   x       dtype ACT8_*, row r at element r * s_row, aligned to its elements (memory is read
+ *           in whole 16-byte vectors that hold an element of the row)
  *   packed  [R, act8_train_row_bytes(H)] out, 16-byte aligned
- * R * act8_train_row_bytes(H) <= 2^42 (RMSN_ERR_UNSUPPORTED above).  R == 0 returns RMSN_OK with
+ * H <= 2^30, R * act8_train_row_bytes(H) <= 2^42 (RMSN_ERR_UNSUPPORTED above).  R == 0 returns RMSN_OK with
  * nothing enqueued (pointers may then be NULL).
  */
 int act8_train_pack(const void* x, int dtype, void* packed, int64_t R, int64_t H, int64_t s_row,

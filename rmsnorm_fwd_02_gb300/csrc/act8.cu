@@ -22,28 +22,90 @@ struct Act8Args {
   void* out;
   int64_t R, H, s_row;   // s_row: elements between rows of the wide tensor
   uint32_t groups;       // groups a row, a multiple of 4
-  uint32_t total;        // flat launches: R * groups, below 2^31,
+  uint32_t tiles;        // wide rows: tiles of 32 groups a row
+  uint32_t total;        // narrow rows: R * groups, below 2^31,
   uint32_t mul, shift;   // and division by groups: (i * mul) >> (32 + shift)
-  int32_t vec;           // 16-byte accesses are allowed
+  int32_t vec;           // rows start at 16-byte vectors and are whole groups
 };
+
+// Elements of group c that the row has: 8, fewer in its last one, 0 or less behind it (a row has at
+// most 2^30).
+__device__ __forceinline__ int group_size(const Act8Args& a, int c) {
+  return min(static_cast<int>(a.H) - 8 * c, 8);
+}
 
 template <typename T>
 using Words = uint4[sizeof(T) / 2];  // a group of eight elements
 
-// Eight elements from p, of which n (1..8) exist.
-template <typename T>
-__device__ __forceinline__ void load_group(const T* p, int64_t n, bool vec, Words<T>& u) {
-  if (vec && n >= 8) {
+// N words from `bytes` bytes on of w (bytes a multiple of the elements' size, below 16).
+template <int N, int kFrom, bool kHalves>
+__device__ __forceinline__ void words_from(const uint32_t (&w)[N + 4], uint32_t bytes, uint32_t (&o)[N]) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-      u[i] = reinterpret_cast<const uint4*>(p)[i];
-  } else {
-    T* q = reinterpret_cast<T*>(u);
+  for (int i = 0; i < N; ++i) o[i] = w[i + kFrom];
+  if constexpr (kHalves) {
+    if (bytes & 2u) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) q[i] = p[i];
+      for (int i = 0; i < N; ++i) o[i] = __funnelshift_r(w[i + kFrom], w[i + kFrom + 1], 16);
+    }
   }
 }
+template <int N, bool kHalves>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[N + 4], uint32_t bytes, uint32_t (&o)[N]) {
+  switch (bytes >> 2) {  // (mostly the same for a whole warp)
+    case 0: words_from<N, 0, kHalves>(w, bytes, o); break;
+    case 1: words_from<N, 1, kHalves>(w, bytes, o); break;
+    case 2: words_from<N, 2, kHalves>(w, bytes, o); break;
+    default: words_from<N, 3, kHalves>(w, bytes, o); break;
+  }
+}
+
+// What memory holds of eight elements from p, of which n exist (1 to 8; none: zeros): the 16-byte
+// vectors from p on, or, unless kVec, those that the elements lie in, from p's own on.
+template <typename T, bool kVec>
+struct Raw {
+  static constexpr int kVecs = static_cast<int>(sizeof(T) / 2) + (kVec ? 0 : 1);
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        v[i] = n > 0 ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      const uint4* q = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+      const int last = n <= 0 ? 0 : static_cast<int>(at & 15u) + n * static_cast<int>(sizeof(T));
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) v[i] = 16 * i < last ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  // the elements in place, zeros from element n on
+  __device__ __forceinline__ void get(const T* p, int n, Words<T>& u) const {
+    constexpr int kOut = static_cast<int>(sizeof(T) / 2);
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) u[i] = v[i];
+    } else {
+      uint32_t w[4 * kVecs], o[4 * kOut];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        w[4 * i] = v[i].x;
+        w[4 * i + 1] = v[i].y;
+        w[4 * i + 2] = v[i].z;
+        w[4 * i + 3] = v[i].w;
+      }
+      shift_words<4 * kOut, sizeof(T) == 2>(w, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u), o);
+#pragma unroll
+      for (int i = 0; i < kOut; ++i)
+        u[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+    if (!kVec && n < 8) {
+      T* e = reinterpret_cast<T*>(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= n) e[i] = T(0.f);
+    }
+  }
+};
 
 // v, or FP16's largest value of its sign where it is finite and past it (NaN stays).
 __device__ __forceinline__ float within_half(float v) {
@@ -69,7 +131,7 @@ __device__ __forceinline__ void values_of(const uint2& q, uint32_t scale, Words<
 }
 
 template <typename T>
-__device__ __forceinline__ void store_group(T* p, int64_t n, bool vec, const Words<T>& u) {
+__device__ __forceinline__ void store_group(T* p, int n, bool vec, const Words<T>& u) {
   if (vec && n >= 8) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
@@ -85,12 +147,12 @@ __device__ __forceinline__ void store_group(T* p, int64_t n, bool vec, const Wor
 // Group c of a packed row, from its values; the four lanes of a block call it together, `here`
 // where the group is within the row's groups.
 template <typename T>
-__device__ __forceinline__ void pack_group(const Act8Args& a, unsigned char* row, uint32_t c, bool here,
+__device__ __forceinline__ void pack_group(const Act8Args& a, unsigned char* row, int c, bool here,
                                            const Words<T>& u) {
   const uint32_t amax = act8_max_block(act8_max8<T>(u));
   const uint32_t s = act8_scale_byte(amax);
   if (!here) return;
-  const uint32_t first_scale = static_cast<uint32_t>(act8_scale_offset(a.H));
+  const int first_scale = static_cast<int>(act8_scale_offset(a.H));
   if (8 * c < first_scale) {
     uint2 q;
     if constexpr (sizeof(T) == 2) {
@@ -103,116 +165,152 @@ __device__ __forceinline__ void pack_group(const Act8Args& a, unsigned char* row
     }
     *reinterpret_cast<uint2*>(row + 8 * c) = q;
   }
-  if ((c & 3) == 0) {
-    unsigned char* p = row + first_scale + (c >> 2);
-    *p = static_cast<unsigned char>(s);
-    if (c + 4 == a.groups)  // the row's last block: the padding behind it
-      for (++p; reinterpret_cast<uintptr_t>(p) & 15u; ++p) *p = 0;
-  }
+  if ((c & 3) == 0)
+    row[first_scale + (c >> 2)] = static_cast<unsigned char>(s);
+  else if (c + 4 > static_cast<int>(a.groups))  // the other lanes of the row's last block: the padding behind it
+    act8_pad_scales(row + first_scale, static_cast<int>(a.groups >> 2), (c & 3) - 1);
 }
 
-// ---- wide rows: a warp takes kAct8Unroll * 32 groups of one row -------------------------------
+// ---- wide rows: a warp takes kAct8Unroll tiles of 32 groups, rows after one another -----------
 //
-// kVec: rows start and end at 16-byte vectors.  Else a warp's 256 elements of each turn pass through
-// shared memory, so that each access of memory takes 32 neighbouring elements (a place of padding
-// in eight: lane l's eight elements from 9 l on, in as many banks as there are lanes).
+// kVec: rows start at 16-byte vectors.  Else memory is read as load_group does, and written in whole
+// vectors too: a lane's vector of memory holds the last elements of the lane before and its own
+// first ones; what is left at the ends of rows and of the warp's tiles goes element by element.
 template <typename T, bool kVec, bool kPack>
-__global__ void __launch_bounds__(kAct8Threads) act8_wide_kernel(const Act8Args a) {
-  __shared__ T turn[kVec ? 1 : kAct8Threads / 32][kVec ? 1 : 288];
+__global__ void __launch_bounds__(kAct8Threads, std::is_same_v<T, __nv_bfloat16> && kVec ? 6 : 4) act8_wide_kernel(const Act8Args a) {
+  constexpr int kVecs = static_cast<int>(sizeof(T) / 2);
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAct8Threads / 32) + warp;
-  if (row >= a.R) return;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kAct8Threads / 32) + warp) * kAct8Unroll;
+  const int64_t row0 = (t0 >> 32) == 0 ? static_cast<uint32_t>(t0) / a.tiles : t0 / a.tiles;
+  if (row0 >= a.R) return;
+  const int c_end = static_cast<int>(a.tiles) * 32 + static_cast<int>(lane);  // behind a row
+  const int c0 = static_cast<int>(t0 - row0 * a.tiles) * 32 + static_cast<int>(lane);
   const int64_t bytes = act8_row_size(a.H);
-  T* wide = static_cast<T*>(const_cast<void*>(kPack ? a.in : a.out)) + row * a.s_row;
-  unsigned char* packed =
-      static_cast<unsigned char*>(const_cast<void*>(kPack ? a.out : a.in)) + row * bytes;
-  const uint32_t first_scale = static_cast<uint32_t>(act8_scale_offset(a.H));
-  for (uint32_t c0 = blockIdx.y * (32 * kAct8Unroll); c0 < a.groups;
-       c0 += gridDim.y * (32 * kAct8Unroll)) {
-    Words<T> u[kAct8Unroll];
-    uint2 q[kAct8Unroll];
-    uint32_t s[kAct8Unroll];
+  const int first_scale = static_cast<int>(act8_scale_offset(a.H));
+  unsigned char* const packed0 =
+      static_cast<unsigned char*>(const_cast<void*>(kPack ? a.out : a.in)) + row0 * bytes;
+  T* const wide0 = static_cast<T*>(const_cast<void*>(kPack ? a.in : a.out)) + row0 * a.s_row;
+  const int rows = static_cast<int>(min(a.R - row0, static_cast<int64_t>(kAct8Unroll)));
+  Raw<T, kVec> raw[kAct8Unroll];
+  uint2 q[kAct8Unroll];
+  uint32_t s[kAct8Unroll];
+  {
+    const T* wide = wide0;
+    const unsigned char* packed = packed0;
+    int c = c0, row = 0;
 #pragma unroll
     for (int i = 0; i < kAct8Unroll; ++i) {  // every load in flight before the first is used
-      const uint32_t c = c0 + i * 32 + lane;
-      const int64_t n = a.H - 8 * static_cast<int64_t>(c);
+      const int n = row < rows ? group_size(a, c) : 0;
       if constexpr (kPack) {
-#pragma unroll
-        for (uint4& w : u[i]) w = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (kVec) {
-          if (n > 0) load_group(wide + 8 * static_cast<int64_t>(c), n, true, u[i]);
-        } else {
-          const int64_t at = 8 * static_cast<int64_t>(c0 + i * 32);
-          T* own = reinterpret_cast<T*>(u[i]);  // for now, elements at + 32 k + lane
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (at + 32 * k + lane < a.H) own[k] = wide[at + 32 * k + lane];
-        }
+        raw[i].load(wide + 8 * static_cast<int64_t>(c), n);
       } else if (n > 0) {
         q[i] = *reinterpret_cast<const uint2*>(packed + 8 * static_cast<int64_t>(c));
         s[i] = packed[first_scale + (c >> 2)];
       }
+      c += 32;
+      if (c == c_end) {
+        c = static_cast<int>(lane);
+        ++row;
+        wide += a.s_row;
+        packed += bytes;
+      }
     }
+  }
+  T* wide = wide0;
+  unsigned char* packed = packed0;
+  int c = c0, row = 0;
+  uint32_t before[4];  // lane 31's last vector of the tile before
 #pragma unroll
-    for (int i = 0; i < kAct8Unroll; ++i) {
-      const uint32_t c = c0 + i * 32 + lane;
-      const int64_t n = a.H - 8 * static_cast<int64_t>(c);
-      T* own = reinterpret_cast<T*>(u[i]);
-      const int64_t at = 8 * static_cast<int64_t>(c0 + i * 32);
-      if constexpr (kPack) {
-        if constexpr (!kVec) {
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) turn[warp][32 * k + lane + (32 * k + lane) / 8] = own[k];
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) own[k] = turn[warp][9 * lane + k];
-        }
-        pack_group<T>(a, packed, c, c < a.groups, u[i]);
+  for (int i = 0; i < kAct8Unroll; ++i) {
+    if (row == rows) return;
+    const int n = group_size(a, c);
+    T* p = wide + 8 * static_cast<int64_t>(c);
+    Words<T> u;
+    if constexpr (kPack) {
+      raw[i].get(p, n, u);
+      pack_group<T>(a, packed, c, c < static_cast<int>(a.groups), u);
+    } else {
+      if (n > 0) values_of<T>(q[i], s[i], u);
+      if constexpr (kVec) {
+        if (n > 0) store_group(p, n, true, u);
       } else {
-        if (n > 0) values_of<T>(q[i], s[i], u[i]);
-        if constexpr (kVec) {
-          if (n > 0) store_group(wide + 8 * static_cast<int64_t>(c), n, true, u[i]);
+        // the lane before's last vector, then own ones; from them the vectors of memory that own
+        // elements begin in: their elements are `shift` places before own ones
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+        const int shift = static_cast<int>(off / sizeof(T));
+        uint32_t w[4 * kVecs + 4], o[4 * kVecs];
+#pragma unroll
+        for (int k = 0; k < 4 * kVecs; ++k) w[4 + k] = u4_get(u[k >> 2], k & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t v = __shfl_sync(0xffffffffu, w[4 * kVecs + k], (lane + 31) & 31);
+          w[k] = lane == 0 && i > 0 ? before[k] : v;
+          before[k] = v;
+        }
+        if (off != 0) {
+          shift_words<4 * kVecs, sizeof(T) == 2>(w, 16u - off, o);
         } else {
-          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) turn[warp][9 * lane + k] = own[k];
-          __syncwarp();
+          for (int k = 0; k < 4 * kVecs; ++k) o[k] = w[4 + k];
+        }
+        constexpr int kIn = static_cast<int>(16 / sizeof(T));  // elements of a vector
+        // of the eight elements from p - shift on, [lo, hi) are this warp's and the row's
+        const int lo = lane == 0 && (i == 0 || c == 0) ? shift : 0;
+        const int hi = min(n + shift, 8);
+        const T* e = reinterpret_cast<const T*>(o);
+        T* d = p - shift;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (at + 32 * k + lane < a.H)
-              wide[at + 32 * k + lane] = turn[warp][32 * k + lane + (32 * k + lane) / 8];
+        for (int k = 0; k < kVecs; ++k) {
+          if (lo <= k * kIn && (k + 1) * kIn <= hi) {
+            reinterpret_cast<uint4*>(d)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else if (hi > k * kIn) {
+#pragma unroll
+            for (int x = k * kIn; x < (k + 1) * kIn; ++x)
+              if (lo <= x && x < hi) d[x] = e[x];
+          }
+        }
+        // what the next tile's first lane would write, were it the same row's and this warp's
+        if (lane == 31 && (i == kAct8Unroll - 1 || c + 32 == c_end)) {
+          const T* own = reinterpret_cast<const T*>(u);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (x >= 8 - shift && x < n) p[x] = own[x];
         }
       }
+    }
+    c += 32;
+    if (c == c_end) {
+      c = static_cast<int>(lane);
+      ++row;
+      wide += a.s_row;
+      packed += bytes;
     }
   }
 }
 
 // ---- narrow rows: the groups of all rows side by side -----------------------------------------
 
-template <typename T, bool kPack>
+template <typename T, bool kVec, bool kPack>
 __global__ void __launch_bounds__(kAct8Threads) act8_flat_kernel(const Act8Args a) {
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const uint32_t first = blockIdx.x * (kAct8Threads * kAct8Unroll) + threadIdx.x;
   const int64_t bytes = act8_row_size(a.H);
   const uint32_t first_scale = static_cast<uint32_t>(act8_scale_offset(a.H));
-  Words<T> u[kAct8Unroll];
+  Raw<T, kVec> raw[kAct8Unroll];
   uint2 q[kAct8Unroll];
-  uint32_t s[kAct8Unroll], row[kAct8Unroll], c[kAct8Unroll];
+  uint32_t s[kAct8Unroll], row[kAct8Unroll];
+  int c[kAct8Unroll];
 #pragma unroll
   for (int i = 0; i < kAct8Unroll; ++i) {
     const uint32_t at = first + i * kAct8Threads;
     row[i] = __umulhi(at, a.mul) >> a.shift;
-    c[i] = at - row[i] * a.groups;
-    const int64_t n = at < a.total ? a.H - 8 * static_cast<int64_t>(c[i]) : 0;
+    c[i] = static_cast<int>(at - row[i] * a.groups);
+    const int n = at < a.total ? group_size(a, c[i]) : 0;
     if constexpr (kPack) {
-#pragma unroll
-      for (uint4& w : u[i]) w = make_uint4(0u, 0u, 0u, 0u);
-      if (n > 0)
-        load_group(static_cast<const T*>(a.in) + row[i] * a.s_row + 8 * c[i], n, a.vec != 0, u[i]);
+      raw[i].load(static_cast<const T*>(a.in) + row[i] * a.s_row + 8 * c[i], n);
     } else if (n > 0) {
       const unsigned char* p = static_cast<const unsigned char*>(a.in) + row[i] * bytes;
       q[i] = *reinterpret_cast<const uint2*>(p + 8 * c[i]);
@@ -222,43 +320,44 @@ __global__ void __launch_bounds__(kAct8Threads) act8_flat_kernel(const Act8Args 
 #pragma unroll
   for (int i = 0; i < kAct8Unroll; ++i) {
     const bool here = first + i * kAct8Threads < a.total;
-    const int64_t n = here ? a.H - 8 * static_cast<int64_t>(c[i]) : 0;
+    const int n = here ? group_size(a, c[i]) : 0;
+    Words<T> u;
     if constexpr (kPack) {
-      pack_group<T>(a, static_cast<unsigned char*>(a.out) + row[i] * bytes, c[i], here, u[i]);
+      raw[i].get(static_cast<const T*>(a.in) + row[i] * a.s_row + 8 * c[i], n, u);
+      pack_group<T>(a, static_cast<unsigned char*>(a.out) + row[i] * bytes, c[i], here, u);
     } else if (n > 0) {
-      values_of<T>(q[i], s[i], u[i]);
-      store_group(static_cast<T*>(a.out) + row[i] * a.s_row + 8 * c[i], n, a.vec != 0, u[i]);
+      values_of<T>(q[i], s[i], u);
+      store_group(static_cast<T*>(a.out) + row[i] * a.s_row + 8 * c[i], n, kVec, u);
     }
   }
 }
 
 template <typename T, bool kPack>
-const void* wide_fn(bool vec) {
-  return vec ? reinterpret_cast<const void*>(&act8_wide_kernel<T, true, kPack>)
-             : reinterpret_cast<const void*>(&act8_wide_kernel<T, false, kPack>);
+const void* pick_of(bool flat, bool vec) {
+  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+  if (flat)
+    return vec ? fn(&act8_flat_kernel<T, true, kPack>) : fn(&act8_flat_kernel<T, false, kPack>);
+  return vec ? fn(&act8_wide_kernel<T, true, kPack>) : fn(&act8_wide_kernel<T, false, kPack>);
 }
 
 template <bool kPack>
 const void* pick(int dtype, bool flat, bool vec) {
-  if (flat)
-    return dtype == ACT8_BF16   ? reinterpret_cast<const void*>(&act8_flat_kernel<__nv_bfloat16, kPack>)
-           : dtype == ACT8_FP32 ? reinterpret_cast<const void*>(&act8_flat_kernel<float, kPack>)
-                                : reinterpret_cast<const void*>(&act8_flat_kernel<__half, kPack>);
-  return dtype == ACT8_BF16   ? wide_fn<__nv_bfloat16, kPack>(vec)
-         : dtype == ACT8_FP32 ? wide_fn<float, kPack>(vec)
-                              : wide_fn<__half, kPack>(vec);
+  return dtype == ACT8_BF16   ? pick_of<__nv_bfloat16, kPack>(flat, vec)
+         : dtype == ACT8_FP32 ? pick_of<float, kPack>(flat, vec)
+                              : pick_of<__half, kPack>(flat, vec);
 }
 
-// Rows of at least this many groups are taken warp by warp: a warp's 128 are then three quarters
-// there, and a row's place costs it no division.
-constexpr uint32_t kAct8WideGroups = 96;
+// Rows of at least this many groups are taken in tiles of 32, three quarters of which are then there;
+// tiles are the same row's for a whole warp.
+constexpr uint32_t kAct8WideGroups = 24;
+constexpr int64_t kAct8MaxH = int64_t{1} << 30;
 constexpr int64_t kAct8MaxBytes = int64_t{1} << 42;  // of a packed tensor
 
 int act8_run(const void* wide, int dtype, const void* packed, int64_t R, int64_t H, int64_t s_row,
              bool pack, void* stream) {
   if (dtype != ACT8_BF16 && dtype != ACT8_FP32 && dtype != ACT8_FP16) return RMSN_ERR_INVALID_ARG;
   if (R < 0 || H < 1 || s_row < 0) return RMSN_ERR_INVALID_ARG;
-  if (H > INT32_MAX || R > kAct8MaxBytes / act8_row_size(H)) return RMSN_ERR_UNSUPPORTED;
+  if (H > kAct8MaxH || R > kAct8MaxBytes / act8_row_size(H)) return RMSN_ERR_UNSUPPORTED;
   if (R > 0 && (!wide || !packed)) return RMSN_ERR_INVALID_ARG;
   const uintptr_t elem = dtype == ACT8_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(wide) % elem || (reinterpret_cast<uintptr_t>(packed) & 15u))
@@ -273,16 +372,15 @@ int act8_run(const void* wide, int dtype, const void* packed, int64_t R, int64_t
   a.H = H;
   a.s_row = R > 1 ? s_row : H;
   a.groups = static_cast<uint32_t>((H + kAct8Block - 1) / kAct8Block * 4);
-  a.vec = reinterpret_cast<uintptr_t>(wide) % 16 == 0 && a.s_row * elem % 16 == 0;
+  a.vec = reinterpret_cast<uintptr_t>(wide) % 16 == 0 && a.s_row * elem % 16 == 0 && H % 8 == 0;
   const bool flat = a.groups < kAct8WideGroups;
   const void* fn = pack ? pick<true>(dtype, flat, a.vec) : pick<false>(dtype, flat, a.vec);
   const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
   void* args[] = {&a};
   if (!flat) {
-    constexpr int64_t warps = kAct8Threads / 32;
-    const int64_t chunks = (a.groups + 32 * kAct8Unroll - 1) / (32 * kAct8Unroll);
-    const dim3 grid(static_cast<unsigned>((R + warps - 1) / warps),  // below 2^42 / 776 / 8
-                    static_cast<unsigned>(chunks < 65535 ? chunks : 65535));
+    a.tiles = (a.groups + 31) / 32;
+    constexpr int64_t per = kAct8Threads / 32 * kAct8Unroll;  // tiles a CTA
+    const dim3 grid(static_cast<unsigned>((R * a.tiles + per - 1) / per));  // below 2^42 / 192 / 32
     return launch_pdl(fn, grid, dim3(kAct8Threads), 0, stream_, args) == cudaSuccess
                ? RMSN_OK
                : RMSN_ERR_CUDA;
@@ -318,7 +416,7 @@ using namespace rmsn;
 
 extern "C" {
 
-int64_t act8_train_row_bytes(int64_t H) { return H < 1 || H > INT32_MAX ? 0 : act8_row_size(H); }
+int64_t act8_train_row_bytes(int64_t H) { return H < 1 || H > kAct8MaxH ? 0 : act8_row_size(H); }
 
 int act8_train_pack(const void* x, int dtype, void* packed, int64_t R, int64_t H, int64_t s_row,
                     void* stream) {

@@ -121,6 +121,14 @@ __device__ __forceinline__ uint2 act8_pack8(const uint4& u, uint32_t amax, uint3
   return act8_pack8(v, amax, scale);
 }
 
+// The zeros behind a row's `blocks` scale bytes at p (16-byte aligned) up to a multiple of 16, by three
+// threads (k = 0 to 2): up to a multiple of four a byte each, then a word each.
+__device__ __forceinline__ void act8_pad_scales(unsigned char* p, int blocks, int k) {
+  if (blocks + k < ((blocks + 3) & ~3)) p[blocks + k] = 0;
+  const int word = ((blocks + 3) & ~3) + 4 * k;
+  if (word < ((blocks + 15) & ~15)) *reinterpret_cast<uint32_t*>(p + word) = 0u;
+}
+
 // The factor of a scale byte's numbers, 2^(e-6); NaN for a block that held one or an infinity.
 __device__ __forceinline__ float act8_unit(uint32_t scale) {
   return __uint_as_float(scale == 255u ? 0x7fc00000u : (max(scale, 6u) - 6u) << 23);

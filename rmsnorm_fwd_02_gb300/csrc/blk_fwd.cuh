@@ -23,12 +23,11 @@ __device__ __forceinline__ void keep8(unsigned char* packed_row, int first_scale
   *reinterpret_cast<uint2*>(packed_row + 8 * c) = act8_pack8<T>(u, amax, s);
   if ((c & 3) == 0) packed_row[first_scale + (c >> 2)] = static_cast<unsigned char>(s);
 }
-// A packed row's padding, by the row's threads.
+// A packed row's padding, by the first threads of its row (at least four).
 __device__ __forceinline__ void keep8_padding(const Args& a, int lt, unsigned char* p) {
   const int first = static_cast<int>(act8_scale_offset(a.H));
-  if (lt == 0 && a.H < first) *reinterpret_cast<uint2*>(p + a.H) = make_uint2(0u, 0u);
-  const int end = static_cast<int>(act8_row_size(a.H));
-  for (int i = first + (a.H + kAct8Block - 1) / kAct8Block + lt; i < end; i += a.ntg) p[i] = 0;
+  if (lt == 3 && a.H < first) *reinterpret_cast<uint2*>(p + a.H) = make_uint2(0u, 0u);
+  if (lt < 3) act8_pad_scales(p + first, (a.H + kAct8Block - 1) / kAct8Block, lt);
 }
 
 template <typename T, int VPT, int kForm, bool kPack, bool kEven>

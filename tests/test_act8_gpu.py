@@ -70,6 +70,35 @@ def test_strides_and_addresses(dtype):
     assert at.data_ptr() % 16 and torch.equal(R.act8_unpack(at, 100, dtype), R.act8_unpack(p, 100, dtype))
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("h", [769, 772, 1024, 1027, 1032, 2055, 5001])
+def test_wide_rows_at_every_alignment(dtype, h):
+    # rows that start anywhere between two 16-byte vectors; rows, chunks and blocks end anywhere
+    flat = normal(h, 9 * h + 8, dtype=dtype)
+    for off in range(8):
+        x = flat[off:off + 9 * h].view(9, h)
+        p = R.act8_pack(x)
+        want = OA.pack(f64(x))
+        assert np.array_equal(p.cpu().numpy(), want)
+        got = R.act8_unpack(p, h, dtype)
+        check(got, OA.unpack(want, h), np.zeros((9, h)))
+    # a narrower part of each row: what lies beside it is neither read into it nor written
+    x = flat[:9 * h].view(9, h)[:, 3:h - 2]
+    assert np.array_equal(R.act8_pack(x).cpu().numpy(), OA.pack(f64(x)))
+
+
+def test_unpacked_rows_end_where_they_end():
+    # through the C ABI into a guarded buffer: nothing before, behind or between is written
+    for rows, h in ((3, 7), (5, 770), (4, 1031), (1, 4099)):
+        p = R.act8_pack(normal(h, rows, h))
+        for off in (0, 1, 5):
+            buf = torch.full((rows * h + 24,), 7.0, dtype=torch.bfloat16, device=DEV)
+            out = buf[8 + off:8 + off + rows * h]
+            N.act8_train_unpack(p, out, N.ACT8_BF16, rows, h)
+            assert torch.equal(out.view(rows, h), R.act8_unpack(p, h))
+            assert (buf[:8 + off] == 7).all() and (buf[8 + off + rows * h:] == 7).all()
+
+
 def test_empty_and_refusals():
     x = torch.empty(0, 40, device=DEV)
     p = R.act8_pack(x)
