@@ -132,9 +132,9 @@ void ring(Shape& s, int H, size_t row, size_t least, int sums) {
 }
 
 Shape plan(int64_t R, int H, int threads_cta, int form, size_t row, size_t least, int sums,
-           bool factor = false) {
+           bool bwd, bool packed) {
   Shape s = team_shape(R, H, threads_cta, form);
-  s.factor = factor;
+  s.factor = bwd && factor_in_smem(form, packed, even_rows(H, s.vpt, s.ntg));
   ring(s, H, row, least, sums);
   return s;
 }
@@ -200,7 +200,8 @@ int run_fwd(const Fwd& f, void* stream) {
   if (st != RMSN_OK) return st;
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
-  const Shape s = plan(f.R, f.H, fwd_threads(f.form), f.form, f.residual != nullptr ? 2 * row : row, row, 0);
+  const Shape s = plan(f.R, f.H, fwd_threads(f.form), f.form, f.residual != nullptr ? 2 * row : row,
+                       row, 0, false, false);
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -282,7 +283,7 @@ int run_bwd(const Bwd& b, void* stream) {
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
   const Shape s = plan(b.R, b.H, bwd_threads(b.form), b.form, row, least,
-                       (pre ? 1 : 0) + (s_sums ? 1 : 0), factor_in_smem(b.form, b.packed));
+                       (pre ? 1 : 0) + (s_sums ? 1 : 0), true, b.packed);
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
   const size_t need = sizeof(float) * ((pre ? pre_floats(s, b.H) : 0) +
@@ -533,8 +534,8 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
   const Shape s = backward ? plan(R, H, bwd_threads(kBoth), kBoth, 2 * wide + 2 * saved,
-                                  wide < saved ? wide : saved, 2, factor_in_smem(kBoth, packed != 0))
-                           : plan(R, H, fwd_threads(kBoth), kBoth, 2 * wide, wide, 0);
+                                  wide < saved ? wide : saved, 2, true, packed != 0)
+                           : plan(R, H, fwd_threads(kBoth), kBoth, 2 * wide, wide, 0, false, false);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
   const int NV = a.H >> 3;
   // From 8 bits with both norms the factor of the branch lives in shared memory, each thread's part
   // for itself alone (the rows of a warp share theirs): the sums, w, the kept vectors and m fill the registers.
-  constexpr bool kFactorMem = factor_in_smem(kForm, kPacked);
+  constexpr bool kFactorMem = factor_in_smem(kForm, kPacked, kEven);
   f2 w[VPT][4], k1[kFactorMem ? 1 : VPT][4], sum_pre[VPT][4], sum_s[VPT][4];
   float4* const k1_mem =
       reinterpret_cast<float4*>(smem + a.factor_at) + t.team * (2 * VPT * a.ntg) + t.lt;

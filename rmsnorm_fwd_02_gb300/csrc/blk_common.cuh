@@ -84,12 +84,6 @@ __device__ __forceinline__ f2 square_onto(uint32_t a, f2 acc) {
   }
 }
 
-// Whether every thread of a row has all its vectors, and every row of a warp is there: kernels are
-// built for that case apart, without a predicate on any vector.
-__host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
-  return ntg >= 32 && H == 8 * vpt * ntg;
-}
-
 // scale * gate * w_post of a thread's columns (each factor where it is there), sample n's gate.
 template <int VPT, bool kPostW>
 __device__ __forceinline__ void load_factor(const Args& a, int32_t n, int lt, f2 (&k1)[VPT][4]) {

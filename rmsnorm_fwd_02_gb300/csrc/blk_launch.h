@@ -95,9 +95,19 @@ struct BwdArgs : Args {
                       // [P * teams + N - 1][H], a row a team and sample
 };
 
+// Whether every thread of a row has all its vectors, and every row of a warp is there: kernels are
+// built for that case apart, without a predicate on any vector.
+__host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
+  return ntg >= 32 && H == 8 * vpt * ntg;
+}
+
 // Backward builds whose branch's factor (scale * gate * w_post of a thread's columns) is in shared
-// memory: 4 bytes an element that a team's threads own, after everything else.
-__host__ __device__ constexpr bool factor_in_smem(int form, bool packed) { return form == kBoth && packed; }
+// memory: 4 bytes an element that a team's threads own, after everything else.  With both norms:
+// from 8 bits, whose kept vectors need the registers (65536 x 4096: 481 us against 525), and where
+// rows are even (65536 x 1536: 202 us against 213; uneven rows 82 against 78 at 30000 x 1000).
+__host__ __device__ constexpr bool factor_in_smem(int form, bool packed, bool even) {
+  return form == kBoth && (packed || even);
+}
 
 // First row of team k of n.
 __host__ __device__ inline int32_t team_row(int64_t k, int64_t R, int64_t n) {
