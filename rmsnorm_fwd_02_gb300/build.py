@@ -60,7 +60,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
-                     "-I", os.path.join(ROOT, "include"), "-Xptxas", "-v"] + os.environ.get("XDEF","").split()
+                     "-I", os.path.join(ROOT, "include"), "-Xptxas", "-v"]
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
