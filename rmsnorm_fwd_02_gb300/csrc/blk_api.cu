@@ -65,9 +65,11 @@ int device_setup(unsigned** err) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads a row, vectors a thread, teams a CTA and CTAs: functions of R, H and the kernel's threads
-// and form.
-Shape team_shape(int64_t R, int H, int threads_cta, int form) {
+// Threads a row, vectors a thread, teams a CTA and CTAs: functions of R, H and the kernel's form (the
+// forward's also give the same results whether it packs or not).
+Shape team_shape(int64_t R, int H, int form, bool bwd, bool packed) {
+  const int threads_cta =
+      bwd ? bwd_threads(form, packed, wide_rows(form, packed, H)) : fwd_threads(form);
   Shape s{};
   const int nv = H / 8;
   auto threads = [&](int vpt) {
@@ -80,9 +82,10 @@ Shape team_shape(int64_t R, int H, int threads_cta, int form) {
     return ntg > threads_cta ? 0 : teams(ntg) * rows * ((nv + vpt - 1) / vpt);
   };
   // Four vectors a thread, fewer in narrow rows, three where that keeps more threads busy (30720 x
-  // 6144 backward, 256 threads against 192: 385 us against 423) -- but not in the 8-bit norm where
-  // its threads are then uneven (32768 x 8192 backward: 334 us against 296).
-  const bool three = busy(3) > busy(4) && (form != kKeep || nv == 3 * threads(3));
+  // 6144 backward, 256 threads against 192: 385 us against 423) -- but not where its threads are then
+  // uneven and the numbers of 8 bits add to their work (32768 x 8192 backward with both norms 555
+  // us against 476).
+  const bool three = busy(3) > busy(4) && (nv == 3 * threads(3) || (form != kKeep && !packed));
   s.vpt = nv <= 4 ? 1 : nv <= 8 ? 2 : three ? 3 : 4;
   // one where the rows are so few that each then has a team at once: the shortest way through a row
   // (64 x 256 forward: 3.1 us against 5.6)
@@ -131,9 +134,8 @@ void ring(Shape& s, int H, size_t row, size_t least, int sums) {
   if (s.smem < join) s.smem = join;
 }
 
-Shape plan(int64_t R, int H, int threads_cta, int form, size_t row, size_t least, int sums,
-           bool bwd, bool packed) {
-  Shape s = team_shape(R, H, threads_cta, form);
+Shape plan(int64_t R, int H, int form, bool bwd, bool packed, size_t row, size_t least, int sums) {
+  Shape s = team_shape(R, H, form, bwd, packed);
   s.factor = bwd && factor_in_smem(form, packed, even_rows(H, s.vpt, s.ntg));
   ring(s, H, row, least, sums);
   return s;
@@ -200,8 +202,8 @@ int run_fwd(const Fwd& f, void* stream) {
   if (st != RMSN_OK) return st;
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
-  const Shape s = plan(f.R, f.H, fwd_threads(f.form), f.form, f.residual != nullptr ? 2 * row : row,
-                       row, 0, false, false);
+  const bool pack = f.x8 != nullptr || f.h8 != nullptr;
+  const Shape s = plan(f.R, f.H, f.form, false, false, f.residual != nullptr ? 2 * row : row, row, 0);
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -220,8 +222,7 @@ int run_fwd(const Fwd& f, void* stream) {
   a.rstd_post = f.rstd_post;
   a.x8 = static_cast<unsigned char*>(f.x8);
   a.h8 = static_cast<unsigned char*>(f.h8);
-  return launch_fwd(a, s, f.dtype, f.form, f.x8 != nullptr || f.h8 != nullptr,
-                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_fwd(a, s, f.dtype, f.form, pack, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RMSN_OK
              : RMSN_ERR_CUDA;
 }
@@ -250,9 +251,15 @@ size_t s_floats(const Shape& s, int32_t H, int64_t N) {
   return static_cast<size_t>(rows) * H;
 }
 size_t workspace_bytes(int64_t R, int32_t H, int64_t N) {
-  const Shape s = team_shape(R, H, bwd_threads(kBoth), kBoth), keep = team_shape(R, H, bwd_threads(kKeep), kKeep);
-  const size_t both = pre_floats(s, H) + s_floats(s, H, N), one = pre_floats(keep, H);
-  return sizeof(float) * (both > one ? both : one);
+  size_t most = 0;
+  for (int form : {kKeep, kPre, kBoth, kPost})
+    for (bool packed : {false, true}) {
+      if (form == kKeep && N > 1) continue;
+      const Shape s = team_shape(R, H, form, true, packed);
+      const size_t n = (form != kPost ? pre_floats(s, H) : 0) + (form != kKeep ? s_floats(s, H, N) : 0);
+      if (n > most) most = n;
+    }
+  return sizeof(float) * most;
 }
 
 int run_bwd(const Bwd& b, void* stream) {
@@ -282,8 +289,7 @@ int run_bwd(const Bwd& b, void* stream) {
   size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
-  const Shape s = plan(b.R, b.H, bwd_threads(b.form), b.form, row, least,
-                       (pre ? 1 : 0) + (s_sums ? 1 : 0), true, b.packed);
+  const Shape s = plan(b.R, b.H, b.form, true, b.packed, row, least, (pre ? 1 : 0) + (s_sums ? 1 : 0));
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
   const size_t need = sizeof(float) * ((pre ? pre_floats(s, b.H) : 0) +
@@ -371,7 +377,7 @@ int rmsnorm_act8_train_fwd(const void* x, const void* residual, int dtype, const
 
 size_t rmsnorm_act8_train_bwd_workspace_bytes(int64_t R, int32_t H) {
   if (check_sizes(R, H, 1) != RMSN_OK || R == 0) return 0;
-  return sizeof(float) * pre_floats(team_shape(R, H, bwd_threads(kKeep), kKeep), H);
+  return sizeof(float) * pre_floats(team_shape(R, H, kKeep, true, true), H);
 }
 
 int rmsnorm_act8_train_bwd(const void* packed, const void* dy, const void* dh, int dtype,
@@ -533,9 +539,9 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   if (R == 0) return RMSN_ERR_INVALID_ARG;
   const size_t wide = 2 * static_cast<size_t>(H);
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
-  const Shape s = backward ? plan(R, H, bwd_threads(kBoth), kBoth, 2 * wide + 2 * saved,
-                                  wide < saved ? wide : saved, 2, true, packed != 0)
-                           : plan(R, H, fwd_threads(kBoth), kBoth, 2 * wide, wide, 0, false, false);
+  const Shape s = backward ? plan(R, H, kBoth, true, packed != 0, 2 * wide + 2 * saved,
+                                  wide < saved ? wide : saved, 2)
+                           : plan(R, H, kBoth, false, false, 2 * wide, wide, 0);
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

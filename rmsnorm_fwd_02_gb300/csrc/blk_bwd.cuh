@@ -72,18 +72,29 @@ __device__ __forceinline__ void join_teams(const Args& a, const float* rows, flo
   }
 }
 
-template <typename T, int VPT, int kForm, bool kPacked, bool kEven>
-__global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const BwdArgs a) {
+template <typename T, int VPT, int kForm, bool kPacked, bool kEven, bool kWide = false>
+__global__ void __launch_bounds__(bwd_threads(kForm, kPacked, kWide), 1) blk_bwd_kernel(const BwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   constexpr bool kX = kForm != kKeep;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint64_t pol = l2_evict_first_policy();
-  Team t = team_begin<4>(a, smem, pol, a.samples == 1);
+  // Sums in tensor memory: for each vector 8 columns of dw_pre's, then 8 of S; the warps that share a
+  // quarter of its lanes side by side.
+  constexpr bool kTm = sums_in_tmem(kForm, kPacked, VPT, kWide);
+  constexpr int kTmVec = kX ? 16 : 8, kTmWarp = kTmVec * VPT;
+  constexpr int kTmCols =
+      kTm ? static_cast<int>(tmem_alloc_cols((bwd_threads(kForm, kPacked, kWide) / 128) * kTmWarp)) : 0;
+  Team t = team_begin<4, kTmCols>(a, smem, pol, a.samples == 1);
+  uint32_t tm = 0;
+  if constexpr (kTm) {
+    const uint32_t warp = threadIdx.x >> 5;
+    tm = tmem_warp_addr(*t.tmem, warp, (warp >> 2) * kTmWarp);
+  }
   const int NV = a.H >> 3;
-  // From 8 bits with both norms the factor of the branch lives in shared memory, each thread's part
-  // for itself alone (the rows of a warp share theirs): the sums, w, the kept vectors and m fill the registers.
+  // (a factor in shared memory: each thread's part is its own, the rows of a warp share theirs)
   constexpr bool kFactorMem = factor_in_smem(kForm, kPacked, kEven);
-  f2 w[VPT][4], k1[kFactorMem ? 1 : VPT][4], sum_pre[VPT][4], sum_s[VPT][4];
+  f2 w[VPT][4], k1[kFactorMem ? 1 : VPT][4];
+  f2 sum_pre[VPT][4], sum_s[VPT][4];  // (kTm: filled from tensor memory where they are written)
   float4* const k1_mem =
       reinterpret_cast<float4*>(smem + a.factor_at) + t.team * (2 * VPT * a.ntg) + t.lt;
   auto set_factor = [&](int32_t n) {
@@ -130,6 +141,27 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
       if (kEven || c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
     }
   }
+  // sums of one kind (at `from` columns) to registers, and zeros in their place
+  auto take_sums = [&](int from, f2 (&sum)[VPT][4]) {
+    if constexpr (kTm) {
+      const f2 zero[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
+      __syncwarp();
+      tmem_wait_st();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) tmem_ld8(tm + kTmVec * v + from, sum[v]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) tmem_st8(tm + kTmVec * v + from, zero);
+    }
+  };
+  if constexpr (kTm) {
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      tmem_st8(tm + kTmVec * v, sum_pre[v]);
+      if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, sum_s[v]);
+    }
+  }
   const float inv_h = 1.f / static_cast<float>(a.H);
   const f2 rscale = f2_splat(a.residual_scale);
   const int side = a.ntg < 32 ? 32 / a.ntg : 1;  // rows side by side
@@ -163,6 +195,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
     for (int32_t i = 0; i < n;) {
       if constexpr (kX) {
         if (a.samples > 1 && ra + i >= next_sample) {
+          take_sums(8, sum_s);
           write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
           sample = (ra + i) / a.L;
           next_sample = (sample + 1) * a.L;
@@ -233,11 +266,19 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
       float dot = 0.f;
       f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
       const size_t out_row = static_cast<size_t>(row) * a.H;
+      if constexpr (kTm) {
+        __syncwarp();
+        tmem_wait_st();  // the row before's sums are stored before they are loaded
+      }
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = t.lt + v * a.ntg;
         const bool live = kEven || (valid && c < NV);
-        f2 g[4];
+        f2 g[4], tp[4], ts[4], ap[4], as[4];
+        if constexpr (kTm) {
+          tmem_ld8(tm + kTmVec * v, tp);
+          if constexpr (kX) tmem_ld8(tm + kTmVec * v + 8, ts);
+        }
         if constexpr (kPreN) {
           f2 h[4], dy[4];
           f2 nc = nc2, rh = r2v;
@@ -253,7 +294,10 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             g[q] = f2_mul(f2_fma(h[q], nc, f2_mul(dy[q], w[v][q])), r2v);
-            sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
+            if constexpr (kTm)
+              ap[q] = f2_mul(dy[q], f2_mul(h[q], rh));
+            else
+              sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
           }
         }
         if (!kPreN || has_dh) {
@@ -275,7 +319,10 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
-            sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
+            if constexpr (kTm)
+              as[q] = f2_mul(g[q], xh);
+            else
+              sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
             m[v][q] = f2_mul(g[q], f[q]);
           }
           if constexpr (kPostN && kPacked) {
@@ -301,6 +348,17 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
         }
         if (!kPostN && live && (kX || a.dx != nullptr))
           stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(m[v]));
+        if constexpr (kTm) {
+          __syncwarp();
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tp[q] = f2_add(tp[q], ap[q]);
+            if constexpr (kX) ts[q] = f2_add(ts[q], as[q]);
+          }
+          tmem_st8(tm + kTmVec * v, tp);
+          if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, ts);
+        }
       }
       if constexpr (kPostN) {
         if constexpr (!kPacked) {
@@ -340,6 +398,19 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
     }
   }
   drain(a, t);
+  if constexpr (kTm) {
+    take_sums(0, sum_pre);
+    if constexpr (kX) take_sums(8, sum_s);
+    __syncwarp();
+    tmem_wait_st();
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      __syncwarp();
+      tmem_fence_after_sync();
+      tmem_dealloc_warp(*t.tmem, kTmCols);
+    }
+  }
   if (kX && a.samples > 1) {
     // (a team without rows writes zeros: it lies among the teams of its first row's sample)
     write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
@@ -361,8 +432,13 @@ __global__ void __launch_bounds__(bwd_threads(kForm), 1) blk_bwd_kernel(const Bw
 }
 
 template <typename T, int VPT, bool kEven>
-const void* pick_bwd(int form, bool packed) {
+const void* pick_bwd(int form, bool packed, bool wide) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+  if constexpr (VPT == 4) {  // (what such rows have)
+    if (wide)
+      return form == kKeep ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, true>)
+                           : fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, true>);
+  }
 #define BLK_PICK(F)                                              \
   (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven>)          \
           : fn(&blk_bwd_kernel<T, VPT, F, false, kEven>))
@@ -377,13 +453,13 @@ const void* pick_bwd(int form, bool packed) {
 
 template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
-  const bool even = even_rows(a.H, s.vpt, s.ntg);
-  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed)
-                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed)
-                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed)
-                                        : pick_bwd<T, 3, false>(form, packed))
-                                : (even ? pick_bwd<T, 4, true>(form, packed)
-                                        : pick_bwd<T, 4, false>(form, packed));
+  const bool even = even_rows(a.H, s.vpt, s.ntg), wide = wide_rows(form, packed, a.H);
+  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, wide)
+                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, wide)
+                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, wide)
+                                        : pick_bwd<T, 3, false>(form, packed, wide))
+                                : (even ? pick_bwd<T, 4, true>(form, packed, wide)
+                                        : pick_bwd<T, 4, false>(form, packed, wide));
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   BwdArgs copy = a;

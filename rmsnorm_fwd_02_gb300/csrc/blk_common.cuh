@@ -10,6 +10,7 @@
 
 #include "act8.cuh"
 #include "blk_launch.h"
+#include "rmsn_tmem.cuh"
 #include "types.cuh"
 
 namespace blk {
@@ -120,6 +121,7 @@ struct Team {
   uint64_t* full;       // its barriers
   float* red;           // [2][16]: warp sums, taken in turns
   volatile int* abort_flag;
+  uint32_t* tmem;       // shared word: the tensor memory's address (kTmem)
   int32_t r0, r1;       // first row; end of the rows
   int32_t stride;       // rows between two of its slots' first
   int32_t nslots;
@@ -186,7 +188,8 @@ __device__ __forceinline__ void issue(const Args& a, Team& t, int32_t j, uint64_
 // turns: a CTA's teams take the slots of its rows in turns (neighbouring rows at one time are
 // fewer streams of memory: 65536 x 1536 forward 151 us against 157); else each has a run of its
 // own.
-template <int kTensors>
+// kTmem: columns of tensor memory that the CTA takes (0: none).
+template <int kTensors, int kTmem = 0>
 __device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, uint64_t pol,
                                            bool turns) {
   Team t;
@@ -213,9 +216,18 @@ __device__ __forceinline__ Team team_begin(const Args& a, unsigned char* smem, u
   if (tid == 0) *zero = make_uint4(0u, 0u, 0u, 0u);
   for (int i = tid; i < 2 * kMaxWarps * a.teams; i += static_cast<int>(blockDim.x)) red[i] = 0.f;
   for (int i = tid; i < a.teams * a.stages; i += static_cast<int>(blockDim.x)) mbar_init(&full[i], 1u);
+  t.tmem = reinterpret_cast<uint32_t*>(zero + 1) + 2;
   if (tid == 0) *t.abort_flag = 0;
   fence_barrier_init();
+  if constexpr (kTmem > 0) {
+    if (tid < 32) {
+      __syncwarp();
+      tmem_alloc_warp(t.tmem, kTmem);
+      tmem_fence_before_sync();
+    }
+  }
   __syncthreads();
+  if constexpr (kTmem > 0) tmem_fence_after_sync();
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   if (turns) {
@@ -243,6 +255,26 @@ __device__ __forceinline__ void wait_slot(const Args& a, const Team& t, int s, u
 // After a wait that gave up: no copy may still write this CTA's shared memory when it exits.
 __device__ __forceinline__ void drain(const Args& a, const Team& t) {
   if (*t.abort_flag && t.leader) mbar_drain(t.full, a.stages, t.issued);
+}
+
+// Eight consecutive columns of this thread's lane of tensor memory <-> four pairs.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, f2 (&r)[4]) {
+  float v[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = f2_make(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const f2 (&r)[4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "f"(f2_lo(r[0])), "f"(f2_hi(r[0])), "f"(f2_lo(r[1])), "f"(f2_hi(r[1])), "f"(f2_lo(r[2])),
+      "f"(f2_hi(r[2])), "f"(f2_lo(r[3])), "f"(f2_hi(r[3]))
+      : "memory");
 }
 
 // Sum over the threads of a row; every one of them gets the same bits.

@@ -13,12 +13,25 @@ constexpr int kMaxH = 8192;
 // the sums' reduction, rstd, addresses) whatever its share of the row, so threads own 32 elements
 // where the row has them, and as many threads run as have the registers for that: the waiting row
 // and one weight in 128 (32768 x 4096 forward: 112 us with 512 threads, 128 with 384), two weights
-// in 168 (with 512 threads of 24 elements 171 us against 177, but from 8 bits 240 against 218); in
+// in 168 (with 512 threads of 24 elements 171 us against 177, but in 8 bits 240 against 218); in
 // the backward column sums besides, of which one fits 168, two take 255 (with 512 threads of 16
-// elements 265 us as well as 266, but from 8 bits 302 against 272).
+// elements 265 us as well as 266).
 enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
 constexpr int fwd_threads(int form) { return form == kKeep ? 512 : 384; }
-constexpr int bwd_threads(int form) { return form == kKeep ? 384 : 256; }
+// From 8 bits the backward can keep a thread's column sums in tensor memory and run more threads with
+// the registers that frees.  It does where that makes room for another row in a CTA: with both norms
+// up to 6144 elements a row (65536 x 4096: 455 us against 481, 30720 x 6144 335 against 389, 65536 x
+// 1536 188 against 222; wider rows are one at a time either way, 32768 x 8192 559 against 476), in the
+// 8-bit norm past that (32768 x 8192 237 us against 295; 65536 x 4096 with dh 306 against 294).
+__host__ __device__ constexpr bool wide_rows(int form, bool packed, int H) {
+  return packed && H > 6144 && (form == kKeep || form == kBoth);
+}
+__host__ __device__ constexpr bool sums_in_tmem(int form, bool packed, int vpt, bool wide) {
+  return packed && vpt >= 3 && (form == kBoth ? !wide : form == kKeep && wide);
+}
+__host__ __device__ constexpr int bwd_threads(int form, bool packed, bool wide) {
+  return form == kKeep ? (wide ? 512 : 384) : (form == kBoth && packed && !wide ? 384 : 256);
+}
 constexpr int kMaxWarps = 16;
 constexpr int kMaxTensors = 4;    // staged
 // CTAs of the backward at most, whatever the GPU: the rows' partition, and with it the order of
