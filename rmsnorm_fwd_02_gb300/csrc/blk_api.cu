@@ -69,7 +69,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // forward's also give the same results whether it packs or not).
 Shape team_shape(int64_t R, int H, int form, bool bwd, bool packed) {
   const int threads_cta =
-      bwd ? bwd_threads(form, packed, wide_rows(form, packed, H)) : fwd_threads(form);
+      bwd ? bwd_threads(form, uses_tmem(form, packed, H)) : fwd_threads(form);
   Shape s{};
   const int nv = H / 8;
   auto threads = [&](int vpt) {
@@ -141,6 +141,12 @@ Shape plan(int64_t R, int H, int form, bool bwd, bool packed, size_t row, size_t
   return s;
 }
 
+// A team of several warps starts a slot's next copies while it works on the slot behind it: the ring
+// has two at least.  (Every size has; a shape without is not launched.)
+bool runs(const Shape& s) {
+  return s.stages >= 2 && s.smem <= kSmemBytes && s.teams >= 1 && s.threads <= 32 * kMaxWarps;
+}
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 bool type_ok(int dtype, bool activation) {
@@ -204,6 +210,7 @@ int run_fwd(const Fwd& f, void* stream) {
   const size_t row = 2 * static_cast<size_t>(f.H);
   const bool pack = f.x8 != nullptr || f.h8 != nullptr;
   const Shape s = plan(f.R, f.H, f.form, false, false, f.residual != nullptr ? 2 * row : row, row, 0);
+  if (!runs(s)) return RMSN_ERR_UNSUPPORTED;
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
   if (f.residual != nullptr) a.in[1] = staged(f.residual, f.R > 1 ? 2 * f.s_res : row, row);
@@ -290,6 +297,7 @@ int run_bwd(const Bwd& b, void* stream) {
   for (const Staged& in : a.in)
     if (in.p != nullptr) row += in.bytes;
   const Shape s = plan(b.R, b.H, b.form, true, b.packed, row, least, (pre ? 1 : 0) + (s_sums ? 1 : 0));
+  if (!runs(s)) return RMSN_ERR_UNSUPPORTED;
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
   const size_t need = sizeof(float) * ((pre ? pre_floats(s, b.H) : 0) +
@@ -542,6 +550,7 @@ int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backwar
   const Shape s = backward ? plan(R, H, kBoth, true, packed != 0, 2 * wide + 2 * saved,
                                   wide < saved ? wide : saved, 2)
                            : plan(R, H, kBoth, false, false, 2 * wide, wide, 0);
+  if (!runs(s)) return RMSN_ERR_UNSUPPORTED;
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
   for (int i = 0; i < n_out && i < BLOCK_PLAN_FIELDS; ++i) out[i] = v[i];

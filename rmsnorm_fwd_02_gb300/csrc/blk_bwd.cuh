@@ -72,18 +72,18 @@ __device__ __forceinline__ void join_teams(const Args& a, const float* rows, flo
   }
 }
 
-template <typename T, int VPT, int kForm, bool kPacked, bool kEven, bool kWide = false>
-__global__ void __launch_bounds__(bwd_threads(kForm, kPacked, kWide), 1) blk_bwd_kernel(const BwdArgs a) {
+template <typename T, int VPT, int kForm, bool kPacked, bool kEven, bool kTmem>
+__global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(const BwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   constexpr bool kX = kForm != kKeep;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint64_t pol = l2_evict_first_policy();
   // Sums in tensor memory: for each vector 8 columns of dw_pre's, then 8 of S; the warps that share a
   // quarter of its lanes side by side.
-  constexpr bool kTm = sums_in_tmem(kForm, kPacked, VPT, kWide);
+  constexpr bool kTm = kTmem && VPT >= 3;
   constexpr int kTmVec = kX ? 16 : 8, kTmWarp = kTmVec * VPT;
   constexpr int kTmCols =
-      kTm ? static_cast<int>(tmem_alloc_cols((bwd_threads(kForm, kPacked, kWide) / 128) * kTmWarp)) : 0;
+      kTm ? static_cast<int>(tmem_alloc_cols((bwd_threads(kForm, kTmem) / 128) * kTmWarp)) : 0;
   Team t = team_begin<4, kTmCols>(a, smem, pol, a.samples == 1);
   uint32_t tm = 0;
   if constexpr (kTm) {
@@ -431,21 +431,23 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kPacked, kWide), 1) blk_bwd
   if (kX && a.samples == 1) join_teams(a, rows_s, a.part_s + cta);
 }
 
+// The build for a shape.  (Few vectors a thread are a matter of narrow rows or of few, which keep no
+// sums in tensor memory but have its builds' threads.)
 template <typename T, int VPT, bool kEven>
-const void* pick_bwd(int form, bool packed, bool wide) {
+const void* pick_bwd(int form, bool packed, bool tmem) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
-  if constexpr (VPT == 4) {  // (what such rows have)
-    if (wide)
-      return form == kKeep ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, true>)
-                           : fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, true>);
+#define BLK_PICK(F)                                                     \
+  (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven, false>)          \
+          : fn(&blk_bwd_kernel<T, VPT, F, false, kEven, false>))
+  if (form == kBoth && tmem) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, true>);
+  if constexpr (VPT == 4) {
+    if (form == kKeep && tmem) return fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, true>);
+    if (form == kBoth && packed) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, false>);
   }
-#define BLK_PICK(F)                                              \
-  (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven>)          \
-          : fn(&blk_bwd_kernel<T, VPT, F, false, kEven>))
   switch (form) {
     case kKeep: return BLK_PICK(kKeep);
     case kPre: return BLK_PICK(kPre);
-    case kBoth: return BLK_PICK(kBoth);
+    case kBoth: return fn(&blk_bwd_kernel<T, VPT, kBoth, false, kEven, false>);
     default: return BLK_PICK(kPost);
   }
 #undef BLK_PICK
@@ -453,13 +455,13 @@ const void* pick_bwd(int form, bool packed, bool wide) {
 
 template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
-  const bool even = even_rows(a.H, s.vpt, s.ntg), wide = wide_rows(form, packed, a.H);
-  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, wide)
-                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, wide)
-                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, wide)
-                                        : pick_bwd<T, 3, false>(form, packed, wide))
-                                : (even ? pick_bwd<T, 4, true>(form, packed, wide)
-                                        : pick_bwd<T, 4, false>(form, packed, wide));
+  const bool even = even_rows(a.H, s.vpt, s.ntg), tmem = uses_tmem(form, packed, a.H);
+  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, tmem)
+                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, tmem)
+                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, tmem)
+                                        : pick_bwd<T, 3, false>(form, packed, tmem))
+                                : (even ? pick_bwd<T, 4, true>(form, packed, tmem)
+                                        : pick_bwd<T, 4, false>(form, packed, tmem));
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   BwdArgs copy = a;

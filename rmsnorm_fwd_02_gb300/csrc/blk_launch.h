@@ -22,15 +22,13 @@ constexpr int fwd_threads(int form) { return form == kKeep ? 512 : 384; }
 // the registers that frees.  It does where that makes room for another row in a CTA: with both norms
 // up to 6144 elements a row (65536 x 4096: 455 us against 481, 30720 x 6144 335 against 389, 65536 x
 // 1536 188 against 222; wider rows are one at a time either way, 32768 x 8192 559 against 476), in the
-// 8-bit norm past that (32768 x 8192 237 us against 295; 65536 x 4096 with dh 306 against 294).
-__host__ __device__ constexpr bool wide_rows(int form, bool packed, int H) {
-  return packed && H > 6144 && (form == kKeep || form == kBoth);
+// 8-bit norm past that (32768 x 8192 237 us against 295; 65536 x 4096 with dh 306 against 294).  From
+// 16 bits it gains nothing (65536 x 1536 200 us against 203, 65536 x 512 86 against 81).
+__host__ __device__ constexpr bool uses_tmem(int form, bool packed, int H) {
+  return packed && (form == kBoth ? H <= 6144 : form == kKeep && H > 6144);
 }
-__host__ __device__ constexpr bool sums_in_tmem(int form, bool packed, int vpt, bool wide) {
-  return packed && vpt >= 3 && (form == kBoth ? !wide : form == kKeep && wide);
-}
-__host__ __device__ constexpr int bwd_threads(int form, bool packed, bool wide) {
-  return form == kKeep ? (wide ? 512 : 384) : (form == kBoth && packed && !wide ? 384 : 256);
+__host__ __device__ constexpr int bwd_threads(int form, bool tmem) {
+  return form == kKeep ? (tmem ? 512 : 384) : (tmem ? 384 : 256);
 }
 constexpr int kMaxWarps = 16;
 constexpr int kMaxTensors = 4;    // staged
