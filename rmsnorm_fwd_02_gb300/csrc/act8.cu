@@ -49,9 +49,21 @@ __device__ __forceinline__ void words_from(const uint32_t (&w)[N + 4], uint32_t 
     }
   }
 }
-template <int N, bool kHalves>
+// kSame: bytes is the same for the whole warp (a branch instead of selections).
+template <int N, bool kHalves, bool kSame>
 __device__ __forceinline__ void shift_words(const uint32_t (&w)[N + 4], uint32_t bytes, uint32_t (&o)[N]) {
-  switch (bytes >> 2) {  // (mostly the same for a whole warp)
+  if constexpr (!kSame) {
+    uint32_t a[N + 2], b[N + 1];
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) a[i] = (bytes & 8u) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) b[i] = (bytes & 4u) ? a[i + 1] : a[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      o[i] = kHalves ? __funnelshift_r(b[i], b[i + 1], (bytes & 2u) * 8u) : b[i];
+    return;
+  }
+  switch (bytes >> 2) {
     case 0: words_from<N, 0, kHalves>(w, bytes, o); break;
     case 1: words_from<N, 1, kHalves>(w, bytes, o); break;
     case 2: words_from<N, 2, kHalves>(w, bytes, o); break;
@@ -79,6 +91,7 @@ struct Raw {
     }
   }
   // the elements in place, zeros from element n on
+  template <bool kSame>
   __device__ __forceinline__ void get(const T* p, int n, Words<T>& u) const {
     constexpr int kOut = static_cast<int>(sizeof(T) / 2);
     if constexpr (kVec) {
@@ -93,7 +106,7 @@ struct Raw {
         w[4 * i + 2] = v[i].z;
         w[4 * i + 3] = v[i].w;
       }
-      shift_words<4 * kOut, sizeof(T) == 2>(w, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u), o);
+      shift_words<4 * kOut, sizeof(T) == 2, kSame>(w, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u), o);
 #pragma unroll
       for (int i = 0; i < kOut; ++i)
         u[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -144,6 +157,19 @@ __device__ __forceinline__ void store_group(T* p, int n, bool vec, const Words<T
   }
 }
 
+// A group's numbers.
+template <typename T>
+__device__ __forceinline__ uint2 numbers_of(const Words<T>& u, uint32_t amax, uint32_t scale) {
+  if constexpr (sizeof(T) == 2) {
+    return act8_pack8<T>(u[0], amax, scale);
+  } else {
+    f2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = VecOf<T>::pair(u[i >> 1], i & 1);
+    return act8_pack8(v, amax, scale);
+  }
+}
+
 // Group c of a packed row, from its values; the four lanes of a block call it together, `here`
 // where the group is within the row's groups.
 template <typename T>
@@ -154,16 +180,7 @@ __device__ __forceinline__ void pack_group(const Act8Args& a, unsigned char* row
   if (!here) return;
   const int first_scale = static_cast<int>(act8_scale_offset(a.H));
   if (8 * c < first_scale) {
-    uint2 q;
-    if constexpr (sizeof(T) == 2) {
-      q = act8_pack8<T>(u[0], amax, s);
-    } else {
-      f2 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = VecOf<T>::pair(u[i >> 1], i & 1);
-      q = act8_pack8(v, amax, s);
-    }
-    *reinterpret_cast<uint2*>(row + 8 * c) = q;
+    *reinterpret_cast<uint2*>(row + 8 * c) = numbers_of<T>(u, amax, s);
   }
   if ((c & 3) == 0)
     row[first_scale + (c >> 2)] = static_cast<unsigned char>(s);
@@ -229,7 +246,7 @@ __global__ void __launch_bounds__(kAct8Threads, std::is_same_v<T, __nv_bfloat16>
     T* p = wide + 8 * static_cast<int64_t>(c);
     Words<T> u;
     if constexpr (kPack) {
-      raw[i].get(p, n, u);
+      raw[i].template get<true>(p, n, u);
       pack_group<T>(a, packed, c, c < static_cast<int>(a.groups), u);
     } else {
       if (n > 0) values_of<T>(q[i], s[i], u);
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(kAct8Threads, std::is_same_v<T, __nv_bfloat16>
           before[k] = v;
         }
         if (off != 0) {
-          shift_words<4 * kVecs, sizeof(T) == 2>(w, 16u - off, o);
+          shift_words<4 * kVecs, sizeof(T) == 2, true>(w, 16u - off, o);
         } else {
 #pragma unroll
           for (int k = 0; k < 4 * kVecs; ++k) o[k] = w[4 + k];
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(kAct8Threads) act8_flat_kernel(const Act8Args 
     const int n = here ? group_size(a, c[i]) : 0;
     Words<T> u;
     if constexpr (kPack) {
-      raw[i].get(static_cast<const T*>(a.in) + row[i] * a.s_row + 8 * c[i], n, u);
+      raw[i].template get<false>(static_cast<const T*>(a.in) + row[i] * a.s_row + 8 * c[i], n, u);
       pack_group<T>(a, static_cast<unsigned char*>(a.out) + row[i] * bytes, c[i], here, u);
     } else if (n > 0) {
       values_of<T>(q[i], s[i], u);
@@ -332,19 +349,121 @@ __global__ void __launch_bounds__(kAct8Threads) act8_flat_kernel(const Act8Args 
   }
 }
 
+// ---- rows of one block: a thread a row (of kG groups; up to 16 elements in 32 bytes, then 48) ----
+
+template <typename T, int kG, bool kVec, bool kPack>
+__global__ void __launch_bounds__(kAct8Threads) act8_block_kernel(const Act8Args a) {
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  // unpacked rows between vectors: the CTA's, which are back to back, pass through shared memory
+  constexpr bool kStaged = !kPack && !kVec && kG > 1;
+  __shared__ __align__(16) T stage[kStaged ? kAct8Threads * 8 * kG : 1];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kAct8Threads, row = row0 + threadIdx.x;
+  if (!kStaged && row >= a.R) return;
+  constexpr int kNumbers = kG > 2 ? 2 : 1;  // 16-byte vectors of numbers
+  uint4* const packed = static_cast<uint4*>(const_cast<void*>(kPack ? a.out : a.in)) +
+                        row * (kNumbers + 1);
+  T* const wide = static_cast<T*>(const_cast<void*>(kPack ? a.in : a.out)) + row * a.s_row;
+  uint2 q[2 * kNumbers];
+  if constexpr (kStaged) {
+    const int H = static_cast<int>(a.H);
+    if (row < a.R) {
+      uint32_t words[4 * kNumbers];
+#pragma unroll
+      for (int i = 0; i < kNumbers; ++i) {
+        const uint4 v = packed[i];
+        words[4 * i] = v.x;
+        words[4 * i + 1] = v.y;
+        words[4 * i + 2] = v.z;
+        words[4 * i + 3] = v.w;
+      }
+      const uint32_t s = *reinterpret_cast<const unsigned char*>(packed + kNumbers);
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        Words<T> u;
+        values_of<T>(make_uint2(words[2 * g], words[2 * g + 1]), s, u);
+        const T* e = reinterpret_cast<const T*>(u);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (8 * g + x < H) stage[static_cast<int>(threadIdx.x) * H + 8 * g + x] = e[x];
+      }
+    }
+    __syncthreads();
+    const int n = static_cast<int>(min(a.R - row0, static_cast<int64_t>(kAct8Threads))) * H;
+    T* const out = static_cast<T*>(a.out) + row0 * H;
+    // (256 rows are whole vectors, so every CTA's start as the tensor does)
+    constexpr int kIn = static_cast<int>(16 / sizeof(T));
+    const int whole = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 ? n / kIn : 0;
+    for (int i = threadIdx.x; i < whole; i += kAct8Threads)
+      reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(stage)[i];
+    for (int i = whole * kIn + threadIdx.x; i < n; i += kAct8Threads) out[i] = stage[i];
+  } else if constexpr (kPack) {
+    Raw<T, kVec> raw[kG];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) raw[g].load(wide + 8 * g, group_size(a, g));
+    Words<T> u[kG];
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      raw[g].template get<false>(wide + 8 * g, group_size(a, g), u[g]);
+      amax = max(amax, act8_max8<T>(u[g]));
+    }
+    const uint32_t s = act8_scale_byte(amax);
+#pragma unroll
+    for (int g = 0; g < 2 * kNumbers; ++g)
+      q[g] = g < kG ? numbers_of<T>(u[g < kG ? g : 0], amax, s) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < kNumbers; ++i)
+      packed[i] = make_uint4(q[2 * i].x, q[2 * i].y, q[2 * i + 1].x, q[2 * i + 1].y);
+    packed[kNumbers] = make_uint4(s, 0u, 0u, 0u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kNumbers; ++i) {
+      const uint4 v = packed[i];
+      q[2 * i] = make_uint2(v.x, v.y);
+      q[2 * i + 1] = make_uint2(v.z, v.w);
+    }
+    const uint32_t s = *reinterpret_cast<const unsigned char*>(packed + kNumbers);
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const int n = group_size(a, g);
+      Words<T> u;
+      values_of<T>(q[g], s, u);
+      if (n > 0) store_group(wide + 8 * g, n, kVec, u);
+    }
+  }
+}
+
 template <typename T, bool kPack>
-const void* pick_of(bool flat, bool vec) {
+const void* pick_block(int64_t H, bool vec) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+#define ACT8_PICK(G)                                           \
+  (vec ? fn(&act8_block_kernel<T, G, true, kPack>)             \
+       : fn(&act8_block_kernel<T, G, false, kPack>))
+  return H <= 8 ? ACT8_PICK(1) : H <= 16 ? ACT8_PICK(2) : ACT8_PICK(4);
+#undef ACT8_PICK
+}
+
+// Whether rows are taken by a thread each: those of one block, but for unpacked rows of whole vectors
+// past 16 elements, which lanes side by side write better.
+bool one_block(int64_t H, bool vec, bool pack) {
+  return H <= (vec && !pack ? kAct8Block / 2 : kAct8Block);
+}
+
+template <typename T, bool kPack>
+const void* pick_of(int64_t H, bool flat, bool vec) {
+  auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
+  if (one_block(H, vec, kPack)) return pick_block<T, kPack>(H, vec);
   if (flat)
     return vec ? fn(&act8_flat_kernel<T, true, kPack>) : fn(&act8_flat_kernel<T, false, kPack>);
   return vec ? fn(&act8_wide_kernel<T, true, kPack>) : fn(&act8_wide_kernel<T, false, kPack>);
 }
 
 template <bool kPack>
-const void* pick(int dtype, bool flat, bool vec) {
-  return dtype == ACT8_BF16   ? pick_of<__nv_bfloat16, kPack>(flat, vec)
-         : dtype == ACT8_FP32 ? pick_of<float, kPack>(flat, vec)
-                              : pick_of<__half, kPack>(flat, vec);
+const void* pick(int dtype, int64_t H, bool flat, bool vec) {
+  return dtype == ACT8_BF16   ? pick_of<__nv_bfloat16, kPack>(H, flat, vec)
+         : dtype == ACT8_FP32 ? pick_of<float, kPack>(H, flat, vec)
+                              : pick_of<__half, kPack>(H, flat, vec);
 }
 
 // Rows of at least this many groups are taken in tiles of 32, three quarters of which are then there;
@@ -374,9 +493,15 @@ int act8_run(const void* wide, int dtype, const void* packed, int64_t R, int64_t
   a.groups = static_cast<uint32_t>((H + kAct8Block - 1) / kAct8Block * 4);
   a.vec = reinterpret_cast<uintptr_t>(wide) % 16 == 0 && a.s_row * elem % 16 == 0 && H % 8 == 0;
   const bool flat = a.groups < kAct8WideGroups;
-  const void* fn = pack ? pick<true>(dtype, flat, a.vec) : pick<false>(dtype, flat, a.vec);
+  const void* fn = pack ? pick<true>(dtype, H, flat, a.vec) : pick<false>(dtype, H, flat, a.vec);
   const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
   void* args[] = {&a};
+  if (one_block(H, a.vec, pack)) {
+    const dim3 grid(static_cast<unsigned>((R + kAct8Threads - 1) / kAct8Threads));  // 2^42 / 32 / 256
+    return launch_pdl(fn, grid, dim3(kAct8Threads), 0, stream_, args) == cudaSuccess
+               ? RMSN_OK
+               : RMSN_ERR_CUDA;
+  }
   if (!flat) {
     a.tiles = (a.groups + 31) / 32;
     constexpr int64_t per = kAct8Threads / 32 * kAct8Unroll;  // tiles a CTA

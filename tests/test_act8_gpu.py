@@ -71,6 +71,18 @@ def test_strides_and_addresses(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("h", list(range(1, 41)) + [47, 64, 190, 191])
+def test_narrow_rows_at_every_alignment(dtype, h):
+    flat = normal(h, 600 * h + 8, dtype=dtype)
+    for off in (0, 1, 2, 3, 5):
+        x = flat[off:off + 600 * h].view(600, h)
+        p = R.act8_pack(x)
+        want = OA.pack(f64(x))
+        assert np.array_equal(p.cpu().numpy(), want)
+        check(R.act8_unpack(p, h, dtype), OA.unpack(want, h), np.zeros((600, h)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("h", [769, 772, 1024, 1027, 1032, 2055, 5001])
 def test_wide_rows_at_every_alignment(dtype, h):
     # rows that start anywhere between two 16-byte vectors; rows, chunks and blocks end anywhere
@@ -89,7 +101,7 @@ def test_wide_rows_at_every_alignment(dtype, h):
 
 def test_unpacked_rows_end_where_they_end():
     # through the C ABI into a guarded buffer: nothing before, behind or between is written
-    for rows, h in ((3, 7), (5, 770), (4, 1031), (1, 4099)):
+    for rows, h in ((3, 7), (300, 13), (257, 16), (700, 27), (256, 32), (5, 770), (4, 1031), (1, 4099)):
         p = R.act8_pack(normal(h, rows, h))
         for off in (0, 1, 5):
             buf = torch.full((rows * h + 24,), 7.0, dtype=torch.bfloat16, device=DEV)
