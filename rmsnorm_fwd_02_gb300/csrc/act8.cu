@@ -307,6 +307,31 @@ __global__ void __launch_bounds__(kAct8Threads, std::is_same_v<T, __nv_bfloat16>
   }
 }
 
+// Elements before p in its 16-byte vector.
+template <typename T>
+__device__ __forceinline__ int in_vector(const T* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+// A CTA's n elements for out, staged from stage + in_vector(out) on, so that the vectors of both
+// coincide.
+template <typename T>
+__device__ __forceinline__ void copy_out(const T* stage, T* out, int n) {
+  constexpr int kIn = static_cast<int>(16 / sizeof(T));
+  const int shift = in_vector(out);
+  T* const base = out - shift;  // elements [shift, shift + n) of it are the CTA's
+  const int end = shift + n;
+  for (int i = static_cast<int>(threadIdx.x); i * kIn < end; i += kAct8Threads) {
+    const int lo = i * kIn;
+    if (lo >= shift && lo + kIn <= end) {
+      reinterpret_cast<uint4*>(base)[i] = reinterpret_cast<const uint4*>(stage)[i];
+    } else {
+#pragma unroll
+      for (int x = 0; x < kIn; ++x)
+        if (lo + x >= shift && lo + x < end) base[lo + x] = stage[lo + x];
+    }
+  }
+}
+
 // ---- narrow rows: the groups of all rows side by side -----------------------------------------
 
 template <typename T, bool kVec, bool kPack>
@@ -316,6 +341,16 @@ __global__ void __launch_bounds__(kAct8Threads) act8_flat_kernel(const Act8Args 
   const uint32_t first = blockIdx.x * (kAct8Threads * kAct8Unroll) + threadIdx.x;
   const int64_t bytes = act8_row_size(a.H);
   const uint32_t first_scale = static_cast<uint32_t>(act8_scale_offset(a.H));
+  // unpacked rows between vectors: the CTA's groups, whose elements are back to back, pass through
+  // shared memory
+  constexpr bool kStaged = !kPack && !kVec;
+  __shared__ __align__(16) T stage[kStaged ? kAct8Threads * kAct8Unroll * 8 + 8 : 1];
+  auto element = [&](uint32_t group) {  // the first element of a group, or of the next row
+    const int64_t r = __umulhi(group, a.mul) >> a.shift;
+    return r * a.H + min(static_cast<int64_t>(8) * (group - static_cast<uint32_t>(r) * a.groups), a.H);
+  };
+  const int64_t at0 = kStaged ? element(blockIdx.x * (kAct8Threads * kAct8Unroll)) : 0;
+  T* const out = kStaged ? static_cast<T*>(a.out) + at0 : nullptr;
   Raw<T, kVec> raw[kAct8Unroll];
   uint2 q[kAct8Unroll];
   uint32_t s[kAct8Unroll], row[kAct8Unroll];
@@ -344,8 +379,23 @@ __global__ void __launch_bounds__(kAct8Threads) act8_flat_kernel(const Act8Args 
       pack_group<T>(a, static_cast<unsigned char*>(a.out) + row[i] * bytes, c[i], here, u);
     } else if (n > 0) {
       values_of<T>(q[i], s[i], u);
-      store_group(static_cast<T*>(a.out) + row[i] * a.s_row + 8 * c[i], n, kVec, u);
+      const int64_t at = row[i] * a.H + 8 * c[i];
+      if constexpr (kStaged) {
+        const T* e = reinterpret_cast<const T*>(u);
+        T* const own = stage + in_vector(out) + static_cast<int>(at - at0);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (x < n) own[x] = e[x];
+      } else {
+        store_group(static_cast<T*>(a.out) + at, n, true, u);
+      }
     }
+  }
+  if constexpr (kStaged) {
+    __syncthreads();
+    const uint32_t end = min(a.total, blockIdx.x * (kAct8Threads * kAct8Unroll) +
+                                          kAct8Threads * kAct8Unroll);
+    copy_out(stage, out, static_cast<int>(element(end) - at0));
   }
 }
 
@@ -357,7 +407,7 @@ __global__ void __launch_bounds__(kAct8Threads) act8_block_kernel(const Act8Args
   pdl_allow_next_grid();
   // unpacked rows between vectors: the CTA's, which are back to back, pass through shared memory
   constexpr bool kStaged = !kPack && !kVec && kG > 1;
-  __shared__ __align__(16) T stage[kStaged ? kAct8Threads * 8 * kG : 1];
+  __shared__ __align__(16) T stage[kStaged ? kAct8Threads * 8 * kG + 8 : 1];
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kAct8Threads, row = row0 + threadIdx.x;
   if (!kStaged && row >= a.R) return;
   constexpr int kNumbers = kG > 2 ? 2 : 1;  // 16-byte vectors of numbers
@@ -367,6 +417,8 @@ __global__ void __launch_bounds__(kAct8Threads) act8_block_kernel(const Act8Args
   uint2 q[2 * kNumbers];
   if constexpr (kStaged) {
     const int H = static_cast<int>(a.H);
+    T* const own = stage + in_vector(static_cast<const T*>(a.out) + row0 * H) +
+                   static_cast<int>(threadIdx.x) * H;
     if (row < a.R) {
       uint32_t words[4 * kNumbers];
 #pragma unroll
@@ -385,18 +437,12 @@ __global__ void __launch_bounds__(kAct8Threads) act8_block_kernel(const Act8Args
         const T* e = reinterpret_cast<const T*>(u);
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          if (8 * g + x < H) stage[static_cast<int>(threadIdx.x) * H + 8 * g + x] = e[x];
+          if (8 * g + x < H) own[8 * g + x] = e[x];
       }
     }
     __syncthreads();
     const int n = static_cast<int>(min(a.R - row0, static_cast<int64_t>(kAct8Threads))) * H;
-    T* const out = static_cast<T*>(a.out) + row0 * H;
-    // (256 rows are whole vectors, so every CTA's start as the tensor does)
-    constexpr int kIn = static_cast<int>(16 / sizeof(T));
-    const int whole = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 ? n / kIn : 0;
-    for (int i = threadIdx.x; i < whole; i += kAct8Threads)
-      reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(stage)[i];
-    for (int i = whole * kIn + threadIdx.x; i < n; i += kAct8Threads) out[i] = stage[i];
+    copy_out(stage, static_cast<T*>(a.out) + row0 * H, n);
   } else if constexpr (kPack) {
     Raw<T, kVec> raw[kG];
 #pragma unroll
