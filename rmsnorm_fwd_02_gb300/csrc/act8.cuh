@@ -21,7 +21,8 @@ __host__ __device__ inline int64_t act8_scale_offset(int64_t H) {
   return (H + 15) & ~static_cast<int64_t>(15);
 }
 __host__ __device__ inline int64_t act8_row_size(int64_t H) {
-  return act8_scale_offset(H) + (((H + kAct8Block - 1) / kAct8Block + 15) & ~static_cast<int64_t>(15));
+  const int64_t blocks = (H + kAct8Block - 1) / kAct8Block;
+  return act8_scale_offset(H) + ((blocks + 15) & ~static_cast<int64_t>(15));
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {

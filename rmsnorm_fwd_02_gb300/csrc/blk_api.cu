@@ -103,17 +103,16 @@ Shape team_shape(int64_t R, int H, int form, bool bwd, bool packed) {
   return s;
 }
 
-}  // namespace
-
-static size_t factor_bytes(const Shape& s) {
+// Bytes of the factors in shared memory, and of all of it but the teams' sums that take its place in
+// the end.
+size_t factor_bytes(const Shape& s) {
   return 32 * static_cast<size_t>(s.teams) * s.ntg * s.vpt;
 }
 size_t smem_bytes(const Shape& s) {
   const size_t n = static_cast<size_t>(s.teams) * s.stages;
-  return (s.factor ? factor_bytes(s) : 0) + n * s.slot + ((8 * n + 15) & ~size_t{15}) + 4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 32;
+  return (s.factor ? factor_bytes(s) : 0) + n * s.slot + ((8 * n + 15) & ~size_t{15}) +
+         4 * 2 * kMaxWarps * static_cast<size_t>(s.teams) + 32;
 }
-
-namespace {
 
 // The ring for staged rows of `row` bytes, of which a copy moves at least `least` at once; the
 // backward's teams' sums take its place in the end (`sums` rows a team).

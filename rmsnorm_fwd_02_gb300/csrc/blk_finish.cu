@@ -8,9 +8,9 @@ namespace {
 
 constexpr int kLanes = kFinishCols / 4;  // threads of four columns each side by side
 
-// Sums of four columns over kFinishSlices threads each (sh: two vectors a thread): `each(add)` adds a thread's vectors, the threads'
-// sums are then joined pairwise.  The errors of the additions are carried along.  Every thread of
-// the block calls it; the result is that of the threads with sl == 0.
+// Sums of four columns over kFinishSlices threads each (sh: two vectors a thread): `each(add)` adds a
+// thread's vectors, the threads' sums are then joined pairwise.  The errors of the additions are
+// carried along.  Every thread of the block calls it; the result is that of the threads with sl == 0.
 template <typename Each>
 __device__ __forceinline__ float4 joined_sums(float4* sh, int sl, int cl, Each each) {
   float4* const se = sh + kFinishSlices * kLanes;

@@ -3,8 +3,12 @@
 // units of the two activation types.
 //
 // HBM-bound: 8 bytes an element (x, residual; h, y) and 1.03 for each tensor kept in 8 bits, for
-// some 20 instructions.  Two row sums follow one another, of x^2 and, through rstd, of h^2, so a
-// row cannot be streamed; it waits in shared memory, h between the sums in registers.
+// some 16 thread instructions.  Two row sums follow one another, of x^2 and, through rstd, of h^2,
+// so a row cannot be streamed; it waits in shared memory, h between the sums in registers.
+//
+// Measured, both norms and a gate, 65536 rows: of 4096 352 us (92 % of a plain copy's rate over the 8
+// bytes), of 1536 137 (88 %), of 512 52 (78 %); keeping 8 bits 425 (95 % of 10), 172, 65.  The norm
+// alone keeping 8 bits: of 4096 214 us (95 %), with a residual 398 (92 %).
 #pragma once
 
 #include "blk_common.cuh"

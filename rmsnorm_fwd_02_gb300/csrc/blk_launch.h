@@ -129,8 +129,6 @@ __host__ __device__ inline int64_t row_team(int64_t r, int64_t R, int64_t n) {
   return ((r + 1) * n - 1) / R;
 }
 
-size_t smem_bytes(const Shape& s);
-
 cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int dtype, int form, bool pack,
                        cudaStream_t st);
 cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int dtype, int form, bool packed,
