@@ -223,13 +223,11 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
       fetch(i + together < n ? row + together : ra + t.stride + t.sub);
       const bool first = i == 0;
       i += together;
-      // Packed vectors stay in registers between the passes over a row (h, then x in its place):
-      // their unpacking is three times that of 16-bit values, which are read again.
+      // Packed vectors stay in registers between the passes over a row, times rstd (h, then x in its
+      // place): their unpacking is three times that of 16-bit values, which are read again.
       f2 kept[kPacked ? VPT : 1][4];
-      float unit[kPacked ? VPT : 1];
       f2 nc2 = f2_splat(0.f);
       if constexpr (kPreN) {
-        float dot = 0.f;
         f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
@@ -237,18 +235,16 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
           const bool live = kEven || (valid && c < NV);
           const uint4 dyw = lds128_at(live ? dys + 16u * c : t.zero);
           if constexpr (kPacked) {
-            f2 h[4], dy[4];
-            const float u = load_saved<T, kPacked>(a, t, hs, c, live, h);
+            f2 dy[4];
+            const f2 rh = f2_splat(load_saved<T, kPacked>(a, t, hs, c, live, kept[v]) * r2);
             VecOf<T>::unpack(dyw, dy);
-            dot0 = f2_mul(f2_mul(dy[0], w[v][0]), h[0]);
-            dot1 = f2_mul(f2_mul(dy[1], w[v][1]), h[1]);
-            dot0 = f2_fma(f2_mul(dy[2], w[v][2]), h[2], dot0);
-            dot1 = f2_fma(f2_mul(dy[3], w[v][3]), h[3], dot1);
-            const f2 d = f2_add(dot0, dot1);
-            dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
-            unit[v] = u;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) kept[v][q] = h[q];
+            for (int q = 0; q < 4; q += 2) {
+              kept[v][q] = f2_mul(kept[v][q], rh);
+              kept[v][q + 1] = f2_mul(kept[v][q + 1], rh);
+              dot0 = f2_fma(f2_mul(dy[q], w[v][q]), kept[v][q], dot0);
+              dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), kept[v][q + 1], dot1);
+            }
           } else {
             const uint4 hw = lds128_at(live ? hs + 16u * c : t.zero);
 #pragma unroll
@@ -258,19 +254,18 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
             }
           }
         }
-        if constexpr (!kPacked) {
-          const f2 d = f2_add(dot0, dot1);
-          dot = f2_lo(d) + f2_hi(d);
-        }
-        dot = row_sum(a, t, dot);
+        const f2 d = f2_add(dot0, dot1);
+        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
         if (first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<4>(a, t, j - 1 + a.stages, pol);
-        // t = r2 (dy w - h (mean r2^2)): the mean's factor times r2, on t's scale
-        nc2 = f2_splat(-(dot * (r2 * inv_h)) * r2);
+        // t = r2 (dy w - hhat mean(dy w hhat)); from 16 bits the sum is of dy w h
+        nc2 = f2_splat(-(kPacked ? dot * inv_h : dot * (r2 * inv_h)));
       }
       const f2 r2v = f2_splat(r2), r1v = f2_splat(r1);
+      // without dh the 8-bit norm's t has no use but its outputs: its factor r2 goes to theirs
+      const bool late = kForm == kKeep && !has_dh;
+      const f2 ro = late ? f2_splat(a.residual_scale * r2) : rscale;
       f2 m[VPT][4];
-      float dot = 0.f;
       f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
       const size_t out_row = static_cast<size_t>(row) * a.H;
       if constexpr (kTm) {
@@ -288,73 +283,63 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
         }
         if constexpr (kPreN) {
           f2 h[4], dy[4];
-          f2 nc = nc2, rh = r2v;
-          if constexpr (kPacked) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) h[q] = kept[v][q];
-            nc = f2_mul(nc2, f2_splat(unit[v]));
-            rh = f2_mul(r2v, f2_splat(unit[v]));
-          } else {
+          if constexpr (!kPacked) {
             load_saved<T, kPacked>(a, t, hs, c, live, h);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[q] = f2_mul(h[q], r2v);
           }
           VecOf<T>::unpack(lds128_at(live ? dys + 16u * c : t.zero), dy);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            g[q] = f2_mul(f2_fma(h[q], nc, f2_mul(dy[q], w[v][q])), r2v);
+            const f2 hhat = kPacked ? kept[kPacked ? v : 0][q] : h[q];
+            g[q] = f2_fma(hhat, nc2, f2_mul(dy[q], w[v][q]));
             if constexpr (kTm)
-              ap[q] = f2_mul(dy[q], f2_mul(h[q], rh));
+              ap[q] = f2_mul(dy[q], hhat);
             else
-              sum_pre[v][q] = f2_fma(dy[q], f2_mul(h[q], rh), sum_pre[v][q]);
+              sum_pre[v][q] = f2_fma(dy[q], hhat, sum_pre[v][q]);
           }
         }
-        if (!kPreN || has_dh) {
-          f2 dh[4];
-          VecOf<T>::unpack(lds128_at(live ? dhs + 16u * c : t.zero), dh);
+        f2 dh[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
+        if (!kPreN || has_dh) VecOf<T>::unpack(lds128_at(live ? dhs + 16u * c : t.zero), dh);
+        if (!late) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_add(g[q], dh[q]) : dh[q];
+          for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_fma(g[q], r2v, dh[q]) : dh[q];
         }
         f2 o[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], rscale);
+        for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], ro);
         if (live) stg128(static_cast<T*>(a.dres) + out_row + 8 * c, VecOf<T>::pack(o));
         if constexpr (kX) {
           f2 x[4];
           const float u = load_saved<T, kPacked>(a, t, xs, c, live, x);
-          f2 rx = kPostN ? r1v : f2_splat(1.f), f[4];
+          const f2 rx = f2_splat(kPostN ? r1 * u : u);
+          f2 f[4];
           get_factor(v, f);
-          if constexpr (kPacked) rx = f2_mul(rx, f2_splat(u));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
+            if constexpr (kPostN && kPacked) kept[v][q] = xh;
             if constexpr (kTm)
               as[q] = f2_mul(g[q], xh);
             else
               sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
             m[v][q] = f2_mul(g[q], f[q]);
           }
-          if constexpr (kPostN && kPacked) {
-            dot0 = f2_mul(m[v][0], x[0]);
-            dot1 = f2_mul(m[v][1], x[1]);
-            dot0 = f2_fma(m[v][2], x[2], dot0);
-            dot1 = f2_fma(m[v][3], x[3], dot1);
-            const f2 d = f2_add(dot0, dot1);
-            dot = __fmaf_rn(f2_lo(d) + f2_hi(d), u, dot);
-            unit[v] = u;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) kept[v][q] = x[q];
-          } else if constexpr (kPostN) {
+          if constexpr (kPostN) {
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
-              dot0 = f2_fma(m[v][q], x[q], dot0);
-              dot1 = f2_fma(m[v][q + 1], x[q + 1], dot1);
+              dot0 = f2_fma(m[v][q], kPacked ? kept[kPacked ? v : 0][q] : x[q], dot0);
+              dot1 = f2_fma(m[v][q + 1], kPacked ? kept[kPacked ? v : 0][q + 1] : x[q + 1], dot1);
             }
           }
-        } else {
+          if (!kPostN && live)
+            stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(m[v]));
+        } else if (live && a.dx != nullptr) {
+          f2 d[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) m[v][q] = f2_mul(g[q], f2_splat(a.scale));
+          for (int q = 0; q < 4; ++q) d[q] = f2_mul(g[q], f2_splat(late ? a.scale * r2 : a.scale));
+          stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(d));
         }
-        if (!kPostN && live && (kX || a.dx != nullptr))
-          stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(m[v]));
         if constexpr (kTm) {
           __syncwarp();
           tmem_wait_ld();
@@ -368,29 +353,24 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
         }
       }
       if constexpr (kPostN) {
-        if constexpr (!kPacked) {
-          const f2 d = f2_add(dot0, dot1);
-          dot = f2_lo(d) + f2_hi(d);
-        }
-        dot = row_sum(a, t, dot);
+        const f2 d = f2_add(dot0, dot1);
+        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
         if (!kPreN && first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
           issue<4>(a, t, j - 1 + a.stages, pol);
-        const f2 nc1 = f2_splat(-(dot * (r1 * inv_h)) * r1);
+        const f2 nc1 = f2_splat(-(kPacked ? dot * inv_h : dot * (r1 * inv_h) * r1));
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
           const bool live = kEven || (valid && c < NV);
           f2 x[4], o[4];
-          f2 nc = nc1;
           if constexpr (kPacked) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
-            nc = f2_mul(nc1, f2_splat(unit[v]));
           } else {
             load_saved<T, kPacked>(a, t, xs, c, live, x);
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc, m[v][q]), r1v);
+          for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc1, m[v][q]), r1v);
           if (live) stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(o));
         }
       }
