@@ -68,8 +68,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Threads a row, vectors a thread, teams a CTA and CTAs: functions of R, H and the kernel's form (the
 // forward's also give the same results whether it packs or not).
 Shape team_shape(int64_t R, int H, int form, bool bwd, bool packed) {
-  const int threads_cta =
-      bwd ? bwd_threads(form, uses_tmem(form, packed, H)) : fwd_threads(form);
+  const bool tmem = uses_tmem(form, packed, H);
+  int threads_cta = bwd ? bwd_threads(form, tmem, false) : fwd_threads(form);
   Shape s{};
   const int nv = H / 8;
   auto threads = [&](int vpt) {
@@ -91,6 +91,7 @@ Shape team_shape(int64_t R, int H, int form, bool bwd, bool packed) {
   // (64 x 256 forward: 3.1 us against 5.6)
   if (nv > 16 && threads(1) <= threads_cta && R <= int64_t{kPartSMs} * teams(threads(1))) s.vpt = 1;
   s.ntg = threads(s.vpt);
+  if (bwd) threads_cta = bwd_threads(form, tmem, more_rows(form, s.vpt, H));
   s.teams = teams(s.ntg);
   // a row (or a warp's rows) a team at least, spread over the CTAs first
   const int side = s.ntg < 32 ? 32 / s.ntg : 1;

@@ -79,8 +79,9 @@ __device__ __forceinline__ void join_teams(const Args& a, const float* rows, flo
   }
 }
 
-template <typename T, int VPT, int kForm, bool kPacked, bool kEven, bool kTmem>
-__global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(const BwdArgs a) {
+template <typename T, int VPT, int kForm, bool kPacked, bool kEven, bool kTmem,
+          bool kMore = false>
+__global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_kernel(const BwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
   constexpr bool kX = kForm != kKeep;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
   constexpr bool kTm = kTmem && VPT >= 3;
   constexpr int kTmVec = kX ? 16 : 8, kTmWarp = kTmVec * VPT;
   constexpr int kTmCols =
-      kTm ? static_cast<int>(tmem_alloc_cols((bwd_threads(kForm, kTmem) / 128) * kTmWarp)) : 0;
+      kTm ? static_cast<int>(tmem_alloc_cols((bwd_threads(kForm, kTmem, kMore) / 128) * kTmWarp))
+          : 0;
   Team t = team_begin<4, kTmCols>(a, smem, pol, a.samples == 1);
   uint32_t tm = 0;
   if constexpr (kTm) {
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem), 1) blk_bwd_kernel(c
 // The build for a shape.  (Few vectors a thread are a matter of narrow rows or of few, which keep no
 // sums in tensor memory but have its builds' threads.)
 template <typename T, int VPT, bool kEven>
-const void* pick_bwd(int form, bool packed, bool tmem) {
+const void* pick_bwd(int form, bool packed, bool tmem, bool more) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
 #define BLK_PICK(F)                                                     \
   (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven, false>)          \
@@ -430,6 +432,11 @@ const void* pick_bwd(int form, bool packed, bool tmem) {
   if constexpr (VPT == 4) {
     if (form == kKeep && tmem) return fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, true>);
     if (form == kBoth && packed) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, false>);
+  }
+  if constexpr (VPT == 3 && kEven) {  // (the widths of more_rows have even rows)
+    if (more)
+      return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, false, true>)
+                    : fn(&blk_bwd_kernel<T, VPT, kKeep, false, kEven, false, true>);
   }
   switch (form) {
     case kKeep: return BLK_PICK(kKeep);
@@ -442,13 +449,14 @@ const void* pick_bwd(int form, bool packed, bool tmem) {
 
 template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
-  const bool even = even_rows(a.H, s.vpt, s.ntg), tmem = uses_tmem(form, packed, a.H);
-  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, tmem)
-                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, tmem)
-                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, tmem)
-                                        : pick_bwd<T, 3, false>(form, packed, tmem))
-                                : (even ? pick_bwd<T, 4, true>(form, packed, tmem)
-                                        : pick_bwd<T, 4, false>(form, packed, tmem));
+  const bool even = even_rows(a.H, s.vpt, s.ntg), tmem = uses_tmem(form, packed, a.H),
+             more = more_rows(form, s.vpt, a.H);
+  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, tmem, more)
+                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, tmem, more)
+                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, tmem, more)
+                                        : pick_bwd<T, 3, false>(form, packed, tmem, more))
+                                : (even ? pick_bwd<T, 4, true>(form, packed, tmem, more)
+                                        : pick_bwd<T, 4, false>(form, packed, tmem, more));
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   BwdArgs copy = a;

@@ -27,8 +27,15 @@ constexpr int fwd_threads(int form) { return form == kKeep ? 512 : 384; }
 __host__ __device__ constexpr bool uses_tmem(int form, bool packed, int H) {
   return packed && (form == kBoth ? H <= 6144 : form == kKeep && H > 6144);
 }
-__host__ __device__ constexpr int bwd_threads(int form, bool tmem) {
-  return form == kKeep ? (tmem ? 512 : 384) : (tmem ? 384 : 256);
+// The 8-bit norm's rows of three vectors a thread leave registers for a third more rows at a time.
+// That pays where a row is a warp or two (65536 x 1536 101 us against 109, 131072 x 768 with dh 122
+// against 131), not where several lie in one (131072 x 384 57 against 53) or with longer teams (65536
+// x 2304 with dh 180 against 171); with both norms registers spill (65536 x 1536 208 against 180).
+constexpr bool more_rows(int form, int vpt, int H) {
+  return form == kKeep && vpt == 3 && H >= 768 && H <= 1536;
+}
+__host__ __device__ constexpr int bwd_threads(int form, bool tmem, bool more) {
+  return form == kKeep ? (tmem || more ? 512 : 384) : (tmem ? 384 : 256);
 }
 constexpr int kMaxWarps = 16;
 constexpr int kMaxTensors = 4;    // staged

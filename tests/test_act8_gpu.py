@@ -142,7 +142,8 @@ def test_rows_past_32_bits():
 # ---- the norm that keeps its input in 8 bits -----------------------------------------------
 
 SHAPES = [(1, 8), (3, 16), (700, 40), (257, 64), (65, 256), (700, 264), (33, 512), (300, 776),
-          (260, 1536), (130, 2048), (300, 4096), (65, 5120), (310, 6144), (2, 7688), (270, 8192)]
+          (260, 1536), (130, 2048), (300, 4096), (65, 5120), (310, 6144), (2, 7688), (270, 8192),
+          (2501, 1536), (5003, 768), (1300, 2304)]
 
 
 def case(rows, h, dtype, w_dtype, seed=0):
