@@ -14,10 +14,10 @@
 // samples, a team writes its S whenever its rows pass into another sample (row k + n for team k and
 // sample n: teams and samples both go forward, so no two share one).
 //
-// Measured, both norms, a gate and dh, 65536 rows: of 4096 516 us (94 % of a plain copy's rate over
-// the 12 bytes), of 1536 203 (89 %), of 512 81 (75 %); from 8 bits 455 (89 % of its 10), 188 and 86.
-// The norm alone from 8 bits, of 4096 with dh 294 us (96 %), without 256 (79 %).  Past bandwidth the
-// threads' own dependencies bound it: two or three warps a scheduler issue in 37 to 48 % of cycles.
+// Measured, both norms, a gate and dh, 65536 rows: of 4096 522 us (93 % of a plain copy's rate over
+// the 12 bytes), of 1536 203 (89 %), of 512 81 (75 %); from 8 bits 447 (91 % of its 10), 180 and 82.
+// The norm alone from 8 bits, of 4096 with dh 294 us (96 %), without 252 (80 %).  Past bandwidth the
+// threads' own dependencies bound it: two to four warps a scheduler issue in 37 to 48 % of cycles.
 #pragma once
 
 #include "blk_common.cuh"

@@ -43,7 +43,6 @@ constexpr int kMaxTensors = 4;    // staged
 // every sum, is a function of the shape.  GB300 has 152 SMs: there it is one wave.
 constexpr int kPartSMs = 152;
 constexpr int kFinishCols = 32;
-constexpr int kFinishSlices = 32;
 
 // What a kernel computes (the enumeration above).
 //   kKeep  h = x [+ residual], rounded; norm before; h held in 8 bits    (rmsnorm_act8)

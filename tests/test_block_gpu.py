@@ -10,7 +10,7 @@ from rmsnorm_fwd_02_gb300 import _native as N
 pytestmark = pytest.mark.gpu
 
 FORMS = [(True, True), (True, False), (False, True)]      # norm before, norm behind
-SHAPES = [(1, 8, 1), (6, 16, 3), (720, 40, 5), (255, 64, 255), (64, 256, 2), (700, 264, 7),
+SHAPES = [(1, 8, 1), (6, 16, 3), (720, 40, 5), (255, 64, 255), (64, 256, 2), (700, 264, 7), (60, 264, 10),
           (33, 512, 1), (310, 776, 31), (260, 1536, 2), (4 * 153, 2048, 153), (300, 4096, 5),
           (66, 5120, 3), (308, 6144, 4), (2, 7688, 2), (270, 8192, 6)]
 
