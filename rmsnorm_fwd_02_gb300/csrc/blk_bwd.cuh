@@ -154,13 +154,19 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
   auto take_sums = [&](int from, f2 (&sum)[VPT][4]) {
     if constexpr (kTm) {
       const f2 zero[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
+      float cells[VPT][8];
       __syncwarp();
       tmem_wait_st();
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) tmem_ld8(tm + kTmVec * v + from, sum[v]);
-      tmem_wait_ld();
+      for (int v = 0; v < VPT; ++v) tmem_ld8(tm + kTmVec * v + from, cells[v]);
+      tmem_wait_ld(cells[0]);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) tmem_st8(tm + kTmVec * v + from, zero);
+      for (int v = 0; v < VPT; ++v) {
+        if (v > 0) tmem_loaded(cells[v]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[v][q] = f2_make(cells[v][2 * q], cells[v][2 * q + 1]);
+        tmem_st8(tm + kTmVec * v + from, zero);
+      }
     }
   };
   if constexpr (kTm) {
@@ -278,7 +284,8 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
       for (int v = 0; v < VPT; ++v) {
         const int c = t.lt + v * a.ntg;
         const bool live = kEven || (valid && c < NV);
-        f2 g[4], tp[4], ts[4], ap[4], as[4];
+        f2 g[4], ap[4], as[4];
+        float tp[8], ts[8];  // sums from tensor memory, to be read after the wait
         if constexpr (kTm) {
           tmem_ld8(tm + kTmVec * v, tp);
           if constexpr (kX) tmem_ld8(tm + kTmVec * v + 8, ts);
@@ -344,14 +351,15 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
         }
         if constexpr (kTm) {
           __syncwarp();
-          tmem_wait_ld();
+          tmem_wait_ld(tp);
+          if constexpr (kX) tmem_loaded(ts);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            tp[q] = f2_add(tp[q], ap[q]);
-            if constexpr (kX) ts[q] = f2_add(ts[q], as[q]);
+            ap[q] = f2_add(f2_make(tp[2 * q], tp[2 * q + 1]), ap[q]);
+            if constexpr (kX) as[q] = f2_add(f2_make(ts[2 * q], ts[2 * q + 1]), as[q]);
           }
-          tmem_st8(tm + kTmVec * v, tp);
-          if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, ts);
+          tmem_st8(tm + kTmVec * v, ap);
+          if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, as);
         }
       }
       if constexpr (kPostN) {
