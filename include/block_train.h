@@ -92,13 +92,20 @@ int rmsnorm_block_train_bwd(const void* dy, const void* dh, const void* x, const
                             void* stream);
 
 /*
- * The launch plan with both norms (backward: with dh; packed: from 8 bits): for tests and
- * diagnostics.  No device access.  out receives min(n_out, BLOCK_PLAN_FIELDS) values: 16-byte
- * vectors a thread, threads a row, teams a CTA, rows a ring slot, slots a team, threads a CTA,
- * CTAs, dynamic shared memory bytes.  R >= 1; sizes as above.
+ * The launch plan of a kernel: for tests and diagnostics.  No device access.  `kernel` is a sum of
+ * the flags below; 0 is the forward with both norms, BLOCK_PLAN_BACKWARD the backward with both
+ * norms, a gate and dh.  packed: the backward from 8 bits.  out receives min(n_out, BLOCK_PLAN_FIELDS)
+ * values: 16-byte vectors a thread, threads a row, teams a CTA, rows a ring slot, slots a team,
+ * threads a CTA, CTAs, dynamic shared memory bytes.  R >= 1; sizes as above; N = 1 without a gate.
  */
 #define BLOCK_PLAN_FIELDS 8
-int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backward, int packed,
+#define BLOCK_PLAN_BACKWARD 1
+#define BLOCK_PLAN_NO_NORM_BEHIND 2 /* w_post NULL */
+#define BLOCK_PLAN_NO_NORM_BEFORE 4 /* w_pre NULL */
+#define BLOCK_PLAN_NO_GATE 8        /* gate NULL */
+#define BLOCK_PLAN_ONE_INPUT 16     /* dh NULL; in rmsnorm_act8_train_fwd residual NULL */
+#define BLOCK_PLAN_ACT8_NORM 32     /* rmsnorm_act8_train_fwd or _bwd (packed = 1) */
+int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int kernel, int packed,
                                     int64_t* out, int n_out);
 
 /*

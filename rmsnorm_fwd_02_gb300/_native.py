@@ -91,6 +91,8 @@ GROUPNORM_PLAN_FIELDS = ("on_chip", "channels", "threads", "cluster_ctas", "ctas
                          "units", "chunks")
 ACT8_BF16, ACT8_FP32, ACT8_FP16 = 0, 1, 2
 BLOCK_PLAN_FIELDS = ("vectors", "row_threads", "teams", "rows", "stages", "threads", "ctas", "smem")
+BLOCK_PLAN_NO_NORM_BEHIND, BLOCK_PLAN_NO_NORM_BEFORE, BLOCK_PLAN_NO_GATE = 2, 4, 8
+BLOCK_PLAN_ONE_INPUT, BLOCK_PLAN_ACT8_NORM = 16, 32
 
 PLAN_FWD, PLAN_FWD_RESIDUAL, PLAN_BWD, PLAN_BWD_DH, PLAN_BWD_ND, PLAN_BWD_ND_DH = 0, 1, 2, 3, 4, 5
 LN_PLAN_FWD, LN_PLAN_BWD = 0, 1
@@ -415,10 +417,11 @@ def rmsnorm_block_train_bwd(dy, dh, x, h, packed, dtype, rstd_pre, rstd_post, w_
         raise RmsnError("rmsnorm_block_train_bwd", st)
 
 
-def rmsnorm_block_train_launch_plan(R, H, N, backward, packed):
-    """The library's launch plan of a block's boundary with both norms for a shape, as a dict."""
+def rmsnorm_block_train_launch_plan(R, H, N, backward, packed, form=0):
+    """The library's launch plan of a block's boundary (both norms, a gate, dh), or of what the
+    BLOCK_PLAN_* flags of `form` make of it, for a shape, as a dict."""
     out = (C.c_int64 * len(BLOCK_PLAN_FIELDS))()
-    st = lib().rmsnorm_block_train_launch_plan(R, H, N, int(backward), int(packed), out,
+    st = lib().rmsnorm_block_train_launch_plan(R, H, N, int(backward) | form, int(packed), out,
                                                len(BLOCK_PLAN_FIELDS))
     if st != RMSN_OK:
         raise RmsnError("rmsnorm_block_train_launch_plan", st)

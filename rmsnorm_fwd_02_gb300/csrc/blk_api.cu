@@ -141,6 +141,23 @@ Shape plan(int64_t R, int H, int form, bool bwd, bool packed, size_t row, size_t
   return s;
 }
 
+// The forward's staged rows: x, and a residual.
+Shape fwd_plan(int64_t R, int H, int form, bool residual) {
+  const size_t row = 2 * static_cast<size_t>(H);
+  return plan(R, H, form, false, false, residual ? 2 * row : row, row, 0);
+}
+// The backward's: with a norm before, h and dy; dh; but for kKeep, x.
+Shape bwd_plan(int64_t R, int H, int form, bool packed, bool dh) {
+  const bool pre = form != kPost, x = form != kKeep;
+  const size_t wide = 2 * static_cast<size_t>(H);
+  const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
+  const size_t row = (pre ? saved + wide : 0) + (dh ? wide : 0) + (x ? saved : 0);
+  return plan(R, H, form, true, packed, row, wide < saved ? wide : saved, (pre ? 1 : 0) + (x ? 1 : 0));
+}
+int bwd_form(bool pre, bool post, bool gate) {
+  return !post ? (gate ? kPre : kKeep) : (pre ? kBoth : kPost);
+}
+
 // A team of several warps starts a slot's next copies while it works on the slot behind it: the ring
 // has two at least.  (Every size has; a shape without is not launched.)
 bool runs(const Shape& s) {
@@ -209,7 +226,7 @@ int run_fwd(const Fwd& f, void* stream) {
   FwdArgs a{};
   const size_t row = 2 * static_cast<size_t>(f.H);
   const bool pack = f.x8 != nullptr || f.h8 != nullptr;
-  const Shape s = plan(f.R, f.H, f.form, false, false, f.residual != nullptr ? 2 * row : row, row, 0);
+  const Shape s = fwd_plan(f.R, f.H, f.form, f.residual != nullptr);
   if (!runs(s)) return RMSN_ERR_UNSUPPORTED;
   set_common(a, s, f.R, f.H, f.N, err);
   a.in[0] = staged(f.x, f.R > 1 ? 2 * f.s_x : row, row);
@@ -293,10 +310,7 @@ int run_bwd(const Bwd& b, void* stream) {
   }
   if (b.dh != nullptr) a.in[2] = staged(b.dh, wide, wide);
   if (s_sums) a.in[3] = staged(b.x, b.packed || b.R == 1 ? saved : 2 * b.s_x, saved);
-  size_t row = 0, least = static_cast<size_t>(wide < saved ? wide : saved);
-  for (const Staged& in : a.in)
-    if (in.p != nullptr) row += in.bytes;
-  const Shape s = plan(b.R, b.H, b.form, true, b.packed, row, least, (pre ? 1 : 0) + (s_sums ? 1 : 0));
+  const Shape s = bwd_plan(b.R, b.H, b.form, b.packed, b.dh != nullptr);
   if (!runs(s)) return RMSN_ERR_UNSUPPORTED;
   set_common(a, s, b.R, b.H, b.N, err);
   set_offsets(a);
@@ -514,7 +528,7 @@ int rmsnorm_block_train_bwd(const void* dy, const void* dh, const void* x, const
   b.h = h;
   b.packed = packed != 0;
   b.dtype = dtype;
-  b.form = !post ? (gated ? kPre : kKeep) : (pre ? kBoth : kPost);
+  b.form = bwd_form(pre, post, gated);
   b.rstd_pre = rstd_pre;
   b.rstd_post = rstd_post;
   b.w_pre = w_pre;
@@ -538,18 +552,26 @@ int rmsnorm_block_train_bwd(const void* dy, const void* dh, const void* x, const
   return run_bwd(b, stream);
 }
 
-int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int backward, int packed,
+int rmsnorm_block_train_launch_plan(int64_t R, int32_t H, int64_t N, int kernel, int packed,
                                     int64_t* out, int n_out) {
-  if (!out || n_out < 0 || (backward != 0 && backward != 1) || (packed != 0 && packed != 1))
+  constexpr int kAll = BLOCK_PLAN_BACKWARD | BLOCK_PLAN_NO_NORM_BEHIND | BLOCK_PLAN_NO_NORM_BEFORE |
+                       BLOCK_PLAN_NO_GATE | BLOCK_PLAN_ONE_INPUT | BLOCK_PLAN_ACT8_NORM;
+  if (!out || n_out < 0 || (kernel & ~kAll) != 0 || (packed != 0 && packed != 1))
+    return RMSN_ERR_INVALID_ARG;
+  const bool backward = kernel & BLOCK_PLAN_BACKWARD, post = !(kernel & BLOCK_PLAN_NO_NORM_BEHIND),
+             pre = !(kernel & BLOCK_PLAN_NO_NORM_BEFORE), gate = !(kernel & BLOCK_PLAN_NO_GATE),
+             one = kernel & BLOCK_PLAN_ONE_INPUT, norm8 = kernel & BLOCK_PLAN_ACT8_NORM;
+  if (norm8 ? !(pre && post && gate) || (backward && !packed)
+            : (!pre && !post) || (one && (!backward || !pre)))
     return RMSN_ERR_INVALID_ARG;
   const int st = check_sizes(R, H, N);
   if (st != RMSN_OK) return st;
-  if (R == 0) return RMSN_ERR_INVALID_ARG;
-  const size_t wide = 2 * static_cast<size_t>(H);
-  const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
-  const Shape s = backward ? plan(R, H, kBoth, true, packed != 0, 2 * wide + 2 * saved,
-                                  wide < saved ? wide : saved, 2)
-                           : plan(R, H, kBoth, false, false, 2 * wide, wide, 0);
+  if (R == 0 || ((norm8 || !gate) && N != 1)) return RMSN_ERR_INVALID_ARG;
+  const int form = norm8       ? kKeep
+                   : backward  ? bwd_form(pre, post, gate)
+                               : (!post ? kPre : pre ? kBoth : kPost);
+  const Shape s = backward ? bwd_plan(R, H, form, packed != 0, !one)
+                           : fwd_plan(R, H, form, !one);
   if (!runs(s)) return RMSN_ERR_UNSUPPORTED;
   const int64_t v[BLOCK_PLAN_FIELDS] = {s.vpt,    s.ntg,     s.teams, s.rows,
                                         s.stages, s.threads, s.P,     static_cast<int64_t>(s.smem)};
