@@ -441,7 +441,7 @@ const void* pick_bwd(int form, bool packed, bool tmem, bool more) {
     if (form == kKeep && tmem) return fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, true>);
     if (form == kBoth && packed) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, false>);
   }
-  if constexpr (VPT == 3 && kEven) {  // (the widths of more_rows have even rows)
+  if constexpr (VPT == 3 && kEven) {  // (more_rows' rows are even)
     if (more)
       return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, false, true>)
                     : fn(&blk_bwd_kernel<T, VPT, kKeep, false, kEven, false, true>);
@@ -458,7 +458,7 @@ const void* pick_bwd(int form, bool packed, bool tmem, bool more) {
 template <typename T>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
   const bool even = even_rows(a.H, s.vpt, s.ntg), tmem = uses_tmem(form, packed, a.H),
-             more = more_rows(form, s.vpt, a.H);
+             more = more_rows(form, s.vpt, s.ntg);
   const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, tmem, more)
                    : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, tmem, more)
                    : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, tmem, more)

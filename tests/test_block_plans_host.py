@@ -43,3 +43,12 @@ def test_the_gpu_tests_take_every_build(lib):
     there = set().union(*(builds(rows, h) for h in range(8, 8193, 8) for rows in ROWS))
     taken = set().union(*(builds(rows, h) for rows, h in SHAPES + MANY))
     assert taken == there, sorted(there - taken)
+
+
+@pytest.mark.parametrize("packed", [0, 1])
+def test_which_widths_take_a_third_more_rows(lib, packed):
+    """As the rule's comment says (blk_launch.h): rows of one or two warps of three vectors a thread."""
+    norm = NO_POST | NO_GATE
+    threads = {h: N.rmsnorm_block_train_launch_plan(100000, h, 1, 1, packed, norm)["threads"]
+               for h in range(8, 6145, 8)}
+    assert [h for h in threads if threads[h] > 384] == [768, 1536]
