@@ -18,7 +18,8 @@ Rows may be strided where the leading axes merge into one, at 16-byte boundaries
 multiple of 8 up to 8192.  w_post and w_pre are [H], both bfloat16, float16 or float32; without
 w_post the branch is x itself, without w_pre there is no y, and one of them is given.  gate is
 None, [H], or [N, H] with a row for each of N equally long runs of rows (the samples of a batch
-[N, ..., H]), of any of the three dtypes.
+[N, ..., H]), of any of the three dtypes.  scale, residual_scale and eps are numbers, which get no
+gradient.
 
 What is not asked for is None in the results.  With act8 the forward also returns what its
 backward reads of x and h in 8 bits (act8.py); rmsnorm_block_bwd takes either kind, x and h
@@ -200,7 +201,14 @@ class RMSNormBlockTrain(torch.autograd.Function):
         return (*grads, None, None, None, None)
 
 
+def _number(v, name: str) -> float:
+    """A scale as the number it is now (a tensor could change before the backward)."""
+    if isinstance(v, torch.Tensor) and v.requires_grad and torch.is_grad_enabled():
+        raise TypeError(f"{name} is a number and gets no gradient (a gate does)")
+    return float(v)
+
+
 def rmsnorm_block_train(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0,
                         residual_scale=1.0, eps=EPS, act8=False):
-    return RMSNormBlockTrain.apply(x, residual, w_pre, w_post, gate, scale, residual_scale, eps,
-                                   act8)
+    return RMSNormBlockTrain.apply(x, residual, w_pre, w_post, gate, _number(scale, "scale"),
+                                   _number(residual_scale, "residual_scale"), eps, act8)
