@@ -86,7 +86,10 @@ size_t rmsnorm_act8_train_bwd_workspace_bytes(int64_t R, int32_t H);
  *   dx = round(rstd * (g - xhat * mean(g * xhat)) [+ dh]),  dw = sum over rows of dy * xhat (FP32)
  * dy, dh (may be NULL) and dx are [R, H], contiguous, dtype ACT8_BF16 or ACT8_FP16.  workspace as
  * rmsnorm_train_bwd's: no initial contents, clobbered, one for each of two calls that may overlap.
- * Bit-reproducible: the order of every sum is a function of R and H alone.  R == 0: dw = 0.
+ * dw is an FP32 sum, of a thread's rows in plain additions (past 64 rows in two levels, runs of them and
+ * the runs' sums), from there on with the additions' errors carried; rmsnorm_train_bwd carries them
+ * throughout.  Bit-reproducible: the order of every sum is a function of R, H and of whether dh is
+ * given.  R == 0: dw = 0.
  */
 int rmsnorm_act8_train_bwd(const void* packed, const void* dy, const void* dh, int dtype,
                            const float* rstd, const void* w, int w_dtype, void* dx, float* dw,

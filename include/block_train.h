@@ -80,7 +80,8 @@ size_t rmsnorm_block_train_bwd_workspace_bytes(int64_t R, int32_t H, int64_t N);
  *   dgate        FP32 [N, H] out, with a gate (else NULL)
  *   workspace    rmsnorm_block_train_bwd_workspace_bytes(R, H, N) bytes, 16-byte aligned, no initial
  *                contents, clobbered; one for each of two calls that may overlap
- * Everything else as the forward.  Bit-reproducible: the order of every sum is a function of R, H,
+ * Everything else as the forward.  dw_pre, dw_post and dgate are summed as rmsnorm_act8_train_bwd's
+ * dw.  Bit-reproducible: the order of every sum is a function of R, H,
  * N and of which arguments are given.  R == 0: dw_pre, dw_post and dgate become 0.
  */
 int rmsnorm_block_train_bwd(const void* dy, const void* dh, const void* x, const void* h,

@@ -22,7 +22,8 @@ SOURCES = ["rmsn_api.cu", "rmsn_fwd.cu", "rmsn_bwd.cu", "rmsn_bwd_rc.cu", "rmsn_
            "rmsn_drop_fwd.cu", "rmsn_drop_bwd.cu", "drop.cu", "gn_api.cu",
            "gn_fwd.cu", "gn_bwd.cu", "ln_api.cu", "ln_fwd.cu", "ln_bwd.cu", "act8.cu",
            "blk_api.cu", "blk_finish.cu", "blk_fwd_bf16.cu", "blk_fwd_fp16.cu",
-           "blk_bwd_bf16.cu", "blk_bwd_fp16.cu"]
+           "blk_bwd_bf16.cu", "blk_bwd_bf16_long.cu", "blk_bwd_bf16_long_dh.cu",
+           "blk_bwd_fp16.cu", "blk_bwd_fp16_long.cu", "blk_bwd_fp16_long_dh.cu"]
 HEADERS = ["rmsn_common.cuh", "rmsn_launch.h", "rmsn_fwd_rows.cuh", "rmsn_bwd_rows.cuh",
            "rmsn_tmem.cuh", "drop_launch.h", "drop_philox.cuh", "types.cuh", "gn_launch.h",
            "gn_common.cuh", "ln_launch.h",

@@ -17,7 +17,7 @@ __device__ unsigned g_blk_err_word = 0u;
 
 template <typename T>
 cudaError_t launch_fwd_t(const FwdArgs& a, const Shape& s, int form, bool pack, cudaStream_t st);
-template <typename T>
+template <typename T, int kLong>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st);
 
 cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int dtype, int form, bool pack,
@@ -27,8 +27,16 @@ cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int dtype, int form, bo
 }
 cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int dtype, int form, bool packed,
                        cudaStream_t st) {
-  return dtype == ACT8_BF16 ? launch_bwd_t<__nv_bfloat16>(a, s, form, packed, st)
-                            : launch_bwd_t<__half>(a, s, form, packed, st);
+  const bool dh = a.in[2].p != nullptr;
+  const auto launch =
+      dtype == ACT8_BF16
+          ? (a.fold == 0 ? launch_bwd_t<__nv_bfloat16, kShort>
+             : dh        ? launch_bwd_t<__nv_bfloat16, kLongDh>
+                         : launch_bwd_t<__nv_bfloat16, kLongNoDh>)
+          : (a.fold == 0 ? launch_bwd_t<__half, kShort>
+             : dh        ? launch_bwd_t<__half, kLongDh>
+                         : launch_bwd_t<__half, kLongNoDh>);
+  return launch(a, s, form, packed, st);
 }
 
 namespace {
@@ -153,6 +161,16 @@ Shape bwd_plan(int64_t R, int H, int form, bool packed, bool dh) {
   const size_t saved = packed ? static_cast<size_t>(rmsn::act8_row_size(H)) : wide;
   const size_t row = (pre ? saved + wide : 0) + (dh ? wide : 0) + (x ? saved : 0);
   return plan(R, H, form, true, packed, row, wide < saved ? wide : saved, (pre ? 1 : 0) + (x ? 1 : 0));
+}
+// Slots after which a thread's column sums go to their second level: rows of about the root of how many
+// it adds up, where that is more than 64; else 0.
+int32_t fold_slots(const Shape& s, int64_t R) {
+  const int64_t side = s.ntg < 32 ? 32 / s.ntg : 1;
+  const int64_t n = ceil_div(R, static_cast<int64_t>(s.P) * s.teams * side);
+  if (n <= 64) return 0;
+  int64_t fold = 16;
+  while (fold * fold < n) fold *= 2;
+  return static_cast<int32_t>(ceil_div(fold * side, s.rows));
 }
 int bwd_form(bool pre, bool post, bool gate) {
   return !post ? (gate ? kPre : kKeep) : (pre ? kBoth : kPost);
@@ -327,6 +345,7 @@ int run_bwd(const Bwd& b, void* stream) {
   a.residual_scale = b.residual_scale;
   a.rstd_pre = b.rstd_pre;
   a.rstd_post = b.rstd_post;
+  a.fold = fold_slots(s, b.R);
   a.factor_at = static_cast<uint32_t>(smem_bytes(s) - (s.factor ? factor_bytes(s) : 0));
   a.dx = b.dx;
   a.dres = b.dres;

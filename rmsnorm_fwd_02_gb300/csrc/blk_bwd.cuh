@@ -10,9 +10,13 @@
 // scale * gate * S.
 //
 // A team sums its columns in FP32 over its rows (in registers, or in tensor memory: uses_tmem), a CTA
-// its teams' sums, which it writes as one row of partials; the finish adds these in a fixed order.  With a gate for each of several
-// samples, a team writes its S whenever its rows pass into another sample (row k + n for team k and
-// sample n: teams and samples both go forward, so no two share one).
+// its teams' sums, which it writes as one row of partials; the finish adds these in a fixed order.
+// Both carry the additions' errors along; a team's own sums are plain.  Past 64 rows they have two
+// levels (kFold): every f rows the sums are added to those in tensor memory and start again, which
+// of the error after n rows of either sign leaves sqrt(f / n + 1 / f), so f is about the root of n.  (dw of
+// 65536 x 8192, where n is 431: at most 1.14 of 1e-4 + 1e-4 |dw| off with one level, 0.41 with two.)
+// With a gate for each of several samples, a team writes its S whenever its rows pass into another
+// sample (row k + n for team k and sample n: teams and samples both go forward, so no two share one).
 //
 // Measured, both norms, a gate and dh, 65536 rows: of 4096 522 us (93 % of a plain copy's rate over
 // the 12 bytes), of 1536 203 (89 %), of 512 81 (75 %); from 8 bits 447 (91 % of its 10), 180 and 82.
@@ -79,23 +83,25 @@ __device__ __forceinline__ void join_teams(const Args& a, const float* rows, flo
   }
 }
 
-template <typename T, int VPT, int kForm, bool kPacked, bool kEven, bool kTmem,
+template <typename T, int VPT, int kForm, bool kPacked, bool kEven, int kLong, bool kTmem,
           bool kMore = false>
 __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_kernel(const BwdArgs a) {
   constexpr bool kPostN = kForm == kBoth || kForm == kPost, kPreN = kForm != kPost;
-  constexpr bool kX = kForm != kKeep;
+  constexpr bool kX = kForm != kKeep, kFold = kLong != kShort;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint64_t pol = l2_evict_first_policy();
-  // Sums in tensor memory: for each vector 8 columns of dw_pre's, then 8 of S; the warps that share a
-  // quarter of its lanes side by side.
+  // Sums in tensor memory (kTm), then their second level (kFold): of each for each vector 8 columns of
+  // dw_pre's, then 8 of S; the warps that share a quarter of its lanes side by side.
   constexpr bool kTm = kTmem && VPT >= 3;
-  constexpr int kTmVec = kX ? 16 : 8, kTmWarp = kTmVec * VPT;
+  constexpr int kTmVec = kX ? 16 : 8, kTmLevel = kTmVec * VPT, kTmWarp = (kTm + kFold) * kTmLevel;
   constexpr int kTmCols =
-      kTm ? static_cast<int>(tmem_alloc_cols((bwd_threads(kForm, kTmem, kMore) / 128) * kTmWarp))
+      kTmWarp > 0
+          ? static_cast<int>(tmem_alloc_cols(bwd_threads(kForm, kTmem, kMore) / 128 * kTmWarp))
           : 0;
+  static_assert(kTmCols <= 512);
   Team t = team_begin<4, kTmCols>(a, smem, pol, a.samples == 1);
-  uint32_t tm = 0;
-  if constexpr (kTm) {
+  uint32_t tm = 0u;
+  if constexpr (kTmCols > 0) {
     const uint32_t warp = threadIdx.x >> 5;
     tm = tmem_warp_addr(*t.tmem, warp, (warp >> 2) * kTmWarp);
   }
@@ -150,37 +156,98 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
       if (kEven || c < NV) load8(a.w_pre, a.w_dtype, c, w[v]);
     }
   }
-  // sums of one kind (at `from` columns) to registers, and zeros in their place
+  const f2 zero[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
+  auto load_cells = [&](uint32_t at, float (&to)[VPT][8]) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) tmem_ld8(at + kTmVec * v, to[v]);
+  };
+  // (after a wait for them)
+  auto add_cells = [&](float (&cells)[VPT][8], f2 (&sum)[VPT][4]) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      tmem_loaded(cells[v]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sum[v][q] = f2_add(sum[v][q], f2_make(cells[v][2 * q], cells[v][2 * q + 1]));
+    }
+  };
+  auto clear = [&](f2 (&sum)[VPT][4]) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[v][q] = f2_splat(0.f);
+  };
+  // what tensor memory has of one kind's sums (at `from`) added to those in registers, and zeros in
+  // its place
   auto take_sums = [&](int from, f2 (&sum)[VPT][4]) {
-    if constexpr (kTm) {
-      const f2 zero[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
-      float cells[VPT][8];
+    if constexpr (kTm || kFold) {
       __syncwarp();
       tmem_wait_st();
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) tmem_ld8(tm + kTmVec * v + from, cells[v]);
-      tmem_wait_ld(cells[0]);
+      for (int o = 0; o < kTmWarp; o += kTmLevel) {
+        float cells[VPT][8];
+        load_cells(tm + o + from, cells);
+        tmem_wait_ld(cells[0]);
+        add_cells(cells, sum);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        if (v > 0) tmem_loaded(cells[v]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum[v][q] = f2_make(cells[v][2 * q], cells[v][2 * q + 1]);
-        tmem_st8(tm + kTmVec * v + from, zero);
+        for (int v = 0; v < VPT; ++v) tmem_st8(tm + o + kTmVec * v + from, zero);
       }
     }
   };
-  if constexpr (kTm) {
+  // every sum to its second level, and zeros in its place; few waits: the team does nothing else
+  auto fold_sums = [&] {
+    const uint32_t second = tm + kTmWarp - kTmLevel;
+    __syncwarp();
+    tmem_wait_st();
+    if constexpr (kTm) {
+#pragma unroll
+      for (int from = kPreN ? 0 : 8; from < kTmVec; from += 8) {
+        float one[VPT][8], two[VPT][8];
+        f2 sum[VPT][4];
+        load_cells(tm + from, one);
+        load_cells(second + from, two);
+        tmem_wait_ld(one[0]);
+        clear(sum);
+        add_cells(one, sum);
+        add_cells(two, sum);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          tmem_st8(second + kTmVec * v + from, sum[v]);
+          tmem_st8(tm + kTmVec * v + from, zero);
+        }
+      }
+    } else {
+      float pre[VPT][8], s[VPT][8];
+      if constexpr (kPreN) load_cells(second, pre);
+      if constexpr (kX) load_cells(second + 8, s);
+      if constexpr (kPreN) tmem_wait_ld(pre[0]);
+      if constexpr (!kPreN) tmem_wait_ld(s[0]);
+      if constexpr (kPreN) add_cells(pre, sum_pre);
+      if constexpr (kX) add_cells(s, sum_s);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        if constexpr (kPreN) tmem_st8(second + kTmVec * v, sum_pre[v]);
+        if constexpr (kX) tmem_st8(second + kTmVec * v + 8, sum_s[v]);
+      }
+      if constexpr (kPreN) clear(sum_pre);
+      if constexpr (kX) clear(sum_s);
+    }
+  };
+  if constexpr (kTmCols > 0) {
     __syncwarp();
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      tmem_st8(tm + kTmVec * v, sum_pre[v]);
-      if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, sum_s[v]);
+#pragma unroll
+      for (int o = 0; o < kTmWarp; o += kTmLevel) {
+        tmem_st8(tm + o + kTmVec * v, sum_pre[v]);
+        if constexpr (kX) tmem_st8(tm + o + kTmVec * v + 8, sum_s[v]);
+      }
     }
   }
   const float inv_h = 1.f / static_cast<float>(a.H);
   const f2 rscale = f2_splat(a.residual_scale);
   const int side = a.ntg < 32 ? 32 / a.ntg : 1;  // rows side by side
-  const bool has_dh = a.in[2].p != nullptr;
+  const bool has_dh = kFold ? kLong == kLongDh : a.in[2].p != nullptr;
   int32_t sample = kX ? t.r0 / a.L : 0;
   int32_t next_sample = (sample + 1) * a.L;  // the row from which k1 and S are another sample's
   if constexpr (kX) {
@@ -203,200 +270,206 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
   };
   int s = 0;
   uint32_t parity = 0;
-  for (int32_t j = 0; j < t.nslots; ++j) {
-    wait_slot(a, t, s, parity);
-    const int32_t ra = t.r0 + j * t.stride;
-    const int32_t n = min(a.rows, t.r1 - ra);
-    for (int32_t i = 0; i < n;) {
-      if constexpr (kX) {
-        if (a.samples > 1 && ra + i >= next_sample) {
-          take_sums(8, sum_s);
-          write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
-          sample = (ra + i) / a.L;
-          next_sample = (sample + 1) * a.L;
-          set_factor(sample);
-        }
-      }
-      const int32_t together = take(ra + i, n - i);
-      const int32_t row = ra + i + t.sub;
-      const bool valid = kEven || t.sub < together;
-      const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
-      const uint32_t at = static_cast<uint32_t>(i + t.sub);  // (lanes without a row read zeros)
-      const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
-      const uint32_t dys = base + a.in[1].off + at * a.in[1].bytes;
-      const uint32_t dhs = base + a.in[2].off + at * a.in[2].bytes;
-      const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
-      // (a lane without a row has zeros throughout, and adds zeros to its columns' sums)
-      const float r1 = valid ? r1_next : 0.f, r2 = valid ? r2_next : 0.f;
-      fetch(i + together < n ? row + together : ra + t.stride + t.sub);
-      const bool first = i == 0;
-      i += together;
-      // Packed vectors stay in registers between the passes over a row, times rstd (h, then x in its
-      // place): their unpacking is three times that of 16-bit values, which are read again.
-      f2 kept[kPacked ? VPT : 1][4];
-      f2 nc2 = f2_splat(0.f);
-      if constexpr (kPreN) {
-        f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          const int c = t.lt + v * a.ntg;
-          const bool live = kEven || (valid && c < NV);
-          const uint4 dyw = lds128_at(live ? dys + 16u * c : t.zero);
-          if constexpr (kPacked) {
-            f2 dy[4];
-            const f2 rh = f2_splat(load_saved<T, kPacked>(a, t, hs, c, live, kept[v]) * r2);
-            VecOf<T>::unpack(dyw, dy);
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              kept[v][q] = f2_mul(kept[v][q], rh);
-              kept[v][q + 1] = f2_mul(kept[v][q + 1], rh);
-              dot0 = f2_fma(f2_mul(dy[q], w[v][q]), kept[v][q], dot0);
-              dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), kept[v][q + 1], dot1);
-            }
-          } else {
-            const uint4 hw = lds128_at(live ? hs + 16u * c : t.zero);
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              dot0 = f2_fma(mul_exact<T>(u4_get(dyw, q), u4_get(hw, q)), w[v][q], dot0);
-              dot1 = f2_fma(mul_exact<T>(u4_get(dyw, q + 1), u4_get(hw, q + 1)), w[v][q + 1], dot1);
-            }
-          }
-        }
-        const f2 d = f2_add(dot0, dot1);
-        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
-        if (first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
-          issue<4>(a, t, j - 1 + a.stages, pol);
-        // t = r2 (dy w - hhat mean(dy w hhat)); from 16 bits the sum is of dy w h
-        nc2 = f2_splat(-(kPacked ? dot * inv_h : dot * (r2 * inv_h)));
-      }
-      const f2 r2v = f2_splat(r2), r1v = f2_splat(r1);
-      // without dh the 8-bit norm's t has no use but its outputs: its factor r2 goes to theirs
-      const bool late = kForm == kKeep && !has_dh;
-      const f2 ro = late ? f2_splat(a.residual_scale * r2) : rscale;
-      f2 m[VPT][4];
-      f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
-      const size_t out_row = static_cast<size_t>(row) * a.H;
-      if constexpr (kTm) {
-        __syncwarp();
-        tmem_wait_st();  // the row before's sums are stored before they are loaded
-      }
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = t.lt + v * a.ntg;
-        const bool live = kEven || (valid && c < NV);
-        f2 g[4], ap[4], as[4];
-        float tp[8], ts[8];  // sums from tensor memory, to be read after the wait
-        if constexpr (kTm) {
-          tmem_ld8(tm + kTmVec * v, tp);
-          if constexpr (kX) tmem_ld8(tm + kTmVec * v + 8, ts);
-        }
-        if constexpr (kPreN) {
-          f2 h[4], dy[4];
-          if constexpr (!kPacked) {
-            load_saved<T, kPacked>(a, t, hs, c, live, h);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) h[q] = f2_mul(h[q], r2v);
-          }
-          VecOf<T>::unpack(lds128_at(live ? dys + 16u * c : t.zero), dy);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f2 hhat = kPacked ? kept[kPacked ? v : 0][q] : h[q];
-            g[q] = f2_fma(hhat, nc2, f2_mul(dy[q], w[v][q]));
-            if constexpr (kTm)
-              ap[q] = f2_mul(dy[q], hhat);
-            else
-              sum_pre[v][q] = f2_fma(dy[q], hhat, sum_pre[v][q]);
-          }
-        }
-        f2 dh[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
-        if (!kPreN || has_dh) VecOf<T>::unpack(lds128_at(live ? dhs + 16u * c : t.zero), dh);
-        if (!late) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_fma(g[q], r2v, dh[q]) : dh[q];
-        }
-        f2 o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], ro);
-        if (live) stg128(static_cast<T*>(a.dres) + out_row + 8 * c, VecOf<T>::pack(o));
+  int32_t j = 0, until = kFold ? min(a.fold, t.nslots) : t.nslots;
+  for (;;) {
+    for (; j < until; ++j) {
+      wait_slot(a, t, s, parity);
+      const int32_t ra = t.r0 + j * t.stride;
+      const int32_t n = min(a.rows, t.r1 - ra);
+      for (int32_t i = 0; i < n;) {
         if constexpr (kX) {
-          f2 x[4];
-          const float u = load_saved<T, kPacked>(a, t, xs, c, live, x);
-          const f2 rx = f2_splat(kPostN ? r1 * u : u);
-          f2 f[4];
-          get_factor(v, f);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
-            if constexpr (kPostN && kPacked) kept[v][q] = xh;
-            if constexpr (kTm)
-              as[q] = f2_mul(g[q], xh);
-            else
-              sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
-            m[v][q] = f2_mul(g[q], f[q]);
+          if (a.samples > 1 && ra + i >= next_sample) {
+            take_sums(8, sum_s);
+            write_sums<VPT>(a, t, a.part_s + (t.k + sample) * a.H, sum_s);
+            sample = (ra + i) / a.L;
+            next_sample = (sample + 1) * a.L;
+            set_factor(sample);
           }
-          if constexpr (kPostN) {
+        }
+        const int32_t together = take(ra + i, n - i);
+        const int32_t row = ra + i + t.sub;
+        const bool valid = kEven || t.sub < together;
+        const uint32_t base = t.ring + static_cast<uint32_t>(s) * a.slot;
+        const uint32_t at = static_cast<uint32_t>(i + t.sub);  // (lanes without a row read zeros)
+        const uint32_t hs = base + a.in[0].off + at * a.in[0].bytes;
+        const uint32_t dys = base + a.in[1].off + at * a.in[1].bytes;
+        const uint32_t dhs = base + a.in[2].off + at * a.in[2].bytes;
+        const uint32_t xs = base + a.in[3].off + at * a.in[3].bytes;
+        // (a lane without a row has zeros throughout, and adds zeros to its columns' sums)
+        const float r1 = valid ? r1_next : 0.f, r2 = valid ? r2_next : 0.f;
+        fetch(i + together < n ? row + together : ra + t.stride + t.sub);
+        const bool first = i == 0;
+        i += together;
+        // Packed vectors stay in registers between the passes over a row, times rstd (h, then x in its
+        // place): their unpacking is three times that of 16-bit values, which are read again.
+        f2 kept[kPacked ? VPT : 1][4];
+        f2 nc2 = f2_splat(0.f);
+        if constexpr (kPreN) {
+          f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
 #pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              dot0 = f2_fma(m[v][q], kPacked ? kept[kPacked ? v : 0][q] : x[q], dot0);
-              dot1 = f2_fma(m[v][q + 1], kPacked ? kept[kPacked ? v : 0][q + 1] : x[q + 1], dot1);
+          for (int v = 0; v < VPT; ++v) {
+            const int c = t.lt + v * a.ntg;
+            const bool live = kEven || (valid && c < NV);
+            const uint4 dyw = lds128_at(live ? dys + 16u * c : t.zero);
+            if constexpr (kPacked) {
+              f2 dy[4];
+              const f2 rh = f2_splat(load_saved<T, kPacked>(a, t, hs, c, live, kept[v]) * r2);
+              VecOf<T>::unpack(dyw, dy);
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                kept[v][q] = f2_mul(kept[v][q], rh);
+                kept[v][q + 1] = f2_mul(kept[v][q + 1], rh);
+                dot0 = f2_fma(f2_mul(dy[q], w[v][q]), kept[v][q], dot0);
+                dot1 = f2_fma(f2_mul(dy[q + 1], w[v][q + 1]), kept[v][q + 1], dot1);
+              }
+            } else {
+              const uint4 hw = lds128_at(live ? hs + 16u * c : t.zero);
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                dot0 = f2_fma(mul_exact<T>(u4_get(dyw, q), u4_get(hw, q)), w[v][q], dot0);
+                dot1 = f2_fma(mul_exact<T>(u4_get(dyw, q + 1), u4_get(hw, q + 1)), w[v][q + 1], dot1);
+              }
             }
           }
-          if (!kPostN && live)
-            stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(m[v]));
-        } else if (live && a.dx != nullptr) {
-          f2 d[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) d[q] = f2_mul(g[q], f2_splat(late ? a.scale * r2 : a.scale));
-          stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(d));
+          const f2 d = f2_add(dot0, dot1);
+          const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
+          if (first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+            issue<4>(a, t, j - 1 + a.stages, pol);
+          // t = r2 (dy w - hhat mean(dy w hhat)); from 16 bits the sum is of dy w h
+          nc2 = f2_splat(-(kPacked ? dot * inv_h : dot * (r2 * inv_h)));
         }
+        const f2 r2v = f2_splat(r2), r1v = f2_splat(r1);
+        // without dh the 8-bit norm's t has no use but its outputs: its factor r2 goes to theirs
+        const bool late = kForm == kKeep && !has_dh;
+        const f2 ro = late ? f2_splat(a.residual_scale * r2) : rscale;
+        f2 m[VPT][4];
+        f2 dot0 = f2_splat(0.f), dot1 = f2_splat(0.f);
+        const size_t out_row = static_cast<size_t>(row) * a.H;
         if constexpr (kTm) {
           __syncwarp();
-          tmem_wait_ld(tp);
-          if constexpr (kX) tmem_loaded(ts);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            ap[q] = f2_add(f2_make(tp[2 * q], tp[2 * q + 1]), ap[q]);
-            if constexpr (kX) as[q] = f2_add(f2_make(ts[2 * q], ts[2 * q + 1]), as[q]);
-          }
-          tmem_st8(tm + kTmVec * v, ap);
-          if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, as);
+          tmem_wait_st();  // the row before's sums are stored before they are loaded
         }
-      }
-      if constexpr (kPostN) {
-        const f2 d = f2_add(dot0, dot1);
-        const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
-        if (!kPreN && first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
-          issue<4>(a, t, j - 1 + a.stages, pol);
-        const f2 nc1 = f2_splat(-(kPacked ? dot * inv_h : dot * (r1 * inv_h) * r1));
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int c = t.lt + v * a.ntg;
           const bool live = kEven || (valid && c < NV);
-          f2 x[4], o[4];
-          if constexpr (kPacked) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
-          } else {
-            load_saved<T, kPacked>(a, t, xs, c, live, x);
+          f2 g[4], ap[4], as[4];
+          float tp[8], ts[8];  // sums from tensor memory, to be read after the wait
+          if constexpr (kTm) {
+            tmem_ld8(tm + kTmVec * v, tp);
+            if constexpr (kX) tmem_ld8(tm + kTmVec * v + 8, ts);
           }
+          if constexpr (kPreN) {
+            f2 h[4], dy[4];
+            if constexpr (!kPacked) {
+              load_saved<T, kPacked>(a, t, hs, c, live, h);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc1, m[v][q]), r1v);
-          if (live) stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(o));
+              for (int q = 0; q < 4; ++q) h[q] = f2_mul(h[q], r2v);
+            }
+            VecOf<T>::unpack(lds128_at(live ? dys + 16u * c : t.zero), dy);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f2 hhat = kPacked ? kept[kPacked ? v : 0][q] : h[q];
+              g[q] = f2_fma(hhat, nc2, f2_mul(dy[q], w[v][q]));
+              if constexpr (kTm)
+                ap[q] = f2_mul(dy[q], hhat);
+              else
+                sum_pre[v][q] = f2_fma(dy[q], hhat, sum_pre[v][q]);
+            }
+          }
+          f2 dh[4] = {f2_splat(0.f), f2_splat(0.f), f2_splat(0.f), f2_splat(0.f)};
+          if (!kPreN || has_dh) VecOf<T>::unpack(lds128_at(live ? dhs + 16u * c : t.zero), dh);
+          if (!late) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] = kPreN ? f2_fma(g[q], r2v, dh[q]) : dh[q];
+          }
+          f2 o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = f2_mul(g[q], ro);
+          if (live) stg128(static_cast<T*>(a.dres) + out_row + 8 * c, VecOf<T>::pack(o));
+          if constexpr (kX) {
+            f2 x[4];
+            const float u = load_saved<T, kPacked>(a, t, xs, c, live, x);
+            const f2 rx = f2_splat(kPostN ? r1 * u : u);
+            f2 f[4];
+            get_factor(v, f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f2 xh = kPostN || kPacked ? f2_mul(x[q], rx) : x[q];
+              if constexpr (kPostN && kPacked) kept[v][q] = xh;
+              if constexpr (kTm)
+                as[q] = f2_mul(g[q], xh);
+              else
+                sum_s[v][q] = f2_fma(g[q], xh, sum_s[v][q]);
+              m[v][q] = f2_mul(g[q], f[q]);
+            }
+            if constexpr (kPostN) {
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                dot0 = f2_fma(m[v][q], kPacked ? kept[kPacked ? v : 0][q] : x[q], dot0);
+                dot1 = f2_fma(m[v][q + 1], kPacked ? kept[kPacked ? v : 0][q + 1] : x[q + 1], dot1);
+              }
+            }
+            if (!kPostN && live)
+              stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(m[v]));
+          } else if (live && a.dx != nullptr) {
+            f2 d[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q] = f2_mul(g[q], f2_splat(late ? a.scale * r2 : a.scale));
+            stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(d));
+          }
+          if constexpr (kTm) {
+            __syncwarp();
+            tmem_wait_ld(tp);
+            if constexpr (kX) tmem_loaded(ts);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              ap[q] = f2_add(f2_make(tp[2 * q], tp[2 * q + 1]), ap[q]);
+              if constexpr (kX) as[q] = f2_add(f2_make(ts[2 * q], ts[2 * q + 1]), as[q]);
+            }
+            tmem_st8(tm + kTmVec * v, ap);
+            if constexpr (kX) tmem_st8(tm + kTmVec * v + 8, as);
+          }
+        }
+        if constexpr (kPostN) {
+          const f2 d = f2_add(dot0, dot1);
+          const float dot = row_sum(a, t, f2_lo(d) + f2_hi(d));
+          if (!kPreN && first && t.warps > 1 && t.leader && j >= 1 && j - 1 + a.stages < t.nslots)
+            issue<4>(a, t, j - 1 + a.stages, pol);
+          const f2 nc1 = f2_splat(-(kPacked ? dot * inv_h : dot * (r1 * inv_h) * r1));
+#pragma unroll
+          for (int v = 0; v < VPT; ++v) {
+            const int c = t.lt + v * a.ntg;
+            const bool live = kEven || (valid && c < NV);
+            f2 x[4], o[4];
+            if constexpr (kPacked) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) x[q] = kept[v][q];
+            } else {
+              load_saved<T, kPacked>(a, t, xs, c, live, x);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = f2_mul(f2_fma(x[q], nc1, m[v][q]), r1v);
+            if (live) stg128(static_cast<T*>(a.dx) + out_row + 8 * c, VecOf<T>::pack(o));
+          }
         }
       }
+      if (t.warps == 1) {
+        __syncwarp();
+        if (t.leader && j + a.stages < t.nslots) issue<4>(a, t, j + a.stages, pol);
+      }
+      if (++s == a.stages) {
+        s = 0;
+        parity ^= 1u;
+      }
     }
-    if (t.warps == 1) {
-      __syncwarp();
-      if (t.leader && j + a.stages < t.nslots) issue<4>(a, t, j + a.stages, pol);
-    }
-    if (++s == a.stages) {
-      s = 0;
-      parity ^= 1u;
-    }
+    if (until == t.nslots) break;
+    if constexpr (kFold) fold_sums();
+    until = t.nslots - until > a.fold ? until + a.fold : t.nslots;
   }
   drain(a, t);
-  if constexpr (kTm) {
-    take_sums(0, sum_pre);
+  if constexpr (kTmCols > 0) {
+    if constexpr (kPreN) take_sums(0, sum_pre);
     if constexpr (kX) take_sums(8, sum_s);
     __syncwarp();
     tmem_wait_st();
@@ -430,41 +503,45 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
 
 // The build for a shape.  (Few vectors a thread are a matter of narrow rows or of few, which keep no
 // sums in tensor memory but have its builds' threads.)
-template <typename T, int VPT, bool kEven>
+template <typename T, int VPT, bool kEven, int kLong>
 const void* pick_bwd(int form, bool packed, bool tmem, bool more) {
   auto fn = [](auto k) { return reinterpret_cast<const void*>(k); };
 #define BLK_PICK(F)                                                     \
-  (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven, false>)          \
-          : fn(&blk_bwd_kernel<T, VPT, F, false, kEven, false>))
-  if (form == kBoth && tmem) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, true>);
+  (packed ? fn(&blk_bwd_kernel<T, VPT, F, true, kEven, kLong, false>)          \
+          : fn(&blk_bwd_kernel<T, VPT, F, false, kEven, kLong, false>))
+  if (form == kBoth && tmem) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, kLong, true>);
   if constexpr (VPT == 4) {
-    if (form == kKeep && tmem) return fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, true>);
-    if (form == kBoth && packed) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, false>);
+    if (form == kKeep && tmem) return fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, kLong, true>);
+    if (form == kBoth && packed) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, kLong, false>);
   }
   if constexpr (VPT == 3 && kEven) {  // (more_rows' rows are even)
     if (more)
-      return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, false, true>)
-                    : fn(&blk_bwd_kernel<T, VPT, kKeep, false, kEven, false, true>);
+      return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, kLong, false, true>)
+                    : fn(&blk_bwd_kernel<T, VPT, kKeep, false, kEven, kLong, false, true>);
   }
   switch (form) {
     case kKeep: return BLK_PICK(kKeep);
     case kPre: return BLK_PICK(kPre);
-    case kBoth: return fn(&blk_bwd_kernel<T, VPT, kBoth, false, kEven, false>);
-    default: return BLK_PICK(kPost);
+    case kBoth: return fn(&blk_bwd_kernel<T, VPT, kBoth, false, kEven, kLong, false>);
+    default:
+      if constexpr (kLong == kLongNoDh)
+        return nullptr;  // (dh is all there is)
+      else
+        return BLK_PICK(kPost);
   }
 #undef BLK_PICK
 }
 
-template <typename T>
+template <typename T, int kLong>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
   const bool even = even_rows(a.H, s.vpt, s.ntg), tmem = uses_tmem(form, packed, a.H),
              more = more_rows(form, s.vpt, s.ntg);
-  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false>(form, packed, tmem, more)
-                   : s.vpt == 2 ? pick_bwd<T, 2, false>(form, packed, tmem, more)
-                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true>(form, packed, tmem, more)
-                                        : pick_bwd<T, 3, false>(form, packed, tmem, more))
-                                : (even ? pick_bwd<T, 4, true>(form, packed, tmem, more)
-                                        : pick_bwd<T, 4, false>(form, packed, tmem, more));
+  const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false, kLong>(form, packed, tmem, more)
+                   : s.vpt == 2 ? pick_bwd<T, 2, false, kLong>(form, packed, tmem, more)
+                   : s.vpt == 3 ? (even ? pick_bwd<T, 3, true, kLong>(form, packed, tmem, more)
+                                        : pick_bwd<T, 3, false, kLong>(form, packed, tmem, more))
+                                : (even ? pick_bwd<T, 4, true, kLong>(form, packed, tmem, more)
+                                        : pick_bwd<T, 4, false, kLong>(form, packed, tmem, more));
   const cudaError_t e = prepare_kernel(fn, s.smem);
   if (e != cudaSuccess) return e;
   BwdArgs copy = a;

@@ -1,0 +1,10 @@
+// blk_bwd_fp16_long.cu -- the FP16 builds of blk_bwd.cuh for column sums of two levels without dh, in a
+// translation unit of their own so that the builds compile in parallel.
+#include "blk_bwd.cuh"
+
+namespace blk {
+
+template cudaError_t launch_bwd_t<__half, kLongNoDh>(const BwdArgs&, const Shape&, int, bool,
+                                            cudaStream_t);
+
+}  // namespace blk

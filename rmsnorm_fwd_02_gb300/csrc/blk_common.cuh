@@ -121,7 +121,7 @@ struct Team {
   uint64_t* full;       // its barriers
   float* red;           // [2][16]: warp sums, taken in turns
   volatile int* abort_flag;
-  uint32_t* tmem;       // shared word: the tensor memory's address (kTmem)
+  uint32_t* tmem;       // shared word: the tensor memory's address
   int32_t r0, r1;       // first row; end of the rows
   int32_t stride;       // rows between two of its slots' first
   int32_t nslots;

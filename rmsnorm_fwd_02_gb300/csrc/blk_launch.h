@@ -109,6 +109,7 @@ struct BwdArgs : Args {
   const float* rstd_post;
   void* dx;
   void* dres;
+  int32_t fold;       // slots after which a thread's column sums go to their second level (0: never)
   uint32_t factor_at; // where the branch's factors lie in shared memory (factor_in_smem)
   float* part_pre;    // [P][H]: sums of dy * hhat, a row a CTA
   float* part_s;      // sums of t * xhat: [P][H], a row a CTA, or with several samples
@@ -128,6 +129,11 @@ __host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
 __host__ __device__ constexpr bool factor_in_smem(int form, bool packed, bool even) {
   return form == kBoth && (packed || even);
 }
+
+// Builds of the backward: for column sums of one level, dh there or not; and for those of two (long
+// runs of rows), with and without dh, each a build: told at run time the row's loop takes 3 % more
+// instructions around the second level (65536 x 1536, both norms, 211 us against 205).
+enum { kShort = 0, kLongNoDh = 1, kLongDh = 2 };
 
 // First row of team k of n.
 __host__ __device__ inline int32_t team_row(int64_t k, int64_t R, int64_t n) {

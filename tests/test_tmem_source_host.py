@@ -40,9 +40,9 @@ def test_a_load_returns_registers_that_nothing_has_read():
 def test_a_wait_stands_before_the_first_use(source):
     calls = 0
     (_, text), = sources(source)
-    for m in re.finditer(r"tmem_ld(?:8|16)\([^;]*?(\w+)(?:\[\w+\])?\);", text):
+    for m in re.finditer(r"(?:tmem_ld(?:8|16)|load_cells)\([^;{]*?(\w+)(?:\[\w+\])?\);", text):
         between = text[m.end():text.index("tmem_wait_ld", m.end())]
-        between = re.sub(r"tmem_ld(8|16)\([^;]*;", "", between)
+        between = re.sub(r"(tmem_ld(8|16)|load_cells)\([^;]*;", "", between)
         assert not re.search(rf"\b{m[1]}\b", between), (source, m[0])
         calls += 1
     assert calls >= 2
