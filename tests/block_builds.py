@@ -19,7 +19,31 @@ def plans(rows, h):
         yield 0, form, 0, N.rmsnorm_block_train_launch_plan(rows, h, 1, 0, 0, flags)
     for packed in (0, 1):
         for form, flags in BACKWARD + (NORM8_BACKWARD if packed else []):
-            yield 1, form, packed, N.rmsnorm_block_train_launch_plan(rows, h, 1, 1, packed, flags)
+            p = N.rmsnorm_block_train_launch_plan(rows, h, 1, 1, packed, flags)
+            p["dh"], p["lane_rows"] = not flags & ONE, lane_rows(p, rows)
+            yield 1, form, packed, p
+
+
+def lane_rows(p, rows):
+    """Rows that a thread sums up."""
+    side = 32 // p["row_threads"] if p["row_threads"] < 32 else 1
+    return -(-rows // (p["ctas"] * p["teams"] * side))
+
+
+def additions(p, rows):
+    """Most additions one after another in a column sum, of one level or of two (runs of about the
+    root of the rows, in whole ring slots)."""
+    side = 32 // p["row_threads"] if p["row_threads"] < 32 else 1
+    slots = -(-(-(-rows // p["ctas"])) // p["rows"])      # of a CTA, which its teams take in turns
+    n = -(-slots // p["teams"]) * (p["rows"] // side)
+    n = max(n, lane_rows(p, rows) + 1)                    # or each a run of its own
+    if lane_rows(p, rows) <= 64:
+        return n + 9
+    f = 16
+    while f * f < lane_rows(p, rows):
+        f *= 2
+    f = -(-f * side // p["rows"]) * (p["rows"] // side)
+    return f + -(-n // f) + 9
 
 
 def most_threads(h, backward, form, packed, p):
@@ -37,7 +61,10 @@ def build(h, backward, form, packed, p):
     even = p["vectors"] >= 3 and p["row_threads"] >= 32 and \
         h == 8 * p["vectors"] * p["row_threads"]
     threads = most_threads(h, backward, form, packed, p) if p["vectors"] >= 3 else 0
-    return backward, form, packed, p["vectors"], even, threads
+    levels = 0
+    if backward and p["lane_rows"] > 64:
+        levels = "dh" if p["dh"] else "no dh"
+    return backward, form, packed, p["vectors"], even, threads, levels
 
 
 def builds(rows, h):

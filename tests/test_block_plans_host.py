@@ -5,6 +5,7 @@ import pytest
 from block_builds import NO_GATE, NO_POST, NO_PRE, NORM8, ONE, build, builds, most_threads, plans
 from test_abi_host import lib  # noqa: F401  (the module fixture)
 from test_block_builds_gpu import MANY, SHAPES
+from test_block_long_gpu import LONG, PART
 
 from rmsnorm_fwd_02_gb300 import _native as N
 
@@ -39,10 +40,17 @@ def test_plans_that_no_call_has_are_refused(lib, backward, flags, packed, n):
         N.rmsnorm_block_train_launch_plan(64, 256, n, backward, packed, flags)
 
 
+def test_the_long_tests_shapes_have_two_levels_in_every_form(lib):
+    for rows, h in LONG:
+        assert rows % (3 * PART) == 0
+        for backward, form, packed, p in plans(rows, h):
+            assert not backward or p["lane_rows"] > 64, (rows, h, form, packed, p)
+
+
 def test_the_gpu_tests_take_every_build(lib):
     there = set().union(*(builds(rows, h) for h in range(8, 8193, 8) for rows in ROWS))
-    taken = set().union(*(builds(rows, h) for rows, h in SHAPES + MANY))
-    assert taken == there, sorted(there - taken)
+    taken = set().union(*(builds(rows, h) for rows, h in SHAPES + MANY + LONG))
+    assert taken == there, sorted(there - taken, key=str)
 
 
 @pytest.mark.parametrize("packed", [0, 1])
