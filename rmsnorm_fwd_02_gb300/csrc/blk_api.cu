@@ -99,7 +99,7 @@ Shape team_shape(int64_t R, int H, int form, bool bwd, bool packed) {
   // (64 x 256 forward: 3.1 us against 5.6)
   if (nv > 16 && threads(1) <= threads_cta && R <= int64_t{kPartSMs} * teams(threads(1))) s.vpt = 1;
   s.ntg = threads(s.vpt);
-  if (bwd) threads_cta = bwd_threads(form, tmem, more_rows(form, s.vpt, s.ntg));
+  if (bwd) threads_cta = bwd_threads(form, tmem, more_rows(form, packed, s.vpt, s.ntg));
   s.teams = teams(s.ntg);
   // a row (or a warp's rows) a team at least, spread over the CTAs first
   const int side = s.ntg < 32 ? 32 / s.ntg : 1;

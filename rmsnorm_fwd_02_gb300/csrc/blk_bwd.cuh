@@ -515,9 +515,7 @@ const void* pick_bwd(int form, bool packed, bool tmem, bool more) {
     if (form == kBoth && packed) return fn(&blk_bwd_kernel<T, VPT, kBoth, true, kEven, kLong, false>);
   }
   if constexpr (VPT == 3 && kEven) {  // (more_rows' rows are even)
-    if (more)
-      return packed ? fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, kLong, false, true>)
-                    : fn(&blk_bwd_kernel<T, VPT, kKeep, false, kEven, kLong, false, true>);
+    if (more) return fn(&blk_bwd_kernel<T, VPT, kKeep, true, kEven, kLong, false, true>);
   }
   switch (form) {
     case kKeep: return BLK_PICK(kKeep);
@@ -535,7 +533,7 @@ const void* pick_bwd(int form, bool packed, bool tmem, bool more) {
 template <typename T, int kLong>
 cudaError_t launch_bwd_t(const BwdArgs& a, const Shape& s, int form, bool packed, cudaStream_t st) {
   const bool even = even_rows(a.H, s.vpt, s.ntg), tmem = uses_tmem(form, packed, a.H),
-             more = more_rows(form, s.vpt, s.ntg);
+             more = more_rows(form, packed, s.vpt, s.ntg);
   const void* fn = s.vpt == 1   ? pick_bwd<T, 1, false, kLong>(form, packed, tmem, more)
                    : s.vpt == 2 ? pick_bwd<T, 2, false, kLong>(form, packed, tmem, more)
                    : s.vpt == 3 ? (even ? pick_bwd<T, 3, true, kLong>(form, packed, tmem, more)

@@ -27,15 +27,16 @@ constexpr int fwd_threads(int form) { return form == kKeep ? 512 : 384; }
 __host__ __device__ constexpr bool uses_tmem(int form, bool packed, int H) {
   return packed && (form == kBoth ? H <= 6144 : form == kKeep && H > 6144);
 }
-// With a norm before alone, rows of three vectors a thread leave registers for a third more rows at a
-// time.  That pays where a row is one warp or two, from 8 bits (65536 x 1536 102 us against 109, with
-// dh 121 against 127; 131072 x 768 96 against 98, 123 against 131) and, with dh, a little from 16
-// (171 against 173; 171 against 176; without 139 against 139, 141 against 141).  This form has three
-// vectors only where every thread has all of them, so that is 768 and 1536 columns.  It does not pay
-// where several rows lie in a warp (131072 x 384 57 against 53) or with longer teams (65536 x 2304
-// with dh 180 against 171); with both norms registers spill (65536 x 1536 208 against 180).
-constexpr bool more_rows(int form, int vpt, int ntg) {
-  return form == kKeep && vpt == 3 && (ntg == 32 || ntg == 64);
+// The 8-bit norm's rows of three vectors a thread leave registers for a third more rows at a time.
+// That pays where a row is one warp or two: without dh 65536 x 1536 102 us against 108, 262144 x 1536
+// 356 against 397 (131072 x 768 96 against 93); with dh 120 against 119, 32768 x 1536 66 against 67 (FP16
+// 66 against 70), 65536 x 768 67 against 70.  This form has three vectors only where every thread has
+// all of them, so that is 768 and 1536 columns.  It does not pay where several rows lie in a warp
+// (131072 x 384 57 against 53), with longer teams (65536 x 2304 with dh 180 against 171), or from 16
+// bits (65536 x 1536 140 against 137, with dh 170 against 170); with both norms registers spill (65536
+// x 1536 208 against 180).
+constexpr bool more_rows(int form, bool packed, int vpt, int ntg) {
+  return form == kKeep && packed && vpt == 3 && (ntg == 32 || ntg == 64);
 }
 __host__ __device__ constexpr int bwd_threads(int form, bool tmem, bool more) {
   return form == kKeep ? (tmem || more ? 512 : 384) : (tmem ? 384 : 256);

@@ -52,7 +52,7 @@ def most_threads(h, backward, form, packed, p):
         return 512 if form == "norm8" else 384
     if form == "norm":
         three = p["vectors"] == 3 and p["row_threads"] in (32, 64)
-        return 512 if three or (packed and h > 6144) else 384
+        return 512 if packed and (three or h > 6144) else 384
     return 384 if form == "both" and packed and h <= 6144 else 256
 
 
