@@ -144,7 +144,7 @@ void ring(Shape& s, int H, size_t row, size_t least, int sums) {
 
 Shape plan(int64_t R, int H, int form, bool bwd, bool packed, size_t row, size_t least, int sums) {
   Shape s = team_shape(R, H, form, bwd, packed);
-  s.factor = bwd && factor_in_smem(form, packed, even_rows(H, s.vpt, s.ntg));
+  s.factor = bwd && factor_in_smem(form, packed);
   ring(s, H, row, least, sums);
   return s;
 }

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(bwd_threads(kForm, kTmem, kMore), 1) blk_bwd_k
   }
   const int NV = a.H >> 3;
   // (a factor in shared memory: each thread's part is its own, the rows of a warp share theirs)
-  constexpr bool kFactorMem = factor_in_smem(kForm, kPacked, kEven);
+  constexpr bool kFactorMem = factor_in_smem(kForm, kPacked);
   f2 w[VPT][4], k1[kFactorMem ? 1 : VPT][4];
   f2 sum_pre[VPT][4], sum_s[VPT][4];  // (kTm: filled from tensor memory where they are written)
   float4* const k1_mem =

@@ -20,10 +20,11 @@ enum { kKeep = 0, kPre = 1, kBoth = 2, kPost = 3 };
 constexpr int fwd_threads(int form) { return form == kKeep ? 512 : 384; }
 // From 8 bits the backward can keep a thread's column sums in tensor memory and run more threads with
 // the registers that frees.  It does where that makes room for another row in a CTA: with both norms
-// up to 6144 elements a row (65536 x 4096: 455 us against 481, 30720 x 6144 335 against 389, 65536 x
-// 1536 188 against 222; wider rows are one at a time either way, 32768 x 8192 559 against 476), in the
-// 8-bit norm past that (32768 x 8192 237 us against 295; 65536 x 4096 with dh 306 against 294).  From
-// 16 bits it gains nothing (65536 x 1536 200 us against 203, 65536 x 512 86 against 81).
+// up to 6144 elements a row (65536 x 4096: 445 us against 464, 30720 x 6144 330 against 352, 65536 x
+// 1536 175 against 202; wider rows are one at a time either way, 32768 x 8192 498 against 451), in the
+// 8-bit norm past that (32768 x 8192 218 us against 278, with dh 317 against 318; 65536 x 4096 with dh 302
+// against 296, though without 221 against 245).  From 16 bits it gains little or loses (65536 x 1536 199
+// us against 202, 65536 x 512 87 against 81).
 __host__ __device__ constexpr bool uses_tmem(int form, bool packed, int H) {
   return packed && (form == kBoth ? H <= 6144 : form == kKeep && H > 6144);
 }
@@ -124,11 +125,12 @@ __host__ __device__ inline bool even_rows(int H, int vpt, int ntg) {
 }
 
 // Backward builds whose branch's factor (scale * gate * w_post of a thread's columns) is in shared
-// memory: 4 bytes an element that a team's threads own, after everything else.  With both norms:
-// from 8 bits, whose kept vectors need the registers (65536 x 4096: 481 us against 525), and where
-// rows are even (65536 x 1536: 202 us against 213; uneven rows 82 against 78 at 30000 x 1000).
-__host__ __device__ constexpr bool factor_in_smem(int form, bool packed, bool even) {
-  return form == kBoth && (packed || even);
+// memory: 4 bytes an element that a team's threads own, after everything else.  With both norms from
+// 8 bits, whose kept vectors need the registers (65536 x 4096: 444 us against 607; 65536 x 1536 175
+// against 176).  From 16 bits it gains nothing (65536 x 4096 523 us against 520, 30720 x 6144 358 against
+// 359, 65536 x 1536 202 against 205, 30000 x 1000 82 against 77).
+__host__ __device__ constexpr bool factor_in_smem(int form, bool packed) {
+  return form == kBoth && packed;
 }
 
 // Builds of the backward: for column sums of one level, dh there or not; and for those of two (long
