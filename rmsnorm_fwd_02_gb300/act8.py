@@ -19,7 +19,9 @@ NaN.  Packed tensors are uint8 [..., act8_row_bytes(H)], contiguous.
 act8_pack / act8_unpack: CUDA bfloat16, float16 or float32 tensors [..., H] of any H; the rows may
 be strided where the leading axes merge into one, the last axis is contiguous.
 rmsnorm_act8_*: the pair that rmsnorm_fwd / rmsnorm_bwd are, with the input that the backward
-reads in 8 bits: rmsnorm_bwd's formulas at the held values.  x is bfloat16 or float16 [..., H],
+reads in 8 bits: rmsnorm_bwd's formulas at the held values (dw's additions carry their errors
+from a thread's sums on, not throughout: act8_train.h).  It saves memory: a step takes longer than
+rmsnorm_fwd and rmsnorm_bwd's.  x is bfloat16 or float16 [..., H],
 H a multiple of 8 up to 8192, rows as above and at 16-byte boundaries; w is bfloat16, float16 or
 float32 [H].  y, h, dx are contiguous; rstd is float32 [...]; dw float32 [H].  All results are
 bit-reproducible.

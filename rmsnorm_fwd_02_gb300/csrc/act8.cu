@@ -6,8 +6,11 @@
 // Groups are counted in multiples of four a row, so that no block straddles a warp.  Rows of one
 // block are a thread's each.
 // Measured: 65536 x 4096 bf16 123 us packing, 122 unpacking, a plain copy's rate over its bytes;
-// 3000000 x 5 bf16 21 and 19 (18.9 of bandwidth).  Rows that start between 16-byte vectors cost
-// the shift of each group into place: 65536 x 2051 bf16 96 and 92 us, two thirds of that rate.
+// 3000000 x 5 bf16 21 and 19 (18.9 of bandwidth).  Rows that start between 16-byte vectors run at two
+// thirds of that rate (65536 x 2051 bf16 96 and 92 us): in 16 bits they are bound by their instructions,
+// 21 an element for 14 and 10 of rows of whole vectors, in 76 % of issue slots (each group's place is
+// found and its words shifted); in FP32, whose groups are loaded as three vectors and shifted by
+// selections, by those and L1 together (65 to 76 % of its throughput, 62 to 71 % of issue slots).
 #include <cstdint>
 #include <type_traits>
 
@@ -519,8 +522,10 @@ const void* pick(int dtype, int64_t H, bool flat, bool vec) {
                               : pick_of<__half, kPack>(H, flat, vec);
 }
 
-// Rows of at least this many groups are taken in tiles of 32, three quarters of which are then there;
-// tiles are the same row's for a whole warp.
+// Rows of at least this many groups (six blocks) are taken in tiles of 32, which are the same row's for a
+// whole warp.  Three quarters of a row's one tile are then there; just past a multiple of 32 fewer,
+// 36 of 64 at the least (65536 x 264 bf16 17 us packing, 14 unpacking, 8 of bandwidth; x 384, where
+// three quarters are there again, 17.5 and 15.5 of 11.5).
 constexpr uint32_t kAct8WideGroups = 24;
 constexpr int64_t kAct8MaxH = int64_t{1} << 30;
 constexpr int64_t kAct8MaxBytes = int64_t{1} << 42;  // of a packed tensor
@@ -558,7 +563,8 @@ int act8_run(const void* wide, int dtype, const void* packed, int64_t R, int64_t
   if (!flat) {
     a.tiles = (a.groups + 31) / 32;
     constexpr int64_t per = kAct8Threads / 32 * kAct8Unroll;  // tiles a CTA
-    const dim3 grid(static_cast<unsigned>((R * a.tiles + per - 1) / per));  // below 2^42 / 192 / 32
+    // (a tile has 144 packed bytes at least, at H = 257: below 2^42 / 144 / 32)
+    const dim3 grid(static_cast<unsigned>((R * a.tiles + per - 1) / per));
     return launch_pdl(fn, grid, dim3(kAct8Threads), 0, stream_, args) == cudaSuccess
                ? RMSN_OK
                : RMSN_ERR_CUDA;

@@ -4,8 +4,7 @@
 //
 // Scales are powers of two: scaling is then exact, so a value's 8-bit number depends on nothing
 // but the value and its block's greatest magnitude, and what is unpacked again has 7 significant
-// bits: exact in BF16, its products with BF16 values exact in FP32.  (A scale of amax / 127 would
-// hold half a bit more on average.)
+// bits: exact in BF16.  (A scale of amax / 127 would hold half a bit more on average.)
 #pragma once
 
 #include <type_traits>

@@ -3,11 +3,12 @@
 // units of the two activation types.
 //
 // HBM-bound: up to 12 bytes an element (h, dy, dh, x; dx, dresidual; h and x 1.03 each where they
-// are kept in 8 bits) for some 29 (34) thread instructions.  Two row sums follow one another: of
-// dy w_pre h for the gradient t of h, then of the branch's gradient times x for dx; t waits between
-// them in registers.  One column sum serves both dw_post and the gate's gradient: S = sum of t * xhat
-// over a sample's rows, of which dgate is scale * w_post * S and dw_post the sum over samples of
-// scale * gate * S.
+// are kept in 8 bits) for some 26 to 29 (32) thread instructions where rows are even, 31 (39) where
+// a thread's last vector may be missing and each vector has a predicate.  Two row sums follow one
+// another: of dy w_pre h for the gradient t of h, then of the branch's gradient times x for dx; t
+// waits between them in registers.  One column sum serves both dw_post and the gate's gradient: S =
+// sum of t * xhat over a sample's rows, of which dgate is scale * w_post * S and dw_post the sum over
+// samples of scale * gate * S.
 //
 // A team sums its columns in FP32 over its rows (in registers, or in tensor memory: uses_tmem), a CTA
 // its teams' sums, which it writes as one row of partials; the finish adds these in a fixed order.
@@ -18,10 +19,10 @@
 // With a gate for each of several samples, a team writes its S whenever its rows pass into another
 // sample (row k + n for team k and sample n: teams and samples both go forward, so no two share one).
 //
-// Measured, both norms, a gate and dh, 65536 rows: of 4096 522 us (93 % of a plain copy's rate over
-// the 12 bytes), of 1536 203 (89 %), of 512 81 (75 %); from 8 bits 447 (91 % of its 10), 180 and 82.
-// The norm alone from 8 bits, of 4096 with dh 294 us (96 %), without 252 (80 %).  Past bandwidth the
-// threads' own dependencies bound it: two to four warps a scheduler issue in 37 to 48 % of cycles.
+// Measured, both norms, a gate and dh, 65536 rows: of 4096 521 us (93 % of a plain copy's rate over
+// the 12 bytes), of 1536 205 (89 %), of 512 81 (75 %); from 8 bits 445 (91 % of its 10), 175 and 82.
+// The norm alone from 8 bits, of 4096 with dh 296 us (96 %), without 245 (83 %).  Past bandwidth the
+// threads' own dependencies bound it: two to four warps a scheduler issue in 33 to 57 % of cycles.
 #pragma once
 
 #include "blk_common.cuh"
