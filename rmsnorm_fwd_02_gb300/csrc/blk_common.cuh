@@ -257,10 +257,7 @@ __device__ __forceinline__ void drain(const Args& a, const Team& t) {
   if (*t.abort_flag && t.leader) mbar_drain(t.full, a.stages, t.issued);
 }
 
-// Eight consecutive columns of this thread's lane of tensor memory <-> r.  A load is asynchronous: r
-// goes through tmem_wait_ld, or, after it, tmem_loaded, before anything reads it (forming pairs of
-// registers is a read).  The registers are operands of both, so that no compiler moves a read
-// ahead of the wait, which as such holds back accesses to memory alone.
+// Eight consecutive columns of this thread's lane of tensor memory <-> r.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -268,18 +265,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
         "=f"(r[7])
       : "r"(taddr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld(float (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]),
-                 "+f"(r[7])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_loaded(float (&r)[8]) {
-  asm volatile(""
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]),
-                 "+f"(r[7]));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const f2 (&r)[4]) {
   asm volatile(

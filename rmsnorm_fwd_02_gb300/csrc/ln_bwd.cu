@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(ln_max_threads(kCls), 1)
           if constexpr (kTm) {
             tmem_ld16(tm + 32u * v, tw);
             tmem_ld8(tm + 32u * v + 16u, tb);
-            tmem_wait_ld();
+            tmem_wait_ld(tw);
+            tmem_loaded(tb);
           }
           if (live) {
             const uint4 xv = lds128_at(st + 16u * c);
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(ln_max_threads(kCls), 1)
       if (qty == 0) {
         float t[16];
         tmem_ld16(tm + 32u * v, t);
-        tmem_wait_ld();
+        tmem_wait_ld(t);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           acc[q] = f2_make(t[2 * q], t[2 * q + 1]);
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(ln_max_threads(kCls), 1)
       } else {
         float t[8];
         tmem_ld8(tm + 32u * v + 16u, t);
-        tmem_wait_ld();
+        tmem_wait_ld(t);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           acc[q] = f2_make(t[2 * q], t[2 * q + 1]);

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kSlim ? bwd_slim_threads(VPT) : bwd_max_thread
         }
         if constexpr (kTm) {
           __syncwarp();
-          tmem_wait_ld();
+          tmem_wait_ld(tv);
           if (live) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // the same update, on the loaded cells
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kSlim ? bwd_slim_threads(VPT) : bwd_max_thread
     for (int v = 0; v < VPT; ++v) {
       float tv[16];
       tmem_ld16(tm + 16u * v, tv);
-      tmem_wait_ld();
+      tmem_wait_ld(tv);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         acc[v][q] = f2_make(tv[2 * q], tv[2 * q + 1]);

@@ -10,7 +10,10 @@
 //
 // Every tcgen05 instruction here is .sync.aligned: all 32 threads of the warp execute it
 // together, converged.  Loads and stores are asynchronous: tcgen05.wait::ld before the
-// loaded registers are read, tcgen05.wait::st before a store's cells are loaded again.
+// loaded registers are read (forming pairs of them is a read), tcgen05.wait::st before a
+// store's cells are loaded again.  The wait as such holds back accesses to memory alone, so
+// what is loaded goes through tmem_wait_ld, or after it tmem_loaded, as an operand: no
+// compiler can then move a read of it ahead.
 // Allocation, its address handed to the other warps through shared memory, and the
 // release follow the tcgen05 fence rules: fence::before_thread_sync before the thread
 // barrier that publishes (or retires) TMEM state, fence::after_thread_sync after it.
@@ -75,8 +78,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16]) 
       "f"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() {
+// Registers of a load that has been waited for.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float (&r)[N]) {
+  static_assert(N % 8 == 0);
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile(""
+                 : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]),
+                   "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7]));
+}
+// Waits for this thread's loads, r's among them.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tmem_loaded(r);
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

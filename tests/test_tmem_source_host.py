@@ -48,8 +48,11 @@ def test_a_wait_stands_before_the_first_use(source):
     assert calls >= 2
 
 
-def test_the_block_backwards_waits_hold_the_registers():
+def test_every_wait_holds_registers():
     """Packing a register into a pair is no memory access, so nothing but the operands of the wait
     keeps a compiler from moving it ahead."""
-    (_, text), = sources("blk_bwd.cuh")
-    assert "tmem_ld8" in text and not re.search(r"tmem_wait_ld\(\s*\)", text)
+    calls = 0
+    for name, text in sources():
+        assert not re.search(r"tmem_wait_ld\(\s*\)", text), name
+        calls += len(re.findall(r"tmem_wait_ld\(\w+(?:\[0\])?\);", text))
+    assert calls >= 8
